@@ -27,6 +27,9 @@ BD_ERR_PLAN = -10
 BD_KV_GATHER = 0
 BD_KV_WINDOW = 1
 
+BD_CACHE_BF16 = 0
+BD_CACHE_E4M3 = 1
+
 BD_BWD_OWNER_ROWS = 1
 BD_BWD_DQ_ZEROED = 2
 
@@ -63,6 +66,19 @@ class bd_tensor(C.Structure):
 class bd_rowstat(C.Structure):
     _fields_ = [("ptr", C.c_void_p), ("stride_b", C.c_int64), ("stride_c", C.c_int64),
                 ("stride_head", C.c_int64)]
+
+
+class bd_paged_cache(C.Structure):
+    _fields_ = [("k", bd_tensor), ("v", bd_tensor), ("k_exp", C.c_void_p), ("v_exp", C.c_void_p),
+                ("exp_stride_page", C.c_int64), ("exp_stride_row", C.c_int64), ("exp_stride_head", C.c_int64),
+                ("fmt", C.c_int32), ("num_pages", C.c_int32)]
+
+
+class bd_paged_desc(C.Structure):
+    _fields_ = [("B", C.c_int32), ("H", C.c_int32), ("Hkv", C.c_int32), ("d", C.c_int32), ("page_size", C.c_int32),
+                ("num_pages", C.c_int32), ("fmt", C.c_int32), ("causal", C.c_int32), ("q_len", C.POINTER(C.c_int32)),
+                ("kv_len", C.POINTER(C.c_int32)), ("pages", C.POINTER(C.c_int32)),
+                ("page_offsets", C.POINTER(C.c_int32))]
 
 
 EXPORTS = {
@@ -119,6 +135,16 @@ EXPORTS = {
                                  C.POINTER(bd_tensor), C.POINTER(bd_tensor), C.c_void_p]),
     "bd_owner_sum_ex": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_tensor), C.POINTER(bd_tensor),
                                     C.POINTER(bd_tensor), C.POINTER(bd_tensor), C.c_int32, C.c_void_p]),
+    "bd_paged_plan_bytes": (C.c_int32, [C.POINTER(bd_paged_desc), C.POINTER(C.c_size_t)]),
+    "bd_paged_plan_build": (C.c_int32, [C.POINTER(bd_paged_desc), C.c_void_p, C.c_size_t]),
+    "bd_paged_plan_key": (C.c_int32, [C.c_void_p, C.POINTER(C.c_uint64)]),
+    "bd_cache_write": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_tensor), C.POINTER(bd_tensor),
+                                   C.POINTER(bd_paged_cache), C.c_void_p]),
+    "bd_cache_read": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_paged_cache), C.POINTER(bd_tensor),
+                                  C.POINTER(bd_tensor), C.c_void_p]),
+    "bd_paged_attn_workspace": (C.c_int32, [C.c_void_p, C.POINTER(C.c_size_t)]),
+    "bd_paged_attn": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_tensor), C.POINTER(bd_paged_cache),
+                                  C.POINTER(bd_tensor), C.POINTER(bd_rowstat), C.c_void_p, C.c_size_t, C.c_void_p]),
     "bd_check_status": (C.c_int32, [C.c_void_p, C.c_int32, C.c_void_p]),
     "bd_selftest_bounded_wait": (C.c_int32, [C.c_void_p, C.c_uint32, C.c_void_p]),
     "bd_last_error": (C.c_char_p, []),

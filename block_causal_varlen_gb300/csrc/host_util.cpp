@@ -94,6 +94,27 @@ int32_t make_tmap_rows_bf16(CUtensorMap* map, const bd_tensor* t, int64_t B, int
                    CU_TENSOR_MAP_SWIZZLE_NONE, cuuint32_t(box_rows), cuuint32_t(box_heads));
 }
 
+int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int64_t heads, int64_t d, int esize,
+                        const char* name, int box_rows, int box_pieces) {
+  auto fn = encode_fn();
+  if (!fn) return fail(BD_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (no CUDA driver?)");
+  const int64_t row_bytes = d * esize, piece = row_bytes < 128 ? row_bytes : 128;
+  const int64_t sh = heads <= 1 ? row_bytes : t->stride_head * esize;
+  const int64_t sr = t->rows <= 1 ? row_bytes : t->stride_row * esize;
+  const int64_t sp = pages <= 1 ? row_bytes : t->stride_b * esize;
+  cuuint64_t dims[5] = {cuuint64_t(piece / esize), cuuint64_t(t->rows), cuuint64_t(row_bytes / piece), cuuint64_t(heads),
+                        cuuint64_t(pages)};
+  cuuint64_t strides[4] = {cuuint64_t(sr), cuuint64_t(piece), cuuint64_t(sh), cuuint64_t(sp)};
+  cuuint32_t box[5] = {cuuint32_t(piece / esize), cuuint32_t(box_rows), cuuint32_t(box_pieces), 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, t->ptr, dims,
+                  strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  piece == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(BD_ERR_ALIGN, "%s: cuTensorMapEncodeTiled failed (%d)", name, int(r));
+  return BD_OK;
+}
+
 int32_t sm_count(int* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -1,0 +1,54 @@
+// Host-side helpers shared by the paged-cache entry points, and their kernels'
+// common arguments.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "host_util.h"
+#include "paged_plan.h"
+
+namespace bd {
+
+// Checks both plan copies and the cache against the plan.
+int32_t check_paged(const void* plan_host, const void* plan_dev, const bd_paged_cache* cache, const int32_t** w);
+
+// Exponent byte b of an e4m3 row as a factor 2^(b - 127); byte 255 marks a row
+// that held an infinity or a NaN.
+__device__ __forceinline__ float exp_factor(uint32_t b) {
+  return b == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(b << 23);
+}
+
+// Partial results of the few-rows kernel: per slot m and l of its kDecRows rows,
+// then O [kDecRows][d]; the tile kernel's slots have kTileSlotRows rows.
+constexpr int kTileSlotRows = 256;
+__host__ __device__ constexpr int64_t slot_floats(int rows, int d) { return int64_t(rows) * (d + 2); }
+
+struct MergeArgs {
+  const int32_t* plan;
+  const float* part;
+  __nv_bfloat16* o;
+  int64_t o_sr, o_sh;
+  float* lse;
+  int64_t l_sh;
+};
+
+// Joins the split blocks of the few-rows (tile = false) or the tile kernel.
+int32_t launch_merge(const MergeArgs& a, int d, bool tile, cudaStream_t stream);
+
+struct AttnArgs {
+  const int32_t* plan;
+  const __nv_bfloat16* q;
+  int64_t q_sr, q_sh;
+  __nv_bfloat16* o;
+  int64_t o_sr, o_sh;
+  float* lse;  // NULL: not wanted
+  int64_t l_sh;
+  float* part;
+  const uint8_t *k_exp, *v_exp;
+  int64_t e_sp, e_sr, e_sh;
+  float scale_log2;
+};
+
+int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* cache, cudaStream_t stream);
+
+}  // namespace bd

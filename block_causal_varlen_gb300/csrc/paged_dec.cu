@@ -1,0 +1,732 @@
+// Attention of few query rows over a paged K/V cache, and the join of split key
+// ranges, on sm_103a.
+//
+// A block of up to 16 rows (the (new row, query head) pairs of one K/V head) over
+// keys [k0, k1) computes, per row, m = max_j s_j, l = sum_j 2^(s_j - m) and
+// O = sum_j 2^(s_j - m) v_j with s_j = log2(e) q . k_j / sqrt(d), in one pass.
+//
+// What bounds it is reading K and V once: 16 rows use 2 x 2 x 16 d operations per
+// key and 4 d bytes, far below the tensor rate, so the products use the
+// register-operand matrix instructions (m16n8k16), which want no TMEM and no
+// 128-row tiles, and everything is laid out to keep HBM busy:
+//   - one persistent CTA per SM; the host cuts all keys of the batch into equal
+//     stretches, one a CTA, so that no SM waits for another;
+//   - every warp runs on its own: it takes every NW-th chunk of 16 keys, loads its
+//     chunks by TMA into a ring of its own (mbarriers, no CTA-wide barrier in the
+//     loop) and keeps its own m, l and O in registers. The ring runs ahead over the
+//     ends of blocks, so loads never stop; the warps meet only to add up a block;
+//   - e4m3 chunks go from shared memory to fp16 fragments in registers (exact). The
+//     contraction order of q . k is permuted so that a lane reads 32 neighbouring
+//     codes, the column order of O so that it reads 16 of a V row, both free of
+//     bank conflicts. Exponents never touch the codes: K's is a factor of the score,
+//     V's an addend of the base-2 exponent (m is then the maximum of s_j + e_j).
+//     q as fp16 is exact too: each row is scaled by a power of two first.
+// P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-9 relative,
+// like O itself), fp16 for e4m3 (2^-12), scaled by 2^7 so that terms down to 2^-31
+// of the largest keep a value.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <atomic>
+#include <cstring>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace bd {
+using namespace dev;
+
+namespace {
+
+constexpr int kChunk = 16;  // keys a warp takes at a time
+
+template <int D, int FMT>
+struct DecCfg {
+  static constexpr bool kF8 = FMT == BD_CACHE_E4M3;
+  static constexpr int kRowBytes = D * (kF8 ? 1 : 2);         // a key's K (or V) of one head
+  static constexpr int kMatBytes = kChunk * kRowBytes;        // K (or V) of a chunk
+  static constexpr int kStageBytes = 2 * kMatBytes;
+  // warps and ring depth: 128 to 192 KB of chunks per SM (some 45 KB must be in
+  // flight to cover HBM's latency at its rate)
+  static constexpr int kWarps = kStageBytes >= 16384 ? 4 : 8;
+  static constexpr int kStages = kStageBytes >= 16384 ? 3 : kStageBytes == 8192 ? 3 : kStageBytes == 4096 ? 5 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kCols = 32, kColPad = 36;              // columns added up at a time
+  static constexpr int kOffRing = 0;
+  static constexpr int kOffSum = kOffRing + kWarps * kStages * kStageBytes;
+  static constexpr int kOffMl = kOffSum + kWarps * 16 * kColPad * 4;   // m, l [kWarps][16]
+  static constexpr int kOffInv = kOffMl + kWarps * 16 * 2 * 4;         // 1 / l of the block's rows
+  static constexpr int kOffRef = kOffInv + 16 * 4;                     // exponent offsets [kWarps][kStages]
+  static constexpr int kOffBar = kOffRef + kWarps * kStages * 8;
+  static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
+  static constexpr int kSmem = kOffAbort + 16 + 1024;         // + alignment slack
+  static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+  return r;
+}
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), operands bf16 or fp16
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// two e4m3 codes (low, high 16 bits of x) -> two fp16 pairs
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Column of O that accumulator element e (0, 1) of n-tile nt holds in lanes j = lane % 4
+// (c = 2 j + e is the tile's column). bf16: the plain order. e4m3: the B operand's
+// column c of tile t is code t of the lane's 16 (8 at head dim 64) neighbouring ones.
+template <int D, bool F8>
+__device__ __forceinline__ int o_column(int nt, int c) {
+  if constexpr (!F8) return nt * 8 + c;
+  else if constexpr (D == 64) return 8 * c + nt;
+  else return (nt >> 4) * 128 + 16 * c + (nt & 15);
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
+    bd_paged_dec_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const AttnArgs a) {
+  using Cfg = DecCfg<D, FMT>;
+  constexpr bool F8 = Cfg::kF8;
+  constexpr int NW = Cfg::kWarps, NST = Cfg::kStages;
+  constexpr int KS = D / 16, NT = D / 8;  // contraction steps of q . k, column tiles of O
+  constexpr float kPShift = F8 ? 7.f : 0.f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 3, rw = lane >> 2;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffAbort);
+  const uint32_t ring = sbase + Cfg::kOffRing + warp * NST * Cfg::kStageBytes;
+  const uint32_t bars = sbase + Cfg::kOffBar + warp * NST * 8;
+  volatile int64_t* eref = reinterpret_cast<volatile int64_t*>(smem + Cfg::kOffRef) + warp * NST;
+  const int32_t* plan = a.plan;
+  const int32_t* first = plan + plan[PH_OFF_DEC];
+  const int32_t* pieces = first + kPagedCtas + 1;
+  const int p0 = first[blockIdx.x], p1 = first[blockIdx.x + 1];
+  if (p0 == p1) return;
+  if (threadIdx.x == 0) *abort_flag = 0;
+  if (lane == 0) {
+    for (int s = 0; s < NST; ++s) mbar_init(bars + 8 * s, 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int G = plan[PH_G], causal = plan[PH_CAUSAL], pshift = plan[PH_PAGE_SHIFT];
+
+  // ---- loads: a cursor over this warp's chunks of all pieces, NST chunks ahead of
+  // the products. The next chunk's page number is fetched when the one before is
+  // issued, so that issuing waits for nothing.
+  int cp = p0 - 1, ck = 0, ck1 = 0, chkv = 0, cpages = 0, cpage = 0;
+  auto next_chunk = [&]() {
+    ck += kChunk * NW;
+    while (ck >= ck1) {
+      if (++cp >= p1) return;
+      const int32_t* W = pieces + cp * kPieceWords;
+      ck = W[PC_K0] + kChunk * warp;
+      ck1 = W[PC_K1];
+      chkv = W[PC_HKV];
+      cpages = W[PC_PAGES];
+    }
+    cpage = plan[cpages + (ck >> pshift)];
+  };
+  auto issue = [&](uint32_t it) {
+    if (cp >= p1) return;
+    const int s = int(it % NST), row = ck & ((1 << pshift) - 1);
+    if (lane == 0) {
+      if constexpr (F8) eref[s] = int64_t(cpage) * a.e_sp + int64_t(row) * a.e_sr + int64_t(chkv) * a.e_sh;
+      const uint32_t dst = ring + s * Cfg::kStageBytes;
+      mbar_expect_tx(bars + 8 * s, Cfg::kStageBytes);
+      tma_load_5d(dst, &tm_k, bars + 8 * s, 0, row, 0, chkv, cpage);
+      tma_load_5d(dst + Cfg::kMatBytes, &tm_v, bars + 8 * s, 0, row, 0, chkv, cpage);
+    }
+    next_chunk();
+  };
+  // exponent bytes of a chunk: lane l < 16 holds K's and V's of key l
+  auto load_exps = [&](uint32_t it, bool any) -> uint32_t {
+    if (!F8 || !any || lane >= 16) return 0u;
+    const int64_t o = eref[it % NST] + int64_t(lane) * a.e_sr;
+    return uint32_t(a.k_exp[o]) | (uint32_t(a.v_exp[o]) << 8);
+  };
+
+  next_chunk();
+  uint32_t issued = 0, it = 0;
+  bool ok = true;
+  for (; issued < uint32_t(NST) && cp < p1; ++issued) issue(issued);
+  __syncwarp();
+  uint32_t ex = load_exps(0, issued > 0);
+
+  for (int p = p0; p < p1; ++p) {
+    const int32_t* W = pieces + p * kPieceWords;
+    const int q0 = W[PC_Q0], qlen = W[PC_QLEN], kvlen = W[PC_KVLEN], hkv = W[PC_HKV], row0 = W[PC_ROW0];
+    const int nrows = W[PC_NROWS], k0 = W[PC_K0], k1 = W[PC_K1], slot = W[PC_SLOT];
+    // ---- the two rows of this lane: their q as A fragments, the keys they see
+    uint32_t qa[KS][4];
+    float qs[2];   // score factor: log2(e) / sqrt(d), and the power of two taken out of q
+    int lim[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rw + 8 * i, n = row0 + r, t = n / G;
+      const bool live = r < nrows;
+      lim[i] = !live ? 0 : causal ? kvlen - qlen + t + 1 : kvlen;
+      qs[i] = a.scale_log2;
+      const __nv_bfloat16* qp = a.q + int64_t(q0 + t) * a.q_sr + int64_t(hkv * G + n % G) * a.q_sh;
+      if constexpr (!F8) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          qa[s][i] = live ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * j) : 0u;
+          qa[s][2 + i] = live ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 8 + 2 * j) : 0u;
+        }
+      } else {
+        // lane j contracts over codes [x, x + 16) of the row, x as in the K loads below;
+        // step s takes four of them
+        uint32_t mx = 0;
+#pragma unroll
+        for (int s = 0; s < KS; s += 4) {
+          const int x = D == 64 ? 16 * j : (s >> 3) * 128 + 32 * j + ((s >> 2) & 1) * 16;
+          uint4 u = make_uint4(0, 0, 0, 0), v = u;
+          if (live) {
+            u = *reinterpret_cast<const uint4*>(qp + x);
+            v = *reinterpret_cast<const uint4*>(qp + x + 8);
+          }
+          qa[s][i] = u.x; qa[s][2 + i] = u.y; qa[s + 1][i] = u.z; qa[s + 1][2 + i] = u.w;
+          qa[s + 2][i] = v.x; qa[s + 2][2 + i] = v.y; qa[s + 3][i] = v.z; qa[s + 3][2 + i] = v.w;
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+          mx = __vmaxu2(mx, __vmaxu2(qa[s][i] & 0x7fff7fffu, qa[s][2 + i] & 0x7fff7fffu));
+        mx = max(mx & 0xffffu, mx >> 16);
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // max|q| = f 2^E -> f 2^14: a row below 2^-110 is scaled by 2^124 only
+        const int E = max(int(mx >> 7) - 127, -110);
+        const float up = __uint_as_float(uint32_t(127 + 14 - min(E, 113)) << 23);
+        qs[i] *= __uint_as_float(uint32_t(127 - 14 + min(E, 113)) << 23);
+        const float up2 = E > 113 ? __uint_as_float(uint32_t(127 - (E - 113)) << 23) : 1.f;
+        if (E > 113) qs[i] *= __uint_as_float(uint32_t(127 + (E - 113)) << 23);
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t u = qa[s][2 * h + i];
+            qa[s][2 * h + i] = pack_f16(__uint_as_float(u << 16) * up * up2, __uint_as_float(u & 0xffff0000u) * up * up2);
+          }
+      }
+    }
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
+    float o[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    // keys every live row sees (rows that do not exist see nothing: they need no mask)
+    const int all_see = causal ? kvlen - qlen + row0 / G + 1 : kvlen;
+
+    for (int k = k0 + kChunk * warp; k < k1; k += kChunk * NW, ++it) {
+      const uint32_t st = ring + (it % NST) * Cfg::kStageBytes;
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (it % NST), (it / NST) & 1, abort_flag))) ok = false;
+      const uint32_t ex_now = ex;
+      ex = load_exps(it + 1, it + 1 < issued);
+      // ---- S = q . k: two tiles of 8 keys
+      float s[2][4];
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      if constexpr (!F8) {
+        const uint32_t krow = st + ((lane >> 4) * 8 + (lane & 7)) * 128;
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          uint32_t b[4];
+          const uint32_t ch = uint32_t(2 * c + ((lane >> 3) & 1));
+          ldsm4(krow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
+          mma16<false>(s[0], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[0], b[1]);
+          mma16<false>(s[1], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[2], b[3]);
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = 8 * n + rw;
+#pragma unroll
+          for (int c = 0; c < KS / 4; ++c) {
+            uint32_t at;
+            if constexpr (D == 64) at = st + key * 64 + ((j ^ ((key >> 1) & 3)) << 4);
+            else at = st + (c >> 1) * (kChunk * 128) + key * 128 + (((2 * j + (c & 1)) ^ (key & 7)) << 4);
+            const uint4 u = lds128(at);
+            const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t b0, b1;
+              e4m3x4_to_f16(w4[x], b0, b1);
+              const int t = 4 * c + x;
+              mma16<true>(s[n], qa[t][0], qa[t][1], qa[t][2], qa[t][3], b0, b1);
+            }
+          }
+        }
+      }
+      // ---- base-2 scores; exponents of this lane's keys k + 8 n + 2 j + e
+      // (ve: V's; vp: the same plus P's shift, NaN for a V row of NaN)
+      float kf[4] = {1.f, 1.f, 1.f, 1.f}, ve[4] = {0.f, 0.f, 0.f, 0.f}, vp[4] = {0.f, 0.f, 0.f, 0.f};
+      if constexpr (F8) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const uint32_t b = __shfl_sync(0xffffffffu, ex_now, 8 * (x >> 1) + 2 * j + (x & 1));
+          kf[x] = exp_factor(b & 255u);
+          ve[x] = float(int(b >> 8) - 127);
+          vp[x] = (b >> 8) == 255u ? __uint_as_float(0x7fc00000u) : ve[x] + kPShift;
+        }
+      }
+      const bool edge = k + kChunk > all_see;
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] *= F8 ? qs[e >> 1] * kf[2 * n + (e & 1)] : a.scale_log2;
+          if (edge && k + 8 * n + 2 * j + (e & 1) >= lim[e >> 1]) s[n][e] = -CUDART_INF_F;
+        }
+      float f[2];
+      bool grow = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) mx = fmaxf(mx, s[n][2 * i + e] + ve[2 * n + e]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // the maximum moves only when it grows by more than 2^8 (exact: l and O use
+        // the same one)
+        f[i] = 1.f;
+        if (mx > m[i] + 8.f) {
+          f[i] = ex2(m[i] - mx);
+          m[i] = mx;
+          l[i] *= f[i];
+          grow = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[n][e] *= f[e >> 1];
+      }
+      uint32_t pa[4];  // P as the A operand: rows rw, rw + 8 x keys 2 j.., 8 + 2 j..
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float me = m[i] == -CUDART_INF_F ? 0.f : m[i];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const float x0 = s[n][2 * i] - me, x1 = s[n][2 * i + 1] - me;
+          if constexpr (F8) {
+            l[i] += ex2(x0) + ex2(x1);
+            pa[2 * n + i] = pack_f16(ex2(x0 + vp[2 * n]), ex2(x1 + vp[2 * n + 1]));
+          } else {
+            const float p0f = ex2(x0), p1f = ex2(x1);
+            l[i] += p0f + p1f;
+            pa[2 * n + i] = pack_bf16(p0f, p1f);
+          }
+        }
+      }
+      if (F8 && edge) {  // a NaN exponent of a key that the row does not see
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int key = k + 8 * n + 2 * j;
+            pa[2 * n + i] &= (key < lim[i] ? 0xffffu : 0u) | (key + 1 < lim[i] ? 0xffff0000u : 0u);
+          }
+      }
+      // ---- O += P V. Keys at or past k1 may hold anything: their V become zeros.
+      const uint32_t sv = st + Cfg::kMatBytes;
+      const bool tail = k + kChunk > k1;
+      uint32_t vm[2] = {~0u, ~0u};
+      if (tail) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          const int key = k + 8 * n + 2 * j;
+          vm[n] = (key < k1 ? 0xffffu : 0u) | (key + 1 < k1 ? 0xffff0000u : 0u);
+        }
+      }
+      if constexpr (!F8) {
+        const uint32_t vrow = sv + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
+#pragma unroll
+        for (int n = 0; n < NT; n += 2) {
+          uint32_t b[4];
+          const uint32_t ch = uint32_t(n + (lane >> 4));
+          ldsm4t(vrow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
+          if (tail) { b[0] &= vm[0]; b[1] &= vm[1]; b[2] &= vm[0]; b[3] &= vm[1]; }
+          mma16<false>(o[n], pa[0], pa[1], pa[2], pa[3], b[0], b[1]);
+          mma16<false>(o[n + 1], pa[0], pa[1], pa[2], pa[3], b[2], b[3]);
+        }
+      } else {
+        // this lane's B column is rw: 16 (8) neighbouring codes of keys 2 j, 2 j + 1,
+        // 8 + 2 j, 9 + 2 j, paired key by key
+#pragma unroll
+        for (int h = 0; h < (D + 127) / 128; ++h) {
+          uint32_t x[4][4];
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int key = 8 * (y >> 1) + 2 * j + (y & 1);
+            if constexpr (D == 64) {
+              const uint2 u = lds64(sv + key * 64 + (((rw >> 1) ^ ((key >> 1) & 3)) << 4) + (rw & 1) * 8);
+              x[y][0] = u.x; x[y][1] = u.y;
+            } else {
+              const uint4 u = lds128(sv + h * (kChunk * 128) + key * 128 + ((rw ^ (key & 7)) << 4));
+              x[y][0] = u.x; x[y][1] = u.y; x[y][2] = u.z; x[y][3] = u.w;
+            }
+          }
+#pragma unroll
+          for (int w4 = 0; w4 < (D == 64 ? 2 : 4); ++w4) {
+            // bytes (k, k') of codes 0, 1 and 2, 3 of the word
+            uint32_t b[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              e4m3x4_to_f16(__byte_perm(x[2 * y][w4], x[2 * y + 1][w4], 0x5140), b[y][0], b[y][1]);
+              e4m3x4_to_f16(__byte_perm(x[2 * y][w4], x[2 * y + 1][w4], 0x7362), b[y][2], b[y][3]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (tail) { b[0][c] &= vm[0]; b[1][c] &= vm[1]; }
+              mma16<true>(o[h * 16 + w4 * 4 + c], pa[0], pa[1], pa[2], pa[3], b[0][c], b[1][c]);
+            }
+          }
+        }
+      }
+      __syncwarp();  // every lane has read the stage
+      if (ok && issued == it + NST && cp < p1) {
+        issue(issued);
+        ++issued;
+      }
+      __syncwarp();
+    }
+
+    // ---- add the warps' results up
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      // NaN scores leave the maximum alone: what they gave was taken relative to 0
+      if (m[i] == -CUDART_INF_F && l[i] != 0.f) m[i] = 0.f;
+    }
+    float* ml = reinterpret_cast<float*>(smem + Cfg::kOffMl);  // [NW][16][2]
+    float* inv = reinterpret_cast<float*>(smem + Cfg::kOffInv);
+    float* sum = reinterpret_cast<float*>(smem + Cfg::kOffSum);
+    if (j == 0)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        ml[(warp * 16 + rw + 8 * i) * 2] = m[i];
+        ml[(warp * 16 + rw + 8 * i) * 2 + 1] = l[i];
+      }
+    __syncthreads();
+    float fac[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float M = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + rw + 8 * i) * 2]);
+      fac[i] = (m[i] == -CUDART_INF_F ? 0.f : ex2(m[i] - M)) * (F8 ? 0.0078125f : 1.f);  // 2^-kPShift
+    }
+    float* part = slot < 0 ? nullptr : a.part + int64_t(slot) * slot_floats(kDecRows, D);
+    if (int(threadIdx.x) < nrows) {
+      const int r = threadIdx.x, n = row0 + r;
+      float M = -CUDART_INF_F, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + r) * 2]);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float mw = ml[(w * 16 + r) * 2];
+        L += mw == -CUDART_INF_F ? 0.f : ml[(w * 16 + r) * 2 + 1] * ex2(mw - M);
+      }
+      inv[r] = M == -CUDART_INF_F ? 0.f : 1.f / L;
+      if (part) {
+        part[r] = M;
+        part[kDecRows + r] = L;
+      } else if (a.lse) {
+        a.lse[int64_t(hkv * G + n % G) * a.l_sh + q0 + n / G] =
+            M == -CUDART_INF_F ? -CUDART_INF_F : (M + lg2(L)) * 0.69314718055994531f;
+      }
+    }
+#pragma unroll
+    for (int c0 = 0; c0 < NT; c0 += 4) {
+      if (c0) __syncthreads();
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (rw + 8 * i < nrows)
+            *reinterpret_cast<float2*>(&sum[(warp * 16 + rw + 8 * i) * Cfg::kColPad + 8 * n + 2 * j]) =
+                make_float2(o[c0 + n][2 * i] * fac[i], o[c0 + n][2 * i + 1] * fac[i]);
+      __syncthreads();
+      for (int x = threadIdx.x; x < nrows * Cfg::kCols; x += Cfg::kThreads) {
+        const int r = x / Cfg::kCols, c = x % Cfg::kCols;
+        float t = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) t += sum[(w * 16 + r) * Cfg::kColPad + c];
+        const int col = o_column<D, F8>(c0 + (c >> 3), c & 7), n = row0 + r;
+        if (part) {
+          part[2 * kDecRows + r * D + col] = t;
+        } else {
+          a.o[int64_t(q0 + n / G) * a.o_sr + int64_t(hkv * G + n % G) * a.o_sh + col] = __float2bfloat16_rn(t * inv[r]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (!ok) {
+    // every copy issued has been waited for in turn; wait (with a limit) for those a
+    // wait gave up on, then say so
+    for (uint32_t s = 0; s < uint32_t(NST) && s < issued; ++s) {
+      const uint32_t last = issued - 1 - ((issued - 1 - s) % NST);
+      mbar_wait_drain(bars + 8 * s, (last / NST) & 1);
+    }
+    if (lane == 0) {
+      atomicExch(const_cast<int32_t*>(plan) + PH_STATUS, DEV_TIMEOUT);
+      atomicExch(const_cast<int32_t*>(plan) + PH_STATUS_DETAIL, 5);
+    }
+  }
+}
+
+// One (split block, row) per WPR warps: the slots' O rows, weighted by 2^(m_i - M).
+template <int D, int ROWS, int WPR>
+__global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) {
+  constexpr int V = D / 32;            // columns of a lane
+  constexpr int RPB = 8 / WPR;         // rows of a block
+  __shared__ float s_o[WPR > 1 ? 8 : 1][D];
+  __shared__ float s_m[8], s_l[8];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int32_t* plan = a.plan;
+  const bool tile = ROWS == kTileSlotRows;
+  const int n = plan[tile ? PH_NTILEM : PH_NDECM], G = plan[PH_G];
+  const int32_t* list = plan + plan[tile ? PH_OFF_TILEM : PH_OFF_DECM];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  for (int x0 = blockIdx.x * RPB; x0 < n * ROWS; x0 += gridDim.x * RPB) {
+    const int x = x0 + warp / WPR, r = x % ROWS;  // RPB divides ROWS: a block's rows are one entry's
+    const int32_t* M = list + (x / ROWS) * kMergeWords;
+    const bool live = r < M[MG_NROWS];
+    if (WPR > 1 && !live) continue;  // the same for the whole block
+    float acc[V], m = -CUDART_INF_F, l = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    if (live) {
+      const int cnt = M[MG_N];
+      const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(ROWS, D);
+#pragma unroll 4
+      for (int i = sub; i < cnt; i += WPR) {
+        const float* P = base + int64_t(i) * slot_floats(ROWS, D);
+        const float mi = __ldcg(P + r), li = __ldcg(P + ROWS + r);
+        float ov[V];
+        const float* op = P + 2 * ROWS + r * D + lane * V;
+        if constexpr (V == 2) {
+          const float2 t = __ldcg(reinterpret_cast<const float2*>(op));
+          ov[0] = t.x; ov[1] = t.y;
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; v += 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(op + v));
+            ov[v] = t.x; ov[v + 1] = t.y; ov[v + 2] = t.z; ov[v + 3] = t.w;
+          }
+        }
+        if (mi == -CUDART_INF_F) continue;
+        const float mn = fmaxf(m, mi), f0 = m == -CUDART_INF_F ? 0.f : ex2(m - mn), f1 = ex2(mi - mn);
+        l = l * f0 + li * f1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = acc[v] * f0 + ov[v] * f1;
+        m = mn;
+      }
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
+      if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+      __syncthreads();
+      if (sub == 0) {
+        const float m0 = m;
+        float mm = m;
+        for (int w = 1; w < WPR; ++w) mm = fmaxf(mm, s_m[warp + w]);
+        const float f0 = m0 == -CUDART_INF_F ? 0.f : ex2(m0 - mm);
+        l *= f0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] *= f0;
+        for (int w = 1; w < WPR; ++w) {
+          const float f = s_m[warp + w] == -CUDART_INF_F ? 0.f : ex2(s_m[warp + w] - mm);
+          l += s_l[warp + w] * f;
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[v] += s_o[warp + w][lane * V + v] * f;
+        }
+        m = mm;
+      }
+    }
+    if (live && sub == 0) {
+      const int nr = M[MG_ROW0] + r, h = M[MG_HKV] * G + nr % G, t = M[MG_Q0] + nr / G;
+      const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
+      __nv_bfloat16* o = a.o + int64_t(t) * a.o_sr + int64_t(h) * a.o_sh + lane * V;
+#pragma unroll
+      for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16(acc[v] * inv, acc[v + 1] * inv);
+      if (lane == 0 && a.lse)
+        a.lse[int64_t(h) * a.l_sh + t] = m == -CUDART_INF_F ? -CUDART_INF_F : (m + lg2(l)) * 0.69314718055994531f;
+    }
+    if constexpr (WPR > 1) __syncthreads();
+  }
+}
+
+template <int D, int FMT>
+int32_t launch_dec_t(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, cudaStream_t s) {
+  using Cfg = DecCfg<D, FMT>;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(bd_paged_dec_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged few-rows)");
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  bd_paged_dec_kernel<D, FMT><<<kPagedCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mk, mv, a);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
+}
+
+template <int D, int ROWS, int WPR>
+cudaError_t launch_merge_t(const MergeArgs& a, cudaStream_t s) {
+  // starts while the attention kernel drains; waits for its results itself
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(kPagedCtas * (WPR > 1 ? 4 : 8));
+  c.blockDim = dim3(256);
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, bd_paged_merge_kernel<D, ROWS, WPR>, a);
+}
+
+}  // namespace
+
+int32_t launch_merge(const MergeArgs& a, int d, bool tile, cudaStream_t s) {
+  cudaError_t e;
+  if (tile)
+    e = d == 64 ? launch_merge_t<64, kTileSlotRows, 1>(a, s)
+        : d == 128 ? launch_merge_t<128, kTileSlotRows, 1>(a, s) : launch_merge_t<256, kTileSlotRows, 1>(a, s);
+  else
+    e = d == 64 ? launch_merge_t<64, kDecRows, 8>(a, s)
+        : d == 128 ? launch_merge_t<128, kDecRows, 8>(a, s) : launch_merge_t<256, kDecRows, 8>(a, s);
+  return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_merge_kernel launch");
+}
+
+int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, cudaStream_t s) {
+  const int es = c->fmt == BD_CACHE_BF16 ? 2 : 1, d = w[PH_D];
+  const int pieces = d * es <= 128 ? 1 : d * es / 128;
+  CUtensorMap mk, mv;
+  int32_t st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", kChunk, pieces))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", kChunk, pieces))) return st;
+  if (c->fmt == BD_CACHE_BF16)
+    return d == 64 ? launch_dec_t<64, BD_CACHE_BF16>(mk, mv, a, s)
+           : d == 128 ? launch_dec_t<128, BD_CACHE_BF16>(mk, mv, a, s) : launch_dec_t<256, BD_CACHE_BF16>(mk, mv, a, s);
+  return d == 64 ? launch_dec_t<64, BD_CACHE_E4M3>(mk, mv, a, s)
+         : d == 128 ? launch_dec_t<128, BD_CACHE_E4M3>(mk, mv, a, s) : launch_dec_t<256, BD_CACHE_E4M3>(mk, mv, a, s);
+}
+
+}  // namespace bd
+
+using namespace bd;
+
+// Partial results: at most two slots a CTA, whatever the lengths.
+static size_t dec_part_bytes(const int32_t* w) {
+  return w[PH_NDEC] ? size_t(2 * kPagedCtas) * slot_floats(kDecRows, w[PH_D]) * 4 : 0;
+}
+
+extern "C" int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes) {
+  if (!bytes) return fail(BD_ERR_ARG, "bytes is NULL");
+  const int32_t* w = nullptr;
+  int32_t st = view_paged_plan(plan_host, &w);
+  if (st) return st;
+  *bytes = dec_part_bytes(w);
+  return ok();
+}
+
+extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q,
+                                 const bd_paged_cache* cache, bd_tensor* out, bd_rowstat* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const int32_t* w = nullptr;
+  int32_t st = check_paged(plan_host, plan_dev, cache, &w);
+  if (st) return st;
+  if (w[PH_T] == 0) return ok();
+  if ((st = check_tensor(q, "q", 2, 1, 1, w[PH_H], false))) return st;
+  if ((st = check_tensor(out, "out", 2, 1, 1, w[PH_H], false))) return st;
+  if (q->rows < w[PH_T] || out->rows < w[PH_T])
+    return fail(BD_ERR_ARG, "q/out rows %d/%d < %d new rows of the plan", q->rows, out->rows, w[PH_T]);
+  if (lse && (!lse->ptr || reinterpret_cast<uintptr_t>(lse->ptr) % 4))
+    return fail(BD_ERR_ARG, "lse: NULL pointer or not 4-byte aligned");
+  if (lse && w[PH_H] > 1 && lse->stride_head < w[PH_T])
+    return fail(BD_ERR_ARG, "lse stride_head %lld < %d rows", (long long)lse->stride_head, w[PH_T]);
+  const size_t need = dec_part_bytes(w);
+  if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256))
+    return fail(BD_ERR_ARG, "workspace NULL or not 256-byte aligned");
+  if (workspace_bytes < need) return fail(BD_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
+  AttnArgs a;
+  a.plan = static_cast<const int32_t*>(plan_dev);
+  a.q = static_cast<const __nv_bfloat16*>(q->ptr);
+  a.q_sr = q->stride_row; a.q_sh = q->stride_head;
+  a.o = static_cast<__nv_bfloat16*>(out->ptr);
+  a.o_sr = out->stride_row; a.o_sh = out->stride_head;
+  a.lse = lse ? lse->ptr : nullptr;
+  a.l_sh = lse ? lse->stride_head : 0;
+  a.part = static_cast<float*>(workspace);
+  a.k_exp = cache->k_exp; a.v_exp = cache->v_exp;
+  a.e_sp = cache->exp_stride_page; a.e_sr = cache->exp_stride_row; a.e_sh = cache->exp_stride_head;
+  float scale;
+  memcpy(&scale, &w[PH_SCALE_BITS], 4);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const MergeArgs m = {a.plan, a.part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh};
+  if (w[PH_NDEC]) {
+    if ((st = launch_dec(w, a, cache, s))) return st;
+    if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, s))) return st;
+  }
+  return ok();
+}

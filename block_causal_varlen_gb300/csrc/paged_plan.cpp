@@ -1,0 +1,309 @@
+// Host side of the paged K/V cache: validation of a step's lengths and pages, and
+// the plan blob the kernels read.
+//
+// The attention's work is cut on the host. A block of query rows (the (new row,
+// query head) pairs of one K/V head) and its keys are an item; items in batch
+// order form one long line of key units, and every CTA takes an equal stretch of
+// it, so a CTA holds whole items and at most two parts of items cut at its ends.
+// Parts write partial results (running maximum, sum, unnormalised O) that a second
+// kernel joins. One long sequence is thereby spread over every SM, and a ragged
+// batch leaves none idle, without counters or atomics on the device.
+#include <algorithm>
+#include <array>
+#include <cmath>
+#include <cstring>
+#include <vector>
+
+#include "common.h"
+#include "paged_plan.h"
+
+namespace bd {
+
+int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
+  if (!plan_host) return fail(BD_ERR_ARG, "plan_host is NULL");
+  const int32_t* w = static_cast<const int32_t*>(plan_host);
+  if (w[PH_MAGIC] != kPagedMagic || w[PH_VERSION] != kPagedVersion)
+    return fail(BD_ERR_PLAN, "not a paged plan blob (bad magic/version)");
+  const int64_t words = w[PH_WORDS];
+  auto in = [&](int64_t off, int64_t n, int stride) { return off >= kPagedHdrWords && n >= 0 && off + n * stride <= words; };
+  if (!in(w[PH_OFF_TOK], w[PH_T], 1) || !in(w[PH_OFF_PAGES], w[PH_NPAGES], 1) || !in(w[PH_OFF_PGROW], w[PH_NPAGES], 1) ||
+      !in(w[PH_OFF_PGCNT], w[PH_NPAGES], 1) || !in(w[PH_OFF_DEC] + kPagedCtas + 1, w[PH_NDEC], kPieceWords) ||
+      !in(w[PH_OFF_DECM], w[PH_NDECM], kMergeWords) || !in(w[PH_OFF_TILE] + kPagedCtas + 1, w[PH_NTILE], kPieceWords) ||
+      !in(w[PH_OFF_TILEM], w[PH_NTILEM], kMergeWords))
+    return fail(BD_ERR_PLAN, "paged plan blob offsets are inconsistent");
+  *out = w;
+  return BD_OK;
+}
+
+namespace {
+
+struct Item {
+  int32_t seq, hkv, row0, nrows, keys;
+};
+
+struct Lists {
+  std::vector<int32_t> first;  // [kPagedCtas + 1] first piece of every CTA
+  std::vector<int32_t> pieces, merges;
+};
+
+// Whether the items fit into n stretches of cost t (in key units; a piece costs
+// its units plus `over`). `cut`, if given, receives every piece as (item, first
+// unit, end unit, CTA).
+bool fits(const std::vector<Item>& items, int unit, int over, int64_t t, int n,
+          std::vector<std::array<int32_t, 4>>* cut) {
+  int cta = 0;
+  int64_t cap = t;
+  for (size_t i = 0; i < items.size(); ++i) {
+    const int32_t units = (items[i].keys + unit - 1) / unit;
+    int32_t at = 0;
+    for (;;) {
+      const int64_t rem = units - at;
+      if (rem + over <= cap) {
+        if (cut) cut->push_back({int32_t(i), at, units, cta});
+        cap -= rem + over;
+        break;
+      }
+      const int64_t part = std::min(cap - over, rem - 1);
+      if (part >= 1) {
+        if (cut) cut->push_back({int32_t(i), at, int32_t(at + part), cta});
+        at += int32_t(part);
+      } else if (cap == t) {
+        return false;
+      }
+      if (++cta == n) return false;
+      cap = t;
+    }
+  }
+  return true;
+}
+
+void build_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
+                 const std::vector<int32_t>& page_off, int unit, int over, Lists* L) {
+  L->first.assign(kPagedCtas + 1, 0);
+  if (items.empty()) return;
+  int64_t total = 0;
+  for (const Item& it : items) total += (it.keys + unit - 1) / unit + over;
+  // smallest stretch that holds everything
+  int64_t lo = std::max<int64_t>(over + 1, (total + kPagedCtas - 1) / kPagedCtas), hi = lo;
+  while (!fits(items, unit, over, hi, kPagedCtas, nullptr)) {
+    lo = hi + 1;
+    hi += std::max<int64_t>(1, hi / 8);
+  }
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (fits(items, unit, over, mid, kPagedCtas, nullptr)) hi = mid;
+    else lo = mid + 1;
+  }
+  std::vector<std::array<int32_t, 4>> cut;
+  fits(items, unit, over, hi, kPagedCtas, &cut);
+  int32_t slot = 0, cta = 0;
+  for (size_t i = 0; i < cut.size(); ++i) {
+    const Item& it = items[cut[i][0]];
+    const bool more = i + 1 < cut.size() && cut[i + 1][0] == cut[i][0], later = i > 0 && cut[i - 1][0] == cut[i][0];
+    const bool split = more || later;
+    while (cta <= cut[i][3]) L->first[cta++] = int32_t(i);
+    int32_t p[kPieceWords] = {0};
+    p[PC_Q0] = q0[it.seq]; p[PC_QLEN] = D.q_len[it.seq]; p[PC_KVLEN] = D.kv_len[it.seq];
+    p[PC_PAGES] = page_off[it.seq]; p[PC_HKV] = it.hkv; p[PC_ROW0] = it.row0; p[PC_NROWS] = it.nrows;
+    p[PC_K0] = cut[i][1] * unit;
+    p[PC_K1] = int32_t(std::min<int64_t>(it.keys, int64_t(cut[i][2]) * unit));
+    p[PC_SLOT] = split ? slot : -1;
+    L->pieces.insert(L->pieces.end(), p, p + kPieceWords);
+    if (split && !later) {
+      int32_t m[kMergeWords] = {0};
+      m[MG_SLOT0] = slot; m[MG_Q0] = q0[it.seq]; m[MG_HKV] = it.hkv; m[MG_ROW0] = it.row0; m[MG_NROWS] = it.nrows;
+      L->merges.insert(L->merges.end(), m, m + kMergeWords);
+    }
+    if (split) {
+      ++L->merges[L->merges.size() - kMergeWords + MG_N];
+      ++slot;
+    }
+  }
+  while (cta <= kPagedCtas) L->first[cta++] = int32_t(cut.size());
+}
+
+int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npages) {
+  if (!D) return fail(BD_ERR_ARG, "desc is NULL");
+  if (D->B <= 0) return fail(BD_ERR_ARG, "B must be positive");
+  if (!D->q_len || !D->kv_len || !D->page_offsets) return fail(BD_ERR_ARG, "q_len, kv_len or page_offsets is NULL");
+  if (D->d != 64 && D->d != 128 && D->d != 256) return fail(BD_ERR_UNSUPPORTED, "head dim %d (64, 128, 256 supported)", D->d);
+  if (D->H <= 0 || D->Hkv <= 0) return fail(BD_ERR_ARG, "H and Hkv must be positive");
+  if (D->H % D->Hkv != 0 || D->H / D->Hkv > 128)
+    return fail(BD_ERR_UNSUPPORTED, "H = %d must be a multiple of Hkv = %d, at most 128 times it", D->H, D->Hkv);
+  if (D->page_size < 16 || D->page_size > 1024 || (D->page_size & (D->page_size - 1)))
+    return fail(BD_ERR_UNSUPPORTED, "page_size %d (a power of two from 16 to 1024)", D->page_size);
+  if (D->num_pages <= 0) return fail(BD_ERR_ARG, "num_pages must be positive");
+  if (int64_t(D->num_pages) * D->page_size > INT32_MAX) return fail(BD_ERR_CAPACITY, "num_pages * page_size past 2^31 - 1");
+  if (D->fmt != BD_CACHE_BF16 && D->fmt != BD_CACHE_E4M3) return fail(BD_ERR_ARG, "cache format %d", D->fmt);
+  if (D->causal != 0 && D->causal != 1) return fail(BD_ERR_ARG, "causal must be 0 or 1");
+  *T = *kv = *npages = 0;
+  for (int32_t b = 0; b < D->B; ++b) {
+    const int32_t q = D->q_len[b], n = D->kv_len[b];
+    if (q < 0 || n < 0) return fail(BD_ERR_ARG, "sequence %d: q_len %d or kv_len %d negative", b, q, n);
+    const int32_t o0 = D->page_offsets[b], o1 = D->page_offsets[b + 1];
+    if (o0 < 0 || o1 < o0) return fail(BD_ERR_ARG, "page_offsets decrease or are negative at sequence %d", b);
+    const int64_t used = (int64_t(n) + D->page_size - 1) / D->page_size;
+    if (used > int64_t(o1) - o0)
+      return fail(BD_ERR_ARG, "sequence %d: %d pages listed, kv_len %d takes %lld", b, o1 - o0, n, (long long)used);
+    if (used && !D->pages) return fail(BD_ERR_ARG, "pages is NULL");
+    for (int64_t i = 0; i < used; ++i)
+      if (D->pages[o0 + i] < 0 || D->pages[o0 + i] >= D->num_pages)
+        return fail(BD_ERR_ARG, "sequence %d: page %d (entry %lld) outside [0, %d)", b, D->pages[o0 + i], (long long)i,
+                    D->num_pages);
+    *T += q; *kv += n; *npages += used;
+  }
+  if (*T > INT32_MAX / D->H || *kv > INT32_MAX) return fail(BD_ERR_CAPACITY, "new rows times H, or cached rows, past 2^31 - 1");
+  return BD_OK;
+}
+
+struct Built {
+  int64_t T, kv, npages;
+  Lists dec, tile;
+};
+
+int32_t prepare(const bd_paged_desc* D, Built* X) {
+  int32_t st = validate(D, &X->T, &X->kv, &X->npages);
+  if (st) return st;
+  const int G = D->H / D->Hkv;
+  std::vector<int32_t> q0(D->B), page_off(D->B);
+  int64_t t = 0, pg = kPagedHdrWords + X->T;
+  for (int32_t b = 0; b < D->B; ++b) {
+    q0[b] = int32_t(t);
+    page_off[b] = int32_t(pg);
+    t += D->q_len[b];
+    pg += (int64_t(D->kv_len[b]) + D->page_size - 1) / D->page_size;
+    if (pg > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
+  }
+  // every row block of a (sequence, K/V head): keys up to what its last row sees
+  std::vector<Item> dec, tile;
+  int64_t nitems = 0;
+  for (int32_t b = 0; b < D->B; ++b) nitems += (int64_t(D->q_len[b]) * G + kDecRows - 1) / kDecRows * D->Hkv;
+  if (nitems > (1 << 26)) return fail(BD_ERR_CAPACITY, "plan of more than 2^26 row blocks");
+  for (int32_t b = 0; b < D->B; ++b) {
+    const int32_t q = D->q_len[b], n = D->kv_len[b], rows = q * G;
+    for (int32_t g = 0; g < D->Hkv; ++g)
+      for (int32_t r0 = 0; r0 < rows; r0 += kDecRows) {
+        const int32_t r1 = std::min(rows, r0 + kDecRows);
+        const int64_t seen = D->causal ? int64_t(n) - q + (r1 - 1) / G + 1 : n;
+        dec.push_back({b, g, r0, r1 - r0, int32_t(std::max<int64_t>(0, seen))});
+      }
+  }
+  build_lists(*D, dec, q0, page_off, kDecUnit, 3, &X->dec);
+  build_lists(*D, tile, q0, page_off, kTile, 1, &X->tile);
+  return BD_OK;
+}
+
+int64_t total_words(const Built& X) {
+  // the lists are read 16 bytes at a time: each starts on a multiple of 4 words
+  auto up = [](int64_t n) { return (n + 3) / 4 * 4; };
+  int64_t w = up(kPagedHdrWords + X.T + 3 * X.npages);
+  for (const Lists* L : {&X.dec, &X.tile})
+    w = up(w + 3 + kPagedCtas + 1) + int64_t(L->pieces.size()) + int64_t(L->merges.size());
+  return up(w);
+}
+
+}  // namespace
+
+}  // namespace bd
+
+using namespace bd;
+
+extern "C" int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes) {
+  if (!bytes) return fail(BD_ERR_ARG, "bytes is NULL");
+  Built X;
+  int32_t st = prepare(desc, &X);
+  if (st) return st;
+  const int64_t w = total_words(X);
+  if (w > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
+  *bytes = size_t(w) * 4;
+  return ok();
+}
+
+extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, size_t blob_bytes) {
+  if (!blob || reinterpret_cast<uintptr_t>(blob) % 16) return fail(BD_ERR_ARG, "blob NULL or not 16-byte aligned");
+  Built X;
+  int32_t st = prepare(desc, &X);
+  if (st) return st;
+  const int64_t words = total_words(X);
+  if (words > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
+  if (blob_bytes < size_t(words) * 4)
+    return fail(BD_ERR_CAPACITY, "plan blob of %zu bytes, %lld needed", blob_bytes, (long long)words * 4);
+  int32_t* w = static_cast<int32_t*>(blob);
+  std::memset(w, 0, size_t(words) * 4);
+  const bd_paged_desc& D = *desc;
+  const int32_t P = D.page_size;
+  w[PH_MAGIC] = kPagedMagic; w[PH_VERSION] = kPagedVersion; w[PH_WORDS] = int32_t(words);
+  w[PH_B] = D.B; w[PH_H] = D.H; w[PH_HKV] = D.Hkv; w[PH_D] = D.d; w[PH_G] = D.H / D.Hkv;
+  w[PH_PAGE] = P;
+  while ((1 << w[PH_PAGE_SHIFT]) < P) ++w[PH_PAGE_SHIFT];
+  w[PH_NUM_PAGES] = D.num_pages; w[PH_FMT] = D.fmt; w[PH_CAUSAL] = D.causal;
+  w[PH_T] = int32_t(X.T); w[PH_KV_TOTAL] = int32_t(X.kv);
+  const float scale = 1.0f / std::sqrt(float(D.d));
+  std::memcpy(&w[PH_SCALE_BITS], &scale, 4);
+  w[PH_NPAGES] = int32_t(X.npages);
+  w[PH_OFF_TOK] = kPagedHdrWords;
+  w[PH_OFF_PAGES] = int32_t(w[PH_OFF_TOK] + X.T);
+  w[PH_OFF_PGROW] = int32_t(w[PH_OFF_PAGES] + X.npages);
+  w[PH_OFF_PGCNT] = int32_t(w[PH_OFF_PGROW] + X.npages);
+  int64_t tok = 0, pg = 0, kv = 0;
+  struct Range { int32_t lo, hi; };
+  std::vector<Range> written;  // cache rows the new rows take, one range per page touched
+  for (int32_t b = 0; b < D.B; ++b) {
+    const int32_t q = D.q_len[b], n = D.kv_len[b];
+    const int32_t* pages = D.pages + D.page_offsets[b];
+    for (int32_t j = 0; j < n; j += P) {
+      w[w[PH_OFF_PAGES] + pg] = pages[j / P];
+      w[w[PH_OFF_PGROW] + pg] = int32_t(kv + j);
+      w[w[PH_OFF_PGCNT] + pg] = std::min(P, n - j);
+      ++pg;
+    }
+    for (int32_t i = 0; i < q; ++i) {
+      const int64_t pos = int64_t(n) - q + i;
+      const int32_t row = pos < 0 ? -1 : pages[pos / P] * P + int32_t(pos % P);
+      w[w[PH_OFF_TOK] + tok++] = row;
+      if (row < 0) continue;
+      if (!written.empty() && written.back().hi == row && row % P) written.back().hi = row + 1;
+      else written.push_back({row, row + 1});
+    }
+    kv += n;
+  }
+  std::sort(written.begin(), written.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  w[PH_WRITE_OK] = D.causal;
+  for (size_t i = 1; i < written.size(); ++i)
+    if (written[i].lo < written[i - 1].hi) w[PH_WRITE_OK] = 0;
+  int64_t at = kPagedHdrWords + X.T + 3 * X.npages;
+  at = (at + 3) / 4 * 4;
+  auto put = [&](const Lists& L, int off, int n, int offm, int nm) {
+    // the CTA table's end, where the pieces start, is a multiple of 4 words
+    while ((at + kPagedCtas + 1) % 4) ++at;
+    w[off] = int32_t(at);
+    w[n] = int32_t(L.pieces.size() / kPieceWords);
+    std::copy(L.first.begin(), L.first.end(), w + at);
+    at += kPagedCtas + 1;
+    std::copy(L.pieces.begin(), L.pieces.end(), w + at);
+    at += int64_t(L.pieces.size());
+    w[offm] = int32_t(at);
+    w[nm] = int32_t(L.merges.size() / kMergeWords);
+    std::copy(L.merges.begin(), L.merges.end(), w + at);
+    at += int64_t(L.merges.size());
+  };
+  put(X.dec, PH_OFF_DEC, PH_NDEC, PH_OFF_DECM, PH_NDECM);
+  put(X.tile, PH_OFF_TILE, PH_NTILE, PH_OFF_TILEM, PH_NTILEM);
+  return ok();
+}
+
+extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
+  if (!key) return fail(BD_ERR_ARG, "key is NULL");
+  const int32_t* w = nullptr;
+  int32_t st = view_paged_plan(plan_host, &w);
+  if (st) return st;
+  // what a captured launch holds of the plan (FNV-1a over the words)
+  const int32_t fields[] = {w[PH_H], w[PH_HKV], w[PH_D], w[PH_PAGE], w[PH_NUM_PAGES], w[PH_FMT], w[PH_CAUSAL],
+                            w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0, w[PH_NDECM] > 0,
+                            w[PH_NTILE] > 0, w[PH_NTILEM] > 0};
+  uint64_t h = 1469598103934665603ull;
+  for (int32_t f : fields)
+    for (int i = 0; i < 4; ++i) h = (h ^ ((uint32_t(f) >> (8 * i)) & 255u)) * 1099511628211ull;
+  *key = h;
+  return ok();
+}

@@ -1,0 +1,63 @@
+// Layout of the plan blob that bd_paged_plan_build writes on the host and the
+// paged-cache kernels read from device memory. All fields are int32; offsets
+// count int32 words from the start of the blob.
+#pragma once
+#include <stdint.h>
+
+#include "../../include/bd_paged.h"
+#include "plan_layout.h"
+
+namespace bd {
+
+constexpr int32_t kPagedMagic = 0x50414442;  // "BDAP"
+constexpr int32_t kPagedVersion = 1;
+// The persistent attention kernels run one CTA per SM of a GB300; the work lists
+// are cut for that many.
+constexpr int kPagedCtas = 152;
+constexpr int kDecRows = 16;   // (new row, query head) pairs of one K/V head in a few-rows block
+constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cut
+
+// header words (the failure status keeps the place it has in attention plans, so
+// that bd_check_status reads either)
+enum : int {
+  PH_MAGIC = 0, PH_VERSION, PH_WORDS, PH_B, PH_H, PH_HKV, PH_D, PH_G, PH_PAGE, PH_PAGE_SHIFT, PH_NUM_PAGES,
+  PH_FMT, PH_CAUSAL, PH_T, PH_KV_TOTAL, PH_WRITE_OK, PH_SCALE_BITS,
+  PH_OFF_TOK,      // int32 [T]: cache row (page * page_size + row) of every new row, -1 for none
+  PH_OFF_PAGES,    // int32 [npages]: the used pages of all sequences back to back
+  PH_NPAGES,
+  PH_OFF_PGROW,    // int32 [npages]: packed row at which the page's first row is read back
+  PH_OFF_PGCNT,    // int32 [npages]: rows of the page in use
+  PH_OFF_DEC,      // few-rows kernel: int32 [kPagedCtas + 1] first piece of every CTA, then the pieces
+  PH_NDEC,         // pieces
+  PH_OFF_DECM,     // joins of its split blocks
+  PH_NDECM,
+  PH_OFF_TILE,     // the same for the tile kernel
+  PH_NTILE,
+  PH_OFF_TILEM,
+  PH_NTILEM,
+  PH_STATUS = H_STATUS, PH_STATUS_DETAIL = H_STATUS_DETAIL, // 5 few-rows attention, 6 tile attention
+  kPagedHdrWords = kHdrWords
+};
+
+// A piece: some keys of one block of rows of one (sequence, K/V head). Row r of a
+// block is (new row, head of the group) number PC_ROW0 + r, new-row-major.
+enum : int {
+  PC_Q0 = 0,    // packed row of the sequence's first new row
+  PC_QLEN, PC_KVLEN,
+  PC_PAGES,     // word offset of the sequence's pages
+  PC_HKV,       // K/V head
+  PC_ROW0,      // first (new row, head) number of the block
+  PC_NROWS,     // rows of the block that exist
+  PC_K0, PC_K1, // keys [k0, k1); k0 a multiple of the kernel's unit
+  PC_SLOT,      // partial-result slot, -1: the whole key range, written to the output
+  PC_RESERVED0, PC_RESERVED1,
+  kPieceWords = 12
+};
+
+// A join of the n partial results in slots slot0, slot0 + 1, ... of one block.
+enum : int { MG_SLOT0 = 0, MG_N, MG_Q0, MG_HKV, MG_ROW0, MG_NROWS, MG_RESERVED0, MG_RESERVED1, kMergeWords = 8 };
+
+// Validated view of a host plan blob.
+int32_t view_paged_plan(const void* plan_host, const int32_t** out);
+
+}  // namespace bd

@@ -1,0 +1,247 @@
+"""Paged K/V cache: the binding of include/bd_paged.h.
+
+Tensor layouts (all strided views are accepted; the head dim is contiguous):
+    cache k, v     bf16 or e4m3 codes [pages, page_size, Hkv, d], either may be a view
+                   of a head-first pool [pages, Hkv, page_size, d]
+    k_exp, v_exp   uint8 [pages, page_size, Hkv], e4m3 caches only
+    q, out         bf16 [rows, H, d], rows >= T: the new rows of all sequences, packed
+    k, v (new)     bf16 [rows, Hkv, d]
+    lse            fp32 [H, rows]
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import numpy as np
+import torch
+
+from . import _abi
+from ._abi import BD_CACHE_BF16, BD_CACHE_E4M3, bd_paged_cache, bd_paged_desc, bd_rowstat, bd_tensor, check, load
+
+__all__ = ["PagedCache", "PagedPlan", "bd_paged_plan_bytes", "bd_paged_plan_build", "bd_paged_plan_key",
+           "bd_cache_write", "bd_cache_read", "bd_paged_attn_workspace", "bd_paged_attn", "paged_attn",
+           "BD_CACHE_BF16", "BD_CACHE_E4M3"]
+
+_P32 = C.POINTER(C.c_int32)
+
+
+def bd_paged_plan_bytes(desc: bd_paged_desc) -> int:
+    """Bytes of the plan blob of a descriptor (validates it)."""
+    n = C.c_size_t()
+    check(load().bd_paged_plan_bytes(C.byref(desc), C.byref(n)))
+    return n.value
+
+
+def bd_paged_plan_build(desc: bd_paged_desc, blob_ptr: int, nbytes: int) -> None:
+    """Build the plan blob into host memory at ``blob_ptr``."""
+    check(load().bd_paged_plan_build(C.byref(desc), C.c_void_p(blob_ptr), nbytes))
+
+
+class PagedCache:
+    """One layer's K/V pool as the library takes it. The tensors stay the caller's;
+    they are kept alive here, and their addresses are fixed for this object."""
+
+    def __init__(self, k, v, k_exp=None, v_exp=None):
+        for t, n in ((k, "k"), (v, "v")):
+            if t.dim() != 4 or t.stride(3) != 1:
+                raise ValueError(f"cache {n}: expected [pages, page_size, Hkv, d] with d contiguous, got {tuple(t.shape)}")
+        if v.shape != k.shape or v.dtype != k.dtype or v.device != k.device:
+            raise ValueError("cache k and v differ in shape, dtype or device")
+        if k.dtype == torch.bfloat16:
+            self.fmt = BD_CACHE_BF16
+            if k_exp is not None or v_exp is not None:
+                raise ValueError("a bf16 cache has no exponents")
+        elif k.dtype == torch.float8_e4m3fn:
+            self.fmt = BD_CACHE_E4M3
+            for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+                if t is None or t.dtype != torch.uint8 or t.shape != k.shape[:3] or t.device != k.device:
+                    raise ValueError(f"{n}: an e4m3 cache needs uint8 exponents [pages, page_size, Hkv] on its device")
+            if k_exp.stride() != v_exp.stride():
+                raise ValueError("k_exp and v_exp must have the same strides")
+        else:
+            raise TypeError(f"cache dtype {k.dtype}, expected bfloat16 or float8_e4m3fn")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.num_pages, self.page_size, self.Hkv, self.d = k.shape
+        self.device = k.device
+        st = [bd_tensor(t.data_ptr(), t.stride(0), 0, t.stride(1), t.stride(2), t.shape[1], 0) for t in (k, v)]
+        es = k_exp.stride() if k_exp is not None else (0, 0, 0)
+        ep = [t.data_ptr() if t is not None else None for t in (k_exp, v_exp)]
+        self._c = bd_paged_cache(st[0], st[1], ep[0], ep[1], es[0], es[1], es[2], self.fmt, self.num_pages)
+        self._ref = C.byref(self._c)
+
+
+class PagedPlan:
+    """Host plan blob of one step over a paged cache, and its device copy.
+
+    ``q_len``, ``kv_len``: new rows of every sequence, and its cached rows with them;
+    ``pages``: a page list per sequence, or an integer table [B, max_pages].
+    """
+
+    def __init__(self, q_len, kv_len, pages, H, Hkv, d, page_size, num_pages, fmt=BD_CACHE_BF16, causal=True):
+        q = np.ascontiguousarray(q_len, dtype=np.int32)
+        kv = np.ascontiguousarray(kv_len, dtype=np.int32)
+        if q.ndim != 1 or q.shape != kv.shape or len(pages) != len(q):
+            raise ValueError("q_len, kv_len and pages must have one entry per sequence")
+        if isinstance(pages, np.ndarray) and pages.ndim == 2:
+            flat = np.ascontiguousarray(pages, dtype=np.int32).reshape(-1)
+            offs = np.arange(len(q) + 1, dtype=np.int64) * pages.shape[1]
+        else:
+            lists = [np.asarray(x, dtype=np.int32).reshape(-1) for x in pages]
+            flat = np.concatenate(lists) if lists else np.zeros(0, np.int32)
+            offs = np.cumsum([0] + [len(x) for x in lists])
+        if offs[-1] >= 2 ** 31:
+            raise ValueError("page lists of more than 2^31 entries")
+        offs = np.ascontiguousarray(offs, dtype=np.int32)
+        self.B, self.H, self.Hkv, self.d = len(q), H, Hkv, d
+        self.page_size, self.num_pages, self.fmt, self.causal = page_size, num_pages, fmt, bool(causal)
+        self.T, self.kv_total = int(q.sum(dtype=np.int64)), int(kv.sum(dtype=np.int64))
+        desc = bd_paged_desc(self.B, H, Hkv, d, page_size, num_pages, fmt, int(self.causal), q.ctypes.data_as(_P32),
+                             kv.ctypes.data_as(_P32), flat.ctypes.data_as(_P32), offs.ctypes.data_as(_P32))
+        self.nbytes = bd_paged_plan_bytes(desc)
+        self._raw = np.zeros(self.nbytes // 4 + 16, dtype=np.int32)
+        off = (-self._raw.ctypes.data % 64) // 4
+        self.host = self._raw[off:off + self.nbytes // 4]
+        bd_paged_plan_build(desc, self.host.ctypes.data, self.nbytes)
+        self._host_ptr = C.c_void_p(self.host.ctypes.data)
+        self.dev = self._dev_ptr = None
+        ws = C.c_size_t()
+        check(load().bd_paged_attn_workspace(self._host_ptr, C.byref(ws)))
+        self._workspace = ws.value
+
+    @property
+    def host_ptr(self):
+        return self._host_ptr
+
+    @property
+    def dev_ptr(self):
+        if self._dev_ptr is None:
+            raise RuntimeError("plan not uploaded: call .upload(device)")
+        return self._dev_ptr
+
+    def upload(self, device="cuda", non_blocking=False, buffer=None):
+        """Copy the plan blob to device memory (once per step): into memory of its own,
+        or into ``buffer``, an int32 device tensor of at least nbytes / 4 words that a
+        captured graph reads (see bd_paged_plan_key)."""
+        src = torch.from_numpy(self.host)
+        if buffer is not None:
+            if buffer.dtype != torch.int32 or buffer.dim() != 1 or not buffer.is_contiguous() or not buffer.is_cuda:
+                raise TypeError("buffer: expected a contiguous 1-D int32 CUDA tensor")
+            if buffer.numel() < src.numel():
+                raise ValueError(f"buffer of {buffer.numel()} words, the plan has {src.numel()}")
+            self.dev = buffer[:src.numel()]
+        elif self.dev is None or self.dev.device != torch.device(device):
+            self.dev = torch.empty_like(src, device=device)
+        self.dev.copy_(src, non_blocking=non_blocking)
+        self._dev_ptr = C.c_void_p(self.dev.data_ptr())
+        return self
+
+    def key(self) -> int:
+        """See bd_paged_plan_key."""
+        return bd_paged_plan_key(self)
+
+
+def bd_paged_plan_key(plan: PagedPlan) -> int:
+    """Plans of equal keys may replace each other under a captured graph (see
+    include/bd_paged.h)."""
+    n = C.c_uint64()
+    check(load().bd_paged_plan_key(plan.host_ptr, C.byref(n)))
+    return n.value
+
+
+def bd_paged_attn_workspace(plan: PagedPlan) -> int:
+    """Workspace bytes of bd_paged_attn."""
+    return plan._workspace
+
+
+def _rows3(t, name, heads, d, rows, dev):
+    """A packed [rows, heads, d] bf16 tensor as the ABI's strided tensor. The C ABI
+    carries neither dtypes nor head counts, so they are checked here."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+    if not t.is_cuda:
+        raise TypeError(f"{name}: must be a CUDA tensor")
+    if t.device != dev:
+        raise ValueError(f"{name}: on {t.device}, the plan was uploaded to {dev}")
+    s = t.shape
+    if len(s) != 3 or s[1] != heads or s[2] != d or s[0] < rows:
+        raise ValueError(f"{name}: shape {tuple(s)}, expected [{rows} or more, {heads}, {d}]")
+    st = t.stride()
+    if st[2] != 1:
+        raise ValueError(f"{name}: head dim must be contiguous")
+    return bd_tensor(t.data_ptr(), 0, 0, st[0], st[1], s[0], 0)
+
+
+def _device(plan, cache):
+    """The device of a call: that of the plan's device copy, which must be the cache's
+    (heads and head dim of the cache are checked too; the ABI does not carry them)."""
+    if plan.dev is None:
+        raise RuntimeError("plan not uploaded: call .upload(device)")
+    dev = plan.dev.device
+    if cache.device != dev:
+        raise ValueError(f"cache: on {cache.device}, the plan was uploaded to {dev}")
+    if cache.Hkv != plan.Hkv or cache.d != plan.d:
+        raise ValueError(f"cache of {cache.Hkv} heads of {cache.d}, the plan was built for {plan.Hkv} of {plan.d}")
+    return dev
+
+
+def _call(fn, dev, stream, *args):
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    if torch.cuda.current_device() == dev.index:
+        check(fn(*args, C.c_void_p(stream.cuda_stream)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn(*args, C.c_void_p(stream.cuda_stream)))
+
+
+def bd_cache_write(plan: PagedPlan, k, v, cache: PagedCache, stream=None):
+    """Store the new rows' K and V at their cache positions (see include/bd_paged.h)."""
+    dev = _device(plan, cache)
+    tk = _rows3(k, "k", plan.Hkv, plan.d, plan.T, dev)
+    tv = _rows3(v, "v", plan.Hkv, plan.d, plan.T, dev)
+    _call(load().bd_cache_write, dev, stream, plan._host_ptr, plan._dev_ptr, C.byref(tk), C.byref(tv), cache._ref)
+
+
+def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
+    """The cached rows of every sequence, packed in batch order (see include/bd_paged.h)."""
+    dev = _device(plan, cache)
+    tk = _rows3(k, "k", plan.Hkv, plan.d, plan.kv_total, dev)
+    tv = _rows3(v, "v", plan.Hkv, plan.d, plan.kv_total, dev)
+    _call(load().bd_cache_read, dev, stream, plan._host_ptr, plan._dev_ptr, cache._ref, C.byref(tk), C.byref(tv))
+
+
+def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspace=None, stream=None):
+    """O and LSE of the new rows over the cache (see include/bd_paged.h). Without a
+    workspace one is allocated for the call."""
+    dev = _device(plan, cache)
+    tq = _rows3(q, "q", plan.H, plan.d, plan.T, dev)
+    to = _rows3(out, "out", plan.H, plan.d, plan.T, dev)
+    tl = None
+    if lse is not None:
+        if lse.dtype != torch.float32:
+            raise TypeError(f"lse: dtype {lse.dtype}, expected torch.float32")
+        if lse.device != dev:
+            raise ValueError(f"lse: on {lse.device}, the plan was uploaded to {dev}")
+        if lse.dim() != 2 or lse.shape[0] != plan.H or lse.shape[1] < plan.T or lse.stride(1) != 1:
+            raise ValueError(f"lse: expected [{plan.H}, {plan.T} or more] with rows contiguous, got {tuple(lse.shape)}")
+        tl = C.byref(bd_rowstat(lse.data_ptr(), 0, 0, lse.stride(0)))
+    if workspace is None and plan._workspace:
+        workspace = torch.empty(plan._workspace, dtype=torch.uint8, device=dev)
+        if stream is not None:
+            workspace.record_stream(stream)
+    wp, wn = None, 0
+    if workspace is not None:
+        if workspace.device != dev:
+            raise ValueError(f"workspace: on {workspace.device}, the plan was uploaded to {dev}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        wp, wn = C.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
+    _call(load().bd_paged_attn, dev, stream, plan._host_ptr, plan._dev_ptr, C.byref(tq), cache._ref, C.byref(to), tl, wp, wn)
+
+
+def paged_attn(plan: PagedPlan, q, cache: PagedCache, stream=None):
+    """Allocate O and LSE and run bd_paged_attn; returns (out, lse)."""
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(plan.H, q.shape[0], dtype=torch.float32, device=q.device)
+    bd_paged_attn(plan, q, cache, out, lse, stream=stream)
+    return out, lse

@@ -1,0 +1,406 @@
+"""GPU parity of the paged K/V cache: writing, reading back and attention of new rows,
+through the C ABI, against the float64 oracle."""
+import pytest
+import torch
+
+import oracle
+from oracle import paged as op
+
+pytestmark = pytest.mark.gpu
+
+bd = pytest.importorskip("block_causal_varlen_gb300")
+pu = pytest.importorskip("paged_util")
+
+HEADS = [(4, 4, 64), (8, 2, 128), (4, 1, 256)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    bd.load()
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8).cpu()
+
+
+# ------------------------------------------------------------------ attention: shapes
+
+SMALL = [([1], [1]), ([1], [16]), ([1, 1, 1], [17, 15, 130]), ([2, 0, 1], [33, 40, 257])]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", HEADS)
+@pytest.mark.parametrize("new,kv", SMALL)
+def test_few_rows(new, kv, H, Hkv, d, fmt):
+    c = pu.Case(new, kv, H, Hkv, d, fmt=fmt, seed=len(kv) + d)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", HEADS)
+def test_long_context_is_split_and_joined(H, Hkv, d, fmt):
+    c = pu.Case([1], [6001], H, Hkv, d, page=64, fmt=fmt, seed=d)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv", [(10, 2), (7, 1), (32, 1), (6, 6), (24, 8)])
+def test_head_groups(H, Hkv, fmt):
+    c = pu.Case([1, 3, 9], [40, 700, 9], H, Hkv, 128, page=32, fmt=fmt, seed=H)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", HEADS)
+@pytest.mark.parametrize("new,kv", [([130], [130]), ([40, 1, 300, 17], [40, 500, 333, 150]), ([257], [1031])])
+def test_chunks(new, kv, H, Hkv, d, fmt):
+    c = pu.Case(new, kv, H, Hkv, d, page=64, fmt=fmt, seed=sum(kv))
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 128, 1024])
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_page_sizes_and_orders(page, heads_first, fmt):
+    c = pu.Case([1, 70, 200], [1500, 70, 1100], 8, 2, 128, page=page, fmt=fmt, heads_first=heads_first, seed=page)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_rows_that_see_nothing(fmt):
+    """Sequences with nothing cached, and more new rows than cached ones."""
+    c = pu.Case([1, 3, 5, 90, 40], [0, 2, 0, 60, 500], 8, 2, 128, fmt=fmt)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_every_row_sees_the_whole_slice(fmt):
+    """causal = False: a slice of a context held elsewhere as well; an empty slice gives
+    O = 0, LSE = -inf."""
+    c = pu.Case([1, 3, 70, 2], [100, 1, 300, 0], 8, 2, 128, fmt=fmt, causal=False)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("qscale", [2.0 ** -40, 30.0])
+def test_flat_and_peaked_scores(fmt, qscale):
+    """Scores near zero (every key the same weight) and scores of some hundreds (one key
+    takes all; the running maximum moves by large steps)."""
+    c = pu.Case([1, 5, 150], [2000, 300, 150], 8, 2, 128, fmt=fmt, qscale=qscale)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+def test_rows_past_the_last_sequence_are_left_alone():
+    c = pu.Case([1, 20], [40, 333], 8, 2, 128, pad_rows=5)
+    out = torch.full((26, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((8, 26), 7.0, device="cuda")
+    bd.bd_paged_attn(c.plan, c.q.cuda(), c.cache, out, lse)
+    torch.cuda.synchronize()
+    assert (out[21:] == 7).all() and (lse[:, 21:] == 7).all()
+    pu.check_attention(c, out.cpu(), lse.cpu())
+
+
+def test_strided_rows_and_no_lse():
+    """q and out as slices of a fused projection's rows; LSE not asked for."""
+    c = pu.Case([1, 40, 130], [900, 40, 600], 8, 2, 128, page=64)
+    big = torch.full((c.T, 14 * 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    q = big[:, 128:9 * 128].view(c.T, 8, 128)
+    q.copy_(c.q)
+    wide = torch.zeros(c.T, 8, 256, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, :, 128:]
+    bd.bd_paged_attn(c.plan, q, c.cache, out)
+    torch.cuda.synchronize()
+    _, lse = pu.run_attention(c)
+    pu.check_attention(c, out.cpu(), lse)
+    assert (wide[:, :, :128] == 0).all()
+
+
+def test_shared_pages():
+    """Two sequences over the same pages, at different lengths."""
+    c = pu.Case([1, 2], [200, 100], 8, 2, 128, page=16)
+    c.pages[1] = c.pages[0][:7]
+    c.kd = c.kd.clone()
+    c.plan = c.make_plan().upload("cuda")
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_nan_in_the_cache_reaches_those_who_see_it_only(fmt):
+    """A NaN row in the middle of a sequence makes that sequence's rows NaN, nobody else's."""
+    c = pu.Case([1, 1], [100, 300], 8, 2, 128, fmt=fmt, junk=0.0)
+    page, row = c.pages[1][3], 5
+    if fmt == "bf16":
+        c.v[page, row, 0] = float("nan")
+    else:
+        c.ve[page, row, 0] = 255
+    out, lse = pu.run_attention(c)
+    assert torch.isnan(out[1, :4]).all() and torch.isfinite(out[1, 4:]).all() and torch.isfinite(out[0]).all()
+    assert torch.isfinite(lse).all()
+    if fmt == "bf16":
+        c.k[page, row, 0] = float("nan")
+    else:
+        c.ke[page, row, 0] = 255
+    out, lse = pu.run_attention(c)
+    assert torch.isnan(lse[:4, 1]).all() and torch.isfinite(lse[4:, 1]).all() and torch.isfinite(lse[:, 0]).all()
+
+
+# ------------------------------------------------------------------ attention: calls
+
+def _mixed(fmt="bf16", seed=0):
+    return pu.Case([1, 1, 60, 200], [5000, 40, 700, 900], 8, 2, 128, page=32, fmt=fmt, seed=seed)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_same_bits_every_time(fmt):
+    c = _mixed(fmt)
+    a, b = pu.run_attention(c), pu.run_attention(c)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_two_calls_at_once_on_one_plan():
+    """Calls on two streams share the device plan and have workspaces of their own."""
+    c = _mixed()
+    want = pu.run_attention(c)
+    q = c.q.cuda()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = []
+    torch.cuda.synchronize()
+    for i in range(6):
+        s = streams[i % 2]
+        with torch.cuda.stream(s):
+            out = torch.empty(c.T, 8, 128, dtype=torch.bfloat16, device="cuda")
+            lse = torch.empty(8, c.T, device="cuda")
+            bd.bd_paged_attn(c.plan, q, c.cache, out, lse)
+            outs.append((out, lse))
+    torch.cuda.synchronize()
+    for out, lse in outs:
+        assert torch.equal(out.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
+
+
+def test_stream_argument():
+    c = _mixed()
+    want = pu.run_attention(c)
+    s = torch.cuda.Stream()
+    got = pu.run_attention(c, stream=s)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_captured_step_replays_with_the_next_steps_plan():
+    """write + attention of a decode step captured once and replayed over three steps,
+    the device plan overwritten between them."""
+    H, Hkv, d, P = 8, 2, 128, 16
+    pages = [list(range(0, 320)), list(range(320, 340))]
+    kv0 = [5000, 250]
+    g = torch.Generator().manual_seed(2)
+    k = torch.randn(340, P, Hkv, d, generator=g).bfloat16().cuda()
+    v = torch.randn(340, P, Hkv, d, generator=g).bfloat16().cuda()
+    cache = bd.PagedCache(k, v)
+
+    def plan_of(step):
+        return bd.PagedPlan([1, 1], [n + step for n in kv0], pages, H, Hkv, d, page_size=P, num_pages=340)
+
+    plan = plan_of(1)
+    buf = torch.zeros(plan.nbytes // 4 + 64, dtype=torch.int32, device="cuda")
+    plan.upload(buffer=buf)
+    q, kn, vn = (torch.zeros(2, h, d, dtype=torch.bfloat16, device="cuda") for h in (H, Hkv, Hkv))
+    out, lse = torch.zeros(2, H, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(H, 2, device="cuda")
+    ws = torch.empty(bd.bd_paged_attn_workspace(plan), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):      # the first calls set kernel attributes
+        bd.bd_cache_write(plan, kn, vn, cache)
+        bd.bd_paged_attn(plan, q, cache, out, lse, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bd.bd_cache_write(plan, kn, vn, cache)
+        bd.bd_paged_attn(plan, q, cache, out, lse, ws)
+    for step in range(1, 4):
+        nxt = plan_of(step)
+        assert nxt.key() == plan.key()
+        nxt.upload(buffer=buf)
+        for t in (q, kn, vn):
+            t.copy_(torch.randn(t.shape, generator=g).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        for b in range(2):
+            n = kv0[b] + step
+            K, V = op.rows_of(k.cpu(), n, pages[b], P), op.rows_of(v.cpu(), n, pages[b], P)
+            assert torch.equal(K[-1], kn[b].cpu()) and torch.equal(V[-1], vn[b].cpu())
+            o, l, A, big = op.attention(q[b:b + 1].cpu(), K, V, n)
+            to, tl = pu.tolerances(d, n, A, big, "bf16")
+            assert ((out[b:b + 1].cpu().double() - o).abs() <= to).all() and ((lse[:, b:b + 1].cpu().double() - l).abs() <= tl).all()
+
+
+def test_nothing_new_and_nothing_cached():
+    c = pu.Case([0, 0], [20, 0], 8, 2, 128)
+    out = torch.full((1, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    k = torch.full((1, 2, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    bd.bd_paged_attn(c.plan, out, c.cache, out)
+    before = bits(c.k)
+    bd.bd_cache_write(c.plan, k, k, c.cache)
+    torch.cuda.synchronize()
+    assert (out == 7).all() and torch.equal(bits(c.k), before)
+    z = pu.Case([1], [0], 8, 2, 128)
+    bd.bd_cache_read(z.plan, z.cache, k, k)
+    torch.cuda.synchronize()
+    assert (k == 7).all()
+
+
+# ------------------------------------------------------------------ write and read
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", HEADS + [(10, 5, 128)])
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("new,kv", [([1], [1]), ([1, 0, 40, 300], [55, 20, 40, 700]), ([5, 3], [2, 0])])
+def test_write(new, kv, heads_first, H, Hkv, d, fmt):
+    c = pu.Case(new, kv, H, Hkv, d, fmt=fmt, heads_first=heads_first, seed=d, junk=0.5, pad_rows=2)
+    want = {n: getattr(c, n).cpu().clone().contiguous() for n in ("k", "v")}
+    exps = {n: getattr(c, n + "e").cpu().clone().contiguous() if fmt == "e4m3" else None for n in ("k", "v")}
+    # the rows come as slices of a fused projection
+    big = torch.randn(c.T + 2, 2 * Hkv * d + 64, generator=torch.Generator().manual_seed(d)).bfloat16()
+    if c.T > 4:   # values the format has to deal with: all zeros, subnormals, a row at a power's edge
+        big[0] = 0
+        big[1] = 2.0 ** -130
+        big[2, 64] = 448.0
+        big[3] *= 2.0 ** 40
+    dev = big.cuda()
+    kn, vn = (dev[:, 64 + i * Hkv * d:64 + (i + 1) * Hkv * d].view(c.T + 2, Hkv, d) for i in range(2))
+    bd.bd_cache_write(c.plan, kn, vn, c.cache)
+    torch.cuda.synchronize()
+    for t, s in enumerate(op.slots(new, kv, c.pages, c.page)):
+        if s < 0:
+            continue
+        for n, x in (("k", kn), ("v", vn)):
+            row = x[t].cpu()
+            if fmt == "bf16":
+                want[n][s // c.page, s % c.page] = row
+            else:
+                codes, e = op.quantise(row)
+                want[n].view(torch.uint8)[s // c.page, s % c.page] = codes
+                exps[n][s // c.page, s % c.page] = e
+    for n in ("k", "v"):
+        assert torch.equal(bits(getattr(c, n)), bits(want[n])), n
+        if fmt == "e4m3":
+            assert torch.equal(getattr(c, n + "e").cpu(), exps[n]), n
+
+
+def test_write_infinities_and_extremes():
+    c = pu.Case([6], [6], 4, 1, 64, fmt="e4m3", junk=0.0)
+    x = torch.randn(6, 1, 64, generator=torch.Generator().manual_seed(4)).bfloat16()
+    x[0, 0, 3], x[1, 0, 9], x[2, 0, 60] = float("inf"), float("nan"), float("-inf")
+    x[3] = 3e38          # past the largest exponent: saturates
+    x[4] = 1e-30         # below the smallest one: rounds to codes of 2^-60
+    bd.bd_cache_write(c.plan, x.cuda(), x.cuda(), c.cache)
+    out = torch.empty(6, 1, 64, dtype=torch.bfloat16, device="cuda")
+    bd.bd_cache_read(c.plan, c.cache, out, torch.empty_like(out))
+    torch.cuda.synchronize()
+    want = op.dequantise(*op.quantise(x))
+    got = out.cpu().double()
+    assert torch.isnan(got[:3]).all() and torch.equal(got[3:], want[3:])
+    assert (got[3] == 448.0 * 2.0 ** 60).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", HEADS + [(10, 5, 128)])
+@pytest.mark.parametrize("heads_first", [False, True])
+@pytest.mark.parametrize("kv", [[1], [16], [33, 0, 500, 7]])
+def test_read(kv, heads_first, H, Hkv, d, fmt):
+    c = pu.Case([0] * len(kv), kv, H, Hkv, d, page=32, fmt=fmt, heads_first=heads_first, seed=d)
+    n = sum(kv)
+    k = torch.full((n + 3, Hkv, 2 * d), 7.0, dtype=torch.bfloat16, device="cuda")[:, :, :d]
+    v = torch.full((n + 3, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    bd.bd_cache_read(c.plan, c.cache, k, v)
+    torch.cuda.synchronize()
+    assert (k[n:] == 7).all() and (v[n:] == 7).all()
+    K = torch.cat([c.rows(b)[0] for b in range(len(kv))])
+    V = torch.cat([c.rows(b)[1] for b in range(len(kv))])
+    assert torch.equal(k[:n].cpu().double(), K) and torch.equal(v[:n].cpu().double(), V)
+
+
+# ------------------------------------------------------------------ as they are used
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_prompt_then_chunk_then_decode(fmt):
+    """Packed prompts through the block-causal forward, their K/V written to the cache, a
+    chunk and then single rows attended over it: the same O as whole documents give, and
+    the rows read back feed the forward again."""
+    H, Hkv, d, P = 8, 2, 128, 16
+    lens, chunk, steps = [200, 37, 150], 70, 3
+    total = [n + chunk + steps for n in lens]
+    g = torch.Generator().manual_seed(9)
+    full = [[torch.randn(n, h, d, generator=g).bfloat16() for h in (H, Hkv, Hkv)] for n in total]
+    if fmt == "e4m3":   # whole documents of the values that the cache holds
+        for f in full:
+            for i in (1, 2):
+                f[i] = op.dequantise(*op.quantise(f[i])).bfloat16()
+    npg = [-(-n // P) for n in total]
+    num_pages = sum(npg)
+    perm = torch.randperm(num_pages, generator=g).tolist()
+    pages, at = [], 0
+    for n in npg:
+        pages.append(perm[at:at + n])
+        at += n
+    dt = torch.bfloat16 if fmt == "bf16" else torch.float8_e4m3fn
+    k = torch.full((num_pages, P, Hkv, d), 0xFF, dtype=torch.uint8, device="cuda").to(torch.float32)
+    k = k.fill_(float("nan")).to(dt)
+    v = k.clone()
+    ex = [torch.full((num_pages, P, Hkv), 255, dtype=torch.uint8, device="cuda") for _ in range(2)] if fmt == "e4m3" else [None] * 2
+    cache = bd.PagedCache(k, v, *ex)
+    done = [0] * 3
+
+    def step(new):
+        nonlocal done
+        kv = [a + b for a, b in zip(done, new)]
+        plan = bd.PagedPlan(new, kv, pages, H, Hkv, d, page_size=P, num_pages=num_pages, fmt=cache.fmt).upload("cuda")
+        q, kn, vn = (torch.cat([f[i][a:b] for f, a, b in zip(full, done, kv)]).cuda() for i in range(3))
+        bd.bd_cache_write(plan, kn, vn, cache)
+        out, lse = bd.paged_attn(plan, q, cache)
+        torch.cuda.synchronize()
+        bd.bd_check_status(plan)
+        at = 0
+        for b in range(3):
+            o, l, A, big = op.attention(full[b][0][done[b]:kv[b]], full[b][1][:kv[b]], full[b][2][:kv[b]], kv[b])
+            to, tl = pu.tolerances(d, kv[b], A, big, fmt)
+            assert ((out[at:at + new[b]].cpu().double() - o).abs() <= to).all(), (new, b)
+            assert ((lse[:, at:at + new[b]].cpu().double() - l).abs() <= tl).all(), (new, b)
+            at += new[b]
+        done = kv
+        return plan, q, out
+
+    # the prompts: the block-causal forward and the paged one agree
+    _, q, out = step(lens)
+    S = sum(lens)
+    cu = [0, lens[0], lens[0] + lens[1], S]
+    fp = bd.Plan([cu], S, 1, H, Hkv, d).upload("cuda")
+    kk, vv = (torch.cat([f[i][:n] for f, n in zip(full, lens)]).cuda() for i in (1, 2))
+    ref, _ = bd.attn_fwd(fp, q.view(1, 1, S, H, d), kk.view(1, 1, S, Hkv, d), vv.view(1, 1, S, Hkv, d))
+    torch.cuda.synchronize()
+    _, _, A, _ = op.attention(q.cpu(), kk.cpu(), vv.cpu(), S, causal=False)
+    assert ((ref.view(S, H, d) - out).abs().cpu().double() <= 4 * 2.0 ** -8 * 3).all()
+    step([chunk] * 3)
+    for _ in range(steps):
+        plan, _, _ = step([1] * 3)
+    n = sum(done)
+    kr, vr = (torch.empty(n, Hkv, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    bd.bd_cache_read(plan, cache, kr, vr)
+    torch.cuda.synchronize()
+    assert torch.equal(kr.cpu(), torch.cat([f[1] for f in full])) and torch.equal(vr.cpu(), torch.cat([f[2] for f in full]))
+
+
+def test_slices_join_by_lse():
+    """A context cut in two slices (as context-parallel ranks hold it), attended without a
+    causal mask and joined by the LSEs, is the whole."""
+    c = pu.Case([1], [900], 8, 2, 128, page=16)
+    K, V = c.rows(0)
+    parts = []
+    for lo, hi in ((0, 512), (512, 900)):
+        plan = bd.PagedPlan([1], [hi - lo], [c.pages[0][lo // 16:]], 8, 2, 128, page_size=16, num_pages=c.num_pages,
+                            causal=False).upload("cuda")
+        parts.append([t.cpu().double() for t in bd.paged_attn(plan, c.q.cuda(), c.cache)])
+    lse = torch.logaddexp(parts[0][1], parts[1][1])
+    out = sum(o * torch.exp(l - lse).t()[..., None] for o, l in parts)
+    want, wl, A, big = op.attention(c.q, K, V, 900)
+    to, tl = pu.tolerances(128, 900, A, big, "bf16")
+    assert ((out - want).abs() <= 2 * to).all() and ((lse - wl).abs() <= 2 * tl).all()
