@@ -94,6 +94,12 @@ int32_t make_tmap_rows_bf16(CUtensorMap* map, const bd_tensor* t, int64_t B, int
                    CU_TENSOR_MAP_SWIZZLE_NONE, cuuint32_t(box_rows), cuuint32_t(box_heads));
 }
 
+int32_t make_tmap_group_bf16(CUtensorMap* map, const bd_tensor* t, int64_t heads, int64_t d, const char* name,
+                             int box_heads, int box_rows) {
+  return make_tmap(map, t, 1, 1, heads, d, name, 2, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 64, CU_TENSOR_MAP_SWIZZLE_128B,
+                   cuuint32_t(box_rows), cuuint32_t(box_heads));
+}
+
 int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int64_t heads, int64_t d, int esize,
                         const char* name, int box_rows, int box_pieces) {
   auto fn = encode_fn();

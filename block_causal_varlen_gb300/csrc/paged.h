@@ -18,9 +18,9 @@ __device__ __forceinline__ float exp_factor(uint32_t b) {
   return b == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(b << 23);
 }
 
-// Partial results of the few-rows kernel: per slot m and l of its kDecRows rows,
-// then O [kDecRows][d]; the tile kernel's slots have kTileSlotRows rows.
-constexpr int kTileSlotRows = 256;
+// Partial results: per slot m and l of its rows, then O [rows][d]. The few-rows
+// kernel's slots have kDecRows rows, the tile kernel's tile_slot_rows(d): 128 for each
+// of its tiles of 128 / G new rows.
 __host__ __device__ constexpr int64_t slot_floats(int rows, int d) { return int64_t(rows) * (d + 2); }
 
 struct MergeArgs {
@@ -49,6 +49,8 @@ struct AttnArgs {
   float scale_log2;
 };
 
+int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, const bd_paged_cache* cache,
+                    cudaStream_t stream);
 int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* cache, cudaStream_t stream);
 
 }  // namespace bd

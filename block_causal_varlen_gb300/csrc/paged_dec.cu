@@ -539,14 +539,16 @@ __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) 
   __shared__ float s_m[8], s_l[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t* plan = a.plan;
-  const bool tile = ROWS == kTileSlotRows;
+  const bool tile = ROWS != kDecRows;
   const int n = plan[tile ? PH_NTILEM : PH_NDECM], G = plan[PH_G];
   const int32_t* list = plan + plan[tile ? PH_OFF_TILEM : PH_OFF_DECM];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
+  const int per = tile ? 128 / G * G : ROWS;  // rows in use of each 128 of a tile slot
   for (int x0 = blockIdx.x * RPB; x0 < n * ROWS; x0 += gridDim.x * RPB) {
     const int x = x0 + warp / WPR, r = x % ROWS;  // RPB divides ROWS: a block's rows are one entry's
     const int32_t* M = list + (x / ROWS) * kMergeWords;
-    const bool live = r < M[MG_NROWS];
+    const int br = tile ? (r >> 7) * per + (r & 127) : r;   // row of the block
+    const bool live = (!tile || (r & 127) < per) && br < M[MG_NROWS];
     if (WPR > 1 && !live) continue;  // the same for the whole block
     float acc[V], m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
@@ -601,7 +603,7 @@ __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) 
       }
     }
     if (live && sub == 0) {
-      const int nr = M[MG_ROW0] + r, h = M[MG_HKV] * G + nr % G, t = M[MG_Q0] + nr / G;
+      const int nr = M[MG_ROW0] + br, h = M[MG_HKV] * G + nr % G, t = M[MG_Q0] + nr / G;
       const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
       __nv_bfloat16* o = a.o + int64_t(t) * a.o_sr + int64_t(h) * a.o_sh + lane * V;
 #pragma unroll
@@ -649,8 +651,8 @@ cudaError_t launch_merge_t(const MergeArgs& a, cudaStream_t s) {
 int32_t launch_merge(const MergeArgs& a, int d, bool tile, cudaStream_t s) {
   cudaError_t e;
   if (tile)
-    e = d == 64 ? launch_merge_t<64, kTileSlotRows, 1>(a, s)
-        : d == 128 ? launch_merge_t<128, kTileSlotRows, 1>(a, s) : launch_merge_t<256, kTileSlotRows, 1>(a, s);
+    e = d == 64 ? launch_merge_t<64, tile_slot_rows(64), 1>(a, s)
+        : d == 128 ? launch_merge_t<128, tile_slot_rows(128), 1>(a, s) : launch_merge_t<256, tile_slot_rows(256), 1>(a, s);
   else
     e = d == 64 ? launch_merge_t<64, kDecRows, 8>(a, s)
         : d == 128 ? launch_merge_t<128, kDecRows, 8>(a, s) : launch_merge_t<256, kDecRows, 8>(a, s);
@@ -675,9 +677,13 @@ int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c,
 
 using namespace bd;
 
-// Partial results: at most two slots a CTA, whatever the lengths.
+// Partial results of the few-rows kernel, then of the tile kernel (kPagedSlots slots
+// each, whatever the lengths; none for a kernel that is not launched).
 static size_t dec_part_bytes(const int32_t* w) {
-  return w[PH_NDEC] ? size_t(2 * kPagedCtas) * slot_floats(kDecRows, w[PH_D]) * 4 : 0;
+  return w[PH_NDEC] ? size_t(kPagedSlots) * slot_floats(kDecRows, w[PH_D]) * 4 : 0;
+}
+static size_t part_bytes(const int32_t* w) {
+  return dec_part_bytes(w) + (w[PH_NTILE] ? size_t(kPagedSlots) * slot_floats(tile_slot_rows(w[PH_D]), w[PH_D]) * 4 : 0);
 }
 
 extern "C" int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes) {
@@ -685,7 +691,7 @@ extern "C" int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes)
   const int32_t* w = nullptr;
   int32_t st = view_paged_plan(plan_host, &w);
   if (st) return st;
-  *bytes = dec_part_bytes(w);
+  *bytes = part_bytes(w);
   return ok();
 }
 
@@ -696,7 +702,7 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   int32_t st = check_paged(plan_host, plan_dev, cache, &w);
   if (st) return st;
   if (w[PH_T] == 0) return ok();
-  if ((st = check_tensor(q, "q", 2, 1, 1, w[PH_H], false))) return st;
+  if ((st = check_tensor(q, "q", 2, 1, 1, w[PH_H], true))) return st;
   if ((st = check_tensor(out, "out", 2, 1, 1, w[PH_H], false))) return st;
   if (q->rows < w[PH_T] || out->rows < w[PH_T])
     return fail(BD_ERR_ARG, "q/out rows %d/%d < %d new rows of the plan", q->rows, out->rows, w[PH_T]);
@@ -704,7 +710,7 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
     return fail(BD_ERR_ARG, "lse: NULL pointer or not 4-byte aligned");
   if (lse && w[PH_H] > 1 && lse->stride_head < w[PH_T])
     return fail(BD_ERR_ARG, "lse stride_head %lld < %d rows", (long long)lse->stride_head, w[PH_T]);
-  const size_t need = dec_part_bytes(w);
+  const size_t need = part_bytes(w);
   if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256))
     return fail(BD_ERR_ARG, "workspace NULL or not 256-byte aligned");
   if (workspace_bytes < need) return fail(BD_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -723,10 +729,16 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   memcpy(&scale, &w[PH_SCALE_BITS], 4);
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const MergeArgs m = {a.plan, a.part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh};
+  MergeArgs m = {a.plan, a.part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh};
   if (w[PH_NDEC]) {
     if ((st = launch_dec(w, a, cache, s))) return st;
     if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, s))) return st;
+  }
+  if (w[PH_NTILE]) {
+    a.part += dec_part_bytes(w) / 4;
+    m.part = a.part;
+    if ((st = launch_tile(w, a, q, cache, s))) return st;
+    if (w[PH_NTILEM] && (st = launch_merge(m, w[PH_D], true, s))) return st;
   }
   return ok();
 }

@@ -37,6 +37,10 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
 
 namespace {
 
+// Sequences of at most this many (new row, head) pairs of a K/V head go to the few-rows
+// kernel, whose blocks hold kDecRows.
+constexpr int kDecMaxRows = kDecRows;
+
 struct Item {
   int32_t seq, hkv, row0, nrows, keys;
 };
@@ -108,6 +112,7 @@ void build_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
     p[PC_K0] = cut[i][1] * unit;
     p[PC_K1] = int32_t(std::min<int64_t>(it.keys, int64_t(cut[i][2]) * unit));
     p[PC_SLOT] = split ? slot : -1;
+    p[PC_T0] = it.row0 / (D.H / D.Hkv);
     L->pieces.insert(L->pieces.end(), p, p + kPieceWords);
     if (split && !later) {
       int32_t m[kMergeWords] = {0};
@@ -181,11 +186,13 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
   if (nitems > (1 << 26)) return fail(BD_ERR_CAPACITY, "plan of more than 2^26 row blocks");
   for (int32_t b = 0; b < D->B; ++b) {
     const int32_t q = D->q_len[b], n = D->kv_len[b], rows = q * G;
+    const bool few = rows <= kDecMaxRows;
+    const int32_t step = few ? kDecRows : 128 / G * G * tile_slots(D->d);
     for (int32_t g = 0; g < D->Hkv; ++g)
-      for (int32_t r0 = 0; r0 < rows; r0 += kDecRows) {
-        const int32_t r1 = std::min(rows, r0 + kDecRows);
+      for (int32_t r0 = 0; r0 < rows; r0 += step) {
+        const int32_t r1 = std::min(rows, r0 + step);
         const int64_t seen = D->causal ? int64_t(n) - q + (r1 - 1) / G + 1 : n;
-        dec.push_back({b, g, r0, r1 - r0, int32_t(std::max<int64_t>(0, seen))});
+        (few ? dec : tile).push_back({b, g, r0, r1 - r0, int32_t(std::max<int64_t>(0, seen))});
       }
   }
   build_lists(*D, dec, q0, page_off, kDecUnit, 3, &X->dec);

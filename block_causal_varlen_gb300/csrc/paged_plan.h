@@ -16,6 +16,12 @@ constexpr int32_t kPagedVersion = 1;
 constexpr int kPagedCtas = 152;
 constexpr int kDecRows = 16;   // (new row, query head) pairs of one K/V head in a few-rows block
 constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cut
+// Tiles (of 128 / G new rows x G heads) of one K/V head that share a key tile in the
+// tile kernel, and the rows of its partial-result slots.
+constexpr int tile_slots(int d) { return d == 256 ? 1 : 2; }
+constexpr int tile_slot_rows(int d) { return 128 * tile_slots(d); }
+// At most this many partial results of a kind: the workspace's size.
+constexpr int kPagedSlots = 2 * kPagedCtas;
 
 // header words (the failure status keeps the place it has in attention plans, so
 // that bd_check_status reads either)
@@ -50,7 +56,8 @@ enum : int {
   PC_NROWS,     // rows of the block that exist
   PC_K0, PC_K1, // keys [k0, k1); k0 a multiple of the kernel's unit
   PC_SLOT,      // partial-result slot, -1: the whole key range, written to the output
-  PC_RESERVED0, PC_RESERVED1,
+  PC_T0,        // PC_ROW0 / G: the block's first new row
+  PC_RESERVED0,
   kPieceWords = 12
 };
 

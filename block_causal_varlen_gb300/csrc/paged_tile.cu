@@ -1,0 +1,665 @@
+// Attention of many query rows over a paged K/V cache on sm_103a: 128-row tiles on
+// the tcgen05 tensor cores.
+//
+// Per row i: O_i = sum_j 2^(s_ij - m_i) v_j / l_i over the keys j below the row's
+// limit, s_ij = log2(e) q_i . k_j / sqrt(d), in one pass over key tiles of 128
+// (bd_paged_dec_kernel gives the formulas; this kernel takes the blocks whose rows
+// fill enough of a tile).
+//
+// A tile's 128 rows are (new row, head of the group) pairs of ONE K/V head, new-row-
+// major: 128 / G new rows of all G heads. Every key tile in shared memory then serves
+// 128 rows per slot however the group is shaped, and the causal edge of a tile is
+// 128 / G positions wide instead of 128. Two slots (one at head dim 256, whose O
+// takes half of TMEM) take neighbouring tiles and the same K/V; while one slot's
+// softmax runs, the tensor core works on the other.
+//
+//   warp 0       TMA: Q tiles (a box of G heads x 128 / G rows), then the key tiles, one
+//                box per page (32 lanes look up and issue pages at once)
+//   warps 1, 2   one thread per slot issues its tcgen05 products, taking turns:
+//                S = Q K^T into TMEM, O += P V with P read from TMEM
+//   warp 3       bf16: clears V rows past the keys' end (a page's unused rows may hold
+//                anything, and 0 x NaN is NaN)
+//   warps 4-11   softmax, thread = row; they also store the results
+//   warps 12-15  e4m3 only: turn raw tiles into bf16 ones. A code's bits, shifted into
+//                a bf16, are its value times 2^-120; one packed multiplication by
+//                2^(120 + e) gives the exact value (e: the row's exponent)
+// Work comes from the plan: every CTA walks its own list of pieces (block, key range).
+// A piece that is not its block's whole key range stores m, l and O for the join.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <atomic>
+#include <cstring>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace bd {
+using namespace dev;
+
+namespace {
+
+template <int D, int FMT>
+struct TileCfg {
+  static constexpr bool kF8 = FMT == BD_CACHE_E4M3;
+  static constexpr int kSlots = tile_slots(D);
+  static constexpr int kTileBytes = 128 * D * 2;  // 128 rows x D bf16
+  static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 4;
+  static constexpr int kRawBytes = kF8 ? 128 * D : 0;
+  static constexpr int kRawStages = !kF8 ? 0 : D == 256 ? 1 : D == 128 ? 2 : 4;  // K, V, K, V, ...
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kSlots * kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * kTileBytes;
+  static constexpr int kOffRaw = kOffV + kStages * kTileBytes;
+  static constexpr int kOffBar = kOffRaw + kRawStages * kRawBytes;
+  static constexpr int kOffPieces = kOffBar + 512;
+  static constexpr int kPre = 16;                 // pieces kept in shared memory
+  static constexpr int kSmem = kOffPieces + kPre * kPieceWords * 4 + 1024;  // + alignment slack
+  static constexpr int kOCol = 256;               // first O column in TMEM
+  static constexpr int kThreads = kF8 ? 512 : 384;
+  // registers after setmaxnreg: warps 0-3, the softmax warps, the converting warps
+  static constexpr int kRegsCtl = kF8 ? 56 : 72, kRegsSoftmax = kF8 ? 200 : 216, kRegsConv = 56;
+  static constexpr int kRegsLaunch = kF8 ? 128 : 168;
+  static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kF8 ? 128 * kRegsConv : 0) <= kRegsLaunch * kThreads,
+                "register split exceeds the launch's registers");
+  static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
+  static_assert(kOCol + kSlots * D <= 512, "O accumulators exceed TMEM");
+};
+
+// barrier indices (8 bytes each)
+enum : int {
+  T_QFULL = 0, T_QEMPTY, T_KFULL = 4, T_KEMPTY = 8, T_VFULL = 12, T_VEMPTY = 16, T_RFULL = 20, T_REMPTY = 24,
+  T_SFULL = 28, T_PFULL = 30, T_OFINAL = 32, T_OEMPTY = 34, T_TURN = 36, T_DRAIN = 38, T_VTAIL = 40, T_COUNT = 44
+};
+static_assert(8 * T_COUNT + 16 <= 512, "barriers, TMEM slot and abort flag overflow their region");
+
+struct Piece {
+  int q0, qlen, kvlen, pages, hkv, t0, k0, k1, slot, nt, ns;
+};
+
+__device__ __forceinline__ uint32_t lop_and_or(uint32_t a, uint32_t m, uint32_t b) { return (a & m) | b; }
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+  uint32_t r;  // subnormal operands keep their values
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// the codes in bytes 0, 1 (sel 0x1404) or 2, 3 (0x3424) of x as a bf16 pair times 2^-120
+__device__ __forceinline__ uint32_t e4m3x2_bits(uint32_t x, uint32_t sel) {
+  const uint32_t t = __byte_perm(x, 0u, sel);
+  return lop_and_or(t, 0x80008000u, (t >> 4) & 0x07f007f0u);
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
+    bd_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
+  using Cfg = TileCfg<D, FMT>;
+  constexpr bool F8 = Cfg::kF8;
+  constexpr int NS = Cfg::kSlots, NST = Cfg::kStages, NR = F8 ? Cfg::kRawStages : 1;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t sQ = sbase + Cfg::kOffQ, sK = sbase + Cfg::kOffK, sV = sbase + Cfg::kOffV, sR = sbase + Cfg::kOffRaw;
+  const uint32_t bars = sbase + Cfg::kOffBar;
+  auto bar = [&](int i) { return bars + 8u * i; };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffBar + 8 * T_COUNT);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffBar + 8 * T_COUNT + 8);
+  int32_t* pre = reinterpret_cast<int32_t*>(smem + Cfg::kOffPieces);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int32_t* plan = a.plan;
+  const int32_t* first = plan + plan[PH_OFF_TILE];
+  const int32_t* pieces = first + kPagedCtas + 1;
+  const int p0 = first[blockIdx.x], p1 = first[blockIdx.x + 1];
+  if (p0 == p1) return;
+  const int G = plan[PH_G], causal = plan[PH_CAUSAL], pshift = plan[PH_PAGE_SHIFT];
+  const int TPS = 128 / G;   // new rows of a slot's tile
+  for (int i = threadIdx.x; i < min(p1 - p0, Cfg::kPre) * kPieceWords; i += Cfg::kThreads)
+    pre[i] = pieces[p0 * kPieceWords + i];
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar(T_QFULL), 1);
+    mbar_init(bar(T_QEMPTY), NS);
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar(T_KFULL + s), F8 ? 128 : 1);
+      mbar_init(bar(T_KEMPTY + s), NS);
+      mbar_init(bar(T_VFULL + s), F8 ? 128 : 1);
+      mbar_init(bar(T_VEMPTY + s), NS);
+      mbar_init(bar(T_VTAIL + s), 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(bar(T_RFULL + s), 1);
+      mbar_init(bar(T_REMPTY + s), 128);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(T_SFULL + s), 1);
+      mbar_init(bar(T_PFULL + s), 128);
+      mbar_init(bar(T_OFINAL + s), 1);
+      mbar_init(bar(T_OEMPTY + s), 128);
+      mbar_init(bar(T_TURN + s), 1);
+      mbar_init(bar(T_DRAIN + s), 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto piece = [&](int p) {
+    const int32_t* W = p - p0 < Cfg::kPre ? pre + (p - p0) * kPieceWords : pieces + p * kPieceWords;
+    Piece P;
+    P.q0 = W[PC_Q0]; P.qlen = W[PC_QLEN]; P.kvlen = W[PC_KVLEN]; P.pages = W[PC_PAGES]; P.hkv = W[PC_HKV];
+    P.t0 = W[PC_T0]; P.k0 = W[PC_K0]; P.k1 = W[PC_K1]; P.slot = W[PC_SLOT];
+    P.nt = (P.k1 - P.k0 + 127) >> 7;
+    P.ns = NS == 2 && P.t0 + TPS < P.qlen ? 2 : 1;
+    return P;
+  };
+
+  if (warp < 4) {
+    regs_set<Cfg::kRegsCtl, Cfg::kRegsLaunch>();
+    if (warp == 0) {
+      // -------------------------------------------------------- producer (whole warp)
+      const int rows = min(1 << pshift, 128);   // rows of a copy
+      const int rshift = min(pshift, 7);
+      const int row_bytes = F8 && D == 64 ? 64 : 128;
+      constexpr int kPieces = F8 ? (D + 127) / 128 : D / 64;
+      uint32_t it = 0, rit = 0, qi = 0;
+      bool ok = true;
+      // one matrix of the key tile at `pos`, `n` copies, into `dst`
+      auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t full, int n, int pos, int page, int hkv) {
+        if (lane == 0) mbar_expect_tx(full, uint32_t(n * rows * row_bytes * kPieces));
+        __syncwarp();
+        if (lane < n) {
+          const int row = (pos + lane * rows) & ((1 << pshift) - 1);
+#pragma unroll
+          for (int c = 0; c < kPieces; ++c)
+            tma_load_5d(dst + c * 128 * row_bytes + lane * rows * row_bytes, m, full, 0, row, c, hkv, page);
+        }
+        __syncwarp();
+      };
+      for (int p = p0; p < p1 && ok; ++p) {
+        const Piece P = piece(p);
+        if (P.nt == 0) continue;
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_QEMPTY), (qi & 1) ^ 1, abort_flag)))) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(T_QFULL), uint32_t(P.ns * TPS * G * D * 2));
+          for (int s = 0; s < P.ns; ++s)
+            for (int c = 0; c < D / 64; ++c)
+              tma_load_5d(sQ + s * Cfg::kTileBytes + c * 16384, &tm_q, bar(T_QFULL), c * 64, P.hkv * G,
+                          P.q0 + P.t0 + s * TPS, 0, 0);
+        }
+        __syncwarp();
+        ++qi;
+        // this lane's page of a tile; the next tile's is fetched one tile ahead
+        auto page_of = [&](int pos) { return pos + lane * rows < P.k1 && lane * rows < 128 ? plan[P.pages + ((pos + lane * rows) >> pshift)] : 0; };
+        int page = page_of(P.k0);
+        for (int j = 0; j < P.nt; ++j, ++it) {
+          const int pos = P.k0 + 128 * j;
+          const int n = (min(P.k1 - pos, 128) + rows - 1) >> rshift;
+          const int next = j + 1 < P.nt ? page_of(pos + 128) : 0;
+          if constexpr (!F8) {
+            const int s = it % NST;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_KEMPTY + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
+            load(&tm_k, sK + s * Cfg::kTileBytes, bar(T_KFULL + s), n, pos, page, P.hkv);
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_VEMPTY + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
+            // a tile with rows past the keys' end goes by way of warp 3
+            load(&tm_v, sV + s * Cfg::kTileBytes, bar((pos + 128 > P.k1 ? T_VTAIL : T_VFULL) + s), n, pos, page, P.hkv);
+          } else {
+            for (int h = 0; h < 2 && ok; ++h, ++rit) {
+              const int s = rit % NR;
+              if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_REMPTY + s), ((rit / NR) & 1) ^ 1, abort_flag)))) break;
+              load(h ? &tm_v : &tm_k, sR + s * Cfg::kRawBytes, bar(T_RFULL + s), n, pos, page, P.hkv);
+            }
+            if (!ok) break;
+          }
+          page = next;
+        }
+      }
+      if (!ok) {
+        // let copies already issued land before the CTA's shared memory goes away (what
+        // has landed returns at once; each wait is bounded)
+        if constexpr (!F8) {
+          for (int s = 0; s < NST; ++s) {
+            const uint32_t lk = it + 1;  // K may be one tile further than V
+            for (uint32_t x = lk > uint32_t(NST) ? lk - NST : 0; x < lk; ++x)
+              if (int(x % NST) == s) mbar_wait_drain(bar(T_KFULL + s), (x / NST) & 1);
+            if (it > 0 && it > uint32_t(s)) {
+              const uint32_t last = it - 1 - ((it - 1 - s) % NST);
+              mbar_wait_drain(bar(T_VFULL + s), (last / NST) & 1);
+            }
+          }
+        } else {
+          for (int s = 0; s < NR; ++s)
+            if (rit > uint32_t(s)) {
+              const uint32_t last = rit - 1 - ((rit - 1 - s) % NR);
+              mbar_wait_drain(bar(T_RFULL + s), (last / NR) & 1);
+            }
+        }
+        if (qi > 0) mbar_wait_drain(bar(T_QFULL), (qi - 1) & 1);
+      }
+    } else if (warp == 1 || (warp == 2 && NS == 2)) {
+      // -------------------------------------------------------- MMA issuers, one per slot
+      if (lane == 0) {
+        const int s = warp - 1;
+        uint32_t my_turn = 0;  // groups (a product P V and the next S) this slot has passed
+        auto take_turn = [&]() -> bool {
+          if (NS == 1 || (s == 0 && my_turn == 0)) return true;
+          const uint32_t k = s == 0 ? my_turn - 1 : my_turn;
+          return mbar_wait_spin(bar(T_TURN + s), k & 1, abort_flag);
+        };
+        auto pass_turn = [&]() {
+          if (NS == 2) mbar_arrive(bar(T_TURN + (s ^ 1)));
+          ++my_turn;
+        };
+        constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
+        const uint32_t d_s = tmem + s * 128, d_o = tmem + Cfg::kOCol + s * D;
+        const uint32_t qa = sdesc_lo(sQ + s * Cfg::kTileBytes, 16);
+        auto issue_s = [&](int st) {
+          const uint32_t kb = sdesc_lo(sK + st * Cfg::kTileBytes, 16);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = uint32_t(((kk >> 2) * 16384 + (kk & 3) * 32) >> 4);
+            mma_ss_lo(d_s, qa + off, kb + off, idS, kk > 0);
+          }
+        };
+        auto issue_pv = [&](int st, bool acc) {
+          const uint32_t vb = sdesc_lo(sV + st * Cfg::kTileBytes, 16384);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_ts_lo(d_o, d_s + kk * 8, vb + uint32_t(kk * 128), idPV, (acc || kk > 0) ? 1u : 0u);
+        };
+        // it: key tiles (stages); qi: blocks; tc, ai: this slot's tiles and blocks
+        uint32_t it = 0, qi = 0, tc = 0, ai = 0;
+        bool ok = true;
+        for (int p = p0; p < p1 && ok; ++p) {
+          const Piece P = piece(p);
+          if (P.nt == 0) continue;
+          const bool act = s < P.ns;
+          if (!(ok = mbar_wait(bar(T_QFULL), qi & 1, abort_flag))) break;
+          ++qi;
+          {
+            const int sk = it % NST;
+            if (!(ok = mbar_wait(bar(T_KFULL + sk), (it / NST) & 1, abort_flag))) break;
+            if (!(ok = take_turn())) break;
+            if (act) {
+              tc_fence_after();
+              issue_s(sk);
+              pass_turn();
+              tc_commit(bar(T_SFULL + s));
+              tc_commit(bar(T_KEMPTY + sk));
+              if (P.nt == 1) tc_commit(bar(T_QEMPTY));
+            } else {
+              pass_turn();
+              mbar_arrive(bar(T_KEMPTY + sk));
+              if (P.nt == 1) mbar_arrive(bar(T_QEMPTY));
+            }
+          }
+          for (int j = 1; j <= P.nt; ++j) {
+            const uint32_t itp = it + j - 1, itn = it + j;
+            const int svp = itp % NST, skn = itn % NST;
+            if (act) {
+              if (!(ok = mbar_wait_spin(bar(T_PFULL + s), (tc + j - 1) & 1, abort_flag))) break;
+              if (j == 1 && !(ok = mbar_wait(bar(T_OEMPTY + s), (ai & 1) ^ 1, abort_flag))) break;
+            }
+            if (!(ok = mbar_wait(bar(T_VFULL + svp), (itp / NST) & 1, abort_flag))) break;
+            if (j < P.nt && !(ok = mbar_wait(bar(T_KFULL + skn), (itn / NST) & 1, abort_flag))) break;
+            if (!(ok = take_turn())) break;
+            if (act) {
+              tc_fence_after();
+              issue_pv(svp, j > 1);
+              if (j < P.nt) issue_s(skn);
+              pass_turn();
+              tc_commit(bar(T_VEMPTY + svp));
+              if (j < P.nt) {
+                tc_commit(bar(T_SFULL + s));
+                tc_commit(bar(T_KEMPTY + skn));
+                if (j == P.nt - 1) tc_commit(bar(T_QEMPTY));
+              } else {
+                tc_commit(bar(T_OFINAL + s));
+              }
+            } else {
+              pass_turn();
+              mbar_arrive(bar(T_VEMPTY + svp));
+              if (j < P.nt) {
+                mbar_arrive(bar(T_KEMPTY + skn));
+                if (j == P.nt - 1) mbar_arrive(bar(T_QEMPTY));
+              }
+            }
+          }
+          it += P.nt;
+          if (act) {
+            tc += P.nt;
+            ++ai;
+          }
+        }
+        if (!ok) {
+          tc_commit(bar(T_DRAIN + s));
+          mbar_wait_drain(bar(T_DRAIN + s), 0);
+        }
+      }
+    } else if (warp == 3 && !F8) {
+      // -------------------------------------------------------- V rows past the keys' end
+      // Such a tile's load completes T_VTAIL of its stage; this warp completes T_VFULL.
+      uint32_t it = 0, parity = 0;  // bit s: phase of T_VTAIL + s (a stage's next such load waits for its products)
+      for (int p = p0; p < p1; ++p) {
+        const Piece P = piece(p);
+        it += P.nt;
+        if (P.nt == 0 || !(P.k1 & 127)) continue;
+        const int st = (it - 1) % NST;
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(T_VTAIL + st), (parity >> st) & 1, abort_flag))) break;
+        parity ^= 1u << st;
+        const uint32_t v = sV + st * Cfg::kTileBytes;
+        const int r0 = P.k1 & 127;
+        for (int i = lane; i < (128 - r0) * 8; i += 32)   // 16-byte pieces of those rows
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) st_shared_v4(v + c * 16384 + (r0 * 8 + i) * 16, 0u, 0u, 0u, 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(T_VFULL + st));
+      }
+    }
+  } else if (warp < 12) {
+    regs_set<Cfg::kRegsSoftmax, Cfg::kRegsLaunch>();
+    // ---------------------------------------------------------- softmax
+    const int s = (warp - 4) >> 2, quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // row within the tile == TMEM lane
+    const uint32_t lane_base = uint32_t(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_base + s * 128, tO = tmem + lane_base + Cfg::kOCol + s * D;
+    const int tl = r / G, hg = r - tl * G;
+    uint32_t tc = 0, ai = 0;
+    bool ok = s < NS;
+    for (int p = p0; p < p1 && ok; ++p) {
+      const Piece P = piece(p);
+      if (s >= P.ns) continue;
+      const int t = P.t0 + s * TPS + tl, h = P.hkv * G + hg;
+      const bool live = tl < TPS && t < P.qlen;
+      const int lim = !live ? 0 : causal ? P.kvlen - P.qlen + t + 1 : P.kvlen;
+      __nv_bfloat16* orow = a.o + int64_t(P.q0 + t) * a.o_sr + int64_t(h) * a.o_sh;
+      float* part = P.slot < 0 ? nullptr : a.part + int64_t(P.slot) * slot_floats(tile_slot_rows(D), D);
+      if (P.nt == 0) {  // rows that see nothing
+        if (live) {
+#pragma unroll
+          for (int k = 0; k < D / 8; ++k) reinterpret_cast<uint4*>(orow)[k] = make_uint4(0, 0, 0, 0);
+          if (a.lse) a.lse[int64_t(h) * a.l_sh + P.q0 + t] = -CUDART_INF_F;
+        }
+        continue;
+      }
+      float m_run = -CUDART_INF_F, l_run = 0.f;
+      for (int j = 0; j < P.nt; ++j, ++tc) {
+        // (warps leave together: what follows is warp-wide)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_SFULL + s), tc & 1, abort_flag)))) break;
+        tc_fence_after();
+        uint32_t u[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, u[q]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) reg_fence(u[q]);
+        float x[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[q * 32 + e] = __uint_as_float(u[q][e]);
+        // the row sees the tile's columns below n; per group of 32 columns the warp
+        // skips what no row sees and leaves alone what every row sees
+        const int n = lim - (P.k0 + 128 * j);
+        uint32_t gone = 0;
+        if (__any_sync(0xffffffffu, n < 128)) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (__all_sync(0xffffffffu, n <= 32 * q)) {
+              gone |= 1u << q;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[32 * q + e] = -CUDART_INF_F;
+            } else if (!__all_sync(0xffffffffu, n >= 32 * q + 32)) {
+              const int c = n - 32 * q;
+              const uint32_t seen = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[32 * q + e] = (seen & (1u << e)) ? x[32 * q + e] : -CUDART_INF_F;
+            }
+          }
+        }
+        float m8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m8[k] = -CUDART_INF_F;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (!(gone & (1u << q)))
+#pragma unroll
+            for (int e = 32 * q; e < 32 * q + 32; e += 16)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) m8[k] = max3f(m8[k], x[e + k], x[e + 8 + k]);
+        const float mx = fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(max3f(m8[3], m8[4], m8[5]), m8[6], m8[7]));
+        const float m_new = fmaxf(m_run, mx * a.scale_log2);
+        const bool need = m_new > m_run + 8.0f;  // O is rescaled only when the maximum grows by more than 2^8
+        float factor = 1.f;
+        if (need) {
+          factor = ex2(m_run - m_new);
+          l_run *= factor;
+          m_run = m_new;
+        }
+        if (__any_sync(0xffffffffu, need && j > 0)) {
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t ov[32];
+            tmem_ld32(tO + q * 32, ov);
+            tmem_ld_wait();
+            reg_fence(ov);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * factor);
+            tmem_st32(tO + q * 32, ov);
+          }
+        }
+        const float m_eff = (m_run == -CUDART_INF_F) ? 0.f : m_run;
+        const float2 cs = make_float2(a.scale_log2, a.scale_log2), cm = make_float2(-m_eff, -m_eff);
+        float2 s4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[2][32];
+#pragma unroll
+        for (int e = 0; e < 64; ++e) {
+          float2 v = ffma2(make_float2(x[2 * e], x[2 * e + 1]), cs, cm);
+          v.x = ex2(v.x);
+          v.y = ex2(v.y);
+          s4[e & 3] = fadd2(s4[e & 3], v);
+          pk[e >> 5][e & 31] = pack_bf16(v.x, v.y);
+        }
+        const float2 st = fadd2(fadd2(s4[0], s4[1]), fadd2(s4[2], s4[3]));
+        l_run += st.x + st.y;
+        tmem_st32(tS, pk[0]);
+        tmem_st32(tS + 32, pk[1]);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(T_PFULL + s));
+      }
+      if (!ok) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_OFINAL + s), ai & 1, abort_flag)))) break;
+      tc_fence_after();
+      ++ai;
+      // NaN scores leave the maximum alone: what they gave was taken relative to 0
+      const float m_fin = m_run == -CUDART_INF_F && l_run != 0.f ? 0.f : m_run;
+      const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+      if (part) {
+        if (live) {
+          part[s * 128 + r] = m_fin;
+          part[tile_slot_rows(D) + s * 128 + r] = l_run;
+        }
+      } else if (live && a.lse) {
+        a.lse[int64_t(h) * a.l_sh + P.q0 + t] =
+            l_run == 0.f ? -CUDART_INF_F : (m_fin + lg2(l_run)) * 0.69314718055994531f;
+      }
+      float* prow = part ? part + 2 * tile_slot_rows(D) + int64_t(s * 128 + r) * D : nullptr;
+      constexpr int QH = D <= 128 ? D / 32 : 1;  // 32-column groups taken out of TMEM at a time
+#pragma unroll 1
+      for (int q0 = 0; q0 < D / 32; q0 += QH) {
+        __syncwarp();
+        uint32_t ov[QH][32];
+#pragma unroll
+        for (int q = 0; q < QH; ++q) tmem_ld32(tO + (q0 + q) * 32, ov[q]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < QH; ++q) reg_fence(ov[q]);
+        if (q0 + QH == D / 32) {  // the next block's first product may overwrite O
+          tc_fence_before();
+          mbar_arrive(bar(T_OEMPTY + s));
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int q = 0; q < QH; ++q) {
+          if (part) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              reinterpret_cast<uint4*>(prow + (q0 + q) * 32)[k] =
+                  make_uint4(ov[q][4 * k], ov[q][4 * k + 1], ov[q][4 * k + 2], ov[q][4 * k + 3]);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = pack_bf16(__uint_as_float(ov[q][8 * k + 2 * e]) * inv, __uint_as_float(ov[q][8 * k + 2 * e + 1]) * inv);
+              reinterpret_cast<uint4*>(orow + (q0 + q) * 32)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+      }
+    }
+  } else {
+    if constexpr (F8) {
+      regs_set<Cfg::kRegsConv, Cfg::kRegsLaunch>();
+      // -------------------------------------------------------- raw tiles to bf16, thread = key
+      const int r = threadIdx.x - 384;
+      uint32_t it = 0, rit = 0;
+      bool ok = true;
+      // codes of this thread's row (at `src`) times 2^e into the bf16 tile at `dst`
+      auto convert = [&](uint32_t src, uint32_t dst, uint32_t byte, bool zero) {
+        const int e = int(byte) - 127;
+        // 2^(120 + e) fits a bf16 up to e = 7; what is left of a larger one is a second factor
+        const uint32_t f1 = zero ? 0u : byte == 255u ? 0x7fc0u : uint32_t(127 + 120 + min(e, 7)) << 7;
+        const uint32_t m1 = f1 | (f1 << 16), f2 = uint32_t(127 + max(e, 7) - 7) << 7, m2 = f2 | (f2 << 16);
+        const bool big = byte != 255u && e > 7;
+        constexpr int PB = D == 64 ? 64 : 128;  // bytes of a raw row's piece
+#pragma unroll 2
+        for (int c = 0; c < D / 16; ++c) {      // 16 codes: two 16-byte pieces of bf16
+          const int pc = c * 16 / PB, cc = c % (PB / 16);
+          const uint32_t at = src + pc * 128 * PB + r * PB + (D == 64 ? ((cc ^ ((r >> 1) & 3)) << 4) : ((cc ^ (r & 7)) << 4));
+          const uint4 u = ld_shared_u4(at);
+          uint32_t w[8];
+          w[0] = e4m3x2_bits(u.x, 0x1404); w[1] = e4m3x2_bits(u.x, 0x3424);
+          w[2] = e4m3x2_bits(u.y, 0x1404); w[3] = e4m3x2_bits(u.y, 0x3424);
+          w[4] = e4m3x2_bits(u.z, 0x1404); w[5] = e4m3x2_bits(u.z, 0x3424);
+          w[6] = e4m3x2_bits(u.w, 0x1404); w[7] = e4m3x2_bits(u.w, 0x3424);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = zero ? 0u : hmul2_bf16(w[i], m1);
+          if (big)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = hmul2_bf16(w[i], m2);
+          const uint32_t d = dst + (c >> 2) * 16384 + r * 128;
+          const int oc = (c & 3) * 2;
+          st_shared_v4(d + ((oc ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+          st_shared_v4(d + (((oc + 1) ^ (r & 7)) << 4), w[4], w[5], w[6], w[7]);
+        }
+        fence_proxy_async_smem();
+      };
+      for (int p = p0; p < p1 && ok; ++p) {
+        const Piece P = piece(p);
+        // this row's exponents come one tile ahead, its page number two
+        auto page_of = [&](int j) {
+          const int pos = P.k0 + 128 * j + r;
+          return j < P.nt && pos < P.k1 ? plan[P.pages + (pos >> pshift)] : -1;
+        };
+        auto exps_of = [&](int j, int page) -> uint32_t {
+          if (page < 0) return 127u | (127u << 8);
+          const int64_t o = int64_t(page) * a.e_sp + int64_t((P.k0 + 128 * j + r) & ((1 << pshift) - 1)) * a.e_sr + int64_t(P.hkv) * a.e_sh;
+          return uint32_t(a.k_exp[o]) | (uint32_t(a.v_exp[o]) << 8);
+        };
+        int pg = page_of(0);
+        uint32_t ex = exps_of(0, pg);
+        pg = page_of(1);
+        for (int j = 0; j < P.nt; ++j, ++it) {
+          const uint32_t now = ex;
+          ex = exps_of(j + 1, pg);
+          pg = page_of(j + 2);
+          const int s = it % NST;
+          const bool past = P.k0 + 128 * j + r >= P.k1;
+          for (int h = 0; h < 2; ++h, ++rit) {
+            const int rs = rit % NR;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_RFULL + rs), (rit / NR) & 1, abort_flag)))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar((h ? T_VEMPTY : T_KEMPTY) + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
+            convert(sR + rs * Cfg::kRawBytes, (h ? sV : sK) + s * Cfg::kTileBytes, (now >> (8 * h)) & 255u, past);
+            mbar_arrive(bar(T_REMPTY + rs));
+            mbar_arrive(bar((h ? T_VFULL : T_KFULL) + s));
+          }
+          if (!ok) break;
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && *abort_flag) {
+    atomicExch(const_cast<int32_t*>(plan) + PH_STATUS, DEV_TIMEOUT);
+    atomicExch(const_cast<int32_t*>(plan) + PH_STATUS_DETAIL, 6);
+  }
+}
+
+template <int D, int FMT>
+int32_t launch_tile_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a,
+                      cudaStream_t s) {
+  using Cfg = TileCfg<D, FMT>;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(bd_paged_tile_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged tile)");
+    cudaFuncAttributes fa;
+    e = cudaFuncGetAttributes(&fa, bd_paged_tile_kernel<D, FMT>);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes(paged tile)");
+    // setmaxnreg.inc waits until registers are free: never launch a split that cannot be met
+    if (fa.numRegs != Cfg::kRegsLaunch)
+      return fail(BD_ERR_UNSUPPORTED, "paged tile kernel built with %d registers/thread, its register split assumes %d",
+                  fa.numRegs, Cfg::kRegsLaunch);
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  bd_paged_tile_kernel<D, FMT><<<kPagedCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a);
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_tile_kernel launch");
+}
+
+}  // namespace
+
+int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, const bd_paged_cache* c, cudaStream_t s) {
+  const int es = c->fmt == BD_CACHE_BF16 ? 2 : 1, d = w[PH_D], G = w[PH_G];
+  const int rows = w[PH_PAGE] < 128 ? w[PH_PAGE] : 128;
+  CUtensorMap mq, mk, mv;
+  int32_t st;
+  if ((st = make_tmap_group_bf16(&mq, q, w[PH_H], d, "q", G, 128 / G))) return st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", rows, 1))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", rows, 1))) return st;
+  if (c->fmt == BD_CACHE_BF16)
+    return d == 64 ? launch_tile_t<64, BD_CACHE_BF16>(mq, mk, mv, a, s)
+           : d == 128 ? launch_tile_t<128, BD_CACHE_BF16>(mq, mk, mv, a, s)
+                      : launch_tile_t<256, BD_CACHE_BF16>(mq, mk, mv, a, s);
+  return d == 64 ? launch_tile_t<64, BD_CACHE_E4M3>(mq, mk, mv, a, s)
+         : d == 128 ? launch_tile_t<128, BD_CACHE_E4M3>(mq, mk, mv, a, s)
+                    : launch_tile_t<256, BD_CACHE_E4M3>(mq, mk, mv, a, s);
+}
+
+}  // namespace bd

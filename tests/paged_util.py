@@ -74,7 +74,7 @@ class Case:
                 op.rows_of(self.vd, self.kv[b], self.pages[b], self.page))
 
 
-def tolerances(d, keys, A, big, fmt):
+def tolerances(d, keys, A, big, fmt, rows=1):
     """(O, LSE) bounds. A = sum p |v| per output, big = max_j sum |q k_j| / sqrt(d) per row.
     Score: products of the operands are exact in fp32, their sum of d terms is off by at
     most d 2^-24 of the sum of magnitudes (twice that allows for chopped additions), the
@@ -82,13 +82,15 @@ def tolerances(d, keys, A, big, fmt):
     2^-22 of the same: ds = (2 d + 8) 2^-24 big, plus 2^-22 for the exponential itself.
     l: a sum of `keys` terms in parts: keys 2^-24 relative at most; the logarithm 2^-21
     absolute and its rounding 2^-23 of |LSE| (< 64 here: 2^-17).
-    O: P rounded to half a step (bf16 2^-8, fp16 2^-11 of each term, which sum to at most
-    that times A; fp16 terms below 2^-31 of the largest vanish: keys 2^-31 A' is below
-    that), products summed as above, and the output rounded by 2^-8 of itself (applied
+    O: P rounded to half a step (2^-11 of each term where it is fp16: e4m3 caches, `rows`
+    (new row, head) pairs of a K/V head up to 16, i.e. the few-rows kernel; 2^-8 where it
+    is bf16, i.e. bf16 caches and the tile kernel, whose e4m3 tiles are bf16 by then),
+    which sum to at most that times A (fp16 terms below 2^-31 of the largest vanish:
+    keys 2^-31 A' is below that), products summed as above, and the output rounded by 2^-8 of itself (applied
     to A, which is no smaller)."""
     ds = (2 * d + 8) * 2.0 ** -24 * big + 2.0 ** -22
     ls = ds + keys * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -17
-    p = 2.0 ** -8 if fmt == "bf16" else 2.0 ** -11
+    p = 2.0 ** -11 if fmt == "e4m3" and rows <= 16 else 2.0 ** -8
     o = A * (p + 2.0 ** -8) * 1.01 + A * (2 * ls.t()[..., None] + 2 * keys * 2.0 ** -24) + 1e-30
     return o, ls
 
@@ -100,7 +102,7 @@ def check_attention(case, out, lse):
         if n:
             k, v = case.rows(b)
             o_ref, l_ref, A, big = op.attention(case.q[at:at + n], k, v, kv, case.causal)
-            tol_o, tol_l = tolerances(case.d, max(kv, 1), A, big, case.fmt)
+            tol_o, tol_l = tolerances(case.d, max(kv, 1), A, big, case.fmt, n * case.H // case.Hkv)
             got, gl = out[at:at + n].double(), lse[:, at:at + n].double()
             empty = torch.isneginf(l_ref)
             assert torch.equal(torch.isneginf(gl), empty), f"sequence {b}: rows that see nothing"
