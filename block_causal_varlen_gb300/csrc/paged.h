@@ -30,6 +30,7 @@ struct MergeArgs {
   int64_t o_sr, o_sh;
   float* lse;
   int64_t l_sh;
+  int32_t G;
 };
 
 // Joins the split blocks of the few-rows (tile = false) or the tile kernel.
@@ -47,6 +48,7 @@ struct AttnArgs {
   const uint8_t *k_exp, *v_exp;
   int64_t e_sp, e_sr, e_sh;
   float scale_log2;
+  int32_t G, causal, page_shift;
 };
 
 int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, const bd_paged_cache* cache,

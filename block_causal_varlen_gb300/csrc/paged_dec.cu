@@ -53,13 +53,17 @@ struct DecCfg {
   static constexpr int kWarps = kStageBytes >= 16384 ? 4 : 8;
   static constexpr int kStages = kStageBytes >= 16384 ? 3 : kStageBytes == 8192 ? 3 : kStageBytes == 4096 ? 5 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kCols = 32, kColPad = 36;              // columns added up at a time
+  // values of a warp added up at a time: 4, 8 or 16 rows of 128, 64 or 32 columns (+ 4)
+  static constexpr int kSumFloats = 16 * 36;
   static constexpr int kOffRing = 0;
   static constexpr int kOffSum = kOffRing + kWarps * kStages * kStageBytes;
-  static constexpr int kOffMl = kOffSum + kWarps * 16 * kColPad * 4;   // m, l [kWarps][16]
+  static constexpr int kOffMl = kOffSum + kWarps * kSumFloats * 4;     // m, l [kWarps][16]
   static constexpr int kOffInv = kOffMl + kWarps * 16 * 2 * 4;         // 1 / l of the block's rows
-  static constexpr int kOffRef = kOffInv + 16 * 4;                     // exponent offsets [kWarps][kStages]
-  static constexpr int kOffBar = kOffRef + kWarps * kStages * 8;
+  // e4m3: 4-byte words around K's (lanes 0-15) and V's exponent bytes of a chunk, and the
+  // low bits of their addresses
+  static constexpr int kOffExp = kOffInv + 16 * 4;                     // [kWarps][kStages][32]
+  static constexpr int kOffRef = kOffExp + (kF8 ? kWarps * kStages * 128 : 0);
+  static constexpr int kOffBar = kOffRef + (kF8 ? kWarps * kStages * 8 : 0);
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmem = kOffAbort + 16 + 1024;         // + alignment slack
   static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
@@ -142,19 +146,23 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffAbort);
   const uint32_t ring = sbase + Cfg::kOffRing + warp * NST * Cfg::kStageBytes;
   const uint32_t bars = sbase + Cfg::kOffBar + warp * NST * 8;
-  volatile int64_t* eref = reinterpret_cast<volatile int64_t*>(smem + Cfg::kOffRef) + warp * NST;
+  volatile uint32_t* eref = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffRef) + warp * NST;
+  const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * 128 + lane * 4;
+  const uint8_t* ebase = lane < 16 ? a.k_exp : a.v_exp;
   const int32_t* plan = a.plan;
-  const int32_t* first = plan + plan[PH_OFF_DEC];
-  const int32_t* pieces = first + kPagedCtas + 1;
-  const int p0 = first[blockIdx.x], p1 = first[blockIdx.x + 1];
+  const int32_t* rec = plan + kOffDecRec + blockIdx.x * kRecordWords;
+  const int p0 = rec[RC_P0], p1 = rec[RC_P1];
   if (p0 == p1) return;
+  const int32_t* pieces = plan + plan[PH_OFF_DEC];
+  auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
-    for (int s = 0; s < NST; ++s) mbar_init(bars + 8 * s, 1);
+    // a chunk's arrivals: the copies' and, e4m3, every lane's exponent word
+    for (int s = 0; s < NST; ++s) mbar_init(bars + 8 * s, F8 ? 33 : 1);
     fence_barrier_init();
   }
   __syncthreads();
-  const int G = plan[PH_G], causal = plan[PH_CAUSAL], pshift = plan[PH_PAGE_SHIFT];
+  const int G = a.G, causal = a.causal, pshift = a.page_shift;
 
   // ---- loads: a cursor over this warp's chunks of all pieces, NST chunks ahead of
   // the products. The next chunk's page number is fetched when the one before is
@@ -164,7 +172,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
     ck += kChunk * NW;
     while (ck >= ck1) {
       if (++cp >= p1) return;
-      const int32_t* W = pieces + cp * kPieceWords;
+      const int32_t* W = piece(cp);
       ck = W[PC_K0] + kChunk * warp;
       ck1 = W[PC_K1];
       chkv = W[PC_HKV];
@@ -175,8 +183,17 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
   auto issue = [&](uint32_t it) {
     if (cp >= p1) return;
     const int s = int(it % NST), row = ck & ((1 << pshift) - 1);
+    if constexpr (F8) {
+      const int64_t o = int64_t(cpage) * a.e_sp + int64_t(row) * a.e_sr + int64_t(chkv) * a.e_sh;
+      if (lane == 0) eref[s] = uint32_t(o);
+      const uintptr_t at = reinterpret_cast<uintptr_t>(ebase + o + int64_t(lane & 15) * a.e_sr) & ~uintptr_t(3);
+      asm volatile(
+          "cp.async.ca.shared.global [%0], [%1], 4;\n\t"
+          "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];" ::"r"(exps + s * 128),
+          "l"(at), "r"(bars + 8 * s)
+          : "memory");
+    }
     if (lane == 0) {
-      if constexpr (F8) eref[s] = int64_t(cpage) * a.e_sp + int64_t(row) * a.e_sr + int64_t(chkv) * a.e_sh;
       const uint32_t dst = ring + s * Cfg::kStageBytes;
       mbar_expect_tx(bars + 8 * s, Cfg::kStageBytes);
       tma_load_5d(dst, &tm_k, bars + 8 * s, 0, row, 0, chkv, cpage);
@@ -184,22 +201,15 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
     }
     next_chunk();
   };
-  // exponent bytes of a chunk: lane l < 16 holds K's and V's of key l
-  auto load_exps = [&](uint32_t it, bool any) -> uint32_t {
-    if (!F8 || !any || lane >= 16) return 0u;
-    const int64_t o = eref[it % NST] + int64_t(lane) * a.e_sr;
-    return uint32_t(a.k_exp[o]) | (uint32_t(a.v_exp[o]) << 8);
-  };
 
   next_chunk();
   uint32_t issued = 0, it = 0;
   bool ok = true;
   for (; issued < uint32_t(NST) && cp < p1; ++issued) issue(issued);
   __syncwarp();
-  uint32_t ex = load_exps(0, issued > 0);
 
   for (int p = p0; p < p1; ++p) {
-    const int32_t* W = pieces + p * kPieceWords;
+    const int32_t* W = piece(p);
     const int q0 = W[PC_Q0], qlen = W[PC_QLEN], kvlen = W[PC_KVLEN], hkv = W[PC_HKV], row0 = W[PC_ROW0];
     const int nrows = W[PC_NROWS], k0 = W[PC_K0], k1 = W[PC_K1], slot = W[PC_SLOT];
     // ---- the two rows of this lane: their q as A fragments, the keys they see
@@ -267,8 +277,6 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
     for (int k = k0 + kChunk * warp; k < k1; k += kChunk * NW, ++it) {
       const uint32_t st = ring + (it % NST) * Cfg::kStageBytes;
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (it % NST), (it / NST) & 1, abort_flag))) ok = false;
-      const uint32_t ex_now = ex;
-      ex = load_exps(it + 1, it + 1 < issued);
       // ---- S = q . k: two tiles of 8 keys
       float s[2][4];
 #pragma unroll
@@ -310,9 +318,14 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
       // (ve: V's; vp: the same plus P's shift, NaN for a V row of NaN)
       float kf[4] = {1.f, 1.f, 1.f, 1.f}, ve[4] = {0.f, 0.f, 0.f, 0.f}, vp[4] = {0.f, 0.f, 0.f, 0.f};
       if constexpr (F8) {
+        // lanes 0-15: the bytes of K and V of key `lane`
+        uint32_t ex, low = (uint32_t(reinterpret_cast<uintptr_t>(ebase)) + eref[it % NST] + uint32_t(lane & 15) * uint32_t(a.e_sr)) & 3u;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ex) : "r"(exps + (it % NST) * 128) : "memory");
+        ex = (ex >> (8 * low)) & 255u;
+        ex |= __shfl_xor_sync(0xffffffffu, ex, 16) << 8;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const uint32_t b = __shfl_sync(0xffffffffu, ex_now, 8 * (x >> 1) + 2 * j + (x & 1));
+          const uint32_t b = __shfl_sync(0xffffffffu, ex, 8 * (x >> 1) + 2 * j + (x & 1));
           kf[x] = exp_factor(b & 255u);
           ve[x] = float(int(b >> 8) - 127);
           vp[x] = (b >> 8) == 255u ? __uint_as_float(0x7fc00000u) : ve[x] + kPShift;
@@ -489,27 +502,44 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
             M == -CUDART_INF_F ? -CUDART_INF_F : (M + lg2(L)) * 0.69314718055994531f;
       }
     }
+    // as many columns at a time as fit for the block's rows
+    const int rl = nrows <= 4 ? 2 : nrows <= 8 ? 3 : 4, tl = 6 - rl;  // log2 of rows, of column tiles
+    const int cols = 8 << tl, pitch = cols + 4;
+    for (int ps = 0; ps << tl < NT; ++ps) {
+      if (ps) __syncthreads();
 #pragma unroll
-    for (int c0 = 0; c0 < NT; c0 += 4) {
-      if (c0) __syncthreads();
+      for (int n = 0; n < NT; ++n)
+        if (n >> tl == ps)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (rw + 8 * i < nrows)
-            *reinterpret_cast<float2*>(&sum[(warp * 16 + rw + 8 * i) * Cfg::kColPad + 8 * n + 2 * j]) =
-                make_float2(o[c0 + n][2 * i] * fac[i], o[c0 + n][2 * i + 1] * fac[i]);
+          for (int i = 0; i < 2; ++i)
+            if (rw + 8 * i < nrows)
+              *reinterpret_cast<float2*>(&sum[warp * Cfg::kSumFloats + (rw + 8 * i) * pitch + 8 * (n - (ps << tl)) + 2 * j]) =
+                  make_float2(o[n][2 * i] * fac[i], o[n][2 * i + 1] * fac[i]);
       __syncthreads();
-      for (int x = threadIdx.x; x < nrows * Cfg::kCols; x += Cfg::kThreads) {
-        const int r = x / Cfg::kCols, c = x % Cfg::kCols;
-        float t = 0.f;
+      const int cw = min(cols, D - ps * cols) >> 1;  // column pairs of this round
+      for (int x = threadIdx.x; x < nrows * cw; x += Cfg::kThreads) {
+        const int r = x / cw, c = 2 * (x - r * cw);
+        float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < NW; ++w) t += sum[(w * 16 + r) * Cfg::kColPad + c];
-        const int col = o_column<D, F8>(c0 + (c >> 3), c & 7), n = row0 + r;
+        for (int w = 0; w < NW; ++w) {
+          const float2 u = *reinterpret_cast<const float2*>(&sum[w * Cfg::kSumFloats + r * pitch + c]);
+          t.x += u.x;
+          t.y += u.y;
+        }
+        const int nt = (ps << tl) + (c >> 3), c0 = o_column<D, F8>(nt, c & 7), c1 = o_column<D, F8>(nt, (c & 7) + 1);
+        const int n = row0 + r;
         if (part) {
-          part[2 * kDecRows + r * D + col] = t;
+          float* P = part + 2 * kDecRows + r * D;
+          P[c0] = t.x;
+          P[c1] = t.y;
         } else {
-          a.o[int64_t(q0 + n / G) * a.o_sr + int64_t(hkv * G + n % G) * a.o_sh + col] = __float2bfloat16_rn(t * inv[r]);
+          __nv_bfloat16* O = a.o + int64_t(q0 + n / G) * a.o_sr + int64_t(hkv * G + n % G) * a.o_sh;
+          if constexpr (F8) {
+            O[c0] = __float2bfloat16_rn(t.x * inv[r]);
+            O[c1] = __float2bfloat16_rn(t.y * inv[r]);
+          } else {
+            *reinterpret_cast<uint32_t*>(O + c0) = pack_bf16(t.x * inv[r], t.y * inv[r]);
+          }
         }
       }
     }
@@ -540,8 +570,8 @@ __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t* plan = a.plan;
   const bool tile = ROWS != kDecRows;
-  const int n = plan[tile ? PH_NTILEM : PH_NDECM], G = plan[PH_G];
-  const int32_t* list = plan + plan[tile ? PH_OFF_TILEM : PH_OFF_DECM];
+  const int n = plan[tile ? PH_NTILEM : PH_NDECM], G = a.G;
+  const int32_t* list = plan + (tile ? kOffTileMerge : kOffDecMerge);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
   const int per = tile ? 128 / G * G : ROWS;  // rows in use of each 128 of a tile slot
   for (int x0 = blockIdx.x * RPB; x0 < n * ROWS; x0 += gridDim.x * RPB) {
@@ -729,7 +759,8 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   memcpy(&scale, &w[PH_SCALE_BITS], 4);
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  MergeArgs m = {a.plan, a.part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh};
+  a.G = w[PH_G]; a.causal = w[PH_CAUSAL]; a.page_shift = w[PH_PAGE_SHIFT];
+  MergeArgs m = {a.plan, a.part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh, a.G};
   if (w[PH_NDEC]) {
     if ((st = launch_dec(w, a, cache, s))) return st;
     if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, s))) return st;

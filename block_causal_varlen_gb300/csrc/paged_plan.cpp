@@ -2,16 +2,17 @@
 // the plan blob the kernels read.
 //
 // The attention's work is cut on the host. A block of query rows (the (new row,
-// query head) pairs of one K/V head) and its keys are an item; items in batch
-// order form one long line of key units, and every CTA takes an equal stretch of
-// it, so a CTA holds whole items and at most two parts of items cut at its ends.
-// Parts write partial results (running maximum, sum, unnormalised O) that a second
-// kernel joins. One long sequence is thereby spread over every SM, and a ragged
-// batch leaves none idle, without counters or atomics on the device.
+// query head) pairs of one K/V head) and its keys are an item; items are given out
+// whole or cut by keys, so that every CTA gets about the same number of key units.
+// Parts of cut items write partial results (running maximum, sum, unnormalised O)
+// that a second kernel joins. One long sequence is thereby spread over every SM, and
+// a ragged batch leaves none idle, without counters or atomics on the device.
 #include <algorithm>
-#include <array>
 #include <cmath>
 #include <cstring>
+#include <functional>
+#include <queue>
+#include <utility>
 #include <vector>
 
 #include "common.h"
@@ -25,11 +26,11 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
   if (w[PH_MAGIC] != kPagedMagic || w[PH_VERSION] != kPagedVersion)
     return fail(BD_ERR_PLAN, "not a paged plan blob (bad magic/version)");
   const int64_t words = w[PH_WORDS];
-  auto in = [&](int64_t off, int64_t n, int stride) { return off >= kPagedHdrWords && n >= 0 && off + n * stride <= words; };
+  auto in = [&](int64_t off, int64_t n, int stride) { return off >= kOffLists && n >= 0 && off + n * stride <= words; };
   if (!in(w[PH_OFF_TOK], w[PH_T], 1) || !in(w[PH_OFF_PAGES], w[PH_NPAGES], 1) || !in(w[PH_OFF_PGROW], w[PH_NPAGES], 1) ||
-      !in(w[PH_OFF_PGCNT], w[PH_NPAGES], 1) || !in(w[PH_OFF_DEC] + kPagedCtas + 1, w[PH_NDEC], kPieceWords) ||
-      !in(w[PH_OFF_DECM], w[PH_NDECM], kMergeWords) || !in(w[PH_OFF_TILE] + kPagedCtas + 1, w[PH_NTILE], kPieceWords) ||
-      !in(w[PH_OFF_TILEM], w[PH_NTILEM], kMergeWords))
+      !in(w[PH_OFF_PGCNT], w[PH_NPAGES], 1) || !in(w[PH_OFF_DEC], w[PH_NDEC], kPieceWords) ||
+      !in(w[PH_OFF_TILE], w[PH_NTILE], kPieceWords) || w[PH_NDECM] < 0 || w[PH_NDECM] > kPagedSlots / 2 ||
+      w[PH_NTILEM] < 0 || w[PH_NTILEM] > kPagedSlots / 2)
     return fail(BD_ERR_PLAN, "paged plan blob offsets are inconsistent");
   *out = w;
   return BD_OK;
@@ -45,31 +46,36 @@ struct Item {
   int32_t seq, hkv, row0, nrows, keys;
 };
 
+// Some key units of an item, and the CTA that takes them.
+struct Part {
+  int32_t item, u0, u1, cta;
+};
+
 struct Lists {
-  std::vector<int32_t> first;  // [kPagedCtas + 1] first piece of every CTA
+  std::vector<int32_t> records;  // [kPagedCtas][kRecordWords]
   std::vector<int32_t> pieces, merges;
 };
 
-// Whether the items fit into n stretches of cost t (in key units; a piece costs
-// its units plus `over`). `cut`, if given, receives every piece as (item, first
-// unit, end unit, CTA).
-bool fits(const std::vector<Item>& items, int unit, int over, int64_t t, int n,
-          std::vector<std::array<int32_t, 4>>* cut) {
+int32_t units_of(const Item& it, int unit) { return int32_t((int64_t(it.keys) + unit - 1) / unit); }
+
+// Cuts the items, in order, into n stretches of at most `t` key units, where a part
+// costs its units plus `over`; false if they do not fit.
+bool stretch(const std::vector<Item>& items, int unit, int over, int64_t t, int n, std::vector<Part>* parts) {
   int cta = 0;
   int64_t cap = t;
   for (size_t i = 0; i < items.size(); ++i) {
-    const int32_t units = (items[i].keys + unit - 1) / unit;
+    const int32_t units = units_of(items[i], unit);
     int32_t at = 0;
     for (;;) {
       const int64_t rem = units - at;
       if (rem + over <= cap) {
-        if (cut) cut->push_back({int32_t(i), at, units, cta});
+        if (parts) parts->push_back({int32_t(i), at, units, cta});
         cap -= rem + over;
         break;
       }
       const int64_t part = std::min(cap - over, rem - 1);
       if (part >= 1) {
-        if (cut) cut->push_back({int32_t(i), at, int32_t(at + part), cta});
+        if (parts) parts->push_back({int32_t(i), at, int32_t(at + part), cta});
         at += int32_t(part);
       } else if (cap == t) {
         return false;
@@ -81,50 +87,141 @@ bool fits(const std::vector<Item>& items, int unit, int over, int64_t t, int n,
   return true;
 }
 
-void build_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
-                 const std::vector<int32_t>& page_off, int unit, int over, Lists* L) {
-  L->first.assign(kPagedCtas + 1, 0);
-  if (items.empty()) return;
+// The shortest stretches that hold everything: equal work for every CTA, at most two
+// parts of cut items in each.
+int64_t cut_evenly(const std::vector<Item>& items, int unit, int over, std::vector<Part>* parts) {
   int64_t total = 0;
-  for (const Item& it : items) total += (it.keys + unit - 1) / unit + over;
-  // smallest stretch that holds everything
+  for (const Item& it : items) total += units_of(it, unit) + over;
   int64_t lo = std::max<int64_t>(over + 1, (total + kPagedCtas - 1) / kPagedCtas), hi = lo;
-  while (!fits(items, unit, over, hi, kPagedCtas, nullptr)) {
+  while (!stretch(items, unit, over, hi, kPagedCtas, nullptr)) {
     lo = hi + 1;
     hi += std::max<int64_t>(1, hi / 8);
   }
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
-    if (fits(items, unit, over, mid, kPagedCtas, nullptr)) hi = mid;
+    if (stretch(items, unit, over, mid, kPagedCtas, nullptr)) hi = mid;
     else lo = mid + 1;
   }
-  std::vector<std::array<int32_t, 4>> cut;
-  fits(items, unit, over, hi, kPagedCtas, &cut);
-  int32_t slot = 0, cta = 0;
-  for (size_t i = 0; i < cut.size(); ++i) {
-    const Item& it = items[cut[i][0]];
-    const bool more = i + 1 < cut.size() && cut[i + 1][0] == cut[i][0], later = i > 0 && cut[i - 1][0] == cut[i][0];
-    const bool split = more || later;
-    while (cta <= cut[i][3]) L->first[cta++] = int32_t(i);
+  stretch(items, unit, over, hi, kPagedCtas, parts);
+  return hi;
+}
+
+// Items of more than `most` units in equal parts, the longest part first to the CTA
+// with the least; returns the longest load, or -1 if the parts of cut items are more
+// than there are slots.
+int64_t cut_longest(const std::vector<Item>& items, int unit, int over, int64_t most, std::vector<Part>* parts) {
+  parts->clear();
+  int64_t split = 0;
+  for (size_t i = 0; i < items.size(); ++i) {
+    const int64_t units = units_of(items[i], unit), n = std::max<int64_t>(1, (units + most - 1) / most);
+    if (n > 1 && (split += n) > kPagedSlots) return -1;
+    for (int64_t k = 0; k < n; ++k)
+      parts->push_back({int32_t(i), int32_t(units * k / n), int32_t(units * (k + 1) / n), 0});
+  }
+  std::stable_sort(parts->begin(), parts->end(), [](const Part& a, const Part& b) { return a.u1 - a.u0 > b.u1 - b.u0; });
+  typedef std::pair<int64_t, int> Load;
+  std::priority_queue<Load, std::vector<Load>, std::greater<Load>> ctas;
+  for (int c = 0; c < kPagedCtas; ++c) ctas.push({0, c});
+  int64_t longest = 0;
+  for (Part& p : *parts) {
+    Load l = ctas.top();
+    ctas.pop();
+    p.cta = l.second;
+    l.first += p.u1 - p.u0 + over;
+    longest = std::max(longest, l.first);
+    ctas.push(l);
+  }
+  std::stable_sort(parts->begin(), parts->end(), [](const Part& a, const Part& b) { return a.cta < b.cta; });
+  return longest;
+}
+
+// Writes the parts (in CTA order) down as pieces, records and joins.
+void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<Part>& parts,
+                 const std::vector<int32_t>& q0, const std::vector<int32_t>& page_off, int unit, Lists* L) {
+  L->records.assign(size_t(kPagedCtas) * kRecordWords, 0);
+  // slots of an item's parts in key order, items in order
+  std::vector<int32_t> count(items.size(), 0), slot0(items.size(), -1);
+  for (const Part& p : parts) ++count[p.item];
+  int32_t slots = 0;
+  for (size_t i = 0; i < items.size(); ++i) {
+    if (count[i] < 2) continue;
+    const Item& it = items[i];
+    int32_t m[kMergeWords] = {0};
+    slot0[i] = m[MG_SLOT0] = slots;
+    m[MG_N] = count[i]; m[MG_Q0] = q0[it.seq]; m[MG_HKV] = it.hkv; m[MG_ROW0] = it.row0; m[MG_NROWS] = it.nrows;
+    L->merges.insert(L->merges.end(), m, m + kMergeWords);
+    slots += count[i];
+  }
+  std::vector<std::vector<int32_t>> starts(items.size());  // first units of a cut item's parts
+  for (const Part& p : parts)
+    if (slot0[p.item] >= 0) starts[p.item].push_back(p.u0);
+  for (auto& v : starts) std::sort(v.begin(), v.end());
+  for (size_t i = 0; i < parts.size(); ++i) {
+    const Part& x = parts[i];
+    const Item& it = items[x.item];
     int32_t p[kPieceWords] = {0};
     p[PC_Q0] = q0[it.seq]; p[PC_QLEN] = D.q_len[it.seq]; p[PC_KVLEN] = D.kv_len[it.seq];
     p[PC_PAGES] = page_off[it.seq]; p[PC_HKV] = it.hkv; p[PC_ROW0] = it.row0; p[PC_NROWS] = it.nrows;
-    p[PC_K0] = cut[i][1] * unit;
-    p[PC_K1] = int32_t(std::min<int64_t>(it.keys, int64_t(cut[i][2]) * unit));
-    p[PC_SLOT] = split ? slot : -1;
+    p[PC_K0] = x.u0 * unit;
+    p[PC_K1] = int32_t(std::min<int64_t>(it.keys, int64_t(x.u1) * unit));
     p[PC_T0] = it.row0 / (D.H / D.Hkv);
+    p[PC_SLOT] = -1;
+    if (slot0[x.item] >= 0) {
+      const auto& v = starts[x.item];
+      p[PC_SLOT] = slot0[x.item] + int32_t(std::lower_bound(v.begin(), v.end(), x.u0) - v.begin());
+    }
     L->pieces.insert(L->pieces.end(), p, p + kPieceWords);
-    if (split && !later) {
-      int32_t m[kMergeWords] = {0};
-      m[MG_SLOT0] = slot; m[MG_Q0] = q0[it.seq]; m[MG_HKV] = it.hkv; m[MG_ROW0] = it.row0; m[MG_NROWS] = it.nrows;
-      L->merges.insert(L->merges.end(), m, m + kMergeWords);
+    int32_t* R = &L->records[size_t(x.cta) * kRecordWords];
+    if (R[RC_P1] == 0) {
+      R[RC_P0] = int32_t(i);
+      std::copy(p, p + kPieceWords, R + RC_PIECE);
     }
-    if (split) {
-      ++L->merges[L->merges.size() - kMergeWords + MG_N];
-      ++slot;
-    }
+    R[RC_P1] = int32_t(i) + 1;
   }
-  while (cta <= kPagedCtas) L->first[cta++] = int32_t(cut.size());
+}
+
+// Few-rows blocks: short against their keys, cheap to join: always cut evenly. A
+// piece's own cost is some 3 units of 32 keys.
+void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
+               const std::vector<int32_t>& page_off, Lists* L) {
+  std::vector<Part> parts;
+  if (!items.empty()) cut_evenly(items, kDecUnit, 3, &parts);
+  write_lists(D, items, parts, q0, page_off, kDecUnit, L);
+}
+
+// Tiles: a partial result is up to 256 rows of O in fp32, written and read again, so
+// blocks are cut only where that shortens the whole: the best of no cuts, equal parts
+// of the longest blocks, and an even cut, by their longest load in key tiles (a piece
+// costs one more, a join of n partial results about 3 + n / 50).
+void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
+                const std::vector<int32_t>& page_off, Lists* L) {
+  std::vector<Part> best, parts;
+  if (!items.empty()) {
+    int64_t total = 0;
+    for (const Item& it : items) total += units_of(it, kTile) + 1;
+    const int64_t share = (total + kPagedCtas - 1) / kPagedCtas;
+    int64_t least = cut_longest(items, kTile, 1, INT32_MAX, &best);
+    auto joined = [&](const std::vector<Part>& v) {
+      std::vector<int32_t> count(items.size(), 0);
+      for (const Part& p : v) ++count[p.item];
+      int64_t n = 0;
+      for (int32_t c : count) n += c > 1 ? c : 0;
+      return n ? 3 + n / 50 : 0;
+    };
+    for (int k = 1; k <= 4 && least > share; ++k) {
+      const int64_t most = std::max<int64_t>(1, share / k), t = cut_longest(items, kTile, 1, most, &parts);
+      if (t < 0) break;
+      const int64_t cost = t + joined(parts);
+      if (cost < least) {
+        least = cost;
+        best.swap(parts);
+      }
+    }
+    parts.clear();
+    const int64_t t = cut_evenly(items, kTile, 1, &parts);
+    if (t + joined(parts) < least) best.swap(parts);
+  }
+  write_lists(D, items, best, q0, page_off, kTile, L);
 }
 
 int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npages) {
@@ -171,7 +268,7 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
   if (st) return st;
   const int G = D->H / D->Hkv;
   std::vector<int32_t> q0(D->B), page_off(D->B);
-  int64_t t = 0, pg = kPagedHdrWords + X->T;
+  int64_t t = 0, pg = kOffLists + X->T;
   for (int32_t b = 0; b < D->B; ++b) {
     q0[b] = int32_t(t);
     page_off[b] = int32_t(pg);
@@ -195,18 +292,16 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
         (few ? dec : tile).push_back({b, g, r0, r1 - r0, int32_t(std::max<int64_t>(0, seen))});
       }
   }
-  build_lists(*D, dec, q0, page_off, kDecUnit, 3, &X->dec);
-  build_lists(*D, tile, q0, page_off, kTile, 1, &X->tile);
+  dec_lists(*D, dec, q0, page_off, &X->dec);
+  tile_lists(*D, tile, q0, page_off, &X->tile);
   return BD_OK;
 }
 
+// The pieces are read 16 bytes at a time: each list starts on a multiple of 4 words.
+int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
+
 int64_t total_words(const Built& X) {
-  // the lists are read 16 bytes at a time: each starts on a multiple of 4 words
-  auto up = [](int64_t n) { return (n + 3) / 4 * 4; };
-  int64_t w = up(kPagedHdrWords + X.T + 3 * X.npages);
-  for (const Lists* L : {&X.dec, &X.tile})
-    w = up(w + 3 + kPagedCtas + 1) + int64_t(L->pieces.size()) + int64_t(L->merges.size());
-  return up(w);
+  return up4(kOffLists + X.T + 3 * X.npages) + int64_t(X.dec.pieces.size()) + int64_t(X.tile.pieces.size());
 }
 
 }  // namespace
@@ -248,7 +343,7 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
   const float scale = 1.0f / std::sqrt(float(D.d));
   std::memcpy(&w[PH_SCALE_BITS], &scale, 4);
   w[PH_NPAGES] = int32_t(X.npages);
-  w[PH_OFF_TOK] = kPagedHdrWords;
+  w[PH_OFF_TOK] = kOffLists;
   w[PH_OFF_PAGES] = int32_t(w[PH_OFF_TOK] + X.T);
   w[PH_OFF_PGROW] = int32_t(w[PH_OFF_PAGES] + X.npages);
   w[PH_OFF_PGCNT] = int32_t(w[PH_OFF_PGROW] + X.npages);
@@ -278,24 +373,18 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
   w[PH_WRITE_OK] = D.causal;
   for (size_t i = 1; i < written.size(); ++i)
     if (written[i].lo < written[i - 1].hi) w[PH_WRITE_OK] = 0;
-  int64_t at = kPagedHdrWords + X.T + 3 * X.npages;
-  at = (at + 3) / 4 * 4;
-  auto put = [&](const Lists& L, int off, int n, int offm, int nm) {
-    // the CTA table's end, where the pieces start, is a multiple of 4 words
-    while ((at + kPagedCtas + 1) % 4) ++at;
+  int64_t at = up4(kOffLists + X.T + 3 * X.npages);
+  auto put = [&](const Lists& L, int off, int n, int nm, int rec, int mrg) {
     w[off] = int32_t(at);
     w[n] = int32_t(L.pieces.size() / kPieceWords);
-    std::copy(L.first.begin(), L.first.end(), w + at);
-    at += kPagedCtas + 1;
+    w[nm] = int32_t(L.merges.size() / kMergeWords);
+    std::copy(L.records.begin(), L.records.end(), w + rec);
+    std::copy(L.merges.begin(), L.merges.end(), w + mrg);
     std::copy(L.pieces.begin(), L.pieces.end(), w + at);
     at += int64_t(L.pieces.size());
-    w[offm] = int32_t(at);
-    w[nm] = int32_t(L.merges.size() / kMergeWords);
-    std::copy(L.merges.begin(), L.merges.end(), w + at);
-    at += int64_t(L.merges.size());
   };
-  put(X.dec, PH_OFF_DEC, PH_NDEC, PH_OFF_DECM, PH_NDECM);
-  put(X.tile, PH_OFF_TILE, PH_NTILE, PH_OFF_TILEM, PH_NTILEM);
+  put(X.dec, PH_OFF_DEC, PH_NDEC, PH_NDECM, kOffDecRec, kOffDecMerge);
+  put(X.tile, PH_OFF_TILE, PH_NTILE, PH_NTILEM, kOffTileRec, kOffTileMerge);
   return ok();
 }
 

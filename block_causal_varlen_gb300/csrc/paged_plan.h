@@ -33,13 +33,11 @@ enum : int {
   PH_NPAGES,
   PH_OFF_PGROW,    // int32 [npages]: packed row at which the page's first row is read back
   PH_OFF_PGCNT,    // int32 [npages]: rows of the page in use
-  PH_OFF_DEC,      // few-rows kernel: int32 [kPagedCtas + 1] first piece of every CTA, then the pieces
-  PH_NDEC,         // pieces
-  PH_OFF_DECM,     // joins of its split blocks
-  PH_NDECM,
+  PH_OFF_DEC,      // few-rows kernel: its pieces, CTA after CTA,
+  PH_NDEC,         // their number,
+  PH_NDECM,        // and the joins of its split blocks
   PH_OFF_TILE,     // the same for the tile kernel
   PH_NTILE,
-  PH_OFF_TILEM,
   PH_NTILEM,
   PH_STATUS = H_STATUS, PH_STATUS_DETAIL = H_STATUS_DETAIL, // 5 few-rows attention, 6 tile attention
   kPagedHdrWords = kHdrWords
@@ -61,8 +59,20 @@ enum : int {
   kPieceWords = 12
 };
 
+// Where a CTA starts reading: its pieces [p0, p1) and a copy of the first one, so that
+// no lookup stands between a launch and its first loads.
+enum : int { RC_P0 = 0, RC_P1, RC_RESERVED0, RC_RESERVED1, RC_PIECE, kRecordWords = RC_PIECE + kPieceWords };
+
 // A join of the n partial results in slots slot0, slot0 + 1, ... of one block.
 enum : int { MG_SLOT0 = 0, MG_N, MG_Q0, MG_HKV, MG_ROW0, MG_NROWS, MG_RESERVED0, MG_RESERVED1, kMergeWords = 8 };
+
+// Records and joins have fixed places and room for the most there can be (a join has
+// two slots at least).
+constexpr int kOffDecRec = kPagedHdrWords;
+constexpr int kOffDecMerge = kOffDecRec + kPagedCtas * kRecordWords;
+constexpr int kOffTileRec = kOffDecMerge + kPagedSlots / 2 * kMergeWords;
+constexpr int kOffTileMerge = kOffTileRec + kPagedCtas * kRecordWords;
+constexpr int kOffLists = kOffTileMerge + kPagedSlots / 2 * kMergeWords;
 
 // Validated view of a host plan blob.
 int32_t view_paged_plan(const void* plan_host, const int32_t** out);

@@ -30,7 +30,7 @@
 #include <math_constants.h>
 
 #include <atomic>
-#include <cstring>
+#include <type_traits>
 
 #include "paged.h"
 #include "ptx.cuh"
@@ -78,16 +78,18 @@ struct Piece {
   int q0, qlen, kvlen, pages, hkv, t0, k0, k1, slot, nt, ns;
 };
 
-__device__ __forceinline__ uint32_t lop_and_or(uint32_t a, uint32_t m, uint32_t b) { return (a & m) | b; }
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
   uint32_t r;  // subnormal operands keep their values
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-// the codes in bytes 0, 1 (sel 0x1404) or 2, 3 (0x3424) of x as a bf16 pair times 2^-120
-__device__ __forceinline__ uint32_t e4m3x2_bits(uint32_t x, uint32_t sel) {
-  const uint32_t t = __byte_perm(x, 0u, sel);
-  return lop_and_or(t, 0x80008000u, (t >> 4) & 0x07f007f0u);
+// four codes as two bf16 pairs times 2^-120: sign, 4 exponent and 3 mantissa bits of
+// each at bits 15, 10..7 and 6..4
+__device__ __forceinline__ void e4m3x4_bits(uint32_t x, uint32_t& a, uint32_t& b) {
+  const uint32_t lo = (x << 4) & 0xf0f0f0f0u;
+  const uint32_t hi = (x & 0x80808080u) | ((x >> 4) & 0x07070707u);
+  a = __byte_perm(lo, hi, 0x5140);
+  b = __byte_perm(lo, hi, 0x7362);
 }
 __device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
   uint4 r;
@@ -114,11 +116,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t* plan = a.plan;
-  const int32_t* first = plan + plan[PH_OFF_TILE];
-  const int32_t* pieces = first + kPagedCtas + 1;
-  const int p0 = first[blockIdx.x], p1 = first[blockIdx.x + 1];
+  const int32_t* rec = plan + kOffTileRec + blockIdx.x * kRecordWords;
+  const int p0 = rec[RC_P0], p1 = rec[RC_P1];
   if (p0 == p1) return;
-  const int G = plan[PH_G], causal = plan[PH_CAUSAL], pshift = plan[PH_PAGE_SHIFT];
+  const int32_t* pieces = plan + plan[PH_OFF_TILE];
+  const int G = a.G, causal = a.causal, pshift = a.page_shift;
   const int TPS = 128 / G;   // new rows of a slot's tile
   for (int i = threadIdx.x; i < min(p1 - p0, Cfg::kPre) * kPieceWords; i += Cfg::kThreads)
     pre[i] = pieces[p0 * kPieceWords + i];
@@ -541,29 +543,39 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       const int r = threadIdx.x - 384;
       uint32_t it = 0, rit = 0;
       bool ok = true;
-      // codes of this thread's row (at `src`) times 2^e into the bf16 tile at `dst`
-      auto convert = [&](uint32_t src, uint32_t dst, uint32_t byte, bool zero) {
+      // codes of this thread's row (at `src`) times 2^e into the bf16 tile at `dst`;
+      // SLOW: some row of the warp is past the keys' end, NaN, or of an exponent that
+      // takes two factors
+      auto convert = [&](auto slow, uint32_t src, uint32_t dst, uint32_t byte, bool zero) {
+        constexpr bool SLOW = decltype(slow)::value;
         const int e = int(byte) - 127;
         // 2^(120 + e) fits a bf16 up to e = 7; what is left of a larger one is a second factor
-        const uint32_t f1 = zero ? 0u : byte == 255u ? 0x7fc0u : uint32_t(127 + 120 + min(e, 7)) << 7;
+        const uint32_t f1 = SLOW && byte == 255u ? 0x7fc0u : uint32_t(127 + 120 + min(e, 7)) << 7;
         const uint32_t m1 = f1 | (f1 << 16), f2 = uint32_t(127 + max(e, 7) - 7) << 7, m2 = f2 | (f2 << 16);
-        const bool big = byte != 255u && e > 7;
+        const uint32_t keep = zero ? 0u : ~0u;
         constexpr int PB = D == 64 ? 64 : 128;  // bytes of a raw row's piece
-#pragma unroll 2
-        for (int c = 0; c < D / 16; ++c) {      // 16 codes: two 16-byte pieces of bf16
+        auto load = [&](int c) {
           const int pc = c * 16 / PB, cc = c % (PB / 16);
-          const uint32_t at = src + pc * 128 * PB + r * PB + (D == 64 ? ((cc ^ ((r >> 1) & 3)) << 4) : ((cc ^ (r & 7)) << 4));
-          const uint4 u = ld_shared_u4(at);
+          return ld_shared_u4(src + pc * 128 * PB + r * PB + (D == 64 ? ((cc ^ ((r >> 1) & 3)) << 4) : ((cc ^ (r & 7)) << 4)));
+        };
+        // four 16-byte loads in flight; 16 codes give two 16-byte pieces of bf16
+        uint4 u[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) u[c] = load(c);
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          const uint4 x = u[c & 3];
+          if (c + 4 < D / 16) u[c & 3] = load(c + 4);
           uint32_t w[8];
-          w[0] = e4m3x2_bits(u.x, 0x1404); w[1] = e4m3x2_bits(u.x, 0x3424);
-          w[2] = e4m3x2_bits(u.y, 0x1404); w[3] = e4m3x2_bits(u.y, 0x3424);
-          w[4] = e4m3x2_bits(u.z, 0x1404); w[5] = e4m3x2_bits(u.z, 0x3424);
-          w[6] = e4m3x2_bits(u.w, 0x1404); w[7] = e4m3x2_bits(u.w, 0x3424);
+          e4m3x4_bits(x.x, w[0], w[1]);
+          e4m3x4_bits(x.y, w[2], w[3]);
+          e4m3x4_bits(x.z, w[4], w[5]);
+          e4m3x4_bits(x.w, w[6], w[7]);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = zero ? 0u : hmul2_bf16(w[i], m1);
-          if (big)
+          for (int i = 0; i < 8; ++i) w[i] = hmul2_bf16(w[i], m1);
+          if constexpr (SLOW)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = hmul2_bf16(w[i], m2);
+            for (int i = 0; i < 8; ++i) w[i] = (byte == 255u ? w[i] : hmul2_bf16(w[i], m2)) & keep;
           const uint32_t d = dst + (c >> 2) * 16384 + r * 128;
           const int oc = (c & 3) * 2;
           st_shared_v4(d + ((oc ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
@@ -596,7 +608,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             const int rs = rit % NR;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_RFULL + rs), (rit / NR) & 1, abort_flag)))) break;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar((h ? T_VEMPTY : T_KEMPTY) + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
-            convert(sR + rs * Cfg::kRawBytes, (h ? sV : sK) + s * Cfg::kTileBytes, (now >> (8 * h)) & 255u, past);
+            const uint32_t src = sR + rs * Cfg::kRawBytes, dst = (h ? sV : sK) + s * Cfg::kTileBytes;
+            const uint32_t byte = (now >> (8 * h)) & 255u;
+            if (__any_sync(0xffffffffu, past || byte > 127u + 7u)) convert(std::true_type(), src, dst, byte, past);
+            else convert(std::false_type(), src, dst, byte, past);
             mbar_arrive(bar(T_REMPTY + rs));
             mbar_arrive(bar((h ? T_VFULL : T_KFULL) + s));
           }

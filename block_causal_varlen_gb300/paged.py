@@ -67,7 +67,7 @@ class PagedCache:
         es = k_exp.stride() if k_exp is not None else (0, 0, 0)
         ep = [t.data_ptr() if t is not None else None for t in (k_exp, v_exp)]
         self._c = bd_paged_cache(st[0], st[1], ep[0], ep[1], es[0], es[1], es[2], self.fmt, self.num_pages)
-        self._ref = C.byref(self._c)
+        self._index = k.get_device()
 
 
 class PagedPlan:
@@ -102,21 +102,22 @@ class PagedPlan:
         off = (-self._raw.ctypes.data % 64) // 4
         self.host = self._raw[off:off + self.nbytes // 4]
         bd_paged_plan_build(desc, self.host.ctypes.data, self.nbytes)
-        self._host_ptr = C.c_void_p(self.host.ctypes.data)
+        self._host_ptr = self.host.ctypes.data
         self.dev = self._dev_ptr = None
+        self._index = -1
         ws = C.c_size_t()
         check(load().bd_paged_attn_workspace(self._host_ptr, C.byref(ws)))
         self._workspace = ws.value
 
     @property
     def host_ptr(self):
-        return self._host_ptr
+        return C.c_void_p(self._host_ptr)
 
     @property
     def dev_ptr(self):
         if self._dev_ptr is None:
             raise RuntimeError("plan not uploaded: call .upload(device)")
-        return self._dev_ptr
+        return C.c_void_p(self._dev_ptr)
 
     def upload(self, device="cuda", non_blocking=False, buffer=None):
         """Copy the plan blob to device memory (once per step): into memory of its own,
@@ -132,7 +133,7 @@ class PagedPlan:
         elif self.dev is None or self.dev.device != torch.device(device):
             self.dev = torch.empty_like(src, device=device)
         self.dev.copy_(src, non_blocking=non_blocking)
-        self._dev_ptr = C.c_void_p(self.dev.data_ptr())
+        self._dev_ptr, self._index = self.dev.data_ptr(), self.dev.get_device()
         return self
 
     def key(self) -> int:
@@ -144,7 +145,7 @@ def bd_paged_plan_key(plan: PagedPlan) -> int:
     """Plans of equal keys may replace each other under a captured graph (see
     include/bd_paged.h)."""
     n = C.c_uint64()
-    check(load().bd_paged_plan_key(plan.host_ptr, C.byref(n)))
+    check(load().bd_paged_plan_key(plan._host_ptr, C.byref(n)))
     return n.value
 
 
@@ -153,15 +154,23 @@ def bd_paged_attn_workspace(plan: PagedPlan) -> int:
     return plan._workspace
 
 
-def _rows3(t, name, heads, d, rows, dev):
-    """A packed [rows, heads, d] bf16 tensor as the ABI's strided tensor. The C ABI
-    carries neither dtypes nor head counts, so they are checked here."""
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name}: dtype {t.dtype}, expected torch.bfloat16")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _refuse(t, name, dtype, idx):
+    """Says what is wrong with a tensor's type or place."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_cuda:
         raise TypeError(f"{name}: must be a CUDA tensor")
-    if t.device != dev:
-        raise ValueError(f"{name}: on {t.device}, the plan was uploaded to {dev}")
+    raise ValueError(f"{name}: on {t.device}, the plan was uploaded to cuda:{idx}")
+
+
+def _rows3(t, name, heads, d, rows, idx):
+    """A packed [rows, heads, d] bf16 tensor as the ABI's strided tensor. The C ABI
+    carries neither dtypes nor head counts, so they are checked here."""
+    if t.dtype is not torch.bfloat16 or t.get_device() != idx or idx < 0:
+        _refuse(t, name, torch.bfloat16, idx)
     s = t.shape
     if len(s) != 3 or s[1] != heads or s[2] != d or s[0] < rows:
         raise ValueError(f"{name}: shape {tuple(s)}, expected [{rows} or more, {heads}, {d}]")
@@ -174,69 +183,68 @@ def _rows3(t, name, heads, d, rows, dev):
 def _device(plan, cache):
     """The device of a call: that of the plan's device copy, which must be the cache's
     (heads and head dim of the cache are checked too; the ABI does not carry them)."""
-    if plan.dev is None:
+    if plan._dev_ptr is None:
         raise RuntimeError("plan not uploaded: call .upload(device)")
-    dev = plan.dev.device
-    if cache.device != dev:
-        raise ValueError(f"cache: on {cache.device}, the plan was uploaded to {dev}")
+    if cache._index != plan._index:
+        raise ValueError(f"cache: on {cache.device}, the plan was uploaded to {plan.dev.device}")
     if cache.Hkv != plan.Hkv or cache.d != plan.d:
         raise ValueError(f"cache of {cache.Hkv} heads of {cache.d}, the plan was built for {plan.Hkv} of {plan.d}")
-    return dev
+    return plan._index
 
 
-def _call(fn, dev, stream, *args):
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    if torch.cuda.current_device() == dev.index:
-        check(fn(*args, C.c_void_p(stream.cuda_stream)))
+def _call(fn, idx, stream, *args):
+    s = _raw_stream(idx) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == idx:
+        st = fn(*args, s)
     else:
-        with torch.cuda.device(dev):
-            check(fn(*args, C.c_void_p(stream.cuda_stream)))
+        with torch.cuda.device(idx):
+            st = fn(*args, s)
+    if st < 0:
+        check(st)
 
 
 def bd_cache_write(plan: PagedPlan, k, v, cache: PagedCache, stream=None):
     """Store the new rows' K and V at their cache positions (see include/bd_paged.h)."""
-    dev = _device(plan, cache)
-    tk = _rows3(k, "k", plan.Hkv, plan.d, plan.T, dev)
-    tv = _rows3(v, "v", plan.Hkv, plan.d, plan.T, dev)
-    _call(load().bd_cache_write, dev, stream, plan._host_ptr, plan._dev_ptr, C.byref(tk), C.byref(tv), cache._ref)
+    idx = _device(plan, cache)
+    tk = _rows3(k, "k", plan.Hkv, plan.d, plan.T, idx)
+    tv = _rows3(v, "v", plan.Hkv, plan.d, plan.T, idx)
+    _call(load().bd_cache_write, idx, stream, plan._host_ptr, plan._dev_ptr, tk, tv, cache._c)
 
 
 def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
     """The cached rows of every sequence, packed in batch order (see include/bd_paged.h)."""
-    dev = _device(plan, cache)
-    tk = _rows3(k, "k", plan.Hkv, plan.d, plan.kv_total, dev)
-    tv = _rows3(v, "v", plan.Hkv, plan.d, plan.kv_total, dev)
-    _call(load().bd_cache_read, dev, stream, plan._host_ptr, plan._dev_ptr, cache._ref, C.byref(tk), C.byref(tv))
+    idx = _device(plan, cache)
+    tk = _rows3(k, "k", plan.Hkv, plan.d, plan.kv_total, idx)
+    tv = _rows3(v, "v", plan.Hkv, plan.d, plan.kv_total, idx)
+    _call(load().bd_cache_read, idx, stream, plan._host_ptr, plan._dev_ptr, cache._c, tk, tv)
 
 
 def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspace=None, stream=None):
     """O and LSE of the new rows over the cache (see include/bd_paged.h). Without a
     workspace one is allocated for the call."""
-    dev = _device(plan, cache)
-    tq = _rows3(q, "q", plan.H, plan.d, plan.T, dev)
-    to = _rows3(out, "out", plan.H, plan.d, plan.T, dev)
+    idx = _device(plan, cache)
+    tq = _rows3(q, "q", plan.H, plan.d, plan.T, idx)
+    to = _rows3(out, "out", plan.H, plan.d, plan.T, idx)
     tl = None
     if lse is not None:
-        if lse.dtype != torch.float32:
-            raise TypeError(f"lse: dtype {lse.dtype}, expected torch.float32")
-        if lse.device != dev:
-            raise ValueError(f"lse: on {lse.device}, the plan was uploaded to {dev}")
-        if lse.dim() != 2 or lse.shape[0] != plan.H or lse.shape[1] < plan.T or lse.stride(1) != 1:
-            raise ValueError(f"lse: expected [{plan.H}, {plan.T} or more] with rows contiguous, got {tuple(lse.shape)}")
-        tl = C.byref(bd_rowstat(lse.data_ptr(), 0, 0, lse.stride(0)))
+        if lse.dtype is not torch.float32 or lse.get_device() != idx:
+            _refuse(lse, "lse", torch.float32, idx)
+        s = lse.shape
+        if len(s) != 2 or s[0] != plan.H or s[1] < plan.T or lse.stride(1) != 1:
+            raise ValueError(f"lse: expected [{plan.H}, {plan.T} or more] with rows contiguous, got {tuple(s)}")
+        tl = bd_rowstat(lse.data_ptr(), 0, 0, lse.stride(0))
+    wp, wn = None, 0
     if workspace is None and plan._workspace:
-        workspace = torch.empty(plan._workspace, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(plan._workspace, dtype=torch.uint8, device=plan.dev.device)
         if stream is not None:
             workspace.record_stream(stream)
-    wp, wn = None, 0
     if workspace is not None:
-        if workspace.device != dev:
-            raise ValueError(f"workspace: on {workspace.device}, the plan was uploaded to {dev}")
+        if workspace.get_device() != idx:
+            raise ValueError(f"workspace: on {workspace.device}, the plan was uploaded to cuda:{idx}")
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
-        wp, wn = C.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()
-    _call(load().bd_paged_attn, dev, stream, plan._host_ptr, plan._dev_ptr, C.byref(tq), cache._ref, C.byref(to), tl, wp, wn)
+        wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _call(load().bd_paged_attn, idx, stream, plan._host_ptr, plan._dev_ptr, tq, cache._c, to, tl, wp, wn)
 
 
 def paged_attn(plan: PagedPlan, q, cache: PagedCache, stream=None):

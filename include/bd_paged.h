@@ -56,7 +56,8 @@ typedef enum {
  * K/V heads (elements, any order of the dimensions; bytes must be multiples of 16,
  * as must the base pointers), rows = page_size, stride_c is unused, and the d
  * elements of a head are contiguous. k_exp, v_exp: exponent bytes of a
- * BD_CACHE_E4M3 cache with their common strides (ignored otherwise). */
+ * BD_CACHE_E4M3 cache with their common strides (ignored otherwise); bd_paged_attn
+ * reads them by the aligned 4-byte words they lie in. */
 typedef struct {
   bd_tensor k, v;
   uint8_t* k_exp;

@@ -12,7 +12,7 @@ from oracle import paged as op  # noqa: E402
 
 # header words and record layouts (csrc/paged_plan.h)
 WORDS = ("MAGIC VERSION WORDS B H HKV D G PAGE PAGE_SHIFT NUM_PAGES FMT CAUSAL T KV_TOTAL WRITE_OK SCALE OFF_TOK "
-         "OFF_PAGES NPAGES OFF_PGROW OFF_PGCNT OFF_DEC NDEC OFF_DECM NDECM OFF_TILE NTILE OFF_TILEM NTILEM").split()
+         "OFF_PAGES NPAGES OFF_PGROW OFF_PGCNT OFF_DEC NDEC NDECM OFF_TILE NTILE NTILEM").split()
 PIECE = ("Q0", "QLEN", "KVLEN", "PAGES", "HKV", "ROW0", "NROWS", "K0", "K1", "SLOT", "T0", "R1")
 MERGE = ("SLOT0", "N", "Q0", "HKV", "ROW0", "NROWS", "R0", "R1")
 CTAS = 152
@@ -23,16 +23,23 @@ def header(plan):
 
 
 def lists(plan, kind):
-    """(first piece of every CTA, pieces, merges) of the kind's work list."""
+    """(pieces of every CTA, merges) of the kind's work list."""
     h, w = header(plan), plan.host
-    off, n = h[f"OFF_{kind}"], h[f"N{kind}"]
-    first = w[off:off + CTAS + 1].tolist()
-    at = off + CTAS + 1
+    rec = 64 if kind == "DEC" else 64 + CTAS * 16 + CTAS * 8
+    at, n = h[f"OFF_{kind}"], h[f"N{kind}"]
+    assert at % 4 == 0
     pieces = [dict(zip(PIECE, w[at + 12 * i:at + 12 * i + 12].tolist())) for i in range(n)]
-    mo, mn = h[f"OFF_{kind}M"], h[f"N{kind}M"]
-    merges = [dict(zip(MERGE, w[mo + 8 * i:mo + 8 * i + 8].tolist())) for i in range(mn)]
-    assert (off + CTAS + 1) % 4 == 0
-    return first, pieces, merges
+    ctas, end = [], 0
+    for c in range(CTAS):
+        r = w[rec + 16 * c:rec + 16 * c + 16].tolist()
+        ctas.append(pieces[r[0]:r[1]])
+        if r[1] > r[0]:
+            assert r[0] == end and r[4:] == w[at + 12 * r[0]:at + 12 * r[0] + 12].tolist()
+            end = r[1]
+    assert end == n
+    mo = rec + CTAS * 16
+    merges = [dict(zip(MERGE, w[mo + 8 * i:mo + 8 * i + 8].tolist())) for i in range(h[f"N{kind}M"])]
+    return ctas, merges
 
 
 def make(new, kv, H=8, Hkv=2, d=128, page=16, causal=True, pages=None, num_pages=None, fmt=bd.BD_CACHE_BF16):
@@ -59,12 +66,10 @@ def test_every_row_meets_every_key_once(new, kv, causal, H, Hkv):
     q0 = np.cumsum([0] + list(new))
     seen = {}
     for kind, unit in (("DEC", 32), ("TILE", 128)):
-        first, pieces, merges = lists(plan, kind)
-        assert first[0] == 0 and first[-1] == len(pieces) and all(a <= b for a, b in zip(first, first[1:]))
-        slots = [p["SLOT"] for p in pieces if p["SLOT"] >= 0]
-        assert slots == list(range(len(slots))), "slots are handed out in order"
-        for c in range(CTAS):
-            assert sum(p["SLOT"] >= 0 for p in pieces[first[c]:first[c + 1]]) <= 2
+        ctas, merges = lists(plan, kind)
+        pieces = [p for c in ctas for p in c]
+        slots = sorted(p["SLOT"] for p in pieces if p["SLOT"] >= 0)
+        assert slots == list(range(len(slots))) and len(slots) <= 2 * CTAS
         joined = {}
         for m in merges:
             assert m["N"] >= 2
@@ -91,7 +96,7 @@ def test_every_row_meets_every_key_once(new, kv, causal, H, Hkv):
         last = (r0 + n - 1) // G
         want = max(0, kv[b] - new[b] + last + 1) if causal else kv[b]
         assert parts[0][0] == 0 and parts[-1][1] == want
-        assert all(a[1] == c[0] for a, c in zip(parts, parts[1:]))
+        assert all(a[1] == c[0] and a[2] + 1 == c[2] for a, c in zip(parts, parts[1:]))
         assert (len(parts) == 1) == (parts[0][2] == -1)
     assert len(rows) == sum(new) * H
 
@@ -101,9 +106,20 @@ def test_work_is_spread_evenly():
     one key unit and one piece's cost over an even share."""
     for new, kv in (([1], [40000]), ([1] * 64, [int(500 * 1.05 ** i) for i in range(64)])):
         plan, _ = make(new, kv, 32, 8)
-        first, pieces, _ = lists(plan, "DEC")
-        load = [sum(-(-(p["K1"] - p["K0"]) // 32) + 3 for p in pieces[a:b]) for a, b in zip(first, first[1:])]
+        ctas, _ = lists(plan, "DEC")
+        load = [sum(-(-(p["K1"] - p["K0"]) // 32) + 3 for p in c) for c in ctas]
         assert max(load) <= sum(load) / CTAS + 5, (max(load), sum(load) / CTAS)
+
+
+def test_tiles_are_cut_only_where_it_helps():
+    """Many equal blocks are given out whole; a few long ones are spread over the SMs."""
+    plan, _ = make([64] * 152, [64] * 152, 8, 2)
+    ctas, merges = lists(plan, "TILE")
+    assert not merges and max(len(c) for c in ctas) == 2
+    plan, _ = make([64], [60000], 8, 2)
+    ctas, merges = lists(plan, "TILE")
+    load = [sum(-(-(p["K1"] - p["K0"]) // 128) + 1 for p in c) for c in ctas]
+    assert merges and max(load) <= sum(load) / CTAS + 3
 
 
 @pytest.mark.parametrize("new,kv", LAYOUTS)
@@ -274,8 +290,7 @@ def test_binding_refusals():
     q = torch.zeros(3, 8, 128, dtype=torch.bfloat16)
     with pytest.raises(RuntimeError, match="not uploaded"):
         bd.bd_paged_attn(plan, q, cache, q)
-    plan.dev = torch.from_numpy(plan.host)      # a host copy stands in: the refusals below come before a launch
-    plan._dev_ptr = plan.host_ptr
+    plan.upload("cpu")      # a host copy stands in: the refusals below come before a launch
     with pytest.raises(TypeError, match="dtype"):
         bd.bd_paged_attn(plan, q.float(), cache, q)
     with pytest.raises(TypeError, match="CUDA"):
