@@ -113,10 +113,12 @@ int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int
   cuuint64_t strides[4] = {cuuint64_t(sr), cuuint64_t(piece), cuuint64_t(sh), cuuint64_t(sp)};
   cuuint32_t box[5] = {cuuint32_t(piece / esize), cuuint32_t(box_rows), cuuint32_t(box_pieces), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  // no promotion past a row's piece: with rows of several heads side by side it would
+  // fetch the neighbouring heads' bytes, for other SMs at other times
   CUresult r = fn(map, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, t->ptr, dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   piece == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  piece == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(BD_ERR_ALIGN, "%s: cuTensorMapEncodeTiled failed (%d)", name, int(r));
   return BD_OK;
 }

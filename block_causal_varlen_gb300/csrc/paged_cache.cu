@@ -241,7 +241,7 @@ extern "C" int32_t bd_cache_write(const void* plan_host, const void* plan_dev, c
     return fail(BD_ERR_ARG, "k/v rows %d/%d < %d new rows of the plan", k->rows, v->rows, w[PH_T]);
   const CacheArgs a = cache_args(plan_dev, cache, k, v);
   const int64_t blocks = (int64_t(w[PH_T]) * w[PH_HKV] * (w[PH_D] / 8) + kThreads - 1) / kThreads;
-  const int grid = int(blocks < kPagedCtas * 8 ? blocks : kPagedCtas * 8);
+  const int grid = int(blocks < kPagedSms * 8 ? blocks : kPagedSms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cache->fmt == BD_CACHE_BF16) launch_write<BD_CACHE_BF16>(w[PH_D], grid, s, a);
   else launch_write<BD_CACHE_E4M3>(w[PH_D], grid, s, a);
@@ -262,7 +262,7 @@ extern "C" int32_t bd_cache_read(const void* plan_host, const void* plan_dev, co
     return fail(BD_ERR_ARG, "k/v rows %d/%d < %d cached rows of the plan", k->rows, v->rows, w[PH_KV_TOTAL]);
   const CacheArgs a = cache_args(plan_dev, cache, k, v);
   const int64_t groups = int64_t(w[PH_NPAGES]) * (w[PH_PAGE] / kReadRows);
-  const int grid = int(groups < kPagedCtas * 8 ? groups : kPagedCtas * 8);
+  const int grid = int(groups < kPagedSms * 8 ? groups : kPagedSms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cache->fmt == BD_CACHE_BF16) launch_read<BD_CACHE_BF16>(w[PH_D], grid, s, a);
   else launch_read<BD_CACHE_E4M3>(w[PH_D], grid, s, a);

@@ -9,9 +9,9 @@
 // key and 4 d bytes, far below the tensor rate, so the products use the
 // register-operand matrix instructions (m16n8k16), which want no TMEM and no
 // 128-row tiles, and everything is laid out to keep HBM busy:
-//   - one persistent CTA per SM; the host cuts all keys of the batch into equal
+//   - two persistent CTAs per SM; the host cuts all keys of the batch into equal
 //     stretches, one a CTA, so that no SM waits for another;
-//   - every warp runs on its own: it takes every NW-th chunk of 16 keys, loads its
+//   - every warp runs on its own: it takes every NW-th chunk of 16 or 32 keys, loads its
 //     chunks by TMA into a ring of its own (mbarriers, no CTA-wide barrier in the
 //     loop) and keeps its own m, l and O in registers. The ring runs ahead over the
 //     ends of blocks, so loads never stop; the warps meet only to add up a block;
@@ -31,6 +31,7 @@
 
 #include <atomic>
 #include <cstring>
+#include <type_traits>
 
 #include "paged.h"
 #include "ptx.cuh"
@@ -40,18 +41,22 @@ using namespace dev;
 
 namespace {
 
-constexpr int kChunk = 16;  // keys a warp takes at a time
-
 template <int D, int FMT>
 struct DecCfg {
   static constexpr bool kF8 = FMT == BD_CACHE_E4M3;
   static constexpr int kRowBytes = D * (kF8 ? 1 : 2);         // a key's K (or V) of one head
+  // keys a warp takes at a time: 32 where two or more such chunks fit a warp's ring
+  // (what a chunk costs besides its products, and the products' latency, then count
+  // half); 16 for bf16 rows of 256 bytes and more, and where O alone takes 128 registers
+  static constexpr int kChunk = kRowBytes <= 128 ? 32 : 16;
+  static constexpr int kPieces = kRowBytes <= 128 ? 1 : kRowBytes / 128;  // 128-byte pieces of a row
+  static constexpr int kPieceBytes = kRowBytes / kPieces;
   static constexpr int kMatBytes = kChunk * kRowBytes;        // K (or V) of a chunk
   static constexpr int kStageBytes = 2 * kMatBytes;
-  // warps and ring depth: 128 to 192 KB of chunks per SM (some 45 KB must be in
-  // flight to cover HBM's latency at its rate)
-  static constexpr int kWarps = kStageBytes >= 16384 ? 4 : 8;
-  static constexpr int kStages = kStageBytes >= 16384 ? 3 : kStageBytes == 8192 ? 3 : kStageBytes == 4096 ? 5 : 8;
+  // warps and ring depth: up to 192 KB of chunks per SM and its two CTAs (some 45 KB
+  // must be in flight to cover HBM's latency at its rate)
+  static constexpr int kWarps = kStageBytes >= 16384 ? 2 : 4;
+  static constexpr int kStages = kStageBytes >= 8192 ? 3 : 5;
   static constexpr int kThreads = 32 * kWarps;
   // values of a warp added up at a time: 4, 8 or 16 rows of 128, 64 or 32 columns (+ 4)
   static constexpr int kSumFloats = 16 * 36;
@@ -59,14 +64,14 @@ struct DecCfg {
   static constexpr int kOffSum = kOffRing + kWarps * kStages * kStageBytes;
   static constexpr int kOffMl = kOffSum + kWarps * kSumFloats * 4;     // m, l [kWarps][16]
   static constexpr int kOffInv = kOffMl + kWarps * 16 * 2 * 4;         // 1 / l of the block's rows
-  // e4m3: 4-byte words around K's (lanes 0-15) and V's exponent bytes of a chunk, and the
-  // low bits of their addresses
-  static constexpr int kOffExp = kOffInv + 16 * 4;                     // [kWarps][kStages][32]
-  static constexpr int kOffRef = kOffExp + (kF8 ? kWarps * kStages * 128 : 0);
-  static constexpr int kOffBar = kOffRef + (kF8 ? kWarps * kStages * 8 : 0);
+  // e4m3: 4-byte words around K's and V's exponent bytes of a chunk's keys, and the low
+  // bits of the bytes' addresses relative to k_exp and v_exp
+  static constexpr int kOffExp = kOffInv + 16 * 4;                     // [kWarps][kStages][2][kChunk]
+  static constexpr int kOffRef = kOffExp + (kF8 ? kWarps * kStages * kChunk * 8 : 0);
+  static constexpr int kOffBar = kOffRef + (kF8 ? kWarps * kStages * kChunk : 0);
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmem = kOffAbort + 16 + 1024;         // + alignment slack
-  static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
+  static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs do not fit an SM's shared memory");
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t a, uint32_t (&r)[4]) {
@@ -131,12 +136,13 @@ __device__ __forceinline__ int o_column(int nt, int c) {
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
+__global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
     bd_paged_dec_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const AttnArgs a) {
   using Cfg = DecCfg<D, FMT>;
   constexpr bool F8 = Cfg::kF8;
-  constexpr int NW = Cfg::kWarps, NST = Cfg::kStages;
+  constexpr int NW = Cfg::kWarps, NST = Cfg::kStages, kChunk = Cfg::kChunk;
+  constexpr int ST = kChunk / 8, PT = kChunk / 16;  // key tiles of S, contraction steps of P V
   constexpr int KS = D / 16, NT = D / 8;  // contraction steps of q . k, column tiles of O
   constexpr float kPShift = F8 ? 7.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
@@ -146,12 +152,12 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffAbort);
   const uint32_t ring = sbase + Cfg::kOffRing + warp * NST * Cfg::kStageBytes;
   const uint32_t bars = sbase + Cfg::kOffBar + warp * NST * 8;
-  volatile uint32_t* eref = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffRef) + warp * NST;
-  const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * 128 + lane * 4;
-  const uint8_t* ebase = lane < 16 ? a.k_exp : a.v_exp;
+  volatile uint8_t* eref = smem + Cfg::kOffRef + warp * NST * kChunk;  // low address bits of the exponents
+  const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * kChunk * 8;
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffDecRec + blockIdx.x * kRecordWords;
   const int p0 = rec[RC_P0], p1 = rec[RC_P1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
   if (p0 == p1) return;
   const int32_t* pieces = plan + plan[PH_OFF_DEC];
   auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
@@ -164,10 +170,12 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
   __syncthreads();
   const int G = a.G, causal = a.causal, pshift = a.page_shift;
 
+  const int brows = min(1 << pshift, kChunk);  // rows of a copy: a chunk's keys lie in one page or, of pages of 16, in two
+
   // ---- loads: a cursor over this warp's chunks of all pieces, NST chunks ahead of
   // the products. The next chunk's page number is fetched when the one before is
   // issued, so that issuing waits for nothing.
-  int cp = p0 - 1, ck = 0, ck1 = 0, chkv = 0, cpages = 0, cpage = 0;
+  int cp = p0 - 1, ck = 0, ck1 = 0, chkv = 0, cpages = 0, cpage = 0;  // cpage: of key ck + lane (mod kChunk)
   auto next_chunk = [&]() {
     ck += kChunk * NW;
     while (ck >= ck1) {
@@ -178,26 +186,40 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
       chkv = W[PC_HKV];
       cpages = W[PC_PAGES];
     }
-    cpage = plan[cpages + (ck >> pshift)];
+    const int k = min(ck + lane % kChunk, ck1 - 1);
+    cpage = plan[cpages + (k >> pshift)];
   };
   auto issue = [&](uint32_t it) {
     if (cp >= p1) return;
-    const int s = int(it % NST), row = ck & ((1 << pshift) - 1);
+    const int s = int(it % NST);
+    const uint32_t full = bars + 8 * s;
+    const int keys = min(kChunk, ck1 - ck);
+    const int n = (keys + brows - 1) / brows;  // copies (1 or 2) of K and of V
     if constexpr (F8) {
-      const int64_t o = int64_t(cpage) * a.e_sp + int64_t(row) * a.e_sr + int64_t(chkv) * a.e_sh;
-      if (lane == 0) eref[s] = uint32_t(o);
-      const uintptr_t at = reinterpret_cast<uintptr_t>(ebase + o + int64_t(lane & 15) * a.e_sr) & ~uintptr_t(3);
-      asm volatile(
-          "cp.async.ca.shared.global [%0], [%1], 4;\n\t"
-          "cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];" ::"r"(exps + s * 128),
-          "l"(at), "r"(bars + 8 * s)
-          : "memory");
+      // the 4-byte words of K's and V's exponents; a word's low address bits for later
+      const int key = min(lane % kChunk, keys - 1);
+      const int64_t o = int64_t(cpage) * a.e_sp + int64_t((ck + key) & ((1 << pshift) - 1)) * a.e_sr + int64_t(chkv) * a.e_sh;
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        if (kChunk == 32 || (lane >> 4) == m) {
+          const uintptr_t at = reinterpret_cast<uintptr_t>((m ? a.v_exp : a.k_exp) + o);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(exps + ((s * 2 + m) * kChunk + lane % kChunk) * 4),
+                       "l"(at & ~uintptr_t(3))
+                       : "memory");
+        }
+      eref[s * kChunk + lane % kChunk] = uint8_t(o & 3);
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
     }
-    if (lane == 0) {
-      const uint32_t dst = ring + s * Cfg::kStageBytes;
-      mbar_expect_tx(bars + 8 * s, Cfg::kStageBytes);
-      tma_load_5d(dst, &tm_k, bars + 8 * s, 0, row, 0, chkv, cpage);
-      tma_load_5d(dst + Cfg::kMatBytes, &tm_v, bars + 8 * s, 0, row, 0, chkv, cpage);
+    if (lane == 0) mbar_expect_tx(full, uint32_t(2 * n * brows * Cfg::kRowBytes));
+    __syncwarp();
+    if (lane % 16 == 0 && lane / 16 < n) {  // lane 16 is at the second page's first key
+      const uint32_t dst = ring + s * Cfg::kStageBytes + (lane / 16) * 16 * Cfg::kPieceBytes;
+      const int row = (ck + lane) & ((1 << pshift) - 1);
+#pragma unroll
+      for (int c = 0; c < Cfg::kPieces; ++c) {
+        tma_load_5d(dst + c * kChunk * Cfg::kPieceBytes, &tm_k, full, 0, row, c, chkv, cpage);
+        tma_load_5d(dst + Cfg::kMatBytes + c * kChunk * Cfg::kPieceBytes, &tm_v, full, 0, row, c, chkv, cpage);
+      }
     }
     next_chunk();
   };
@@ -208,20 +230,13 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
   for (; issued < uint32_t(NST) && cp < p1; ++issued) issue(issued);
   __syncwarp();
 
-  for (int p = p0; p < p1; ++p) {
-    const int32_t* W = piece(p);
-    const int q0 = W[PC_Q0], qlen = W[PC_QLEN], kvlen = W[PC_KVLEN], hkv = W[PC_HKV], row0 = W[PC_ROW0];
-    const int nrows = W[PC_NROWS], k0 = W[PC_K0], k1 = W[PC_K1], slot = W[PC_SLOT];
-    // ---- the two rows of this lane: their q as A fragments, the keys they see
-    uint32_t qa[KS][4];
-    float qs[2];   // score factor: log2(e) / sqrt(d), and the power of two taken out of q
-    int lim[2];
+  // ---- q of a block's rows rw, rw + 8 as A fragments (bf16 as it is)
+  uint32_t qa[KS][4];
+  auto load_q = [&](int q0, int hkv, int row0, int nrows) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = rw + 8 * i, n = row0 + r, t = n / G;
       const bool live = r < nrows;
-      lim[i] = !live ? 0 : causal ? kvlen - qlen + t + 1 : kvlen;
-      qs[i] = a.scale_log2;
       const __nv_bfloat16* qp = a.q + int64_t(q0 + t) * a.q_sr + int64_t(hkv * G + n % G) * a.q_sh;
       if constexpr (!F8) {
 #pragma unroll
@@ -232,7 +247,6 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
       } else {
         // lane j contracts over codes [x, x + 16) of the row, x as in the K loads below;
         // step s takes four of them
-        uint32_t mx = 0;
 #pragma unroll
         for (int s = 0; s < KS; s += 4) {
           const int x = D == 64 ? 16 * j : (s >> 3) * 128 + 32 * j + ((s >> 2) & 1) * 16;
@@ -244,6 +258,29 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
           qa[s][i] = u.x; qa[s][2 + i] = u.y; qa[s + 1][i] = u.z; qa[s + 1][2 + i] = u.w;
           qa[s + 2][i] = v.x; qa[s + 2][2 + i] = v.y; qa[s + 3][i] = v.z; qa[s + 3][2 + i] = v.w;
         }
+      }
+    }
+  };
+  load_q(rec[RC_PIECE + PC_Q0], rec[RC_PIECE + PC_HKV], rec[RC_PIECE + PC_ROW0], rec[RC_PIECE + PC_NROWS]);
+
+  for (int p = p0; p < p1; ++p) {
+    const int32_t* W = piece(p);
+    const int q0 = W[PC_Q0], qlen = W[PC_QLEN], kvlen = W[PC_KVLEN], hkv = W[PC_HKV], row0 = W[PC_ROW0];
+    const int nrows = W[PC_NROWS], k0 = W[PC_K0], k1 = W[PC_K1], slot = W[PC_SLOT];
+    // the next block's rows, for its q
+    const int32_t* X = piece(min(p + 1, p1 - 1));
+    const int xq0 = X[PC_Q0], xhkv = X[PC_HKV], xrow0 = X[PC_ROW0], xnrows = X[PC_NROWS];
+    // ---- the two rows of this lane: the keys they see, their score factors (log2(e) /
+    // sqrt(d), e4m3: and the power of two taken out of q)
+    float qs[2];
+    int lim[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rw + 8 * i, t = (row0 + r) / G;
+      lim[i] = r >= nrows ? 0 : causal ? kvlen - qlen + t + 1 : kvlen;
+      qs[i] = a.scale_log2;
+      if constexpr (F8) {
+        uint32_t mx = 0;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
           mx = __vmaxu2(mx, __vmaxu2(qa[s][i] & 0x7fff7fffu, qa[s][2 + i] & 0x7fff7fffu));
@@ -277,77 +314,88 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
     for (int k = k0 + kChunk * warp; k < k1; k += kChunk * NW, ++it) {
       const uint32_t st = ring + (it % NST) * Cfg::kStageBytes;
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (it % NST), (it / NST) & 1, abort_flag))) ok = false;
-      // ---- S = q . k: two tiles of 8 keys
-      float s[2][4];
+      // ---- S = q . k: tiles of 8 keys
+      float s[ST][4];
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int n = 0; n < ST; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
       if constexpr (!F8) {
-        const uint32_t krow = st + ((lane >> 4) * 8 + (lane & 7)) * 128;
 #pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          uint32_t b[4];
-          const uint32_t ch = uint32_t(2 * c + ((lane >> 3) & 1));
-          ldsm4(krow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
-          mma16<false>(s[0], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[0], b[1]);
-          mma16<false>(s[1], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[2], b[3]);
+        for (int n = 0; n < ST; n += 2) {
+          const uint32_t krow = st + (8 * n + (lane >> 4) * 8 + (lane & 7)) * 128;
+#pragma unroll
+          for (int c = 0; c < KS; ++c) {
+            uint32_t b[4];
+            const uint32_t ch = uint32_t(2 * c + ((lane >> 3) & 1));
+            ldsm4(krow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
+            mma16<false>(s[n], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[0], b[1]);
+            mma16<false>(s[n + 1], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[2], b[3]);
+          }
         }
       } else {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int key = 8 * n + rw;
+        for (int c = 0; c < KS / 4; ++c) {
+          uint4 u[ST];
 #pragma unroll
-          for (int c = 0; c < KS / 4; ++c) {
-            uint32_t at;
-            if constexpr (D == 64) at = st + key * 64 + ((j ^ ((key >> 1) & 3)) << 4);
-            else at = st + (c >> 1) * (kChunk * 128) + key * 128 + (((2 * j + (c & 1)) ^ (key & 7)) << 4);
-            const uint4 u = lds128(at);
-            const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+          for (int n = 0; n < ST; ++n) {
+            const int key = 8 * n + rw;
+            if constexpr (D == 64) u[n] = lds128(st + key * 64 + ((j ^ ((key >> 1) & 3)) << 4));
+            else u[n] = lds128(st + (c >> 1) * (kChunk * 128) + key * 128 + (((2 * j + (c & 1)) ^ (key & 7)) << 4));
+          }
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
+          for (int x = 0; x < 4; ++x) {
+            const int t = 4 * c + x;
+#pragma unroll
+            for (int n = 0; n < ST; ++n) {
               uint32_t b0, b1;
-              e4m3x4_to_f16(w4[x], b0, b1);
-              const int t = 4 * c + x;
+              e4m3x4_to_f16(x == 0 ? u[n].x : x == 1 ? u[n].y : x == 2 ? u[n].z : u[n].w, b0, b1);
               mma16<true>(s[n], qa[t][0], qa[t][1], qa[t][2], qa[t][3], b0, b1);
             }
           }
         }
       }
-      // ---- base-2 scores; exponents of this lane's keys k + 8 n + 2 j + e
-      // (ve: V's; vp: the same plus P's shift, NaN for a V row of NaN)
-      float kf[4] = {1.f, 1.f, 1.f, 1.f}, ve[4] = {0.f, 0.f, 0.f, 0.f}, vp[4] = {0.f, 0.f, 0.f, 0.f};
+      // ---- base-2 scores. This lane's keys are k + 8 n + 2 j + e; e4m3: ks, K's factor
+      // (first times the scores), and ve, V's exponent
+      float ve[2 * ST];
+      bool vnan = false;
+      uint32_t vb = 0;
       if constexpr (F8) {
-        // lanes 0-15: the bytes of K and V of key `lane`
-        uint32_t ex, low = (uint32_t(reinterpret_cast<uintptr_t>(ebase)) + eref[it % NST] + uint32_t(lane & 15) * uint32_t(a.e_sr)) & 3u;
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(ex) : "r"(exps + (it % NST) * 128) : "memory");
-        ex = (ex >> (8 * low)) & 255u;
-        ex |= __shfl_xor_sync(0xffffffffu, ex, 16) << 8;
+        uint32_t kb, low = eref[(it % NST) * kChunk + lane % kChunk];
+        const uint32_t at = exps + ((it % NST) * 2 * kChunk + lane % kChunk) * 4;
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(kb) : "r"(at) : "memory");
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vb) : "r"(at + kChunk * 4) : "memory");
+        kb = (kb >> (8 * ((low + uint32_t(reinterpret_cast<uintptr_t>(a.k_exp))) & 3u))) & 255u;
+        vb = (vb >> (8 * ((low + uint32_t(reinterpret_cast<uintptr_t>(a.v_exp))) & 3u))) & 255u;
+        vnan = __any_sync(0xffffffffu, vb == 255u);
+        const float kf = exp_factor(kb), vf = vb == 255u ? 0.f : float(int(vb) - 127);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const uint32_t b = __shfl_sync(0xffffffffu, ex, 8 * (x >> 1) + 2 * j + (x & 1));
-          kf[x] = exp_factor(b & 255u);
-          ve[x] = float(int(b >> 8) - 127);
-          vp[x] = (b >> 8) == 255u ? __uint_as_float(0x7fc00000u) : ve[x] + kPShift;
+        for (int x = 0; x < 2 * ST; ++x) {
+          const int src = 8 * (x >> 1) + 2 * j + (x & 1);
+          const float f = __shfl_sync(0xffffffffu, kf, src);
+          ve[x] = __shfl_sync(0xffffffffu, vf, src);
+          s[x >> 1][x & 1] *= f;
+          s[x >> 1][2 + (x & 1)] *= f;
         }
       }
       const bool edge = k + kChunk > all_see;
+      if (edge) {
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < ST; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] *= F8 ? qs[e >> 1] * kf[2 * n + (e & 1)] : a.scale_log2;
-          if (edge && k + 8 * n + 2 * j + (e & 1) >= lim[e >> 1]) s[n][e] = -CUDART_INF_F;
-        }
+          for (int e = 0; e < 4; ++e)
+            if (k + 8 * n + 2 * j + (e & 1) >= lim[e >> 1]) s[n][e] = -CUDART_INF_F;
+      }
       float f[2];
       bool grow = false;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float mx = -CUDART_INF_F;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < ST; ++n)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) mx = fmaxf(mx, s[n][2 * i + e] + ve[2 * n + e]);
+          for (int e = 0; e < 2; ++e)
+            mx = fmaxf(mx, F8 ? fmaf(s[n][2 * i + e], qs[i], ve[2 * n + e]) : s[n][2 * i + e] * a.scale_log2);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         // the maximum moves only when it grows by more than 2^8 (exact: l and O use
@@ -366,88 +414,98 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o[n][e] *= f[e >> 1];
       }
-      uint32_t pa[4];  // P as the A operand: rows rw, rw + 8 x keys 2 j.., 8 + 2 j..
+      uint32_t pa[PT][4];  // P as A operands: rows rw, rw + 8 x keys 16 y + 2 j.., 16 y + 8 + 2 j..
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float me = m[i] == -CUDART_INF_F ? 0.f : m[i];
+        float ls = 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float x0 = s[n][2 * i] - me, x1 = s[n][2 * i + 1] - me;
+        for (int n = 0; n < ST; ++n) {
           if constexpr (F8) {
-            l[i] += ex2(x0) + ex2(x1);
-            pa[2 * n + i] = pack_f16(ex2(x0 + vp[2 * n]), ex2(x1 + vp[2 * n + 1]));
+            const float x0 = fmaf(s[n][2 * i], qs[i], -me), x1 = fmaf(s[n][2 * i + 1], qs[i], -me);
+            ls += ex2(x0) + ex2(x1);
+            pa[n >> 1][2 * (n & 1) + i] = pack_f16(ex2(x0 + (ve[2 * n] + kPShift)), ex2(x1 + (ve[2 * n + 1] + kPShift)));
           } else {
-            const float p0f = ex2(x0), p1f = ex2(x1);
-            l[i] += p0f + p1f;
-            pa[2 * n + i] = pack_bf16(p0f, p1f);
+            const float p0f = ex2(fmaf(s[n][2 * i], a.scale_log2, -me)), p1f = ex2(fmaf(s[n][2 * i + 1], a.scale_log2, -me));
+            ls += p0f + p1f;
+            pa[n >> 1][2 * (n & 1) + i] = pack_bf16(p0f, p1f);
           }
         }
+        l[i] += ls;
       }
-      if (F8 && edge) {  // a NaN exponent of a key that the row does not see
+      if (F8 && vnan) {  // a V row of NaN makes P NaN for the rows that see its key
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int x = 0; x < 2 * ST; ++x) {
+          const bool bad = __shfl_sync(0xffffffffu, vb, 8 * (x >> 1) + 2 * j + (x & 1)) == 255u;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int key = k + 8 * n + 2 * j;
-            pa[2 * n + i] &= (key < lim[i] ? 0xffffu : 0u) | (key + 1 < lim[i] ? 0xffff0000u : 0u);
-          }
+          for (int i = 0; i < 2; ++i)
+            if (bad && k + 8 * (x >> 1) + 2 * j + (x & 1) < lim[i])
+              pa[x >> 2][2 * ((x >> 1) & 1) + i] |= 0x7e00u << (16 * (x & 1));
+        }
       }
       // ---- O += P V. Keys at or past k1 may hold anything: their V become zeros.
       const uint32_t sv = st + Cfg::kMatBytes;
-      const bool tail = k + kChunk > k1;
-      uint32_t vm[2] = {~0u, ~0u};
-      if (tail) {
+      auto values = [&](auto cut) {
+        constexpr bool TAIL = decltype(cut)::value;
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const int key = k + 8 * n + 2 * j;
-          vm[n] = (key < k1 ? 0xffffu : 0u) | (key + 1 < k1 ? 0xffff0000u : 0u);
-        }
-      }
-      if constexpr (!F8) {
-        const uint32_t vrow = sv + (((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
+        for (int y = 0; y < PT; ++y) {
+          uint32_t vm[2] = {~0u, ~0u};
+          if constexpr (TAIL) {
 #pragma unroll
-        for (int n = 0; n < NT; n += 2) {
-          uint32_t b[4];
-          const uint32_t ch = uint32_t(n + (lane >> 4));
-          ldsm4t(vrow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
-          if (tail) { b[0] &= vm[0]; b[1] &= vm[1]; b[2] &= vm[0]; b[3] &= vm[1]; }
-          mma16<false>(o[n], pa[0], pa[1], pa[2], pa[3], b[0], b[1]);
-          mma16<false>(o[n + 1], pa[0], pa[1], pa[2], pa[3], b[2], b[3]);
-        }
-      } else {
-        // this lane's B column is rw: 16 (8) neighbouring codes of keys 2 j, 2 j + 1,
-        // 8 + 2 j, 9 + 2 j, paired key by key
-#pragma unroll
-        for (int h = 0; h < (D + 127) / 128; ++h) {
-          uint32_t x[4][4];
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int key = 8 * (y >> 1) + 2 * j + (y & 1);
-            if constexpr (D == 64) {
-              const uint2 u = lds64(sv + key * 64 + (((rw >> 1) ^ ((key >> 1) & 3)) << 4) + (rw & 1) * 8);
-              x[y][0] = u.x; x[y][1] = u.y;
-            } else {
-              const uint4 u = lds128(sv + h * (kChunk * 128) + key * 128 + ((rw ^ (key & 7)) << 4));
-              x[y][0] = u.x; x[y][1] = u.y; x[y][2] = u.z; x[y][3] = u.w;
+            for (int n = 0; n < 2; ++n) {
+              const int key = k + 16 * y + 8 * n + 2 * j;
+              vm[n] = (key < k1 ? 0xffffu : 0u) | (key + 1 < k1 ? 0xffff0000u : 0u);
             }
           }
+          if constexpr (!F8) {
+            const uint32_t vrow = sv + (16 * y + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
 #pragma unroll
-          for (int w4 = 0; w4 < (D == 64 ? 2 : 4); ++w4) {
-            // bytes (k, k') of codes 0, 1 and 2, 3 of the word
-            uint32_t b[2][4];
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              e4m3x4_to_f16(__byte_perm(x[2 * y][w4], x[2 * y + 1][w4], 0x5140), b[y][0], b[y][1]);
-              e4m3x4_to_f16(__byte_perm(x[2 * y][w4], x[2 * y + 1][w4], 0x7362), b[y][2], b[y][3]);
+            for (int n = 0; n < NT; n += 2) {
+              uint32_t b[4];
+              const uint32_t ch = uint32_t(n + (lane >> 4));
+              ldsm4t(vrow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
+              if constexpr (TAIL) { b[0] &= vm[0]; b[1] &= vm[1]; b[2] &= vm[0]; b[3] &= vm[1]; }
+              mma16<false>(o[n], pa[y][0], pa[y][1], pa[y][2], pa[y][3], b[0], b[1]);
+              mma16<false>(o[n + 1], pa[y][0], pa[y][1], pa[y][2], pa[y][3], b[2], b[3]);
             }
+          } else {
+            // this lane's B column is rw: 16 (8) neighbouring codes of keys 2 j, 2 j + 1,
+            // 8 + 2 j, 9 + 2 j, paired key by key
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if (tail) { b[0][c] &= vm[0]; b[1][c] &= vm[1]; }
-              mma16<true>(o[h * 16 + w4 * 4 + c], pa[0], pa[1], pa[2], pa[3], b[0][c], b[1][c]);
+            for (int h = 0; h < (D + 127) / 128; ++h) {
+              uint32_t x[4][4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const int key = 16 * y + 8 * (z >> 1) + 2 * j + (z & 1);
+                if constexpr (D == 64) {
+                  const uint2 u = lds64(sv + key * 64 + (((rw >> 1) ^ ((key >> 1) & 3)) << 4) + (rw & 1) * 8);
+                  x[z][0] = u.x; x[z][1] = u.y;
+                } else {
+                  const uint4 u = lds128(sv + h * (kChunk * 128) + key * 128 + ((rw ^ (key & 7)) << 4));
+                  x[z][0] = u.x; x[z][1] = u.y; x[z][2] = u.z; x[z][3] = u.w;
+                }
+              }
+#pragma unroll
+              for (int w4 = 0; w4 < (D == 64 ? 2 : 4); ++w4) {
+                // bytes (k, k') of codes 0, 1 and 2, 3 of the word
+                uint32_t b[2][4];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  e4m3x4_to_f16(__byte_perm(x[2 * z][w4], x[2 * z + 1][w4], 0x5140), b[z][0], b[z][1]);
+                  e4m3x4_to_f16(__byte_perm(x[2 * z][w4], x[2 * z + 1][w4], 0x7362), b[z][2], b[z][3]);
+                }
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  if constexpr (TAIL) { b[0][c] &= vm[0]; b[1][c] &= vm[1]; }
+                  mma16<true>(o[h * 16 + w4 * 4 + c], pa[y][0], pa[y][1], pa[y][2], pa[y][3], b[0][c], b[1][c]);
+                }
+              }
             }
           }
         }
-      }
+      };
+      if (k + kChunk > k1) values(std::true_type());
+      else values(std::false_type());
       __syncwarp();  // every lane has read the stage
       if (ok && issued == it + NST && cp < p1) {
         issue(issued);
@@ -455,6 +513,9 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
       }
       __syncwarp();
     }
+
+    // the next block's q comes while this block's results are added up
+    if (p + 1 < p1) load_q(xq0, xhkv, xrow0, xnrows);
 
     // ---- add the warps' results up
 #pragma unroll
@@ -545,7 +606,6 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
     }
     __syncthreads();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!ok) {
     // every copy issued has been waited for in turn; wait (with a limit) for those a
     // wait gave up on, then say so
@@ -560,88 +620,113 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 1)
   }
 }
 
-// One (split block, row) per WPR warps: the slots' O rows, weighted by 2^(m_i - M).
-template <int D, int ROWS, int WPR>
+// m, l and D / 32 columns of O of one row: state (a) joined with a slot's (b), each
+// relative to its own m.
+template <int V>
+__device__ __forceinline__ void join(float& m, float& l, float (&o)[V], float mi, float li, const float (&oi)[V]) {
+  if (mi == -CUDART_INF_F) return;
+  const float mn = fmaxf(m, mi), f0 = m == -CUDART_INF_F ? 0.f : ex2(m - mn), f1 = ex2(mi - mn);
+  l = l * f0 + li * f1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) o[v] = o[v] * f0 + oi[v] * f1;
+  m = mn;
+}
+
+template <int V>
+__device__ __forceinline__ void load_cols(const float* p, float (&o)[V]) {
+  if constexpr (V == 2) {
+    const float2 t = __ldcg(reinterpret_cast<const float2*>(p));
+    o[0] = t.x; o[1] = t.y;
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; v += 4) {
+      const float4 t = __ldcg(reinterpret_cast<const float4*>(p + v));
+      o[v] = t.x; o[v + 1] = t.y; o[v + 2] = t.z; o[v + 3] = t.w;
+    }
+  }
+}
+
+template <int V>
+__device__ __forceinline__ void store_row(const MergeArgs& a, int t, int h, int lane, float m, float l, const float (&acc)[V]) {
+  const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
+  __nv_bfloat16* o = a.o + int64_t(t) * a.o_sr + int64_t(h) * a.o_sh + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16(acc[v] * inv, acc[v + 1] * inv);
+  if (lane == 0 && a.lse)
+    a.lse[int64_t(h) * a.l_sh + t] = m == -CUDART_INF_F ? -CUDART_INF_F : (m + lg2(l)) * 0.69314718055994531f;
+}
+
+// Joins of the few-rows kernel: block (x, y) takes rows y, y + 4, ... of split block x,
+// its 8 warps every eighth slot each (one long sequence has as many slots as a K/V
+// head's share of the CTAs). Bound by latency: the entry, then the slots, then the sum.
+constexpr int kMergeY = 4;
+template <int D>
 __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) {
-  constexpr int V = D / 32;            // columns of a lane
-  constexpr int RPB = 8 / WPR;         // rows of a block
-  __shared__ float s_o[WPR > 1 ? 8 : 1][D];
+  constexpr int V = D / 32;  // columns of a lane
+  __shared__ float s_o[8][D];
   __shared__ float s_m[8], s_l[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int32_t* plan = a.plan;
-  const bool tile = ROWS != kDecRows;
-  const int n = plan[tile ? PH_NTILEM : PH_NDECM], G = a.G;
-  const int32_t* list = plan + (tile ? kOffTileMerge : kOffDecMerge);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
-  const int per = tile ? 128 / G * G : ROWS;  // rows in use of each 128 of a tile slot
-  for (int x0 = blockIdx.x * RPB; x0 < n * ROWS; x0 += gridDim.x * RPB) {
-    const int x = x0 + warp / WPR, r = x % ROWS;  // RPB divides ROWS: a block's rows are one entry's
-    const int32_t* M = list + (x / ROWS) * kMergeWords;
-    const int br = tile ? (r >> 7) * per + (r & 127) : r;   // row of the block
-    const bool live = (!tile || (r & 127) < per) && br < M[MG_NROWS];
-    if (WPR > 1 && !live) continue;  // the same for the whole block
+  const int32_t* M = a.plan + kOffDecMerge + blockIdx.x * kMergeWords;
+  const int n = a.plan[PH_NDECM], cnt = M[MG_N], rows = M[MG_NROWS];
+  if (int(blockIdx.x) >= n) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(kDecRows, D);
+  for (int r = blockIdx.y; r < rows; r += kMergeY) {
     float acc[V], m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    if (live) {
-      const int cnt = M[MG_N];
-      const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(ROWS, D);
 #pragma unroll 4
-      for (int i = sub; i < cnt; i += WPR) {
-        const float* P = base + int64_t(i) * slot_floats(ROWS, D);
-        const float mi = __ldcg(P + r), li = __ldcg(P + ROWS + r);
+    for (int i = warp; i < cnt; i += 8) {
+      const float* P = base + int64_t(i) * slot_floats(kDecRows, D);
+      const float mi = __ldcg(P + r), li = __ldcg(P + kDecRows + r);
+      float ov[V];
+      load_cols(P + 2 * kDecRows + r * D + lane * V, ov);
+      join(m, l, acc, mi, li, ov);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
+    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+    __syncthreads();
+    if (warp == 0) {
+      for (int w = 1; w < min(cnt, 8); ++w) {
         float ov[V];
-        const float* op = P + 2 * ROWS + r * D + lane * V;
-        if constexpr (V == 2) {
-          const float2 t = __ldcg(reinterpret_cast<const float2*>(op));
-          ov[0] = t.x; ov[1] = t.y;
-        } else {
 #pragma unroll
-          for (int v = 0; v < V; v += 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(op + v));
-            ov[v] = t.x; ov[v + 1] = t.y; ov[v + 2] = t.z; ov[v + 3] = t.w;
-          }
-        }
-        if (mi == -CUDART_INF_F) continue;
-        const float mn = fmaxf(m, mi), f0 = m == -CUDART_INF_F ? 0.f : ex2(m - mn), f1 = ex2(mi - mn);
-        l = l * f0 + li * f1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = acc[v] * f0 + ov[v] * f1;
-        m = mn;
+        for (int v = 0; v < V; ++v) ov[v] = s_o[w][lane * V + v];
+        join(m, l, acc, s_m[w], s_l[w], ov);
       }
+      const int nr = M[MG_ROW0] + r;
+      store_row(a, M[MG_Q0] + nr / a.G, M[MG_HKV] * a.G + nr % a.G, lane, m, l, acc);
     }
-    if constexpr (WPR > 1) {
+    __syncthreads();
+  }
+}
+
+// Joins of the tile kernel: a warp per row, rows of all split blocks over the grid.
+template <int D>
+__global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArgs a) {
+  constexpr int V = D / 32, ROWS = tile_slot_rows(D);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int n = a.plan[PH_NTILEM], G = a.G, per = 128 / G * G;  // rows in use of each 128 of a slot
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int x = blockIdx.x * 8 + warp; x < n * ROWS; x += gridDim.x * 8) {
+    const int r = x % ROWS, br = (r >> 7) * per + (r & 127);  // row of the block
+    const int32_t* M = a.plan + kOffTileMerge + (x / ROWS) * kMergeWords;
+    if ((r & 127) >= per || br >= M[MG_NROWS]) continue;
+    const int cnt = M[MG_N];
+    const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(ROWS, D);
+    float acc[V], m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
-      if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
-      __syncthreads();
-      if (sub == 0) {
-        const float m0 = m;
-        float mm = m;
-        for (int w = 1; w < WPR; ++w) mm = fmaxf(mm, s_m[warp + w]);
-        const float f0 = m0 == -CUDART_INF_F ? 0.f : ex2(m0 - mm);
-        l *= f0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] *= f0;
-        for (int w = 1; w < WPR; ++w) {
-          const float f = s_m[warp + w] == -CUDART_INF_F ? 0.f : ex2(s_m[warp + w] - mm);
-          l += s_l[warp + w] * f;
-#pragma unroll
-          for (int v = 0; v < V; ++v) acc[v] += s_o[warp + w][lane * V + v] * f;
-        }
-        m = mm;
-      }
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < cnt; ++i) {
+      const float* P = base + int64_t(i) * slot_floats(ROWS, D);
+      const float mi = __ldcg(P + r), li = __ldcg(P + ROWS + r);
+      float ov[V];
+      load_cols(P + 2 * ROWS + int64_t(r) * D + lane * V, ov);
+      join(m, l, acc, mi, li, ov);
     }
-    if (live && sub == 0) {
-      const int nr = M[MG_ROW0] + br, h = M[MG_HKV] * G + nr % G, t = M[MG_Q0] + nr / G;
-      const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
-      __nv_bfloat16* o = a.o + int64_t(t) * a.o_sr + int64_t(h) * a.o_sh + lane * V;
-#pragma unroll
-      for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16(acc[v] * inv, acc[v + 1] * inv);
-      if (lane == 0 && a.lse)
-        a.lse[int64_t(h) * a.l_sh + t] = m == -CUDART_INF_F ? -CUDART_INF_F : (m + lg2(l)) * 0.69314718055994531f;
-    }
-    if constexpr (WPR > 1) __syncthreads();
+    const int nr = M[MG_ROW0] + br;
+    store_row(a, M[MG_Q0] + nr / G, M[MG_HKV] * G + nr % G, lane, m, l, acc);
   }
 }
 
@@ -656,16 +741,15 @@ int32_t launch_dec_t(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArg
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged few-rows)");
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
-  bd_paged_dec_kernel<D, FMT><<<kPagedCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mk, mv, a);
+  bd_paged_dec_kernel<D, FMT><<<kDecCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mk, mv, a);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
 }
 
-template <int D, int ROWS, int WPR>
-cudaError_t launch_merge_t(const MergeArgs& a, cudaStream_t s) {
-  // starts while the attention kernel drains; waits for its results itself
+// The join starts while the attention kernel drains, and waits for its results itself.
+cudaError_t launch_join(void (*kernel)(MergeArgs), dim3 grid, const MergeArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(kPagedCtas * (WPR > 1 ? 4 : 8));
+  c.gridDim = grid;
   c.blockDim = dim3(256);
   c.stream = s;
   cudaLaunchAttribute at[1];
@@ -673,7 +757,7 @@ cudaError_t launch_merge_t(const MergeArgs& a, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, bd_paged_merge_kernel<D, ROWS, WPR>, a);
+  return cudaLaunchKernelEx(&c, kernel, a);
 }
 
 }  // namespace
@@ -681,21 +765,21 @@ cudaError_t launch_merge_t(const MergeArgs& a, cudaStream_t s) {
 int32_t launch_merge(const MergeArgs& a, int d, bool tile, cudaStream_t s) {
   cudaError_t e;
   if (tile)
-    e = d == 64 ? launch_merge_t<64, tile_slot_rows(64), 1>(a, s)
-        : d == 128 ? launch_merge_t<128, tile_slot_rows(128), 1>(a, s) : launch_merge_t<256, tile_slot_rows(256), 1>(a, s);
+    e = launch_join(d == 64 ? bd_paged_tile_merge_kernel<64> : d == 128 ? bd_paged_tile_merge_kernel<128> : bd_paged_tile_merge_kernel<256>,
+                    dim3(kPagedSms * 8), a, s);
   else
-    e = d == 64 ? launch_merge_t<64, kDecRows, 8>(a, s)
-        : d == 128 ? launch_merge_t<128, kDecRows, 8>(a, s) : launch_merge_t<256, kDecRows, 8>(a, s);
-  return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_merge_kernel launch");
+    e = launch_join(d == 64 ? bd_paged_merge_kernel<64> : d == 128 ? bd_paged_merge_kernel<128> : bd_paged_merge_kernel<256>,
+                    dim3(kDecSlots / 2, kMergeY), a, s);
+  return e == cudaSuccess ? BD_OK : cuda_fail(e, "paged join launch");
 }
 
 int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, cudaStream_t s) {
   const int es = c->fmt == BD_CACHE_BF16 ? 2 : 1, d = w[PH_D];
-  const int pieces = d * es <= 128 ? 1 : d * es / 128;
+  const int chunk = d * es <= 128 ? 32 : 16, rows = w[PH_PAGE] < chunk ? w[PH_PAGE] : chunk;
   CUtensorMap mk, mv;
   int32_t st;
-  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", kChunk, pieces))) return st;
-  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", kChunk, pieces))) return st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", rows, 1))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", rows, 1))) return st;
   if (c->fmt == BD_CACHE_BF16)
     return d == 64 ? launch_dec_t<64, BD_CACHE_BF16>(mk, mv, a, s)
            : d == 128 ? launch_dec_t<128, BD_CACHE_BF16>(mk, mv, a, s) : launch_dec_t<256, BD_CACHE_BF16>(mk, mv, a, s);
@@ -707,13 +791,13 @@ int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c,
 
 using namespace bd;
 
-// Partial results of the few-rows kernel, then of the tile kernel (kPagedSlots slots
-// each, whatever the lengths; none for a kernel that is not launched).
+// Partial results of the few-rows kernel, then of the tile kernel (at most
+// kDecSlots and kTilePartSlots slots, whatever the lengths; none for a kernel that is not launched).
 static size_t dec_part_bytes(const int32_t* w) {
-  return w[PH_NDEC] ? size_t(kPagedSlots) * slot_floats(kDecRows, w[PH_D]) * 4 : 0;
+  return w[PH_NDEC] ? size_t(kDecSlots) * slot_floats(kDecRows, w[PH_D]) * 4 : 0;
 }
 static size_t part_bytes(const int32_t* w) {
-  return dec_part_bytes(w) + (w[PH_NTILE] ? size_t(kPagedSlots) * slot_floats(tile_slot_rows(w[PH_D]), w[PH_D]) * 4 : 0);
+  return dec_part_bytes(w) + (w[PH_NTILE] ? size_t(kTilePartSlots) * slot_floats(tile_slot_rows(w[PH_D]), w[PH_D]) * 4 : 0);
 }
 
 extern "C" int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes) {

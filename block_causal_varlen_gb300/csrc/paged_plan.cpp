@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <cstdlib>
 #include <functional>
 #include <queue>
 #include <utility>
@@ -29,8 +30,8 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
   auto in = [&](int64_t off, int64_t n, int stride) { return off >= kOffLists && n >= 0 && off + n * stride <= words; };
   if (!in(w[PH_OFF_TOK], w[PH_T], 1) || !in(w[PH_OFF_PAGES], w[PH_NPAGES], 1) || !in(w[PH_OFF_PGROW], w[PH_NPAGES], 1) ||
       !in(w[PH_OFF_PGCNT], w[PH_NPAGES], 1) || !in(w[PH_OFF_DEC], w[PH_NDEC], kPieceWords) ||
-      !in(w[PH_OFF_TILE], w[PH_NTILE], kPieceWords) || w[PH_NDECM] < 0 || w[PH_NDECM] > kPagedSlots / 2 ||
-      w[PH_NTILEM] < 0 || w[PH_NTILEM] > kPagedSlots / 2)
+      !in(w[PH_OFF_TILE], w[PH_NTILE], kPieceWords) || w[PH_NDECM] < 0 || w[PH_NDECM] > kDecSlots / 2 ||
+      w[PH_NTILEM] < 0 || w[PH_NTILEM] > kTilePartSlots / 2)
     return fail(BD_ERR_PLAN, "paged plan blob offsets are inconsistent");
   *out = w;
   return BD_OK;
@@ -52,7 +53,7 @@ struct Part {
 };
 
 struct Lists {
-  std::vector<int32_t> records;  // [kPagedCtas][kRecordWords]
+  std::vector<int32_t> records;  // [CTAs][kRecordWords]
   std::vector<int32_t> pieces, merges;
 };
 
@@ -89,20 +90,20 @@ bool stretch(const std::vector<Item>& items, int unit, int over, int64_t t, int 
 
 // The shortest stretches that hold everything: equal work for every CTA, at most two
 // parts of cut items in each.
-int64_t cut_evenly(const std::vector<Item>& items, int unit, int over, std::vector<Part>* parts) {
+int64_t cut_evenly(const std::vector<Item>& items, int unit, int over, int ctas, std::vector<Part>* parts) {
   int64_t total = 0;
   for (const Item& it : items) total += units_of(it, unit) + over;
-  int64_t lo = std::max<int64_t>(over + 1, (total + kPagedCtas - 1) / kPagedCtas), hi = lo;
-  while (!stretch(items, unit, over, hi, kPagedCtas, nullptr)) {
+  int64_t lo = std::max<int64_t>(over + 1, (total + ctas - 1) / ctas), hi = lo;
+  while (!stretch(items, unit, over, hi, ctas, nullptr)) {
     lo = hi + 1;
     hi += std::max<int64_t>(1, hi / 8);
   }
   while (lo < hi) {
     const int64_t mid = (lo + hi) / 2;
-    if (stretch(items, unit, over, mid, kPagedCtas, nullptr)) hi = mid;
+    if (stretch(items, unit, over, mid, ctas, nullptr)) hi = mid;
     else lo = mid + 1;
   }
-  stretch(items, unit, over, hi, kPagedCtas, parts);
+  stretch(items, unit, over, hi, ctas, parts);
   return hi;
 }
 
@@ -114,14 +115,14 @@ int64_t cut_longest(const std::vector<Item>& items, int unit, int over, int64_t 
   int64_t split = 0;
   for (size_t i = 0; i < items.size(); ++i) {
     const int64_t units = units_of(items[i], unit), n = std::max<int64_t>(1, (units + most - 1) / most);
-    if (n > 1 && (split += n) > kPagedSlots) return -1;
+    if (n > 1 && (split += n) > kTilePartSlots) return -1;
     for (int64_t k = 0; k < n; ++k)
       parts->push_back({int32_t(i), int32_t(units * k / n), int32_t(units * (k + 1) / n), 0});
   }
   std::stable_sort(parts->begin(), parts->end(), [](const Part& a, const Part& b) { return a.u1 - a.u0 > b.u1 - b.u0; });
   typedef std::pair<int64_t, int> Load;
   std::priority_queue<Load, std::vector<Load>, std::greater<Load>> ctas;
-  for (int c = 0; c < kPagedCtas; ++c) ctas.push({0, c});
+  for (int c = 0; c < kTileCtas; ++c) ctas.push({0, c});
   int64_t longest = 0;
   for (Part& p : *parts) {
     Load l = ctas.top();
@@ -135,10 +136,54 @@ int64_t cut_longest(const std::vector<Item>& items, int unit, int over, int64_t 
   return longest;
 }
 
+// Whole items, longest first, to the CTA with the least, as long as its load stays
+// within `t`; the others cut to fill what is left of the CTAs. False if that does not
+// hold everything (gaps of less than 4 units beyond a part's cost stay empty).
+bool fill(const std::vector<Item>& items, int unit, int over, int64_t t, std::vector<Part>* parts) {
+  parts->clear();
+  std::vector<int32_t> order(items.size()), left;
+  for (size_t i = 0; i < items.size(); ++i) order[i] = int32_t(i);
+  std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return items[a].keys > items[b].keys; });
+  typedef std::pair<int64_t, int> Load;
+  std::priority_queue<Load, std::vector<Load>, std::greater<Load>> ctas;
+  for (int c = 0; c < kTileCtas; ++c) ctas.push({0, c});
+  for (int32_t i : order) {
+    Load l = ctas.top();
+    const int64_t units = units_of(items[i], unit);
+    if (l.first + units + over > t) {
+      left.push_back(i);
+      continue;
+    }
+    ctas.pop();
+    parts->push_back({i, 0, int32_t(units), l.second});
+    l.first += units + over;
+    ctas.push(l);
+  }
+  int64_t split = 0;
+  for (int32_t i : left) {
+    const int64_t units = units_of(items[i], unit);
+    int64_t at = 0, n = 0;
+    while (at < units) {
+      Load l = ctas.top();
+      const int64_t part = std::min(t - l.first - over, units - at);
+      if (part < std::min<int64_t>(4, units - at)) return false;
+      ctas.pop();
+      parts->push_back({i, int32_t(at), int32_t(at + part), l.second});
+      l.first += part + over;
+      ctas.push(l);
+      at += part;
+      ++n;
+    }
+    if (n > 1 && (split += n) > kTilePartSlots) return false;
+  }
+  std::stable_sort(parts->begin(), parts->end(), [](const Part& a, const Part& b) { return a.cta < b.cta; });
+  return true;
+}
+
 // Writes the parts (in CTA order) down as pieces, records and joins.
 void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<Part>& parts,
-                 const std::vector<int32_t>& q0, const std::vector<int32_t>& page_off, int unit, Lists* L) {
-  L->records.assign(size_t(kPagedCtas) * kRecordWords, 0);
+                 const std::vector<int32_t>& q0, const std::vector<int32_t>& page_off, int unit, int ctas, Lists* L) {
+  L->records.assign(size_t(ctas) * kRecordWords, 0);
   // slots of an item's parts in key order, items in order
   std::vector<int32_t> count(items.size(), 0), slot0(items.size(), -1);
   for (const Part& p : parts) ++count[p.item];
@@ -184,44 +229,53 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
 // piece's own cost is some 3 units of 32 keys.
 void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
                const std::vector<int32_t>& page_off, Lists* L) {
+  const int kOver = getenv("BD_OVER") ? atoi(getenv("BD_OVER")) : 6;
   std::vector<Part> parts;
-  if (!items.empty()) cut_evenly(items, kDecUnit, 3, &parts);
-  write_lists(D, items, parts, q0, page_off, kDecUnit, L);
+  if (!items.empty()) cut_evenly(items, kDecUnit, kOver, kDecCtas, &parts);
+  write_lists(D, items, parts, q0, page_off, kDecUnit, kDecCtas, L);
 }
 
 // Tiles: a partial result is up to 256 rows of O in fp32, written and read again, so
 // blocks are cut only where that shortens the whole: the best of no cuts, equal parts
-// of the longest blocks, and an even cut, by their longest load in key tiles (a piece
-// costs one more, a join of n partial results about 3 + n / 50).
+// of the longest blocks, and whole blocks with the gaps filled by parts of the others,
+// by their longest load in key tiles (a piece costs kOver more, a join of n partial
+// results about 3 + n / 40).
 void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
                 const std::vector<int32_t>& page_off, Lists* L) {
+  const int kOver = getenv("BD_TOVER") ? atoi(getenv("BD_TOVER")) : 2;
   std::vector<Part> best, parts;
   if (!items.empty()) {
     int64_t total = 0;
-    for (const Item& it : items) total += units_of(it, kTile) + 1;
-    const int64_t share = (total + kPagedCtas - 1) / kPagedCtas;
-    int64_t least = cut_longest(items, kTile, 1, INT32_MAX, &best);
+    for (const Item& it : items) total += units_of(it, kTile) + kOver;
+    const int64_t share = (total + kTileCtas - 1) / kTileCtas;
+    int64_t least = cut_longest(items, kTile, kOver, INT32_MAX, &best);
+    std::vector<int32_t> count(items.size());
     auto joined = [&](const std::vector<Part>& v) {
-      std::vector<int32_t> count(items.size(), 0);
+      std::fill(count.begin(), count.end(), 0);
       for (const Part& p : v) ++count[p.item];
       int64_t n = 0;
       for (int32_t c : count) n += c > 1 ? c : 0;
-      return n ? 3 + n / 50 : 0;
+      return n ? 3 + n / 40 : 0;
+    };
+    auto better = [&](int64_t t) {
+      const int64_t cost = t + joined(parts);
+      if (cost >= least) return;
+      least = cost;
+      best.swap(parts);
     };
     for (int k = 1; k <= 4 && least > share; ++k) {
-      const int64_t most = std::max<int64_t>(1, share / k), t = cut_longest(items, kTile, 1, most, &parts);
+      const int64_t t = cut_longest(items, kTile, kOver, std::max<int64_t>(1, share / k), &parts);
       if (t < 0) break;
-      const int64_t cost = t + joined(parts);
-      if (cost < least) {
-        least = cost;
-        best.swap(parts);
-      }
+      better(t);
     }
-    parts.clear();
-    const int64_t t = cut_evenly(items, kTile, 1, &parts);
-    if (t + joined(parts) < least) best.swap(parts);
+    // the least t that can be filled, within 2%
+    for (int64_t t = share + 1; t + 3 < least; t += 1 + t / 50)
+      if (fill(items, kTile, kOver, t, &parts)) {
+        better(t);
+        break;
+      }
   }
-  write_lists(D, items, best, q0, page_off, kTile, L);
+  write_lists(D, items, best, q0, page_off, kTile, kTileCtas, L);
 }
 
 int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npages) {

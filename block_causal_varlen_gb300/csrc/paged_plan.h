@@ -11,9 +11,10 @@ namespace bd {
 
 constexpr int32_t kPagedMagic = 0x50414442;  // "BDAP"
 constexpr int32_t kPagedVersion = 1;
-// The persistent attention kernels run one CTA per SM of a GB300; the work lists
-// are cut for that many.
-constexpr int kPagedCtas = 152;
+// SMs of a GB300. The persistent attention kernels' work lists are cut for one CTA
+// (tiles) or two (few rows: one adds up a block while the other's loads go on) on each.
+constexpr int kPagedSms = 152;
+constexpr int kDecCtas = 2 * kPagedSms, kTileCtas = kPagedSms;
 constexpr int kDecRows = 16;   // (new row, query head) pairs of one K/V head in a few-rows block
 constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cut
 // Tiles (of 128 / G new rows x G heads) of one K/V head that share a key tile in the
@@ -21,7 +22,7 @@ constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cu
 constexpr int tile_slots(int d) { return d == 256 ? 1 : 2; }
 constexpr int tile_slot_rows(int d) { return 128 * tile_slots(d); }
 // At most this many partial results of a kind: the workspace's size.
-constexpr int kPagedSlots = 2 * kPagedCtas;
+constexpr int kDecSlots = 2 * kDecCtas, kTilePartSlots = 2 * kTileCtas;
 
 // header words (the failure status keeps the place it has in attention plans, so
 // that bd_check_status reads either)
@@ -69,10 +70,10 @@ enum : int { MG_SLOT0 = 0, MG_N, MG_Q0, MG_HKV, MG_ROW0, MG_NROWS, MG_RESERVED0,
 // Records and joins have fixed places and room for the most there can be (a join has
 // two slots at least).
 constexpr int kOffDecRec = kPagedHdrWords;
-constexpr int kOffDecMerge = kOffDecRec + kPagedCtas * kRecordWords;
-constexpr int kOffTileRec = kOffDecMerge + kPagedSlots / 2 * kMergeWords;
-constexpr int kOffTileMerge = kOffTileRec + kPagedCtas * kRecordWords;
-constexpr int kOffLists = kOffTileMerge + kPagedSlots / 2 * kMergeWords;
+constexpr int kOffDecMerge = kOffDecRec + kDecCtas * kRecordWords;
+constexpr int kOffTileRec = kOffDecMerge + kDecSlots / 2 * kMergeWords;
+constexpr int kOffTileMerge = kOffTileRec + kTileCtas * kRecordWords;
+constexpr int kOffLists = kOffTileMerge + kTilePartSlots / 2 * kMergeWords;
 
 // Validated view of a host plan blob.
 int32_t view_paged_plan(const void* plan_host, const int32_t** out);

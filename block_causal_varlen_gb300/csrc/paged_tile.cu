@@ -52,7 +52,11 @@ struct TileCfg {
   static constexpr int kOffK = kOffQ + kSlots * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffRaw = kOffV + kStages * kTileBytes;
-  static constexpr int kOffBar = kOffRaw + kRawStages * kRawBytes;
+  // results leave TMEM through 4 KB of shared memory per softmax warp; where none is
+  // left, through the slot's Q tile, which then is free only after the results are out
+  static constexpr bool kStageInQ = kF8 && D >= 128;
+  static constexpr int kOffStage = kOffRaw + kRawStages * kRawBytes;
+  static constexpr int kOffBar = kOffStage + (kStageInQ ? 0 : kSlots * 16384);
   static constexpr int kOffPieces = kOffBar + 512;
   static constexpr int kPre = 16;                 // pieces kept in shared memory
   static constexpr int kSmem = kOffPieces + kPre * kPieceWords * 4 + 1024;  // + alignment slack
@@ -91,6 +95,9 @@ __device__ __forceinline__ void e4m3x4_bits(uint32_t x, uint32_t& a, uint32_t& b
   a = __byte_perm(lo, hi, 0x5140);
   b = __byte_perm(lo, hi, 0x7362);
 }
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(n) : "memory");
+}
 __device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
@@ -118,6 +125,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffTileRec + blockIdx.x * kRecordWords;
   const int p0 = rec[RC_P0], p1 = rec[RC_P1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
   if (p0 == p1) return;
   const int32_t* pieces = plan + plan[PH_OFF_TILE];
   const int G = a.G, causal = a.causal, pshift = a.page_shift;
@@ -127,7 +135,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
 
   if (threadIdx.x == 0) {
     mbar_init(bar(T_QFULL), 1);
-    mbar_init(bar(T_QEMPTY), NS);
+    mbar_init(bar(T_QEMPTY), Cfg::kStageInQ ? 4 * NS : NS);  // softmax warps, or MMA threads
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(T_KFULL + s), F8 ? 128 : 1);
       mbar_init(bar(T_KEMPTY + s), NS);
@@ -194,16 +202,22 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       for (int p = p0; p < p1 && ok; ++p) {
         const Piece P = piece(p);
         if (P.nt == 0) continue;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_QEMPTY), (qi & 1) ^ 1, abort_flag)))) break;
-        if (lane == 0) {
-          mbar_expect_tx(bar(T_QFULL), uint32_t(P.ns * TPS * G * D * 2));
-          for (int s = 0; s < P.ns; ++s)
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_5d(sQ + s * Cfg::kTileBytes + c * 16384, &tm_q, bar(T_QFULL), c * 64, P.hkv * G,
-                          P.q0 + P.t0 + s * TPS, 0, 0);
-        }
-        __syncwarp();
-        ++qi;
+        // Q follows the first key tiles: their stages were the block before's, the Q tiles
+        // may be in use until its results are out
+        const int q_after = min(NST, P.nt) - 1;
+        auto load_q = [&]() -> bool {
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(T_QEMPTY), (qi & 1) ^ 1, abort_flag))) return false;
+          if (lane == 0) {
+            mbar_expect_tx(bar(T_QFULL), uint32_t(P.ns * TPS * G * D * 2));
+            for (int s = 0; s < P.ns; ++s)
+              for (int c = 0; c < D / 64; ++c)
+                tma_load_5d(sQ + s * Cfg::kTileBytes + c * 16384, &tm_q, bar(T_QFULL), c * 64, P.hkv * G,
+                            P.q0 + P.t0 + s * TPS, 0, 0);
+          }
+          __syncwarp();
+          ++qi;
+          return true;
+        };
         // this lane's page of a tile; the next tile's is fetched one tile ahead
         auto page_of = [&](int pos) { return pos + lane * rows < P.k1 && lane * rows < 128 ? plan[P.pages + ((pos + lane * rows) >> pshift)] : 0; };
         int page = page_of(P.k0);
@@ -226,6 +240,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             }
             if (!ok) break;
           }
+          if (j == q_after && !(ok = load_q())) break;
           page = next;
         }
       }
@@ -282,6 +297,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) mma_ts_lo(d_o, d_s + kk * 8, vb + uint32_t(kk * 128), idPV, (acc || kk > 0) ? 1u : 0u);
         };
+        // this slot's part of releasing the Q tiles, after its last product S
+        auto release_q = [&](bool act) {
+          if (act && !Cfg::kStageInQ) tc_commit(bar(T_QEMPTY));
+          if (!act) mbar_arrive_n(bar(T_QEMPTY), Cfg::kStageInQ ? 4 : 1);
+        };
         // it: key tiles (stages); qi: blocks; tc, ai: this slot's tiles and blocks
         uint32_t it = 0, qi = 0, tc = 0, ai = 0;
         bool ok = true;
@@ -301,12 +321,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
               pass_turn();
               tc_commit(bar(T_SFULL + s));
               tc_commit(bar(T_KEMPTY + sk));
-              if (P.nt == 1) tc_commit(bar(T_QEMPTY));
             } else {
               pass_turn();
               mbar_arrive(bar(T_KEMPTY + sk));
-              if (P.nt == 1) mbar_arrive(bar(T_QEMPTY));
             }
+            if (P.nt == 1) release_q(act);
           }
           for (int j = 1; j <= P.nt; ++j) {
             const uint32_t itp = it + j - 1, itn = it + j;
@@ -327,18 +346,15 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
               if (j < P.nt) {
                 tc_commit(bar(T_SFULL + s));
                 tc_commit(bar(T_KEMPTY + skn));
-                if (j == P.nt - 1) tc_commit(bar(T_QEMPTY));
               } else {
                 tc_commit(bar(T_OFINAL + s));
               }
             } else {
               pass_turn();
               mbar_arrive(bar(T_VEMPTY + svp));
-              if (j < P.nt) {
-                mbar_arrive(bar(T_KEMPTY + skn));
-                if (j == P.nt - 1) mbar_arrive(bar(T_QEMPTY));
-              }
+              if (j < P.nt) mbar_arrive(bar(T_KEMPTY + skn));
             }
+            if (j == P.nt - 1) release_q(act);
           }
           it += P.nt;
           if (act) {
@@ -500,7 +516,27 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         a.lse[int64_t(h) * a.l_sh + P.q0 + t] =
             l_run == 0.f ? -CUDART_INF_F : (m_fin + lg2(l_run)) * 0.69314718055994531f;
       }
-      float* prow = part ? part + 2 * tile_slot_rows(D) + int64_t(s * 128 + r) * D : nullptr;
+      // Rows leave in 128-byte pieces (64 columns of bf16, 32 of a partial result): the
+      // warp's 32 pieces go to its staging box (16-byte part c of row x at c ^ (x & 7)),
+      // from where 8 lanes store each row's piece. Rows stored by a thread each (32 rows
+      // in every store) held the load/store unit some 9000 cycles a block.
+      const uint32_t box = (Cfg::kStageInQ ? sQ + s * Cfg::kTileBytes : sbase + Cfg::kOffStage + s * 16384) + quarter * 4096;
+      const int64_t off = !live ? -1 : part ? int64_t(s * 128 + r) * D * 4 : (int64_t(P.q0 + t) * a.o_sr + int64_t(h) * a.o_sh) * 2;
+      uint8_t* const dst = part ? reinterpret_cast<uint8_t*>(part + 2 * tile_slot_rows(D)) : reinterpret_cast<uint8_t*>(a.o);
+      auto put = [&](int c, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
+        st_shared_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4), w0, w1, w2, w3);
+      };
+      auto send = [&](int byte) {  // the box, to bytes [byte, byte + 128) of the rows
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int x = 4 * i + (lane >> 3);
+          const int64_t o = __shfl_sync(0xffffffffu, off, x);
+          const uint4 v = ld_shared_u4(box + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
+          if (o >= 0) *reinterpret_cast<uint4*>(dst + o + byte + (lane & 7) * 16) = v;
+        }
+        __syncwarp();
+      };
       constexpr int QH = D <= 128 ? D / 32 : 1;  // 32-column groups taken out of TMEM at a time
 #pragma unroll 1
       for (int q0 = 0; q0 < D / 32; q0 += QH) {
@@ -515,25 +551,32 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(bar(T_OEMPTY + s));
         }
-        if (!live) continue;
+        if (part) {
 #pragma unroll
-        for (int q = 0; q < QH; ++q) {
-          if (part) {
+          for (int q = 0; q < QH; ++q) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              reinterpret_cast<uint4*>(prow + (q0 + q) * 32)[k] =
-                  make_uint4(ov[q][4 * k], ov[q][4 * k + 1], ov[q][4 * k + 2], ov[q][4 * k + 3]);
-          } else {
+            for (int c = 0; c < 8; ++c) put(c, ov[q][4 * c], ov[q][4 * c + 1], ov[q][4 * c + 2], ov[q][4 * c + 3]);
+            send((q0 + q) * 128);
+          }
+        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+          for (int q = 0; q < QH; ++q) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(ov[q][8 * k + 2 * e]) * inv, __uint_as_float(ov[q][8 * k + 2 * e + 1]) * inv);
-              reinterpret_cast<uint4*>(orow + (q0 + q) * 32)[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                w[e] = pack_bf16(__uint_as_float(ov[q][8 * c + 2 * e]) * inv, __uint_as_float(ov[q][8 * c + 2 * e + 1]) * inv);
+              put(((q0 + q) & 1) * 4 + c, w[0], w[1], w[2], w[3]);
             }
+            if ((q0 + q) & 1) send((q0 + q) / 2 * 128);
           }
         }
+      }
+      if constexpr (Cfg::kStageInQ) {
+        fence_proxy_async_smem();  // the box is Q's again
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(T_QEMPTY));
       }
     }
   } else {
@@ -623,7 +666,6 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -653,7 +695,7 @@ int32_t launch_tile_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
                   fa.numRegs, Cfg::kRegsLaunch);
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
-  bd_paged_tile_kernel<D, FMT><<<kPagedCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a);
+  bd_paged_tile_kernel<D, FMT><<<kTileCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_tile_kernel launch");
 }

@@ -15,7 +15,7 @@ WORDS = ("MAGIC VERSION WORDS B H HKV D G PAGE PAGE_SHIFT NUM_PAGES FMT CAUSAL T
          "OFF_PAGES NPAGES OFF_PGROW OFF_PGCNT OFF_DEC NDEC NDECM OFF_TILE NTILE NTILEM").split()
 PIECE = ("Q0", "QLEN", "KVLEN", "PAGES", "HKV", "ROW0", "NROWS", "K0", "K1", "SLOT", "T0", "R1")
 MERGE = ("SLOT0", "N", "Q0", "HKV", "ROW0", "NROWS", "R0", "R1")
-CTAS = 152
+CTAS = {"DEC": 304, "TILE": 152}
 
 
 def header(plan):
@@ -25,19 +25,20 @@ def header(plan):
 def lists(plan, kind):
     """(pieces of every CTA, merges) of the kind's work list."""
     h, w = header(plan), plan.host
-    rec = 64 if kind == "DEC" else 64 + CTAS * 16 + CTAS * 8
+    n_ctas = CTAS[kind]
+    rec = 64 if kind == "DEC" else 64 + CTAS["DEC"] * (16 + 8)
     at, n = h[f"OFF_{kind}"], h[f"N{kind}"]
     assert at % 4 == 0
     pieces = [dict(zip(PIECE, w[at + 12 * i:at + 12 * i + 12].tolist())) for i in range(n)]
     ctas, end = [], 0
-    for c in range(CTAS):
+    for c in range(n_ctas):
         r = w[rec + 16 * c:rec + 16 * c + 16].tolist()
         ctas.append(pieces[r[0]:r[1]])
         if r[1] > r[0]:
             assert r[0] == end and r[4:] == w[at + 12 * r[0]:at + 12 * r[0] + 12].tolist()
             end = r[1]
     assert end == n
-    mo = rec + CTAS * 16
+    mo = rec + n_ctas * 16
     merges = [dict(zip(MERGE, w[mo + 8 * i:mo + 8 * i + 8].tolist())) for i in range(h[f"N{kind}M"])]
     return ctas, merges
 
@@ -69,7 +70,7 @@ def test_every_row_meets_every_key_once(new, kv, causal, H, Hkv):
         ctas, merges = lists(plan, kind)
         pieces = [p for c in ctas for p in c]
         slots = sorted(p["SLOT"] for p in pieces if p["SLOT"] >= 0)
-        assert slots == list(range(len(slots))) and len(slots) <= 2 * CTAS
+        assert slots == list(range(len(slots))) and len(slots) <= 2 * CTAS[kind]
         joined = {}
         for m in merges:
             assert m["N"] >= 2
@@ -107,8 +108,8 @@ def test_work_is_spread_evenly():
     for new, kv in (([1], [40000]), ([1] * 64, [int(500 * 1.05 ** i) for i in range(64)])):
         plan, _ = make(new, kv, 32, 8)
         ctas, _ = lists(plan, "DEC")
-        load = [sum(-(-(p["K1"] - p["K0"]) // 32) + 3 for p in c) for c in ctas]
-        assert max(load) <= sum(load) / CTAS + 5, (max(load), sum(load) / CTAS)
+        load = [sum(-(-(p["K1"] - p["K0"]) // 32) + 6 for p in c) for c in ctas]
+        assert max(load) <= sum(load) / len(ctas) + 8, (max(load), sum(load) / len(ctas))
 
 
 def test_tiles_are_cut_only_where_it_helps():
@@ -119,7 +120,7 @@ def test_tiles_are_cut_only_where_it_helps():
     plan, _ = make([64], [60000], 8, 2)
     ctas, merges = lists(plan, "TILE")
     load = [sum(-(-(p["K1"] - p["K0"]) // 128) + 1 for p in c) for c in ctas]
-    assert merges and max(load) <= sum(load) / CTAS + 3
+    assert merges and max(load) <= sum(load) / len(ctas) + 3
 
 
 @pytest.mark.parametrize("new,kv", LAYOUTS)
