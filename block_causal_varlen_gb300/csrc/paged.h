@@ -19,7 +19,7 @@ __device__ __forceinline__ float exp_factor(uint32_t b) {
 }
 
 // Partial results: per slot m and l of its rows, then O [rows][d]. The few-rows
-// kernel's slots have kDecRows rows, the tile kernel's tile_slot_rows(d): 128 for each
+// kernel's slots have kDecSlotRows rows, the tile kernel's tile_slot_rows(d): 128 for each
 // of its tiles of 128 / G new rows.
 __host__ __device__ constexpr int64_t slot_floats(int rows, int d) { return int64_t(rows) * (d + 2); }
 

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArg
   const uint32_t sub = threadIdx.x % LPR;
   // (the whole warp takes part in the shuffles: rows past the last repeat the last)
   for (uint32_t r0 = blockIdx.x * uint32_t(RPB); r0 < n; r0 += gridDim.x * uint32_t(RPB)) {
-    const uint32_t r = min(r0 + threadIdx.x / LPR, n - 1), t = r / Hkv, h = r % Hkv;
+    const uint32_t r = min(r0 + threadIdx.x / LPR, n - 1), t = r / Hkv, h = r - t * Hkv;
     const uint4 kx = __ldcs(reinterpret_cast<const uint4*>(a.kx + int64_t(t) * a.kx_sr + int64_t(h) * a.kx_sh) + sub);
     const uint4 vx = __ldcs(reinterpret_cast<const uint4*>(a.vx + int64_t(t) * a.vx_sr + int64_t(h) * a.vx_sh) + sub);
     const int32_t row = tok[t];
@@ -128,6 +128,7 @@ constexpr int kReadRows = 8;
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) bd_cache_read_kernel(const CacheArgs a) {
   constexpr uint32_t LPR = D / 8;
+  constexpr int U = FMT == BD_CACHE_BF16 ? 2 : 4;  // rows in flight per thread: 64 bytes of loads
   const int32_t* plan = a.plan;
   const uint32_t Hkv = uint32_t(plan[PH_HKV]);
   const int32_t* pages = plan + plan[PH_OFF_PAGES];
@@ -137,32 +138,55 @@ __global__ void __launch_bounds__(kThreads) bd_cache_read_kernel(const CacheArgs
   static_assert(kReadRows == 8, "gshift");
   const uint32_t ngroups = uint32_t(plan[PH_NPAGES]) << gshift;
   const uint32_t sub = threadIdx.x % LPR;
+  // a group's place is looked up while the group before is copied
+  auto place = [&](uint32_t g, int& page, int& dst, int& rows) {
+    const uint32_t e = min(g, ngroups - 1) >> gshift;
+    page = pages[e];
+    dst = pgrow[e];
+    rows = pgcnt[e];
+  };
+  int page, first, count;
+  if (blockIdx.x < ngroups) place(blockIdx.x, page, first, count);
   for (uint32_t g = blockIdx.x; g < ngroups; g += gridDim.x) {
-    const uint32_t e = g >> gshift;
     const int r0 = int(g & ((1u << gshift) - 1)) * kReadRows;
-    const int rows = min(kReadRows, pgcnt[e] - r0);
+    const int rows = min(kReadRows, count - r0);
+    const int64_t pg = page, dst = int64_t(first) + r0;
+    place(g + gridDim.x, page, first, count);
     if (rows <= 0) continue;
-    const int64_t pg = pages[e], dst = int64_t(pgrow[e]) + r0;
     const uint32_t n = uint32_t(rows) * Hkv;
-#pragma unroll 2
-    for (uint32_t i = threadIdx.x / LPR; i < n; i += kThreads / LPR) {
-      const uint32_t ri = i / Hkv, h = i % Hkv;
-      const uint8_t* ks = a.k + pg * a.k_sp + int64_t(r0 + ri) * a.k_sr + int64_t(h) * a.k_sh;
-      const uint8_t* vs = a.v + pg * a.v_sp + int64_t(r0 + ri) * a.v_sr + int64_t(h) * a.v_sh;
-      uint4* kd = reinterpret_cast<uint4*>(a.kx + (dst + ri) * a.kx_sr + int64_t(h) * a.kx_sh) + sub;
-      uint4* vd = reinterpret_cast<uint4*>(a.vx + (dst + ri) * a.vx_sr + int64_t(h) * a.vx_sh) + sub;
-      if constexpr (FMT == BD_CACHE_BF16) {
-        const uint4 x = reinterpret_cast<const uint4*>(ks)[sub], y = reinterpret_cast<const uint4*>(vs)[sub];
-        __stcs(kd, x);
-        __stcs(vd, y);
-      } else {
-        const uint2 x = reinterpret_cast<const uint2*>(ks)[sub], y = reinterpret_cast<const uint2*>(vs)[sub];
-        const int64_t eo = pg * a.e_sp + int64_t(r0 + ri) * a.e_sr + int64_t(h) * a.e_sh;
-        const float fk = exp_factor(a.k_exp[eo]), fv = exp_factor(a.v_exp[eo]);
-        const uint2 k0 = dequantise4(x.x, fk), k1 = dequantise4(x.y, fk);
-        const uint2 v0 = dequantise4(y.x, fv), v1 = dequantise4(y.y, fv);
-        __stcs(kd, make_uint4(k0.x, k0.y, k1.x, k1.y));
-        __stcs(vd, make_uint4(v0.x, v0.y, v1.x, v1.y));
+    for (uint32_t i0 = threadIdx.x / LPR; i0 < n; i0 += U * (kThreads / LPR)) {
+      uint4 x[U], y[U];
+      float fk[U], fv[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t i = i0 + u * (kThreads / LPR), ri = i / Hkv, h = i - ri * Hkv;
+        if (i >= n) continue;
+        const uint8_t* ks = a.k + pg * a.k_sp + int64_t(r0 + ri) * a.k_sr + int64_t(h) * a.k_sh;
+        const uint8_t* vs = a.v + pg * a.v_sp + int64_t(r0 + ri) * a.v_sr + int64_t(h) * a.v_sh;
+        if constexpr (FMT == BD_CACHE_BF16) {
+          x[u] = __ldcs(reinterpret_cast<const uint4*>(ks) + sub);
+          y[u] = __ldcs(reinterpret_cast<const uint4*>(vs) + sub);
+        } else {
+          const uint2 k2 = __ldcs(reinterpret_cast<const uint2*>(ks) + sub), v2 = __ldcs(reinterpret_cast<const uint2*>(vs) + sub);
+          x[u].x = k2.x; x[u].y = k2.y;
+          y[u].x = v2.x; y[u].y = v2.y;
+          const int64_t eo = pg * a.e_sp + int64_t(r0 + ri) * a.e_sr + int64_t(h) * a.e_sh;
+          fk[u] = exp_factor(a.k_exp[eo]);
+          fv[u] = exp_factor(a.v_exp[eo]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t i = i0 + u * (kThreads / LPR), ri = i / Hkv, h = i - ri * Hkv;
+        if (i >= n) continue;
+        if constexpr (FMT == BD_CACHE_E4M3) {
+          const uint2 k0 = dequantise4(x[u].x, fk[u]), k1 = dequantise4(x[u].y, fk[u]);
+          const uint2 v0 = dequantise4(y[u].x, fv[u]), v1 = dequantise4(y[u].y, fv[u]);
+          x[u] = make_uint4(k0.x, k0.y, k1.x, k1.y);
+          y[u] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        }
+        __stcs(reinterpret_cast<uint4*>(a.kx + (dst + ri) * a.kx_sr + int64_t(h) * a.kx_sh) + sub, x[u]);
+        __stcs(reinterpret_cast<uint4*>(a.vx + (dst + ri) * a.vx_sr + int64_t(h) * a.vx_sh) + sub, y[u]);
       }
     }
   }
@@ -218,6 +242,8 @@ int32_t check_paged(const void* plan_host, const void* plan_dev, const bd_paged_
     if ((c->num_pages > 1 && c->exp_stride_page <= 0) || c->exp_stride_row <= 0 ||
         (w[PH_HKV] > 1 && c->exp_stride_head <= 0))
       return fail(BD_ERR_ARG, "exponent strides must be positive");
+    if (c->exp_stride_row > INT32_MAX / w[PH_PAGE] / 2 || (w[PH_HKV] > 1 && c->exp_stride_head > INT32_MAX / w[PH_HKV] / 2))
+      return fail(BD_ERR_UNSUPPORTED, "exponents of a page spread over more than 2^31 bytes");
   }
   *out = w;
   return BD_OK;

@@ -5,22 +5,27 @@
 // keys [k0, k1) computes, per row, m = max_j s_j, l = sum_j 2^(s_j - m) and
 // O = sum_j 2^(s_j - m) v_j with s_j = log2(e) q . k_j / sqrt(d), in one pass.
 //
-// What bounds it is reading K and V once: 16 rows use 2 x 2 x 16 d operations per
-// key and 4 d bytes, far below the tensor rate, so the products use the
-// register-operand matrix instructions (m16n8k16), which want no TMEM and no
-// 128-row tiles, and everything is laid out to keep HBM busy:
+// What bounds it is reading K and V once: a few rows use 2 x 2 x rows x d operations
+// per key and 4 d bytes, far below the tensor rate, so the products use the
+// register-operand matrix instructions (m16n8k16), which want no TMEM and no 128-row
+// tiles, and everything is laid out to keep HBM busy:
 //   - two persistent CTAs per SM; the host cuts all keys of the batch into equal
-//     stretches, one a CTA, so that no SM waits for another;
+//     stretches, one a CTA, so that no SM waits for another, and one CTA's loads go on
+//     while the other adds up a block;
 //   - every warp runs on its own: it takes every NW-th chunk of 16 or 32 keys, loads its
 //     chunks by TMA into a ring of its own (mbarriers, no CTA-wide barrier in the
 //     loop) and keeps its own m, l and O in registers. The ring runs ahead over the
 //     ends of blocks, so loads never stop; the warps meet only to add up a block;
+//   - the products are S^T = K Q^T and O^T = V^T P^T: keys and head columns fill the 16
+//     rows of the A operand, the block's rows its 8 columns, so a block of up to 8 rows
+//     (a group's heads of one new row) wastes nothing, and 16 or 32 rows reuse K's and
+//     V's fragments;
 //   - e4m3 chunks go from shared memory to fp16 fragments in registers (exact). The
 //     contraction order of q . k is permuted so that a lane reads 32 neighbouring
-//     codes, the column order of O so that it reads 16 of a V row, both free of
-//     bank conflicts. Exponents never touch the codes: K's is a factor of the score,
-//     V's an addend of the base-2 exponent (m is then the maximum of s_j + e_j).
-//     q as fp16 is exact too: each row is scaled by a power of two first.
+//     codes, the row order of V^T so that it reads 16 of a V row, both free of bank
+//     conflicts. Exponents never touch the codes: K's is a factor of the score, V's an
+//     addend of the base-2 exponent (m is then the maximum of s_j + e_j). q as fp16 is
+//     exact too: each row is scaled by a power of two first.
 // P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-9 relative,
 // like O itself), fp16 for e4m3 (2^-12), scaled by 2^7 so that terms down to 2^-31
 // of the largest keep a value.
@@ -41,32 +46,32 @@ using namespace dev;
 
 namespace {
 
-template <int D, int FMT>
+template <int D, int FMT, int NB>
 struct DecCfg {
   static constexpr bool kF8 = FMT == BD_CACHE_E4M3;
   static constexpr int kRowBytes = D * (kF8 ? 1 : 2);         // a key's K (or V) of one head
-  // keys a warp takes at a time: 32 where two or more such chunks fit a warp's ring
-  // (what a chunk costs besides its products, and the products' latency, then count
-  // half); 16 for bf16 rows of 256 bytes and more, and where O alone takes 128 registers
-  static constexpr int kChunk = kRowBytes <= 128 ? 32 : 16;
   static constexpr int kPieces = kRowBytes <= 128 ? 1 : kRowBytes / 128;  // 128-byte pieces of a row
   static constexpr int kPieceBytes = kRowBytes / kPieces;
+  // keys a warp takes at a time: 32 where that is no more than 8 KB and registers allow
+  // (what a chunk costs besides its products then counts half)
+  static constexpr int kChunk = kRowBytes <= 128 && NB <= 2 ? 32 : 16;
   static constexpr int kMatBytes = kChunk * kRowBytes;        // K (or V) of a chunk
   static constexpr int kStageBytes = 2 * kMatBytes;
   // warps and ring depth: up to 192 KB of chunks per SM and its two CTAs (some 45 KB
   // must be in flight to cover HBM's latency at its rate)
   static constexpr int kWarps = kStageBytes >= 16384 ? 2 : 4;
-  static constexpr int kStages = kStageBytes >= 8192 ? 3 : 5;
+  static constexpr int kStages = kStageBytes >= 8192 ? 3 : kStageBytes == 4096 ? 5 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  // values of a warp added up at a time: 4, 8 or 16 rows of 128, 64 or 32 columns (+ 4)
-  static constexpr int kSumFloats = 16 * 36;
+  // a warp's share of a block is added up 8 rows x kCols columns at a time
+  static constexpr int kCols = D == 64 ? 32 : 64, kPitch = kCols + 4, kSumFloats = 8 * kPitch;
   static constexpr int kOffRing = 0;
   static constexpr int kOffSum = kOffRing + kWarps * kStages * kStageBytes;
-  static constexpr int kOffMl = kOffSum + kWarps * kSumFloats * 4;     // m, l [kWarps][16]
-  static constexpr int kOffInv = kOffMl + kWarps * 16 * 2 * 4;         // 1 / l of the block's rows
+  static constexpr int kOffMl = kOffSum + kWarps * kSumFloats * 4;     // m, l [kWarps][8 NB]
+  static constexpr int kOffInv = kOffMl + kWarps * 8 * NB * 2 * 4;     // 1 / l of the block's rows
+  static constexpr int kOffRow = kOffInv + 8 * NB * 4;                 // their places in O
   // e4m3: 4-byte words around K's and V's exponent bytes of a chunk's keys, and the low
   // bits of the bytes' addresses relative to k_exp and v_exp
-  static constexpr int kOffExp = kOffInv + 16 * 4;                     // [kWarps][kStages][2][kChunk]
+  static constexpr int kOffExp = kOffRow + 8 * NB * 8;                 // [kWarps][kStages][2][kChunk]
   static constexpr int kOffRef = kOffExp + (kF8 ? kWarps * kStages * kChunk * 8 : 0);
   static constexpr int kOffBar = kOffRef + (kF8 ? kWarps * kStages * kChunk : 0);
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
@@ -125,25 +130,23 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Column of O that accumulator element e (0, 1) of n-tile nt holds in lanes j = lane % 4
-// (c = 2 j + e is the tile's column). bf16: the plain order. e4m3: the B operand's
-// column c of tile t is code t of the lane's 16 (8 at head dim 64) neighbouring ones.
-template <int D, bool F8>
-__device__ __forceinline__ int o_column(int nt, int c) {
-  if constexpr (!F8) return nt * 8 + c;
-  else if constexpr (D == 64) return 8 * c + nt;
-  else return (nt >> 4) * 128 + 16 * c + (nt & 15);
+// Transpose of an 8 x 8 matrix of 16-bit values: a lane's pair (row lane / 4, columns
+// 2 (lane % 4)..) becomes (column lane / 4, rows 2 (lane % 4)..).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 
-template <int D, int FMT>
-__global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
+template <int D, int FMT, int NB>
+__global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     bd_paged_dec_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const AttnArgs a) {
-  using Cfg = DecCfg<D, FMT>;
+  using Cfg = DecCfg<D, FMT, NB>;
   constexpr bool F8 = Cfg::kF8;
   constexpr int NW = Cfg::kWarps, NST = Cfg::kStages, kChunk = Cfg::kChunk;
-  constexpr int ST = kChunk / 8, PT = kChunk / 16;  // key tiles of S, contraction steps of P V
-  constexpr int KS = D / 16, NT = D / 8;  // contraction steps of q . k, column tiles of O
+  constexpr int KT = kChunk / 16;          // 16-key tiles of a chunk
+  constexpr int KS = D / 16, MT = D / 16;  // contraction steps of q . k, 16-column tiles of O
   constexpr float kPShift = F8 ? 7.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -189,60 +192,63 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
     const int k = min(ck + lane % kChunk, ck1 - 1);
     cpage = plan[cpages + (k >> pshift)];
   };
-  auto issue = [&](uint32_t it) {
-    if (cp >= p1) return;
-    const int s = int(it % NST);
-    const uint32_t full = bars + 8 * s;
-    const int keys = min(kChunk, ck1 - ck);
-    const int n = (keys + brows - 1) / brows;  // copies (1 or 2) of K and of V
+  int is = 0;  // stage of the next chunk to come
+  uint32_t issued = 0;
+  auto issue = [&]() {
+    const uint32_t full = bars + 8 * is;
+    const int keys = ck1 - ck, row = (ck + lane % kChunk) & ((1 << pshift) - 1);
+    const bool two = kChunk == 32 && brows == 16 && keys > 16;  // copies of K and of V: one, or two
     if constexpr (F8) {
-      // the 4-byte words of K's and V's exponents; a word's low address bits for later
-      const int key = min(lane % kChunk, keys - 1);
-      const int64_t o = int64_t(cpage) * a.e_sp + int64_t((ck + key) & ((1 << pshift) - 1)) * a.e_sr + int64_t(chkv) * a.e_sh;
+      // the 4-byte words of K's and V's exponents; a word's low address bits for later.
+      // (Past the keys' end: the last key's.)
+      const int back = max(lane % kChunk - keys + 1, 0);
+      const int64_t o = int64_t(cpage) * a.e_sp + (row - back) * int(a.e_sr) + chkv * int(a.e_sh);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         if (kChunk == 32 || (lane >> 4) == m) {
           const uintptr_t at = reinterpret_cast<uintptr_t>((m ? a.v_exp : a.k_exp) + o);
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(exps + ((s * 2 + m) * kChunk + lane % kChunk) * 4),
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(exps + ((is * 2 + m) * kChunk + lane % kChunk) * 4),
                        "l"(at & ~uintptr_t(3))
                        : "memory");
         }
-      eref[s * kChunk + lane % kChunk] = uint8_t(o & 3);
+      eref[is * kChunk + lane % kChunk] = uint8_t(o & 3);
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
     }
-    if (lane == 0) mbar_expect_tx(full, uint32_t(2 * n * brows * Cfg::kRowBytes));
+    if (lane == 0) mbar_expect_tx(full, uint32_t(2 * Cfg::kRowBytes) * uint32_t(two ? kChunk : brows));
     __syncwarp();
-    if (lane % 16 == 0 && lane / 16 < n) {  // lane 16 is at the second page's first key
-      const uint32_t dst = ring + s * Cfg::kStageBytes + (lane / 16) * 16 * Cfg::kPieceBytes;
-      const int row = (ck + lane) & ((1 << pshift) - 1);
+    if (lane == 0 || (two && lane == 16)) {  // lane 16 is at the second page's first key
+      const uint32_t dst = ring + is * Cfg::kStageBytes + lane * Cfg::kPieceBytes;
 #pragma unroll
       for (int c = 0; c < Cfg::kPieces; ++c) {
         tma_load_5d(dst + c * kChunk * Cfg::kPieceBytes, &tm_k, full, 0, row, c, chkv, cpage);
         tma_load_5d(dst + Cfg::kMatBytes + c * kChunk * Cfg::kPieceBytes, &tm_v, full, 0, row, c, chkv, cpage);
       }
     }
+    is = is + 1 == NST ? 0 : is + 1;
+    ++issued;
     next_chunk();
   };
 
   next_chunk();
-  uint32_t issued = 0, it = 0;
   bool ok = true;
-  for (; issued < uint32_t(NST) && cp < p1; ++issued) issue(issued);
+  for (int i = 0; i < NST && cp < p1; ++i) issue();
   __syncwarp();
+  int cs = 0;  // stage and phase of the next chunk to use
+  uint32_t phase = 0;
 
-  // ---- q of a block's rows rw, rw + 8 as A fragments (bf16 as it is)
-  uint32_t qa[KS][4];
+  // ---- q of a block's rows rw + 8 b as B fragments (bf16 as it is)
+  uint32_t qb[KS][NB][2];
   auto load_q = [&](int q0, int hkv, int row0, int nrows) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = rw + 8 * i, n = row0 + r, t = n / G;
+    for (int b = 0; b < NB; ++b) {
+      const int r = rw + 8 * b, n = row0 + r, t = n / G;
       const bool live = r < nrows;
       const __nv_bfloat16* qp = a.q + int64_t(q0 + t) * a.q_sr + int64_t(hkv * G + n % G) * a.q_sh;
       if constexpr (!F8) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          qa[s][i] = live ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * j) : 0u;
-          qa[s][2 + i] = live ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 8 + 2 * j) : 0u;
+          qb[s][b][0] = live ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * j) : 0u;
+          qb[s][b][1] = live ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 8 + 2 * j) : 0u;
         }
       } else {
         // lane j contracts over codes [x, x + 16) of the row, x as in the K loads below;
@@ -255,8 +261,8 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
             u = *reinterpret_cast<const uint4*>(qp + x);
             v = *reinterpret_cast<const uint4*>(qp + x + 8);
           }
-          qa[s][i] = u.x; qa[s][2 + i] = u.y; qa[s + 1][i] = u.z; qa[s + 1][2 + i] = u.w;
-          qa[s + 2][i] = v.x; qa[s + 2][2 + i] = v.y; qa[s + 3][i] = v.z; qa[s + 3][2 + i] = v.w;
+          qb[s][b][0] = u.x; qb[s][b][1] = u.y; qb[s + 1][b][0] = u.z; qb[s + 1][b][1] = u.w;
+          qb[s + 2][b][0] = v.x; qb[s + 2][b][1] = v.y; qb[s + 3][b][0] = v.z; qb[s + 3][b][1] = v.w;
         }
       }
     }
@@ -270,99 +276,108 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
     // the next block's rows, for its q
     const int32_t* X = piece(min(p + 1, p1 - 1));
     const int xq0 = X[PC_Q0], xhkv = X[PC_HKV], xrow0 = X[PC_ROW0], xnrows = X[PC_NROWS];
-    // ---- the two rows of this lane: the keys they see, their score factors (log2(e) /
-    // sqrt(d), e4m3: and the power of two taken out of q)
-    float qs[2];
-    int lim[2];
+    // ---- the rows of this lane's scores, 2 j + e + 8 b: the keys they see, their score
+    // factors (e4m3: log2(e) / sqrt(d) and the power of two taken out of q)
+    float qs[NB][2];
+    int lim[NB][2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = rw + 8 * i, t = (row0 + r) / G;
-      lim[i] = r >= nrows ? 0 : causal ? kvlen - qlen + t + 1 : kvlen;
-      qs[i] = a.scale_log2;
+    for (int b = 0; b < NB; ++b) {
+      float up_inv = 1.f;
       if constexpr (F8) {
         uint32_t mx = 0;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
-          mx = __vmaxu2(mx, __vmaxu2(qa[s][i] & 0x7fff7fffu, qa[s][2 + i] & 0x7fff7fffu));
+          mx = __vmaxu2(mx, __vmaxu2(qb[s][b][0] & 0x7fff7fffu, qb[s][b][1] & 0x7fff7fffu));
         mx = max(mx & 0xffffu, mx >> 16);
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         // max|q| = f 2^E -> f 2^14: a row below 2^-110 is scaled by 2^124 only
-        const int E = max(int(mx >> 7) - 127, -110);
-        const float up = __uint_as_float(uint32_t(127 + 14 - min(E, 113)) << 23);
-        qs[i] *= __uint_as_float(uint32_t(127 - 14 + min(E, 113)) << 23);
-        const float up2 = E > 113 ? __uint_as_float(uint32_t(127 - (E - 113)) << 23) : 1.f;
-        if (E > 113) qs[i] *= __uint_as_float(uint32_t(127 + (E - 113)) << 23);
+        const int E = max(int(mx >> 7) - 127, -110), E0 = min(E, 113);
+        const float up = __uint_as_float(uint32_t(127 + 14 - E0) << 23), up2 = __uint_as_float(uint32_t(127 - (E - E0)) << 23);
+        up_inv = __uint_as_float(uint32_t(127 - 14 + E0) << 23) * __uint_as_float(uint32_t(127 + (E - E0)) << 23);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t u = qa[s][2 * h + i];
-            qa[s][2 * h + i] = pack_f16(__uint_as_float(u << 16) * up * up2, __uint_as_float(u & 0xffff0000u) * up * up2);
+            const uint32_t u = qb[s][b][h];
+            qb[s][b][h] = pack_f16(__uint_as_float(u << 16) * up * up2, __uint_as_float(u & 0xffff0000u) * up * up2);
           }
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 2 * j + e + 8 * b;
+        lim[b][e] = r >= nrows ? 0 : causal ? kvlen - qlen + (row0 + r) / G + 1 : kvlen;
+        qs[b][e] = a.scale_log2 * (F8 ? __shfl_sync(0xffffffffu, up_inv, 4 * (2 * j + e)) : 1.f);
+      }
     }
-    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};
-    float o[NT][4];
+    float m[NB][2], l[NB][2], o[MT][NB][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int b = 0; b < NB; ++b) {
+      m[b][0] = m[b][1] = -CUDART_INF_F;
+      l[b][0] = l[b][1] = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+      for (int n = 0; n < MT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][b][e] = 0.f;
+    }
     // keys every live row sees (rows that do not exist see nothing: they need no mask)
     const int all_see = causal ? kvlen - qlen + row0 / G + 1 : kvlen;
 
-    for (int k = k0 + kChunk * warp; k < k1; k += kChunk * NW, ++it) {
-      const uint32_t st = ring + (it % NST) * Cfg::kStageBytes;
-      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * (it % NST), (it / NST) & 1, abort_flag))) ok = false;
-      // ---- S = q . k: tiles of 8 keys
-      float s[ST][4];
+    for (int k = k0 + kChunk * warp; k < k1; k += kChunk * NW) {
+      const uint32_t st = ring + cs * Cfg::kStageBytes;
+      if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * cs, phase, abort_flag))) ok = false;
+      // ---- S^T: tiles of 16 keys x 8 rows. Element (e, h) of a tile: row 2 j + e, key
+      // rw + 8 h
+      float s[KT][NB][4];
 #pragma unroll
-      for (int n = 0; n < ST; ++n)
+      for (int y = 0; y < KT; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[y][b][e] = 0.f;
       if constexpr (!F8) {
 #pragma unroll
-        for (int n = 0; n < ST; n += 2) {
-          const uint32_t krow = st + (8 * n + (lane >> 4) * 8 + (lane & 7)) * 128;
+        for (int c = 0; c < KS; ++c)
 #pragma unroll
-          for (int c = 0; c < KS; ++c) {
-            uint32_t b[4];
-            const uint32_t ch = uint32_t(2 * c + ((lane >> 3) & 1));
-            ldsm4(krow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
-            mma16<false>(s[n], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[0], b[1]);
-            mma16<false>(s[n + 1], qa[c][0], qa[c][1], qa[c][2], qa[c][3], b[2], b[3]);
+          for (int y = 0; y < KT; ++y) {
+            uint32_t x[4];
+            const uint32_t ch = uint32_t(2 * c + (lane >> 4));
+            ldsm4(st + (16 * y + (lane & 15)) * 128 + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), x);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) mma16<false>(s[y][b], x[0], x[1], x[2], x[3], qb[c][b][0], qb[c][b][1]);
           }
-        }
       } else {
 #pragma unroll
         for (int c = 0; c < KS / 4; ++c) {
-          uint4 u[ST];
+          uint4 u[2 * KT];
 #pragma unroll
-          for (int n = 0; n < ST; ++n) {
-            const int key = 8 * n + rw;
-            if constexpr (D == 64) u[n] = lds128(st + key * 64 + ((j ^ ((key >> 1) & 3)) << 4));
-            else u[n] = lds128(st + (c >> 1) * (kChunk * 128) + key * 128 + (((2 * j + (c & 1)) ^ (key & 7)) << 4));
+          for (int y = 0; y < 2 * KT; ++y) {
+            const int key = 8 * y + rw;
+            if constexpr (D == 64) u[y] = lds128(st + key * 64 + ((j ^ ((key >> 1) & 3)) << 4));
+            else u[y] = lds128(st + (c >> 1) * (kChunk * 128) + key * 128 + (((2 * j + (c & 1)) ^ (key & 7)) << 4));
           }
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int t = 4 * c + x;
+          for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int n = 0; n < ST; ++n) {
-              uint32_t b0, b1;
-              e4m3x4_to_f16(x == 0 ? u[n].x : x == 1 ? u[n].y : x == 2 ? u[n].z : u[n].w, b0, b1);
-              mma16<true>(s[n], qa[t][0], qa[t][1], qa[t][2], qa[t][3], b0, b1);
+            for (int y = 0; y < KT; ++y) {
+              uint32_t f[4];
+              auto word = [&](const uint4& v) { return x == 0 ? v.x : x == 1 ? v.y : x == 2 ? v.z : v.w; };
+              e4m3x4_to_f16(word(u[2 * y]), f[0], f[2]);
+              e4m3x4_to_f16(word(u[2 * y + 1]), f[1], f[3]);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                mma16<true>(s[y][b], f[0], f[1], f[2], f[3], qb[4 * c + x][b][0], qb[4 * c + x][b][1]);
             }
-          }
         }
       }
-      // ---- base-2 scores. This lane's keys are k + 8 n + 2 j + e; e4m3: ks, K's factor
-      // (first times the scores), and ve, V's exponent
-      float ve[2 * ST];
+      // ---- e4m3: the scores times K's factors; ve, V's exponents of this lane's keys
+      // k + 8 y + rw
+      float ve[2 * KT];
       bool vnan = false;
       uint32_t vb = 0;
       if constexpr (F8) {
-        uint32_t kb, low = eref[(it % NST) * kChunk + lane % kChunk];
-        const uint32_t at = exps + ((it % NST) * 2 * kChunk + lane % kChunk) * 4;
+        uint32_t kb, low = eref[cs * kChunk + lane % kChunk];
+        const uint32_t at = exps + (cs * 2 * kChunk + lane % kChunk) * 4;
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(kb) : "r"(at) : "memory");
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(vb) : "r"(at + kChunk * 4) : "memory");
         kb = (kb >> (8 * ((low + uint32_t(reinterpret_cast<uintptr_t>(a.k_exp))) & 3u))) & 255u;
@@ -370,85 +385,92 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
         vnan = __any_sync(0xffffffffu, vb == 255u);
         const float kf = exp_factor(kb), vf = vb == 255u ? 0.f : float(int(vb) - 127);
 #pragma unroll
-        for (int x = 0; x < 2 * ST; ++x) {
-          const int src = 8 * (x >> 1) + 2 * j + (x & 1);
-          const float f = __shfl_sync(0xffffffffu, kf, src);
-          ve[x] = __shfl_sync(0xffffffffu, vf, src);
-          s[x >> 1][x & 1] *= f;
-          s[x >> 1][2 + (x & 1)] *= f;
-        }
-      }
-      const bool edge = k + kChunk > all_see;
-      if (edge) {
+        for (int y = 0; y < 2 * KT; ++y) {
+          const float f = __shfl_sync(0xffffffffu, kf, 8 * y + rw);
+          ve[y] = __shfl_sync(0xffffffffu, vf, 8 * y + rw);
 #pragma unroll
-        for (int n = 0; n < ST; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (k + 8 * n + 2 * j + (e & 1) >= lim[e >> 1]) s[n][e] = -CUDART_INF_F;
-      }
-      float f[2];
-      bool grow = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float mx = -CUDART_INF_F;
-#pragma unroll
-        for (int n = 0; n < ST; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            mx = fmaxf(mx, F8 ? fmaf(s[n][2 * i + e], qs[i], ve[2 * n + e]) : s[n][2 * i + e] * a.scale_log2);
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // the maximum moves only when it grows by more than 2^8 (exact: l and O use
-        // the same one)
-        f[i] = 1.f;
-        if (mx > m[i] + 8.f) {
-          f[i] = ex2(m[i] - mx);
-          m[i] = mx;
-          l[i] *= f[i];
-          grow = true;
-        }
-      }
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[n][e] *= f[e >> 1];
-      }
-      uint32_t pa[PT][4];  // P as A operands: rows rw, rw + 8 x keys 16 y + 2 j.., 16 y + 8 + 2 j..
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float me = m[i] == -CUDART_INF_F ? 0.f : m[i];
-        float ls = 0.f;
-#pragma unroll
-        for (int n = 0; n < ST; ++n) {
-          if constexpr (F8) {
-            const float x0 = fmaf(s[n][2 * i], qs[i], -me), x1 = fmaf(s[n][2 * i + 1], qs[i], -me);
-            ls += ex2(x0) + ex2(x1);
-            pa[n >> 1][2 * (n & 1) + i] = pack_f16(ex2(x0 + (ve[2 * n] + kPShift)), ex2(x1 + (ve[2 * n + 1] + kPShift)));
-          } else {
-            const float p0f = ex2(fmaf(s[n][2 * i], a.scale_log2, -me)), p1f = ex2(fmaf(s[n][2 * i + 1], a.scale_log2, -me));
-            ls += p0f + p1f;
-            pa[n >> 1][2 * (n & 1) + i] = pack_bf16(p0f, p1f);
+          for (int b = 0; b < NB; ++b) {
+            s[y >> 1][b][2 * (y & 1)] *= f;
+            s[y >> 1][b][2 * (y & 1) + 1] *= f;
           }
         }
-        l[i] += ls;
       }
-      if (F8 && vnan) {  // a V row of NaN makes P NaN for the rows that see its key
+      if (k + kChunk > all_see) {
 #pragma unroll
-        for (int x = 0; x < 2 * ST; ++x) {
-          const bool bad = __shfl_sync(0xffffffffu, vb, 8 * (x >> 1) + 2 * j + (x & 1)) == 255u;
+        for (int y = 0; y < 2 * KT; ++y)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (bad && k + 8 * (x >> 1) + 2 * j + (x & 1) < lim[i])
-              pa[x >> 2][2 * ((x >> 1) & 1) + i] |= 0x7e00u << (16 * (x & 1));
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              if (k + 8 * y + rw >= lim[b][e]) s[y >> 1][b][2 * (y & 1) + e] = -CUDART_INF_F;
+      }
+      // ---- running maximum. It moves only when it grows by more than 2^8 (exact: l and O
+      // use the same one)
+      float f[NB][2];
+      bool grow = false;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = -CUDART_INF_F;
+#pragma unroll
+          for (int y = 0; y < 2 * KT; ++y) {
+            const float v = s[y >> 1][b][2 * (y & 1) + e];
+            mx = fmaxf(mx, F8 ? fmaf(v, qs[b][e], ve[y]) : v * a.scale_log2);
+          }
+#pragma unroll
+          for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+          f[b][e] = 1.f;
+          if (mx > m[b][e] + 8.f) {
+            f[b][e] = ex2(m[b][e] - mx);
+            m[b][e] = mx;
+            l[b][e] *= f[b][e];
+            grow = true;
+          }
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int n = 0; n < MT; ++n)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][b][e] *= f[b][e & 1];
+      }
+      // ---- P^T as B operands: rows 2 j, 2 j + 1 of key rw, turned into keys 2 j, 2 j + 1 of
+      // row rw
+      uint32_t pb[KT][NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float me[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) me[e] = m[b][e] == -CUDART_INF_F ? 0.f : m[b][e];
+#pragma unroll
+        for (int y = 0; y < 2 * KT; ++y) {
+          const float x0 = fmaf(s[y >> 1][b][2 * (y & 1)], F8 ? qs[b][0] : a.scale_log2, -me[0]);
+          const float x1 = fmaf(s[y >> 1][b][2 * (y & 1) + 1], F8 ? qs[b][1] : a.scale_log2, -me[1]);
+          const float p0f = ex2(x0), p1f = ex2(x1);
+          l[b][0] += p0f;
+          l[b][1] += p1f;
+          uint32_t w;
+          if constexpr (F8) {
+            w = pack_f16(ex2(x0 + (ve[y] + kPShift)), ex2(x1 + (ve[y] + kPShift)));
+            if (vnan) {  // a V row of NaN makes P NaN for the rows that see its key
+              const int key = 8 * y + rw;
+              if (__shfl_sync(0xffffffffu, vb, key) == 255u)
+                w |= (k + key < lim[b][0] ? 0x7e00u : 0u) | (k + key < lim[b][1] ? 0x7e000000u : 0u);
+            }
+          } else {
+            w = pack_bf16(p0f, p1f);
+          }
+          pb[y >> 1][b][y & 1] = transpose8(w);
         }
       }
-      // ---- O += P V. Keys at or past k1 may hold anything: their V become zeros.
+      // ---- O^T += V^T P^T. Keys at or past k1 may hold anything: their V become zeros.
       const uint32_t sv = st + Cfg::kMatBytes;
       auto values = [&](auto cut) {
         constexpr bool TAIL = decltype(cut)::value;
 #pragma unroll
-        for (int y = 0; y < PT; ++y) {
+        for (int y = 0; y < KT; ++y) {
           uint32_t vm[2] = {~0u, ~0u};
           if constexpr (TAIL) {
 #pragma unroll
@@ -458,19 +480,19 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
             }
           }
           if constexpr (!F8) {
-            const uint32_t vrow = sv + (16 * y + ((lane >> 3) & 1) * 8 + (lane & 7)) * 128;
+            const uint32_t vrow = sv + (16 * y + ((lane >> 4) & 1) * 8 + (lane & 7)) * 128;
 #pragma unroll
-            for (int n = 0; n < NT; n += 2) {
-              uint32_t b[4];
-              const uint32_t ch = uint32_t(n + (lane >> 4));
-              ldsm4t(vrow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), b);
-              if constexpr (TAIL) { b[0] &= vm[0]; b[1] &= vm[1]; b[2] &= vm[0]; b[3] &= vm[1]; }
-              mma16<false>(o[n], pa[y][0], pa[y][1], pa[y][2], pa[y][3], b[0], b[1]);
-              mma16<false>(o[n + 1], pa[y][0], pa[y][1], pa[y][2], pa[y][3], b[2], b[3]);
+            for (int n = 0; n < MT; ++n) {
+              uint32_t x[4];
+              const uint32_t ch = uint32_t(2 * n + ((lane >> 3) & 1));
+              ldsm4t(vrow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), x);
+              if constexpr (TAIL) { x[0] &= vm[0]; x[1] &= vm[0]; x[2] &= vm[1]; x[3] &= vm[1]; }
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16<false>(o[n][b], x[0], x[1], x[2], x[3], pb[y][b][0], pb[y][b][1]);
             }
           } else {
-            // this lane's B column is rw: 16 (8) neighbouring codes of keys 2 j, 2 j + 1,
-            // 8 + 2 j, 9 + 2 j, paired key by key
+            // A's rows rw and rw + 8 of a tile are neighbouring columns of V: of this lane's
+            // 16 (8) neighbouring codes of keys 2 j, 2 j + 1, 8 + 2 j, 9 + 2 j, paired key by key
 #pragma unroll
             for (int h = 0; h < (D + 127) / 128; ++h) {
               uint32_t x[4][4];
@@ -486,20 +508,18 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
                 }
               }
 #pragma unroll
-              for (int w4 = 0; w4 < (D == 64 ? 2 : 4); ++w4) {
-                // bytes (k, k') of codes 0, 1 and 2, 3 of the word
-                uint32_t b[2][4];
+              for (int w4 = 0; w4 < (D == 64 ? 2 : 4); ++w4)
 #pragma unroll
-                for (int z = 0; z < 2; ++z) {
-                  e4m3x4_to_f16(__byte_perm(x[2 * z][w4], x[2 * z + 1][w4], 0x5140), b[z][0], b[z][1]);
-                  e4m3x4_to_f16(__byte_perm(x[2 * z][w4], x[2 * z + 1][w4], 0x7362), b[z][2], b[z][3]);
-                }
+                for (int c = 0; c < 2; ++c) {
+                  // bytes (k, k') of codes 0, 1 (c = 0) or 2, 3 of the word
+                  uint32_t g[4];
+                  e4m3x4_to_f16(__byte_perm(x[0][w4], x[1][w4], c ? 0x7362 : 0x5140), g[0], g[1]);
+                  e4m3x4_to_f16(__byte_perm(x[2][w4], x[3][w4], c ? 0x7362 : 0x5140), g[2], g[3]);
+                  if constexpr (TAIL) { g[0] &= vm[0]; g[1] &= vm[0]; g[2] &= vm[1]; g[3] &= vm[1]; }
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  if constexpr (TAIL) { b[0][c] &= vm[0]; b[1][c] &= vm[1]; }
-                  mma16<true>(o[h * 16 + w4 * 4 + c], pa[y][0], pa[y][1], pa[y][2], pa[y][3], b[0][c], b[1][c]);
+                  for (int b = 0; b < NB; ++b)
+                    mma16<true>(o[h * 8 + w4 * 2 + c][b], g[0], g[1], g[2], g[3], pb[y][b][0], pb[y][b][1]);
                 }
-              }
             }
           }
         }
@@ -507,99 +527,97 @@ __global__ void __launch_bounds__(DecCfg<D, FMT>::kThreads, 2)
       if (k + kChunk > k1) values(std::true_type());
       else values(std::false_type());
       __syncwarp();  // every lane has read the stage
-      if (ok && issued == it + NST && cp < p1) {
-        issue(issued);
-        ++issued;
-      }
+      if (ok && cp < p1) issue();
       __syncwarp();
+      cs = cs + 1 == NST ? 0 : cs + 1;
+      phase ^= cs == 0 ? 1u : 0u;
     }
 
     // the next block's q comes while this block's results are added up
     if (p + 1 < p1) load_q(xq0, xhkv, xrow0, xnrows);
 
     // ---- add the warps' results up
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      // NaN scores leave the maximum alone: what they gave was taken relative to 0
-      if (m[i] == -CUDART_INF_F && l[i] != 0.f) m[i] = 0.f;
-    }
-    float* ml = reinterpret_cast<float*>(smem + Cfg::kOffMl);  // [NW][16][2]
+    float* ml = reinterpret_cast<float*>(smem + Cfg::kOffMl);  // [NW][8 NB][2]
     float* inv = reinterpret_cast<float*>(smem + Cfg::kOffInv);
+    int64_t* orow = reinterpret_cast<int64_t*>(smem + Cfg::kOffRow);
     float* sum = reinterpret_cast<float*>(smem + Cfg::kOffSum);
-    if (j == 0)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        ml[(warp * 16 + rw + 8 * i) * 2] = m[i];
-        ml[(warp * 16 + rw + 8 * i) * 2 + 1] = l[i];
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], x);
+        // NaN scores leave the maximum alone: what they gave was taken relative to 0
+        if (m[b][e] == -CUDART_INF_F && l[b][e] != 0.f) m[b][e] = 0.f;
+        if (rw == 0)
+          *reinterpret_cast<float2*>(&ml[(warp * 8 * NB + 8 * b + 2 * j + e) * 2]) = make_float2(m[b][e], l[b][e]);
       }
     __syncthreads();
-    float fac[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float M = -CUDART_INF_F;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + rw + 8 * i) * 2]);
-      fac[i] = (m[i] == -CUDART_INF_F ? 0.f : ex2(m[i] - M)) * (F8 ? 0.0078125f : 1.f);  // 2^-kPShift
-    }
-    float* part = slot < 0 ? nullptr : a.part + int64_t(slot) * slot_floats(kDecRows, D);
+    float* part = slot < 0 ? nullptr : a.part + int64_t(slot) * slot_floats(kDecSlotRows, D);
     if (int(threadIdx.x) < nrows) {
-      const int r = threadIdx.x, n = row0 + r;
+      const int r = threadIdx.x, n = row0 + r, t = q0 + n / G, h = hkv * G + n % G;
       float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 16 + r) * 2]);
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 8 * NB + r) * 2]);
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float mw = ml[(w * 16 + r) * 2];
-        L += mw == -CUDART_INF_F ? 0.f : ml[(w * 16 + r) * 2 + 1] * ex2(mw - M);
+        const float mw = ml[(w * 8 * NB + r) * 2];
+        L += mw == -CUDART_INF_F ? 0.f : ml[(w * 8 * NB + r) * 2 + 1] * ex2(mw - M);
       }
       inv[r] = M == -CUDART_INF_F ? 0.f : 1.f / L;
+      orow[r] = int64_t(t) * a.o_sr + int64_t(h) * a.o_sh;
       if (part) {
         part[r] = M;
-        part[kDecRows + r] = L;
+        part[kDecSlotRows + r] = L;
       } else if (a.lse) {
-        a.lse[int64_t(hkv * G + n % G) * a.l_sh + q0 + n / G] =
-            M == -CUDART_INF_F ? -CUDART_INF_F : (M + lg2(L)) * 0.69314718055994531f;
+        a.lse[int64_t(h) * a.l_sh + t] = M == -CUDART_INF_F ? -CUDART_INF_F : (M + lg2(L)) * 0.69314718055994531f;
       }
     }
-    // as many columns at a time as fit for the block's rows
-    const int rl = nrows <= 4 ? 2 : nrows <= 8 ? 3 : 4, tl = 6 - rl;  // log2 of rows, of column tiles
-    const int cols = 8 << tl, pitch = cols + 4;
-    for (int ps = 0; ps << tl < NT; ++ps) {
-      if (ps) __syncthreads();
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-        if (n >> tl == ps)
+    for (int b = 0; b < NB; ++b) {
+      float fac[2];
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (rw + 8 * i < nrows)
-              *reinterpret_cast<float2*>(&sum[warp * Cfg::kSumFloats + (rw + 8 * i) * pitch + 8 * (n - (ps << tl)) + 2 * j]) =
-                  make_float2(o[n][2 * i] * fac[i], o[n][2 * i + 1] * fac[i]);
-      __syncthreads();
-      const int cw = min(cols, D - ps * cols) >> 1;  // column pairs of this round
-      for (int x = threadIdx.x; x < nrows * cw; x += Cfg::kThreads) {
-        const int r = x / cw, c = 2 * (x - r * cw);
-        float2 t = make_float2(0.f, 0.f);
+      for (int e = 0; e < 2; ++e) {
+        float M = -CUDART_INF_F;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-          const float2 u = *reinterpret_cast<const float2*>(&sum[w * Cfg::kSumFloats + r * pitch + c]);
-          t.x += u.x;
-          t.y += u.y;
-        }
-        const int nt = (ps << tl) + (c >> 3), c0 = o_column<D, F8>(nt, c & 7), c1 = o_column<D, F8>(nt, (c & 7) + 1);
-        const int n = row0 + r;
-        if (part) {
-          float* P = part + 2 * kDecRows + r * D;
-          P[c0] = t.x;
-          P[c1] = t.y;
-        } else {
-          __nv_bfloat16* O = a.o + int64_t(q0 + n / G) * a.o_sr + int64_t(hkv * G + n % G) * a.o_sh;
-          if constexpr (F8) {
-            O[c0] = __float2bfloat16_rn(t.x * inv[r]);
-            O[c1] = __float2bfloat16_rn(t.y * inv[r]);
+        for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 8 * NB + 8 * b + 2 * j + e) * 2]);
+        fac[e] = (m[b][e] == -CUDART_INF_F ? 0.f : ex2(m[b][e] - M)) * (F8 ? 0.0078125f : 1.f);  // 2^-kPShift
+      }
+#pragma unroll
+      for (int rd = 0; rd < D / Cfg::kCols; ++rd) {
+        if (b || rd) __syncthreads();
+        // e4m3: a lane has columns [16 rw, 16 rw + 16) of 128 (8 of 64), half of which, W, go
+        // in a round, kept together
+        constexpr int NR = Cfg::kCols / 16, W = Cfg::kCols / 8;
+#pragma unroll
+        for (int n = 0; n < NR; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x0 = o[rd * NR + n][b][e] * fac[e], x1 = o[rd * NR + n][b][2 + e] * fac[e];
+            float* S = sum + warp * Cfg::kSumFloats + (2 * j + e) * Cfg::kPitch;
+            if constexpr (F8) {
+              *reinterpret_cast<float2*>(&S[W * rw + 2 * n]) = make_float2(x0, x1);
+            } else {
+              S[16 * n + rw] = x0;
+              S[16 * n + 8 + rw] = x1;
+            }
+          }
+        __syncthreads();
+        const int rows = min(8, nrows - 8 * b);
+        for (int x = threadIdx.x; x < rows * (Cfg::kCols / 4); x += Cfg::kThreads) {
+          const int r = x / (Cfg::kCols / 4), c = 4 * (x % (Cfg::kCols / 4));
+          float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int w = 0; w < NW; ++w) {
+            const float4 u = *reinterpret_cast<const float4*>(&sum[w * Cfg::kSumFloats + r * Cfg::kPitch + c]);
+            t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+          }
+          const int col = F8 ? (rd >> 1) * 128 + (c / W) * 2 * W + (rd & 1) * W + c % W : rd * Cfg::kCols + c;
+          if (part) {
+            *reinterpret_cast<float4*>(part + 2 * kDecSlotRows + (8 * b + r) * D + col) = t;
           } else {
-            *reinterpret_cast<uint32_t*>(O + c0) = pack_bf16(t.x * inv[r], t.y * inv[r]);
+            const float g = inv[8 * b + r];
+            *reinterpret_cast<uint2*>(a.o + orow[8 * b + r] + col) = make_uint2(pack_bf16(t.x * g, t.y * g), pack_bf16(t.z * g, t.w * g));
           }
         }
       }
@@ -670,17 +688,17 @@ __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) 
   const int n = a.plan[PH_NDECM], cnt = M[MG_N], rows = M[MG_NROWS];
   if (int(blockIdx.x) >= n) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(kDecRows, D);
+  const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(kDecSlotRows, D);
   for (int r = blockIdx.y; r < rows; r += kMergeY) {
     float acc[V], m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
 #pragma unroll 4
     for (int i = warp; i < cnt; i += 8) {
-      const float* P = base + int64_t(i) * slot_floats(kDecRows, D);
-      const float mi = __ldcg(P + r), li = __ldcg(P + kDecRows + r);
+      const float* P = base + int64_t(i) * slot_floats(kDecSlotRows, D);
+      const float mi = __ldcg(P + r), li = __ldcg(P + kDecSlotRows + r);
       float ov[V];
-      load_cols(P + 2 * kDecRows + r * D + lane * V, ov);
+      load_cols(P + 2 * kDecSlotRows + r * D + lane * V, ov);
       join(m, l, acc, mi, li, ov);
     }
 #pragma unroll
@@ -730,20 +748,35 @@ __global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArg
   }
 }
 
-template <int D, int FMT>
-int32_t launch_dec_t(const CUtensorMap& mk, const CUtensorMap& mv, const AttnArgs& a, cudaStream_t s) {
-  using Cfg = DecCfg<D, FMT>;
+template <int D, int FMT, int NB>
+int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+  using Cfg = DecCfg<D, FMT, NB>;
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(bd_paged_dec_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(bd_paged_dec_kernel<D, FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged few-rows)");
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
-  bd_paged_dec_kernel<D, FMT><<<kDecCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mk, mv, a);
+  const int es = Cfg::kF8 ? 1 : 2, rows = w[PH_PAGE] < Cfg::kChunk ? w[PH_PAGE] : Cfg::kChunk;
+  CUtensorMap mk, mv;
+  int32_t st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, 1))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, 1))) return st;
+  bd_paged_dec_kernel<D, FMT, NB><<<kDecCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mk, mv, a);
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
+}
+
+template <int D, int FMT>
+int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+  const int rows = w[PH_DEC_ROWS];
+  if (rows == 8) return launch_dec_t<D, FMT, 1>(w, c, a, s);
+  if (rows == 16) return launch_dec_t<D, FMT, 2>(w, c, a, s);
+  if constexpr (dec_block_rows(D, FMT) == 32)
+    if (rows == 32) return launch_dec_t<D, FMT, 4>(w, c, a, s);
+  return fail(BD_ERR_PLAN, "few-rows blocks of %d rows at head dim %d", rows, D);
 }
 
 // The join starts while the attention kernel drains, and waits for its results itself.
@@ -774,17 +807,12 @@ int32_t launch_merge(const MergeArgs& a, int d, bool tile, cudaStream_t s) {
 }
 
 int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, cudaStream_t s) {
-  const int es = c->fmt == BD_CACHE_BF16 ? 2 : 1, d = w[PH_D];
-  const int chunk = d * es <= 128 ? 32 : 16, rows = w[PH_PAGE] < chunk ? w[PH_PAGE] : chunk;
-  CUtensorMap mk, mv;
-  int32_t st;
-  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", rows, 1))) return st;
-  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", rows, 1))) return st;
+  const int d = w[PH_D];
   if (c->fmt == BD_CACHE_BF16)
-    return d == 64 ? launch_dec_t<64, BD_CACHE_BF16>(mk, mv, a, s)
-           : d == 128 ? launch_dec_t<128, BD_CACHE_BF16>(mk, mv, a, s) : launch_dec_t<256, BD_CACHE_BF16>(mk, mv, a, s);
-  return d == 64 ? launch_dec_t<64, BD_CACHE_E4M3>(mk, mv, a, s)
-         : d == 128 ? launch_dec_t<128, BD_CACHE_E4M3>(mk, mv, a, s) : launch_dec_t<256, BD_CACHE_E4M3>(mk, mv, a, s);
+    return d == 64 ? launch_dec_rows<64, BD_CACHE_BF16>(w, c, a, s)
+           : d == 128 ? launch_dec_rows<128, BD_CACHE_BF16>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_BF16>(w, c, a, s);
+  return d == 64 ? launch_dec_rows<64, BD_CACHE_E4M3>(w, c, a, s)
+         : d == 128 ? launch_dec_rows<128, BD_CACHE_E4M3>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_E4M3>(w, c, a, s);
 }
 
 }  // namespace bd
@@ -794,7 +822,7 @@ using namespace bd;
 // Partial results of the few-rows kernel, then of the tile kernel (at most
 // kDecSlots and kTilePartSlots slots, whatever the lengths; none for a kernel that is not launched).
 static size_t dec_part_bytes(const int32_t* w) {
-  return w[PH_NDEC] ? size_t(kDecSlots) * slot_floats(kDecRows, w[PH_D]) * 4 : 0;
+  return w[PH_NDEC] ? size_t(kDecSlots) * slot_floats(kDecSlotRows, w[PH_D]) * 4 : 0;
 }
 static size_t part_bytes(const int32_t* w) {
   return dec_part_bytes(w) + (w[PH_NTILE] ? size_t(kTilePartSlots) * slot_floats(tile_slot_rows(w[PH_D]), w[PH_D]) * 4 : 0);

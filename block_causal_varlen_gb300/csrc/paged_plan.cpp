@@ -10,7 +10,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <cstdlib>
 #include <functional>
 #include <queue>
 #include <utility>
@@ -38,10 +37,6 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
 }
 
 namespace {
-
-// Sequences of at most this many (new row, head) pairs of a K/V head go to the few-rows
-// kernel, whose blocks hold kDecRows.
-constexpr int kDecMaxRows = kDecRows;
 
 struct Item {
   int32_t seq, hkv, row0, nrows, keys;
@@ -226,12 +221,13 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
 }
 
 // Few-rows blocks: short against their keys, cheap to join: always cut evenly. A
-// piece's own cost is some 3 units of 32 keys.
+// piece's own cost (its q, adding up the warps' results, the pipeline's start) is some
+// 6 units of 32 keys: 64 ragged sequences, e4m3: 145 us counting 3, 138 counting 10, bf16
+// the other way round by 1%.
 void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
                const std::vector<int32_t>& page_off, Lists* L) {
-  const int kOver = getenv("BD_OVER") ? atoi(getenv("BD_OVER")) : 6;
   std::vector<Part> parts;
-  if (!items.empty()) cut_evenly(items, kDecUnit, kOver, kDecCtas, &parts);
+  if (!items.empty()) cut_evenly(items, kDecUnit, 6, kDecCtas, &parts);
   write_lists(D, items, parts, q0, page_off, kDecUnit, kDecCtas, L);
 }
 
@@ -242,7 +238,7 @@ void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std
 // results about 3 + n / 40).
 void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
                 const std::vector<int32_t>& page_off, Lists* L) {
-  const int kOver = getenv("BD_TOVER") ? atoi(getenv("BD_TOVER")) : 2;
+  constexpr int kOver = 2;
   std::vector<Part> best, parts;
   if (!items.empty()) {
     int64_t total = 0;
@@ -315,6 +311,7 @@ int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npage
 struct Built {
   int64_t T, kv, npages;
   Lists dec, tile;
+  int32_t dec_rows;
 };
 
 int32_t prepare(const bd_paged_desc* D, Built* X) {
@@ -330,15 +327,25 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
     pg += (int64_t(D->kv_len[b]) + D->page_size - 1) / D->page_size;
     if (pg > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
   }
+  // Sequences of up to 32 (new row, head) pairs of a K/V head go to the few-rows kernel, in
+  // blocks of one size (a tile of 32 rows in use costs what one of 128 does). e4m3: two
+  // blocks of 16 (16 sequences of 20000 rows, 32 pairs, d 128: 230 us, as tiles 346); at
+  // head dim 256, where two blocks read twice what a tile does, up to 16 (605 us as
+  // tiles, 768 as two blocks).
+  const int most = D->d == 256 ? 16 : 32;
+  int32_t widest = 1;
+  for (int32_t b = 0; b < D->B; ++b)
+    if (int64_t(D->q_len[b]) * G <= most) widest = std::max(widest, D->q_len[b] * G);
+  X->dec_rows = std::min(widest <= 8 ? 8 : widest <= 16 ? 16 : 32, dec_block_rows(D->d, D->fmt));
   // every row block of a (sequence, K/V head): keys up to what its last row sees
   std::vector<Item> dec, tile;
   int64_t nitems = 0;
-  for (int32_t b = 0; b < D->B; ++b) nitems += (int64_t(D->q_len[b]) * G + kDecRows - 1) / kDecRows * D->Hkv;
+  for (int32_t b = 0; b < D->B; ++b) nitems += (int64_t(D->q_len[b]) * G + 7) / 8 * D->Hkv;
   if (nitems > (1 << 26)) return fail(BD_ERR_CAPACITY, "plan of more than 2^26 row blocks");
   for (int32_t b = 0; b < D->B; ++b) {
     const int32_t q = D->q_len[b], n = D->kv_len[b], rows = q * G;
-    const bool few = rows <= kDecMaxRows;
-    const int32_t step = few ? kDecRows : 128 / G * G * tile_slots(D->d);
+    const bool few = rows <= most;
+    const int32_t step = few ? X->dec_rows : 128 / G * G * tile_slots(D->d);
     for (int32_t g = 0; g < D->Hkv; ++g)
       for (int32_t r0 = 0; r0 < rows; r0 += step) {
         const int32_t r1 = std::min(rows, r0 + step);
@@ -437,6 +444,7 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
     std::copy(L.pieces.begin(), L.pieces.end(), w + at);
     at += int64_t(L.pieces.size());
   };
+  w[PH_DEC_ROWS] = X.dec_rows;
   put(X.dec, PH_OFF_DEC, PH_NDEC, PH_NDECM, kOffDecRec, kOffDecMerge);
   put(X.tile, PH_OFF_TILE, PH_NTILE, PH_NTILEM, kOffTileRec, kOffTileMerge);
   return ok();
@@ -449,7 +457,7 @@ extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
   if (st) return st;
   // what a captured launch holds of the plan (FNV-1a over the words)
   const int32_t fields[] = {w[PH_H], w[PH_HKV], w[PH_D], w[PH_PAGE], w[PH_NUM_PAGES], w[PH_FMT], w[PH_CAUSAL],
-                            w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0, w[PH_NDECM] > 0,
+                            w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0, w[PH_NDECM] > 0,
                             w[PH_NTILE] > 0, w[PH_NTILEM] > 0};
   uint64_t h = 1469598103934665603ull;
   for (int32_t f : fields)

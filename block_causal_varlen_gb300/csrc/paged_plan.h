@@ -15,7 +15,11 @@ constexpr int32_t kPagedVersion = 1;
 // (tiles) or two (few rows: one adds up a block while the other's loads go on) on each.
 constexpr int kPagedSms = 152;
 constexpr int kDecCtas = 2 * kPagedSms, kTileCtas = kPagedSms;
-constexpr int kDecRows = 16;   // (new row, query head) pairs of one K/V head in a few-rows block
+// A few-rows block has 8, 16 or (where registers hold it: bf16, head dims 64 and 128) 32
+// (new row, query head) pairs of one K/V head: the least that holds every sequence of
+// the plan that goes there.
+constexpr int dec_block_rows(int d, int fmt) { return d <= 128 && fmt == BD_CACHE_BF16 ? 32 : 16; }
+constexpr int kDecSlotRows = 32;
 constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cut
 // Tiles (of 128 / G new rows x G heads) of one K/V head that share a key tile in the
 // tile kernel, and the rows of its partial-result slots.
@@ -36,7 +40,8 @@ enum : int {
   PH_OFF_PGCNT,    // int32 [npages]: rows of the page in use
   PH_OFF_DEC,      // few-rows kernel: its pieces, CTA after CTA,
   PH_NDEC,         // their number,
-  PH_NDECM,        // and the joins of its split blocks
+  PH_NDECM,        // the joins of its split blocks,
+  PH_DEC_ROWS,     // and the rows of a block
   PH_OFF_TILE,     // the same for the tile kernel
   PH_NTILE,
   PH_NTILEM,
