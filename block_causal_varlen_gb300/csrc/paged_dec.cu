@@ -18,7 +18,7 @@
 //     ends of blocks, so loads never stop; the warps meet only to add up a block;
 //   - the products are S^T = K Q^T and O^T = V^T P^T: keys and head columns fill the 16
 //     rows of the A operand, the block's rows its 8 columns, so a block of up to 8 rows
-//     (a group's heads of one new row) wastes nothing, and 16 or 32 rows reuse K's and
+//     (a group's heads of one new row) wastes nothing, and up to 32 rows reuse K's and
 //     V's fragments;
 //   - e4m3 chunks go from shared memory to fp16 fragments in registers (exact). The
 //     contraction order of q . k is permuted so that a lane reads 32 neighbouring
@@ -49,24 +49,34 @@ namespace {
 template <int D, int FMT, int NB>
 struct DecCfg {
   static constexpr bool kF8 = FMT == BD_CACHE_E4M3;
-  static constexpr int kRowBytes = D * (kF8 ? 1 : 2);         // a key's K (or V) of one head
-  static constexpr int kPieces = kRowBytes <= 128 ? 1 : kRowBytes / 128;  // 128-byte pieces of a row
+  // head dim 256: two warps share a chunk's keys, each with half of the columns. Each
+  // loads its half, forms its half of the scores, and adds the other's to them (through
+  // shared memory); O's columns are its own.
+  static constexpr int kDim = D == 256 ? 128 : D, kSplit = D / kDim;
+  static constexpr int kRowBytes = kDim * (kF8 ? 1 : 2);      // a warp's part of a key's K (or V) of one head
+  static constexpr int kPieces = kRowBytes <= 128 ? 1 : kRowBytes / 128;  // 128-byte pieces of it
   static constexpr int kPieceBytes = kRowBytes / kPieces;
   // keys a warp takes at a time: 32 where that is no more than 8 KB and registers allow
   // (what a chunk costs besides its products then counts half)
   static constexpr int kChunk = kRowBytes <= 128 && NB <= 2 ? 32 : 16;
   static constexpr int kMatBytes = kChunk * kRowBytes;        // K (or V) of a chunk
   static constexpr int kStageBytes = 2 * kMatBytes;
-  // warps and ring depth: up to 192 KB of chunks per SM and its two CTAs (some 45 KB
-  // must be in flight to cover HBM's latency at its rate)
-  static constexpr int kWarps = kStageBytes >= 16384 ? 2 : 4;
-  static constexpr int kStages = kStageBytes >= 8192 ? 3 : kStageBytes == 4096 ? 5 : 8;
+  static constexpr int kWarps = 4, kLanes = kWarps / kSplit;  // kLanes: chunks in work at a time
   static constexpr int kThreads = 32 * kWarps;
-  // a warp's share of a block is added up 8 rows x kCols columns at a time
+  // a warp's share of a block is added up 8 rows x kCols columns at a time; head dim 256's
+  // scores pass through the same place, two chunks in turn
   static constexpr int kCols = D == 64 ? 32 : 64, kPitch = kCols + 4, kSumFloats = 8 * kPitch;
+  static constexpr int kXchg = kSplit == 2 ? kChunk / 16 * NB * 512 : 0;  // a warp's scores
+  static constexpr int kSumBytes = kWarps * (kSumFloats * 4 > 2 * kXchg ? kSumFloats * 4 : 2 * kXchg);
+  // ring depth: up to 192 KB of chunks per SM and its two CTAs (some 45 KB must be in
+  // flight to cover HBM's latency at its rate)
+  static constexpr int kPerStage = kWarps * (kStageBytes + 8 + (kF8 ? 9 * kChunk : 0));
+  static constexpr int kRest = kSumBytes + kWarps * 8 * NB * 8 + 8 * NB * 12 + 16 + 1024;
+  static constexpr int kStages = (115712 - kRest) / kPerStage < 6 ? (115712 - kRest) / kPerStage : 6;
+  static_assert(kStages >= 2, "a ring of two chunks at least");
   static constexpr int kOffRing = 0;
   static constexpr int kOffSum = kOffRing + kWarps * kStages * kStageBytes;
-  static constexpr int kOffMl = kOffSum + kWarps * kSumFloats * 4;     // m, l [kWarps][8 NB]
+  static constexpr int kOffMl = kOffSum + kSumBytes;                   // m, l [kWarps][8 NB]
   static constexpr int kOffInv = kOffMl + kWarps * 8 * NB * 2 * 4;     // 1 / l of the block's rows
   static constexpr int kOffRow = kOffInv + 8 * NB * 4;                 // their places in O
   // e4m3: 4-byte words around K's and V's exponent bytes of a chunk's keys, and the low
@@ -145,13 +155,15 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   using Cfg = DecCfg<D, FMT, NB>;
   constexpr bool F8 = Cfg::kF8;
   constexpr int NW = Cfg::kWarps, NST = Cfg::kStages, kChunk = Cfg::kChunk;
-  constexpr int KT = kChunk / 16;          // 16-key tiles of a chunk
-  constexpr int KS = D / 16, MT = D / 16;  // contraction steps of q . k, 16-column tiles of O
+  constexpr int DW = Cfg::kDim, PW = Cfg::kSplit, NL = Cfg::kLanes;
+  constexpr int KT = kChunk / 16;            // 16-key tiles of a chunk
+  constexpr int KS = DW / 16, MT = DW / 16;  // contraction steps of q . k, 16-column tiles of O
   constexpr float kPShift = F8 ? 7.f : 0.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane & 3, rw = lane >> 2;
+  const int half = warp % PW, kl = warp / PW;  // this warp's columns, and its place among the chunks
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffAbort);
   const uint32_t ring = sbase + Cfg::kOffRing + warp * NST * Cfg::kStageBytes;
   const uint32_t bars = sbase + Cfg::kOffBar + warp * NST * 8;
@@ -161,6 +173,10 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   const int32_t* rec = plan + kOffDecRec + blockIdx.x * kRecordWords;
   const int p0 = rec[RC_P0], p1 = rec[RC_P1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
   if (p0 == p1) return;
   const int32_t* pieces = plan + plan[PH_OFF_DEC];
   auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
@@ -180,11 +196,11 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   // issued, so that issuing waits for nothing.
   int cp = p0 - 1, ck = 0, ck1 = 0, chkv = 0, cpages = 0, cpage = 0;  // cpage: of key ck + lane (mod kChunk)
   auto next_chunk = [&]() {
-    ck += kChunk * NW;
+    ck += kChunk * NL;
     while (ck >= ck1) {
       if (++cp >= p1) return;
       const int32_t* W = piece(cp);
-      ck = W[PC_K0] + kChunk * warp;
+      ck = W[PC_K0] + kChunk * kl;
       ck1 = W[PC_K1];
       chkv = W[PC_HKV];
       cpages = W[PC_PAGES];
@@ -220,8 +236,8 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
       const uint32_t dst = ring + is * Cfg::kStageBytes + lane * Cfg::kPieceBytes;
 #pragma unroll
       for (int c = 0; c < Cfg::kPieces; ++c) {
-        tma_load_5d(dst + c * kChunk * Cfg::kPieceBytes, &tm_k, full, 0, row, c, chkv, cpage);
-        tma_load_5d(dst + Cfg::kMatBytes + c * kChunk * Cfg::kPieceBytes, &tm_v, full, 0, row, c, chkv, cpage);
+        tma_load_5d(dst + c * kChunk * Cfg::kPieceBytes, &tm_k, full, 0, row, half * Cfg::kPieces + c, chkv, cpage);
+        tma_load_5d(dst + Cfg::kMatBytes + c * kChunk * Cfg::kPieceBytes, &tm_v, full, 0, row, half * Cfg::kPieces + c, chkv, cpage);
       }
     }
     is = is + 1 == NST ? 0 : is + 1;
@@ -234,7 +250,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   for (int i = 0; i < NST && cp < p1; ++i) issue();
   __syncwarp();
   int cs = 0;  // stage and phase of the next chunk to use
-  uint32_t phase = 0;
+  uint32_t phase = 0, cs2 = 0;
 
   // ---- q of a block's rows rw + 8 b as B fragments (bf16 as it is)
   uint32_t qb[KS][NB][2];
@@ -243,7 +259,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     for (int b = 0; b < NB; ++b) {
       const int r = rw + 8 * b, n = row0 + r, t = n / G;
       const bool live = r < nrows;
-      const __nv_bfloat16* qp = a.q + int64_t(q0 + t) * a.q_sr + int64_t(hkv * G + n % G) * a.q_sh;
+      const __nv_bfloat16* qp = a.q + int64_t(q0 + t) * a.q_sr + int64_t(hkv * G + n % G) * a.q_sh + half * DW;
       if constexpr (!F8) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
@@ -255,7 +271,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         // step s takes four of them
 #pragma unroll
         for (int s = 0; s < KS; s += 4) {
-          const int x = D == 64 ? 16 * j : (s >> 3) * 128 + 32 * j + ((s >> 2) & 1) * 16;
+          const int x = D == 64 ? 16 * j : 32 * j + (s >> 2) * 16;
           uint4 u = make_uint4(0, 0, 0, 0), v = u;
           if (live) {
             u = *reinterpret_cast<const uint4*>(qp + x);
@@ -323,7 +339,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     // keys every live row sees (rows that do not exist see nothing: they need no mask)
     const int all_see = causal ? kvlen - qlen + row0 / G + 1 : kvlen;
 
-    for (int k = k0 + kChunk * warp; k < k1; k += kChunk * NW) {
+    for (int k = k0 + kChunk * kl; k < k1; k += kChunk * NL) {
       const uint32_t st = ring + cs * Cfg::kStageBytes;
       if (!__all_sync(0xffffffffu, mbar_wait(bars + 8 * cs, phase, abort_flag))) ok = false;
       // ---- S^T: tiles of 16 keys x 8 rows. Element (e, h) of a tile: row 2 j + e, key
@@ -354,7 +370,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
           for (int y = 0; y < 2 * KT; ++y) {
             const int key = 8 * y + rw;
             if constexpr (D == 64) u[y] = lds128(st + key * 64 + ((j ^ ((key >> 1) & 3)) << 4));
-            else u[y] = lds128(st + (c >> 1) * (kChunk * 128) + key * 128 + (((2 * j + (c & 1)) ^ (key & 7)) << 4));
+            else u[y] = lds128(st + key * 128 + (((2 * j + c) ^ (key & 7)) << 4));
           }
 #pragma unroll
           for (int x = 0; x < 4; ++x)
@@ -370,6 +386,34 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
             }
         }
       }
+      if constexpr (PW == 2) {
+        // the halves of the scores, each times its factor, meet
+        const uint32_t xb = sbase + Cfg::kOffSum + ((cs2 * NW + warp) * KT * NB * 32 + lane) * 16;
+        const uint32_t xo = sbase + Cfg::kOffSum + ((cs2 * NW + (warp ^ 1)) * KT * NB * 32 + lane) * 16;
+#pragma unroll
+        for (int y = 0; y < KT; ++y)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[y][b][e] *= qs[b][e & 1];
+            st_shared_v4(xb + (y * NB + b) * 512, __float_as_uint(s[y][b][0]), __float_as_uint(s[y][b][1]),
+                         __float_as_uint(s[y][b][2]), __float_as_uint(s[y][b][3]));
+          }
+        named_bar_sync(1 + kl, 64);
+#pragma unroll
+        for (int y = 0; y < KT; ++y)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint4 u = lds128(xo + (y * NB + b) * 512);
+            s[y][b][0] += __uint_as_float(u.x);
+            s[y][b][1] += __uint_as_float(u.y);
+            s[y][b][2] += __uint_as_float(u.z);
+            s[y][b][3] += __uint_as_float(u.w);
+          }
+        cs2 ^= 1;
+      }
+      // what is left to multiply the scores by
+      auto factor = [&](int b, int e) { return PW == 2 ? 1.f : F8 ? qs[b][e] : a.scale_log2; };
       // ---- e4m3: the scores times K's factors; ve, V's exponents of this lane's keys
       // k + 8 y + rw
       float ve[2 * KT];
@@ -416,7 +460,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
 #pragma unroll
           for (int y = 0; y < 2 * KT; ++y) {
             const float v = s[y >> 1][b][2 * (y & 1) + e];
-            mx = fmaxf(mx, F8 ? fmaf(v, qs[b][e], ve[y]) : v * a.scale_log2);
+            mx = fmaxf(mx, F8 ? fmaf(v, factor(b, e), ve[y]) : v * factor(b, e));
           }
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -446,8 +490,8 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         for (int e = 0; e < 2; ++e) me[e] = m[b][e] == -CUDART_INF_F ? 0.f : m[b][e];
 #pragma unroll
         for (int y = 0; y < 2 * KT; ++y) {
-          const float x0 = fmaf(s[y >> 1][b][2 * (y & 1)], F8 ? qs[b][0] : a.scale_log2, -me[0]);
-          const float x1 = fmaf(s[y >> 1][b][2 * (y & 1) + 1], F8 ? qs[b][1] : a.scale_log2, -me[1]);
+          const float x0 = fmaf(s[y >> 1][b][2 * (y & 1)], factor(b, 0), -me[0]);
+          const float x1 = fmaf(s[y >> 1][b][2 * (y & 1) + 1], factor(b, 1), -me[1]);
           const float p0f = ex2(x0), p1f = ex2(x1);
           l[b][0] += p0f;
           l[b][1] += p1f;
@@ -493,34 +537,31 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
           } else {
             // A's rows rw and rw + 8 of a tile are neighbouring columns of V: of this lane's
             // 16 (8) neighbouring codes of keys 2 j, 2 j + 1, 8 + 2 j, 9 + 2 j, paired key by key
+            uint32_t x[4][4];
 #pragma unroll
-            for (int h = 0; h < (D + 127) / 128; ++h) {
-              uint32_t x[4][4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z) {
-                const int key = 16 * y + 8 * (z >> 1) + 2 * j + (z & 1);
-                if constexpr (D == 64) {
-                  const uint2 u = lds64(sv + key * 64 + (((rw >> 1) ^ ((key >> 1) & 3)) << 4) + (rw & 1) * 8);
-                  x[z][0] = u.x; x[z][1] = u.y;
-                } else {
-                  const uint4 u = lds128(sv + h * (kChunk * 128) + key * 128 + ((rw ^ (key & 7)) << 4));
-                  x[z][0] = u.x; x[z][1] = u.y; x[z][2] = u.z; x[z][3] = u.w;
-                }
+            for (int z = 0; z < 4; ++z) {
+              const int key = 16 * y + 8 * (z >> 1) + 2 * j + (z & 1);
+              if constexpr (D == 64) {
+                const uint2 u = lds64(sv + key * 64 + (((rw >> 1) ^ ((key >> 1) & 3)) << 4) + (rw & 1) * 8);
+                x[z][0] = u.x; x[z][1] = u.y;
+              } else {
+                const uint4 u = lds128(sv + key * 128 + ((rw ^ (key & 7)) << 4));
+                x[z][0] = u.x; x[z][1] = u.y; x[z][2] = u.z; x[z][3] = u.w;
               }
-#pragma unroll
-              for (int w4 = 0; w4 < (D == 64 ? 2 : 4); ++w4)
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  // bytes (k, k') of codes 0, 1 (c = 0) or 2, 3 of the word
-                  uint32_t g[4];
-                  e4m3x4_to_f16(__byte_perm(x[0][w4], x[1][w4], c ? 0x7362 : 0x5140), g[0], g[1]);
-                  e4m3x4_to_f16(__byte_perm(x[2][w4], x[3][w4], c ? 0x7362 : 0x5140), g[2], g[3]);
-                  if constexpr (TAIL) { g[0] &= vm[0]; g[1] &= vm[0]; g[2] &= vm[1]; g[3] &= vm[1]; }
-#pragma unroll
-                  for (int b = 0; b < NB; ++b)
-                    mma16<true>(o[h * 8 + w4 * 2 + c][b], g[0], g[1], g[2], g[3], pb[y][b][0], pb[y][b][1]);
-                }
             }
+#pragma unroll
+            for (int w4 = 0; w4 < (D == 64 ? 2 : 4); ++w4)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                // bytes (k, k') of codes 0, 1 (c = 0) or 2, 3 of the word
+                uint32_t g[4];
+                e4m3x4_to_f16(__byte_perm(x[0][w4], x[1][w4], c ? 0x7362 : 0x5140), g[0], g[1]);
+                e4m3x4_to_f16(__byte_perm(x[2][w4], x[3][w4], c ? 0x7362 : 0x5140), g[2], g[3]);
+                if constexpr (TAIL) { g[0] &= vm[0]; g[1] &= vm[0]; g[2] &= vm[1]; g[3] &= vm[1]; }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+                  mma16<true>(o[w4 * 2 + c][b], g[0], g[1], g[2], g[3], pb[y][b][0], pb[y][b][1]);
+              }
           }
         }
       };
@@ -560,7 +601,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
 #pragma unroll
       for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 8 * NB + r) * 2]);
 #pragma unroll
-      for (int w = 0; w < NW; ++w) {
+      for (int w = 0; w < NW; w += PW) {
         const float mw = ml[(w * 8 * NB + r) * 2];
         L += mw == -CUDART_INF_F ? 0.f : ml[(w * 8 * NB + r) * 2 + 1] * ex2(mw - M);
       }
@@ -584,7 +625,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         fac[e] = (m[b][e] == -CUDART_INF_F ? 0.f : ex2(m[b][e] - M)) * (F8 ? 0.0078125f : 1.f);  // 2^-kPShift
       }
 #pragma unroll
-      for (int rd = 0; rd < D / Cfg::kCols; ++rd) {
+      for (int rd = 0; rd < DW / Cfg::kCols; ++rd) {
         if (b || rd) __syncthreads();
         // e4m3: a lane has columns [16 rw, 16 rw + 16) of 128 (8 of 64), half of which, W, go
         // in a round, kept together
@@ -604,15 +645,15 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
           }
         __syncthreads();
         const int rows = min(8, nrows - 8 * b);
-        for (int x = threadIdx.x; x < rows * (Cfg::kCols / 4); x += Cfg::kThreads) {
-          const int r = x / (Cfg::kCols / 4), c = 4 * (x % (Cfg::kCols / 4));
+        for (int x = threadIdx.x; x < rows * (PW * Cfg::kCols / 4); x += Cfg::kThreads) {
+          const int r = x / (PW * Cfg::kCols / 4), hs = x / (Cfg::kCols / 4) % PW, c = 4 * (x % (Cfg::kCols / 4));
           float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int w = 0; w < NW; ++w) {
-            const float4 u = *reinterpret_cast<const float4*>(&sum[w * Cfg::kSumFloats + r * Cfg::kPitch + c]);
+          for (int w = 0; w < NL; ++w) {
+            const float4 u = *reinterpret_cast<const float4*>(&sum[(w * PW + hs) * Cfg::kSumFloats + r * Cfg::kPitch + c]);
             t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
           }
-          const int col = F8 ? (rd >> 1) * 128 + (c / W) * 2 * W + (rd & 1) * W + c % W : rd * Cfg::kCols + c;
+          const int col = hs * DW + (F8 ? (c / W) * 2 * W + rd * W + c % W : rd * Cfg::kCols + c);
           if (part) {
             *reinterpret_cast<float4*>(part + 2 * kDecSlotRows + (8 * b + r) * D + col) = t;
           } else {
@@ -676,19 +717,20 @@ __device__ __forceinline__ void store_row(const MergeArgs& a, int t, int h, int 
 
 // Joins of the few-rows kernel: block (x, y) takes rows y, y + 4, ... of split block x,
 // its 8 warps every eighth slot each (one long sequence has as many slots as a K/V
-// head's share of the CTAs). Bound by latency: the entry, then the slots, then the sum.
+// head's share of the CTAs). Bound by latency: the plan's entry (which the attention
+// kernel does not change: fetched before waiting for that), then the slots, then the sum.
 constexpr int kMergeY = 4;
 template <int D>
 __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) {
   constexpr int V = D / 32;  // columns of a lane
   __shared__ float s_o[8][D];
   __shared__ float s_m[8], s_l[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int32_t* M = a.plan + kOffDecMerge + blockIdx.x * kMergeWords;
-  const int n = a.plan[PH_NDECM], cnt = M[MG_N], rows = M[MG_NROWS];
-  if (int(blockIdx.x) >= n) return;
+  const int n = a.plan[PH_NDECM], cnt = M[MG_N], rows = M[MG_NROWS], row0 = M[MG_ROW0], q0 = M[MG_Q0], hkv = M[MG_HKV];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(kDecSlotRows, D);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (int(blockIdx.x) >= n) return;
   for (int r = blockIdx.y; r < rows; r += kMergeY) {
     float acc[V], m = -CUDART_INF_F, l = 0.f;
 #pragma unroll
@@ -712,8 +754,8 @@ __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) 
         for (int v = 0; v < V; ++v) ov[v] = s_o[w][lane * V + v];
         join(m, l, acc, s_m[w], s_l[w], ov);
       }
-      const int nr = M[MG_ROW0] + r;
-      store_row(a, M[MG_Q0] + nr / a.G, M[MG_HKV] * a.G + nr % a.G, lane, m, l, acc);
+      const int nr = row0 + r;
+      store_row(a, q0 + nr / a.G, hkv * a.G + nr % a.G, lane, m, l, acc);
     }
     __syncthreads();
   }
@@ -774,8 +816,10 @@ int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArg
   const int rows = w[PH_DEC_ROWS];
   if (rows == 8) return launch_dec_t<D, FMT, 1>(w, c, a, s);
   if (rows == 16) return launch_dec_t<D, FMT, 2>(w, c, a, s);
-  if constexpr (dec_block_rows(D, FMT) == 32)
+  if constexpr (dec_block_rows(FMT) == 32) {
+    if (rows == 24) return launch_dec_t<D, FMT, 3>(w, c, a, s);
     if (rows == 32) return launch_dec_t<D, FMT, 4>(w, c, a, s);
+  }
   return fail(BD_ERR_PLAN, "few-rows blocks of %d rows at head dim %d", rows, D);
 }
 

@@ -328,15 +328,14 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
     if (pg > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
   }
   // Sequences of up to 32 (new row, head) pairs of a K/V head go to the few-rows kernel, in
-  // blocks of one size (a tile of 32 rows in use costs what one of 128 does). e4m3: two
-  // blocks of 16 (16 sequences of 20000 rows, 32 pairs, d 128: 230 us, as tiles 346); at
-  // head dim 256, where two blocks read twice what a tile does, up to 16 (605 us as
-  // tiles, 768 as two blocks).
-  const int most = D->d == 256 ? 16 : 32;
+  // blocks of one size (a tile of 32 rows in use costs what one of 128 does). 16 sequences
+  // of 20000 rows, 32 pairs, d 128: bf16 257 us, as tiles 306; e4m3, two blocks of 16, 230,
+  // as tiles 346.
+  const int most = kDecMaxRows;
   int32_t widest = 1;
   for (int32_t b = 0; b < D->B; ++b)
     if (int64_t(D->q_len[b]) * G <= most) widest = std::max(widest, D->q_len[b] * G);
-  X->dec_rows = std::min(widest <= 8 ? 8 : widest <= 16 ? 16 : 32, dec_block_rows(D->d, D->fmt));
+  X->dec_rows = std::min((widest + 7) / 8 * 8, dec_block_rows(D->fmt));
   // every row block of a (sequence, K/V head): keys up to what its last row sees
   std::vector<Item> dec, tile;
   int64_t nitems = 0;

@@ -15,10 +15,10 @@ constexpr int32_t kPagedVersion = 1;
 // (tiles) or two (few rows: one adds up a block while the other's loads go on) on each.
 constexpr int kPagedSms = 152;
 constexpr int kDecCtas = 2 * kPagedSms, kTileCtas = kPagedSms;
-// A few-rows block has 8, 16 or (where registers hold it: bf16, head dims 64 and 128) 32
-// (new row, query head) pairs of one K/V head: the least that holds every sequence of
-// the plan that goes there.
-constexpr int dec_block_rows(int d, int fmt) { return d <= 128 && fmt == BD_CACHE_BF16 ? 32 : 16; }
+// A few-rows block has 8, 16 or (bf16: e4m3 lacks the registers) 24 or 32 (new row, query head)
+// pairs of one K/V head: the least that holds every sequence of the plan that goes there.
+constexpr int kDecMaxRows = 32;
+constexpr int dec_block_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 16; }
 constexpr int kDecSlotRows = 32;
 constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cut
 // Tiles (of 128 / G new rows x G heads) of one K/V head that share a key tile in the
