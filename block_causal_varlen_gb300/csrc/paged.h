@@ -33,8 +33,9 @@ struct MergeArgs {
   int32_t G;
 };
 
-// Joins the split blocks of the few-rows (tile = false) or the tile kernel.
-int32_t launch_merge(const MergeArgs& a, int d, bool tile, cudaStream_t stream);
+// Joins the split blocks of the few-rows (tile = false; wide: some in many parts) or the
+// tile kernel.
+int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream_t stream);
 
 struct AttnArgs {
   const int32_t* plan;

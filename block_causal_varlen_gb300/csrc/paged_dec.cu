@@ -679,18 +679,6 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   }
 }
 
-// m, l and D / 32 columns of O of one row: state (a) joined with a slot's (b), each
-// relative to its own m.
-template <int V>
-__device__ __forceinline__ void join(float& m, float& l, float (&o)[V], float mi, float li, const float (&oi)[V]) {
-  if (mi == -CUDART_INF_F) return;
-  const float mn = fmaxf(m, mi), f0 = m == -CUDART_INF_F ? 0.f : ex2(m - mn), f1 = ex2(mi - mn);
-  l = l * f0 + li * f1;
-#pragma unroll
-  for (int v = 0; v < V; ++v) o[v] = o[v] * f0 + oi[v] * f1;
-  m = mn;
-}
-
 template <int V>
 __device__ __forceinline__ void load_cols(const float* p, float (&o)[V]) {
   if constexpr (V == 2) {
@@ -705,89 +693,156 @@ __device__ __forceinline__ void load_cols(const float* p, float (&o)[V]) {
   }
 }
 
+// A row's result from its total l relative to m and this lane's D / 32 columns of O.
 template <int V>
 __device__ __forceinline__ void store_row(const MergeArgs& a, int t, int h, int lane, float m, float l, const float (&acc)[V]) {
-  const float inv = m == -CUDART_INF_F ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   __nv_bfloat16* o = a.o + int64_t(t) * a.o_sr + int64_t(h) * a.o_sh + lane * V;
 #pragma unroll
   for (int v = 0; v < V; v += 2) *reinterpret_cast<uint32_t*>(o + v) = pack_bf16(acc[v] * inv, acc[v + 1] * inv);
-  if (lane == 0 && a.lse)
-    a.lse[int64_t(h) * a.l_sh + t] = m == -CUDART_INF_F ? -CUDART_INF_F : (m + lg2(l)) * 0.69314718055994531f;
+  if (lane == 0 && a.lse) a.lse[int64_t(h) * a.l_sh + t] = l == 0.f ? -CUDART_INF_F : (m + lg2(l)) * 0.69314718055994531f;
 }
 
-// Joins of the few-rows kernel: block (x, y) takes rows y, y + 4, ... of split block x,
-// its 8 warps every eighth slot each (one long sequence has as many slots as a K/V
-// head's share of the CTAs). Bound by latency: the plan's entry (which the attention
-// kernel does not change: fetched before waiting for that), then the slots, then the sum.
-constexpr int kMergeY = 4;
+// One row of `cnt` slots by one warp: the maximum and the weights 2^(m_i - M), then the
+// sums, whose loads do not depend on one another. P: the row's m in the first slot; l is
+// ROWS floats on, O at `o` floats (this lane's columns). Slots first, first + by, ...
+template <int D, int ROWS>
+__device__ __forceinline__ void join_row(const float* P, int64_t o, int cnt, int first, int by, int lane, float* M, float* L,
+                                         float (&acc)[D / 32]) {
+  constexpr int V = D / 32;
+  constexpr int64_t SL = slot_floats(ROWS, D);
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  float mx = -CUDART_INF_F, l = 0.f;
+  for (int i0 = first; i0 < cnt; i0 += 32 * by) {  // 32 slots at a time, lane by lane
+    const int i = i0 + lane * by, n = min(32, (cnt - i0 + by - 1) / by);
+    const float mi = i < cnt ? __ldcg(P + i * SL) : -CUDART_INF_F, li = i < cnt ? __ldcg(P + i * SL + ROWS) : 0.f;
+    float ov[4][V];  // the first slots' O come along with their m and l
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) load_cols(P + o + (i0 + k * by) * SL, ov[k]);
+    float mn = mi;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+    mn = fmaxf(mn, mx);
+    const float f = mx == -CUDART_INF_F ? 0.f : ex2(mx - mn), w = mi == -CUDART_INF_F ? 0.f : ex2(mi - mn);
+    float ls = mi == -CUDART_INF_F ? 0.f : li * w;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+    l = l * f + ls;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] *= f;
+    mx = mn;
+    auto add = [&](int k, const float (&x)[V]) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += wk == 0.f ? 0.f : x[v] * wk;
+    };
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (k < n) add(k, ov[k]);
+#pragma unroll 4
+    for (int k = 4; k < n; ++k) {
+      float t[V];
+      load_cols(P + o + (i0 + k * by) * SL, t);
+      add(k, t);
+    }
+  }
+  *M = mx;
+  *L = l;
+}
+
+// Joins of the few-rows kernel, a warp per row. Bound by latency: the plan's entry (which
+// the attention kernel does not change: fetched before waiting for that), then the
+// slots. With no shared memory and few registers, a CTA or two find room beside the
+// attention's.
 template <int D>
 __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) {
-  constexpr int V = D / 32;  // columns of a lane
+  constexpr int ROWS = kDecSlotRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = a.plan[PH_NDECM], live = a.plan[PH_DEC_LIVE];
+  bool waited = false;
+  for (int x = blockIdx.x * 8 + warp; x < n * live; x += gridDim.x * 8) {
+    const int32_t* M = a.plan + kOffDecMerge + (x / live) * kMergeWords;
+    const int r = x % live, cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + r;
+    const int t = M[MG_Q0] + nr / a.G, h = M[MG_HKV] * a.G + nr % a.G;
+    if (r >= M[MG_NROWS]) continue;
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
+    float acc[D / 32], m, l;
+    join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + r * D + lane * (D / 32), cnt, 0, 1,
+                      lane, &m, &l, acc);
+    store_row(a, t, h, lane, m, l, acc);
+  }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The same where blocks have many slots (few long sequences, cut over every SM): a CTA
+// per row, its warps every eighth slot each.
+template <int D>
+__global__ void __launch_bounds__(256) bd_paged_wide_merge_kernel(const MergeArgs a) {
+  constexpr int V = D / 32, ROWS = kDecSlotRows;
   __shared__ float s_o[8][D];
   __shared__ float s_m[8], s_l[8];
-  const int32_t* M = a.plan + kOffDecMerge + blockIdx.x * kMergeWords;
-  const int n = a.plan[PH_NDECM], cnt = M[MG_N], rows = M[MG_NROWS], row0 = M[MG_ROW0], q0 = M[MG_Q0], hkv = M[MG_HKV];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(kDecSlotRows, D);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (int(blockIdx.x) >= n) return;
-  for (int r = blockIdx.y; r < rows; r += kMergeY) {
-    float acc[V], m = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 4
-    for (int i = warp; i < cnt; i += 8) {
-      const float* P = base + int64_t(i) * slot_floats(kDecSlotRows, D);
-      const float mi = __ldcg(P + r), li = __ldcg(P + kDecSlotRows + r);
-      float ov[V];
-      load_cols(P + 2 * kDecSlotRows + r * D + lane * V, ov);
-      join(m, l, acc, mi, li, ov);
-    }
+  const int n = a.plan[PH_NDECM], live = a.plan[PH_DEC_LIVE];
+  bool waited = false;
+  for (int x = blockIdx.x; x < n * live; x += gridDim.x) {
+    const int32_t* M = a.plan + kOffDecMerge + (x / live) * kMergeWords;
+    const int r = x % live, cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + r;
+    const int t = M[MG_Q0] + nr / a.G, h = M[MG_HKV] * a.G + nr % a.G;
+    if (r >= M[MG_NROWS]) continue;
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
+    float acc[V], m, l;
+    join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + r * D + lane * V, cnt, warp, 8, lane,
+                      &m, &l, acc);
 #pragma unroll
     for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = acc[v];
     if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
     __syncthreads();
     if (warp == 0) {
-      for (int w = 1; w < min(cnt, 8); ++w) {
-        float ov[V];
+      float mm = -CUDART_INF_F, ll = 0.f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) ov[v] = s_o[w][lane * V + v];
-        join(m, l, acc, s_m[w], s_l[w], ov);
+      for (int w = 0; w < 8; ++w) mm = fmaxf(mm, s_m[w]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        if (s_m[w] == -CUDART_INF_F) continue;
+        const float f = ex2(s_m[w] - mm);
+        ll += s_l[w] * f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += s_o[w][lane * V + v] * f;
       }
-      const int nr = row0 + r;
-      store_row(a, q0 + nr / a.G, hkv * a.G + nr % a.G, lane, m, l, acc);
+      store_row(a, t, h, lane, mm, ll, acc);
     }
     __syncthreads();
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Joins of the tile kernel: a warp per row, rows of all split blocks over the grid.
 template <int D>
 __global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArgs a) {
   constexpr int V = D / 32, ROWS = tile_slot_rows(D);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int n = a.plan[PH_NTILEM], G = a.G, per = 128 / G * G;  // rows in use of each 128 of a slot
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  bool waited = false;
   for (int x = blockIdx.x * 8 + warp; x < n * ROWS; x += gridDim.x * 8) {
     const int r = x % ROWS, br = (r >> 7) * per + (r & 127);  // row of the block
     const int32_t* M = a.plan + kOffTileMerge + (x / ROWS) * kMergeWords;
+    const int cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + br;
+    const int t = M[MG_Q0] + nr / G, h = M[MG_HKV] * G + nr % G;
     if ((r & 127) >= per || br >= M[MG_NROWS]) continue;
-    const int cnt = M[MG_N];
-    const float* base = a.part + int64_t(M[MG_SLOT0]) * slot_floats(ROWS, D);
-    float acc[V], m = -CUDART_INF_F, l = 0.f;
-#pragma unroll
-    for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < cnt; ++i) {
-      const float* P = base + int64_t(i) * slot_floats(ROWS, D);
-      const float mi = __ldcg(P + r), li = __ldcg(P + ROWS + r);
-      float ov[V];
-      load_cols(P + 2 * ROWS + int64_t(r) * D + lane * V, ov);
-      join(m, l, acc, mi, li, ov);
-    }
-    const int nr = M[MG_ROW0] + br;
-    store_row(a, M[MG_Q0] + nr / G, M[MG_HKV] * G + nr % G, lane, m, l, acc);
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
+    float acc[V], m, l;
+    join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + int64_t(r) * D + lane * V, cnt, 0, 1,
+                      lane, &m, &l, acc);
+    store_row(a, t, h, lane, m, l, acc);
   }
+  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, int FMT, int NB>
@@ -839,14 +894,13 @@ cudaError_t launch_join(void (*kernel)(MergeArgs), dim3 grid, const MergeArgs& a
 
 }  // namespace
 
-int32_t launch_merge(const MergeArgs& a, int d, bool tile, cudaStream_t s) {
-  cudaError_t e;
-  if (tile)
-    e = launch_join(d == 64 ? bd_paged_tile_merge_kernel<64> : d == 128 ? bd_paged_tile_merge_kernel<128> : bd_paged_tile_merge_kernel<256>,
-                    dim3(kPagedSms * 8), a, s);
-  else
-    e = launch_join(d == 64 ? bd_paged_merge_kernel<64> : d == 128 ? bd_paged_merge_kernel<128> : bd_paged_merge_kernel<256>,
-                    dim3(kDecSlots / 2, kMergeY), a, s);
+int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream_t s) {
+  typedef void (*Kernel)(MergeArgs);
+  auto pick = [d](Kernel k64, Kernel k128, Kernel k256) { return d == 64 ? k64 : d == 128 ? k128 : k256; };
+  const Kernel k = tile   ? pick(bd_paged_tile_merge_kernel<64>, bd_paged_tile_merge_kernel<128>, bd_paged_tile_merge_kernel<256>)
+                   : wide ? pick(bd_paged_wide_merge_kernel<64>, bd_paged_wide_merge_kernel<128>, bd_paged_wide_merge_kernel<256>)
+                          : pick(bd_paged_merge_kernel<64>, bd_paged_merge_kernel<128>, bd_paged_merge_kernel<256>);
+  const cudaError_t e = launch_join(k, dim3(kPagedSms * (tile ? 8 : wide ? 4 : 2)), a, s);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "paged join launch");
 }
 
@@ -919,13 +973,13 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   MergeArgs m = {a.plan, a.part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh, a.G};
   if (w[PH_NDEC]) {
     if ((st = launch_dec(w, a, cache, s))) return st;
-    if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, s))) return st;
+    if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, w[PH_DECM_WIDE] != 0, s))) return st;
   }
   if (w[PH_NTILE]) {
     a.part += dec_part_bytes(w) / 4;
     m.part = a.part;
     if ((st = launch_tile(w, a, q, cache, s))) return st;
-    if (w[PH_NTILEM] && (st = launch_merge(m, w[PH_D], true, s))) return st;
+    if (w[PH_NTILEM] && (st = launch_merge(m, w[PH_D], true, false, s))) return st;
   }
   return ok();
 }

@@ -311,7 +311,7 @@ int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npage
 struct Built {
   int64_t T, kv, npages;
   Lists dec, tile;
-  int32_t dec_rows;
+  int32_t dec_rows, dec_live = 0;
 };
 
 int32_t prepare(const bd_paged_desc* D, Built* X) {
@@ -349,6 +349,7 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
       for (int32_t r0 = 0; r0 < rows; r0 += step) {
         const int32_t r1 = std::min(rows, r0 + step);
         const int64_t seen = D->causal ? int64_t(n) - q + (r1 - 1) / G + 1 : n;
+        if (few) X->dec_live = std::max(X->dec_live, r1 - r0);
         (few ? dec : tile).push_back({b, g, r0, r1 - r0, int32_t(std::max<int64_t>(0, seen))});
       }
   }
@@ -444,6 +445,9 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
     at += int64_t(L.pieces.size());
   };
   w[PH_DEC_ROWS] = X.dec_rows;
+  w[PH_DEC_LIVE] = X.dec_live;
+  for (size_t i = 0; i < X.dec.merges.size(); i += kMergeWords)
+    if (X.dec.merges[i + MG_N] > kWideJoin) w[PH_DECM_WIDE] = 1;
   put(X.dec, PH_OFF_DEC, PH_NDEC, PH_NDECM, kOffDecRec, kOffDecMerge);
   put(X.tile, PH_OFF_TILE, PH_NTILE, PH_NTILEM, kOffTileRec, kOffTileMerge);
   return ok();
@@ -456,7 +460,7 @@ extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
   if (st) return st;
   // what a captured launch holds of the plan (FNV-1a over the words)
   const int32_t fields[] = {w[PH_H], w[PH_HKV], w[PH_D], w[PH_PAGE], w[PH_NUM_PAGES], w[PH_FMT], w[PH_CAUSAL],
-                            w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0, w[PH_NDECM] > 0,
+                            w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0, w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0,
                             w[PH_NTILE] > 0, w[PH_NTILEM] > 0};
   uint64_t h = 1469598103934665603ull;
   for (int32_t f : fields)

@@ -20,6 +20,7 @@ constexpr int kDecCtas = 2 * kPagedSms, kTileCtas = kPagedSms;
 constexpr int kDecMaxRows = 32;
 constexpr int dec_block_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 16; }
 constexpr int kDecSlotRows = 32;
+constexpr int kWideJoin = 16;  // parts of a block from which on its rows are joined by a CTA each
 constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cut
 // Tiles (of 128 / G new rows x G heads) of one K/V head that share a key tile in the
 // tile kernel, and the rows of its partial-result slots.
@@ -41,6 +42,8 @@ enum : int {
   PH_OFF_DEC,      // few-rows kernel: its pieces, CTA after CTA,
   PH_NDEC,         // their number,
   PH_NDECM,        // the joins of its split blocks,
+  PH_DECM_WIDE,    // whether one of them has more than kWideJoin parts,
+  PH_DEC_LIVE,     // the most rows of a block in use,
   PH_DEC_ROWS,     // and the rows of a block
   PH_OFF_TILE,     // the same for the tile kernel
   PH_NTILE,

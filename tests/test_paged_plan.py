@@ -12,7 +12,7 @@ from oracle import paged as op  # noqa: E402
 
 # header words and record layouts (csrc/paged_plan.h)
 WORDS = ("MAGIC VERSION WORDS B H HKV D G PAGE PAGE_SHIFT NUM_PAGES FMT CAUSAL T KV_TOTAL WRITE_OK SCALE OFF_TOK "
-         "OFF_PAGES NPAGES OFF_PGROW OFF_PGCNT OFF_DEC NDEC NDECM DEC_ROWS OFF_TILE NTILE NTILEM").split()
+         "OFF_PAGES NPAGES OFF_PGROW OFF_PGCNT OFF_DEC NDEC NDECM DECM_WIDE DEC_LIVE DEC_ROWS OFF_TILE NTILE NTILEM").split()
 PIECE = ("Q0", "QLEN", "KVLEN", "PAGES", "HKV", "ROW0", "NROWS", "K0", "K1", "SLOT", "T0", "R1")
 MERGE = ("SLOT0", "N", "Q0", "HKV", "ROW0", "NROWS", "R0", "R1")
 CTAS = {"DEC": 304, "TILE": 152}
