@@ -963,6 +963,10 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   a.lse = lse ? lse->ptr : nullptr;
   a.l_sh = lse ? lse->stride_head : 0;
   a.part = static_cast<float*>(workspace);
+  const int64_t es = cache->fmt == BD_CACHE_BF16 ? 2 : 1;
+  a.kc = static_cast<const uint8_t*>(cache->k.ptr); a.vc = static_cast<const uint8_t*>(cache->v.ptr);
+  a.k_sp = cache->k.stride_b * es; a.k_sr = cache->k.stride_row * es; a.k_sh = cache->k.stride_head * es;
+  a.v_sp = cache->v.stride_b * es; a.v_sr = cache->v.stride_row * es; a.v_sh = cache->v.stride_head * es;
   a.k_exp = cache->k_exp; a.v_exp = cache->v_exp;
   a.e_sp = cache->exp_stride_page; a.e_sr = cache->exp_stride_row; a.e_sh = cache->exp_stride_head;
   float scale;

@@ -259,17 +259,28 @@ void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const st
       least = cost;
       best.swap(parts);
     };
-    for (int k = 1; k <= 4 && least > share; ++k) {
+    // (within 1.5% of an even share nothing is gained)
+    const int64_t fine = share + share / 64;
+    for (int k = 1; k <= 4 && least > fine; ++k) {
       const int64_t t = cut_longest(items, kTile, kOver, std::max<int64_t>(1, share / k), &parts);
       if (t < 0) break;
       better(t);
     }
-    // the least t that can be filled, within 2%
-    for (int64_t t = share + 1; t + 3 < least; t += 1 + t / 50)
-      if (fill(items, kTile, kOver, t, &parts)) {
-        better(t);
-        break;
-      }
+    // the least t that can be filled, between one that cannot (or an even share) and one
+    // that can, to 0.5%
+    int64_t lo = share, step = 1 + share / 200, hi = lo + step;
+    if (least <= fine) hi = least;
+    while (hi + 3 < least && !fill(items, kTile, kOver, hi, &parts)) {
+      lo = hi;
+      step *= 2;
+      hi += step;
+    }
+    while (hi + 3 < least && hi - lo > 1 + share / 200) {
+      const int64_t mid = (lo + hi) / 2;
+      if (fill(items, kTile, kOver, mid, &parts)) hi = mid;
+      else lo = mid;
+    }
+    if (hi + 3 < least && fill(items, kTile, kOver, hi, &parts)) better(hi);
   }
   write_lists(D, items, best, q0, page_off, kTile, kTileCtas, L);
 }
@@ -310,15 +321,19 @@ int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npage
 
 struct Built {
   int64_t T, kv, npages;
-  Lists dec, tile;
+  std::vector<Item> dec_items, tile_items;
+  std::vector<int32_t> q0, page_off;
   int32_t dec_rows, dec_live = 0;
 };
 
+// Validates a description and lists its blocks.
 int32_t prepare(const bd_paged_desc* D, Built* X) {
   int32_t st = validate(D, &X->T, &X->kv, &X->npages);
   if (st) return st;
   const int G = D->H / D->Hkv;
-  std::vector<int32_t> q0(D->B), page_off(D->B);
+  std::vector<int32_t>&q0 = X->q0, &page_off = X->page_off;
+  q0.resize(D->B);
+  page_off.resize(D->B);
   int64_t t = 0, pg = kOffLists + X->T;
   for (int32_t b = 0; b < D->B; ++b) {
     q0[b] = int32_t(t);
@@ -337,7 +352,7 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
     if (int64_t(D->q_len[b]) * G <= most) widest = std::max(widest, D->q_len[b] * G);
   X->dec_rows = std::min((widest + 7) / 8 * 8, dec_block_rows(D->fmt));
   // every row block of a (sequence, K/V head): keys up to what its last row sees
-  std::vector<Item> dec, tile;
+  std::vector<Item>&dec = X->dec_items, &tile = X->tile_items;
   int64_t nitems = 0;
   for (int32_t b = 0; b < D->B; ++b) nitems += (int64_t(D->q_len[b]) * G + 7) / 8 * D->Hkv;
   if (nitems > (1 << 26)) return fail(BD_ERR_CAPACITY, "plan of more than 2^26 row blocks");
@@ -353,16 +368,19 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
         (few ? dec : tile).push_back({b, g, r0, r1 - r0, int32_t(std::max<int64_t>(0, seen))});
       }
   }
-  dec_lists(*D, dec, q0, page_off, &X->dec);
-  tile_lists(*D, tile, q0, page_off, &X->tile);
   return BD_OK;
 }
 
 // The pieces are read 16 bytes at a time: each list starts on a multiple of 4 words.
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
-int64_t total_words(const Built& X) {
-  return up4(kOffLists + X.T + 3 * X.npages) + int64_t(X.dec.pieces.size()) + int64_t(X.tile.pieces.size());
+// Words that hold the plan however its blocks are cut: a cut block's parts but one come
+// out of the slots.
+int64_t most_words(const Built& X) {
+  int64_t w = up4(kOffLists + X.T + 3 * X.npages);
+  if (!X.dec_items.empty()) w += (int64_t(X.dec_items.size()) + kDecSlots) * kPieceWords;
+  if (!X.tile_items.empty()) w += (int64_t(X.tile_items.size()) + kTilePartSlots) * kPieceWords;
+  return w;
 }
 
 }  // namespace
@@ -376,7 +394,7 @@ extern "C" int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes)
   Built X;
   int32_t st = prepare(desc, &X);
   if (st) return st;
-  const int64_t w = total_words(X);
+  const int64_t w = most_words(X);
   if (w > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
   *bytes = size_t(w) * 4;
   return ok();
@@ -387,13 +405,16 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
   Built X;
   int32_t st = prepare(desc, &X);
   if (st) return st;
-  const int64_t words = total_words(X);
-  if (words > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
-  if (blob_bytes < size_t(words) * 4)
-    return fail(BD_ERR_CAPACITY, "plan blob of %zu bytes, %lld needed", blob_bytes, (long long)words * 4);
+  if (most_words(X) > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
+  if (blob_bytes < size_t(most_words(X)) * 4)
+    return fail(BD_ERR_CAPACITY, "plan blob of %zu bytes, %lld needed", blob_bytes, (long long)most_words(X) * 4);
+  const bd_paged_desc& D = *desc;
+  Lists dec, tile;
+  dec_lists(D, X.dec_items, X.q0, X.page_off, &dec);
+  tile_lists(D, X.tile_items, X.q0, X.page_off, &tile);
+  const int64_t words = up4(kOffLists + X.T + 3 * X.npages) + int64_t(dec.pieces.size()) + int64_t(tile.pieces.size());
   int32_t* w = static_cast<int32_t*>(blob);
   std::memset(w, 0, size_t(words) * 4);
-  const bd_paged_desc& D = *desc;
   const int32_t P = D.page_size;
   w[PH_MAGIC] = kPagedMagic; w[PH_VERSION] = kPagedVersion; w[PH_WORDS] = int32_t(words);
   w[PH_B] = D.B; w[PH_H] = D.H; w[PH_HKV] = D.Hkv; w[PH_D] = D.d; w[PH_G] = D.H / D.Hkv;
@@ -446,10 +467,10 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
   };
   w[PH_DEC_ROWS] = X.dec_rows;
   w[PH_DEC_LIVE] = X.dec_live;
-  for (size_t i = 0; i < X.dec.merges.size(); i += kMergeWords)
-    if (X.dec.merges[i + MG_N] > kWideJoin) w[PH_DECM_WIDE] = 1;
-  put(X.dec, PH_OFF_DEC, PH_NDEC, PH_NDECM, kOffDecRec, kOffDecMerge);
-  put(X.tile, PH_OFF_TILE, PH_NTILE, PH_NTILEM, kOffTileRec, kOffTileMerge);
+  for (size_t i = 0; i < dec.merges.size(); i += kMergeWords)
+    if (dec.merges[i + MG_N] > kWideJoin) w[PH_DECM_WIDE] = 1;
+  put(dec, PH_OFF_DEC, PH_NDEC, PH_NDECM, kOffDecRec, kOffDecMerge);
+  put(tile, PH_OFF_TILE, PH_NTILE, PH_NTILEM, kOffTileRec, kOffTileMerge);
   return ok();
 }
 

@@ -63,7 +63,7 @@ struct TileCfg {
   static constexpr int kOCol = 256;               // first O column in TMEM
   static constexpr int kThreads = kF8 ? 512 : 384;
   // registers after setmaxnreg: warps 0-3, the softmax warps, the converting warps
-  static constexpr int kRegsCtl = kF8 ? 56 : 72, kRegsSoftmax = kF8 ? 200 : 216, kRegsConv = 56;
+  static constexpr int kRegsCtl = kF8 ? 40 : 72, kRegsSoftmax = kF8 ? 200 : 216, kRegsConv = 72;
   static constexpr int kRegsLaunch = kF8 ? 128 : 168;
   static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kF8 ? 128 * kRegsConv : 0) <= kRegsLaunch * kThreads,
                 "register split exceeds the launch's registers");
@@ -130,10 +130,15 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
   const int32_t* pieces = plan + plan[PH_OFF_TILE];
   const int G = a.G, causal = a.causal, pshift = a.page_shift;
   const int TPS = 128 / G;   // new rows of a slot's tile
-  for (int i = threadIdx.x; i < min(p1 - p0, Cfg::kPre) * kPieceWords; i += Cfg::kThreads)
+  // the record has the first piece; a CTA with more fetches them now
+  if (threadIdx.x < kPieceWords) pre[threadIdx.x] = rec[RC_PIECE + threadIdx.x];
+  for (int i = kPieceWords + threadIdx.x; i < min(p1 - p0, Cfg::kPre) * kPieceWords; i += Cfg::kThreads)
     pre[i] = pieces[p0 * kPieceWords + i];
 
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
     mbar_init(bar(T_QFULL), 1);
     mbar_init(bar(T_QEMPTY), Cfg::kStageInQ ? 4 * NS : NS);  // softmax warps, or MMA threads
     for (int s = 0; s < NST; ++s) {

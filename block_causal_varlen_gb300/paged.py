@@ -98,10 +98,11 @@ class PagedPlan:
         desc = bd_paged_desc(self.B, H, Hkv, d, page_size, num_pages, fmt, int(self.causal), q.ctypes.data_as(_P32),
                              kv.ctypes.data_as(_P32), flat.ctypes.data_as(_P32), offs.ctypes.data_as(_P32))
         self.nbytes = bd_paged_plan_bytes(desc)
-        self._raw = np.zeros(self.nbytes // 4 + 16, dtype=np.int32)
+        self._raw = np.empty(self.nbytes // 4 + 16, dtype=np.int32)
         off = (-self._raw.ctypes.data % 64) // 4
         self.host = self._raw[off:off + self.nbytes // 4]
         bd_paged_plan_build(desc, self.host.ctypes.data, self.nbytes)
+        self.host = self.host[:int(self.host[2])]       # the words in use (csrc/paged_plan.h: PH_WORDS)
         self._host_ptr = self.host.ctypes.data
         self.dev = self._dev_ptr = None
         self._index = -1
@@ -121,8 +122,8 @@ class PagedPlan:
 
     def upload(self, device="cuda", non_blocking=False, buffer=None):
         """Copy the plan blob to device memory (once per step): into memory of its own,
-        or into ``buffer``, an int32 device tensor of at least nbytes / 4 words that a
-        captured graph reads (see bd_paged_plan_key)."""
+        or into ``buffer``, an int32 device tensor that a captured graph reads (see
+        bd_paged_plan_key; nbytes / 4 words always suffice)."""
         src = torch.from_numpy(self.host)
         if buffer is not None:
             if buffer.dtype != torch.int32 or buffer.dim() != 1 or not buffer.is_contiguous() or not buffer.is_cuda:

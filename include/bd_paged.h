@@ -89,8 +89,9 @@ typedef struct {
                                   ones in [0, num_pages). Sequences may share pages.  */
 } bd_paged_desc;
 
-/* Bytes of the plan blob for `desc`, which is validated in full (lengths, head
- * counts, every page index used). Errors: BD_ERR_ARG, BD_ERR_UNSUPPORTED (head dim,
+/* Bytes that hold the plan blob for `desc`, which is validated in full (lengths, head
+ * counts, every page index used). A bound: the plan itself may be shorter (its third
+ * 32-bit word is the number of words in use, all that has to be copied to the device). Errors: BD_ERR_ARG, BD_ERR_UNSUPPORTED (head dim,
  * head ratio, page size), BD_ERR_CAPACITY (sizes past 2^31). */
 BD_API int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes);
 
