@@ -4,6 +4,8 @@
 
 #include <mutex>
 
+#include "tmap_pages.h"
+
 namespace bd {
 
 int32_t cuda_fail(cudaError_t e, const char* what) {

@@ -32,19 +32,6 @@ int32_t make_tmap_f32_reduce(CUtensorMap* map, const bd_tensor* t, int64_t B, in
 int32_t make_tmap_rows_bf16(CUtensorMap* map, const bd_tensor* t, int64_t B, int64_t C, int64_t heads, int64_t d,
                             const char* name, int box_heads, int box_rows);
 
-// Encodes a 5-D tiled TMA map over packed bf16 rows [rows, heads, d] (t's b and c
-// dimensions unused) whose box is 64 columns of box_heads heads x box_rows rows,
-// 128-byte swizzle: in shared memory row-major [row][head][64].
-int32_t make_tmap_group_bf16(CUtensorMap* map, const bd_tensor* t, int64_t heads, int64_t d, const char* name,
-                             int box_heads, int box_rows);
-
-// Encodes a 5-D tiled TMA map over a paged cache's K or V (esize 2: bf16, 1: 8-bit
-// codes): dims (128-byte piece of a head's d elements or all 64 bytes of them, row of
-// a page, piece, head, page), box = box_rows rows of every piece of one head, 128- (or
-// 64-)byte swizzle: in shared memory [piece][row][bytes].
-int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int64_t heads, int64_t d, int esize,
-                        const char* name, int box_rows, int box_pieces);
-
 // Number of SMs of the current device (cached per device).
 int32_t sm_count(int* out);
 

@@ -6,6 +6,7 @@
 
 #include "host_util.h"
 #include "paged_plan.h"
+#include "tmap_pages.h"
 
 namespace bd {
 

@@ -11,7 +11,9 @@
 #include <cmath>
 #include <cstring>
 #include <functional>
+#include <new>
 #include <queue>
+#include <stdexcept>
 #include <utility>
 #include <vector>
 
@@ -303,6 +305,8 @@ int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npage
   for (int32_t b = 0; b < D->B; ++b) {
     const int32_t q = D->q_len[b], n = D->kv_len[b];
     if (q < 0 || n < 0) return fail(BD_ERR_ARG, "sequence %d: q_len %d or kv_len %d negative", b, q, n);
+    // (kernels step up to a tile past a sequence's end)
+    if (n > INT32_MAX - 4096) return fail(BD_ERR_CAPACITY, "sequence %d: kv_len %d", b, n);
     const int32_t o0 = D->page_offsets[b], o1 = D->page_offsets[b + 1];
     if (o0 < 0 || o1 < o0) return fail(BD_ERR_ARG, "page_offsets decrease or are negative at sequence %d", b);
     const int64_t used = (int64_t(n) + D->page_size - 1) / D->page_size;
@@ -389,7 +393,19 @@ int64_t most_words(const Built& X) {
 
 using namespace bd;
 
-extern "C" int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes) {
+// No exception leaves the library: running out of host memory is an error like others.
+template <class F>
+static int32_t guarded(F&& f) {
+  try {
+    return f();
+  } catch (const std::bad_alloc&) {
+    return fail(BD_ERR_CAPACITY, "out of host memory");
+  } catch (const std::length_error&) {
+    return fail(BD_ERR_CAPACITY, "plan too large for host memory");
+  }
+}
+
+static int32_t plan_bytes(const bd_paged_desc* desc, size_t* bytes) {
   if (!bytes) return fail(BD_ERR_ARG, "bytes is NULL");
   Built X;
   int32_t st = prepare(desc, &X);
@@ -400,7 +416,7 @@ extern "C" int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes)
   return ok();
 }
 
-extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, size_t blob_bytes) {
+static int32_t plan_build(const bd_paged_desc* desc, void* blob, size_t blob_bytes) {
   if (!blob || reinterpret_cast<uintptr_t>(blob) % 16) return fail(BD_ERR_ARG, "blob NULL or not 16-byte aligned");
   Built X;
   int32_t st = prepare(desc, &X);
@@ -434,7 +450,7 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
   std::vector<Range> written;  // cache rows the new rows take, one range per page touched
   for (int32_t b = 0; b < D.B; ++b) {
     const int32_t q = D.q_len[b], n = D.kv_len[b];
-    const int32_t* pages = D.pages + D.page_offsets[b];
+    const int32_t* pages = n ? D.pages + D.page_offsets[b] : nullptr;  // (pages may be NULL when nothing is cached)
     for (int32_t j = 0; j < n; j += P) {
       w[w[PH_OFF_PAGES] + pg] = pages[j / P];
       w[w[PH_OFF_PGROW] + pg] = int32_t(kv + j);
@@ -472,6 +488,14 @@ extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, si
   put(dec, PH_OFF_DEC, PH_NDEC, PH_NDECM, kOffDecRec, kOffDecMerge);
   put(tile, PH_OFF_TILE, PH_NTILE, PH_NTILEM, kOffTileRec, kOffTileMerge);
   return ok();
+}
+
+extern "C" int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes) {
+  return guarded([&] { return plan_bytes(desc, bytes); });
+}
+
+extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, size_t blob_bytes) {
+  return guarded([&] { return plan_build(desc, blob, blob_bytes); });
 }
 
 extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {

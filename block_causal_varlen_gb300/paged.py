@@ -70,6 +70,14 @@ class PagedCache:
         self._index = k.get_device()
 
 
+def _ints(x, name):
+    """x as int32, if it is whole numbers in range."""
+    a = np.asarray(x)
+    if a.size and (a.dtype.kind not in "iu" or a.min() < -2 ** 31 or a.max() >= 2 ** 31):
+        raise ValueError(f"{name}: expected whole numbers of 32 bits")
+    return np.ascontiguousarray(a, dtype=np.int32)
+
+
 class PagedPlan:
     """Host plan blob of one step over a paged cache, and its device copy.
 
@@ -78,15 +86,14 @@ class PagedPlan:
     """
 
     def __init__(self, q_len, kv_len, pages, H, Hkv, d, page_size, num_pages, fmt=BD_CACHE_BF16, causal=True):
-        q = np.ascontiguousarray(q_len, dtype=np.int32)
-        kv = np.ascontiguousarray(kv_len, dtype=np.int32)
+        q, kv = _ints(q_len, "q_len"), _ints(kv_len, "kv_len")
         if q.ndim != 1 or q.shape != kv.shape or len(pages) != len(q):
             raise ValueError("q_len, kv_len and pages must have one entry per sequence")
         if isinstance(pages, np.ndarray) and pages.ndim == 2:
-            flat = np.ascontiguousarray(pages, dtype=np.int32).reshape(-1)
+            flat = _ints(pages, "pages").reshape(-1)
             offs = np.arange(len(q) + 1, dtype=np.int64) * pages.shape[1]
         else:
-            lists = [np.asarray(x, dtype=np.int32).reshape(-1) for x in pages]
+            lists = [_ints(x, "pages").reshape(-1) for x in pages]
             flat = np.concatenate(lists) if lists else np.zeros(0, np.int32)
             offs = np.cumsum([0] + [len(x) for x in lists])
         if offs[-1] >= 2 ** 31:

@@ -15,7 +15,8 @@ class Case:
     NaN unless `junk` says otherwise."""
 
     def __init__(self, new, kv, H, Hkv, d, page=16, fmt="bf16", heads_first=False, causal=True, seed=0, spare=2,
-                 device="cuda", junk=float("nan"), qscale=1.0, pad_rows=0):
+                 device="cuda", junk=float("nan"), qscale=1.0, pad_rows=0, kmag=(-3, 2),
+                 vmag=(-6, 6)):
         g = torch.Generator().manual_seed(seed)
         self.new, self.kv, self.H, self.Hkv, self.d, self.page = list(new), list(kv), H, Hkv, d, page
         self.fmt, self.causal = fmt, causal
@@ -27,8 +28,8 @@ class Case:
         shape = (self.num_pages, page, Hkv, d)
         k, v = torch.randn(shape, generator=g), torch.randn(shape, generator=g)
         if fmt == "e4m3":  # rows of different sizes
-            k = k * 2.0 ** torch.randint(-3, 3, shape[:3], generator=g)[..., None]
-            v = v * 2.0 ** torch.randint(-6, 7, shape[:3], generator=g)[..., None]
+            k = k * 2.0 ** torch.randint(kmag[0], kmag[1] + 1, shape[:3], generator=g)[..., None]
+            v = v * 2.0 ** torch.randint(vmag[0], vmag[1] + 1, shape[:3], generator=g)[..., None]
         used = torch.zeros(self.num_pages, page, dtype=torch.bool)
         for n, pg in zip(kv, self.pages):
             for j in range(0, n, page):

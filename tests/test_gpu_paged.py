@@ -46,7 +46,7 @@ def test_long_context_is_split_and_joined(H, Hkv, d, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
-@pytest.mark.parametrize("H,Hkv", [(10, 2), (7, 1), (32, 1), (6, 6), (24, 8)])
+@pytest.mark.parametrize("H,Hkv", [(10, 2), (7, 1), (32, 1), (20, 1), (6, 6), (24, 8), (128, 1)])
 def test_head_groups(H, Hkv, fmt):
     c = pu.Case([1, 3, 9], [40, 700, 9], H, Hkv, 128, page=32, fmt=fmt, seed=H)
     pu.check_attention(c, *pu.run_attention(c))
@@ -144,6 +144,72 @@ def test_nan_in_the_cache_reaches_those_who_see_it_only(fmt):
         c.ke[page, row, 0] = 255
     out, lse = pu.run_attention(c)
     assert torch.isnan(lse[:4, 1]).all() and torch.isfinite(lse[4:, 1]).all() and torch.isfinite(lse[:, 0]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d", HEADS)
+def test_chunk_over_a_long_context_is_split_and_joined(H, Hkv, d, fmt):
+    """Few blocks of tiles: their keys are cut over the SMs; at G = 3 a tile has idle rows."""
+    c = pu.Case([70], [9001], H, Hkv, d, page=64, fmt=fmt, seed=d)
+    pu.check_attention(c, *pu.run_attention(c))
+    c = pu.Case([50, 3], [5000, 700], 3, 1, d, page=16, fmt=fmt, seed=d + 1)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("new,kv", [([1, 2], [300, 90]), ([60], [200])])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("vmag", [(20, 40), (-40, 40), (-58, -50)])
+def test_exponents_of_any_size(vmag, d, new, kv):
+    """V rows whose exponents take two factors in a bf16 tile, span 2^80, or sit at the
+    format's lower end; K's exponents away from q's."""
+    c = pu.Case(new, kv, 4, 1, d, fmt="e4m3", seed=d, vmag=vmag, kmag=(18, 20), qscale=2.0 ** -20)
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_one_pool_for_k_and_v(fmt):
+    """K and V as slices of one pool [pages, 2, page, heads, d], exponents likewise."""
+    c = pu.Case([1, 40], [300, 90], 8, 2, 128, page=32, fmt=fmt)
+    want = pu.run_attention(c)
+    both = torch.stack([c.k.view(torch.uint8), c.v.view(torch.uint8)], 1).view(c.k.dtype)
+    ex = (None, None) if fmt == "bf16" else torch.stack([c.ke, c.ve], 1).unbind(1)
+    c.cache = bd.PagedCache(both[:, 0], both[:, 1], *ex)
+    got = pu.run_attention(c)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    k = torch.empty(390, 2, 128, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    bd.bd_cache_read(c.plan, c.cache, k, v)
+    assert torch.equal(k.cpu().double(), torch.cat([c.rows(b)[0] for b in range(2)]))
+    assert torch.equal(v.cpu().double(), torch.cat([c.rows(b)[1] for b in range(2)]))
+
+
+def test_pools_past_2_31_elements():
+    """The last pages of pools of more than 2^31 elements each."""
+    H, Hkv, d, P = 8, 8, 128, 1024
+    n = 2 ** 31 // (P * Hkv * d) + 3
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    k = torch.empty(n, P, Hkv, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    cache = bd.PagedCache(k, v)
+    g = torch.Generator().manual_seed(0)
+    new = [40, 1]
+    kn, vn, q = (torch.randn(41, h, d, generator=g).bfloat16() for h in (Hkv, Hkv, H))
+    plan = bd.PagedPlan(new, new, [[n - 1], [n - 2]], H, Hkv, d, page_size=P, num_pages=n).upload("cuda")
+    bd.bd_cache_write(plan, kn.cuda(), vn.cuda(), cache)
+    out, lse = bd.paged_attn(plan, q.cuda(), cache)
+    kr, vr = torch.empty(41, Hkv, d, dtype=torch.bfloat16, device="cuda"), torch.empty(41, Hkv, d, dtype=torch.bfloat16, device="cuda")
+    bd.bd_cache_read(plan, cache, kr, vr)
+    torch.cuda.synchronize()
+    bd.bd_check_status(plan)
+    assert torch.equal(kr.cpu(), kn) and torch.equal(vr.cpu(), vn)
+    assert torch.equal(k[n - 1, :40].cpu(), kn[:40]) and torch.equal(v[n - 2, :1].cpu(), vn[40:])
+    at = 0
+    for m in new:
+        o, l, A, big = op.attention(q[at:at + m], kn[at:at + m], vn[at:at + m], m)
+        to, tl = pu.tolerances(d, m, A, big, "bf16")
+        assert ((out[at:at + m].cpu().double() - o).abs() <= to).all() and ((lse[:, at:at + m].cpu().double() - l).abs() <= tl).all()
+        at += m
 
 
 # ------------------------------------------------------------------ attention: calls

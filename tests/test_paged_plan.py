@@ -341,3 +341,84 @@ def test_oracle_attention_matches_the_chunk_oracle():
     o, lse = oracle.attention_fwd(q, k, v, [0, 50])
     got, gl, _, _ = op.attention(q[43:], k, v, 50)
     assert torch.allclose(got, o[43:].double(), atol=1e-12) and torch.allclose(gl, lse[:, 43:].double(), atol=1e-12)
+
+
+def test_lengths_and_pages_are_whole_numbers_in_range():
+    for bad in ([1.5], [2 ** 32], np.array([2 ** 40])):
+        with pytest.raises(ValueError, match="whole"):
+            bd.PagedPlan([1], bad, [[0, 1]], 8, 2, 128, page_size=16, num_pages=4)
+        with pytest.raises(ValueError, match="whole"):
+            bd.PagedPlan([1], [16], [bad], 8, 2, 128, page_size=16, num_pages=4)
+    a = bd.PagedPlan(np.array([1], np.int64), torch.tensor([17]), [torch.tensor([2, 0])], 8, 2, 128, page_size=16, num_pages=4)
+    b = bd.PagedPlan([1], [17], [[2, 0]], 8, 2, 128, page_size=16, num_pages=4)
+    assert np.array_equal(a.host, b.host)
+
+
+def test_no_lengths_past_the_kernels_arithmetic():
+    """A page may be listed again and again: kv_len is bounded by itself, not by the pool."""
+    n = 2 ** 31 - 1
+    pages = np.zeros((1, 2 ** 21), np.int32)
+    with pytest.raises(bd.BDError) as e:
+        bd.PagedPlan([1], [n], pages, 8, 2, 128, page_size=1024, num_pages=4)
+    assert e.value.status == _abi.BD_ERR_CAPACITY
+
+
+def test_a_blob_too_small_is_refused():
+    plan, pages = make([300, 1], [300, 5000])
+    q, kv, flat = (np.array(x, np.int32) for x in ([300, 1], [300, 5000], sum(pages, [])))
+    offs = np.array([0, len(pages[0]), len(flat)], np.int32)
+    p32 = ctypes.POINTER(ctypes.c_int32)
+    desc = _abi.bd_paged_desc(2, 8, 2, 128, 16, plan.num_pages, 0, 1, *[x.ctypes.data_as(p32) for x in (q, kv, flat, offs)])
+    need = bd.bd_paged_plan_bytes(desc)
+    blob = np.full(need // 4 + 16, 7, np.int32)
+    at = blob.ctypes.data + (-blob.ctypes.data % 64)
+    lib = bd.load()
+    assert lib.bd_paged_plan_build(ctypes.byref(desc), ctypes.c_void_p(at), need - 4) == _abi.BD_ERR_CAPACITY
+    assert (blob == 7).all()
+    assert lib.bd_paged_plan_build(ctypes.byref(desc), ctypes.c_void_p(at + 4), need) == _abi.BD_ERR_ARG      # alignment
+    assert lib.bd_paged_plan_build(ctypes.byref(desc), ctypes.c_void_p(at), need) == 0
+    off = (at - blob.ctypes.data) // 4
+    assert np.array_equal(blob[off:off + len(plan.host)], plan.host) and len(plan.host) * 4 <= need
+
+
+_C = r"""
+#include <stdio.h>
+#include <string.h>
+#include "bd_paged.h"
+int main(void) {
+  const int32_t q[2] = {1, 3}, kv[2] = {40, 17}, pages[5] = {4, 0, 2, 1, 3}, offs[3] = {0, 3, 5}, bad[5] = {4, 0, 9, 1, 3};
+  bd_paged_desc d;
+  size_t n = 0;
+  static int32_t blob[1 << 16];
+  uint64_t key = 0;
+  memset(&d, 0, sizeof d);
+  d.B = 2; d.H = 8; d.Hkv = 2; d.d = 128; d.page_size = 16; d.num_pages = 5; d.fmt = BD_CACHE_E4M3; d.causal = 1;
+  d.q_len = q; d.kv_len = kv; d.pages = pages; d.page_offsets = offs;
+  if (bd_paged_plan_bytes(&d, &n) != BD_OK || n > sizeof blob) { printf("error %s\n", bd_last_error()); return 1; }
+  if (bd_paged_plan_build(&d, (void*)(((size_t)blob + 15) & ~(size_t)15), sizeof blob - 16) != BD_OK) return 1;
+  if (bd_paged_plan_key((void*)(((size_t)blob + 15) & ~(size_t)15), &key) != BD_OK || key == 0) return 1;
+  d.pages = bad;
+  printf("reject %d\n", (int)bd_paged_plan_bytes(&d, &n));
+  printf("sizeof %u %u\n", (unsigned)sizeof(bd_paged_cache), (unsigned)sizeof(bd_paged_desc));
+  return 0;
+}
+"""
+
+
+def test_c99_consumer(tmp_path):
+    """The header is plain C99, the structs have the binding's sizes, and a C program
+    plans and is refused like the binding."""
+    import os
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc")
+    if cc is None:
+        pytest.skip("no C compiler")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    src, exe = tmp_path / "p.c", tmp_path / "p"
+    src.write_text(_C)
+    subprocess.run([cc, "-std=c99", "-pedantic", "-Wall", "-Werror", "-I", os.path.join(root, "include"), str(src), "-o", str(exe),
+                    _abi.LIB_PATH, f"-Wl,-rpath,{os.path.dirname(_abi.LIB_PATH)}"], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    assert out == ["reject", str(_abi.BD_ERR_ARG), "sizeof", str(ctypes.sizeof(_abi.bd_paged_cache)),
+                   str(ctypes.sizeof(_abi.bd_paged_desc))]
