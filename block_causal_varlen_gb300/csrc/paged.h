@@ -57,6 +57,6 @@ struct AttnArgs {
 
 int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, const bd_paged_cache* cache,
                     cudaStream_t stream);
-int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* cache, cudaStream_t stream);
+int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* cache, bool behind, cudaStream_t stream);
 
 }  // namespace bd

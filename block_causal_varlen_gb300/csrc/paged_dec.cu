@@ -665,6 +665,9 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     }
     __syncthreads();
   }
+  // (launched behind the tile kernel, this grid starts as that one's CTAs leave their SMs;
+  // the joins that follow wait for this grid's end, which so is that one's as well)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (!ok) {
     // every copy issued has been waited for in turn; wait (with a limit) for those a
     // wait gave up on, then say so
@@ -845,8 +848,25 @@ __global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArg
   if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// `behind`: the grid may start before the one in front of it has ended (and waits for that
+// itself, where it needs to).
+template <class... P, class... A>
+cudaError_t launch_kernel(void (*kernel)(P...), int grid, int threads, size_t smem, bool behind, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
+
 template <int D, int FMT, int NB>
-int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, bool behind, cudaStream_t s) {
   using Cfg = DecCfg<D, FMT, NB>;
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -861,35 +881,20 @@ int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& 
   int32_t st;
   if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, 1))) return st;
   if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, 1))) return st;
-  bd_paged_dec_kernel<D, FMT, NB><<<kDecCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mk, mv, a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB>, kDecCtas, Cfg::kThreads, Cfg::kSmem, behind, s, mk, mv, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
 }
 
 template <int D, int FMT>
-int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, bool behind, cudaStream_t s) {
   const int rows = w[PH_DEC_ROWS];
-  if (rows == 8) return launch_dec_t<D, FMT, 1>(w, c, a, s);
-  if (rows == 16) return launch_dec_t<D, FMT, 2>(w, c, a, s);
+  if (rows == 8) return launch_dec_t<D, FMT, 1>(w, c, a, behind, s);
+  if (rows == 16) return launch_dec_t<D, FMT, 2>(w, c, a, behind, s);
   if constexpr (dec_block_rows(FMT) == 32) {
-    if (rows == 24) return launch_dec_t<D, FMT, 3>(w, c, a, s);
-    if (rows == 32) return launch_dec_t<D, FMT, 4>(w, c, a, s);
+    if (rows == 24) return launch_dec_t<D, FMT, 3>(w, c, a, behind, s);
+    if (rows == 32) return launch_dec_t<D, FMT, 4>(w, c, a, behind, s);
   }
   return fail(BD_ERR_PLAN, "few-rows blocks of %d rows at head dim %d", rows, D);
-}
-
-// The join starts while the attention kernel drains, and waits for its results itself.
-cudaError_t launch_join(void (*kernel)(MergeArgs), dim3 grid, const MergeArgs& a, cudaStream_t s) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = grid;
-  c.blockDim = dim3(256);
-  c.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, a);
 }
 
 }  // namespace
@@ -900,17 +905,17 @@ int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream
   const Kernel k = tile   ? pick(bd_paged_tile_merge_kernel<64>, bd_paged_tile_merge_kernel<128>, bd_paged_tile_merge_kernel<256>)
                    : wide ? pick(bd_paged_wide_merge_kernel<64>, bd_paged_wide_merge_kernel<128>, bd_paged_wide_merge_kernel<256>)
                           : pick(bd_paged_merge_kernel<64>, bd_paged_merge_kernel<128>, bd_paged_merge_kernel<256>);
-  const cudaError_t e = launch_join(k, dim3(kPagedSms * (tile ? 8 : wide ? 4 : 2)), a, s);
+  const cudaError_t e = launch_kernel(k, kPagedSms * (tile ? 8 : wide ? 4 : 2), 256, 0, true, s, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "paged join launch");
 }
 
-int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, cudaStream_t s) {
+int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, bool behind, cudaStream_t s) {
   const int d = w[PH_D];
   if (c->fmt == BD_CACHE_BF16)
-    return d == 64 ? launch_dec_rows<64, BD_CACHE_BF16>(w, c, a, s)
-           : d == 128 ? launch_dec_rows<128, BD_CACHE_BF16>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_BF16>(w, c, a, s);
-  return d == 64 ? launch_dec_rows<64, BD_CACHE_E4M3>(w, c, a, s)
-         : d == 128 ? launch_dec_rows<128, BD_CACHE_E4M3>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_E4M3>(w, c, a, s);
+    return d == 64 ? launch_dec_rows<64, BD_CACHE_BF16>(w, c, a, behind, s)
+           : d == 128 ? launch_dec_rows<128, BD_CACHE_BF16>(w, c, a, behind, s) : launch_dec_rows<256, BD_CACHE_BF16>(w, c, a, behind, s);
+  return d == 64 ? launch_dec_rows<64, BD_CACHE_E4M3>(w, c, a, behind, s)
+         : d == 128 ? launch_dec_rows<128, BD_CACHE_E4M3>(w, c, a, behind, s) : launch_dec_rows<256, BD_CACHE_E4M3>(w, c, a, behind, s);
 }
 
 }  // namespace bd
@@ -974,16 +979,21 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   a.scale_log2 = scale * 1.4426950408889634f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   a.G = w[PH_G]; a.causal = w[PH_CAUSAL]; a.page_shift = w[PH_PAGE_SHIFT];
-  MergeArgs m = {a.plan, a.part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh, a.G};
-  if (w[PH_NDEC]) {
-    if ((st = launch_dec(w, a, cache, s))) return st;
-    if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, w[PH_DECM_WIDE] != 0, s))) return st;
-  }
-  if (w[PH_NTILE]) {
-    a.part += dec_part_bytes(w) / 4;
-    m.part = a.part;
+  float* const dec_part = a.part;
+  float* const tile_part = a.part + dec_part_bytes(w) / 4;
+  const bool dec = w[PH_NDEC] > 0, tile = w[PH_NTILE] > 0;
+  // tiles first: their CTAs leave their SMs at different times, which few-rows CTAs fill
+  if (tile) {
+    a.part = tile_part;
     if ((st = launch_tile(w, a, q, cache, s))) return st;
-    if (w[PH_NTILEM] && (st = launch_merge(m, w[PH_D], true, false, s))) return st;
   }
+  if (dec) {
+    a.part = dec_part;
+    if ((st = launch_dec(w, a, cache, tile, s))) return st;
+  }
+  MergeArgs m = {a.plan, dec_part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh, a.G};
+  if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, w[PH_DECM_WIDE] != 0, s))) return st;
+  m.part = tile_part;
+  if (w[PH_NTILEM] && (st = launch_merge(m, w[PH_D], true, false, s))) return st;
   return ok();
 }
