@@ -61,6 +61,11 @@ struct TileCfg {
   static constexpr int kPre = 16;                 // pieces kept in shared memory
   static constexpr int kSmem = kOffPieces + kPre * kPieceWords * 4 + 1024;  // + alignment slack
   static constexpr int kOCol = 256;               // first O column in TMEM
+  // Whether P is handed to the tensor core in halves. With one slot the first half of P V
+  // runs while the second half of P is made (4096 rows over 16384 at d 256: 2090 ->
+  // 1890 us); with two the other slot's products fill that time, and the early half only
+  // gets in their way (d 128: 668 -> 724).
+  static constexpr bool kPHalves = kSlots == 1;
   static constexpr int kThreads = kF8 ? 512 : 384;
   // registers after setmaxnreg: warps 0-3, the softmax warps, the converting warps
   static constexpr int kRegsCtl = kF8 ? 40 : 72, kRegsSoftmax = kF8 ? 200 : 216, kRegsConv = 72;
@@ -74,7 +79,8 @@ struct TileCfg {
 // barrier indices (8 bytes each)
 enum : int {
   T_QFULL = 0, T_QEMPTY, T_KFULL = 4, T_KEMPTY = 8, T_VFULL = 12, T_VEMPTY = 16, T_RFULL = 20, T_REMPTY = 24,
-  T_SFULL = 28, T_PFULL = 30, T_OFINAL = 32, T_OEMPTY = 34, T_TURN = 36, T_DRAIN = 38, T_VTAIL = 40, T_COUNT = 44
+  T_SFULL = 28, T_PFULL = 30, T_OFINAL = 32, T_OEMPTY = 34, T_TURN = 36, T_DRAIN = 38, T_VTAIL = 40, T_PHALF = 44,
+  T_COUNT = 46
 };
 static_assert(8 * T_COUNT + 16 <= 512, "barriers, TMEM slot and abort flag overflow their region");
 
@@ -155,6 +161,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(T_SFULL + s), 1);
       mbar_init(bar(T_PFULL + s), 128);
+      mbar_init(bar(T_PHALF + s), 128);
       mbar_init(bar(T_OFINAL + s), 1);
       mbar_init(bar(T_OEMPTY + s), 128);
       mbar_init(bar(T_TURN + s), 1);
@@ -297,11 +304,15 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             mma_ss_lo(d_s, qa + off, kb + off, idS, kk > 0);
           }
         };
-        auto issue_pv = [&](int st, bool acc) {
+        constexpr int kHalf = Cfg::kPHalves ? 4 : 0;  // steps of P V that start after the first half of P
+        auto issue_pv = [&](auto from, auto to, int st, bool acc) {
           const uint32_t vb = sdesc_lo(sV + st * Cfg::kTileBytes, 16384);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_ts_lo(d_o, d_s + kk * 8, vb + uint32_t(kk * 128), idPV, (acc || kk > 0) ? 1u : 0u);
+          for (int kk = from; kk < to; ++kk) mma_ts_lo(d_o, d_s + kk * 8, vb + uint32_t(kk * 128), idPV, (acc || kk > 0) ? 1u : 0u);
         };
+        using Steps0 = std::integral_constant<int, 0>;
+        using StepsH = std::integral_constant<int, kHalf>;
+        using Steps8 = std::integral_constant<int, 8>;
         // this slot's part of releasing the Q tiles, after its last product S
         auto release_q = [&](bool act) {
           if (act && !Cfg::kStageInQ) tc_commit(bar(T_QEMPTY));
@@ -336,15 +347,22 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             const uint32_t itp = it + j - 1, itn = it + j;
             const int svp = itp % NST, skn = itn % NST;
             if (act) {
-              if (!(ok = mbar_wait_spin(bar(T_PFULL + s), (tc + j - 1) & 1, abort_flag))) break;
+              if (!(ok = mbar_wait_spin(bar((kHalf ? T_PHALF : T_PFULL) + s), (tc + j - 1) & 1, abort_flag))) break;
               if (j == 1 && !(ok = mbar_wait(bar(T_OEMPTY + s), (ai & 1) ^ 1, abort_flag))) break;
             }
             if (!(ok = mbar_wait(bar(T_VFULL + svp), (itp / NST) & 1, abort_flag))) break;
+            if constexpr (kHalf > 0) {
+              if (act) {
+                tc_fence_after();
+                issue_pv(Steps0{}, StepsH{}, svp, j > 1);
+                if (!(ok = mbar_wait_spin(bar(T_PFULL + s), (tc + j - 1) & 1, abort_flag))) break;
+              }
+            }
             if (j < P.nt && !(ok = mbar_wait(bar(T_KFULL + skn), (itn / NST) & 1, abort_flag))) break;
             if (!(ok = take_turn())) break;
             if (act) {
               tc_fence_after();
-              issue_pv(svp, j > 1);
+              issue_pv(StepsH{}, Steps8{}, svp, j > 1);
               if (j < P.nt) issue_s(skn);
               pass_turn();
               tc_commit(bar(T_VEMPTY + svp));
@@ -496,10 +514,16 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           v.y = ex2(v.y);
           s4[e & 3] = fadd2(s4[e & 3], v);
           pk[e >> 5][e & 31] = pack_bf16(v.x, v.y);
+          if (Cfg::kPHalves && e == 31) {
+            tmem_st32(tS, pk[0]);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(bar(T_PHALF + s));
+          }
         }
         const float2 st = fadd2(fadd2(s4[0], s4[1]), fadd2(s4[2], s4[3]));
         l_run += st.x + st.y;
-        tmem_st32(tS, pk[0]);
+        if (!Cfg::kPHalves) tmem_st32(tS, pk[0]);
         tmem_st32(tS + 32, pk[1]);
         tmem_st_wait();
         tc_fence_before();
