@@ -47,8 +47,8 @@ struct AttnArgs {
   float* lse;  // NULL: not wanted
   int64_t l_sh;
   float* part;
-  const uint8_t *kc, *vc;  // the cache, strides in bytes
-  int64_t k_sp, k_sr, k_sh, v_sp, v_sr, v_sh;
+  const uint8_t* vc;  // the cache's V, strides in bytes
+  int64_t v_sp, v_sr, v_sh;
   const uint8_t *k_exp, *v_exp;
   int64_t e_sp, e_sr, e_sh;
   float scale_log2;

@@ -26,9 +26,13 @@
 //     conflicts. Exponents never touch the codes: K's is a factor of the score, V's an
 //     addend of the base-2 exponent (m is then the maximum of s_j + e_j). q as fp16 is
 //     exact too: each row is scaled by a power of two first.
-// P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-9 relative,
-// like O itself), fp16 for e4m3 (2^-12), scaled by 2^7 so that terms down to 2^-31
-// of the largest keep a value.
+// P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-8 relative at
+// most, like O itself), fp16 for e4m3 (2^-11), scaled by 2^7 so that terms down to
+// 2^-31 of the largest keep a value.
+//
+// A row takes nothing from a key it does not see, whatever is there: V's infinities
+// and NaN, which a probability of zero would turn to NaN, stay out of the products of
+// chunks that some row does not see in full, and are added for the rows that do see them.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -509,10 +513,18 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
           pb[y >> 1][b][y & 1] = transpose8(w);
         }
       }
-      // ---- O^T += V^T P^T. Keys at or past k1 may hold anything: their V become zeros.
+      // ---- O^T += V^T P^T. Keys at or past k1 may hold anything: their V become zeros. So
+      // do V's infinities and NaN where some row does not see every key (e4m3: where a row
+      // of V is NaN, which P says to those who see it).
       const uint32_t sv = st + Cfg::kMatBytes;
+      uint32_t odd = 0;
       auto values = [&](auto cut) {
         constexpr bool TAIL = decltype(cut)::value;
+        auto clean = [&](uint32_t& x) {
+          const uint32_t u = __vcmpeq2(x & 0x7f807f80u, 0x7f807f80u);
+          x &= ~u;
+          odd |= u;
+        };
 #pragma unroll
         for (int y = 0; y < KT; ++y) {
           uint32_t vm[2] = {~0u, ~0u};
@@ -521,6 +533,11 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
             for (int n = 0; n < 2; ++n) {
               const int key = k + 16 * y + 8 * n + 2 * j;
               vm[n] = (key < k1 ? 0xffffu : 0u) | (key + 1 < k1 ? 0xffff0000u : 0u);
+              if constexpr (F8) {
+                const int at = 16 * y + 8 * n + 2 * j;
+                const uint32_t e0 = __shfl_sync(0xffffffffu, vb, at), e1 = __shfl_sync(0xffffffffu, vb, at + 1);
+                vm[n] &= (e0 == 255u ? 0u : 0xffffu) | (e1 == 255u ? 0u : 0xffff0000u);
+              }
             }
           }
           if constexpr (!F8) {
@@ -530,7 +547,11 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
               uint32_t x[4];
               const uint32_t ch = uint32_t(2 * n + ((lane >> 3) & 1));
               ldsm4t(vrow + (ch >> 3) * (kChunk * 128) + (((ch & 7) ^ (lane & 7)) << 4), x);
-              if constexpr (TAIL) { x[0] &= vm[0]; x[1] &= vm[0]; x[2] &= vm[1]; x[3] &= vm[1]; }
+              if constexpr (TAIL) {
+                x[0] &= vm[0]; x[1] &= vm[0]; x[2] &= vm[1]; x[3] &= vm[1];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) clean(x[i]);
+              }
 #pragma unroll
               for (int b = 0; b < NB; ++b) mma16<false>(o[n][b], x[0], x[1], x[2], x[3], pb[y][b][0], pb[y][b][1]);
             }
@@ -565,8 +586,24 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
           }
         }
       };
-      if (k + kChunk > k1) values(std::true_type());
+      if (k + kChunk > min(k1, all_see) || (F8 && vnan)) values(std::true_type());
       else values(std::false_type());
+      if constexpr (!F8) {
+        if (__any_sync(0xffffffffu, odd != 0)) {
+          for (int key = 0; key < min(kChunk, k1 - k); ++key)
+#pragma unroll
+            for (int n = 0; n < 2 * MT; ++n) {  // this lane's columns 8 n + rw
+              uint16_t u;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(sv + key * 128 + (n >> 3) * (kChunk * 128) + (((n & 7) ^ (key & 7)) << 4) + rw * 2) : "memory");
+              if ((u & 0x7f80u) != 0x7f80u) continue;
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                  if (k + key < lim[b][e]) o[n >> 1][b][2 * (n & 1) + e] += __uint_as_float(uint32_t(u) << 16);
+            }
+        }
+      }
       __syncwarp();  // every lane has read the stage
       if (ok && cp < p1) issue();
       __syncwarp();
@@ -728,8 +765,8 @@ __device__ __forceinline__ void join_row(const float* P, int64_t o, int cnt, int
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
     mn = fmaxf(mn, mx);
-    const float f = mx == -CUDART_INF_F ? 0.f : ex2(mx - mn), w = mi == -CUDART_INF_F ? 0.f : ex2(mi - mn);
-    float ls = mi == -CUDART_INF_F ? 0.f : li * w;
+    const float f = mx == -CUDART_INF_F ? 0.f : ex2(mx - mn), w = mi == -CUDART_INF_F ? -1.f : ex2(mi - mn);
+    float ls = w < 0.f ? 0.f : li * w;
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
     l = l * f + ls;
@@ -739,7 +776,7 @@ __device__ __forceinline__ void join_row(const float* P, int64_t o, int cnt, int
     auto add = [&](int k, const float (&x)[V]) {
       const float wk = __shfl_sync(0xffffffffu, w, k);
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[v] += wk == 0.f ? 0.f : x[v] * wk;
+      for (int v = 0; v < V; ++v) acc[v] += wk < 0.f ? 0.f : x[v] * wk;
     };
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -969,8 +1006,7 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   a.l_sh = lse ? lse->stride_head : 0;
   a.part = static_cast<float*>(workspace);
   const int64_t es = cache->fmt == BD_CACHE_BF16 ? 2 : 1;
-  a.kc = static_cast<const uint8_t*>(cache->k.ptr); a.vc = static_cast<const uint8_t*>(cache->v.ptr);
-  a.k_sp = cache->k.stride_b * es; a.k_sr = cache->k.stride_row * es; a.k_sh = cache->k.stride_head * es;
+  a.vc = static_cast<const uint8_t*>(cache->v.ptr);
   a.v_sp = cache->v.stride_b * es; a.v_sr = cache->v.stride_row * es; a.v_sh = cache->v.stride_head * es;
   a.k_exp = cache->k_exp; a.v_exp = cache->v_exp;
   a.e_sp = cache->exp_stride_page; a.e_sr = cache->exp_stride_row; a.e_sh = cache->exp_stride_head;

@@ -18,7 +18,9 @@
 //   warps 1, 2   one thread per slot issues its tcgen05 products, taking turns:
 //                S = Q K^T into TMEM, O += P V with P read from TMEM
 //   warp 3       bf16: clears V rows past the keys' end (a page's unused rows may hold
-//                anything, and 0 x NaN is NaN)
+//                anything, and 0 x NaN is NaN), and infinities and NaN out of V rows that
+//                not every row sees; those who see them get them at the block's end, read
+//                from the cache (a rare and slow path)
 //   warps 4-11   softmax, thread = row; they also store the results
 //   warps 12-15  e4m3 only: turn raw tiles into bf16 ones. A code's bits, shifted into
 //                a bf16, are its value times 2^-120; one packed multiplication by
@@ -82,10 +84,12 @@ enum : int {
   T_SFULL = 28, T_PFULL = 30, T_OFINAL = 32, T_OEMPTY = 34, T_TURN = 36, T_DRAIN = 38, T_VTAIL = 40, T_PHALF = 44,
   T_COUNT = 46
 };
-static_assert(8 * T_COUNT + 16 <= 512, "barriers, TMEM slot and abort flag overflow their region");
+constexpr int kOddMarks = 8;  // at most 4 key tiles, so 4 blocks, are under way at a time
+static_assert(8 * T_COUNT + 16 + 4 * kOddMarks <= 512, "barriers, TMEM slot, abort flag and marks overflow their region");
 
 struct Piece {
   int q0, qlen, kvlen, pages, hkv, t0, k0, k1, slot, nt, ns;
+  int clear;  // keys that every row of the block sees: below this
 };
 
 __device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
@@ -125,6 +129,9 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
   auto bar = [&](int i) { return bars + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffBar + 8 * T_COUNT);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + Cfg::kOffBar + 8 * T_COUNT + 8);
+  // of the n-th block with keys (n = 1, 2, ...): odd[(n - 1) % kOddMarks] >= n if V values
+  // were taken out (or if a later block has written over the mark)
+  volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffBar + 8 * T_COUNT + 16);
   int32_t* pre = reinterpret_cast<int32_t*>(smem + Cfg::kOffPieces);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -167,6 +174,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       mbar_init(bar(T_TURN + s), 1);
       mbar_init(bar(T_DRAIN + s), 1);
     }
+    for (int i = 0; i < kOddMarks; ++i) odd[i] = 0;
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -186,6 +194,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     P.t0 = W[PC_T0]; P.k0 = W[PC_K0]; P.k1 = W[PC_K1]; P.slot = W[PC_SLOT];
     P.nt = (P.k1 - P.k0 + 127) >> 7;
     P.ns = NS == 2 && P.t0 + TPS < P.qlen ? 2 : 1;
+    P.clear = min(P.k1, causal ? P.kvlen - P.qlen + P.t0 + 1 : P.kvlen);
     return P;
   };
 
@@ -242,8 +251,9 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_KEMPTY + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
             load(&tm_k, sK + s * Cfg::kTileBytes, bar(T_KFULL + s), n, pos, page, P.hkv);
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_VEMPTY + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
-            // a tile with rows past the keys' end goes by way of warp 3
-            load(&tm_v, sV + s * Cfg::kTileBytes, bar((pos + 128 > P.k1 ? T_VTAIL : T_VFULL) + s), n, pos, page, P.hkv);
+            // a tile with rows past the keys' end, or that some row does not see, goes by
+            // way of warp 3
+            load(&tm_v, sV + s * Cfg::kTileBytes, bar((pos + 128 > P.clear ? T_VTAIL : T_VFULL) + s), n, pos, page, P.hkv);
           } else {
             for (int h = 0; h < 2 && ok; ++h, ++rit) {
               const int s = rit % NR;
@@ -391,24 +401,44 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         }
       }
     } else if (warp == 3 && !F8) {
-      // -------------------------------------------------------- V rows past the keys' end
+      // -------------------------------------------------------- V rows some do not see
       // Such a tile's load completes T_VTAIL of its stage; this warp completes T_VFULL.
-      uint32_t it = 0, parity = 0;  // bit s: phase of T_VTAIL + s (a stage's next such load waits for its products)
-      for (int p = p0; p < p1; ++p) {
+      uint32_t it = 0, n = 0, parity = 0;  // bit s: phase of T_VTAIL + s (a stage's next such load waits for its products)
+      bool ok = true;
+      for (int p = p0; p < p1 && ok; ++p) {
         const Piece P = piece(p);
-        it += P.nt;
-        if (P.nt == 0 || !(P.k1 & 127)) continue;
-        const int st = (it - 1) % NST;
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(T_VTAIL + st), (parity >> st) & 1, abort_flag))) break;
-        parity ^= 1u << st;
-        const uint32_t v = sV + st * Cfg::kTileBytes;
-        const int r0 = P.k1 & 127;
-        for (int i = lane; i < (128 - r0) * 8; i += 32)   // 16-byte pieces of those rows
+        if (P.nt == 0) continue;
+        ++n;
+        for (int j = max(0, P.clear - P.k0) >> 7; j < P.nt; ++j) {
+          const int st = (it + j) % NST, pos = P.k0 + 128 * j;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_VTAIL + st), (parity >> st) & 1, abort_flag)))) break;
+          parity ^= 1u << st;
+          const uint32_t v = sV + st * Cfg::kTileBytes;
+          const int r0 = max(0, P.clear - pos), r1 = min(128, P.k1 - pos);
+          // 16-byte pieces of rows [r0, r1), then of those past the end
+          uint32_t bad = 0;
+#pragma unroll 2
+          for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) st_shared_v4(v + c * 16384 + (r0 * 8 + i) * 16, 0u, 0u, 0u, 0u);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(T_VFULL + st));
+            for (int c = 0; c < D / 64; ++c) {
+              const uint32_t at = v + c * 16384 + i * 16;
+              const uint4 x = ld_shared_u4(at);
+              // bit 15 of a half is set if its exponent is all ones
+              auto ones = [](uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; };
+              if (((ones(x.x) | ones(x.y) | ones(x.z) | ones(x.w)) & 0x80008000u) == 0) continue;
+              auto clean = [](uint32_t w) { return w & ~__vcmpeq2(w & 0x7f807f80u, 0x7f807f80u); };
+              st_shared_v4(at, clean(x.x), clean(x.y), clean(x.z), clean(x.w));
+              bad = 1;
+            }
+          for (int i = r1 * 8 + lane; i < 1024; i += 32)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) st_shared_v4(v + c * 16384 + i * 16, 0u, 0u, 0u, 0u);
+          if (bad) odd[(n - 1) % kOddMarks] = n;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(T_VFULL + st));
+        }
+        it += P.nt;
       }
     }
   } else if (warp < 12) {
@@ -419,10 +449,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_base + s * 128, tO = tmem + lane_base + Cfg::kOCol + s * D;
     const int tl = r / G, hg = r - tl * G;
-    uint32_t tc = 0, ai = 0;
+    uint32_t tc = 0, ai = 0, n = 0;
     bool ok = s < NS;
     for (int p = p0; p < p1 && ok; ++p) {
       const Piece P = piece(p);
+      n += P.nt > 0 ? 1 : 0;
       if (s >= P.ns) continue;
       const int t = P.t0 + s * TPS + tl, h = P.hkv * G + hg;
       const bool live = tl < TPS && t < P.qlen;
@@ -453,19 +484,19 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[q * 32 + e] = __uint_as_float(u[q][e]);
-        // the row sees the tile's columns below n; per group of 32 columns the warp
+        // the row sees the tile's columns below `see`; per group of 32 columns the warp
         // skips what no row sees and leaves alone what every row sees
-        const int n = lim - (P.k0 + 128 * j);
+        const int see = lim - (P.k0 + 128 * j);
         uint32_t gone = 0;
-        if (__any_sync(0xffffffffu, n < 128)) {
+        if (__any_sync(0xffffffffu, see < 128)) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (__all_sync(0xffffffffu, n <= 32 * q)) {
+            if (__all_sync(0xffffffffu, see <= 32 * q)) {
               gone |= 1u << q;
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[32 * q + e] = -CUDART_INF_F;
-            } else if (!__all_sync(0xffffffffu, n >= 32 * q + 32)) {
-              const int c = n - 32 * q;
+            } else if (!__all_sync(0xffffffffu, see >= 32 * q + 32)) {
+              const int c = see - 32 * q;
               const uint32_t seen = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
 #pragma unroll
               for (int e = 0; e < 32; ++e) x[32 * q + e] = (seen & (1u << e)) ? x[32 * q + e] : -CUDART_INF_F;
@@ -533,6 +564,31 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_OFINAL + s), ai & 1, abort_flag)))) break;
       tc_fence_after();
       ++ai;
+      const bool mend = odd[(n - 1) % kOddMarks] >= n;
+      // V's infinities and NaN that were taken out of columns [c0, c0 + 32), for the keys
+      // this row sees
+      auto put_back = [&](uint32_t (&o)[32], int c0) {
+        for (int key = max(P.k0, P.clear); key < min(lim, P.k1); ++key) {
+          const int64_t page = plan[P.pages + (key >> pshift)], row = key & ((1 << pshift) - 1);
+          if constexpr (F8) {
+            if (a.v_exp[page * a.e_sp + row * a.e_sr + P.hkv * a.e_sh] == 255u)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = 0x7fffffffu;
+          } else {
+            const uint4* v = reinterpret_cast<const uint4*>(a.vc + page * a.v_sp + row * a.v_sr + P.hkv * a.v_sh + c0 * 2);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 x = v[c];
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t b = e & 1 ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16;
+                if ((b & 0x7f800000u) == 0x7f800000u) o[8 * c + e] = __float_as_uint(__uint_as_float(o[8 * c + e]) + __uint_as_float(b));
+              }
+            }
+          }
+        }
+      };
       // NaN scores leave the maximum alone: what they gave was taken relative to 0
       const float m_fin = m_run == -CUDART_INF_F && l_run != 0.f ? 0.f : m_run;
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
@@ -580,6 +636,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           tc_fence_before();
           mbar_arrive(bar(T_OEMPTY + s));
         }
+        if (mend)
+#pragma unroll
+          for (int q = 0; q < QH; ++q) put_back(ov[q], (q0 + q) * 32);
+        __syncwarp();
         if (part) {
 #pragma unroll
           for (int q = 0; q < QH; ++q) {
@@ -613,11 +673,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       regs_set<Cfg::kRegsConv, Cfg::kRegsLaunch>();
       // -------------------------------------------------------- raw tiles to bf16, thread = key
       const int r = threadIdx.x - 384;
-      uint32_t it = 0, rit = 0;
+      uint32_t it = 0, rit = 0, n = 0;
       bool ok = true;
       // codes of this thread's row (at `src`) times 2^e into the bf16 tile at `dst`;
-      // SLOW: some row of the warp is past the keys' end, NaN, or of an exponent that
-      // takes two factors
+      // SLOW: some row of the warp is to be zeros (past the keys' end, or V of NaN that not
+      // every row sees), NaN, or of an exponent that takes two factors
       auto convert = [&](auto slow, uint32_t src, uint32_t dst, uint32_t byte, bool zero) {
         constexpr bool SLOW = decltype(slow)::value;
         const int e = int(byte) - 127;
@@ -667,6 +727,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           const int64_t o = int64_t(page) * a.e_sp + int64_t((P.k0 + 128 * j + r) & ((1 << pshift) - 1)) * a.e_sr + int64_t(P.hkv) * a.e_sh;
           return uint32_t(a.k_exp[o]) | (uint32_t(a.v_exp[o]) << 8);
         };
+        n += P.nt > 0 ? 1 : 0;
         int pg = page_of(0);
         uint32_t ex = exps_of(0, pg);
         pg = page_of(1);
@@ -682,8 +743,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar((h ? T_VEMPTY : T_KEMPTY) + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
             const uint32_t src = sR + rs * Cfg::kRawBytes, dst = (h ? sV : sK) + s * Cfg::kTileBytes;
             const uint32_t byte = (now >> (8 * h)) & 255u;
-            if (__any_sync(0xffffffffu, past || byte > 127u + 7u)) convert(std::true_type(), src, dst, byte, past);
-            else convert(std::false_type(), src, dst, byte, past);
+            const bool out = h && byte == 255u && !past && P.k0 + 128 * j + r >= P.clear;
+            if (out) odd[(n - 1) % kOddMarks] = n;
+            if (__any_sync(0xffffffffu, past || byte > 127u + 7u)) convert(std::true_type(), src, dst, byte, past || out);
+            else convert(std::false_type(), src, dst, byte, false);
             mbar_arrive(bar(T_REMPTY + rs));
             mbar_arrive(bar((h ? T_VFULL : T_KFULL) + s));
           }

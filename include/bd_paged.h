@@ -28,7 +28,7 @@
  *     captured call may be replayed after the device copy has been overwritten
  *     with another step's plan of the same bd_paged_plan_key.
  *   - new rows are rows [0, T) of the packed tensors, T = sum of q_len; rows past
- *     T are neither read nor written.
+ *     T have no influence and are not written.
  */
 #ifndef BD_PAGED_H
 #define BD_PAGED_H
@@ -47,7 +47,8 @@ typedef enum {
    * max|x| <= 448 * 2^e (60 if there is none) and stores code = x * 2^-e rounded to
    * nearest even, saturating at +-448, and byte e + 127. A row with an infinity or a
    * NaN is stored as NaN codes with byte 255 and reads back as NaN. Values read back
-   * are exact in bf16. Caches filled by other means may use bytes 67..187 and 255. */
+   * are exact in bf16. Caches filled by other means may use bytes 67..187 and 255, and
+   * the NaN codes 0x7f and 0xff in rows of byte 255 only. */
   BD_CACHE_E4M3 = 1
 } bd_cache_fmt;
 
@@ -129,8 +130,9 @@ BD_API int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes);
 /* bd_paged_attn -- O (bf16) and LSE (fp32, may be NULL) of the new rows over their
  * sequences' cached rows; q, out: rows >= T, stride_b and stride_c unused; lse
  * [H, rows], stride_head between heads, stride_b and stride_c unused. K/V rows past
- * kv_len, and pages past the last one used, may hold anything. out must not
- * alias q or the cache. workspace: bd_paged_attn_workspace bytes, 256-byte aligned;
+ * kv_len, and pages past the last one used, may hold anything; so may cached rows that
+ * a new row does not see: an infinity or a NaN there reaches the rows that see it only.
+ * out must not alias q or the cache. workspace: bd_paged_attn_workspace bytes, 256-byte aligned;
  * it needs no clearing and holds nothing between calls. */
 BD_API int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q,
                              const bd_paged_cache* cache, bd_tensor* out, bd_rowstat* lse, void* workspace,

@@ -147,6 +147,57 @@ def test_nan_in_the_cache_reaches_those_who_see_it_only(fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,Hkv,d,new,kv", [(8, 2, 64, 4, 100), (8, 2, 128, 4, 100), (8, 2, 256, 4, 100), (8, 2, 128, 8, 70),
+                                            (8, 2, 256, 8, 70), (8, 2, 128, 3, 3000), (8, 2, 64, 150, 400),
+                                            (8, 2, 128, 150, 400), (8, 2, 256, 150, 400), (2, 2, 128, 300, 300),
+                                            (2, 2, 64, 300, 290), (8, 2, 128, 70, 9001), (8, 2, 256, 40, 5000)])
+def test_rows_take_nothing_from_keys_they_do_not_see(H, Hkv, d, new, kv, fmt):
+    """Infinities and NaN in cached rows of the step itself reach the new rows that see
+    them, in the columns they are in, and no others."""
+    c = pu.Case([new], [kv], H, Hkv, d, fmt=fmt, page=32, seed=new)
+    first = kv - new  # position of new row 0
+    spots = sorted({max(0, first + new // 2), max(0, first + 1), kv - 1})
+    bad = torch.zeros(new, d, dtype=torch.bool)  # of K/V head 0
+    for n, pos in enumerate(spots):
+        page, row = c.pages[0][pos // 32], pos % 32
+        if fmt == "bf16":
+            for col, x in ((7 + n, float("nan")), (d // 2 + n, float("inf")), (d - 9 + n, float("-inf"))):
+                c.v[page, row, 0, col] = x
+                c.vd[page, row, 0, col] = 0
+                bad[pos - first:, col] = True
+        else:
+            c.v.view(torch.uint8)[page, row, 0] = 0x7f
+            c.ve[page, row, 0] = 255
+            c.vd[page, row, 0] = 0
+            bad[pos - first:] = True
+    out, lse = pu.run_attention(c)
+    G = H // Hkv
+    o, l, A, big = op.attention(c.q[:new], *c.rows(0), kv)
+    to, tl = pu.tolerances(d, kv, A, big, fmt, new * G)
+    hit = torch.zeros(new, H, d, dtype=torch.bool)
+    hit[:, :G] = bad[:, None]
+    assert not torch.isfinite(out[hit]).any()
+    assert torch.isfinite(out[~hit]).all()
+    assert ((out.double() - o).abs() <= to)[~hit].all()
+    seen = ~torch.isneginf(l)
+    assert torch.equal(~torch.isneginf(lse), seen) and ((lse.double() - l).abs() <= tl)[seen].all()
+    # a K row of NaN
+    page, row = c.pages[0][spots[1] // 32], spots[1] % 32
+    if fmt == "bf16":
+        c.k[page, row, 0, 3] = float("nan")
+    else:
+        c.ke[page, row, 0] = 255
+    out2, lse2 = pu.run_attention(c)
+    rows = torch.zeros(new, dtype=torch.bool)
+    rows[spots[1] - first:] = True
+    assert torch.isnan(lse2[:G, rows]).all() and torch.isnan(out2[rows, :G]).all()
+    assert torch.equal(lse2[:G, ~rows], lse[:G, ~rows]) and torch.equal(lse2[G:], lse[G:])
+    assert torch.equal(out2[:, G:], out[:, G:])
+    a, b = out2[~rows, :G], out[~rows, :G]
+    assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(a.nan_to_num(1.0), b.nan_to_num(1.0))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("H,Hkv,d", HEADS)
 def test_chunk_over_a_long_context_is_split_and_joined(H, Hkv, d, fmt):
     """Few blocks of tiles: their keys are cut over the SMs; at G = 3 a tile has idle rows."""
