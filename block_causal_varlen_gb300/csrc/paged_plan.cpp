@@ -319,6 +319,8 @@ int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npage
                     D->num_pages);
     *T += q; *kv += n; *npages += used;
   }
+  // (the read back counts groups of 8 rows of pages, also of pages used in part)
+  if (*npages > INT32_MAX / (D->page_size / 8)) return fail(BD_ERR_CAPACITY, "pages in use times page_size past 2^34");
   if (*T > INT32_MAX / D->H || *kv > INT32_MAX) return fail(BD_ERR_CAPACITY, "new rows times H, or cached rows, past 2^31 - 1");
   return BD_OK;
 }

@@ -78,6 +78,12 @@ def _ints(x, name):
     return np.ascontiguousarray(a, dtype=np.int32)
 
 
+def _int(x, name):
+    if np.ndim(x) != 0:
+        raise ValueError(f"{name}: expected one number")
+    return int(_ints(x, name)[0])
+
+
 class PagedPlan:
     """Host plan blob of one step over a paged cache, and its device copy.
 
@@ -87,6 +93,8 @@ class PagedPlan:
 
     def __init__(self, q_len, kv_len, pages, H, Hkv, d, page_size, num_pages, fmt=BD_CACHE_BF16, causal=True):
         q, kv = _ints(q_len, "q_len"), _ints(kv_len, "kv_len")
+        H, Hkv, d, fmt = _int(H, "H"), _int(Hkv, "Hkv"), _int(d, "d"), _int(fmt, "fmt")
+        page_size, num_pages = _int(page_size, "page_size"), _int(num_pages, "num_pages")
         if q.ndim != 1 or q.shape != kv.shape or len(pages) != len(q):
             raise ValueError("q_len, kv_len and pages must have one entry per sequence")
         if isinstance(pages, np.ndarray) and pages.ndim == 2:
@@ -112,7 +120,7 @@ class PagedPlan:
         self.host = self.host[:int(self.host[2])]       # the words in use (csrc/paged_plan.h: PH_WORDS)
         self._host_ptr = self.host.ctypes.data
         self.dev = self._dev_ptr = None
-        self._index = -1
+        self._index, self._own = -1, False
         ws = C.c_size_t()
         check(load().bd_paged_attn_workspace(self._host_ptr, C.byref(ws)))
         self._workspace = ws.value
@@ -137,9 +145,9 @@ class PagedPlan:
                 raise TypeError("buffer: expected a contiguous 1-D int32 CUDA tensor")
             if buffer.numel() < src.numel():
                 raise ValueError(f"buffer of {buffer.numel()} words, the plan has {src.numel()}")
-            self.dev = buffer[:src.numel()]
-        elif self.dev is None or self.dev.device != torch.device(device):
-            self.dev = torch.empty_like(src, device=device)
+            self.dev, self._own = buffer[:src.numel()], False
+        elif not self._own or self.dev.device != torch.device(device):
+            self.dev, self._own = torch.empty_like(src, device=device), True
         self.dev.copy_(src, non_blocking=non_blocking)
         self._dev_ptr, self._index = self.dev.data_ptr(), self.dev.get_device()
         return self
@@ -243,9 +251,8 @@ def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspac
         tl = bd_rowstat(lse.data_ptr(), 0, 0, lse.stride(0))
     wp, wn = None, 0
     if workspace is None and plan._workspace:
-        workspace = torch.empty(plan._workspace, dtype=torch.uint8, device=plan.dev.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        with torch.cuda.stream(stream):      # memory of the stream that uses it
+            workspace = torch.empty(plan._workspace, dtype=torch.uint8, device=plan.dev.device)
     if workspace is not None:
         if workspace.get_device() != idx:
             raise ValueError(f"workspace: on {workspace.device}, the plan was uploaded to cuda:{idx}")
@@ -256,8 +263,13 @@ def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspac
 
 
 def paged_attn(plan: PagedPlan, q, cache: PagedCache, stream=None):
-    """Allocate O and LSE and run bd_paged_attn; returns (out, lse)."""
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(plan.H, q.shape[0], dtype=torch.float32, device=q.device)
+    """Allocate O and LSE and run bd_paged_attn; returns (out, lse). Rows past the new ones
+    are not written."""
+    with torch.cuda.stream(stream):      # memory of the stream that writes it
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(plan.H, q.shape[0], dtype=torch.float32, device=q.device)
+    if stream is not None:
+        for t in (out, lse):             # and of the caller's, which reads it
+            t.record_stream(torch.cuda.current_stream(q.device))
     bd_paged_attn(plan, q, cache, out, lse, stream=stream)
     return out, lse

@@ -350,6 +350,92 @@ def test_captured_step_replays_with_the_next_steps_plan():
             assert ((out[b:b + 1].cpu().double() - o).abs() <= to).all() and ((lse[:, b:b + 1].cpu().double() - l).abs() <= tl).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+def test_captured_layers_replay_with_tiles_and_few_rows(fmt):
+    """Two layers' writes and attention (few-rows blocks, tiles and both joins) in one graph,
+    on one workspace, replayed over other lengths of the same key: the bits of eager calls."""
+    H, Hkv, d, P, pages = 8, 2, 128, 32, [list(range(0, 300)), list(range(300, 600)), list(range(600, 700))]
+    g = torch.Generator().manual_seed(5)
+
+    def pool():
+        x = [torch.randn(700, P, Hkv, d, generator=g).bfloat16() for _ in range(2)]
+        if fmt == "bf16":
+            return bd.PagedCache(*[t.cuda() for t in x])
+        (kc, ke), (vc, ve) = op.quantise(x[0]), op.quantise(x[1])
+        return bd.PagedCache(*[t.cuda().view(torch.float8_e4m3fn) for t in (kc, vc)], ke.cuda(), ve.cuda())
+
+    layers = [pool() for _ in range(2)]
+
+    def plan_of(new, kv):
+        return bd.PagedPlan(new, kv, pages, H, Hkv, d, page_size=P, num_pages=700, fmt=layers[0].fmt)
+
+    steps = [([70, 1, 3], [9001, 8000, 900]), ([50, 3, 1], [7000, 9500, 3]), ([90, 1, 4], [9600, 6000, 1000])]
+    plans = [plan_of(*s) for s in steps]
+    assert len({p.key() for p in plans}) == 1
+    buf = torch.zeros(max(p.nbytes for p in plans) // 4, dtype=torch.int32, device="cuda")
+    ws = torch.empty(bd.bd_paged_attn_workspace(plans[0]), dtype=torch.uint8, device="cuda")
+    q, kn, vn = (torch.randn(2, 100, h, d, generator=g).bfloat16().cuda() for h in (H, Hkv, Hkv))
+    out = torch.zeros(2, 100, H, d, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros(2, H, 100, device="cuda")
+
+    def step(plan):
+        for i, c in enumerate(layers):
+            bd.bd_cache_write(plan, kn[i], vn[i], c)
+            bd.bd_paged_attn(plan, q[i], c, out[i], lse[i], ws)
+
+    want = []
+    for p in plans + plans:  # (rows one step writes are others' context: they are there the second time)
+        out.fill_(7)
+        lse.fill_(7)
+        step(p.upload("cuda"))
+        want.append((out.clone(), lse.clone()))
+    want = want[3:]
+    torch.cuda.synchronize()
+    plans[0].upload(buffer=buf)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(plans[0])
+    for i in (1, 2, 0):
+        plans[i].upload(buffer=buf)
+        out.fill_(7)
+        lse.fill_(7)
+        graph.replay()
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+        bd.bd_check_status(plans[i])
+
+
+def test_upload_leaves_another_plans_buffer_alone():
+    """A plan once uploaded into a shared buffer takes memory of its own the next time."""
+    a, b = (bd.PagedPlan([1], [n], [[0, 1, 2]], 4, 2, 64, page_size=16, num_pages=3) for n in (20, 40))
+    buf = torch.zeros(max(a.nbytes, b.nbytes) // 4, dtype=torch.int32, device="cuda")
+    a.upload(buffer=buf)
+    b.upload(buffer=buf)
+    a.upload("cuda:0")
+    assert torch.equal(buf[:len(b.host)].cpu(), torch.from_numpy(b.host))
+    assert torch.equal(a.dev.cpu(), torch.from_numpy(a.host))
+    own = a.dev.data_ptr()
+    assert a.upload("cuda:0").dev.data_ptr() == own  # and keeps that
+
+
+def test_memory_allocated_for_a_call_is_its_streams():
+    """Results and workspace allocated by a call on a stream argument are not memory the
+    caller's stream still works on."""
+    c = _mixed()
+    want = pu.run_attention(c)
+    q, s = c.q.cuda(), torch.cuda.Stream()
+    n = 1 << 28
+    bd.paged_attn(c.plan, q, c.cache, stream=s)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    x = torch.ones(n, device="cuda")
+    for _ in range(20):  # work in flight on the caller's stream, its memory given back
+        x = x * 1.5
+    x = None
+    got = bd.paged_attn(c.plan, q, c.cache, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(got[0].cpu(), want[0]) and torch.equal(got[1].cpu(), want[1])
+
+
 def test_nothing_new_and_nothing_cached():
     c = pu.Case([0, 0], [20, 0], 8, 2, 128)
     out = torch.full((1, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")

@@ -354,6 +354,15 @@ def test_lengths_and_pages_are_whole_numbers_in_range():
     assert np.array_equal(a.host, b.host)
 
 
+@pytest.mark.parametrize("name", ["H", "Hkv", "d", "page_size", "num_pages", "fmt"])
+def test_sizes_are_whole_numbers_in_range(name):
+    a = dict(H=8, Hkv=2, d=128, page_size=16, num_pages=4, fmt=0)
+    bd.PagedPlan([1], [17], [[0, 1]], **{**a, name: np.int64(a[name])})
+    for bad in (a[name] + 2 ** 32, a[name] + 0.5, [a[name]]):
+        with pytest.raises(ValueError, match=name):
+            bd.PagedPlan([1], [17], [[0, 1]], **{**a, name: bad})
+
+
 def test_no_lengths_past_the_kernels_arithmetic():
     """A page may be listed again and again: kv_len is bounded by itself, not by the pool."""
     n = 2 ** 31 - 1
