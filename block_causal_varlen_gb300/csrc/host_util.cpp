@@ -103,7 +103,7 @@ int32_t make_tmap_group_bf16(CUtensorMap* map, const bd_tensor* t, int64_t heads
 }
 
 int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int64_t heads, int64_t d, int esize,
-                        const char* name, int box_rows, int box_pieces) {
+                        const char* name, int box_rows, int box_pieces, bool neighbours) {
   auto fn = encode_fn();
   if (!fn) return fail(BD_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (no CUDA driver?)");
   const int64_t row_bytes = d * esize, piece = row_bytes < 128 ? row_bytes : 128;
@@ -115,12 +115,14 @@ int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int
   cuuint64_t strides[4] = {cuuint64_t(sr), cuuint64_t(piece), cuuint64_t(sh), cuuint64_t(sp)};
   cuuint32_t box[5] = {cuuint32_t(piece / esize), cuuint32_t(box_rows), cuuint32_t(box_pieces), 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  // no promotion past a row's piece: with rows of several heads side by side it would
-  // fetch the neighbouring heads' bytes, for other SMs at other times
+  // without neighbours no promotion past a row's piece: with rows of several heads side by
+  // side it would fetch the neighbouring heads' bytes, for other SMs at other times
   CUresult r = fn(map, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, t->ptr, dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   piece == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                  piece == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  neighbours ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                  : piece == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(BD_ERR_ALIGN, "%s: cuTensorMapEncodeTiled failed (%d)", name, int(r));
   return BD_OK;
 }

@@ -914,10 +914,12 @@ int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& 
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
   const int es = Cfg::kF8 ? 1 : 2, rows = w[PH_PAGE] < Cfg::kChunk ? w[PH_PAGE] : Cfg::kChunk;
+  // (256-byte promotion where heads go in gangs: 64 ragged sequences of 32 e4m3 heads 370 -> 349 us)
+  const bool near = gang_of(w[PH_HKV]) > 1;
   CUtensorMap mk, mv;
   int32_t st;
-  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, 1))) return st;
-  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, 1))) return st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, 1, near))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, 1, near))) return st;
   const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB>, kDecCtas, Cfg::kThreads, Cfg::kSmem, behind, s, mk, mv, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
 }

@@ -29,6 +29,14 @@ constexpr int tile_slot_rows(int d) { return 128 * tile_slots(d); }
 // At most this many partial results of a kind: the workspace's size.
 constexpr int kDecSlots = 2 * kDecCtas, kTilePartSlots = 2 * kTileCtas;
 
+// K/V heads whose few-rows CTAs walk the same keys side by side: all of them, or the most
+// that leave no more than 1 in 64 CTAs over.
+constexpr int gang_of(int hkv) {
+  for (int g = hkv < kDecCtas ? hkv : kDecCtas; g > 1; --g)
+    if (hkv % g == 0 && kDecCtas % g * 64 <= kDecCtas) return g;
+  return 1;
+}
+
 // header words (the failure status keeps the place it has in attention plans, so
 // that bd_check_status reads either)
 enum : int {

@@ -112,6 +112,24 @@ def test_work_is_spread_evenly():
         assert max(load) <= sum(load) / len(ctas) + 8, (max(load), sum(load) / len(ctas))
 
 
+@pytest.mark.parametrize("Hkv,gang", [(1, 1), (3, 3), (7, 7), (10, 10), (24, 12), (29, 1), (32, 16), (64, 16), (128, 16), (320, 20)])
+def test_heads_go_in_gangs(Hkv, gang):
+    """Any number of K/V heads: everything is covered, at most 4 CTAs are left over, and a
+    gang's CTAs have the same blocks and keys of neighbouring heads."""
+    new, kv = [1, 2, 0, 1, 1], [3000, 47, 5, 1, 900]
+    for causal in (True, False):
+        test_every_row_meets_every_key_once(new, kv, causal, Hkv, Hkv)
+    plan, _ = make(new, kv, Hkv, Hkv)
+    ctas, _ = lists(plan, "DEC")
+    assert 304 % gang <= 4
+    for c in range(0, 304 - 304 % gang, gang):
+        for g in range(1, gang):
+            a, b = ([{k: v for k, v in p.items() if k not in ("HKV", "SLOT")} for p in ctas[c + i]] for i in (0, g))
+            assert a == b and [p["HKV"] + g for p in ctas[c]] == [p["HKV"] for p in ctas[c + g]]
+    load = [sum(-(-(p["K1"] - p["K0"]) // 32) + 8 for p in c) for c in ctas]
+    assert max(load) <= sum(load) / (304 - 304 % gang) + 10
+
+
 def test_tiles_are_cut_only_where_it_helps():
     """Many equal blocks are given out whole; a few long ones are spread over the SMs."""
     plan, _ = make([64] * 152, [64] * 152, 8, 2)
