@@ -54,11 +54,16 @@ struct TileCfg {
   static constexpr int kOffK = kOffQ + kSlots * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
   static constexpr int kOffRaw = kOffV + kStages * kTileBytes;
-  // results leave TMEM through 4 KB of shared memory per softmax warp; where none is
-  // left, through the slot's Q tile, which then is free only after the results are out
+  // Results leave in 128-byte pieces of rows that 8 lanes turn into stores of whole pieces:
+  // in registers, or through 4 KB of shared memory per softmax warp; e4m3 has none left
+  // for that and takes the slot's Q tile, which then is free only after the results are
+  // out. 4096 rows over 16384 (10 ragged sequences for e4m3) in registers and through
+  // shared memory: bf16 d 64 624 and 590 us, d 128 650 and 672, d 256 1856 and 1872; e4m3
+  // d 128 274 and 272.
+  static constexpr bool kTurnInRegs = !kF8 && D >= 128;
   static constexpr bool kStageInQ = kF8 && D >= 128;
   static constexpr int kOffStage = kOffRaw + kRawStages * kRawBytes;
-  static constexpr int kOffBar = kOffStage + (kStageInQ ? 0 : kSlots * 16384);
+  static constexpr int kOffBar = kOffStage + (kStageInQ || kTurnInRegs ? 0 : kSlots * 16384);
   static constexpr int kOffPieces = kOffBar + 512;
   static constexpr int kPre = 16;                 // pieces kept in shared memory
   static constexpr int kSmem = kOffPieces + kPre * kPieceWords * 4 + 1024;  // + alignment slack
@@ -223,9 +228,6 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       for (int p = p0; p < p1 && ok; ++p) {
         const Piece P = piece(p);
         if (P.nt == 0) continue;
-        // Q follows the first key tiles: their stages were the block before's, the Q tiles
-        // may be in use until its results are out
-        const int q_after = min(NST, P.nt) - 1;
         auto load_q = [&]() -> bool {
           if (!__all_sync(0xffffffffu, mbar_wait(bar(T_QEMPTY), (qi & 1) ^ 1, abort_flag))) return false;
           if (lane == 0) {
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             }
             if (!ok) break;
           }
-          if (j == q_after && !(ok = load_q())) break;
+          if (j == 0 && !(ok = load_q())) break;
           page = next;
         }
       }
@@ -601,28 +603,49 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         a.lse[int64_t(h) * a.l_sh + P.q0 + t] =
             l_run == 0.f ? -CUDART_INF_F : (m_fin + lg2(l_run)) * 0.69314718055994531f;
       }
-      // Rows leave in 128-byte pieces (64 columns of bf16, 32 of a partial result): the
-      // warp's 32 pieces go to its staging box (16-byte part c of row x at c ^ (x & 7)),
-      // from where 8 lanes store each row's piece. Rows stored by a thread each (32 rows
-      // in every store) held the load/store unit some 9000 cycles a block.
-      const uint32_t box = (Cfg::kStageInQ ? sQ + s * Cfg::kTileBytes : sbase + Cfg::kOffStage + s * 16384) + quarter * 4096;
+      // Rows leave in 128-byte pieces (64 columns of bf16, 32 of a partial result), 8 lanes
+      // storing a piece. (Rows stored by a thread each, 32 rows in every store, held the
+      // load/store unit some 9000 cycles a block.)
       const int64_t off = !live ? -1 : part ? int64_t(s * 128 + r) * D * 4 : (int64_t(P.q0 + t) * a.o_sr + int64_t(h) * a.o_sh) * 2;
       uint8_t* const dst = part ? reinterpret_cast<uint8_t*>(part + 2 * tile_slot_rows(D)) : reinterpret_cast<uint8_t*>(a.o);
-      auto put = [&](int c, uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
-        st_shared_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4), w0, w1, w2, w3);
-      };
-      auto send = [&](int byte) {  // the box, to bytes [byte, byte + 128) of the rows
-        __syncwarp();
+      auto send = [&](uint32_t (&w)[32], int byte) {  // this row's bytes [byte, byte + 128)
+        if constexpr (Cfg::kTurnInRegs) {
+          // 8 lanes swap 16-byte parts until each has one part of all 8 rows
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int x = 4 * i + (lane >> 3);
-          const int64_t o = __shfl_sync(0xffffffffu, off, x);
-          const uint4 v = ld_shared_u4(box + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
-          if (o >= 0) *reinterpret_cast<uint4*>(dst + o + byte + (lane & 7) * 16) = v;
+          for (int b = 1; b < 8; b <<= 1) {
+            const bool up = (lane & b) != 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if ((i >> 2) & b) continue;
+              const uint32_t x = __shfl_xor_sync(0xffffffffu, up ? w[i] : w[i + 4 * b], b);
+              w[i] = up ? x : w[i];
+              w[i + 4 * b] = up ? w[i + 4 * b] : x;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int64_t o = __shfl_sync(0xffffffffu, off, (lane & 24) + i);
+            if (o >= 0)
+              *reinterpret_cast<uint4*>(dst + o + byte + (lane & 7) * 16) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
+        } else {
+          // part c of row x at c ^ (x & 7) of the warp's box
+          const uint32_t box = (Cfg::kStageInQ ? sQ + s * Cfg::kTileBytes : sbase + Cfg::kOffStage + s * 16384) + quarter * 4096;
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            st_shared_v4(box + lane * 128 + ((c ^ (lane & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int x = 4 * i + (lane >> 3);
+            const int64_t o = __shfl_sync(0xffffffffu, off, x);
+            const uint4 v = ld_shared_u4(box + x * 128 + (((lane & 7) ^ (x & 7)) << 4));
+            if (o >= 0) *reinterpret_cast<uint4*>(dst + o + byte + (lane & 7) * 16) = v;
+          }
+          __syncwarp();
         }
-        __syncwarp();
       };
-      constexpr int QH = D <= 128 ? D / 32 : 1;  // 32-column groups taken out of TMEM at a time
+      constexpr int QH = Cfg::kTurnInRegs || D == 256 ? 2 : D / 32;  // 32-column groups taken out of TMEM at a time
 #pragma unroll 1
       for (int q0 = 0; q0 < D / 32; q0 += QH) {
         __syncwarp();
@@ -642,23 +665,17 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         __syncwarp();
         if (part) {
 #pragma unroll
-          for (int q = 0; q < QH; ++q) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) put(c, ov[q][4 * c], ov[q][4 * c + 1], ov[q][4 * c + 2], ov[q][4 * c + 3]);
-            send((q0 + q) * 128);
-          }
+          for (int q = 0; q < QH; ++q) send(ov[q], (q0 + q) * 128);
         } else {
 #pragma unroll
-          for (int q = 0; q < QH; ++q) {
+          for (int q = 0; q < QH; q += 2) {
+            uint32_t w[32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16(__uint_as_float(ov[q][8 * c + 2 * e]) * inv, __uint_as_float(ov[q][8 * c + 2 * e + 1]) * inv);
-              put(((q0 + q) & 1) * 4 + c, w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 32; ++e) {
+              const uint32_t (&x)[32] = ov[q + (e >> 4)];
+              w[e] = pack_bf16(__uint_as_float(x[2 * (e & 15)]) * inv, __uint_as_float(x[2 * (e & 15) + 1]) * inv);
             }
-            if ((q0 + q) & 1) send((q0 + q) / 2 * 128);
+            send(w, (q0 + q) * 64);
           }
         }
       }
