@@ -79,6 +79,8 @@ def _ints(x, name):
 
 
 def _int(x, name):
+    if type(x) is int and 0 <= x < 2 ** 31:
+        return x
     if np.ndim(x) != 0:
         raise ValueError(f"{name}: expected one number")
     return int(_ints(x, name)[0])
@@ -101,9 +103,10 @@ class PagedPlan:
             flat = _ints(pages, "pages").reshape(-1)
             offs = np.arange(len(q) + 1, dtype=np.int64) * pages.shape[1]
         else:
-            lists = [_ints(x, "pages").reshape(-1) for x in pages]
-            flat = np.concatenate(lists) if lists else np.zeros(0, np.int32)
-            offs = np.cumsum([0] + [len(x) for x in lists])
+            lists = [np.asarray(x).reshape(-1) for x in pages]
+            offs = np.cumsum([0] + [x.size for x in lists])
+            some = [x for x in lists if x.size]
+            flat = _ints(np.concatenate(some) if some else (), "pages")
         if offs[-1] >= 2 ** 31:
             raise ValueError("page lists of more than 2^31 entries")
         offs = np.ascontiguousarray(offs, dtype=np.int32)
