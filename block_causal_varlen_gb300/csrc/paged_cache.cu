@@ -10,7 +10,10 @@
 //
 // Both kernels are streams: what bounds them is HBM (or, for a few rows, the
 // launch). A thread takes 16 bytes of bf16 (8 values) of K and of V, so a head's
-// row is d / 8 neighbouring lanes and its maximum a few shuffles.
+// row is d / 8 neighbouring lanes and its maximum a few shuffles. 30000 rows of 8 heads of
+// 128 written: bf16 37.5 us (6607 GB/s), e4m3 33.4 (5577); 49152 read back: bf16 62.1
+// (6483), e4m3 53.9 (5615). Walking the rows without a division each, or scaling bf16
+// pairs at once, changes nothing.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -267,7 +270,9 @@ extern "C" int32_t bd_cache_write(const void* plan_host, const void* plan_dev, c
     return fail(BD_ERR_ARG, "k/v rows %d/%d < %d new rows of the plan", k->rows, v->rows, w[PH_T]);
   const CacheArgs a = cache_args(plan_dev, cache, k, v);
   const int64_t blocks = (int64_t(w[PH_T]) * w[PH_HKV] * (w[PH_D] / 8) + kThreads - 1) / kThreads;
-  const int grid = int(blocks < kPagedSms * 8 ? blocks : kPagedSms * 8);
+  // three rounds of 8 CTAs an SM: 30000 / 100000 e4m3 rows of 8 heads 33.4 / 93-95 us, with
+  // one round 35.5 / 97-99, with two 33.4 / 97
+  const int grid = int(blocks < kPagedSms * 24 ? blocks : kPagedSms * 24);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cache->fmt == BD_CACHE_BF16) launch_write<BD_CACHE_BF16>(w[PH_D], grid, s, a);
   else launch_write<BD_CACHE_E4M3>(w[PH_D], grid, s, a);

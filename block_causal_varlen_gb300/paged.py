@@ -11,12 +11,13 @@ Tensor layouts (all strided views are accepted; the head dim is contiguous):
 from __future__ import annotations
 
 import ctypes as C
+import struct
 
 import numpy as np
 import torch
 
 from . import _abi
-from ._abi import BD_CACHE_BF16, BD_CACHE_E4M3, bd_paged_cache, bd_paged_desc, bd_rowstat, bd_tensor, check, load
+from ._abi import BD_CACHE_BF16, BD_CACHE_E4M3, bd_paged_cache, bd_paged_desc, bd_tensor, check, load
 
 __all__ = ["PagedCache", "PagedPlan", "bd_paged_plan_bytes", "bd_paged_plan_build", "bd_paged_plan_key",
            "bd_cache_write", "bd_cache_read", "bd_paged_attn_workspace", "bd_paged_attn", "paged_attn",
@@ -67,6 +68,7 @@ class PagedCache:
         es = k_exp.stride() if k_exp is not None else (0, 0, 0)
         ep = [t.data_ptr() if t is not None else None for t in (k_exp, v_exp)]
         self._c = bd_paged_cache(st[0], st[1], ep[0], ep[1], es[0], es[1], es[2], self.fmt, self.num_pages)
+        self._addr = C.addressof(self._c)
         self._index = k.get_device()
 
 
@@ -176,6 +178,24 @@ def bd_paged_attn_workspace(plan: PagedPlan) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
+# The device calls take their structs as packed bytes and every pointer as an address: half
+# the binding's cost of a small call otherwise goes into ctypes structures.
+_tensor = struct.Struct("PqqqqiI").pack        # bd_tensor
+_rowstat = struct.Struct("Pqqq").pack          # bd_rowstat
+_entries = {}
+
+
+def _entry(name):
+    f = _entries.get(name)
+    if f is None:
+        lib = load()
+        f = lib[name]  # a function object of its own
+        args = getattr(lib, name).argtypes
+        f.restype, f.argtypes = C.c_int32, [C.c_size_t if a is C.c_size_t else C.c_void_p for a in args]
+        _entries[name] = f
+    return f
+
+
 def _refuse(t, name, dtype, idx):
     """Says what is wrong with a tensor's type or place."""
     if t.dtype != dtype:
@@ -186,7 +206,7 @@ def _refuse(t, name, dtype, idx):
 
 
 def _rows3(t, name, heads, d, rows, idx):
-    """A packed [rows, heads, d] bf16 tensor as the ABI's strided tensor. The C ABI
+    """A packed [rows, heads, d] bf16 tensor as the ABI's strided tensor (its bytes). The C ABI
     carries neither dtypes nor head counts, so they are checked here."""
     if t.dtype is not torch.bfloat16 or t.get_device() != idx or idx < 0:
         _refuse(t, name, torch.bfloat16, idx)
@@ -196,7 +216,7 @@ def _rows3(t, name, heads, d, rows, idx):
     st = t.stride()
     if st[2] != 1:
         raise ValueError(f"{name}: head dim must be contiguous")
-    return bd_tensor(t.data_ptr(), 0, 0, st[0], st[1], s[0], 0)
+    return _tensor(t.data_ptr(), 0, 0, st[0], st[1], s[0], 0)
 
 
 def _device(plan, cache):
@@ -227,7 +247,7 @@ def bd_cache_write(plan: PagedPlan, k, v, cache: PagedCache, stream=None):
     idx = _device(plan, cache)
     tk = _rows3(k, "k", plan.Hkv, plan.d, plan.T, idx)
     tv = _rows3(v, "v", plan.Hkv, plan.d, plan.T, idx)
-    _call(load().bd_cache_write, idx, stream, plan._host_ptr, plan._dev_ptr, tk, tv, cache._c)
+    _call(_entry("bd_cache_write"), idx, stream, plan._host_ptr, plan._dev_ptr, tk, tv, cache._addr)
 
 
 def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
@@ -235,7 +255,7 @@ def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
     idx = _device(plan, cache)
     tk = _rows3(k, "k", plan.Hkv, plan.d, plan.kv_total, idx)
     tv = _rows3(v, "v", plan.Hkv, plan.d, plan.kv_total, idx)
-    _call(load().bd_cache_read, idx, stream, plan._host_ptr, plan._dev_ptr, cache._c, tk, tv)
+    _call(_entry("bd_cache_read"), idx, stream, plan._host_ptr, plan._dev_ptr, cache._addr, tk, tv)
 
 
 def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspace=None, stream=None):
@@ -251,7 +271,7 @@ def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspac
         s = lse.shape
         if len(s) != 2 or s[0] != plan.H or s[1] < plan.T or lse.stride(1) != 1:
             raise ValueError(f"lse: expected [{plan.H}, {plan.T} or more] with rows contiguous, got {tuple(s)}")
-        tl = bd_rowstat(lse.data_ptr(), 0, 0, lse.stride(0))
+        tl = _rowstat(lse.data_ptr(), 0, 0, lse.stride(0))
     wp, wn = None, 0
     if workspace is None and plan._workspace:
         with torch.cuda.stream(stream):      # memory of the stream that uses it
@@ -262,7 +282,7 @@ def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspac
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(load().bd_paged_attn, idx, stream, plan._host_ptr, plan._dev_ptr, tq, cache._c, to, tl, wp, wn)
+    _call(_entry("bd_paged_attn"), idx, stream, plan._host_ptr, plan._dev_ptr, tq, cache._addr, to, tl, wp, wn)
 
 
 def paged_attn(plan: PagedPlan, q, cache: PagedCache, stream=None):
