@@ -72,11 +72,11 @@ struct DecCfg {
   static constexpr int kCols = D == 64 ? 32 : 64, kPitch = kCols + 4, kSumFloats = 8 * kPitch;
   static constexpr int kXchg = kSplit == 2 ? kChunk / 16 * NB * 512 : 0;  // a warp's scores
   static constexpr int kSumBytes = kWarps * (kSumFloats * 4 > 2 * kXchg ? kSumFloats * 4 : 2 * kXchg);
-  // ring depth: up to 192 KB of chunks per SM and its two CTAs (some 45 KB must be in
-  // flight to cover HBM's latency at its rate)
-  static constexpr int kPerStage = kWarps * (kStageBytes + 8 + (kF8 ? 9 * kChunk : 0));
-  static constexpr int kRest = kSumBytes + kWarps * 8 * NB * 8 + 8 * NB * 12 + 16 + 1024;
-  static constexpr int kStages = (115712 - kRest) / kPerStage < 6 ? (115712 - kRest) / kPerStage : 6;
+  // ring depth: 64 KB of chunks a CTA. (Some 45 KB per SM must be in flight to cover HBM's
+  // latency at its rate. More than 128 spreads the SMs' reads over too many pages of HBM:
+  // with 96 KB a CTA 64 ragged bf16 sequences took 175 us, 166.5 now; 32 e4m3 heads 352
+  // and 339, bf16 d 64 94 and 91.)
+  static constexpr int kStages = 65536 / (kWarps * kStageBytes);
   static_assert(kStages >= 2, "a ring of two chunks at least");
   static constexpr int kOffRing = 0;
   static constexpr int kOffSum = kOffRing + kWarps * kStages * kStageBytes;
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
             const float4 u = *reinterpret_cast<const float4*>(&sum[(w * PW + hs) * Cfg::kSumFloats + r * Cfg::kPitch + c]);
             t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
           }
-          const int col = hs * DW + (F8 ? (c / W) * 2 * W + rd * W + c % W : rd * Cfg::kCols + c);
+          const int col = hs * DW + (F8 ? (c / W) * (DW / 8) + rd * W + c % W : rd * Cfg::kCols + c);
           if (part) {
             *reinterpret_cast<float4*>(part + 2 * kDecSlotRows + (8 * b + r) * D + col) = t;
           } else {
@@ -944,7 +944,7 @@ int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream
   const Kernel k = tile   ? pick(bd_paged_tile_merge_kernel<64>, bd_paged_tile_merge_kernel<128>, bd_paged_tile_merge_kernel<256>)
                    : wide ? pick(bd_paged_wide_merge_kernel<64>, bd_paged_wide_merge_kernel<128>, bd_paged_wide_merge_kernel<256>)
                           : pick(bd_paged_merge_kernel<64>, bd_paged_merge_kernel<128>, bd_paged_merge_kernel<256>);
-  const cudaError_t e = launch_kernel(k, kPagedSms * (tile ? 8 : wide ? 4 : 2), 256, 0, true, s, a);
+  const cudaError_t e = launch_kernel(k, kPagedSms * (tile ? 8 : 4), 256, 0, true, s, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "paged join launch");
 }
 
