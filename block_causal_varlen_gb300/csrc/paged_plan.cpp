@@ -378,11 +378,12 @@ int32_t prepare(const bd_paged_desc* D, Built* X) {
     pg += (int64_t(D->kv_len[b]) + D->page_size - 1) / D->page_size;
     if (pg > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
   }
-  // Sequences of up to 32 (new row, head) pairs of a K/V head go to the few-rows kernel, in
-  // blocks of one size (a tile of 32 rows in use costs what one of 128 does). 16 sequences
-  // of 20000 rows, 32 pairs, d 128: bf16 257 us, as tiles 306; e4m3, two blocks of 16, 230,
-  // as tiles 346.
-  const int most = kDecMaxRows;
+  // Sequences of up to 32 (bf16) or 48 (e4m3) (new row, head) pairs of a K/V head go to the
+  // few-rows kernel, in blocks of one size (a tile of 32 rows in use costs what one of 128
+  // does). 16 sequences of 8000 rows, bf16 d 256, 32 pairs: 220 us, as tiles 253; d 128, 48
+  // pairs: 195 and 138; e4m3 d 128, 48 pairs in three blocks: 144, as tiles 167; 64 pairs of
+  // 300-8000 rows: 66 and 63.
+  const int most = dec_most_rows(D->fmt);
   int32_t widest = 1;
   for (int32_t b = 0; b < D->B; ++b)
     if (int64_t(D->q_len[b]) * G <= most) widest = std::max(widest, D->q_len[b] * G);

@@ -17,7 +17,7 @@ constexpr int kPagedSms = 152;
 constexpr int kDecCtas = 2 * kPagedSms, kTileCtas = kPagedSms;
 // A few-rows block has 8, 16 or (bf16: e4m3 lacks the registers) 24 or 32 (new row, query head)
 // pairs of one K/V head: the least that holds every sequence of the plan that goes there.
-constexpr int kDecMaxRows = 32;
+constexpr int dec_most_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 48; }  // of a sequence that goes there
 constexpr int dec_block_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 16; }
 constexpr int kDecSlotRows = 32;
 constexpr int kWideJoin = 16;  // parts of a block from which on its rows are joined by a CTA each

@@ -39,6 +39,15 @@ def test_few_rows(new, kv, H, Hkv, d, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new,kv", [([8, 9], [300, 1000]), ([12, 5, 13], [700, 33, 2000]), ([12], [9001])])
+def test_around_the_few_rows_limit(new, kv, d, fmt):
+    """32 (bf16) and 48 (e4m3) pairs of a K/V head, in several blocks, and one row more."""
+    c = pu.Case(new, kv, 8, 2, d, page=32, fmt=fmt, seed=d + len(new))
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 @pytest.mark.parametrize("H,Hkv,d", HEADS)
 def test_long_context_is_split_and_joined(H, Hkv, d, fmt):
     c = pu.Case([1], [6001], H, Hkv, d, page=64, fmt=fmt, seed=d)
