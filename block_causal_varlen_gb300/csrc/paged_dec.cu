@@ -944,7 +944,7 @@ int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream
   const Kernel k = tile   ? pick(bd_paged_tile_merge_kernel<64>, bd_paged_tile_merge_kernel<128>, bd_paged_tile_merge_kernel<256>)
                    : wide ? pick(bd_paged_wide_merge_kernel<64>, bd_paged_wide_merge_kernel<128>, bd_paged_wide_merge_kernel<256>)
                           : pick(bd_paged_merge_kernel<64>, bd_paged_merge_kernel<128>, bd_paged_merge_kernel<256>);
-  const cudaError_t e = launch_kernel(k, kPagedSms * (tile ? 8 : 4), 256, 0, true, s, a);
+  const cudaError_t e = launch_kernel(k, tile ? kPagedSms * 8 : kWideCtas, 256, 0, true, s, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "paged join launch");
 }
 

@@ -104,10 +104,10 @@ int64_t cut_evenly(const std::vector<Item>& items, int unit, int over, int ctas,
   return hi;
 }
 
-// Items of more than `most` units in equal parts, the longest part first to the CTA
+// Items of more than `most` units in equal parts, the longest part first to that of `num` CTAs
 // with the least; returns the longest load, or -1 if the parts of cut items are more
 // than there are slots.
-int64_t cut_longest(const std::vector<Item>& items, int unit, int over, int64_t most, std::vector<Part>* parts) {
+int64_t cut_longest(const std::vector<Item>& items, int unit, int over, int64_t most, int num, std::vector<Part>* parts) {
   parts->clear();
   int64_t split = 0;
   for (size_t i = 0; i < items.size(); ++i) {
@@ -119,7 +119,7 @@ int64_t cut_longest(const std::vector<Item>& items, int unit, int over, int64_t 
   std::stable_sort(parts->begin(), parts->end(), [](const Part& a, const Part& b) { return a.u1 - a.u0 > b.u1 - b.u0; });
   typedef std::pair<int64_t, int> Load;
   std::priority_queue<Load, std::vector<Load>, std::greater<Load>> ctas;
-  for (int c = 0; c < kTileCtas; ++c) ctas.push({0, c});
+  for (int c = 0; c < num; ++c) ctas.push({0, c});
   int64_t longest = 0;
   for (Part& p : *parts) {
     Load l = ctas.top();
@@ -222,8 +222,10 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
   }
 }
 
-// Few-rows blocks: short against their keys, cheap to join: always cut evenly. A
-// piece's own cost (its q, adding up the warps' results, the pipeline's start) is some
+// Few-rows blocks: short against their keys, cheap to join: cut evenly, unless whole blocks
+// take no more than a join does longer (8 units of 32 keys, 4 at head dim 256: one sequence
+// of 128 keys takes 4.5 us whole and 5.1 cut, of 256 keys 5.9 and 5.3, and a launch less on
+// the host). A piece's own cost (its q, adding up the warps' results, the pipeline's start) is some
 // 8 units of 32 keys (64 ragged e4m3 sequences of 32 heads: 352 us counting 6, 348 counting 8,
 // 351 counting 14). One head's blocks are cut into as many stretches as there are gangs
 // of CTAs, a CTA for each head: neighbouring CTAs then read neighbouring heads' parts
@@ -232,6 +234,8 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
 // -> 172).
 void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
                const std::vector<int32_t>& page_off, Lists* L) {
+  constexpr int kOver = 8;
+  const int join = D.d == 256 ? 4 : 8;
   std::vector<Part> parts;
   if (!items.empty()) {
     const int gang = gang_of(D.Hkv);
@@ -248,8 +252,9 @@ void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std
         }
       i += n * D.Hkv;
     }
-    std::vector<Part> first;
-    cut_evenly(lead, kDecUnit, 8, kDecCtas / gang, &first);
+    std::vector<Part> first, whole;
+    const int64_t even = cut_evenly(lead, kDecUnit, kOver, kDecCtas / gang, &first);
+    if (cut_longest(lead, kDecUnit, kOver, INT32_MAX, kDecCtas / gang, &whole) <= even + join) first.swap(whole);
     parts.reserve(first.size() * gang);
     for (size_t i = 0, j = 0; i < first.size(); i = j) {
       while (j < first.size() && first[j].cta == first[i].cta) ++j;
@@ -276,7 +281,7 @@ void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const st
     int64_t total = 0;
     for (const Item& it : items) total += units_of(it, kTile) + kOver;
     const int64_t share = (total + kTileCtas - 1) / kTileCtas;
-    int64_t least = cut_longest(items, kTile, kOver, INT32_MAX, &best);
+    int64_t least = cut_longest(items, kTile, kOver, INT32_MAX, kTileCtas, &best);
     std::vector<int32_t> count(items.size());
     auto joined = [&](const std::vector<Part>& v) {
       std::fill(count.begin(), count.end(), 0);
@@ -294,7 +299,7 @@ void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const st
     // (within 1.5% of an even share nothing is gained)
     const int64_t fine = share + share / 64;
     for (int k = 1; k <= 4 && least > fine; ++k) {
-      const int64_t t = cut_longest(items, kTile, kOver, std::max<int64_t>(1, share / k), &parts);
+      const int64_t t = cut_longest(items, kTile, kOver, std::max<int64_t>(1, share / k), kTileCtas, &parts);
       if (t < 0) break;
       better(t);
     }
@@ -516,8 +521,10 @@ static int32_t plan_build(const bd_paged_desc* desc, void* blob, size_t blob_byt
   };
   w[PH_DEC_ROWS] = X.dec_rows;
   w[PH_DEC_LIVE] = X.dec_live;
-  for (size_t i = 0; i < dec.merges.size(); i += kMergeWords)
-    if (dec.merges[i + MG_N] > kWideJoin) w[PH_DECM_WIDE] = 1;
+  int32_t most_parts = 0;
+  for (size_t i = 0; i < dec.merges.size(); i += kMergeWords) most_parts = std::max(most_parts, dec.merges[i + MG_N]);
+  const int64_t joined = int64_t(dec.merges.size() / kMergeWords) * X.dec_live;
+  w[PH_DECM_WIDE] = most_parts > kWideJoin || (most_parts > kWideJoinFew && joined <= kWideCtas);
   put(dec, PH_OFF_DEC, PH_NDEC, PH_NDECM, kOffDecRec, kOffDecMerge);
   put(tile, PH_OFF_TILE, PH_NTILE, PH_NTILEM, kOffTileRec, kOffTileMerge);
   return ok();

@@ -112,6 +112,14 @@ def test_work_is_spread_evenly():
         assert max(load) <= sum(load) / len(ctas) + 8, (max(load), sum(load) / len(ctas))
 
 
+def test_short_contexts_are_not_cut():
+    """Blocks that a CTA reads about as fast as a join takes stay whole: no join is launched."""
+    for new, kv, d, cut in (([1], [128], 128, False), ([1], [128], 256, False), ([1], [256], 256, True), ([1], [2000], 128, True),
+                            ([1] * 8, [200] * 8, 64, False), ([1, 1], [100, 5000], 128, True)):
+        plan, _ = make(new, kv, 32, 8, d)
+        assert (header(plan)["NDECM"] > 0) == cut, (kv, d)
+
+
 @pytest.mark.parametrize("Hkv,gang", [(1, 1), (3, 3), (7, 7), (10, 10), (24, 12), (29, 1), (32, 16), (64, 16), (128, 16), (320, 20)])
 def test_heads_go_in_gangs(Hkv, gang):
     """Any number of K/V heads: everything is covered, at most 4 CTAs are left over, and a
