@@ -90,6 +90,7 @@ template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArgs a) {
   constexpr int LPR = D / 8, RPB = kThreads / LPR;  // lanes of a head's row, such rows of a block
   const int32_t* plan = a.plan;
+  grid_wait();
   const uint32_t Hkv = uint32_t(plan[PH_HKV]), n = uint32_t(plan[PH_T]) * Hkv;
   const int32_t* tok = plan + plan[PH_OFF_TOK];
   const int shift = plan[PH_PAGE_SHIFT];
@@ -133,6 +134,7 @@ __global__ void __launch_bounds__(kThreads) bd_cache_read_kernel(const CacheArgs
   constexpr uint32_t LPR = D / 8;
   constexpr int U = FMT == BD_CACHE_BF16 ? 2 : 4;  // rows in flight per thread: 64 bytes of loads
   const int32_t* plan = a.plan;
+  grid_wait();
   const uint32_t Hkv = uint32_t(plan[PH_HKV]);
   const int32_t* pages = plan + plan[PH_OFF_PAGES];
   const int32_t* pgrow = plan + plan[PH_OFF_PGROW];
@@ -211,17 +213,15 @@ CacheArgs cache_args(const void* plan_dev, const bd_paged_cache* c, const bd_ten
 }
 
 template <int FMT>
-void launch_write(int d, int grid, cudaStream_t s, const CacheArgs& a) {
-  if (d == 64) bd_cache_write_kernel<64, FMT><<<grid, kThreads, 0, s>>>(a);
-  else if (d == 128) bd_cache_write_kernel<128, FMT><<<grid, kThreads, 0, s>>>(a);
-  else bd_cache_write_kernel<256, FMT><<<grid, kThreads, 0, s>>>(a);
+cudaError_t launch_write(int d, int grid, cudaStream_t s, const CacheArgs& a) {
+  auto kernel = d == 64 ? bd_cache_write_kernel<64, FMT> : d == 128 ? bd_cache_write_kernel<128, FMT> : bd_cache_write_kernel<256, FMT>;
+  return launch_kernel(kernel, grid, kThreads, 0, s, a);
 }
 
 template <int FMT>
-void launch_read(int d, int grid, cudaStream_t s, const CacheArgs& a) {
-  if (d == 64) bd_cache_read_kernel<64, FMT><<<grid, kThreads, 0, s>>>(a);
-  else if (d == 128) bd_cache_read_kernel<128, FMT><<<grid, kThreads, 0, s>>>(a);
-  else bd_cache_read_kernel<256, FMT><<<grid, kThreads, 0, s>>>(a);
+cudaError_t launch_read(int d, int grid, cudaStream_t s, const CacheArgs& a) {
+  auto kernel = d == 64 ? bd_cache_read_kernel<64, FMT> : d == 128 ? bd_cache_read_kernel<128, FMT> : bd_cache_read_kernel<256, FMT>;
+  return launch_kernel(kernel, grid, kThreads, 0, s, a);
 }
 
 }  // namespace
@@ -274,9 +274,8 @@ extern "C" int32_t bd_cache_write(const void* plan_host, const void* plan_dev, c
   // one round 35.5 / 97-99, with two 33.4 / 97
   const int grid = int(blocks < kPagedSms * 24 ? blocks : kPagedSms * 24);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cache->fmt == BD_CACHE_BF16) launch_write<BD_CACHE_BF16>(w[PH_D], grid, s, a);
-  else launch_write<BD_CACHE_E4M3>(w[PH_D], grid, s, a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cache->fmt == BD_CACHE_BF16 ? launch_write<BD_CACHE_BF16>(w[PH_D], grid, s, a)
+                                                    : launch_write<BD_CACHE_E4M3>(w[PH_D], grid, s, a);
   if (e != cudaSuccess) return cuda_fail(e, "bd_cache_write_kernel launch");
   return ok();
 }
@@ -295,9 +294,8 @@ extern "C" int32_t bd_cache_read(const void* plan_host, const void* plan_dev, co
   const int64_t groups = int64_t(w[PH_NPAGES]) * (w[PH_PAGE] / kReadRows);
   const int grid = int(groups < kPagedSms * 8 ? groups : kPagedSms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cache->fmt == BD_CACHE_BF16) launch_read<BD_CACHE_BF16>(w[PH_D], grid, s, a);
-  else launch_read<BD_CACHE_E4M3>(w[PH_D], grid, s, a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cache->fmt == BD_CACHE_BF16 ? launch_read<BD_CACHE_BF16>(w[PH_D], grid, s, a)
+                                                    : launch_read<BD_CACHE_E4M3>(w[PH_D], grid, s, a);
   if (e != cudaSuccess) return cuda_fail(e, "bd_cache_read_kernel launch");
   return ok();
 }

@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * kChunk * 8;
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffDecRec + blockIdx.x * kRecordWords;
+  if (!a.behind) grid_wait();
   const int p0 = rec[RC_P0], p1 = rec[RC_P1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
   if (threadIdx.x == 0) {
@@ -704,7 +705,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   }
   // (launched behind the tile kernel, this grid starts as that one's CTAs leave their SMs;
   // the joins that follow wait for this grid's end, which so is that one's as well)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
   if (!ok) {
     // every copy issued has been waited for in turn; wait (with a limit) for those a
     // wait gave up on, then say so
@@ -807,14 +808,14 @@ __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) 
     const int r = x % live, cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + r;
     const int t = M[MG_Q0] + nr / a.G, h = M[MG_HKV] * a.G + nr % a.G;
     if (r >= M[MG_NROWS]) continue;
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!waited) grid_wait();
     waited = true;
     float acc[D / 32], m, l;
     join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + r * D + lane * (D / 32), cnt, 0, 1,
                       lane, &m, &l, acc);
     store_row(a, t, h, lane, m, l, acc);
   }
-  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!waited) grid_wait();
 }
 
 // The same where blocks have many slots (few long sequences, cut over every SM): a CTA
@@ -832,7 +833,7 @@ __global__ void __launch_bounds__(256) bd_paged_wide_merge_kernel(const MergeArg
     const int r = x % live, cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + r;
     const int t = M[MG_Q0] + nr / a.G, h = M[MG_HKV] * a.G + nr % a.G;
     if (r >= M[MG_NROWS]) continue;
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!waited) grid_wait();
     waited = true;
     float acc[V], m, l;
     join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + r * D + lane * V, cnt, warp, 8, lane,
@@ -859,7 +860,7 @@ __global__ void __launch_bounds__(256) bd_paged_wide_merge_kernel(const MergeArg
     }
     __syncthreads();
   }
-  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (!waited) grid_wait();
 }
 
 // Joins of the tile kernel: a warp per row, rows of all split blocks over the grid.
@@ -875,35 +876,18 @@ __global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArg
     const int cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + br;
     const int t = M[MG_Q0] + nr / G, h = M[MG_HKV] * G + nr % G;
     if ((r & 127) >= per || br >= M[MG_NROWS]) continue;
-    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!waited) grid_wait();
     waited = true;
     float acc[V], m, l;
     join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + int64_t(r) * D + lane * V, cnt, 0, 1,
                       lane, &m, &l, acc);
     store_row(a, t, h, lane, m, l, acc);
   }
-  if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
-// `behind`: the grid may start before the one in front of it has ended (and waits for that
-// itself, where it needs to).
-template <class... P, class... A>
-cudaError_t launch_kernel(void (*kernel)(P...), int grid, int threads, size_t smem, bool behind, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(grid);
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = at;
-  c.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&c, kernel, args...);
+  if (!waited) grid_wait();
 }
 
 template <int D, int FMT, int NB>
-int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, bool behind, cudaStream_t s) {
+int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
   using Cfg = DecCfg<D, FMT, NB>;
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -920,18 +904,18 @@ int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& 
   int32_t st;
   if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, 1, near))) return st;
   if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, 1, near))) return st;
-  const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB>, kDecCtas, Cfg::kThreads, Cfg::kSmem, behind, s, mk, mv, a);
+  const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB>, kDecCtas, Cfg::kThreads, Cfg::kSmem, s, mk, mv, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
 }
 
 template <int D, int FMT>
-int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, bool behind, cudaStream_t s) {
+int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
   const int rows = w[PH_DEC_ROWS];
-  if (rows == 8) return launch_dec_t<D, FMT, 1>(w, c, a, behind, s);
-  if (rows == 16) return launch_dec_t<D, FMT, 2>(w, c, a, behind, s);
+  if (rows == 8) return launch_dec_t<D, FMT, 1>(w, c, a, s);
+  if (rows == 16) return launch_dec_t<D, FMT, 2>(w, c, a, s);
   if constexpr (dec_block_rows(FMT) == 32) {
-    if (rows == 24) return launch_dec_t<D, FMT, 3>(w, c, a, behind, s);
-    if (rows == 32) return launch_dec_t<D, FMT, 4>(w, c, a, behind, s);
+    if (rows == 24) return launch_dec_t<D, FMT, 3>(w, c, a, s);
+    if (rows == 32) return launch_dec_t<D, FMT, 4>(w, c, a, s);
   }
   return fail(BD_ERR_PLAN, "few-rows blocks of %d rows at head dim %d", rows, D);
 }
@@ -944,17 +928,17 @@ int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream
   const Kernel k = tile   ? pick(bd_paged_tile_merge_kernel<64>, bd_paged_tile_merge_kernel<128>, bd_paged_tile_merge_kernel<256>)
                    : wide ? pick(bd_paged_wide_merge_kernel<64>, bd_paged_wide_merge_kernel<128>, bd_paged_wide_merge_kernel<256>)
                           : pick(bd_paged_merge_kernel<64>, bd_paged_merge_kernel<128>, bd_paged_merge_kernel<256>);
-  const cudaError_t e = launch_kernel(k, tile ? kPagedSms * 8 : kWideCtas, 256, 0, true, s, a);
+  const cudaError_t e = launch_kernel(k, tile ? kPagedSms * 8 : kWideCtas, 256, 0, s, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "paged join launch");
 }
 
-int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, bool behind, cudaStream_t s) {
+int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, cudaStream_t s) {
   const int d = w[PH_D];
   if (c->fmt == BD_CACHE_BF16)
-    return d == 64 ? launch_dec_rows<64, BD_CACHE_BF16>(w, c, a, behind, s)
-           : d == 128 ? launch_dec_rows<128, BD_CACHE_BF16>(w, c, a, behind, s) : launch_dec_rows<256, BD_CACHE_BF16>(w, c, a, behind, s);
-  return d == 64 ? launch_dec_rows<64, BD_CACHE_E4M3>(w, c, a, behind, s)
-         : d == 128 ? launch_dec_rows<128, BD_CACHE_E4M3>(w, c, a, behind, s) : launch_dec_rows<256, BD_CACHE_E4M3>(w, c, a, behind, s);
+    return d == 64 ? launch_dec_rows<64, BD_CACHE_BF16>(w, c, a, s)
+           : d == 128 ? launch_dec_rows<128, BD_CACHE_BF16>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_BF16>(w, c, a, s);
+  return d == 64 ? launch_dec_rows<64, BD_CACHE_E4M3>(w, c, a, s)
+         : d == 128 ? launch_dec_rows<128, BD_CACHE_E4M3>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_E4M3>(w, c, a, s);
 }
 
 }  // namespace bd
@@ -1020,6 +1004,7 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   float* const dec_part = a.part;
   float* const tile_part = a.part + dec_part_bytes(w) / 4;
   const bool dec = w[PH_NDEC] > 0, tile = w[PH_NTILE] > 0;
+  a.behind = 0;
   // tiles first: their CTAs leave their SMs at different times, which few-rows CTAs fill
   if (tile) {
     a.part = tile_part;
@@ -1027,7 +1012,8 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   }
   if (dec) {
     a.part = dec_part;
-    if ((st = launch_dec(w, a, cache, tile, s))) return st;
+    a.behind = tile;
+    if ((st = launch_dec(w, a, cache, s))) return st;
   }
   MergeArgs m = {a.plan, dec_part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh, a.G};
   if (w[PH_NDECM] && (st = launch_merge(m, w[PH_D], false, w[PH_DECM_WIDE] != 0, s))) return st;

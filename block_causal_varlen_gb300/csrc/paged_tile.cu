@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffTileRec + blockIdx.x * kRecordWords;
+  grid_wait();
   const int p0 = rec[RC_P0], p1 = rec[RC_P1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
   if (p0 == p1) return;
@@ -804,8 +805,7 @@ int32_t launch_tile_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
                   fa.numRegs, Cfg::kRegsLaunch);
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
-  bd_paged_tile_kernel<D, FMT><<<kTileCtas, Cfg::kThreads, Cfg::kSmem, s>>>(mq, mk, mv, a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_kernel(bd_paged_tile_kernel<D, FMT>, kTileCtas, Cfg::kThreads, Cfg::kSmem, s, mq, mk, mv, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_tile_kernel launch");
 }
 

@@ -413,6 +413,63 @@ def test_captured_layers_replay_with_tiles_and_few_rows(fmt):
         bd.bd_check_status(plans[i])
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,kv", [([1], [90]), ([1, 2], [3000, 40]), ([60, 1, 200], [5000, 700, 260])])
+def test_calls_in_a_row_wait_for_each_other(new, kv, fmt):
+    """Grids may start before the one in front of them has ended: q, K and V written by other
+    kernels right before a call, the cache rows that a write leaves for the attention behind it, results
+    read right after, a plan copied in between; eager and in a graph, the bits of calls with a
+    synchronisation after each operation."""
+    c = pu.Case(new, kv, 8, 2, 128, page=32, fmt=fmt, junk=0.0)
+    other = pu.Case(new, kv, 8, 2, 128, page=32, fmt=fmt, junk=0.0, seed=1)  # same key, other pages
+    assert c.plan.key() == other.plan.key() and c.num_pages == other.num_pages
+    buf = torch.zeros(max(c.plan.nbytes, other.plan.nbytes) // 4, dtype=torch.int32, device="cuda")
+    blobs = [torch.zeros_like(buf) for _ in range(2)]
+    for b, x in zip(blobs, (c, other)):
+        b[:len(x.plan.host)] = torch.from_numpy(x.plan.host).cuda()
+    c.plan.upload(buffer=buf)
+    T, N = c.T, 12
+    g = torch.Generator().manual_seed(3)
+    qs, ks, vs = (torch.randn(N, T, h, 128, generator=g).bfloat16().cuda() for h in (8, 2, 2))
+    q, k, v = (torch.empty_like(t[0]) for t in (qs, ks, vs))
+    out, lse = torch.empty_like(q), torch.empty(8, T, device="cuda")
+    ws = torch.empty(max(256, bd.bd_paged_attn_workspace(c.plan)), dtype=torch.uint8, device="cuda")
+    back = [torch.empty(sum(kv), 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    start = [t.clone() if t is not None else None for t in (c.k, c.v, c.ke, c.ve)]
+
+    def rows(sync):
+        ops = []
+        for t, t0 in zip((c.k, c.v, c.ke, c.ve), start):
+            if t is not None:
+                t.view(torch.uint8).copy_(t0.view(torch.uint8))
+        got = []
+        for i in range(N):
+            ops = [lambda: buf.copy_(blobs[i % 2]), lambda: q.copy_(qs[i]), lambda: k.copy_(ks[i]), lambda: v.copy_(vs[i]),
+                   lambda: bd.bd_cache_write(c.plan, k, v, c.cache), lambda: bd.bd_paged_attn(c.plan, q, c.cache, out, lse, ws),
+                   lambda: got.extend([out.clone(), lse.clone()]), lambda: bd.bd_cache_read(c.plan, c.cache, *back),
+                   lambda: got.extend([b.clone() for b in back])]
+            for op_ in ops:
+                op_()
+                if sync:
+                    torch.cuda.synchronize()
+        return got
+
+    want = rows(True)
+    for _ in range(3):
+        got = rows(False)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = rows(False)
+    for _ in range(3):
+        for t in got:
+            t.fill_(1)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_upload_leaves_another_plans_buffer_alone():
     """A plan once uploaded into a shared buffer takes memory of its own the next time."""
     a, b = (bd.PagedPlan([1], [n], [[0, 1, 2]], 4, 2, 64, page_size=16, num_pages=3) for n in (20, 40))
