@@ -1,7 +1,7 @@
 // Attention of few query rows over a paged K/V cache, and the join of split key
 // ranges, on sm_103a.
 //
-// A block of up to 16 rows (the (new row, query head) pairs of one K/V head) over
+// A block of up to 32 rows (the (new row, query head) pairs of one K/V head) over
 // keys [k0, k1) computes, per row, m = max_j s_j, l = sum_j 2^(s_j - m) and
 // O = sum_j 2^(s_j - m) v_j with s_j = log2(e) q . k_j / sqrt(d), in one pass.
 //
@@ -11,7 +11,7 @@
 // tiles, and everything is laid out to keep HBM busy:
 //   - two persistent CTAs per SM; the host cuts all keys of the batch into equal
 //     stretches, one a CTA, so that no SM waits for another, and one CTA's loads go on
-//     while the other adds up a block;
+//     while the other adds up a block. CTAs of neighbouring heads walk the same keys;
 //   - every warp runs on its own: it takes every NW-th chunk of 16 or 32 keys, loads its
 //     chunks by TMA into a ring of its own (mbarriers, no CTA-wide barrier in the
 //     loop) and keeps its own m, l and O in registers. The ring runs ahead over the
@@ -29,6 +29,9 @@
 // P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-8 relative at
 // most, like O itself), fp16 for e4m3 (2^-11), scaled by 2^7 so that terms down to
 // 2^-31 of the largest keep a value.
+//
+// 64 ragged sequences of 500-16000 rows, 8 K/V heads of 128: bf16 (4 pairs a head) 164 us,
+// 6.8 TB/s; e4m3 (2 pairs) 90 us, 6.2 TB/s. One sequence of 4096 rows 7.5 us in a graph.
 //
 // A row takes nothing from a key it does not see, whatever is there: V's infinities
 // and NaN, which a probability of zero would turn to NaN, stay out of the products of
