@@ -470,6 +470,48 @@ def test_calls_in_a_row_wait_for_each_other(new, kv, fmt):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_captured_fork_and_join():
+    """A call behind two branches of a graph, one of kernels and one of a copy, and two calls
+    in branches of their own: each waits for what is in front of it."""
+    c = _mixed()
+    q0 = c.q.cuda()
+    want = pu.run_attention(c)
+    q, half, big = torch.zeros_like(q0), torch.zeros_like(q0), torch.ones(1 << 24, device="cuda")
+    outs = [torch.zeros(c.T, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    lses = [torch.zeros(8, c.T, device="cuda") for _ in range(3)]
+    ws = [torch.empty(bd.bd_paged_attn_workspace(c.plan), dtype=torch.uint8, device="cuda") for _ in range(3)]
+    side = torch.cuda.Stream()
+    bd.bd_paged_attn(c.plan, q0, c.cache, outs[0], lses[0], ws[0])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            for _ in range(8):
+                big.mul_(1.0)
+            torch.mul(q0, 0.5, out=half)
+        big2 = big.clone()
+        main.wait_stream(side)
+        torch.add(half, half, out=q)
+        bd.bd_paged_attn(c.plan, q, c.cache, outs[0], lses[0], ws[0])
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            bd.bd_paged_attn(c.plan, q, c.cache, outs[1], lses[1], ws[1])
+        bd.bd_paged_attn(c.plan, q, c.cache, outs[2], lses[2], ws[2])
+        main.wait_stream(side)
+        sums = [o.float().sum() for o in outs]
+    for _ in range(5):
+        for t in outs + lses + [q, half]:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for o, l, s in zip(outs, lses, sums):
+            assert torch.equal(o.cpu(), want[0]) and torch.equal(l.cpu(), want[1])
+            assert torch.equal(s, o.float().sum())
+    assert big2.numel() == big.numel()
+
+
 def test_upload_leaves_another_plans_buffer_alone():
     """A plan once uploaded into a shared buffer takes memory of its own the next time."""
     a, b = (bd.PagedPlan([1], [n], [[0, 1, 2]], 4, 2, 64, page_size=16, num_pages=3) for n in (20, 40))
