@@ -11,11 +11,12 @@
 namespace bd {
 
 // Every paged kernel is launched so that its grid may start while the one in front of it in
-// the stream ends (one sequence of 64 keys 3.9 -> 3.7 us in a graph, of 2048 6.5 -> 6.2; from
-// Python, 4096 keys 9.2 -> 8.6, small chunks 9.8 -> 7.6): none reads anything, the plan included, before grid_wait, when that grid and
-// all in front of it have ended and their writes are seen. Only joins look at the plan
+// the stream ends: none reads anything, the plan included, before grid_wait, when that grid
+// and all in front of it have ended and their writes are seen. Only joins look at the plan
 // before: their call's attention kernels, which they follow, let them start after waiting
 // themselves. The few-rows kernel behind the tile kernel of its call waits at its end.
+// One sequence of 64 keys 3.9 -> 3.7 us in a graph, of 2048 6.5 -> 6.2; from Python, 4096
+// keys 9.2 -> 8.6, small chunks 9.8 -> 7.6.
 template <class... P, class... A>
 cudaError_t launch_kernel(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t c = {};

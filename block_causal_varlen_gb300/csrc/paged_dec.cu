@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
 #pragma unroll
             for (int n = 0; n < 2 * MT; ++n) {  // this lane's columns 8 n + rw
               uint16_t u;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(sv + key * 128 + (n >> 3) * (kChunk * 128) + (((n & 7) ^ (key & 7)) << 4) + rw * 2) : "memory");
+              const uint32_t at = sv + key * 128 + (n >> 3) * (kChunk * 128) + (((n & 7) ^ (key & 7)) << 4) + rw * 2;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
               if ((u & 0x7f80u) != 0x7f80u) continue;
 #pragma unroll
               for (int b = 0; b < NB; ++b)

@@ -545,8 +545,8 @@ extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
   if (st) return st;
   // what a captured launch holds of the plan (FNV-1a over the words)
   const int32_t fields[] = {w[PH_H], w[PH_HKV], w[PH_D], w[PH_PAGE], w[PH_NUM_PAGES], w[PH_FMT], w[PH_CAUSAL],
-                            w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0, w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0,
-                            w[PH_NTILE] > 0, w[PH_NTILEM] > 0};
+                            w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0,
+                            w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0, w[PH_NTILE] > 0, w[PH_NTILEM] > 0};
   uint64_t h = 1469598103934665603ull;
   for (int32_t f : fields)
     for (int i = 0; i < 4; ++i) h = (h ^ ((uint32_t(f) >> (8 * i)) & 255u)) * 1099511628211ull;

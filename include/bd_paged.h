@@ -92,8 +92,9 @@ typedef struct {
 
 /* Bytes that hold the plan blob for `desc`, which is validated in full (lengths, head
  * counts, every page index used). A bound: the plan itself may be shorter (its third
- * 32-bit word is the number of words in use, all that has to be copied to the device). Errors: BD_ERR_ARG, BD_ERR_UNSUPPORTED (head dim,
- * head ratio, page size), BD_ERR_CAPACITY (sizes past 2^31). */
+ * 32-bit word is the number of words in use, all that has to be copied to the device).
+ * Errors: BD_ERR_ARG, BD_ERR_UNSUPPORTED (head dim, head ratio, page size),
+ * BD_ERR_CAPACITY (sizes past 2^31; pages in use times page_size past 2^34). */
 BD_API int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes);
 
 /* Build the plan blob into caller-owned host memory (16-byte aligned, blob_bytes
