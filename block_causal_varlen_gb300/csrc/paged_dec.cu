@@ -27,8 +27,8 @@
 //     addend of the base-2 exponent (m is then the maximum of s_j + e_j). q as fp16 is
 //     exact too: each row is scaled by a power of two first.
 // P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-8 relative at
-// most, like O itself), fp16 for e4m3 (2^-11), scaled by 2^7 so that terms down to
-// 2^-31 of the largest keep a value.
+// most, like O itself), fp16 for e4m3 (2^-11; its subnormals, p 2^e below 2^-21 of the
+// row's largest, to 2^-32 of that), scaled by 2^7 for their sake.
 //
 // 64 ragged sequences of 500-16000 rows, 8 K/V heads of 128: bf16 (4 pairs a head) 164 us,
 // 6.8 TB/s; e4m3 (2 pairs) 90 us, 6.2 TB/s. One sequence of 4096 rows 7.5 us in a graph.
@@ -220,13 +220,12 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   uint32_t issued = 0;
   auto issue = [&]() {
     const uint32_t full = bars + 8 * is;
-    const int keys = ck1 - ck, row = (ck + lane % kChunk) & ((1 << pshift) - 1);
+    // row of key ck + lane (mod kChunk) in its page, past the keys' end of the last key in its own
+    const int keys = ck1 - ck, row = min(ck + lane % kChunk, ck1 - 1) & ((1 << pshift) - 1);
     const bool two = kChunk == 32 && brows == 16 && keys > 16;  // copies of K and of V: one, or two
     if constexpr (F8) {
-      // the 4-byte words of K's and V's exponents; a word's low address bits for later.
-      // (Past the keys' end: the last key's.)
-      const int back = max(lane % kChunk - keys + 1, 0);
-      const int64_t o = int64_t(cpage) * a.e_sp + (row - back) * int(a.e_sr) + chkv * int(a.e_sh);
+      // the 4-byte words of K's and V's exponents; a word's low address bits for later
+      const int64_t o = int64_t(cpage) * a.e_sp + row * int(a.e_sr) + chkv * int(a.e_sh);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
         if (kChunk == 32 || (lane >> 4) == m) {

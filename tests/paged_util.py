@@ -86,13 +86,19 @@ def tolerances(d, keys, A, big, fmt, rows=1):
     O: P rounded to half a step (2^-11 of each term where it is fp16: e4m3 caches, `rows`
     (new row, head) pairs of a K/V head up to 16, i.e. the few-rows kernel; 2^-8 where it
     is bf16, i.e. bf16 caches and the tile kernel, whose e4m3 tiles are bf16 by then),
-    which sum to at most that times A (fp16 terms below 2^-31 of the largest vanish:
-    keys 2^-31 A' is below that), products summed as above, and the output rounded by 2^-8 of itself (applied
-    to A, which is no smaller)."""
+    which sum to at most that times A, products summed as above, and the output rounded by
+    2^-8 of itself (applied to A, which is no smaller). Few-rows e4m3 blocks (up to 48 pairs)
+    hold p 2^e (e: V's exponent) as fp16, the largest of a row at 2^7 at least: below 2^-14
+    its rounding is 2^-25 absolute, 2^-32 of the largest, times a code of at most 448. The
+    key with the largest has a code above 224 somewhere (its row's maximum), where A is at
+    least 224 times it: the sum over the keys is within keys 2^-31 of A's largest column.
+    (It counts where the keys with the largest p have zeros in a column.)"""
     ds = (2 * d + 8) * 2.0 ** -24 * big + 2.0 ** -22
     ls = ds + keys * 2.0 ** -24 + 2.0 ** -21 + 2.0 ** -17
     p = 2.0 ** -11 if fmt == "e4m3" and rows <= 16 else 2.0 ** -8
     o = A * (p + 2.0 ** -8) * 1.01 + A * (2 * ls.t()[..., None] + 2 * keys * 2.0 ** -24) + 1e-30
+    if fmt == "e4m3" and rows <= 48:
+        o = o + keys * 2.0 ** -31 * A.amax(-1, keepdim=True)
     return o, ls
 
 

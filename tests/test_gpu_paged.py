@@ -78,6 +78,27 @@ def test_page_sizes_and_orders(page, heads_first, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("kv", [1, 15, 17, 33, 40, 47, 49, 64, 131])
+def test_last_chunk_in_the_pools_first_page(kv, d, fmt):
+    """Pages of 16 and chunks of 32 keys: a last chunk of one page, which is the first of the
+    pool (exponents past the keys' end are the last key's, never before the page)."""
+    c = pu.Case([1, 2], [kv, 5], 4, 2, d, page=16, fmt=fmt, seed=kv)
+    a, b = c.pages[0][-1], 0
+    for pool in (c.k, c.v, c.ke, c.ve):
+        if pool is not None:
+            raw = pool.view(torch.uint8)
+            raw[[a, b]] = raw[[b, a]]
+    for t in (c.kd, c.vd):
+        t[[a, b]] = t[[b, a]]
+    swap = {a: b, b: a}
+    c.pages = [[swap.get(x, x) for x in pg] for pg in c.pages]
+    assert c.pages[0][-1] == 0
+    c.plan = c.make_plan().upload("cuda")
+    pu.check_attention(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
 def test_rows_that_see_nothing(fmt):
     """Sequences with nothing cached, and more new rows than cached ones."""
     c = pu.Case([1, 3, 5, 90, 40], [0, 2, 0, 60, 500], 8, 2, 128, fmt=fmt)
