@@ -11,12 +11,9 @@
 namespace bd {
 
 // Every paged kernel is launched so that its grid may start while the one in front of it in
-// the stream ends: none reads anything, the plan included, before grid_wait, when that grid
-// and all in front of it have ended and their writes are seen. Only joins look at the plan
-// before: their call's attention kernels, which they follow, let them start after waiting
-// themselves. The few-rows kernel behind the tile kernel of its call waits at its end.
-// One sequence of 64 keys 3.9 -> 3.7 us in a graph, of 2048 6.5 -> 6.2; from Python, 4096
-// keys 9.2 -> 8.6, small chunks 9.8 -> 7.6.
+// the stream ends: it waits in grid_wait, until that grid and all in front of it have ended
+// and their writes are seen, before it reads anything, the plan included (what needs no
+// memory of others comes before). One sequence of 64 keys 3.9 -> 3.7 us in a graph.
 template <class... P, class... A>
 cudaError_t launch_kernel(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
   cudaLaunchConfig_t c = {};
@@ -32,6 +29,29 @@ cudaError_t launch_kernel(void (*kernel)(P...), int grid, int threads, size_t sm
   return cudaLaunchKernelEx(&c, kernel, args...);
 }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The few-rows kernel behind the tile kernel of its call does not depend on it, only on what
+// that one waited for, and runs on SMs that its CTAs have left. A grid that starts early is
+// promised others' writes by a wait of its own only, so the tile kernel's CTAs hand on what
+// they have waited for: each releases a word for two few-rows CTAs, which acquire it
+// before their first read, or wait for the tile kernel's end if it is not there. The CTA
+// that takes a word clears it; a workspace that holds anything else needs no clearing. (10
+// ragged e4m3 sequences, one row to 1024: 268 us, 280 where one kernel follows the other.)
+constexpr unsigned long long kGo = 0x9e1c5a37d20b64f1ull;
+constexpr int kGoTries = 64;
+__device__ __forceinline__ void give_go(unsigned long long* go) {
+  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(go), "l"(kGo) : "memory");
+}
+// By one thread of the CTA; the others follow behind a barrier of the CTA.
+__device__ __forceinline__ bool take_go(unsigned long long* go) {
+  unsigned long long x = 0;
+  for (int i = 0; i < kGoTries && x != kGo; ++i) asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(x) : "l"(go) : "memory");
+  if (x != kGo) grid_wait();
+  asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(go), "l"(0ull) : "memory");
+  return x == kGo;
+}
+// Orders what was acquired before this thread's asynchronous copies (TMA) as well.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Checks both plan copies and the cache against the plan.
 int32_t check_paged(const void* plan_host, const void* plan_dev, const bd_paged_cache* cache, const int32_t** w);
@@ -76,7 +96,7 @@ struct AttnArgs {
   int64_t e_sp, e_sr, e_sh;
   float scale_log2;
   int32_t G, causal, page_shift;
-  int32_t behind;  // the few-rows kernel: launched behind the tile kernel of the same call
+  unsigned long long* go;  // a word for each few-rows CTA if both kernels run, else NULL
 };
 
 int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, const bd_paged_cache* cache,

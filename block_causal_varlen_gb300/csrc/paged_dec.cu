@@ -178,23 +178,28 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * kChunk * 8;
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffDecRec + blockIdx.x * kRecordWords;
-  if (!a.behind) grid_wait();
-  const int p0 = rec[RC_P0], p1 = rec[RC_P1];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
+    *abort_flag = 0;
   }
-  if (p0 == p1) return;
-  const int32_t* pieces = plan + plan[PH_OFF_DEC];
-  auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
-  if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
     // a chunk's arrivals: the copies' and, e4m3, every lane's exponent word
     for (int s = 0; s < NST; ++s) mbar_init(bars + 8 * s, F8 ? 33 : 1);
     fence_barrier_init();
   }
+  if (a.go && threadIdx.x == 0) abort_flag[1] = take_go(a.go + blockIdx.x);
   __syncthreads();
+  if (!a.go || !abort_flag[1]) grid_wait();
+  else fence_proxy_async_all();
+  const int p0 = rec[RC_P0], p1 = rec[RC_P1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
+  if (p0 == p1) {
+    grid_wait();
+    return;
+  }
+  const int32_t* pieces = plan + plan[PH_OFF_DEC];
+  auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
   const int G = a.G, causal = a.causal, pshift = a.page_shift;
 
   const int brows = min(1 << pshift, kChunk);  // rows of a copy: a chunk's keys lie in one page or, of pages of 16, in two
@@ -706,9 +711,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     }
     __syncthreads();
   }
-  // (launched behind the tile kernel, this grid starts as that one's CTAs leave their SMs;
-  // the joins that follow wait for this grid's end, which so is that one's as well)
-  grid_wait();
+  grid_wait();  // (behind the tile kernel: who waits for this grid's end, waits for that one's)
   if (!ok) {
     // every copy issued has been waited for in turn; wait (with a limit) for those a
     // wait gave up on, then say so
@@ -796,29 +799,25 @@ __device__ __forceinline__ void join_row(const float* P, int64_t o, int cnt, int
   *L = l;
 }
 
-// Joins of the few-rows kernel, a warp per row. Bound by latency: the plan's entry (which
-// the attention kernel does not change: fetched before waiting for that), then the
+// Joins of the few-rows kernel, a warp per row. Bound by latency: the plan's entry, then the
 // slots. With no shared memory and few registers, a CTA or two find room beside the
 // attention's.
 template <int D>
 __global__ void __launch_bounds__(256) bd_paged_merge_kernel(const MergeArgs a) {
   constexpr int ROWS = kDecSlotRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_wait();
   const int n = a.plan[PH_NDECM], live = a.plan[PH_DEC_LIVE];
-  bool waited = false;
   for (int x = blockIdx.x * 8 + warp; x < n * live; x += gridDim.x * 8) {
     const int32_t* M = a.plan + kOffDecMerge + (x / live) * kMergeWords;
     const int r = x % live, cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + r;
     const int t = M[MG_Q0] + nr / a.G, h = M[MG_HKV] * a.G + nr % a.G;
     if (r >= M[MG_NROWS]) continue;
-    if (!waited) grid_wait();
-    waited = true;
     float acc[D / 32], m, l;
     join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + r * D + lane * (D / 32), cnt, 0, 1,
                       lane, &m, &l, acc);
     store_row(a, t, h, lane, m, l, acc);
   }
-  if (!waited) grid_wait();
 }
 
 // The same where blocks have many slots (few long sequences, cut over every SM): a CTA
@@ -829,15 +828,13 @@ __global__ void __launch_bounds__(256) bd_paged_wide_merge_kernel(const MergeArg
   __shared__ float s_o[8][D];
   __shared__ float s_m[8], s_l[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_wait();
   const int n = a.plan[PH_NDECM], live = a.plan[PH_DEC_LIVE];
-  bool waited = false;
   for (int x = blockIdx.x; x < n * live; x += gridDim.x) {
     const int32_t* M = a.plan + kOffDecMerge + (x / live) * kMergeWords;
     const int r = x % live, cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + r;
     const int t = M[MG_Q0] + nr / a.G, h = M[MG_HKV] * a.G + nr % a.G;
     if (r >= M[MG_NROWS]) continue;
-    if (!waited) grid_wait();
-    waited = true;
     float acc[V], m, l;
     join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + r * D + lane * V, cnt, warp, 8, lane,
                       &m, &l, acc);
@@ -863,30 +860,26 @@ __global__ void __launch_bounds__(256) bd_paged_wide_merge_kernel(const MergeArg
     }
     __syncthreads();
   }
-  if (!waited) grid_wait();
 }
 
 // Joins of the tile kernel: a warp per row, rows of all split blocks over the grid.
 template <int D>
 __global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArgs a) {
   constexpr int V = D / 32, ROWS = tile_slot_rows(D);
+  grid_wait();
   const int n = a.plan[PH_NTILEM], G = a.G, per = 128 / G * G;  // rows in use of each 128 of a slot
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  bool waited = false;
   for (int x = blockIdx.x * 8 + warp; x < n * ROWS; x += gridDim.x * 8) {
     const int r = x % ROWS, br = (r >> 7) * per + (r & 127);  // row of the block
     const int32_t* M = a.plan + kOffTileMerge + (x / ROWS) * kMergeWords;
     const int cnt = M[MG_N], slot0 = M[MG_SLOT0], nr = M[MG_ROW0] + br;
     const int t = M[MG_Q0] + nr / G, h = M[MG_HKV] * G + nr % G;
     if ((r & 127) >= per || br >= M[MG_NROWS]) continue;
-    if (!waited) grid_wait();
-    waited = true;
     float acc[V], m, l;
     join_row<D, ROWS>(a.part + int64_t(slot0) * slot_floats(ROWS, D) + r, 2 * ROWS - r + int64_t(r) * D + lane * V, cnt, 0, 1,
                       lane, &m, &l, acc);
     store_row(a, t, h, lane, m, l, acc);
   }
-  if (!waited) grid_wait();
 }
 
 template <int D, int FMT, int NB>
@@ -956,13 +949,17 @@ static size_t dec_part_bytes(const int32_t* w) {
 static size_t part_bytes(const int32_t* w) {
   return dec_part_bytes(w) + (w[PH_NTILE] ? size_t(kTilePartSlots) * slot_floats(tile_slot_rows(w[PH_D]), w[PH_D]) * 4 : 0);
 }
+// ... and behind them the words that order the kernels.
+static size_t workspace_size(const int32_t* w) {
+  return part_bytes(w) + (w[PH_NDEC] && w[PH_NTILE] ? kDecCtas * sizeof(unsigned long long) : 0);
+}
 
 extern "C" int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes) {
   if (!bytes) return fail(BD_ERR_ARG, "bytes is NULL");
   const int32_t* w = nullptr;
   int32_t st = view_paged_plan(plan_host, &w);
   if (st) return st;
-  *bytes = part_bytes(w);
+  *bytes = workspace_size(w);
   return ok();
 }
 
@@ -981,7 +978,7 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
     return fail(BD_ERR_ARG, "lse: NULL pointer or not 4-byte aligned");
   if (lse && w[PH_H] > 1 && lse->stride_head < w[PH_T])
     return fail(BD_ERR_ARG, "lse stride_head %lld < %d rows", (long long)lse->stride_head, w[PH_T]);
-  const size_t need = part_bytes(w);
+  const size_t need = workspace_size(w);
   if (need && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256))
     return fail(BD_ERR_ARG, "workspace NULL or not 256-byte aligned");
   if (workspace_bytes < need) return fail(BD_ERR_CAPACITY, "workspace of %zu bytes, %zu needed", workspace_bytes, need);
@@ -1007,7 +1004,7 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   float* const dec_part = a.part;
   float* const tile_part = a.part + dec_part_bytes(w) / 4;
   const bool dec = w[PH_NDEC] > 0, tile = w[PH_NTILE] > 0;
-  a.behind = 0;
+  a.go = dec && tile ? reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + part_bytes(w)) : nullptr;
   // tiles first: their CTAs leave their SMs at different times, which few-rows CTAs fill
   if (tile) {
     a.part = tile_part;
@@ -1015,7 +1012,6 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   }
   if (dec) {
     a.part = dec_part;
-    a.behind = tile;
     if ((st = launch_dec(w, a, cache, s))) return st;
   }
   MergeArgs m = {a.plan, dec_part, a.o, a.o_sr, a.o_sh, a.lse, a.l_sh, a.G};

@@ -147,6 +147,8 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffTileRec + blockIdx.x * kRecordWords;
   grid_wait();
+  static_assert(kDecCtas == 2 * kTileCtas, "a word for two few-rows CTAs each");
+  if (a.go && threadIdx.x < 2) give_go(a.go + 2 * blockIdx.x + threadIdx.x);
   const int p0 = rec[RC_P0], p1 = rec[RC_P1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
   if (p0 == p1) return;
