@@ -126,6 +126,7 @@ class PagedPlan:
         self._host_ptr = self.host.ctypes.data
         self.dev = self._dev_ptr = None
         self._index, self._own = -1, False
+        self._streams = set()       # raw streams that the allocator knows to use the plan's own memory
         ws = C.c_size_t()
         check(load().bd_paged_attn_workspace(self._host_ptr, C.byref(ws)))
         self._workspace = ws.value
@@ -143,7 +144,9 @@ class PagedPlan:
     def upload(self, device="cuda", non_blocking=False, buffer=None):
         """Copy the plan blob to device memory (once per step): into memory of its own,
         or into ``buffer``, an int32 device tensor that a captured graph reads (see
-        bd_paged_plan_key; nbytes / 4 words always suffice)."""
+        bd_paged_plan_key; nbytes / 4 words always suffice). Memory of its own stays the
+        plan's until the calls made with it have run, on whichever streams; ``buffer`` is
+        the caller's to keep, and so is a plan whose own memory a captured graph reads."""
         src = torch.from_numpy(self.host)
         if buffer is not None:
             if buffer.dtype != torch.int32 or buffer.dim() != 1 or not buffer.is_contiguous() or not buffer.is_cuda:
@@ -153,9 +156,19 @@ class PagedPlan:
             self.dev, self._own = buffer[:src.numel()], False
         elif not self._own or self.dev.device != torch.device(device):
             self.dev, self._own = torch.empty_like(src, device=device), True
-        self.dev.copy_(src, non_blocking=non_blocking)
+            self._streams = {_raw_stream(self.dev.get_device())} if self.dev.is_cuda else set()
         self._dev_ptr, self._index = self.dev.data_ptr(), self.dev.get_device()
+        if self.dev.is_cuda:
+            self._used_on(_raw_stream(self._index), None)
+        self.dev.copy_(src, non_blocking=non_blocking)
         return self
+
+    def _used_on(self, raw, stream):
+        """Work is about to be queued on ``stream`` (None: the current one) that uses the device
+        copy: its own memory is not to be given to others before that has run."""
+        if self._own and raw not in self._streams:
+            self.dev.record_stream(torch.cuda.current_stream(self._index) if stream is None else stream)
+            self._streams.add(raw)
 
     def key(self) -> int:
         """See bd_paged_plan_key."""
@@ -231,8 +244,9 @@ def _device(plan, cache):
     return plan._index
 
 
-def _call(fn, idx, stream, *args):
+def _call(fn, plan, idx, stream, *args):
     s = _raw_stream(idx) if stream is None else stream.cuda_stream
+    plan._used_on(s, stream)
     if torch.cuda.current_device() == idx:
         st = fn(*args, s)
     else:
@@ -247,7 +261,7 @@ def bd_cache_write(plan: PagedPlan, k, v, cache: PagedCache, stream=None):
     idx = _device(plan, cache)
     tk = _rows3(k, "k", plan.Hkv, plan.d, plan.T, idx)
     tv = _rows3(v, "v", plan.Hkv, plan.d, plan.T, idx)
-    _call(_entry("bd_cache_write"), idx, stream, plan._host_ptr, plan._dev_ptr, tk, tv, cache._addr)
+    _call(_entry("bd_cache_write"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tk, tv, cache._addr)
 
 
 def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
@@ -255,7 +269,7 @@ def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
     idx = _device(plan, cache)
     tk = _rows3(k, "k", plan.Hkv, plan.d, plan.kv_total, idx)
     tv = _rows3(v, "v", plan.Hkv, plan.d, plan.kv_total, idx)
-    _call(_entry("bd_cache_read"), idx, stream, plan._host_ptr, plan._dev_ptr, cache._addr, tk, tv)
+    _call(_entry("bd_cache_read"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, cache._addr, tk, tv)
 
 
 def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspace=None, stream=None):
@@ -282,7 +296,7 @@ def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspac
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(_entry("bd_paged_attn"), idx, stream, plan._host_ptr, plan._dev_ptr, tq, cache._addr, to, tl, wp, wn)
+    _call(_entry("bd_paged_attn"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tq, cache._addr, to, tl, wp, wn)
 
 
 def paged_attn(plan: PagedPlan, q, cache: PagedCache, stream=None):
