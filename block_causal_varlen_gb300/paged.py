@@ -88,6 +88,14 @@ def _int(x, name):
     return int(_ints(x, name)[0])
 
 
+def _placed(device):
+    """``device`` as tensors on it say it: "cuda" is the current device."""
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
 class PagedPlan:
     """Host plan blob of one step over a paged cache, and its device copy.
 
@@ -154,7 +162,7 @@ class PagedPlan:
             if buffer.numel() < src.numel():
                 raise ValueError(f"buffer of {buffer.numel()} words, the plan has {src.numel()}")
             self.dev, self._own = buffer[:src.numel()], False
-        elif not self._own or self.dev.device != torch.device(device):
+        elif not self._own or self.dev.device != _placed(device):
             self.dev, self._own = torch.empty_like(src, device=device), True
             self._streams = {_raw_stream(self.dev.get_device())} if self.dev.is_cuda else set()
         self._dev_ptr, self._index = self.dev.data_ptr(), self.dev.get_device()

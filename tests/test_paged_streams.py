@@ -58,6 +58,36 @@ def test_a_plans_memory_is_known_to_be_used_on_other_streams(which, monkeypatch)
     assert plan.dev.seen == [5, 7]
 
 
+@pytest.mark.parametrize("device", [None, "cuda", 0, "cuda:0"])
+def test_a_plan_keeps_its_own_memory(device, monkeypatch):
+    """Uploaded again, however the device is named: graphs captured over it and calls on other
+    streams keep its address."""
+    plan, _, _ = _uploaded(monkeypatch)
+    mem = plan.dev
+    mem.device, mem.is_cuda = torch.device("cuda:0"), True
+    mem.get_device, mem.data_ptr, mem.copy_ = lambda: 0, lambda: 64, lambda *a, **k: None
+
+    def other(*a, **k):
+        raise AssertionError("allocated")
+
+    monkeypatch.setattr(torch, "empty_like", other)
+    plan.upload() if device is None else plan.upload(device)
+    assert plan.dev is mem
+    with pytest.raises(AssertionError, match="allocated"):
+        plan.upload("cuda:1")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("args", [(), ("cuda",), (0,)])
+def test_a_plans_address_after_more_uploads(args):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    plan = bd.PagedPlan([1], [20], [[0, 1]], 4, 2, 64, page_size=16, num_pages=3)
+    at = plan.upload(*args).dev.data_ptr()
+    assert all(plan.upload(*args).dev.data_ptr() == at for _ in range(3))
+    assert torch.equal(plan.dev.cpu(), torch.from_numpy(plan.host))
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("ambient", [False, True])
 def test_a_dropped_plan_is_read_to_the_end(ambient):
