@@ -147,6 +147,14 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// l times 2^x, x <= 0. An e4m3 cache's m is the maximum of s_j + e_j, l the sum of 2^(s_j - m):
+// up to 2^60 for a key, which a single factor, zero below 2^-126, would lose while the
+// product still counts (l is 2^-60 at least in the end). O's terms have their 2^e_j already.
+__device__ __forceinline__ float weigh_l(float l, float x) {
+  const float h = ex2(0.5f * x);
+  return x > -120.f ? l * ex2(x) : l * h * h;
+}
+
 // Transpose of an 8 x 8 matrix of 16-bit values: a lane's pair (row lane / 4, columns
 // 2 (lane % 4)..) becomes (column lane / 4, rows 2 (lane % 4)..).
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -461,7 +469,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
               if (k + 8 * y + rw >= lim[b][e]) s[y >> 1][b][2 * (y & 1) + e] = -CUDART_INF_F;
       }
       // ---- running maximum. It moves only when it grows by more than 2^8 (exact: l and O
-      // use the same one)
+      // use the same one); f: how far it moves, then as a factor
       float f[NB][2];
       bool grow = false;
 #pragma unroll
@@ -476,15 +484,22 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
           }
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-          f[b][e] = 1.f;
+          f[b][e] = 0.f;
           if (mx > m[b][e] + 8.f) {
-            f[b][e] = ex2(m[b][e] - mx);
+            f[b][e] = m[b][e] - mx;
             m[b][e] = mx;
-            l[b][e] *= f[b][e];
             grow = true;
           }
         }
       if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = f[b][e];
+            f[b][e] = ex2(x);
+            l[b][e] = F8 ? weigh_l(l[b][e], x) : l[b][e] * f[b][e];
+          }
 #pragma unroll
         for (int n = 0; n < MT; ++n)
 #pragma unroll
@@ -649,7 +664,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
 #pragma unroll
       for (int w = 0; w < NW; w += PW) {
         const float mw = ml[(w * 8 * NB + r) * 2];
-        L += mw == -CUDART_INF_F ? 0.f : ml[(w * 8 * NB + r) * 2 + 1] * ex2(mw - M);
+        L += mw == -CUDART_INF_F ? 0.f : weigh_l(ml[(w * 8 * NB + r) * 2 + 1], mw - M);
       }
       inv[r] = M == -CUDART_INF_F ? 0.f : 1.f / L;
       orow[r] = int64_t(t) * a.o_sr + int64_t(h) * a.o_sh;
@@ -773,10 +788,10 @@ __device__ __forceinline__ void join_row(const float* P, int64_t o, int cnt, int
     for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
     mn = fmaxf(mn, mx);
     const float f = mx == -CUDART_INF_F ? 0.f : ex2(mx - mn), w = mi == -CUDART_INF_F ? -1.f : ex2(mi - mn);
-    float ls = w < 0.f ? 0.f : li * w;
+    float ls = w < 0.f ? 0.f : weigh_l(li, mi - mn);
 #pragma unroll
     for (int x = 16; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
-    l = l * f + ls;
+    l = (mx == -CUDART_INF_F ? 0.f : weigh_l(l, mx - mn)) + ls;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] *= f;
     mx = mn;
@@ -852,7 +867,7 @@ __global__ void __launch_bounds__(256) bd_paged_wide_merge_kernel(const MergeArg
       for (int w = 0; w < 8; ++w) {
         if (s_m[w] == -CUDART_INF_F) continue;
         const float f = ex2(s_m[w] - mm);
-        ll += s_l[w] * f;
+        ll += weigh_l(s_l[w], s_m[w] - mm);
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] += s_o[w][lane * V + v] * f;
       }
