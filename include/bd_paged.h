@@ -48,7 +48,10 @@ typedef enum {
    * nearest even, saturating at +-448, and byte e + 127. A row with an infinity or a
    * NaN is stored as NaN codes with byte 255 and reads back as NaN. Values read back
    * are exact in bf16. Caches filled by other means may use bytes 67..187 and 255, and
-   * the NaN codes 0x7f and 0xff in rows of byte 255 only. */
+   * the NaN codes 0x7f and 0xff in rows of byte 255 only; their V rows take the exponent
+   * bd_cache_write would, or one near it: bd_paged_attn may hold a key's weight p * 2^e (p: its
+   * probability, e: its V row's exponent) to no more than 2^-32 of the row's largest, so that
+   * zeros of a high byte, say, would hide the keys that matter. */
   BD_CACHE_E4M3 = 1
 } bd_cache_fmt;
 
@@ -133,6 +136,9 @@ BD_API int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes);
  * [H, rows], stride_head between heads, stride_b and stride_c unused. K/V rows past
  * kv_len, and pages past the last one used, may hold anything; so may cached rows that
  * a new row does not see: an infinity or a NaN there reaches the rows that see it only.
+ * O's error is that of probabilities rounded to bf16 (2^-8 of each) and of its own rounding; few
+ * rows over a BD_CACHE_E4M3 cache (up to 48 (new row, query head) pairs of a K/V head) have
+ * weights p * 2^e in fp16 instead: 2^-11 of each, and 2^-32 of the row's largest where that is more.
  * out must not alias q or the cache. workspace: bd_paged_attn_workspace bytes, 256-byte aligned;
  * it needs no clearing and holds nothing between calls. */
 BD_API int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q,

@@ -93,3 +93,39 @@ def test_few_rows_of_17_to_48_pairs(new, kv, d):
     """Within the bound of a P in fp16."""
     c = pu.Case(new, kv, 8, 2, d, page=32, fmt="e4m3", seed=d + len(new))
     check(c, *pu.run_attention(c))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new,kv", [([1], [200]), ([2, 12], [3000, 400])])
+@pytest.mark.parametrize("gap", [3, 12, 24])
+def test_zeros_of_a_high_byte(gap, new, kv, d):
+    """A cache filled by other means: every third row of V is zeros with an exponent `gap` above
+    the largest other one's. Weights are then good to 2^-32 of the largest p 2^e, that of such a
+    row or not, times a code of at most 448 each."""
+    c = pu.Case(new, kv, 4, 1, d, page=32, fmt="e4m3", seed=gap, vmag=(-2, 2))
+    codes, ve = c.v.view(torch.uint8).cpu(), c.ve.cpu()
+    top = int(ve[c.used].max())
+    zero = torch.zeros(c.num_pages, 32, dtype=torch.bool)
+    zero[:, ::3] = True
+    zero &= c.used
+    codes[zero], ve[zero] = 0, top + gap
+    c.v.view(torch.uint8).copy_(codes.cuda())
+    c.ve.copy_(ve.cuda())
+    c.vd = op.dequantise(codes, ve)
+    out, lse = pu.run_attention(c)
+    at = 0
+    for b, (n, m) in enumerate(zip(c.new, c.kv)):
+        k, v = c.rows(b)
+        e = op.rows_of(ve, m, c.pages[b], 32)[:, 0].double() - 127
+        o_ref, l_ref, A, big = op.attention(c.q[at:at + n], k, v, m)
+        tol_o, tol_l = pu.tolerances(d, m, A, big, "e4m3", 1)
+        # p of every (row, head, key), and the largest weight of a row
+        s = torch.einsum("ihd,jd->ihj", c.q[at:at + n].double(), k[:, 0]) / math.sqrt(d)
+        s = s.masked_fill((torch.arange(m) > m - n + torch.arange(n)[:, None])[:, None], -math.inf)
+        w = (torch.softmax(s, -1) * 2.0 ** e).amax(-1)
+        more = 3 * 2.0 ** -22 * (40 + 32)        # as in check(): exponents up to 40 from zero
+        tol_o = tol_o + A * 2 * more + m * 448 * 2.0 ** -32 * w[..., None]
+        tol_l = tol_l + more
+        assert ((out[at:at + n].double() - o_ref).abs() <= tol_o).all()
+        assert ((lse[:, at:at + n].double() - l_ref).abs() <= tol_l).all()
+        at += n
