@@ -291,7 +291,7 @@ def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspac
         if lse.dtype is not torch.float32 or lse.get_device() != idx:
             _refuse(lse, "lse", torch.float32, idx)
         s = lse.shape
-        if len(s) != 2 or s[0] != plan.H or s[1] < plan.T or lse.stride(1) != 1:
+        if len(s) != 2 or s[0] != plan.H or s[1] < plan.T or (s[1] > 1 and lse.stride(1) != 1):
             raise ValueError(f"lse: expected [{plan.H}, {plan.T} or more] with rows contiguous, got {tuple(s)}")
         tl = _rowstat(lse.data_ptr(), 0, 0, lse.stride(0))
     wp, wn = None, 0
