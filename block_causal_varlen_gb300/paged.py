@@ -57,7 +57,7 @@ class PagedCache:
             for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")):
                 if t is None or t.dtype != torch.uint8 or t.shape != k.shape[:3] or t.device != k.device:
                     raise ValueError(f"{n}: an e4m3 cache needs uint8 exponents [pages, page_size, Hkv] on its device")
-            if k_exp.stride() != v_exp.stride():
+            if any(n > 1 and a != b for n, a, b in zip(k.shape, k_exp.stride(), v_exp.stride())):
                 raise ValueError("k_exp and v_exp must have the same strides")
         else:
             raise TypeError(f"cache dtype {k.dtype}, expected bfloat16 or float8_e4m3fn")
