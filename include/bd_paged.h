@@ -51,7 +51,8 @@ typedef enum {
    * the NaN codes 0x7f and 0xff in rows of byte 255 only; their V rows take the exponent
    * bd_cache_write would, or one near it: bd_paged_attn may hold a key's weight p * 2^e (p: its
    * probability, e: its V row's exponent) to no more than 2^-32 of the row's largest, so that
-   * zeros of a high byte, say, would hide the keys that matter. */
+   * zeros of a high byte, say, would hide the keys that matter (bd_cache_write's zeros, of
+   * byte 67, hide nothing above 2^-83 of a key's p * v). */
   BD_CACHE_E4M3 = 1
 } bd_cache_fmt;
 

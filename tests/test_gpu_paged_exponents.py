@@ -20,13 +20,15 @@ def _gpu():
     bd.load()
 
 
-def check(case, out, lse, span=0):
+def check(case, out, lse, span=0, zeros=False):
     """Against the oracle under pu.tolerances, where P is fp16 for all sequences that the
     few-rows kernel takes (up to 48 pairs of a K/V head). span: V's exponents reach as far from
     zero; the running maximum includes them there, so a score's distance from it and the
     sum's logarithm reach span + 8 + 24 (a margin of 2^8, 2^24 keys): their roundings and the
     logarithm's error relative to itself are within 2^-22 of that each (2^-24 for the
-    roundings; 2^-22 is the approximate logarithm's bound), as is that of their sum."""
+    roundings; 2^-22 is the approximate logarithm's bound), as is that of their sum. zeros: V has
+    zero rows, which count as codes of exponent -60: a weight is within 2^-32 of theirs, 2^-60 at
+    most, times a code of at most 448 for each key."""
     at = 0
     for b, (n, kv) in enumerate(zip(case.new, case.kv)):
         k, v = case.rows(b)
@@ -36,6 +38,8 @@ def check(case, out, lse, span=0):
         if span:
             more = 3 * 2.0 ** -22 * (span + 32)
             tol_l, tol_o = tol_l + more, tol_o + A * 2 * more
+        if zeros:
+            tol_o = tol_o + kv * 448 * 2.0 ** -92
         got, gl = out[at:at + n].double(), lse[:, at:at + n].double()
         assert torch.isfinite(got).all() and torch.isfinite(gl).all()
         bad = (gl - l_ref).abs() > tol_l
@@ -85,6 +89,21 @@ def test_large_rows_beside_zeros(large, d, new, kv):
 def test_large_rows_in_a_long_context(e, score, new):
     c = spread([new], [65536], 128, score, e, [0.6])
     check(c, *pu.run_attention(c), span=60)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new,kv", [([1], [21]), ([3, 12], [400, 3000])])
+@pytest.mark.parametrize("vmag", [(-40, -30), (-7, 15), (30, 58)])
+def test_most_rows_zeros(vmag, new, kv, d):
+    """Peaked scores that mostly fall on zero rows of V, as bd_cache_write stores them."""
+    c = pu.Case(new, kv, 8, 2, d, page=32, fmt="e4m3", seed=d, vmag=vmag, kmag=(-3, 1), qscale=8.0)
+    codes, ve = c.v.view(torch.uint8).cpu(), c.ve.cpu()
+    zero = (torch.rand(ve.shape, generator=torch.Generator().manual_seed(d)) < 0.9) & c.used[..., None]
+    codes[zero], ve[zero] = 0, 67
+    c.v.view(torch.uint8).copy_(codes.cuda())
+    c.ve.copy_(ve.cuda())
+    c.vd = op.dequantise(codes, ve)
+    check(c, *pu.run_attention(c), span=60, zeros=True)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
