@@ -103,7 +103,7 @@ int32_t make_tmap_group_bf16(CUtensorMap* map, const bd_tensor* t, int64_t heads
 }
 
 int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int64_t heads, int64_t d, int esize,
-                        const char* name, int box_rows, int box_pieces, bool neighbours) {
+                        const char* name, int box_rows, bool neighbours) {
   auto fn = encode_fn();
   if (!fn) return fail(BD_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (no CUDA driver?)");
   const int64_t row_bytes = d * esize, piece = row_bytes < 128 ? row_bytes : 128;
@@ -113,7 +113,7 @@ int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int
   cuuint64_t dims[5] = {cuuint64_t(piece / esize), cuuint64_t(t->rows), cuuint64_t(row_bytes / piece), cuuint64_t(heads),
                         cuuint64_t(pages)};
   cuuint64_t strides[4] = {cuuint64_t(sr), cuuint64_t(piece), cuuint64_t(sh), cuuint64_t(sp)};
-  cuuint32_t box[5] = {cuuint32_t(piece / esize), cuuint32_t(box_rows), cuuint32_t(box_pieces), 1, 1};
+  cuuint32_t box[5] = {cuuint32_t(piece / esize), cuuint32_t(box_rows), 1, 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   // without neighbours no promotion past a row's piece: with rows of several heads side by
   // side it would fetch the neighbouring heads' bytes, for other SMs at other times

@@ -24,8 +24,9 @@
 //     contraction order of q . k is permuted so that a lane reads 32 neighbouring
 //     codes, the row order of V^T so that it reads 16 of a V row, both free of bank
 //     conflicts. Exponents never touch the codes: K's is a factor of the score, V's an
-//     addend of the base-2 exponent (m is then the maximum of s_j + e_j). q as fp16 is
-//     exact too: each row is scaled by a power of two first.
+//     addend of the base-2 exponent (m is then the maximum of s_j + e_j, l still the sum of
+//     2^(s_j - m)). q is fp16 as well, each row scaled by a power of two to a maximum of 2^14
+//     first: exact but for what is below 2^-31 of the row's largest, zero below 2^-40.
 // P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-8 relative at
 // most, like O itself), fp16 for e4m3 (2^-11; its subnormals, p 2^e below 2^-21 of the
 // row's largest, to 2^-32 of that), scaled by 2^7 for their sake.
@@ -913,8 +914,8 @@ int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& 
   const bool near = gang_of(w[PH_HKV]) > 1;
   CUtensorMap mk, mv;
   int32_t st;
-  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, 1, near))) return st;
-  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, 1, near))) return st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, near))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, near))) return st;
   const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB>, kDecCtas, Cfg::kThreads, Cfg::kSmem, s, mk, mv, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
 }

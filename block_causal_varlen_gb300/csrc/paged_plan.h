@@ -53,7 +53,7 @@ enum : int {
   PH_OFF_DEC,      // few-rows kernel: its pieces, CTA after CTA,
   PH_NDEC,         // their number,
   PH_NDECM,        // the joins of its split blocks,
-  PH_DECM_WIDE,    // whether one of them has more than kWideJoin parts,
+  PH_DECM_WIDE,    // whether their rows get a CTA each (by kWideJoin, kWideJoinFew and kWideCtas),
   PH_DEC_LIVE,     // the most rows of a block in use,
   PH_DEC_ROWS,     // and the rows of a block
   PH_OFF_TILE,     // the same for the tile kernel

@@ -823,8 +823,8 @@ int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, con
   CUtensorMap mq, mk, mv;
   int32_t st;
   if ((st = make_tmap_group_bf16(&mq, q, w[PH_H], d, "q", G, 128 / G))) return st;
-  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", rows, 1, false))) return st;
-  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", rows, 1, false))) return st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", rows, false))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", rows, false))) return st;
   if (c->fmt == BD_CACHE_BF16)
     return d == 64 ? launch_tile_t<64, BD_CACHE_BF16>(mq, mk, mv, a, s)
            : d == 128 ? launch_tile_t<128, BD_CACHE_BF16>(mq, mk, mv, a, s)
