@@ -152,8 +152,7 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // up to 2^60 for a key, which a single factor, zero below 2^-126, would lose while the
 // product still counts (l is 2^-60 at least in the end). O's terms have their 2^e_j already.
 __device__ __forceinline__ float weigh_l(float l, float x) {
-  const float h = ex2(0.5f * x);
-  return x > -120.f ? l * ex2(x) : l * h * h;
+  return l * ex2(fmaxf(x, -64.f)) * ex2(fminf(x + 64.f, 0.f));
 }
 
 // Transpose of an 8 x 8 matrix of 16-bit values: a lane's pair (row lane / 4, columns
@@ -164,7 +163,9 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-template <int D, int FMT, int NB>
+// BEHIND: launched behind the tile kernel of the same call (a parameter looked at in the kernel
+// instead costs 0.1 us of the smallest calls' 3.7).
+template <int D, int FMT, int NB, bool BEHIND>
 __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     bd_paged_dec_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const AttnArgs a) {
@@ -187,28 +188,33 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * kChunk * 8;
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffDecRec + blockIdx.x * kRecordWords;
+  if constexpr (BEHIND) {
+    if (threadIdx.x == 0) abort_flag[1] = take_go(a.go + blockIdx.x);
+    __syncthreads();
+    if (!abort_flag[1]) grid_wait();
+    else fence_proxy_async_all();
+  } else {
+    grid_wait();
+  }
+  const int p0 = rec[RC_P0], p1 = rec[RC_P1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
-    *abort_flag = 0;
   }
+  if (p0 == p1) {
+    if constexpr (BEHIND) grid_wait();
+    return;
+  }
+  const int32_t* pieces = plan + plan[PH_OFF_DEC];
+  auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
+  if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
     // a chunk's arrivals: the copies' and, e4m3, every lane's exponent word
     for (int s = 0; s < NST; ++s) mbar_init(bars + 8 * s, F8 ? 33 : 1);
     fence_barrier_init();
   }
-  if (a.go && threadIdx.x == 0) abort_flag[1] = take_go(a.go + blockIdx.x);
   __syncthreads();
-  if (!a.go || !abort_flag[1]) grid_wait();
-  else fence_proxy_async_all();
-  const int p0 = rec[RC_P0], p1 = rec[RC_P1];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join: it waits for this grid's end
-  if (p0 == p1) {
-    grid_wait();
-    return;
-  }
-  const int32_t* pieces = plan + plan[PH_OFF_DEC];
-  auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
   const int G = a.G, causal = a.causal, pshift = a.page_shift;
 
   const int brows = min(1 << pshift, kChunk);  // rows of a copy: a chunk's keys lie in one page or, of pages of 16, in two
@@ -665,7 +671,8 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
 #pragma unroll
       for (int w = 0; w < NW; w += PW) {
         const float mw = ml[(w * 8 * NB + r) * 2];
-        L += mw == -CUDART_INF_F ? 0.f : weigh_l(ml[(w * 8 * NB + r) * 2 + 1], mw - M);
+        const float lw = ml[(w * 8 * NB + r) * 2 + 1];
+        L += mw == -CUDART_INF_F ? 0.f : F8 ? weigh_l(lw, mw - M) : lw * ex2(mw - M);
       }
       inv[r] = M == -CUDART_INF_F ? 0.f : 1.f / L;
       orow[r] = int64_t(t) * a.o_sr + int64_t(h) * a.o_sh;
@@ -727,7 +734,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     }
     __syncthreads();
   }
-  grid_wait();  // (behind the tile kernel: who waits for this grid's end, waits for that one's)
+  if constexpr (BEHIND) grid_wait();  // (who waits for this grid's end, waits for the tile kernel's)
   if (!ok) {
     // every copy issued has been waited for in turn; wait (with a limit) for those a
     // wait gave up on, then say so
@@ -898,14 +905,14 @@ __global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArg
   }
 }
 
-template <int D, int FMT, int NB>
-int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+template <int D, int FMT, int NB, bool BEHIND>
+int32_t launch_dec_tb(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
   using Cfg = DecCfg<D, FMT, NB>;
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(bd_paged_dec_kernel<D, FMT, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(bd_paged_dec_kernel<D, FMT, NB, BEHIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged few-rows)");
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
@@ -916,8 +923,13 @@ int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& 
   int32_t st;
   if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, near))) return st;
   if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, near))) return st;
-  const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB>, kDecCtas, Cfg::kThreads, Cfg::kSmem, s, mk, mv, a);
+  const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB, BEHIND>, kDecCtas, Cfg::kThreads, Cfg::kSmem, s, mk, mv, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
+}
+
+template <int D, int FMT, int NB>
+int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+  return a.go ? launch_dec_tb<D, FMT, NB, true>(w, c, a, s) : launch_dec_tb<D, FMT, NB, false>(w, c, a, s);
 }
 
 template <int D, int FMT>

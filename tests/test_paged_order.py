@@ -38,14 +38,17 @@ def test_every_kernel_waits_before_its_first_read():
         assert wait, (f, name)
         early = re.search(READ, body[:wait.start()])
         assert early is None, (f, name, early and early.group(0))
-        # a wait that may be passed over has the other form of it beside it
-        line = body[body.rfind("\n", 0, wait.start()):wait.end()]
-        if "if" in line:
-            assert "take_go" in line and re.search(r"if \(!a\.go \|\| [^\n]*\) grid_wait\(\);\n\s*else fence_proxy_async_all\(\);", body), name
-            assert re.search(READ, body[:body.index("else fence_proxy_async_all()")]) is None, name
-            # and no CTA ends sooner than the grid in front of it
-            assert re.search(r"if \(p0 == p1\) \{\s*grid_wait\(\);\s*return;", body), name
-            assert body.rindex("grid_wait()") > body.rindex("for (int p = p0; p < p1; ++p)"), name
+        # what is not this wait takes a word instead, orders the copies behind it as well, and ends
+        # no sooner than the grid in front of it
+        if "take_go" in body:
+            m = re.search(r"if constexpr \(BEHIND\) \{\s*if \(threadIdx\.x == 0\) abort_flag\[1\] = take_go\([^;]*;\s*__syncthreads\(\);\s*"
+                          r"if \(!abort_flag\[1\]\) grid_wait\(\);\s*else fence_proxy_async_all\(\);\s*\} else \{\s*grid_wait\(\);\s*\}", body)
+            assert m and re.search(READ, body[:m.end()]) is None, name
+            assert re.search(r"if \(p0 == p1\) \{\s*if constexpr \(BEHIND\) grid_wait\(\);\s*return;", body), name
+            assert body.rindex("if constexpr (BEHIND) grid_wait()") > body.rindex("for (int p = p0; p < p1; ++p)"), name
+        else:
+            line = body[body.rfind("\n", 0, wait.start()):wait.start()]
+            assert line.strip() == "", (name, line)
     assert {"bd_cache_write_kernel", "bd_cache_read_kernel", "bd_paged_dec_kernel", "bd_paged_tile_kernel", "bd_paged_merge_kernel",
             "bd_paged_wide_merge_kernel", "bd_paged_tile_merge_kernel"} == set(names)
 
