@@ -32,7 +32,8 @@
 // row's largest, to 2^-32 of that), scaled by 2^7 for their sake.
 //
 // 64 ragged sequences of 500-16000 rows, 8 K/V heads of 128: bf16 (4 pairs a head) 164 us,
-// 6.8 TB/s; e4m3 (2 pairs) 90 us, 6.2 TB/s. One sequence of 4096 rows 7.5 us in a graph.
+// 6.8 TB/s; e4m3 (2 pairs) 92 us, 6.1 TB/s. One sequence of 4096 rows 7.7 us in a graph.
+// (Blocks of 32 bf16 rows at d 128 and 256 spill some 30 registers, 132 bytes.)
 //
 // A row takes nothing from a key it does not see, whatever is there: V's infinities
 // and NaN, which a probability of zero would turn to NaN, stay out of the products of

@@ -224,7 +224,7 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
 
 // Few-rows blocks: short against their keys, cheap to join: cut evenly, unless whole blocks
 // take no more than a join does longer (8 units of 32 keys, 4 at head dim 256: one sequence
-// of 128 keys takes 4.5 us whole and 5.1 cut, of 256 keys 5.9 and 5.3, and a launch less on
+// of 128 keys takes 4.4 us whole and 5.6 cut, of 256 keys 5.9 and 5.8, and a launch less on
 // the host). A piece's own cost (its q, adding up the warps' results, the pipeline's start) is some
 // 8 units of 32 keys (64 ragged e4m3 sequences of 32 heads: 352 us counting 6, 348 counting 8,
 // 351 counting 14). One head's blocks are cut into as many stretches as there are gangs

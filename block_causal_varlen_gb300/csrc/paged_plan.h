@@ -21,8 +21,8 @@ constexpr int dec_most_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 48; } 
 constexpr int dec_block_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 16; }
 constexpr int kDecSlotRows = 32;
 // Rows of the joins get a CTA each, not a warp, if a block has more parts than kWideJoin, or
-// more than kWideJoinFew and every row finds a CTA at once (one sequence of 512 keys: 7.0 us by
-// warps, 5.9 by CTAs).
+// more than kWideJoinFew and every row finds a CTA at once (one sequence of 512 keys: 8.7 us by
+// warps, 6.3 by CTAs).
 constexpr int kWideJoin = 16, kWideJoinFew = 4, kWideCtas = 4 * kPagedSms;
 constexpr int kDecUnit = 32;   // keys by which the few-rows kernel's work is cut
 // Tiles (of 128 / G new rows x G heads) of one K/V head that share a key tile in the

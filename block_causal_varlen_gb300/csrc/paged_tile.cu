@@ -30,7 +30,9 @@
 //
 // What bounds it is the chain softmax -> P V -> next S of a slot: a tile pair takes 3250
 // cycles for 2048 of products (4000 with the conversion beside it), a block some 4500
-// more. 4096 rows over 16384 keys, 32 / 8 heads of 128: bf16 650 us (1480 TFLOP/s), e4m3 793.
+// more. 4096 rows over 16384 keys, 32 / 8 heads of 128: bf16 653 us (1473 TFLOP/s), e4m3 792, with
+// pauses between calls; bf16 681-696 in a row, under the power cap. (The e4m3 kernels spill some 10
+// registers, 36-44 bytes.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>

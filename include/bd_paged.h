@@ -129,7 +129,8 @@ BD_API int32_t bd_cache_read(const void* plan_host, const void* plan_dev, const 
                              bd_tensor* v, void* stream);
 
 /* Workspace bytes of bd_paged_attn: partial results of rows whose keys are split
- * over several blocks. A function of the plan's key and d only. */
+ * over several blocks. A function of the plan's key and d only: for the most there can be
+ * (5 to 20 MB for few rows, 20 to 40 MB for more of them), however few are cut. */
 BD_API int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes);
 
 /* bd_paged_attn -- O (bf16) and LSE (fp32, may be NULL) of the new rows over their
