@@ -129,3 +129,27 @@ def test_a_dropped_plan_is_read_to_the_end(ambient):
     want = torch.zeros_like(pool)
     want[torch.from_numpy(lists[0]).cuda()] = rows.view(n, P, 2, 64)
     assert torch.equal(pool, want)
+
+
+@pytest.mark.gpu
+def test_capture_over_a_plans_own_memory():
+    """Captured on another stream than the upload's, replayed while the plan is kept and other
+    plans come and go."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    c = pu.Case([60, 1, 3], [2000, 700, 90], 8, 2, 128, page=32)
+    want = pu.run_attention(c)
+    q = c.q.cuda()
+    out, lse = torch.empty_like(q), torch.empty(8, c.T, device="cuda")
+    ws = torch.empty(bd.bd_paged_attn_workspace(c.plan), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        bd.bd_paged_attn(c.plan, q, c.cache, out, lse, ws)
+    for _ in range(3):
+        for _ in range(4):
+            c.make_plan().upload()
+        c.plan.upload()
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu(), want[0]) and torch.equal(lse.cpu(), want[1])
