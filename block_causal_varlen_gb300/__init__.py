@@ -15,7 +15,8 @@ Tensor layouts (all strided views are accepted; the head dim is contiguous):
 A whole packed sequence [B, S, H, d] is the view [B, cp, L, H, d].
 
 Continuing documents over a paged K/V cache (PagedPlan, PagedCache, bd_cache_write,
-bd_cache_read, bd_paged_attn): see paged.py and include/bd_paged.h.
+bd_cache_append, bd_cache_read, bd_paged_attn, and over selected blocks of it BlockBounds,
+bd_block_bounds, bd_block_select, bd_sparse_attn): see paged.py and include/bd_paged.h.
 """
 from __future__ import annotations
 
@@ -27,16 +28,18 @@ import torch
 from . import _abi
 from ._abi import (BD_BWD_DQ_ZEROED, BD_BWD_OWNER_ROWS, BD_KV_GATHER, BD_KV_WINDOW, BDError,  # noqa: F401
                    bd_chunk_hdr, bd_rowstat, bd_segment_t, bd_tensor, check, load)
-from .paged import (BD_CACHE_BF16, BD_CACHE_E4M3, PagedCache, PagedPlan, bd_cache_read, bd_cache_write,  # noqa: F401
-                    bd_paged_attn, bd_paged_attn_workspace, bd_paged_plan_build, bd_paged_plan_bytes,
-                    bd_paged_plan_key, paged_attn)
+from .paged import (BD_CACHE_BF16, BD_CACHE_E2M1, BD_CACHE_E4M3, BlockBounds, PagedCache, PagedPlan, Rope,  # noqa: F401
+                    bd_block_bounds, bd_block_select, bd_cache_append, bd_cache_read, bd_cache_write, bd_paged_attn,
+                    bd_paged_attn_workspace, bd_paged_plan_build, bd_paged_plan_bytes, bd_paged_plan_key, bd_rope_phases,
+                    bd_sparse_attn, bd_sparse_plan_build, bd_sparse_plan_bytes, paged_attn, sparse_attn)
 
 __all__ = ["Plan", "bd_segment", "bd_doc_ids_to_cu", "bd_exchange_plan", "bd_attn_fwd", "bd_attn_fwd_ex", "bd_attn_bwd",
            "bd_attn_bwd_ex", "bd_attn_bwd_pre", "bd_attn_bwd_main", "bd_attn_bwd_main_ex", "bd_owner_sum",
            "bd_check_status", "bd_attn_bwd_workspace", "attn_fwd", "attn_bwd", "BD_KV_GATHER", "BD_KV_WINDOW",
            "BD_BWD_OWNER_ROWS", "BD_BWD_DQ_ZEROED", "BDError", "load", "PagedCache", "PagedPlan", "bd_cache_write",
            "bd_cache_read", "bd_paged_attn", "bd_paged_attn_workspace", "bd_paged_plan_key", "paged_attn",
-           "BD_CACHE_BF16", "BD_CACHE_E4M3"]
+           "BD_CACHE_BF16", "BD_CACHE_E4M3", "BD_CACHE_E2M1", "Rope", "BlockBounds", "bd_rope_phases", "bd_cache_append",
+           "bd_block_bounds", "bd_block_select", "bd_sparse_attn", "sparse_attn"]
 
 _HDR_FIELDS = ("S", "cp", "rank", "L", "row_offset", "s_valid", "n_pad", "kv_start", "kv_end", "nseg")
 _SEG_FIELDS = ("doc", "q_start", "q_len", "k_start", "k_len", "diag_off")

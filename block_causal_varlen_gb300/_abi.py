@@ -29,6 +29,7 @@ BD_KV_WINDOW = 1
 
 BD_CACHE_BF16 = 0
 BD_CACHE_E4M3 = 1
+BD_CACHE_E2M1 = 4
 
 BD_BWD_OWNER_ROWS = 1
 BD_BWD_DQ_ZEROED = 2
@@ -79,6 +80,26 @@ class bd_paged_desc(C.Structure):
                 ("num_pages", C.c_int32), ("fmt", C.c_int32), ("causal", C.c_int32), ("q_len", C.POINTER(C.c_int32)),
                 ("kv_len", C.POINTER(C.c_int32)), ("pages", C.POINTER(C.c_int32)),
                 ("page_offsets", C.POINTER(C.c_int32))]
+
+
+class bd_rope(C.Structure):
+    _fields_ = [("phase", C.c_void_p), ("dim", C.c_int32), ("interleaved", C.c_int32), ("scale", C.c_float),
+                ("reserved", C.c_int32)]
+
+
+class bd_sparse_desc(C.Structure):
+    _fields_ = [("blocks", C.c_int32), ("first", C.c_int32), ("recent", C.c_int32), ("reserved", C.c_int32)]
+
+
+class bd_bounds(C.Structure):
+    _fields_ = [("code", C.c_void_p), ("stride_page", C.c_int64), ("stride_head", C.c_int64), ("stride_bound", C.c_int64),
+                ("exp", C.c_void_p), ("exp_stride_page", C.c_int64), ("exp_stride_head", C.c_int64),
+                ("num_pages", C.c_int32), ("reserved", C.c_int32)]
+
+
+class bd_blocks(C.Structure):
+    _fields_ = [("ptr", C.c_void_p), ("stride_row", C.c_int64), ("stride_head", C.c_int64), ("rows", C.c_int32),
+                ("reserved", C.c_int32)]
 
 
 EXPORTS = {
@@ -145,6 +166,19 @@ EXPORTS = {
     "bd_paged_attn_workspace": (C.c_int32, [C.c_void_p, C.POINTER(C.c_size_t)]),
     "bd_paged_attn": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_tensor), C.POINTER(bd_paged_cache),
                                   C.POINTER(bd_tensor), C.POINTER(bd_rowstat), C.c_void_p, C.c_size_t, C.c_void_p]),
+    "bd_rope_phases": (C.c_int32, [C.POINTER(C.c_double), C.c_int32, C.POINTER(C.c_uint64)]),
+    "bd_cache_append": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_tensor), C.POINTER(bd_tensor),
+                                    C.POINTER(bd_tensor), C.POINTER(bd_rope), C.POINTER(bd_paged_cache),
+                                    C.POINTER(bd_tensor), C.c_void_p]),
+    "bd_sparse_plan_bytes": (C.c_int32, [C.POINTER(bd_paged_desc), C.POINTER(bd_sparse_desc), C.POINTER(C.c_size_t)]),
+    "bd_sparse_plan_build": (C.c_int32, [C.POINTER(bd_paged_desc), C.POINTER(bd_sparse_desc), C.c_void_p, C.c_size_t]),
+    "bd_block_bounds": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_paged_cache), C.POINTER(bd_bounds),
+                                    C.c_void_p]),
+    "bd_block_select": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_tensor), C.POINTER(bd_bounds),
+                                    C.POINTER(bd_blocks), C.c_void_p]),
+    "bd_sparse_attn": (C.c_int32, [C.c_void_p, C.c_void_p, C.POINTER(bd_tensor), C.POINTER(bd_paged_cache),
+                                   C.POINTER(bd_blocks), C.POINTER(bd_tensor), C.POINTER(bd_rowstat), C.c_void_p,
+                                   C.c_size_t, C.c_void_p]),
     "bd_check_status": (C.c_int32, [C.c_void_p, C.c_int32, C.c_void_p]),
     "bd_selftest_bounded_wait": (C.c_int32, [C.c_void_p, C.c_uint32, C.c_void_p]),
     "bd_last_error": (C.c_char_p, []),

@@ -1,0 +1,232 @@
+// Appending rows to a paged K/V cache with the position rotation on the way, on sm_103a.
+//
+// Pair i of a head's turned elements, at position p: (x, y) -> scale (x cos a - y sin a,
+// y cos a + x sin a), a = p f_i. The angle is kept as turns: the host gives f_i / 2 pi modulo 1
+// in units of 2^-64 (bd_rope_phases), so p times it modulo 2^64 is the angle's fraction of a
+// turn, whatever p, and its upper 32 bits lose 2^-33 of a turn. No table of angles is read.
+//
+// A group of d / 8 lanes takes some heads of a row, 8 elements a lane: cosines and sines are made
+// once and used for all of them. Pairs d / 2 apart meet by a shuffle. K goes on as
+// bf16 into the cache's format (paged_quant.cuh), as bd_cache_write stores it.
+//
+// What bounds it is HBM, or for a few rows the launch and the chain plan - rows - stores; few
+// rows are cut into many groups of few heads each.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "paged.h"
+#include "paged_quant.cuh"
+
+namespace bd {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr uint32_t kFull = 0xffffffffu;
+
+struct AppendArgs {
+  const int32_t* plan;
+  const uint64_t* phase;
+  float scale;
+  int32_t rot;                               // turned elements of a head
+  int32_t H, Hkv;                            // H = 0: no q
+  int32_t per, chunks;                       // heads of a group, groups of a row
+  const uint8_t *q, *k, *v;                  // packed bf16 rows, strides in bytes
+  uint8_t* qo;
+  int64_t q_sr, q_sh, k_sr, k_sh, v_sr, v_sh, o_sr, o_sh;
+  uint8_t *kc, *vc;                          // cache bytes
+  int64_t k_cp, k_cr, k_ch, v_cp, v_cr, v_ch;
+  uint8_t *k_exp, *v_exp;
+  int64_t e_sp, e_sr, e_sh;
+};
+
+template <int D, int FMT, bool PAIRS>
+__global__ void __launch_bounds__(kThreads) bd_cache_append_kernel(const AppendArgs a) {
+  constexpr int LPR = D / 8, RPB = kThreads / LPR;
+  constexpr int NF = PAIRS ? 4 : 8;  // frequencies of a lane
+  const int sub = threadIdx.x % LPR;
+  const int32_t* plan = a.plan;
+  // (the phases are weights, and not written by the kernels in front of this one, but by whom is
+  // not known here: everything is read behind the wait)
+  grid_wait();
+  const uint32_t T = uint32_t(plan[PH_T]), n = T * uint32_t(a.chunks);
+  const int32_t* tok = plan + plan[PH_OFF_TOK];
+  const int32_t* where = plan + plan[PH_OFF_POS];
+  const int shift = plan[PH_PAGE_SHIFT];
+  const int half = a.rot / 16;                    // lanes of half of the turned elements
+  const bool turns = sub < 2 * half;
+  const bool upper = !PAIRS && sub >= half;       // the second elements of their pairs
+  const int other = PAIRS ? 0 : upper ? sub - half : sub + half;
+  const int partner = int(threadIdx.x & 31u) - sub + (turns ? other : sub);
+  uint64_t f[NF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i) f[i] = turns ? a.phase[PAIRS ? sub * 4 + i : (upper ? sub - half : sub) * 8 + i] : 0ull;
+
+  // (whole warps stay together for the shuffles: groups past the last repeat the last)
+  for (uint32_t g0 = blockIdx.x * uint32_t(RPB); g0 < n; g0 += gridDim.x * uint32_t(RPB)) {
+    const bool there = g0 + threadIdx.x / LPR < n;
+    const uint32_t g = min(g0 + threadIdx.x / LPR, n - 1), t = g / uint32_t(a.chunks);
+    const int h0 = int(g - t * uint32_t(a.chunks)) * a.per, h1 = min(h0 + a.per, a.H + 2 * a.Hkv);
+    const int32_t row = tok[t], pos = where[t];
+    const int64_t pg = row >> shift, ro = row & ((1 << shift) - 1);
+    const bool place = there && row >= 0;
+    auto from = [&](int h) {
+      return h < a.H           ? a.q + int64_t(t) * a.q_sr + int64_t(h) * a.q_sh
+             : h < a.H + a.Hkv ? a.k + int64_t(t) * a.k_sr + int64_t(h - a.H) * a.k_sh
+                               : a.v + int64_t(t) * a.v_sr + int64_t(h - a.H - a.Hkv) * a.v_sh;
+    };
+    constexpr int U = 4;  // heads in flight
+    uint4 x[U];
+    auto load = [&](int h) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) x[u] = __ldcs(reinterpret_cast<const uint4*>(from(min(h + u, h1 - 1))) + sub);
+    };
+    load(h0);
+    float c[NF], s[NF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      const int32_t turn = int32_t(uint32_t((f[i] * uint64_t(uint32_t(max(pos, 0)))) >> 32));
+      sincospif(float(turn) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
+      c[i] *= a.scale;
+      s[i] *= a.scale;
+    }
+    for (int hb = 0; hb < a.per; hb += U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (hb + u >= a.per) break;
+        const int h = h0 + hb + u;                 // past h1 the last head comes again, and is not stored
+        uint4 y = x[u];
+        uint32_t z[4] = {y.x, y.y, y.z, y.w};
+        if constexpr (!PAIRS) {
+          z[0] = __shfl_sync(kFull, y.x, partner); z[1] = __shfl_sync(kFull, y.y, partner);
+          z[2] = __shfl_sync(kFull, y.z, partner); z[3] = __shfl_sync(kFull, y.w, partner);
+        }
+        if (turns && h < a.H + a.Hkv && pos >= 0) {
+          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+          uint32_t r[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = bf16_lo(w[i]), hi = bf16_hi(w[i]);
+            if constexpr (PAIRS) {
+              r[i] = bf16_pair(lo * c[i] - hi * s[i], hi * c[i] + lo * s[i]);
+            } else {
+              const float pl = bf16_lo(z[i]), ph = bf16_hi(z[i]);
+              const float sl = upper ? s[2 * i] : -s[2 * i], sh = upper ? s[2 * i + 1] : -s[2 * i + 1];
+              r[i] = bf16_pair(lo * c[2 * i] + pl * sl, hi * c[2 * i + 1] + ph * sh);
+            }
+          }
+          y = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+        const bool mine = h < h1, is_q = h < a.H, is_k = h < a.H + a.Hkv;
+        if (mine && is_q && there) __stcs(reinterpret_cast<uint4*>(a.qo + int64_t(t) * a.o_sr + int64_t(h) * a.o_sh) + sub, y);
+        const bool store = place && mine && !is_q;
+        if (!__any_sync(kFull, store)) continue;
+        const int64_t hk = is_q ? 0 : is_k ? h - a.H : h - a.H - a.Hkv;
+        uint8_t* d = is_k ? a.kc + pg * a.k_cp + ro * a.k_cr + hk * a.k_ch : a.vc + pg * a.v_cp + ro * a.v_cr + hk * a.v_ch;
+        if constexpr (FMT == BD_CACHE_BF16) {
+          if (store) reinterpret_cast<uint4*>(d)[sub] = y;
+        } else {
+          uint8_t* e = (is_k ? a.k_exp : a.v_exp) + pg * a.e_sp + ro * a.e_sr + hk * a.e_sh;
+          store_quantised<LPR, FMT>(y, sub, store, d, e);
+        }
+      }
+      if (hb + U < a.per) load(h0 + hb + U);
+    }
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_append(bool pairs, int grid, cudaStream_t s, const AppendArgs& a) {
+  return pairs ? launch_kernel(bd_cache_append_kernel<D, FMT, true>, grid, kThreads, 0, s, a)
+               : launch_kernel(bd_cache_append_kernel<D, FMT, false>, grid, kThreads, 0, s, a);
+}
+
+template <int FMT>
+cudaError_t launch_append(int d, bool pairs, int grid, cudaStream_t s, const AppendArgs& a) {
+  return d == 64    ? launch_append<64, FMT>(pairs, grid, s, a)
+         : d == 128 ? launch_append<128, FMT>(pairs, grid, s, a)
+                    : launch_append<256, FMT>(pairs, grid, s, a);
+}
+
+}  // namespace
+
+}  // namespace bd
+
+using namespace bd;
+
+extern "C" int32_t bd_rope_phases(const double* inv_freq, int32_t n, uint64_t* out) {
+  if (n < 0 || (n > 0 && (!inv_freq || !out))) return fail(BD_ERR_ARG, "inv_freq or out is NULL, or n negative");
+  // 1 / 2 pi in two parts; the products are exact to some 100 bits
+  constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  for (int32_t i = 0; i < n; ++i) {
+    const double f = inv_freq[i];
+    if (!std::isfinite(f)) return fail(BD_ERR_ARG, "inv_freq[%d] is not finite", i);
+    const double a = f * hi, b = std::fma(f, hi, -a) + f * lo;
+    // a and b modulo 1, in [0, 1), as 64-bit fractions
+    auto turns = [](double x) {
+      x -= std::floor(x);
+      const double u = std::ldexp(x, 32), w = std::floor(u);  // x < 1, or 1 by rounding: both parts wrap
+      return (uint64_t(w) << 32) + uint64_t(std::ldexp(u - w, 32));
+    };
+    out[i] = std::isfinite(a) ? turns(a) + turns(b) : 0;
+  }
+  return ok();
+}
+
+extern "C" int32_t bd_cache_append(const void* plan_host, const void* plan_dev, const bd_tensor* q, const bd_tensor* k,
+                                   const bd_tensor* v, const bd_rope* rope, const bd_paged_cache* cache, bd_tensor* q_out,
+                                   void* stream) {
+  const int32_t* w = nullptr;
+  int32_t st = check_write(plan_host, plan_dev, k, v, cache, &w);
+  if (st) return st;
+  if (!rope || !rope->phase || reinterpret_cast<uintptr_t>(rope->phase) % 8)
+    return fail(BD_ERR_ARG, "rope: NULL, or phase NULL or not 8-byte aligned");
+  if (rope->dim <= 0 || rope->dim % 16 || rope->dim > w[PH_D])
+    return fail(BD_ERR_ARG, "rope of %d elements (a multiple of 16, at most the head dim %d)", rope->dim, w[PH_D]);
+  if (rope->interleaved != 0 && rope->interleaved != 1) return fail(BD_ERR_ARG, "rope: interleaved must be 0 or 1");
+  if (!q != !q_out) return fail(BD_ERR_ARG, "q and q_out come together");
+  if (w[PH_T] == 0) return ok();
+  if (q) {
+    if ((st = check_tensor(q, "q", 2, 1, 1, w[PH_H], false))) return st;
+    if ((st = check_tensor(q_out, "q_out", 2, 1, 1, w[PH_H], false))) return st;
+    if (q->rows < w[PH_T] || q_out->rows < w[PH_T])
+      return fail(BD_ERR_ARG, "q/q_out rows %d/%d < %d new rows of the plan", q->rows, q_out->rows, w[PH_T]);
+  }
+  AppendArgs a = {};
+  a.plan = static_cast<const int32_t*>(plan_dev);
+  a.phase = rope->phase;
+  a.scale = rope->scale;
+  a.rot = rope->dim;
+  a.H = q ? w[PH_H] : 0;
+  a.Hkv = w[PH_HKV];
+  if (q) {
+    a.q = static_cast<const uint8_t*>(q->ptr); a.qo = static_cast<uint8_t*>(q_out->ptr);
+    a.q_sr = q->stride_row * 2; a.q_sh = q->stride_head * 2;
+    a.o_sr = q_out->stride_row * 2; a.o_sh = q_out->stride_head * 2;
+  }
+  a.k = static_cast<const uint8_t*>(k->ptr); a.v = static_cast<const uint8_t*>(v->ptr);
+  a.k_sr = k->stride_row * 2; a.k_sh = k->stride_head * 2; a.v_sr = v->stride_row * 2; a.v_sh = v->stride_head * 2;
+  const int64_t es = elem_bytes(cache->fmt);
+  a.kc = static_cast<uint8_t*>(cache->k.ptr); a.vc = static_cast<uint8_t*>(cache->v.ptr);
+  a.k_cp = cache->k.stride_b * es; a.k_cr = cache->k.stride_row * es; a.k_ch = cache->k.stride_head * es;
+  a.v_cp = cache->v.stride_b * es; a.v_cr = cache->v.stride_row * es; a.v_ch = cache->v.stride_head * es;
+  a.k_exp = cache->k_exp; a.v_exp = cache->v_exp;
+  a.e_sp = cache->exp_stride_page; a.e_sr = cache->exp_stride_row; a.e_sh = cache->exp_stride_head;
+  // heads of a group: as many as leave every SM 2048 lanes
+  const int heads = a.H + 2 * a.Hkv;
+  const int64_t lanes = int64_t(w[PH_T]) * heads * (w[PH_D] / 8);
+  a.per = int(lanes / (int64_t(kPagedSms) * 2048));
+  a.per = a.per < 1 ? 1 : a.per > 16 ? 16 : a.per;
+  a.chunks = (heads + a.per - 1) / a.per;
+  if (int64_t(w[PH_T]) * a.chunks > INT32_MAX) return fail(BD_ERR_CAPACITY, "new rows times heads past 2^31 - 1");
+  const int64_t blocks = (int64_t(w[PH_T]) * a.chunks * (w[PH_D] / 8) + kThreads - 1) / kThreads;
+  const int grid = int(blocks < kPagedSms * 8 ? blocks : kPagedSms * 8);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool pairs = rope->interleaved != 0;
+  const cudaError_t e = cache->fmt == BD_CACHE_BF16   ? launch_append<BD_CACHE_BF16>(w[PH_D], pairs, grid, s, a)
+                        : cache->fmt == BD_CACHE_E4M3 ? launch_append<BD_CACHE_E4M3>(w[PH_D], pairs, grid, s, a)
+                                                      : launch_append<BD_CACHE_E2M1>(w[PH_D], pairs, grid, s, a);
+  if (e != cudaSuccess) return cuda_fail(e, "bd_cache_append_kernel launch");
+  return ok();
+}

@@ -102,11 +102,10 @@ int32_t make_tmap_group_bf16(CUtensorMap* map, const bd_tensor* t, int64_t heads
                    cuuint32_t(box_rows), cuuint32_t(box_heads));
 }
 
-int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int64_t heads, int64_t d, int esize,
-                        const char* name, int box_rows, bool neighbours) {
+int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int64_t heads, int64_t row_bytes, int esize,
+                        const char* name, int box_rows, bool neighbours, int piece) {
   auto fn = encode_fn();
   if (!fn) return fail(BD_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (no CUDA driver?)");
-  const int64_t row_bytes = d * esize, piece = row_bytes < 128 ? row_bytes : 128;
   const int64_t sh = heads <= 1 ? row_bytes : t->stride_head * esize;
   const int64_t sr = t->rows <= 1 ? row_bytes : t->stride_row * esize;
   const int64_t sp = pages <= 1 ? row_bytes : t->stride_b * esize;
@@ -119,9 +118,10 @@ int32_t make_tmap_pages(CUtensorMap* map, const bd_tensor* t, int64_t pages, int
   // side it would fetch the neighbouring heads' bytes, for other SMs at other times
   CUresult r = fn(map, esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, t->ptr, dims,
                   strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  piece == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  piece == 32   ? CU_TENSOR_MAP_SWIZZLE_32B
+                  : piece == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                   neighbours ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
-                  : piece == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  : piece < 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(BD_ERR_ALIGN, "%s: cuTensorMapEncodeTiled failed (%d)", name, int(r));
   return BD_OK;

@@ -1,6 +1,7 @@
 // Host-side helpers shared by the paged-cache entry points, and their kernels'
 // common arguments.
 #pragma once
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -56,11 +57,12 @@ __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.pr
 // Checks both plan copies and the cache against the plan.
 int32_t check_paged(const void* plan_host, const void* plan_dev, const bd_paged_cache* cache, const int32_t** w);
 
-// Exponent byte b of an e4m3 row as a factor 2^(b - 127); byte 255 marks a row
-// that held an infinity or a NaN.
-__device__ __forceinline__ float exp_factor(uint32_t b) {
-  return b == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float(b << 23);
-}
+// The same and the new rows' K and V (if there are any) for a call that stores them.
+int32_t check_write(const void* plan_host, const void* plan_dev, const bd_tensor* k, const bd_tensor* v,
+                    const bd_paged_cache* cache, const int32_t** w);
+
+// Checks the lists of a sparse plan's new rows.
+int32_t check_blocks(const bd_blocks* blocks, const int32_t* w);
 
 // Partial results: per slot m and l of its rows, then O [rows][d]. The few-rows
 // kernel's slots have kDecSlotRows rows, the tile kernel's tile_slot_rows(d): 128 for each
@@ -96,11 +98,16 @@ struct AttnArgs {
   int64_t e_sp, e_sr, e_sh;
   float scale_log2;
   int32_t G, causal, page_shift;
+  const int32_t* blocks;     // sparse plans: the rows' lists, strides in elements
+  int64_t b_sr, b_sh;
   unsigned long long* go;  // a word for each few-rows CTA if both kernels run, else NULL
 };
 
 int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, const bd_paged_cache* cache,
                     cudaStream_t stream);
+// The few-rows kernel; of a plan with lists of blocks if a.blocks is there.
 int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* cache, cudaStream_t stream);
+int32_t launch_dec_e2m1(const int32_t* w, const AttnArgs& a, const bd_paged_cache* cache, cudaStream_t stream);
+int32_t launch_dec_blocks(const int32_t* w, const AttnArgs& a, const bd_paged_cache* cache, cudaStream_t stream);
 
 }  // namespace bd

@@ -1,12 +1,7 @@
 // Writing K/V rows into a paged cache and reading sequences back out of it, on
 // sm_103a.
 //
-// An e4m3 cache holds, per (row, head), codes c_i and an exponent e with
-// x_i ~ c_i 2^e. e4m3 is a floating-point format, so a scale's mantissa would buy
-// next to nothing; a power of two makes the scaling exact in both directions: the
-// only rounding is that of x 2^-e to e4m3's four significant bits, and c 2^e is
-// exact in bf16. e = ceil(log2(max|x| / 448)) comes from the bits of max|x|:
-// 448 = 1.75 * 2^8, so with max|x| = f * 2^E, 1 <= f < 2, e = E - 8 (+ 1 if f > 1.75).
+// (paged_quant.cuh has the formats' arithmetic.)
 //
 // Both kernels are streams: what bounds them is HBM (or, for a few rows, the
 // launch). A thread takes 16 bytes of bf16 (8 values) of K and of V, so a head's
@@ -14,11 +9,10 @@
 // 128 written: bf16 37.5 us (6607 GB/s), e4m3 33.4 (5577); 49152 read back: bf16 62.1
 // (6483), e4m3 53.9 (5615). Walking the rows without a division each, or scaling bf16
 // pairs at once, changes nothing.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "paged.h"
+#include "paged_quant.cuh"
 
 namespace bd {
 
@@ -35,56 +29,6 @@ struct CacheArgs {
   uint8_t *kx, *vx;                // packed bf16 rows
   int64_t kx_sr, kx_sh, vx_sr, vx_sh;          // in bytes
 };
-
-// max|x| of 8 bf16 values as bits (the order of magnitudes is that of their bits)
-__device__ __forceinline__ uint32_t absmax8(const uint4& x) {
-  const uint32_t m = 0x7fff7fffu;
-  const uint32_t t = __vmaxu2(__vmaxu2(x.x & m, x.y & m), __vmaxu2(x.z & m, x.w & m));
-  return max(t & 0xffffu, t >> 16);
-}
-
-__device__ __forceinline__ uint32_t pack4_e4m3(float a, float b, float c, float d) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\t"
-      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
-      "mov.b32 %0, {lo, hi};\n\t}"
-      : "=r"(r)
-      : "f"(a), "f"(b), "f"(c), "f"(d));
-  return r;
-}
-
-// Quantises a row spread over LPR lanes (8 values each): codes, and the exponent byte.
-template <int LPR>
-__device__ __forceinline__ uint2 quantise8(const uint4& x, uint32_t* byte) {
-  uint32_t mx = absmax8(x);
-#pragma unroll
-  for (int s = LPR / 2; s > 0; s >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-  if (mx >= 0x7f80u) {
-    *byte = 255u;
-    return make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-  }
-  // bits of max|x|: exponent field E + 127, 7 mantissa bits (1.75 = 0x60); a value
-  // below the clamp, zero and subnormals among them, takes the lowest exponent
-  int e = int(mx >> 7) - 127 - 8 + ((mx & 0x7fu) > 0x60u ? 1 : 0);
-  e = min(60, max(-60, e));
-  *byte = uint32_t(e + 127);
-  const float f = __uint_as_float(uint32_t(127 - e) << 23);
-  auto lo = [&](uint32_t u) { return __uint_as_float(u << 16) * f; };
-  auto hi = [&](uint32_t u) { return __uint_as_float(u & 0xffff0000u) * f; };
-  return make_uint2(pack4_e4m3(lo(x.x), hi(x.x), lo(x.y), hi(x.y)), pack4_e4m3(lo(x.z), hi(x.z), lo(x.w), hi(x.w)));
-}
-
-// 4 codes times f as bf16 (exact: 4 significant bits and a power of two)
-__device__ __forceinline__ uint2 dequantise4(uint32_t c, float f) {
-  uint32_t a, b;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
-      : "=r"(a), "=r"(b)
-      : "r"(c));
-  const float2 x = __half22float2(*reinterpret_cast<__half2*>(&a)), y = __half22float2(*reinterpret_cast<__half2*>(&b));
-  __nv_bfloat162 p = __floats2bfloat162_rn(x.x * f, x.y * f), q = __floats2bfloat162_rn(y.x * f, y.y * f);
-  return make_uint2(*reinterpret_cast<uint32_t*>(&p), *reinterpret_cast<uint32_t*>(&q));
-}
 
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArgs a) {
@@ -111,17 +55,9 @@ __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArg
         reinterpret_cast<uint4*>(vd)[sub] = vx;
       }
     } else {
-      uint32_t kb, vb;
-      const uint2 kc = quantise8<LPR>(kx, &kb), vc = quantise8<LPR>(vx, &vb);
-      if (store) {
-        reinterpret_cast<uint2*>(kd)[sub] = kc;
-        reinterpret_cast<uint2*>(vd)[sub] = vc;
-        if (sub == 0) {
-          const int64_t eo = pg * a.e_sp + ro * a.e_sr + int64_t(h) * a.e_sh;
-          a.k_exp[eo] = uint8_t(kb);
-          a.v_exp[eo] = uint8_t(vb);
-        }
-      }
+      const int64_t eo = pg * a.e_sp + ro * a.e_sr + int64_t(h) * a.e_sh;
+      store_quantised<LPR, FMT>(kx, sub, store, kd, a.k_exp + eo);
+      store_quantised<LPR, FMT>(vx, sub, store, vd, a.v_exp + eo);
     }
   }
 }
@@ -171,6 +107,12 @@ __global__ void __launch_bounds__(kThreads) bd_cache_read_kernel(const CacheArgs
         if constexpr (FMT == BD_CACHE_BF16) {
           x[u] = __ldcs(reinterpret_cast<const uint4*>(ks) + sub);
           y[u] = __ldcs(reinterpret_cast<const uint4*>(vs) + sub);
+        } else if constexpr (FMT == BD_CACHE_E2M1) {
+          x[u].x = __ldcs(reinterpret_cast<const uint32_t*>(ks) + sub);
+          y[u].x = __ldcs(reinterpret_cast<const uint32_t*>(vs) + sub);
+          const int64_t eo = pg * a.e_sp + int64_t(r0 + ri) * a.e_sr + int64_t(h) * a.e_sh + sub / 2;
+          x[u].y = a.k_exp[eo];
+          y[u].y = a.v_exp[eo];
         } else {
           const uint2 k2 = __ldcs(reinterpret_cast<const uint2*>(ks) + sub), v2 = __ldcs(reinterpret_cast<const uint2*>(vs) + sub);
           x[u].x = k2.x; x[u].y = k2.y;
@@ -189,6 +131,9 @@ __global__ void __launch_bounds__(kThreads) bd_cache_read_kernel(const CacheArgs
           const uint2 v0 = dequantise4(y[u].x, fv[u]), v1 = dequantise4(y[u].y, fv[u]);
           x[u] = make_uint4(k0.x, k0.y, k1.x, k1.y);
           y[u] = make_uint4(v0.x, v0.y, v1.x, v1.y);
+        } else if constexpr (FMT == BD_CACHE_E2M1) {
+          x[u] = dequantise8_e2m1(x[u].x, x[u].y);
+          y[u] = dequantise8_e2m1(y[u].x, y[u].y);
         }
         __stcs(reinterpret_cast<uint4*>(a.kx + (dst + ri) * a.kx_sr + int64_t(h) * a.kx_sh) + sub, x[u]);
         __stcs(reinterpret_cast<uint4*>(a.vx + (dst + ri) * a.vx_sr + int64_t(h) * a.vx_sh) + sub, y[u]);
@@ -198,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) bd_cache_read_kernel(const CacheArgs
 }
 
 CacheArgs cache_args(const void* plan_dev, const bd_paged_cache* c, const bd_tensor* k, const bd_tensor* v) {
-  const int64_t es = c->fmt == BD_CACHE_BF16 ? 2 : 1;
+  const int64_t es = elem_bytes(c->fmt);
   CacheArgs a;
   a.plan = static_cast<const int32_t*>(plan_dev);
   a.k = static_cast<uint8_t*>(c->k.ptr); a.v = static_cast<uint8_t*>(c->v.ptr);
@@ -237,18 +182,39 @@ int32_t check_paged(const void* plan_host, const void* plan_dev, const bd_paged_
   if (c->num_pages != w[PH_NUM_PAGES] || c->k.rows != w[PH_PAGE] || c->v.rows != w[PH_PAGE])
     return fail(BD_ERR_PLAN, "cache of %d pages of %d / %d rows, the plan was built for %d of %d", c->num_pages, c->k.rows,
                 c->v.rows, w[PH_NUM_PAGES], w[PH_PAGE]);
-  const int es = c->fmt == BD_CACHE_BF16 ? 2 : 1;
+  const int es = elem_bytes(c->fmt);
   if ((st = check_tensor(&c->k, "cache k", es, c->num_pages, 1, w[PH_HKV], true))) return st;
   if ((st = check_tensor(&c->v, "cache v", es, c->num_pages, 1, w[PH_HKV], true))) return st;
-  if (c->fmt == BD_CACHE_E4M3) {
-    if (!c->k_exp || !c->v_exp) return fail(BD_ERR_ARG, "an e4m3 cache needs k_exp and v_exp");
+  if (c->fmt != BD_CACHE_BF16) {
+    if (!c->k_exp || !c->v_exp) return fail(BD_ERR_ARG, "an e4m3 or e2m1 cache needs k_exp and v_exp");
     if ((c->num_pages > 1 && c->exp_stride_page <= 0) || c->exp_stride_row <= 0 ||
         (w[PH_HKV] > 1 && c->exp_stride_head <= 0))
       return fail(BD_ERR_ARG, "exponent strides must be positive");
     if (c->exp_stride_row > INT32_MAX / w[PH_PAGE] / 2 || (w[PH_HKV] > 1 && c->exp_stride_head > INT32_MAX / w[PH_HKV] / 2))
       return fail(BD_ERR_UNSUPPORTED, "exponents of a page spread over more than 2^31 bytes");
   }
+  if (c->fmt == BD_CACHE_E2M1) {
+    const int al = scale_align(w[PH_D]);
+    const uintptr_t p = reinterpret_cast<uintptr_t>(c->k_exp) | reinterpret_cast<uintptr_t>(c->v_exp);
+    if (p % al || c->exp_stride_row % al || (c->num_pages > 1 && c->exp_stride_page % al) || (w[PH_HKV] > 1 && c->exp_stride_head % al))
+      return fail(BD_ERR_ALIGN, "scales: pointers and strides must be multiples of %d bytes", al);
+  }
   *out = w;
+  return BD_OK;
+}
+
+int32_t check_write(const void* plan_host, const void* plan_dev, const bd_tensor* k, const bd_tensor* v,
+                    const bd_paged_cache* cache, const int32_t** out) {
+  int32_t st = check_paged(plan_host, plan_dev, cache, out);
+  if (st) return st;
+  const int32_t* w = *out;
+  if (!w[PH_CAUSAL]) return fail(BD_ERR_PLAN, "new rows of a plan that is not causal have no cache positions");
+  if (!w[PH_WRITE_OK]) return fail(BD_ERR_PLAN, "two new rows of the batch have the same cache row");
+  if (w[PH_T] == 0) return BD_OK;
+  if ((st = check_tensor(k, "k", 2, 1, 1, w[PH_HKV], false))) return st;
+  if ((st = check_tensor(v, "v", 2, 1, 1, w[PH_HKV], false))) return st;
+  if (k->rows < w[PH_T] || v->rows < w[PH_T])
+    return fail(BD_ERR_ARG, "k/v rows %d/%d < %d new rows of the plan", k->rows, v->rows, w[PH_T]);
   return BD_OK;
 }
 
@@ -259,23 +225,18 @@ using namespace bd;
 extern "C" int32_t bd_cache_write(const void* plan_host, const void* plan_dev, const bd_tensor* k, const bd_tensor* v,
                                   const bd_paged_cache* cache, void* stream) {
   const int32_t* w = nullptr;
-  int32_t st = check_paged(plan_host, plan_dev, cache, &w);
+  int32_t st = check_write(plan_host, plan_dev, k, v, cache, &w);
   if (st) return st;
-  if (!w[PH_CAUSAL]) return fail(BD_ERR_PLAN, "new rows of a plan that is not causal have no cache positions");
-  if (!w[PH_WRITE_OK]) return fail(BD_ERR_PLAN, "two new rows of the batch have the same cache row");
   if (w[PH_T] == 0) return ok();
-  if ((st = check_tensor(k, "k", 2, 1, 1, w[PH_HKV], false))) return st;
-  if ((st = check_tensor(v, "v", 2, 1, 1, w[PH_HKV], false))) return st;
-  if (k->rows < w[PH_T] || v->rows < w[PH_T])
-    return fail(BD_ERR_ARG, "k/v rows %d/%d < %d new rows of the plan", k->rows, v->rows, w[PH_T]);
   const CacheArgs a = cache_args(plan_dev, cache, k, v);
   const int64_t blocks = (int64_t(w[PH_T]) * w[PH_HKV] * (w[PH_D] / 8) + kThreads - 1) / kThreads;
   // three rounds of 8 CTAs an SM: 30000 / 100000 e4m3 rows of 8 heads 33.4 / 93-95 us, with
   // one round 35.5 / 97-99, with two 33.4 / 97
   const int grid = int(blocks < kPagedSms * 24 ? blocks : kPagedSms * 24);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->fmt == BD_CACHE_BF16 ? launch_write<BD_CACHE_BF16>(w[PH_D], grid, s, a)
-                                                    : launch_write<BD_CACHE_E4M3>(w[PH_D], grid, s, a);
+  const cudaError_t e = cache->fmt == BD_CACHE_BF16   ? launch_write<BD_CACHE_BF16>(w[PH_D], grid, s, a)
+                        : cache->fmt == BD_CACHE_E4M3 ? launch_write<BD_CACHE_E4M3>(w[PH_D], grid, s, a)
+                                                      : launch_write<BD_CACHE_E2M1>(w[PH_D], grid, s, a);
   if (e != cudaSuccess) return cuda_fail(e, "bd_cache_write_kernel launch");
   return ok();
 }
@@ -294,8 +255,9 @@ extern "C" int32_t bd_cache_read(const void* plan_host, const void* plan_dev, co
   const int64_t groups = int64_t(w[PH_NPAGES]) * (w[PH_PAGE] / kReadRows);
   const int grid = int(groups < kPagedSms * 8 ? groups : kPagedSms * 8);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = cache->fmt == BD_CACHE_BF16 ? launch_read<BD_CACHE_BF16>(w[PH_D], grid, s, a)
-                                                    : launch_read<BD_CACHE_E4M3>(w[PH_D], grid, s, a);
+  const cudaError_t e = cache->fmt == BD_CACHE_BF16   ? launch_read<BD_CACHE_BF16>(w[PH_D], grid, s, a)
+                        : cache->fmt == BD_CACHE_E4M3 ? launch_read<BD_CACHE_E4M3>(w[PH_D], grid, s, a)
+                                                      : launch_read<BD_CACHE_E2M1>(w[PH_D], grid, s, a);
   if (e != cudaSuccess) return cuda_fail(e, "bd_cache_read_kernel launch");
   return ok();
 }

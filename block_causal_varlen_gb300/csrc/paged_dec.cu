@@ -1,5 +1,6 @@
 // Attention of few query rows over a paged K/V cache, and the join of split key
-// ranges, on sm_103a.
+// ranges, on sm_103a. (dec_e2m1.cu and dec_blocks.cu take the kernel and its launch from here
+// for other instantiations: the units are compiled side by side.)
 //
 // A block of up to 32 rows (the (new row, query head) pairs of one K/V head) over
 // keys [k0, k1) computes, per row, m = max_j s_j, l = sum_j 2^(s_j - m) and
@@ -26,10 +27,12 @@
 //     conflicts. Exponents never touch the codes: K's is a factor of the score, V's an
 //     addend of the base-2 exponent (m is then the maximum of s_j + e_j, l still the sum of
 //     2^(s_j - m)). q is fp16 as well, each row scaled by a power of two to a maximum of 2^14
-//     first: exact but for what is below 2^-31 of the row's largest, zero below 2^-40.
+//     first: exact but for what is below 2^-31 of the row's largest, zero below 2^-40;
+//   - e2m1 chunks likewise: a lane's codes of a key share one scale (V) or two (K), which
+//     multiply the converted pairs (exact: six significant bits).
 // P is rounded to the type of V's operand: bf16 for a bf16 cache (2^-8 relative at
-// most, like O itself), fp16 for e4m3 (2^-11; its subnormals, p 2^e below 2^-21 of the
-// row's largest, to 2^-32 of that), scaled by 2^7 for their sake.
+// most, like O itself), fp16 for e4m3 and e2m1 (2^-11; its subnormals, p 2^e (e2m1: p) below
+// 2^-21 of the row's largest, to 2^-32 of that), scaled by 2^7 for their sake.
 //
 // 64 ragged sequences of 500-16000 rows, 8 K/V heads of 128: bf16 (4 pairs a head) 164 us,
 // 6.8 TB/s; e4m3 (2 pairs) 92 us, 6.1 TB/s. One sequence of 4096 rows 7.7 us in a graph.
@@ -48,6 +51,7 @@
 #include <type_traits>
 
 #include "paged.h"
+#include "paged_quant.cuh"
 #include "ptx.cuh"
 
 namespace bd {
@@ -57,12 +61,13 @@ namespace {
 
 template <int D, int FMT, int NB>
 struct DecCfg {
-  static constexpr bool kF8 = FMT == BD_CACHE_E4M3;
+  static constexpr bool kF8 = FMT == BD_CACHE_E4M3, kF4 = FMT == BD_CACHE_E2M1;
+  static constexpr bool kF16 = kF8 || kF4;                    // operands of the products are fp16
   // head dim 256: two warps share a chunk's keys, each with half of the columns. Each
   // loads its half, forms its half of the scores, and adds the other's to them (through
   // shared memory); O's columns are its own.
   static constexpr int kDim = D == 256 ? 128 : D, kSplit = D / kDim;
-  static constexpr int kRowBytes = kDim * (kF8 ? 1 : 2);      // a warp's part of a key's K (or V) of one head
+  static constexpr int kRowBytes = row_bytes(FMT, kDim);      // a warp's part of a key's K (or V) of one head
   static constexpr int kPieces = kRowBytes <= 128 ? 1 : kRowBytes / 128;  // 128-byte pieces of it
   static constexpr int kPieceBytes = kRowBytes / kPieces;
   // keys a warp takes at a time: 32 where that is no more than 8 KB and registers allow
@@ -90,8 +95,10 @@ struct DecCfg {
   static constexpr int kOffRow = kOffInv + 8 * NB * 4;                 // their places in O
   // e4m3: 4-byte words around K's and V's exponent bytes of a chunk's keys, and the low
   // bits of the bytes' addresses relative to k_exp and v_exp
+  // (e2m1: kScale scale bytes of a warp's part of a key's K or V instead)
+  static constexpr int kScale = kF8 ? 4 : kF4 ? kDim / 16 : 0;
   static constexpr int kOffExp = kOffRow + 8 * NB * 8;                 // [kWarps][kStages][2][kChunk]
-  static constexpr int kOffRef = kOffExp + (kF8 ? kWarps * kStages * kChunk * 8 : 0);
+  static constexpr int kOffRef = kOffExp + kWarps * kStages * 2 * kChunk * kScale;
   static constexpr int kOffBar = kOffRef + (kF8 ? kWarps * kStages * kChunk : 0);
   static constexpr int kOffAbort = kOffBar + kWarps * kStages * 8;
   static constexpr int kSmem = kOffAbort + 16 + 1024;         // + alignment slack
@@ -113,6 +120,21 @@ __device__ __forceinline__ void ldsm4t(uint32_t a, uint32_t (&r)[4]) {
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 r;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
   return r;
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
@@ -144,10 +166,6 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
       : "=r"(lo), "=r"(hi)
       : "r"(x));
 }
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // l times 2^x, x <= 0. An e4m3 cache's m is the maximum of s_j + e_j, l the sum of 2^(s_j - m):
 // up to 2^60 for a key, which a single factor, zero below 2^-126, would lose while the
@@ -165,18 +183,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 }
 
 // BEHIND: launched behind the tile kernel of the same call (a parameter looked at in the kernel
-// instead costs 0.1 us of the smallest calls' 3.7).
-template <int D, int FMT, int NB, bool BEHIND>
+// instead costs 0.1 us of the smallest calls' 3.7). BLOCKS: pieces are of single new rows, whose
+// keys are those of the row's listed blocks, one after another.
+template <int D, int FMT, int NB, bool BEHIND, bool BLOCKS>
 __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     bd_paged_dec_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const AttnArgs a) {
   using Cfg = DecCfg<D, FMT, NB>;
-  constexpr bool F8 = Cfg::kF8;
+  constexpr bool F8 = Cfg::kF8, F4 = Cfg::kF4, F16 = Cfg::kF16;
   constexpr int NW = Cfg::kWarps, NST = Cfg::kStages, kChunk = Cfg::kChunk;
   constexpr int DW = Cfg::kDim, PW = Cfg::kSplit, NL = Cfg::kLanes;
   constexpr int KT = kChunk / 16;            // 16-key tiles of a chunk
   constexpr int KS = DW / 16, MT = DW / 16;  // contraction steps of q . k, 16-column tiles of O
-  constexpr float kPShift = F8 ? 7.f : 0.f;
+  constexpr float kPShift = 7.f;             // F16: P is held times 2^7
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -186,7 +205,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   const uint32_t ring = sbase + Cfg::kOffRing + warp * NST * Cfg::kStageBytes;
   const uint32_t bars = sbase + Cfg::kOffBar + warp * NST * 8;
   volatile uint8_t* eref = smem + Cfg::kOffRef + warp * NST * kChunk;  // low address bits of the exponents
-  const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * kChunk * 8;
+  const uint32_t exps = sbase + Cfg::kOffExp + warp * NST * kChunk * 2 * Cfg::kScale;
   const int32_t* plan = a.plan;
   const int32_t* rec = plan + kOffDecRec + blockIdx.x * kRecordWords;
   if constexpr (BEHIND) {
@@ -211,8 +230,8 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   auto piece = [&](int p) { return p == p0 ? rec + RC_PIECE : pieces + p * kPieceWords; };
   if (threadIdx.x == 0) *abort_flag = 0;
   if (lane == 0) {
-    // a chunk's arrivals: the copies' and, e4m3, every lane's exponent word
-    for (int s = 0; s < NST; ++s) mbar_init(bars + 8 * s, F8 ? 33 : 1);
+    // a chunk's arrivals: the copies' and every lane's exponents or scales
+    for (int s = 0; s < NST; ++s) mbar_init(bars + 8 * s, F16 ? 33 : 1);
     fence_barrier_init();
   }
   __syncthreads();
@@ -224,8 +243,11 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   // the products. The next chunk's page number is fetched when the one before is
   // issued, so that issuing waits for nothing.
   int cp = p0 - 1, ck = 0, ck1 = 0, chkv = 0, cpages = 0, cpage = 0;  // cpage: of key ck + lane (mod kChunk)
+  const int32_t* list = nullptr;  // BLOCKS: the row's list, its entry for the chunk after next, its blocks' number
+  int entry = 0, nblk = 0;
   auto next_chunk = [&]() {
     ck += kChunk * NL;
+    bool other = false;  // another piece
     while (ck >= ck1) {
       if (++cp >= p1) return;
       const int32_t* W = piece(cp);
@@ -233,9 +255,21 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
       ck1 = W[PC_K1];
       chkv = W[PC_HKV];
       cpages = W[PC_PAGES];
+      if constexpr (BLOCKS) {
+        list = a.blocks + W[PC_Q0] * a.b_sr + chkv * a.b_sh;
+        nblk = W[PC_NBLK];
+        other = true;
+      }
     }
     const int k = min(ck + lane % kChunk, ck1 - 1);
-    cpage = plan[cpages + (k >> pshift)];
+    if constexpr (BLOCKS) {
+      // (whatever the list holds, no block but the row's own sequence's is read)
+      if (other) entry = list[k >> pshift];
+      cpage = plan[cpages + min(max(entry, 0), nblk - 1)];
+      entry = list[min(ck + kChunk * NL + lane % kChunk, ck1 - 1) >> pshift];
+    } else {
+      cpage = plan[cpages + (k >> pshift)];
+    }
   };
   int is = 0;  // stage of the next chunk to come
   uint32_t issued = 0;
@@ -244,6 +278,16 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     // row of key ck + lane (mod kChunk) in its page, past the keys' end of the last key in its own
     const int keys = ck1 - ck, row = min(ck + lane % kChunk, ck1 - 1) & ((1 << pshift) - 1);
     const bool two = kChunk == 32 && brows == 16 && keys > 16;  // copies of K and of V: one, or two
+    if constexpr (F4) {
+      const int64_t o = int64_t(cpage) * a.e_sp + row * int(a.e_sr) + chkv * int(a.e_sh) + half * Cfg::kScale;
+      static_assert(!F4 || kChunk == 32, "a lane for each key");
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(exps + ((is * 2 + m) * kChunk + lane) * Cfg::kScale),
+                     "l"((m ? a.v_exp : a.k_exp) + o), "n"(F4 ? Cfg::kScale : 4)
+                     : "memory");
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
+    }
     if constexpr (F8) {
       // the 4-byte words of K's and V's exponents; a word's low address bits for later
       const int64_t o = int64_t(cpage) * a.e_sp + row * int(a.e_sr) + chkv * int(a.e_sh);
@@ -288,7 +332,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
       const int r = rw + 8 * b, n = row0 + r, t = n / G;
       const bool live = r < nrows;
       const __nv_bfloat16* qp = a.q + int64_t(q0 + t) * a.q_sr + int64_t(hkv * G + n % G) * a.q_sh + half * DW;
-      if constexpr (!F8) {
+      if constexpr (!F16) {
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
           qb[s][b][0] = live ? *reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * j) : 0u;
@@ -321,13 +365,13 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     const int32_t* X = piece(min(p + 1, p1 - 1));
     const int xq0 = X[PC_Q0], xhkv = X[PC_HKV], xrow0 = X[PC_ROW0], xnrows = X[PC_NROWS];
     // ---- the rows of this lane's scores, 2 j + e + 8 b: the keys they see, their score
-    // factors (e4m3: log2(e) / sqrt(d) and the power of two taken out of q)
+    // factors (fp16: log2(e) / sqrt(d) and the power of two taken out of q)
     float qs[NB][2];
     int lim[NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float up_inv = 1.f;
-      if constexpr (F8) {
+      if constexpr (F16) {
         uint32_t mx = 0;
 #pragma unroll
         for (int s = 0; s < KS; ++s)
@@ -335,23 +379,20 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         mx = max(mx & 0xffffu, mx >> 16);
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // max|q| = f 2^E -> f 2^14: a row below 2^-110 is scaled by 2^124 only
-        const int E = max(int(mx >> 7) - 127, -110), E0 = min(E, 113);
-        const float up = __uint_as_float(uint32_t(127 + 14 - E0) << 23), up2 = __uint_as_float(uint32_t(127 - (E - E0)) << 23);
-        up_inv = __uint_as_float(uint32_t(127 - 14 + E0) << 23) * __uint_as_float(uint32_t(127 + (E - E0)) << 23);
+        const float2 up = q_factors(mx, &up_inv);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const uint32_t u = qb[s][b][h];
-            qb[s][b][h] = pack_f16(__uint_as_float(u << 16) * up * up2, __uint_as_float(u & 0xffff0000u) * up * up2);
+            qb[s][b][h] = pack_f16(bf16_lo(u) * up.x * up.y, bf16_hi(u) * up.x * up.y);
           }
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int r = 2 * j + e + 8 * b;
         lim[b][e] = r >= nrows ? 0 : causal ? kvlen - qlen + (row0 + r) / G + 1 : kvlen;
-        qs[b][e] = a.scale_log2 * (F8 ? __shfl_sync(0xffffffffu, up_inv, 4 * (2 * j + e)) : 1.f);
+        qs[b][e] = a.scale_log2 * (F16 ? __shfl_sync(0xffffffffu, up_inv, 4 * (2 * j + e)) : 1.f);
       }
     }
     float m[NB][2], l[NB][2], o[MT][NB][4];
@@ -379,7 +420,45 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[y][b][e] = 0.f;
-      if constexpr (!F8) {
+      if constexpr (F4) {
+        // a lane's 32 (head dim 64: 16) neighbouring codes of keys rw + 8 y, and their scales
+        uint4 u[2 * KT];
+        uint32_t sc[2 * KT];
+#pragma unroll
+        for (int y = 0; y < 2 * KT; ++y) {
+          const int key = 8 * y + rw;
+          const uint32_t at = exps + (cs * 2 * kChunk + key) * Cfg::kScale;
+          if constexpr (D == 64) {
+            const uint2 t = lds64(st + key * 32 + (((j >> 1) ^ ((key >> 2) & 1)) << 4) + (j & 1) * 8);
+            u[y] = make_uint4(t.x, t.y, 0u, 0u);
+            sc[y] = lds8(at + j);
+          } else {
+            u[y] = lds128(st + key * 64 + ((j ^ ((key >> 1) & 3)) << 4));
+            sc[y] = lds16(at + 2 * j);
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < KS / 2; ++x)
+#pragma unroll
+          for (int y = 0; y < KT; ++y) {
+            auto word = [&](const uint4& v) { return x == 0 ? v.x : x == 1 ? v.y : x == 2 ? v.z : v.w; };
+            uint32_t f[4], g[4];
+            e2m1x8_to_f16(word(u[2 * y]), f);
+            e2m1x8_to_f16(word(u[2 * y + 1]), g);
+            const uint32_t fs = scale_twice(D == 64 ? sc[2 * y] : x < 2 ? sc[2 * y] & 255u : sc[2 * y] >> 8);
+            const uint32_t gs = scale_twice(D == 64 ? sc[2 * y + 1] : x < 2 ? sc[2 * y + 1] & 255u : sc[2 * y + 1] >> 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f[i] = mul_f16x2(f[i], fs);
+              g[i] = mul_f16x2(g[i], gs);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                mma16<true>(s[y][b], f[2 * i], g[2 * i], f[2 * i + 1], g[2 * i + 1], qb[2 * x + i][b][0], qb[2 * x + i][b][1]);
+          }
+      } else if constexpr (!F8) {
 #pragma unroll
         for (int c = 0; c < KS; ++c)
 #pragma unroll
@@ -441,7 +520,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         cs2 ^= 1;
       }
       // what is left to multiply the scores by
-      auto factor = [&](int b, int e) { return PW == 2 ? 1.f : F8 ? qs[b][e] : a.scale_log2; };
+      auto factor = [&](int b, int e) { return PW == 2 ? 1.f : F16 ? qs[b][e] : a.scale_log2; };
       // ---- e4m3: the scores times K's factors; ve, V's exponents of this lane's keys
       // k + 8 y + rw
       float ve[2 * KT];
@@ -538,6 +617,8 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
               if (__shfl_sync(0xffffffffu, vb, key) == 255u)
                 w |= (k + key < lim[b][0] ? 0x7e00u : 0u) | (k + key < lim[b][1] ? 0x7e000000u : 0u);
             }
+          } else if constexpr (F4) {
+            w = pack_f16(p0f * 128.f, p1f * 128.f);  // 2^kPShift
           } else {
             w = pack_bf16(p0f, p1f);
           }
@@ -571,7 +652,46 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
               }
             }
           }
-          if constexpr (!F8) {
+          if constexpr (F4) {
+            // this lane's 16 (head dim 64: 8) neighbouring codes of keys 2 j, 2 j + 1, 8 + 2 j,
+            // 9 + 2 j: codes of two keys side by side in a byte, their scales in a pair
+            uint32_t x[4][2], sb[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const int key = 16 * y + 8 * (z >> 1) + 2 * j + (z & 1);
+              const uint32_t at = exps + ((cs * 2 + 1) * kChunk + key) * Cfg::kScale;
+              if constexpr (D == 64) {
+                x[z][0] = lds32(sv + key * 32 + (((rw >> 2) ^ ((key >> 2) & 1)) << 4) + (rw & 3) * 4);
+                sb[z] = lds8(at + (rw >> 1));
+              } else {
+                const uint2 u = lds64(sv + key * 64 + (((rw >> 1) ^ ((key >> 1) & 3)) << 4) + (rw & 1) * 8);
+                x[z][0] = u.x; x[z][1] = u.y;
+                sb[z] = lds8(at + rw);
+              }
+              if constexpr (TAIL) {
+                if (k + key >= k1) sb[z] = 0u;
+                if (sb[z] > kMostScale) { sb[z] = 0u; odd = 1u; }
+              }
+            }
+            const uint32_t s0 = scale_pair(sb[0] | (sb[1] << 16)), s1 = scale_pair(sb[2] | (sb[3] << 16));
+#pragma unroll
+            for (int w4 = 0; w4 < (D == 64 ? 1 : 2); ++w4) {
+              uint32_t g[4][4];
+              auto even = [](uint32_t p, uint32_t q) { return (p & 0x0f0f0f0fu) | ((q << 4) & 0xf0f0f0f0u); };
+              auto odds = [](uint32_t p, uint32_t q) { return ((p >> 4) & 0x0f0f0f0fu) | (q & 0xf0f0f0f0u); };
+              e2m1x8_to_f16(even(x[0][w4], x[1][w4]), g[0]);
+              e2m1x8_to_f16(odds(x[0][w4], x[1][w4]), g[1]);
+              e2m1x8_to_f16(even(x[2][w4], x[3][w4]), g[2]);
+              e2m1x8_to_f16(odds(x[2][w4], x[3][w4]), g[3]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t a0 = mul_f16x2(g[0][i], s0), a1 = mul_f16x2(g[1][i], s0);
+                const uint32_t a2 = mul_f16x2(g[2][i], s1), a3 = mul_f16x2(g[3][i], s1);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) mma16<true>(o[w4 * 4 + i][b], a0, a1, a2, a3, pb[y][b][0], pb[y][b][1]);
+              }
+            }
+          } else if constexpr (!F8) {
             const uint32_t vrow = sv + (16 * y + ((lane >> 4) & 1) * 8 + (lane & 7)) * 128;
 #pragma unroll
             for (int n = 0; n < MT; ++n) {
@@ -619,7 +739,21 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
       };
       if (k + kChunk > min(k1, all_see) || (F8 && vnan)) values(std::true_type());
       else values(std::false_type());
-      if constexpr (!F8) {
+      if constexpr (F4) {
+        if (__any_sync(0xffffffffu, odd != 0)) {
+          for (int key = 0; key < min(kChunk, k1 - k); ++key) {  // this lane's columns are of one scale
+            if (lds8(exps + ((cs * 2 + 1) * kChunk + key) * Cfg::kScale + (D == 64 ? rw >> 1 : rw)) <= kMostScale) continue;
+#pragma unroll
+            for (int n = 0; n < MT; ++n)
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (k + key < lim[b][e & 1]) o[n][b][e] = CUDART_NAN_F;
+          }
+        }
+      }
+      if constexpr (!F16) {
         if (__any_sync(0xffffffffu, odd != 0)) {
           for (int key = 0; key < min(kChunk, k1 - k); ++key)
 #pragma unroll
@@ -692,12 +826,12 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         float M = -CUDART_INF_F;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 8 * NB + 8 * b + 2 * j + e) * 2]);
-        fac[e] = (m[b][e] == -CUDART_INF_F ? 0.f : ex2(m[b][e] - M)) * (F8 ? 0.0078125f : 1.f);  // 2^-kPShift
+        fac[e] = (m[b][e] == -CUDART_INF_F ? 0.f : ex2(m[b][e] - M)) * (F16 ? 0.0078125f : 1.f);  // 2^-kPShift
       }
 #pragma unroll
       for (int rd = 0; rd < DW / Cfg::kCols; ++rd) {
         if (b || rd) __syncthreads();
-        // e4m3: a lane has columns [16 rw, 16 rw + 16) of 128 (8 of 64), half of which, W, go
+        // fp16: a lane has columns [16 rw, 16 rw + 16) of 128 (8 of 64), half of which, W, go
         // in a round, kept together
         constexpr int NR = Cfg::kCols / 16, W = Cfg::kCols / 8;
 #pragma unroll
@@ -706,7 +840,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
           for (int e = 0; e < 2; ++e) {
             const float x0 = o[rd * NR + n][b][e] * fac[e], x1 = o[rd * NR + n][b][2 + e] * fac[e];
             float* S = sum + warp * Cfg::kSumFloats + (2 * j + e) * Cfg::kPitch;
-            if constexpr (F8) {
+            if constexpr (F16) {
               *reinterpret_cast<float2*>(&S[W * rw + 2 * n]) = make_float2(x0, x1);
             } else {
               S[16 * n + rw] = x0;
@@ -723,7 +857,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
             const float4 u = *reinterpret_cast<const float4*>(&sum[(w * PW + hs) * Cfg::kSumFloats + r * Cfg::kPitch + c]);
             t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
           }
-          const int col = hs * DW + (F8 ? (c / W) * (DW / 8) + rd * W + c % W : rd * Cfg::kCols + c);
+          const int col = hs * DW + (F16 ? (c / W) * (DW / 8) + rd * W + c % W : rd * Cfg::kCols + c);
           if (part) {
             *reinterpret_cast<float4*>(part + 2 * kDecSlotRows + (8 * b + r) * D + col) = t;
           } else {
@@ -749,6 +883,66 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     }
   }
 }
+
+template <int D, int FMT, int NB, bool BEHIND, bool BLOCKS>
+int32_t launch_dec_tb(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+  using Cfg = DecCfg<D, FMT, NB>;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(bd_paged_dec_kernel<D, FMT, NB, BEHIND, BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged few-rows)");
+    if (dev < 64) done[dev].store(true, std::memory_order_release);
+  }
+  const int rows = w[PH_PAGE] < Cfg::kChunk ? w[PH_PAGE] : Cfg::kChunk;
+  // (256-byte promotion where heads go in gangs: 64 ragged sequences of 32 e4m3 heads 370 -> 349 us)
+  const bool near = gang_of(w[PH_HKV]) > 1;
+  CUtensorMap mk, mv;
+  int32_t st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], row_bytes(FMT, D), elem_bytes(FMT), "cache k", rows, near,
+                            Cfg::kPieceBytes))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], row_bytes(FMT, D), elem_bytes(FMT), "cache v", rows, near,
+                            Cfg::kPieceBytes))) return st;
+  const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB, BEHIND, BLOCKS>, kDecCtas, Cfg::kThreads, Cfg::kSmem, s, mk, mv, a);
+  return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
+}
+
+template <int D, int FMT, int NB, bool BLOCKS>
+int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+  if constexpr (BLOCKS) return launch_dec_tb<D, FMT, NB, false, true>(w, c, a, s);
+  else return a.go ? launch_dec_tb<D, FMT, NB, true, false>(w, c, a, s) : launch_dec_tb<D, FMT, NB, false, false>(w, c, a, s);
+}
+
+template <int D, int FMT, bool BLOCKS>
+int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+  const int rows = w[PH_DEC_ROWS];
+  if (rows == 8) return launch_dec_t<D, FMT, 1, BLOCKS>(w, c, a, s);
+  if (rows == 16) return launch_dec_t<D, FMT, 2, BLOCKS>(w, c, a, s);
+  if constexpr (dec_block_rows(FMT) == 32) {
+    if (rows == 24) return launch_dec_t<D, FMT, 3, BLOCKS>(w, c, a, s);
+    if (rows == 32) return launch_dec_t<D, FMT, 4, BLOCKS>(w, c, a, s);
+  }
+  return fail(BD_ERR_PLAN, "few-rows blocks of %d rows at head dim %d", rows, D);
+}
+
+template <int FMT, bool BLOCKS>
+int32_t launch_dec_fmt(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
+  const int d = w[PH_D];
+  return d == 64    ? launch_dec_rows<64, FMT, BLOCKS>(w, c, a, s)
+         : d == 128 ? launch_dec_rows<128, FMT, BLOCKS>(w, c, a, s)
+                    : launch_dec_rows<256, FMT, BLOCKS>(w, c, a, s);
+}
+
+}  // namespace
+
+}  // namespace bd
+
+#ifndef BD_DEC_KERNEL_ONLY
+
+namespace bd {
+
+namespace {
 
 template <int V>
 __device__ __forceinline__ void load_cols(const float* p, float (&o)[V]) {
@@ -906,45 +1100,6 @@ __global__ void __launch_bounds__(256) bd_paged_tile_merge_kernel(const MergeArg
   }
 }
 
-template <int D, int FMT, int NB, bool BEHIND>
-int32_t launch_dec_tb(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
-  using Cfg = DecCfg<D, FMT, NB>;
-  static std::atomic<bool> done[64];
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(bd_paged_dec_kernel<D, FMT, NB, BEHIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmem);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged few-rows)");
-    if (dev < 64) done[dev].store(true, std::memory_order_release);
-  }
-  const int es = Cfg::kF8 ? 1 : 2, rows = w[PH_PAGE] < Cfg::kChunk ? w[PH_PAGE] : Cfg::kChunk;
-  // (256-byte promotion where heads go in gangs: 64 ragged sequences of 32 e4m3 heads 370 -> 349 us)
-  const bool near = gang_of(w[PH_HKV]) > 1;
-  CUtensorMap mk, mv;
-  int32_t st;
-  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], D, es, "cache k", rows, near))) return st;
-  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], D, es, "cache v", rows, near))) return st;
-  const cudaError_t e = launch_kernel(bd_paged_dec_kernel<D, FMT, NB, BEHIND>, kDecCtas, Cfg::kThreads, Cfg::kSmem, s, mk, mv, a);
-  return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_paged_dec_kernel launch");
-}
-
-template <int D, int FMT, int NB>
-int32_t launch_dec_t(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
-  return a.go ? launch_dec_tb<D, FMT, NB, true>(w, c, a, s) : launch_dec_tb<D, FMT, NB, false>(w, c, a, s);
-}
-
-template <int D, int FMT>
-int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArgs& a, cudaStream_t s) {
-  const int rows = w[PH_DEC_ROWS];
-  if (rows == 8) return launch_dec_t<D, FMT, 1>(w, c, a, s);
-  if (rows == 16) return launch_dec_t<D, FMT, 2>(w, c, a, s);
-  if constexpr (dec_block_rows(FMT) == 32) {
-    if (rows == 24) return launch_dec_t<D, FMT, 3>(w, c, a, s);
-    if (rows == 32) return launch_dec_t<D, FMT, 4>(w, c, a, s);
-  }
-  return fail(BD_ERR_PLAN, "few-rows blocks of %d rows at head dim %d", rows, D);
-}
-
 }  // namespace
 
 int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream_t s) {
@@ -958,12 +1113,10 @@ int32_t launch_merge(const MergeArgs& a, int d, bool tile, bool wide, cudaStream
 }
 
 int32_t launch_dec(const int32_t* w, const AttnArgs& a, const bd_paged_cache* c, cudaStream_t s) {
-  const int d = w[PH_D];
-  if (c->fmt == BD_CACHE_BF16)
-    return d == 64 ? launch_dec_rows<64, BD_CACHE_BF16>(w, c, a, s)
-           : d == 128 ? launch_dec_rows<128, BD_CACHE_BF16>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_BF16>(w, c, a, s);
-  return d == 64 ? launch_dec_rows<64, BD_CACHE_E4M3>(w, c, a, s)
-         : d == 128 ? launch_dec_rows<128, BD_CACHE_E4M3>(w, c, a, s) : launch_dec_rows<256, BD_CACHE_E4M3>(w, c, a, s);
+  if (a.blocks) return launch_dec_blocks(w, a, c, s);
+  return c->fmt == BD_CACHE_BF16   ? launch_dec_fmt<BD_CACHE_BF16, false>(w, c, a, s)
+         : c->fmt == BD_CACHE_E4M3 ? launch_dec_fmt<BD_CACHE_E4M3, false>(w, c, a, s)
+                                   : launch_dec_e2m1(w, a, c, s);
 }
 
 }  // namespace bd
@@ -992,13 +1145,17 @@ extern "C" int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes)
   return ok();
 }
 
-extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q,
-                                 const bd_paged_cache* cache, bd_tensor* out, bd_rowstat* lse, void* workspace,
-                                 size_t workspace_bytes, void* stream) {
+// bd_paged_attn, or with lists of blocks bd_sparse_attn.
+static int32_t attend(bool sparse, const void* plan_host, const void* plan_dev, const bd_tensor* q, const bd_paged_cache* cache,
+                      const bd_blocks* blocks, bd_tensor* out, bd_rowstat* lse, void* workspace, size_t workspace_bytes,
+                      void* stream) {
   const int32_t* w = nullptr;
   int32_t st = check_paged(plan_host, plan_dev, cache, &w);
   if (st) return st;
+  if (sparse != (w[PH_BLOCKS] > 0))
+    return fail(BD_ERR_PLAN, sparse ? "not a sparse plan" : "a sparse plan: its rows attend over lists of blocks (bd_sparse_attn)");
   if (w[PH_T] == 0) return ok();
+  if (sparse && (st = check_blocks(blocks, w))) return st;
   if ((st = check_tensor(q, "q", 2, 1, 1, w[PH_H], true))) return st;
   if ((st = check_tensor(out, "out", 2, 1, 1, w[PH_H], false))) return st;
   if (q->rows < w[PH_T] || out->rows < w[PH_T])
@@ -1020,7 +1177,9 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   a.lse = lse ? lse->ptr : nullptr;
   a.l_sh = lse ? lse->stride_head : 0;
   a.part = static_cast<float*>(workspace);
-  const int64_t es = cache->fmt == BD_CACHE_BF16 ? 2 : 1;
+  a.blocks = sparse ? blocks->ptr : nullptr;
+  a.b_sr = sparse ? blocks->stride_row : 0; a.b_sh = sparse ? blocks->stride_head : 0;
+  const int64_t es = elem_bytes(cache->fmt);
   a.vc = static_cast<const uint8_t*>(cache->v.ptr);
   a.v_sp = cache->v.stride_b * es; a.v_sr = cache->v.stride_row * es; a.v_sh = cache->v.stride_head * es;
   a.k_exp = cache->k_exp; a.v_exp = cache->v_exp;
@@ -1049,3 +1208,17 @@ extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, co
   if (w[PH_NTILEM] && (st = launch_merge(m, w[PH_D], true, false, s))) return st;
   return ok();
 }
+
+extern "C" int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q,
+                                 const bd_paged_cache* cache, bd_tensor* out, bd_rowstat* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  return attend(false, plan_host, plan_dev, q, cache, nullptr, out, lse, workspace, workspace_bytes, stream);
+}
+
+extern "C" int32_t bd_sparse_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q, const bd_paged_cache* cache,
+                                  const bd_blocks* blocks, bd_tensor* out, bd_rowstat* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return attend(true, plan_host, plan_dev, q, cache, blocks, out, lse, workspace, workspace_bytes, stream);
+}
+
+#endif  // BD_DEC_KERNEL_ONLY

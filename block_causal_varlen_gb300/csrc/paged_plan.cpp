@@ -31,6 +31,8 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
   auto in = [&](int64_t off, int64_t n, int stride) { return off >= kOffLists && n >= 0 && off + n * stride <= words; };
   if (!in(w[PH_OFF_TOK], w[PH_T], 1) || !in(w[PH_OFF_PAGES], w[PH_NPAGES], 1) || !in(w[PH_OFF_PGROW], w[PH_NPAGES], 1) ||
       !in(w[PH_OFF_PGCNT], w[PH_NPAGES], 1) || !in(w[PH_OFF_DEC], w[PH_NDEC], kPieceWords) ||
+      !in(w[PH_OFF_POS], w[PH_T], 1) || !in(w[PH_OFF_TOUCH], w[PH_NTOUCH], 1) ||
+      (w[PH_BLOCKS] && !in(w[PH_OFF_ROWPG], w[PH_T], 1)) ||
       !in(w[PH_OFF_TILE], w[PH_NTILE], kPieceWords) || w[PH_NDECM] < 0 || w[PH_NDECM] > kDecSlots / 2 ||
       w[PH_NTILEM] < 0 || w[PH_NTILEM] > kTilePartSlots / 2)
     return fail(BD_ERR_PLAN, "paged plan blob offsets are inconsistent");
@@ -40,8 +42,14 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
 
 namespace {
 
+// seq: a sequence of the batch or, in sparse plans, a new row, which has keys of its own
 struct Item {
   int32_t seq, hkv, row0, nrows, keys;
+};
+
+// What the pieces say of the sequences (or new rows) that items belong to.
+struct Seqs {
+  std::vector<int32_t> q0, q_len, kv_len, page_off, nblk;
 };
 
 // Some key units of an item, and the CTA that takes them.
@@ -178,8 +186,8 @@ bool fill(const std::vector<Item>& items, int unit, int over, int64_t t, std::ve
 }
 
 // Writes the parts (in CTA order) down as pieces, records and joins.
-void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<Part>& parts,
-                 const std::vector<int32_t>& q0, const std::vector<int32_t>& page_off, int unit, int ctas, Lists* L) {
+void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<Part>& parts, const Seqs& S,
+                 int unit, int ctas, Lists* L) {
   L->records.assign(size_t(ctas) * kRecordWords, 0);
   // slots of an item's parts in key order, items in order
   std::vector<int32_t> count(items.size(), 0), slot0(items.size(), -1);
@@ -190,7 +198,7 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
     const Item& it = items[i];
     int32_t m[kMergeWords] = {0};
     slot0[i] = m[MG_SLOT0] = slots;
-    m[MG_N] = count[i]; m[MG_Q0] = q0[it.seq]; m[MG_HKV] = it.hkv; m[MG_ROW0] = it.row0; m[MG_NROWS] = it.nrows;
+    m[MG_N] = count[i]; m[MG_Q0] = S.q0[it.seq]; m[MG_HKV] = it.hkv; m[MG_ROW0] = it.row0; m[MG_NROWS] = it.nrows;
     L->merges.insert(L->merges.end(), m, m + kMergeWords);
     slots += count[i];
   }
@@ -202,8 +210,8 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
     const Part& x = parts[i];
     const Item& it = items[x.item];
     int32_t p[kPieceWords] = {0};
-    p[PC_Q0] = q0[it.seq]; p[PC_QLEN] = D.q_len[it.seq]; p[PC_KVLEN] = D.kv_len[it.seq];
-    p[PC_PAGES] = page_off[it.seq]; p[PC_HKV] = it.hkv; p[PC_ROW0] = it.row0; p[PC_NROWS] = it.nrows;
+    p[PC_Q0] = S.q0[it.seq]; p[PC_QLEN] = S.q_len[it.seq]; p[PC_KVLEN] = S.kv_len[it.seq];
+    p[PC_PAGES] = S.page_off[it.seq]; p[PC_NBLK] = S.nblk[it.seq]; p[PC_HKV] = it.hkv; p[PC_ROW0] = it.row0; p[PC_NROWS] = it.nrows;
     p[PC_K0] = x.u0 * unit;
     p[PC_K1] = int32_t(std::min<int64_t>(it.keys, int64_t(x.u1) * unit));
     p[PC_T0] = it.row0 / (D.H / D.Hkv);
@@ -232,8 +240,7 @@ void write_lists(const bd_paged_desc& D, const std::vector<Item>& items, const s
 // of the same rows at the same time, which HBM serves faster than rows of a head on their own
 // (64 ragged sequences: e4m3 rows of 8 x 128 bytes 105 -> 94 us, 8 x 256 bytes of bf16 177
 // -> 172).
-void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
-               const std::vector<int32_t>& page_off, Lists* L) {
+void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const Seqs& S, Lists* L) {
   constexpr int kOver = 8;
   const int join = D.d == 256 ? 4 : 8;
   std::vector<Part> parts;
@@ -265,7 +272,7 @@ void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std
         }
     }
   }
-  write_lists(D, items, parts, q0, page_off, kDecUnit, kDecCtas, L);
+  write_lists(D, items, parts, S, kDecUnit, kDecCtas, L);
 }
 
 // Tiles: a partial result is up to 256 rows of O in fp32, written and read again, so
@@ -273,8 +280,7 @@ void dec_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std
 // of the longest blocks, and whole blocks with the gaps filled by parts of the others,
 // by their longest load in key tiles (a piece costs kOver more, a join of n partial
 // results about 3 + n / 40).
-void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const std::vector<int32_t>& q0,
-                const std::vector<int32_t>& page_off, Lists* L) {
+void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const Seqs& S, Lists* L) {
   constexpr int kOver = 2;
   std::vector<Part> best, parts;
   if (!items.empty()) {
@@ -319,7 +325,7 @@ void tile_lists(const bd_paged_desc& D, const std::vector<Item>& items, const st
     }
     if (hi + 3 < least && fill(items, kTile, kOver, hi, &parts)) better(hi);
   }
-  write_lists(D, items, best, q0, page_off, kTile, kTileCtas, L);
+  write_lists(D, items, best, S, kTile, kTileCtas, L);
 }
 
 int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npages) {
@@ -334,7 +340,7 @@ int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npage
     return fail(BD_ERR_UNSUPPORTED, "page_size %d (a power of two from 16 to 1024)", D->page_size);
   if (D->num_pages <= 0) return fail(BD_ERR_ARG, "num_pages must be positive");
   if (int64_t(D->num_pages) * D->page_size > INT32_MAX) return fail(BD_ERR_CAPACITY, "num_pages * page_size past 2^31 - 1");
-  if (D->fmt != BD_CACHE_BF16 && D->fmt != BD_CACHE_E4M3) return fail(BD_ERR_ARG, "cache format %d", D->fmt);
+  if (D->fmt != BD_CACHE_BF16 && D->fmt != BD_CACHE_E4M3 && D->fmt != BD_CACHE_E2M1) return fail(BD_ERR_ARG, "cache format %d", D->fmt);
   if (D->causal != 0 && D->causal != 1) return fail(BD_ERR_ARG, "causal must be 0 or 1");
   *T = *kv = *npages = 0;
   for (int32_t b = 0; b < D->B; ++b) {
@@ -361,65 +367,120 @@ int32_t validate(const bd_paged_desc* D, int64_t* T, int64_t* kv, int64_t* npage
 }
 
 struct Built {
-  int64_t T, kv, npages;
+  int64_t T, kv, npages, ntouch = 0;
   std::vector<Item> dec_items, tile_items;
-  std::vector<int32_t> q0, page_off;
-  int32_t dec_rows, dec_live = 0;
+  Seqs S;                          // of the items
+  std::vector<int32_t> page_off;   // of the sequences
+  int32_t dec_rows, dec_live = 0, sel_cap = 0;
 };
 
+int32_t check_sparse(const bd_paged_desc* D, const bd_sparse_desc* X) {
+  if (!X) return fail(BD_ERR_ARG, "sparse is NULL");
+  if (!D) return fail(BD_ERR_ARG, "desc is NULL");
+  if (X->first < 0 || X->recent < 1 || X->blocks < 1 || X->blocks > kMostListed)
+    return fail(BD_ERR_ARG, "lists of %d blocks with %d first and %d recent ones (1..%d, at least 0 and 1)", X->blocks, X->first,
+                X->recent, kMostListed);
+  if (int64_t(X->first) + X->recent > X->blocks)
+    return fail(BD_ERR_ARG, "lists of %d blocks do not hold %d first and %d recent ones", X->blocks, X->first, X->recent);
+  if (D->causal != 1) return fail(BD_ERR_ARG, "rows of a plan that is not causal have no position: it cannot be sparse");
+  return BD_OK;
+}
+
 // Validates a description and lists its blocks.
-int32_t prepare(const bd_paged_desc* D, Built* X) {
-  int32_t st = validate(D, &X->T, &X->kv, &X->npages);
+int32_t prepare(const bd_paged_desc* D, const bd_sparse_desc* X, Built* B) {
+  int32_t st = validate(D, &B->T, &B->kv, &B->npages);
   if (st) return st;
-  const int G = D->H / D->Hkv;
-  std::vector<int32_t>&q0 = X->q0, &page_off = X->page_off;
-  q0.resize(D->B);
-  page_off.resize(D->B);
-  int64_t t = 0, pg = kOffLists + X->T;
+  const int G = D->H / D->Hkv, P = D->page_size;
+  std::vector<int32_t> q0(D->B);
+  B->page_off.resize(D->B);
+  int64_t t = 0, pg = kOffLists + B->T;
   for (int32_t b = 0; b < D->B; ++b) {
+    const int32_t q = D->q_len[b], n = D->kv_len[b];
     q0[b] = int32_t(t);
-    page_off[b] = int32_t(pg);
-    t += D->q_len[b];
-    pg += (int64_t(D->kv_len[b]) + D->page_size - 1) / D->page_size;
+    B->page_off[b] = int32_t(pg);
+    t += q;
+    pg += (int64_t(n) + P - 1) / P;
     if (pg > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
+    if (D->causal && q > 0 && n > 0) B->ntouch += (n - 1) / P - std::max(0, n - q) / P + 1;
+    if (X && (int64_t(n) + P - 1) / P > kMostBlocks)
+      return fail(BD_ERR_UNSUPPORTED, "sequence %d: kv_len %d is more than %d blocks of %d rows", b, n, kMostBlocks, P);
   }
-  // Sequences of up to 32 (bf16) or 48 (e4m3) (new row, head) pairs of a K/V head go to the
+  // Sequences of up to 32 (bf16) or 48 (8 and 4 bits) (new row, head) pairs of a K/V head go to the
   // few-rows kernel, in blocks of one size (a tile of 32 rows in use costs what one of 128
   // does). 16 sequences of 8000 rows, bf16 d 256, 32 pairs: 220 us, as tiles 253; d 128, 48
   // pairs: 195 and 138; e4m3 d 128, 48 pairs in three blocks: 144, as tiles 167; 64 pairs of
-  // 300-8000 rows: 66 and 63.
-  const int most = dec_most_rows(D->fmt);
+  // 300-8000 rows: 66 and 63. Rows with blocks of their own go there one by one.
+  const int most = dec_most_rows(D->fmt), block = dec_block_rows(D->fmt);
   int32_t widest = 1;
-  for (int32_t b = 0; b < D->B; ++b)
-    if (int64_t(D->q_len[b]) * G <= most) widest = std::max(widest, D->q_len[b] * G);
-  X->dec_rows = std::min((widest + 7) / 8 * 8, dec_block_rows(D->fmt));
+  if (X) widest = std::min(G, block);
+  else
+    for (int32_t b = 0; b < D->B; ++b)
+      if (int64_t(D->q_len[b]) * G <= most) widest = std::max(widest, D->q_len[b] * G);
+  B->dec_rows = std::min((widest + 7) / 8 * 8, block);
   // every row block of a (sequence, K/V head): keys up to what its last row sees
-  std::vector<Item>&dec = X->dec_items, &tile = X->tile_items;
+  std::vector<Item>&dec = B->dec_items, &tile = B->tile_items;
   int64_t nitems = 0;
-  for (int32_t b = 0; b < D->B; ++b) nitems += (int64_t(D->q_len[b]) * G + 7) / 8 * D->Hkv;
+  for (int32_t b = 0; b < D->B; ++b)
+    nitems += X ? int64_t(D->q_len[b]) * ((G + 7) / 8) * D->Hkv : (int64_t(D->q_len[b]) * G + 7) / 8 * D->Hkv;
   if (nitems > (1 << 26)) return fail(BD_ERR_CAPACITY, "plan of more than 2^26 row blocks");
+  if (X) {
+    Seqs& S = B->S;
+    int32_t widest_row = 1;
+    for (int32_t b = 0; b < D->B; ++b)
+      for (int32_t i = 0; i < D->q_len[b]; ++i) {
+        const int64_t pos = int64_t(D->kv_len[b]) - D->q_len[b] + i;
+        const int32_t nblk = pos < 0 ? 0 : int32_t(pos / P) + 1, n = std::min(nblk, X->blocks);
+        const int32_t keys = pos < 0 ? 0 : int32_t((n - 1) * P + pos % P + 1);
+        const int32_t row = int32_t(S.q0.size());
+        widest_row = std::max(widest_row, nblk);
+        S.q0.push_back(row);
+        S.q_len.push_back(1);
+        S.kv_len.push_back(keys);
+        S.page_off.push_back(B->page_off[b]);
+        S.nblk.push_back(nblk);
+        for (int32_t g = 0; g < D->Hkv; ++g)
+          for (int32_t r0 = 0; r0 < G; r0 += B->dec_rows) {
+            const int32_t r1 = std::min(G, r0 + B->dec_rows);
+            B->dec_live = std::max(B->dec_live, r1 - r0);
+            dec.push_back({row, g, r0, r1 - r0, keys});
+          }
+      }
+    B->sel_cap = 512;
+    while (B->sel_cap < widest_row) B->sel_cap *= 2;
+    return BD_OK;
+  }
   for (int32_t b = 0; b < D->B; ++b) {
     const int32_t q = D->q_len[b], n = D->kv_len[b], rows = q * G;
     const bool few = rows <= most;
-    const int32_t step = few ? X->dec_rows : 128 / G * G * tile_slots(D->d);
+    const int32_t step = few ? B->dec_rows : 128 / G * G * tile_slots(D->d);
     for (int32_t g = 0; g < D->Hkv; ++g)
       for (int32_t r0 = 0; r0 < rows; r0 += step) {
         const int32_t r1 = std::min(rows, r0 + step);
         const int64_t seen = D->causal ? int64_t(n) - q + (r1 - 1) / G + 1 : n;
-        if (few) X->dec_live = std::max(X->dec_live, r1 - r0);
+        if (few) B->dec_live = std::max(B->dec_live, r1 - r0);
         (few ? dec : tile).push_back({b, g, r0, r1 - r0, int32_t(std::max<int64_t>(0, seen))});
       }
   }
+  B->S.q0 = q0;
+  B->S.q_len.assign(D->q_len, D->q_len + D->B);
+  B->S.kv_len.assign(D->kv_len, D->kv_len + D->B);
+  B->S.page_off = B->page_off;
+  B->S.nblk.assign(D->B, 0);
   return BD_OK;
 }
 
 // The pieces are read 16 bytes at a time: each list starts on a multiple of 4 words.
 int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
+// Words of the header, the fixed places and the lists of rows and pages.
+int64_t list_words(const Built& X, bool sparse) {
+  return up4(kOffLists + (sparse ? 3 : 2) * X.T + 3 * X.npages + X.ntouch);
+}
+
 // Words that hold the plan however its blocks are cut: a cut block's parts but one come
 // out of the slots.
-int64_t most_words(const Built& X) {
-  int64_t w = up4(kOffLists + X.T + 3 * X.npages);
+int64_t most_words(const Built& X, bool sparse) {
+  int64_t w = list_words(X, sparse);
   if (!X.dec_items.empty()) w += (int64_t(X.dec_items.size()) + kDecSlots) * kPieceWords;
   if (!X.tile_items.empty()) w += (int64_t(X.tile_items.size()) + kTilePartSlots) * kPieceWords;
   return w;
@@ -443,30 +504,31 @@ static int32_t guarded(F&& f) {
   }
 }
 
-static int32_t plan_bytes(const bd_paged_desc* desc, size_t* bytes) {
+static int32_t plan_bytes(const bd_paged_desc* desc, const bd_sparse_desc* sparse, size_t* bytes) {
   if (!bytes) return fail(BD_ERR_ARG, "bytes is NULL");
   Built X;
-  int32_t st = prepare(desc, &X);
+  int32_t st = prepare(desc, sparse, &X);
   if (st) return st;
-  const int64_t w = most_words(X);
+  const int64_t w = most_words(X, sparse);
   if (w > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
   *bytes = size_t(w) * 4;
   return ok();
 }
 
-static int32_t plan_build(const bd_paged_desc* desc, void* blob, size_t blob_bytes) {
+static int32_t plan_build(const bd_paged_desc* desc, const bd_sparse_desc* sparse, void* blob, size_t blob_bytes) {
   if (!blob || reinterpret_cast<uintptr_t>(blob) % 16) return fail(BD_ERR_ARG, "blob NULL or not 16-byte aligned");
   Built X;
-  int32_t st = prepare(desc, &X);
+  int32_t st = prepare(desc, sparse, &X);
   if (st) return st;
-  if (most_words(X) > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
-  if (blob_bytes < size_t(most_words(X)) * 4)
-    return fail(BD_ERR_CAPACITY, "plan blob of %zu bytes, %lld needed", blob_bytes, (long long)most_words(X) * 4);
+  const int64_t most = most_words(X, sparse);
+  if (most > INT32_MAX) return fail(BD_ERR_CAPACITY, "plan blob past 2^31 words");
+  if (blob_bytes < size_t(most) * 4)
+    return fail(BD_ERR_CAPACITY, "plan blob of %zu bytes, %lld needed", blob_bytes, (long long)most * 4);
   const bd_paged_desc& D = *desc;
   Lists dec, tile;
-  dec_lists(D, X.dec_items, X.q0, X.page_off, &dec);
-  tile_lists(D, X.tile_items, X.q0, X.page_off, &tile);
-  const int64_t words = up4(kOffLists + X.T + 3 * X.npages) + int64_t(dec.pieces.size()) + int64_t(tile.pieces.size());
+  dec_lists(D, X.dec_items, X.S, &dec);
+  tile_lists(D, X.tile_items, X.S, &tile);
+  const int64_t words = list_words(X, sparse) + int64_t(dec.pieces.size()) + int64_t(tile.pieces.size());
   int32_t* w = static_cast<int32_t*>(blob);
   std::memset(w, 0, size_t(words) * 4);
   const int32_t P = D.page_size;
@@ -483,7 +545,17 @@ static int32_t plan_build(const bd_paged_desc* desc, void* blob, size_t blob_byt
   w[PH_OFF_PAGES] = int32_t(w[PH_OFF_TOK] + X.T);
   w[PH_OFF_PGROW] = int32_t(w[PH_OFF_PAGES] + X.npages);
   w[PH_OFF_PGCNT] = int32_t(w[PH_OFF_PGROW] + X.npages);
-  int64_t tok = 0, pg = 0, kv = 0;
+  w[PH_OFF_POS] = int32_t(w[PH_OFF_PGCNT] + X.npages);
+  w[PH_OFF_TOUCH] = int32_t(w[PH_OFF_POS] + X.T);
+  w[PH_NTOUCH] = int32_t(X.ntouch);
+  if (sparse) {
+    w[PH_BLOCKS] = sparse->blocks; w[PH_FIRST] = sparse->first; w[PH_RECENT] = sparse->recent;
+    w[PH_OFF_ROWPG] = int32_t(w[PH_OFF_TOUCH] + X.ntouch);
+    w[PH_SEL_CAP] = X.sel_cap;
+    std::copy(X.S.page_off.begin(), X.S.page_off.end(), w + w[PH_OFF_ROWPG]);
+  }
+  int64_t tok = 0, pg = 0, kv = 0, touch = 0;
+  std::vector<int32_t> entered;  // pages that new rows enter
   struct Range { int32_t lo, hi; };
   std::vector<Range> written;  // cache rows the new rows take, one range per page touched
   for (int32_t b = 0; b < D.B; ++b) {
@@ -493,11 +565,16 @@ static int32_t plan_build(const bd_paged_desc* desc, void* blob, size_t blob_byt
       w[w[PH_OFF_PAGES] + pg] = pages[j / P];
       w[w[PH_OFF_PGROW] + pg] = int32_t(kv + j);
       w[w[PH_OFF_PGCNT] + pg] = std::min(P, n - j);
+      if (D.causal && j + P > n - q && q > 0) {
+        w[w[PH_OFF_TOUCH] + touch++] = int32_t(pg);
+        entered.push_back(pages[j / P]);
+      }
       ++pg;
     }
     for (int32_t i = 0; i < q; ++i) {
       const int64_t pos = int64_t(n) - q + i;
       const int32_t row = pos < 0 ? -1 : pages[pos / P] * P + int32_t(pos % P);
+      w[w[PH_OFF_POS] + tok] = int32_t(std::max<int64_t>(pos, -1));
       w[w[PH_OFF_TOK] + tok++] = row;
       if (row < 0) continue;
       if (!written.empty() && written.back().hi == row && row % P) written.back().hi = row + 1;
@@ -509,7 +586,9 @@ static int32_t plan_build(const bd_paged_desc* desc, void* blob, size_t blob_byt
   w[PH_WRITE_OK] = D.causal;
   for (size_t i = 1; i < written.size(); ++i)
     if (written[i].lo < written[i - 1].hi) w[PH_WRITE_OK] = 0;
-  int64_t at = up4(kOffLists + X.T + 3 * X.npages);
+  std::sort(entered.begin(), entered.end());
+  w[PH_BOUNDS_OK] = D.causal && std::adjacent_find(entered.begin(), entered.end()) == entered.end();
+  int64_t at = list_words(X, sparse);
   auto put = [&](const Lists& L, int off, int n, int nm, int rec, int mrg) {
     w[off] = int32_t(at);
     w[n] = int32_t(L.pieces.size() / kPieceWords);
@@ -531,11 +610,21 @@ static int32_t plan_build(const bd_paged_desc* desc, void* blob, size_t blob_byt
 }
 
 extern "C" int32_t bd_paged_plan_bytes(const bd_paged_desc* desc, size_t* bytes) {
-  return guarded([&] { return plan_bytes(desc, bytes); });
+  return guarded([&] { return plan_bytes(desc, nullptr, bytes); });
 }
 
 extern "C" int32_t bd_paged_plan_build(const bd_paged_desc* desc, void* blob, size_t blob_bytes) {
-  return guarded([&] { return plan_build(desc, blob, blob_bytes); });
+  return guarded([&] { return plan_build(desc, nullptr, blob, blob_bytes); });
+}
+
+extern "C" int32_t bd_sparse_plan_bytes(const bd_paged_desc* desc, const bd_sparse_desc* sparse, size_t* bytes) {
+  int32_t st = check_sparse(desc, sparse);
+  return st ? st : guarded([&] { return plan_bytes(desc, sparse, bytes); });
+}
+
+extern "C" int32_t bd_sparse_plan_build(const bd_paged_desc* desc, const bd_sparse_desc* sparse, void* blob, size_t blob_bytes) {
+  int32_t st = check_sparse(desc, sparse);
+  return st ? st : guarded([&] { return plan_build(desc, sparse, blob, blob_bytes); });
 }
 
 extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
@@ -546,7 +635,8 @@ extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
   // what a captured launch holds of the plan (FNV-1a over the words)
   const int32_t fields[] = {w[PH_H], w[PH_HKV], w[PH_D], w[PH_PAGE], w[PH_NUM_PAGES], w[PH_FMT], w[PH_CAUSAL],
                             w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0,
-                            w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0, w[PH_NTILE] > 0, w[PH_NTILEM] > 0};
+                            w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0, w[PH_NTILE] > 0, w[PH_NTILEM] > 0,
+                            w[PH_NTOUCH] > 0, w[PH_BOUNDS_OK], w[PH_BLOCKS], w[PH_FIRST], w[PH_RECENT], w[PH_SEL_CAP]};
   uint64_t h = 1469598103934665603ull;
   for (int32_t f : fields)
     for (int i = 0; i < 4; ++i) h = (h ^ ((uint32_t(f) >> (8 * i)) & 255u)) * 1099511628211ull;

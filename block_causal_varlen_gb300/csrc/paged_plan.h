@@ -10,7 +10,7 @@
 namespace bd {
 
 constexpr int32_t kPagedMagic = 0x50414442;  // "BDAP"
-constexpr int32_t kPagedVersion = 1;
+constexpr int32_t kPagedVersion = 2;
 // SMs of a GB300. The persistent attention kernels' work lists are cut for one CTA
 // (tiles) or two (few rows: one adds up a block while the other's loads go on) on each.
 constexpr int kPagedSms = 152;
@@ -59,6 +59,15 @@ enum : int {
   PH_OFF_TILE,     // the same for the tile kernel
   PH_NTILE,
   PH_NTILEM,
+  PH_OFF_POS,      // int32 [T]: position of every new row, negative for none
+  PH_OFF_TOUCH,    // int32 [NTOUCH]: entries of the page list that hold new rows
+  PH_NTOUCH,
+  PH_BOUNDS_OK,    // whether their pages are all different (causal plans)
+  PH_BLOCKS,       // sparse plans: blocks of a list (0: not sparse), first and recent ones
+  PH_FIRST,
+  PH_RECENT,
+  PH_OFF_ROWPG,    // int32 [T]: word offset of the pages of every new row's sequence
+  PH_SEL_CAP,      // a power of two that no new row has more blocks than
   PH_STATUS = H_STATUS, PH_STATUS_DETAIL = H_STATUS_DETAIL, // 5 few-rows attention, 6 tile attention
   kPagedHdrWords = kHdrWords
 };
@@ -75,7 +84,7 @@ enum : int {
   PC_K0, PC_K1, // keys [k0, k1); k0 a multiple of the kernel's unit
   PC_SLOT,      // partial-result slot, -1: the whole key range, written to the output
   PC_T0,        // PC_ROW0 / G: the block's first new row
-  PC_RESERVED0,
+  PC_NBLK,      // sparse plans: blocks of the sequence up to the row's own
   kPieceWords = 12
 };
 
@@ -93,6 +102,15 @@ constexpr int kOffDecMerge = kOffDecRec + kDecCtas * kRecordWords;
 constexpr int kOffTileRec = kOffDecMerge + kDecSlots / 2 * kMergeWords;
 constexpr int kOffTileMerge = kOffTileRec + kTileCtas * kRecordWords;
 constexpr int kOffLists = kOffTileMerge + kTilePartSlots / 2 * kMergeWords;
+
+// Sparse plans: the most blocks of a list, and of a sequence (its scores stay in one CTA's
+// shared memory, 4 bytes each).
+constexpr int kMostListed = 4096, kMostBlocks = 16384;
+
+// Bytes of one head's K (or V) of a cached row, and of its scales' alignment (e2m1).
+constexpr int row_bytes(int fmt, int d) { return fmt == BD_CACHE_BF16 ? 2 * d : fmt == BD_CACHE_E4M3 ? d : d / 2; }
+constexpr int elem_bytes(int fmt) { return fmt == BD_CACHE_BF16 ? 2 : 1; }  // of a cache's strides
+constexpr int scale_align(int d) { return d == 64 ? 4 : 8; }
 
 // Validated view of a host plan blob.
 int32_t view_paged_plan(const void* plan_host, const int32_t** out);

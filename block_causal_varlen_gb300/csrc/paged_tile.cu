@@ -22,9 +22,13 @@
 //                not every row sees; those who see them get them at the block's end, read
 //                from the cache (a rare and slow path)
 //   warps 4-11   softmax, thread = row; they also store the results
-//   warps 12-15  e4m3 only: turn raw tiles into bf16 ones. A code's bits, shifted into
+//   warps 12-15  e4m3: turn raw tiles into bf16 ones. A code's bits, shifted into
 //                a bf16, are its value times 2^-120; one packed multiplication by
-//                2^(120 + e) gives the exact value (e: the row's exponent)
+//                2^(120 + e) gives the exact value (e: the row's exponent). e2m1: turn raw
+//                tiles, and Q's, into fp16 ones, where a conversion and a multiplication
+//                give two exact values; Q's rows are scaled by a power of two to a maximum
+//                of 2^14 first (exact but for what is below 2^-31 of the row's largest), and
+//                P is fp16 as well
 // Work comes from the plan: every CTA walks its own list of pieces (block, key range).
 // A piece that is not its block's whole key range stores m, l and O for the join.
 //
@@ -41,6 +45,7 @@
 #include <type_traits>
 
 #include "paged.h"
+#include "paged_quant.cuh"
 #include "ptx.cuh"
 
 namespace bd {
@@ -50,12 +55,15 @@ namespace {
 
 template <int D, int FMT>
 struct TileCfg {
-  static constexpr bool kF8 = FMT == BD_CACHE_E4M3;
+  static constexpr bool kF8 = FMT == BD_CACHE_E4M3, kF4 = FMT == BD_CACHE_E2M1;
+  static constexpr bool kConv = kF8 || kF4;       // tiles are converted
   static constexpr int kSlots = tile_slots(D);
   static constexpr int kTileBytes = 128 * D * 2;  // 128 rows x D bf16
   static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 4;
-  static constexpr int kRawBytes = kF8 ? 128 * D : 0;
-  static constexpr int kRawStages = !kF8 ? 0 : D == 256 ? 1 : D == 128 ? 2 : 4;  // K, V, K, V, ...
+  static constexpr int kRowBytes = row_bytes(FMT, D);
+  static constexpr int kPieceBytes = kRowBytes < 128 ? kRowBytes : 128;  // of a row in shared memory
+  static constexpr int kRawBytes = kConv ? 128 * kRowBytes : 0;
+  static constexpr int kRawStages = !kConv ? 0 : kF4 && D == 256 ? 2 : D == 256 ? 1 : D == 128 ? 2 : 4;  // K, V, K, V, ...
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kSlots * kTileBytes;
   static constexpr int kOffV = kOffK + kStages * kTileBytes;
@@ -66,24 +74,25 @@ struct TileCfg {
   // out. 4096 rows over 16384 (10 ragged sequences for e4m3) in registers and through
   // shared memory: bf16 d 64 624 and 590 us, d 128 650 and 672, d 256 1856 and 1872; e4m3
   // d 128 274 and 272.
-  static constexpr bool kTurnInRegs = !kF8 && D >= 128;
-  static constexpr bool kStageInQ = kF8 && D >= 128;
+  static constexpr bool kTurnInRegs = !kConv && D >= 128;
+  static constexpr bool kStageInQ = kConv && D >= 128;
   static constexpr int kOffStage = kOffRaw + kRawStages * kRawBytes;
   static constexpr int kOffBar = kOffStage + (kStageInQ || kTurnInRegs ? 0 : kSlots * 16384);
   static constexpr int kOffPieces = kOffBar + 512;
-  static constexpr int kPre = 16;                 // pieces kept in shared memory
-  static constexpr int kSmem = kOffPieces + kPre * kPieceWords * 4 + 1024;  // + alignment slack
+  static constexpr int kPre = kF4 ? 8 : 16;       // pieces kept in shared memory
+  static constexpr int kOffQs = kOffPieces + kPre * kPieceWords * 4;  // e2m1: score factors of the rows of two blocks
+  static constexpr int kSmem = kOffQs + (kF4 ? 2 * 128 * kSlots * 4 : 0) + 1024;  // + alignment slack
   static constexpr int kOCol = 256;               // first O column in TMEM
   // Whether P is handed to the tensor core in halves. With one slot the first half of P V
   // runs while the second half of P is made (4096 rows over 16384 at d 256: 2090 ->
   // 1890 us); with two the other slot's products fill that time, and the early half only
   // gets in their way (d 128: 668 -> 724).
   static constexpr bool kPHalves = kSlots == 1;
-  static constexpr int kThreads = kF8 ? 512 : 384;
+  static constexpr int kThreads = kConv ? 512 : 384;
   // registers after setmaxnreg: warps 0-3, the softmax warps, the converting warps
-  static constexpr int kRegsCtl = kF8 ? 40 : 72, kRegsSoftmax = kF8 ? 200 : 216, kRegsConv = 72;
-  static constexpr int kRegsLaunch = kF8 ? 128 : 168;
-  static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kF8 ? 128 * kRegsConv : 0) <= kRegsLaunch * kThreads,
+  static constexpr int kRegsCtl = kConv ? 40 : 72, kRegsSoftmax = kConv ? 200 : 216, kRegsConv = 72;
+  static constexpr int kRegsLaunch = kConv ? 128 : 168;
+  static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kConv ? 128 * kRegsConv : 0) <= kRegsLaunch * kThreads,
                 "register split exceeds the launch's registers");
   static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
   static_assert(kOCol + kSlots * D <= 512, "O accumulators exceed TMEM");
@@ -93,7 +102,7 @@ struct TileCfg {
 enum : int {
   T_QFULL = 0, T_QEMPTY, T_KFULL = 4, T_KEMPTY = 8, T_VFULL = 12, T_VEMPTY = 16, T_RFULL = 20, T_REMPTY = 24,
   T_SFULL = 28, T_PFULL = 30, T_OFINAL = 32, T_OEMPTY = 34, T_TURN = 36, T_DRAIN = 38, T_VTAIL = 40, T_PHALF = 44,
-  T_COUNT = 46
+  T_QCONV = 46, T_COUNT = 47
 };
 constexpr int kOddMarks = 8;  // at most 4 key tiles, so 4 blocks, are under way at a time
 static_assert(8 * T_COUNT + 16 + 4 * kOddMarks <= 512, "barriers, TMEM slot, abort flag and marks overflow their region");
@@ -130,8 +139,8 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     bd_paged_tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const AttnArgs a) {
   using Cfg = TileCfg<D, FMT>;
-  constexpr bool F8 = Cfg::kF8;
-  constexpr int NS = Cfg::kSlots, NST = Cfg::kStages, NR = F8 ? Cfg::kRawStages : 1;
+  constexpr bool F8 = Cfg::kF8, F4 = Cfg::kF4, CONV = Cfg::kConv;
+  constexpr int NS = Cfg::kSlots, NST = Cfg::kStages, NR = CONV ? Cfg::kRawStages : 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -144,6 +153,9 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
   // were taken out (or if a later block has written over the mark)
   volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(smem + Cfg::kOffBar + 8 * T_COUNT + 16);
   int32_t* pre = reinterpret_cast<int32_t*>(smem + Cfg::kOffPieces);
+  // e2m1: score factors of the n-th block's rows at ((n - 1) & 1) * 128 NS. They are read before the
+  // block's first P goes to the tensor core, and the block after next is not turned before that
+  volatile float* qs = reinterpret_cast<volatile float*>(smem + Cfg::kOffQs);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int32_t* plan = a.plan;
@@ -167,11 +179,12 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     mbar_init(bar(T_QFULL), 1);
+    mbar_init(bar(T_QCONV), 128);
     mbar_init(bar(T_QEMPTY), Cfg::kStageInQ ? 4 * NS : NS);  // softmax warps, or MMA threads
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar(T_KFULL + s), F8 ? 128 : 1);
+      mbar_init(bar(T_KFULL + s), CONV ? 128 : 1);
       mbar_init(bar(T_KEMPTY + s), NS);
-      mbar_init(bar(T_VFULL + s), F8 ? 128 : 1);
+      mbar_init(bar(T_VFULL + s), CONV ? 128 : 1);
       mbar_init(bar(T_VEMPTY + s), NS);
       mbar_init(bar(T_VTAIL + s), 1);
     }
@@ -218,19 +231,18 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       // -------------------------------------------------------- producer (whole warp)
       const int rows = min(1 << pshift, 128);   // rows of a copy
       const int rshift = min(pshift, 7);
-      const int row_bytes = F8 && D == 64 ? 64 : 128;
-      constexpr int kPieces = F8 ? (D + 127) / 128 : D / 64;
+      constexpr int kPieceBytes = Cfg::kPieceBytes, kPieces = Cfg::kRowBytes / kPieceBytes;
       uint32_t it = 0, rit = 0, qi = 0;
       bool ok = true;
       // one matrix of the key tile at `pos`, `n` copies, into `dst`
       auto load = [&](const CUtensorMap* m, uint32_t dst, uint32_t full, int n, int pos, int page, int hkv) {
-        if (lane == 0) mbar_expect_tx(full, uint32_t(n * rows * row_bytes * kPieces));
+        if (lane == 0) mbar_expect_tx(full, uint32_t(n * rows * kPieceBytes * kPieces));
         __syncwarp();
         if (lane < n) {
           const int row = (pos + lane * rows) & ((1 << pshift) - 1);
 #pragma unroll
           for (int c = 0; c < kPieces; ++c)
-            tma_load_5d(dst + c * 128 * row_bytes + lane * rows * row_bytes, m, full, 0, row, c, hkv, page);
+            tma_load_5d(dst + c * 128 * kPieceBytes + lane * rows * kPieceBytes, m, full, 0, row, c, hkv, page);
         }
         __syncwarp();
       };
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           const int pos = P.k0 + 128 * j;
           const int n = (min(P.k1 - pos, 128) + rows - 1) >> rshift;
           const int next = j + 1 < P.nt ? page_of(pos + 128) : 0;
-          if constexpr (!F8) {
+          if constexpr (!CONV) {
             const int s = it % NST;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_KEMPTY + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
             load(&tm_k, sK + s * Cfg::kTileBytes, bar(T_KFULL + s), n, pos, page, P.hkv);
@@ -280,7 +292,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       if (!ok) {
         // let copies already issued land before the CTA's shared memory goes away (what
         // has landed returns at once; each wait is bounded)
-        if constexpr (!F8) {
+        if constexpr (!CONV) {
           for (int s = 0; s < NST; ++s) {
             const uint32_t lk = it + 1;  // K may be one tile further than V
             for (uint32_t x = lk > uint32_t(NST) ? lk - NST : 0; x < lk; ++x)
@@ -313,8 +325,8 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           if (NS == 2) mbar_arrive(bar(T_TURN + (s ^ 1)));
           ++my_turn;
         };
-        constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
-        constexpr uint32_t idPV = idesc_bf16(128, D, false, true);
+        constexpr uint32_t idS = F4 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idPV = F4 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
         const uint32_t d_s = tmem + s * 128, d_o = tmem + Cfg::kOCol + s * D;
         const uint32_t qa = sdesc_lo(sQ + s * Cfg::kTileBytes, 16);
         auto issue_s = [&](int st) {
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           const Piece P = piece(p);
           if (P.nt == 0) continue;
           const bool act = s < P.ns;
-          if (!(ok = mbar_wait(bar(T_QFULL), qi & 1, abort_flag))) break;
+          if (!(ok = mbar_wait(bar(F4 ? T_QCONV : T_QFULL), qi & 1, abort_flag))) break;
           ++qi;
           {
             const int sk = it % NST;
@@ -411,7 +423,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           mbar_wait_drain(bar(T_DRAIN + s), 0);
         }
       }
-    } else if (warp == 3 && !F8) {
+    } else if (warp == 3 && !CONV) {
       // -------------------------------------------------------- V rows some do not see
       // Such a tile's load completes T_VTAIL of its stage; this warp completes T_VFULL.
       uint32_t it = 0, n = 0, parity = 0;  // bit s: phase of T_VTAIL + s (a stage's next such load waits for its products)
@@ -460,6 +472,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_base + s * 128, tO = tmem + lane_base + Cfg::kOCol + s * D;
     const int tl = r / G, hg = r - tl * G;
+    constexpr float kPShift = F4 ? 7.f : 0.f;  // P, and with it l and O, are held times 2^this
     uint32_t tc = 0, ai = 0, n = 0;
     bool ok = s < NS;
     for (int p = p0; p < p1 && ok; ++p) {
@@ -479,11 +492,12 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         }
         continue;
       }
-      float m_run = -CUDART_INF_F, l_run = 0.f;
+      float m_run = -CUDART_INF_F, l_run = 0.f, scale = a.scale_log2;
       for (int j = 0; j < P.nt; ++j, ++tc) {
         // (warps leave together: what follows is warp-wide)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_SFULL + s), tc & 1, abort_flag)))) break;
         tc_fence_after();
+        if (F4 && j == 0) scale = qs[((n - 1) & 1) * 128 * NS + s * 128 + r];
         uint32_t u[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, u[q]);
@@ -525,7 +539,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 8; ++k) m8[k] = max3f(m8[k], x[e + k], x[e + 8 + k]);
         const float mx = fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(max3f(m8[3], m8[4], m8[5]), m8[6], m8[7]));
-        const float m_new = fmaxf(m_run, mx * a.scale_log2);
+        const float m_new = fmaxf(m_run, mx * scale);
         const bool need = m_new > m_run + 8.0f;  // O is rescaled only when the maximum grows by more than 2^8
         float factor = 1.f;
         if (need) {
@@ -545,8 +559,8 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             tmem_st32(tO + q * 32, ov);
           }
         }
-        const float m_eff = (m_run == -CUDART_INF_F) ? 0.f : m_run;
-        const float2 cs = make_float2(a.scale_log2, a.scale_log2), cm = make_float2(-m_eff, -m_eff);
+        const float m_eff = ((m_run == -CUDART_INF_F) ? 0.f : m_run) - kPShift;
+        const float2 cs = make_float2(scale, scale), cm = make_float2(-m_eff, -m_eff);
         float2 s4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[2][32];
 #pragma unroll
@@ -555,7 +569,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           v.x = ex2(v.x);
           v.y = ex2(v.y);
           s4[e & 3] = fadd2(s4[e & 3], v);
-          pk[e >> 5][e & 31] = pack_bf16(v.x, v.y);
+          pk[e >> 5][e & 31] = F4 ? pack_f16(v.x, v.y) : pack_bf16(v.x, v.y);
           if (Cfg::kPHalves && e == 31) {
             tmem_st32(tS, pk[0]);
             tmem_st_wait();
@@ -585,6 +599,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             if (a.v_exp[page * a.e_sp + row * a.e_sr + P.hkv * a.e_sh] == 255u)
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = 0x7fffffffu;
+          } else if constexpr (F4) {
+            const uint8_t* b = a.v_exp + page * a.e_sp + row * a.e_sr + P.hkv * a.e_sh + c0 / 16;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (b[e / 16] > kMostScale) o[e] = 0x7fffffffu;
           } else {
             const uint4* v = reinterpret_cast<const uint4*>(a.vc + page * a.v_sp + row * a.v_sr + P.hkv * a.v_sh + c0 * 2);
 #pragma unroll
@@ -601,7 +620,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         }
       };
       // NaN scores leave the maximum alone: what they gave was taken relative to 0
-      const float m_fin = m_run == -CUDART_INF_F && l_run != 0.f ? 0.f : m_run;
+      const float m_fin = (m_run == -CUDART_INF_F && l_run != 0.f ? 0.f : m_run) - kPShift;
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       if (part) {
         if (live) {
@@ -695,7 +714,112 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
       }
     }
   } else {
-    if constexpr (F8) {
+    if constexpr (F4) {
+      regs_set<Cfg::kRegsConv, Cfg::kRegsLaunch>();
+      // -------------------------------------------------------- raw tiles to fp16, thread = key
+      const int r = threadIdx.x - 384;
+      constexpr int RB = Cfg::kRowBytes, NW = D / 64;  // words of a row's scales
+      struct Scales { uint32_t k[NW], v[NW]; };
+      uint32_t it = 0, rit = 0, n = 0;
+      bool ok = true;
+      auto convert = [&](uint32_t src, uint32_t dst, const uint32_t (&sc)[NW]) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {  // 16 bytes: 32 codes, two scales
+          const int x = RB == 32 ? c ^ ((r >> 2) & 1) : RB == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7);
+          const uint4 u = ld_shared_u4(src + r * RB + (x << 4));
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w}, two = sc[c >> 1] >> (16 * (c & 1));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+            e2m1x8_to_f16(w[i], h);
+            const uint32_t f = scale_twice(i < 2 ? two & 255u : (two >> 8) & 255u);
+            const int oc = (c & 1) * 4 + i;
+            st_shared_v4(dst + (c >> 1) * 16384 + r * 128 + ((oc ^ (r & 7)) << 4), mul_f16x2(h[0], f), mul_f16x2(h[1], f),
+                         mul_f16x2(h[2], f), mul_f16x2(h[3], f));
+          }
+        }
+        fence_proxy_async_smem();
+      };
+      // Q's rows of a block: bf16 to fp16, times a power of two each (its inverse goes to the
+      // row's score factor)
+      auto convert_q = [&](int ns) {
+        for (int s = 0; s < ns; ++s) {
+          const uint32_t q = sQ + s * Cfg::kTileBytes + r * 128;
+          auto at = [&](int c) { return q + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4); };
+          uint32_t mx = 0;
+#pragma unroll 8
+          for (int c = 0; c < D / 8; ++c) mx = max(mx, absmax8(ld_shared_u4(at(c))));
+          float inv;
+          const float2 up = q_factors(mx, &inv);
+          qs[((n - 1) & 1) * 128 * NS + s * 128 + r] = a.scale_log2 * inv;
+#pragma unroll 4
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 u = ld_shared_u4(at(c));
+            auto f16 = [&](uint32_t x) { return pack_f16(bf16_lo(x) * up.x * up.y, bf16_hi(x) * up.x * up.y); };
+            st_shared_v4(at(c), f16(u.x), f16(u.y), f16(u.z), f16(u.w));
+          }
+        }
+        fence_proxy_async_smem();
+      };
+      for (int p = p0; p < p1 && ok; ++p) {
+        const Piece P = piece(p);
+        // this row's scales come one tile ahead, its page number two
+        auto page_of = [&](int j) {
+          const int pos = P.k0 + 128 * j + r;
+          return j < P.nt && pos < P.k1 ? plan[P.pages + (pos >> pshift)] : -1;
+        };
+        auto scales_of = [&](int j, int page) {
+          Scales x = {};
+          if (page < 0) return x;
+          const int64_t o = int64_t(page) * a.e_sp + int64_t((P.k0 + 128 * j + r) & ((1 << pshift) - 1)) * a.e_sr + int64_t(P.hkv) * a.e_sh;
+          if constexpr (D == 64) {
+            x.k[0] = *reinterpret_cast<const uint32_t*>(a.k_exp + o);
+            x.v[0] = *reinterpret_cast<const uint32_t*>(a.v_exp + o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < NW; i += 2) {
+              const uint2 k = *reinterpret_cast<const uint2*>(a.k_exp + o + 4 * i), v = *reinterpret_cast<const uint2*>(a.v_exp + o + 4 * i);
+              x.k[i] = k.x; x.k[i + 1] = k.y;
+              x.v[i] = v.x; x.v[i + 1] = v.y;
+            }
+          }
+          return x;
+        };
+        if (P.nt == 0) continue;
+        ++n;
+        int pg = page_of(0);
+        Scales ahead = scales_of(0, pg);
+        pg = page_of(1);
+        for (int j = 0; j < P.nt; ++j, ++it) {
+          Scales now = ahead;  // rows past the keys' end: zeros
+          ahead = scales_of(j + 1, pg);
+          pg = page_of(j + 2);
+          const int s = it % NST;
+          // V's scales of NaN stay out of the products where some row does not see the key
+          if (P.k0 + 128 * j + r >= P.clear)
+#pragma unroll
+            for (int i = 0; i < NW; ++i) {
+              const uint32_t gone = __vcmpgtu4(now.v[i], kMostScale * 0x01010101u);
+              now.v[i] &= ~gone;
+              if (gone) odd[(n - 1) % kOddMarks] = n;
+            }
+          for (int h = 0; h < 2; ++h, ++rit) {
+            const int rs = rit % NR;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_RFULL + rs), (rit / NR) & 1, abort_flag)))) break;
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar((h ? T_VEMPTY : T_KEMPTY) + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
+            convert(sR + rs * Cfg::kRawBytes, (h ? sV : sK) + s * Cfg::kTileBytes, h ? now.v : now.k);
+            mbar_arrive(bar(T_REMPTY + rs));
+            mbar_arrive(bar((h ? T_VFULL : T_KFULL) + s));
+          }
+          if (!ok) break;
+          if (j == 0) {
+            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_QFULL), (n - 1) & 1, abort_flag)))) break;
+            convert_q(P.ns);
+            mbar_arrive(bar(T_QCONV));
+          }
+        }
+      }
+    } else if constexpr (F8) {
       regs_set<Cfg::kRegsConv, Cfg::kRegsLaunch>();
       // -------------------------------------------------------- raw tiles to bf16, thread = key
       const int r = threadIdx.x - 384;
@@ -820,17 +944,21 @@ int32_t launch_tile_t(const CUtensorMap& mq, const CUtensorMap& mk, const CUtens
 }  // namespace
 
 int32_t launch_tile(const int32_t* w, const AttnArgs& a, const bd_tensor* q, const bd_paged_cache* c, cudaStream_t s) {
-  const int es = c->fmt == BD_CACHE_BF16 ? 2 : 1, d = w[PH_D], G = w[PH_G];
+  const int d = w[PH_D], G = w[PH_G], es = elem_bytes(c->fmt), bytes = row_bytes(c->fmt, d), piece = bytes < 128 ? bytes : 128;
   const int rows = w[PH_PAGE] < 128 ? w[PH_PAGE] : 128;
   CUtensorMap mq, mk, mv;
   int32_t st;
   if ((st = make_tmap_group_bf16(&mq, q, w[PH_H], d, "q", G, 128 / G))) return st;
-  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], d, es, "cache k", rows, false))) return st;
-  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], d, es, "cache v", rows, false))) return st;
+  if ((st = make_tmap_pages(&mk, &c->k, c->num_pages, w[PH_HKV], bytes, es, "cache k", rows, false, piece))) return st;
+  if ((st = make_tmap_pages(&mv, &c->v, c->num_pages, w[PH_HKV], bytes, es, "cache v", rows, false, piece))) return st;
   if (c->fmt == BD_CACHE_BF16)
     return d == 64 ? launch_tile_t<64, BD_CACHE_BF16>(mq, mk, mv, a, s)
            : d == 128 ? launch_tile_t<128, BD_CACHE_BF16>(mq, mk, mv, a, s)
                       : launch_tile_t<256, BD_CACHE_BF16>(mq, mk, mv, a, s);
+  if (c->fmt == BD_CACHE_E2M1)
+    return d == 64 ? launch_tile_t<64, BD_CACHE_E2M1>(mq, mk, mv, a, s)
+           : d == 128 ? launch_tile_t<128, BD_CACHE_E2M1>(mq, mk, mv, a, s)
+                      : launch_tile_t<256, BD_CACHE_E2M1>(mq, mk, mv, a, s);
   return d == 64 ? launch_tile_t<64, BD_CACHE_E4M3>(mq, mk, mv, a, s)
          : d == 128 ? launch_tile_t<128, BD_CACHE_E4M3>(mq, mk, mv, a, s)
                     : launch_tile_t<256, BD_CACHE_E4M3>(mq, mk, mv, a, s);

@@ -1,12 +1,16 @@
 """Paged K/V cache: the binding of include/bd_paged.h.
 
 Tensor layouts (all strided views are accepted; the head dim is contiguous):
-    cache k, v     bf16 or e4m3 codes [pages, page_size, Hkv, d], either may be a view
-                   of a head-first pool [pages, Hkv, page_size, d]
-    k_exp, v_exp   uint8 [pages, page_size, Hkv], e4m3 caches only
+    cache k, v     bf16 or e4m3 codes [pages, page_size, Hkv, d], or e2m1 codes, two a byte,
+                   uint8 [pages, page_size, Hkv, d / 2]; either may be a view of a head-first
+                   pool [pages, Hkv, page_size, ...]
+    k_exp, v_exp   uint8 [pages, page_size, Hkv] exponents of an e4m3 cache, or
+                   uint8 [pages, page_size, Hkv, d / 16] scales of an e2m1 cache
     q, out         bf16 [rows, H, d], rows >= T: the new rows of all sequences, packed
     k, v (new)     bf16 [rows, Hkv, d]
     lse            fp32 [H, rows]
+    bounds         int8 [pages, Hkv, 2, d] and uint8 [pages, Hkv]: what block selection goes by
+    blocks         int32 [rows, Hkv, blocks]: the blocks that a new row attends
 """
 from __future__ import annotations
 
@@ -17,11 +21,14 @@ import numpy as np
 import torch
 
 from . import _abi
-from ._abi import BD_CACHE_BF16, BD_CACHE_E4M3, bd_paged_cache, bd_paged_desc, bd_tensor, check, load
+from ._abi import (BD_CACHE_BF16, BD_CACHE_E2M1, BD_CACHE_E4M3, bd_bounds, bd_paged_cache, bd_paged_desc, bd_rope,
+                   bd_sparse_desc, bd_tensor, check, load)
 
 __all__ = ["PagedCache", "PagedPlan", "bd_paged_plan_bytes", "bd_paged_plan_build", "bd_paged_plan_key",
            "bd_cache_write", "bd_cache_read", "bd_paged_attn_workspace", "bd_paged_attn", "paged_attn",
-           "BD_CACHE_BF16", "BD_CACHE_E4M3"]
+           "BD_CACHE_BF16", "BD_CACHE_E4M3", "BD_CACHE_E2M1", "Rope", "bd_rope_phases", "bd_cache_append",
+           "bd_sparse_plan_bytes", "bd_sparse_plan_build", "BlockBounds", "bd_block_bounds", "bd_block_select",
+           "bd_sparse_attn", "sparse_attn"]
 
 _P32 = C.POINTER(C.c_int32)
 
@@ -38,9 +45,22 @@ def bd_paged_plan_build(desc: bd_paged_desc, blob_ptr: int, nbytes: int) -> None
     check(load().bd_paged_plan_build(C.byref(desc), C.c_void_p(blob_ptr), nbytes))
 
 
+def bd_sparse_plan_bytes(desc: bd_paged_desc, sparse: bd_sparse_desc) -> int:
+    """Bytes of the plan blob of a sparse plan (validates both descriptors)."""
+    n = C.c_size_t()
+    check(load().bd_sparse_plan_bytes(C.byref(desc), C.byref(sparse), C.byref(n)))
+    return n.value
+
+
+def bd_sparse_plan_build(desc: bd_paged_desc, sparse: bd_sparse_desc, blob_ptr: int, nbytes: int) -> None:
+    """Build the blob of a sparse plan into host memory at ``blob_ptr``."""
+    check(load().bd_sparse_plan_build(C.byref(desc), C.byref(sparse), C.c_void_p(blob_ptr), nbytes))
+
+
 class PagedCache:
-    """One layer's K/V pool as the library takes it. The tensors stay the caller's;
-    they are kept alive here, and their addresses are fixed for this object."""
+    """One layer's K/V pool as the library takes it; the tensors' dtype says its format
+    (bfloat16, float8_e4m3fn with exponents, uint8 with scales: e2m1). The tensors stay the
+    caller's; they are kept alive here, and their addresses are fixed for this object."""
 
     def __init__(self, k, v, k_exp=None, v_exp=None):
         for t, n in ((k, "k"), (v, "v")):
@@ -59,10 +79,23 @@ class PagedCache:
                     raise ValueError(f"{n}: an e4m3 cache needs uint8 exponents [pages, page_size, Hkv] on its device")
             if any(n > 1 and a != b for n, a, b in zip(k.shape, k_exp.stride(), v_exp.stride())):
                 raise ValueError("k_exp and v_exp must have the same strides")
+        elif k.dtype == torch.uint8:
+            self.fmt = BD_CACHE_E2M1
+            if k.shape[3] % 8:
+                raise ValueError(f"cache of {k.shape[3]} bytes of codes a head, expected half of a head dim of 64, 128 or 256")
+            for t, n in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+                if (t is None or t.dtype != torch.uint8 or t.shape != (*k.shape[:3], k.shape[3] // 8) or t.device != k.device
+                        or t.stride(3) != 1):
+                    raise ValueError(f"{n}: an e2m1 cache needs uint8 scales [pages, page_size, Hkv, d / 16] on its device, "
+                                     "those of a head contiguous")
+            if any(n > 1 and a != b for n, a, b in zip(k.shape[:3], k_exp.stride(), v_exp.stride())):
+                raise ValueError("k_exp and v_exp must have the same strides")
         else:
-            raise TypeError(f"cache dtype {k.dtype}, expected bfloat16 or float8_e4m3fn")
+            raise TypeError(f"cache dtype {k.dtype}, expected bfloat16, float8_e4m3fn or uint8 (e2m1 codes)")
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.num_pages, self.page_size, self.Hkv, self.d = k.shape
+        if self.fmt == BD_CACHE_E2M1:
+            self.d *= 2
         self.device = k.device
         st = [bd_tensor(t.data_ptr(), t.stride(0), 0, t.stride(1), t.stride(2), t.shape[1], 0) for t in (k, v)]
         es = k_exp.stride() if k_exp is not None else (0, 0, 0)
@@ -100,10 +133,14 @@ class PagedPlan:
     """Host plan blob of one step over a paged cache, and its device copy.
 
     ``q_len``, ``kv_len``: new rows of every sequence, and its cached rows with them;
-    ``pages``: a page list per sequence, or an integer table [B, max_pages].
+    ``pages``: a page list per sequence, or an integer table [B, max_pages]. With ``blocks``
+    the plan is a sparse one: every new row attends that many blocks (pages) of its sequence,
+    the ``first`` and the ``recent`` last ones always among them (bd_block_select,
+    bd_sparse_attn).
     """
 
-    def __init__(self, q_len, kv_len, pages, H, Hkv, d, page_size, num_pages, fmt=BD_CACHE_BF16, causal=True):
+    def __init__(self, q_len, kv_len, pages, H, Hkv, d, page_size, num_pages, fmt=BD_CACHE_BF16, causal=True, blocks=0,
+                 first=0, recent=1):
         q, kv = _ints(q_len, "q_len"), _ints(kv_len, "kv_len")
         H, Hkv, d, fmt = _int(H, "H"), _int(Hkv, "Hkv"), _int(d, "d"), _int(fmt, "fmt")
         page_size, num_pages = _int(page_size, "page_size"), _int(num_pages, "num_pages")
@@ -125,11 +162,16 @@ class PagedPlan:
         self.T, self.kv_total = int(q.sum(dtype=np.int64)), int(kv.sum(dtype=np.int64))
         desc = bd_paged_desc(self.B, H, Hkv, d, page_size, num_pages, fmt, int(self.causal), q.ctypes.data_as(_P32),
                              kv.ctypes.data_as(_P32), flat.ctypes.data_as(_P32), offs.ctypes.data_as(_P32))
-        self.nbytes = bd_paged_plan_bytes(desc)
+        self.blocks = _int(blocks, "blocks")
+        sparse = bd_sparse_desc(self.blocks, _int(first, "first"), _int(recent, "recent"), 0) if self.blocks else None
+        self.nbytes = bd_sparse_plan_bytes(desc, sparse) if sparse else bd_paged_plan_bytes(desc)
         self._raw = np.empty(self.nbytes // 4 + 16, dtype=np.int32)
         off = (-self._raw.ctypes.data % 64) // 4
         self.host = self._raw[off:off + self.nbytes // 4]
-        bd_paged_plan_build(desc, self.host.ctypes.data, self.nbytes)
+        if sparse:
+            bd_sparse_plan_build(desc, sparse, self.host.ctypes.data, self.nbytes)
+        else:
+            bd_paged_plan_build(desc, self.host.ctypes.data, self.nbytes)
         self.host = self.host[:int(self.host[2])]       # the words in use (csrc/paged_plan.h: PH_WORDS)
         self._host_ptr = self.host.ctypes.data
         self.dev = self._dev_ptr = None
@@ -272,6 +314,50 @@ def bd_cache_write(plan: PagedPlan, k, v, cache: PagedCache, stream=None):
     _call(_entry("bd_cache_write"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tk, tv, cache._addr)
 
 
+def bd_rope_phases(inv_freq) -> np.ndarray:
+    """Frequencies (radians a position, host numbers) as the kernels take them: uint64 turns a
+    position, modulo 1, in units of 2^-64 (see include/bd_paged.h)."""
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1)
+    out = np.empty(f.size, dtype=np.uint64)
+    check(load().bd_rope_phases(f.ctypes.data_as(C.POINTER(C.c_double)), f.size, out.ctypes.data_as(C.POINTER(C.c_uint64))))
+    return out
+
+
+class Rope:
+    """A position rotation of the first 2 * len(inv_freq) elements of a head: pair i turns by
+    inv_freq[i] radians a position. ``interleaved``: pairs (2 i, 2 i + 1) instead of
+    (i, i + len(inv_freq)); ``scale``: a factor of the turned elements. Made once (the
+    frequencies go through host memory), for the device of ``inv_freq`` or ``device``."""
+
+    def __init__(self, inv_freq, interleaved=False, scale=1.0, device=None):
+        if isinstance(inv_freq, torch.Tensor):
+            device = inv_freq.device if device is None else device
+            inv_freq = inv_freq.detach().double().cpu().numpy()
+        if np.ndim(inv_freq) != 1 or np.size(inv_freq) == 0:
+            raise ValueError("inv_freq: expected a vector, one frequency for each pair")
+        phase = bd_rope_phases(inv_freq)
+        self.dim, self.interleaved, self.scale = 2 * phase.size, bool(interleaved), float(scale)
+        self.phase = torch.from_numpy(phase.view(np.int64)).to("cuda" if device is None else device)
+        self._c = bd_rope(self.phase.data_ptr(), self.dim, int(self.interleaved), self.scale, 0)
+        self._addr = C.addressof(self._c)
+        self._index = self.phase.get_device()
+
+
+def bd_cache_append(plan: PagedPlan, q, k, v, rope: Rope, cache: PagedCache, q_out=None, stream=None):
+    """bd_cache_write of K turned by its positions, and of V as it is; q (or None) turned into
+    q_out, which may be q itself (see include/bd_paged.h)."""
+    idx = _device(plan, cache)
+    if rope._index != idx:
+        raise ValueError(f"rope: on {rope.phase.device}, the plan was uploaded to cuda:{idx}")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    tq = _rows3(q, "q", plan.H, plan.d, plan.T, idx) if q is not None else None
+    to = _rows3(q_out, "q_out", plan.H, plan.d, plan.T, idx) if q is not None else None
+    tk = _rows3(k, "k", plan.Hkv, plan.d, plan.T, idx)
+    tv = _rows3(v, "v", plan.Hkv, plan.d, plan.T, idx)
+    _call(_entry("bd_cache_append"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tq, tk, tv, rope._addr, cache._addr, to)
+
+
 def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
     """The cached rows of every sequence, packed in batch order (see include/bd_paged.h)."""
     idx = _device(plan, cache)
@@ -280,9 +366,7 @@ def bd_cache_read(plan: PagedPlan, cache: PagedCache, k, v, stream=None):
     _call(_entry("bd_cache_read"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, cache._addr, tk, tv)
 
 
-def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspace=None, stream=None):
-    """O and LSE of the new rows over the cache (see include/bd_paged.h). Without a
-    workspace one is allocated for the call."""
+def _attend(name, plan, q, cache, out, lse, workspace, stream, *more):
     idx = _device(plan, cache)
     tq = _rows3(q, "q", plan.H, plan.d, plan.T, idx)
     to = _rows3(out, "out", plan.H, plan.d, plan.T, idx)
@@ -304,17 +388,111 @@ def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspac
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
         wp, wn = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call(_entry("bd_paged_attn"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tq, cache._addr, to, tl, wp, wn)
+    _call(_entry(name), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tq, cache._addr, *more, to, tl, wp, wn)
+
+
+def bd_paged_attn(plan: PagedPlan, q, cache: PagedCache, out, lse=None, workspace=None, stream=None):
+    """O and LSE of the new rows over the cache (see include/bd_paged.h). Without a
+    workspace one is allocated for the call."""
+    _attend("bd_paged_attn", plan, q, cache, out, lse, workspace, stream)
+
+
+def _outputs(plan, q, stream):
+    with torch.cuda.stream(stream):      # memory of the stream that writes it
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(plan.H, q.shape[0], dtype=torch.float32, device=q.device)
+        blocks = torch.empty(q.shape[0], plan.Hkv, plan.blocks, dtype=torch.int32, device=q.device) if plan.blocks else None
+    if stream is not None:
+        for t in (out, lse) if blocks is None else (out, lse, blocks):  # and of the caller's, which reads it
+            t.record_stream(torch.cuda.current_stream(q.device))
+    return out, lse, blocks
 
 
 def paged_attn(plan: PagedPlan, q, cache: PagedCache, stream=None):
     """Allocate O and LSE and run bd_paged_attn; returns (out, lse). Rows past the new ones
     are not written."""
-    with torch.cuda.stream(stream):      # memory of the stream that writes it
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(plan.H, q.shape[0], dtype=torch.float32, device=q.device)
-    if stream is not None:
-        for t in (out, lse):             # and of the caller's, which reads it
-            t.record_stream(torch.cuda.current_stream(q.device))
+    out, lse, _ = _outputs(plan, q, stream)
     bd_paged_attn(plan, q, cache, out, lse, stream=stream)
     return out, lse
+
+
+# ---------------------------------------------------------------- selected blocks
+
+class BlockBounds:
+    """The bounds of a pool's blocks as the library takes them: ``code`` int8 [pages, Hkv, 2, d],
+    ``exp`` uint8 [pages, Hkv]. The tensors stay the caller's and are kept alive here."""
+
+    def __init__(self, code, exp):
+        if code.dim() != 4 or code.shape[2] != 2 or code.dtype != torch.int8 or code.stride(3) != 1:
+            raise ValueError(f"bounds: expected int8 [pages, Hkv, 2, d] with d contiguous, got {code.dtype} {tuple(code.shape)}")
+        if exp.dtype != torch.uint8 or exp.shape != code.shape[:2] or exp.device != code.device:
+            raise ValueError("bounds: expected uint8 exponents [pages, Hkv] on the codes' device")
+        self.code, self.exp = code, exp
+        self.num_pages, self.Hkv, _, self.d = code.shape
+        s, e = code.stride(), exp.stride()
+        self._c = bd_bounds(code.data_ptr(), s[0], s[1], s[2], exp.data_ptr(), e[0], e[1], self.num_pages, 0)
+        self._addr = C.addressof(self._c)
+        self._index = code.get_device()
+
+    @classmethod
+    def empty(cls, cache: PagedCache):
+        """Bounds for a cache's pool; a block's are there once bd_block_bounds has seen its rows."""
+        return cls(torch.zeros(cache.num_pages, cache.Hkv, 2, cache.d, dtype=torch.int8, device=cache.device),
+                   torch.zeros(cache.num_pages, cache.Hkv, dtype=torch.uint8, device=cache.device))
+
+
+def _check_bounds(plan, bounds, idx):
+    if bounds._index != idx:
+        raise ValueError(f"bounds: on {bounds.code.device}, the plan was uploaded to cuda:{idx}")
+    if bounds.Hkv != plan.Hkv or bounds.d != plan.d:
+        raise ValueError(f"bounds of {bounds.Hkv} heads of {bounds.d}, the plan was built for {plan.Hkv} of {plan.d}")
+
+
+_blocks = struct.Struct("PqqiI").pack          # bd_blocks
+
+
+def _lists(t, plan, idx):
+    """The rows' lists as the ABI's struct (its bytes)."""
+    if t.dtype is not torch.int32 or t.get_device() != idx:
+        _refuse(t, "blocks", torch.int32, idx)
+    s = t.shape
+    if not plan.blocks:
+        raise ValueError("not a sparse plan: build it with blocks=...")
+    if len(s) != 3 or s[0] < plan.T or s[1] != plan.Hkv or s[2] != plan.blocks or (s[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"blocks: expected [{plan.T} or more, {plan.Hkv}, {plan.blocks}] with lists contiguous, got {tuple(s)}")
+    return _blocks(t.data_ptr(), t.stride(0), t.stride(1), s[0], 0)
+
+
+def bd_block_bounds(plan: PagedPlan, cache: PagedCache, bounds: BlockBounds, stream=None):
+    """Bounds of the blocks that hold new rows, from the cache (see include/bd_paged.h)."""
+    idx = _device(plan, cache)
+    _check_bounds(plan, bounds, idx)
+    _call(_entry("bd_block_bounds"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, cache._addr, bounds._addr)
+
+
+def bd_block_select(plan: PagedPlan, q, bounds: BlockBounds, blocks, stream=None):
+    """The blocks that each new row attends, int32 [rows, Hkv, plan.blocks] (see include/bd_paged.h)."""
+    if plan._dev_ptr is None:
+        raise RuntimeError("plan not uploaded: call .upload(device)")
+    idx = plan._index
+    _check_bounds(plan, bounds, idx)
+    tq = _rows3(q, "q", plan.H, plan.d, plan.T, idx)
+    _call(_entry("bd_block_select"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tq, bounds._addr, _lists(blocks, plan, idx))
+
+
+def bd_sparse_attn(plan: PagedPlan, q, cache: PagedCache, blocks, out, lse=None, workspace=None, stream=None):
+    """O and LSE of the new rows over their listed blocks (see include/bd_paged.h). Without a
+    workspace one is allocated for the call."""
+    _attend("bd_sparse_attn", plan, q, cache, out, lse, workspace, stream, _lists(blocks, plan, _device(plan, cache)))
+
+
+def sparse_attn(plan: PagedPlan, q, cache: PagedCache, bounds: BlockBounds, stream=None):
+    """Select the new rows' blocks and attend over them; returns (out, lse, blocks). The bounds of
+    the blocks that new rows entered are brought up to date first."""
+    out, lse, blocks = _outputs(plan, q, stream)
+    if blocks is None:
+        raise ValueError("not a sparse plan: build it with blocks=...")
+    bd_block_bounds(plan, cache, bounds, stream=stream)
+    bd_block_select(plan, q, bounds, blocks, stream=stream)
+    bd_sparse_attn(plan, q, cache, blocks, out, lse, stream=stream)
+    return out, lse, blocks

@@ -53,7 +53,16 @@ typedef enum {
    * probability, e: its V row's exponent) to no more than 2^-32 of the row's largest, so that
    * zeros of a high byte, say, would hide the keys that matter (bd_cache_write's zeros, of
    * byte 67, hide nothing above 2^-83 of a key's p * v). */
-  BD_CACHE_E4M3 = 1
+  BD_CACHE_E4M3 = 1,
+  /* e2m1 codes, two a byte (the even element's in the low half; magnitudes 0, 0.5, 1, 1.5, 2, 3,
+   * 4, 6 and a sign), and a scale byte for every 16 elements of a (row, head): value = code * s,
+   * s = (1 + m / 8) * 2^(e - 15) for byte 8 e + m (m / 8 * 2^-14 for e = 0). bd_cache_write
+   * takes, for every 16 values, the smallest byte of [8, 226] with max|x| <= 6 s (226, that is
+   * 10240, if there is none) and stores x / s rounded to the nearest code (ties to the even one),
+   * saturating at +-6. 16 values with an infinity or a NaN among them are stored as byte 255 and
+   * read back as NaN. Values read back are exact in bf16 (and in fp16). Caches filled by other
+   * means may use bytes 0..226 and 255. */
+  BD_CACHE_E2M1 = 4
 } bd_cache_fmt;
 
 /* A paged K/V cache of one layer. k and v: stride_b is the stride from page to
@@ -61,8 +70,10 @@ typedef enum {
  * K/V heads (elements, any order of the dimensions; bytes must be multiples of 16,
  * as must the base pointers), rows = page_size, stride_c is unused, and the d
  * elements of a head are contiguous. k_exp, v_exp: exponent bytes of a
- * BD_CACHE_E4M3 cache with their common strides (ignored otherwise); bd_paged_attn
- * reads them by the aligned 4-byte words they lie in. */
+ * BD_CACHE_E4M3 cache with their common strides (ignored for bf16); bd_paged_attn
+ * reads them by the aligned 4-byte words they lie in. Of a BD_CACHE_E2M1 cache k and v are bytes
+ * (strides in bytes, d / 2 of them a head) and k_exp, v_exp the scale bytes, d / 16 contiguous
+ * ones of a (row, head): pointers and strides are multiples of 8 bytes (4 at d = 64). */
 typedef struct {
   bd_tensor k, v;
   uint8_t* k_exp;
@@ -122,6 +133,33 @@ BD_API int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key);
 BD_API int32_t bd_cache_write(const void* plan_host, const void* plan_dev, const bd_tensor* k, const bd_tensor* v,
                               const bd_paged_cache* cache, void* stream);
 
+/* Frequencies of a position rotation as the kernels take them: out[i] = turns a position
+ * advances pair i by, modulo 1, in units of 2^-64 (host, n values; inv_freq in radians a
+ * position, any finite number). Angles of far positions lose nothing: a position's is its product
+ * with out[i], modulo 2^64. BD_ERR_ARG for an infinity or a NaN. Pure host function. */
+BD_API int32_t bd_rope_phases(const double* inv_freq, int32_t n, uint64_t* out);
+
+/* A rotation of pairs of elements of a head by angles p * inv_freq[i] at position p. */
+typedef struct {
+  const uint64_t* phase; /* device uint64[dim / 2], from bd_rope_phases, 8-byte aligned         */
+  int32_t dim;           /* elements that take part, the first ones of a head: a multiple of 16,
+                            0 < dim <= d                                                        */
+  int32_t interleaved;   /* 1: pairs (2 i, 2 i + 1), 0: pairs (i, i + dim / 2)                  */
+  float scale;           /* factor of the turned elements (1: none)                             */
+  int32_t reserved;
+} bd_rope;
+
+/* bd_cache_append -- bd_cache_write with a rotation on the way: the new rows' K are turned by
+ * their cache positions, (x, y) -> scale (x cos a - y sin a, y cos a + x sin a), rounded to bf16
+ * and stored as bd_cache_write stores them; V is stored as it is. q (may be NULL, with q_out) is
+ * turned the same way into q_out, both bf16 [rows, H, d] as in bd_paged_attn; q_out may be q itself and
+ * overlaps nothing else. q rows without a position are copied. The turned values are off by at
+ * most 2^-21 of the pair's length times scale before they are rounded. Errors as bd_cache_write;
+ * BD_ERR_ARG for a rope's fields. */
+BD_API int32_t bd_cache_append(const void* plan_host, const void* plan_dev, const bd_tensor* q, const bd_tensor* k,
+                               const bd_tensor* v, const bd_rope* rope, const bd_paged_cache* cache, bd_tensor* q_out,
+                               void* stream);
+
 /* bd_cache_read -- rows [0, kv_len) of every sequence of the plan as bf16, packed back
  * to back in batch order into rows [0, sum of kv_len) of k and v; rows past that are
  * left alone. */
@@ -146,6 +184,76 @@ BD_API int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes);
 BD_API int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q,
                              const bd_paged_cache* cache, bd_tensor* out, bd_rowstat* lse, void* workspace,
                              size_t workspace_bytes, void* stream);
+
+/* ---- attention over selected blocks
+ *
+ * A block is a page of a sequence: block j holds its rows [j * page_size, (j + 1) * page_size).
+ * Every new row attends, for every K/V head, a list of at most `blocks` of the blocks up to its
+ * own; the heads of a group share the list. A block is chosen by the least and the greatest value
+ * of each element of its keys, held in 8 bits beside the cache (2 d + 1 bytes a block and K/V head):
+ *   bd_block_bounds   brings the bounds of the blocks up to date that new rows entered,
+ *   bd_block_select   scores the blocks of every new row and lists the best,
+ *   bd_sparse_attn    attends over the listed blocks.
+ * A sparse plan serves these, bd_cache_write and bd_cache_append of a step (bd_block_bounds takes
+ * the other causal plans too); its bd_paged_plan_key covers the sparse description. */
+typedef struct {
+  int32_t blocks; /* blocks of a list, 1..4096, at least first + recent                      */
+  int32_t first;  /* the first blocks of a sequence are always listed, >= 0                  */
+  int32_t recent; /* as are the last ones up to the row's own, which counts as one, >= 1     */
+  int32_t reserved;
+} bd_sparse_desc;
+
+/* Like bd_paged_plan_bytes / bd_paged_plan_build, for a step whose rows attend over selected
+ * blocks. desc->causal must be 1. BD_ERR_UNSUPPORTED: a sequence of more than 16384 blocks. */
+BD_API int32_t bd_sparse_plan_bytes(const bd_paged_desc* desc, const bd_sparse_desc* sparse, size_t* bytes);
+BD_API int32_t bd_sparse_plan_build(const bd_paged_desc* desc, const bd_sparse_desc* sparse, void* blob, size_t blob_bytes);
+
+/* The bounds of a pool's blocks: code[page][head][0][c] the lower, [1][c] the upper bound of
+ * element c, value = code * 2^(exp[page][head] - 127). bd_block_bounds takes the smallest e in
+ * [-50, 50] with max|k| <= 127 * 2^e (50 if there is none) and stores floor(min k * 2^-e) and
+ * ceil(max k * 2^-e), saturating at +-127, and byte e + 127; a block with an infinity or a NaN among
+ * its keys gets byte 255, which outscores every other. Base pointers and strides of code are
+ * multiples of 16 bytes; strides of exp positive. */
+typedef struct {
+  int8_t* code;
+  int64_t stride_page, stride_head, stride_bound; /* of code, in bytes; d contiguous         */
+  uint8_t* exp;
+  int64_t exp_stride_page, exp_stride_head;
+  int32_t num_pages, reserved;
+} bd_bounds;
+
+/* bd_block_bounds -- bounds of the blocks that hold new rows, from their cached rows below kv_len
+ * (all blocks of a sequence whose rows are all new). BD_ERR_PLAN if two sequences have new rows
+ * in the same page, or the plan is not causal. */
+BD_API int32_t bd_block_bounds(const void* plan_host, const void* plan_dev, const bd_paged_cache* cache,
+                               const bd_bounds* bounds, void* stream);
+
+/* The lists of the new rows: row t's blocks for K/V head g are entries [0, blocks) at
+ * ptr + t * stride_row + g * stride_head, ascending, -1 past the last one. */
+typedef struct {
+  int32_t* ptr;
+  int64_t stride_row, stride_head; /* elements */
+  int32_t rows, reserved;
+} bd_blocks;
+
+/* bd_block_select -- the lists of the new rows (q [rows, H, d] as bd_paged_attn takes it). q is held
+ * in 8 bits for this, codes rn(q * 2^-e) with the smallest e in [-50, 50] that has max|q| <= 127 * 2^e
+ * (50 if there is none) for every row and head (codes saturate; a head with an infinity or a NaN
+ * counts as zeros). A block's score for a head is sum_c max(q_c lo_c, q_c hi_c), for the group the largest of its
+ * heads'. Listed are the first and the recent blocks and those of the largest scores, of equal ones the
+ * lowest; all blocks up to the row's own if they are no more than `blocks`. Scores are exact: equal
+ * inputs give equal lists. Rows without a position get -1 throughout. */
+BD_API int32_t bd_block_select(const void* plan_host, const void* plan_dev, const bd_tensor* q, const bd_bounds* bounds,
+                               bd_blocks* blocks, void* stream);
+
+/* bd_sparse_attn -- O and LSE of the new rows over the listed blocks of their sequences, as
+ * bd_paged_attn computes them: new row at position p takes the listed blocks' rows, n = min(blocks, number of
+ * blocks up to its own) of them, the last listed one up to row p % page_size. Lists are those of bd_block_select, or
+ * others of that form (n blocks, the row's own last; an entry outside the row's blocks stands for the nearest one).
+ * Workspace as for bd_paged_attn (bd_paged_attn_workspace). */
+BD_API int32_t bd_sparse_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q, const bd_paged_cache* cache,
+                              const bd_blocks* blocks, bd_tensor* out, bd_rowstat* lse, void* workspace,
+                              size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }
