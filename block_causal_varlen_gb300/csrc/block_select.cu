@@ -10,10 +10,12 @@
 // bd_block_bounds_kernel: a CTA for each (block with new rows, K/V head); a stream over the
 // block's keys.
 //
-// bd_block_select_kernel: a CTA for each (new row, K/V head). Scores: d / 16 lanes take a block,
-// four blocks at a time, by dp4a (positive q against hi, negative against lo); they stay in shared
-// memory as whole numbers of the same order. Choice: the threshold two bits a round from the highest bit
-// in which scores differ, then the blocks above it and the first ones equal to it, in order.
+// bd_block_select_kernel: a CTA for some new rows of a sequence and a K/V head. Scores by
+// 8-bit matrix instructions (m16n8k32): 16 blocks against 8 (row, head) columns, positive q
+// against hi, negative against lo; they stay in shared memory as whole numbers of the same order. Choice:
+// the threshold eight bits a pass from the highest bit in which scores differ, by counts of
+// the digits, then the blocks above it and the first ones equal to it, in order. What bounds it is the chain of lookups for few rows
+// (a row then has 16 warps), the choice for many (a row has a warp, eight share the bounds they read).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -154,52 +156,97 @@ struct SelectArgs {
   int64_t x_sp, x_sh;
   int32_t* out;
   int64_t o_sr, o_sh;
-  int32_t G, Hkv, blocks, first, recent, page_shift, cap;
+  int32_t G, Hkv, blocks, first, recent, page_shift, cap, rows;
 };
 
-constexpr int kSelThreads = 256, kSelWarps = kSelThreads / 32;
-// shared memory: positive and negative parts of q's codes [G][2][d], their powers of two [G], keys [cap]
-constexpr size_t select_smem(int G, int d, int cap) { return size_t(G) * (2 * d + 4) + size_t(cap) * 4; }
-
-// A score as a whole number of the same order. Above all of them: an infinity of a block with NaN
-// or infinities, and the blocks that are always listed.
+// A score as a whole number of the same order (0: below all of them), an infinity of a block with
+// NaN or infinities above all of them.
 __device__ __forceinline__ uint32_t order_of(float s) {
   const uint32_t u = __float_as_uint(s);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-constexpr uint32_t kOddBlock = 0xff800000u, kAlways = 0xffffffffu;
+constexpr uint32_t kOddBlock = 0xff800000u;
 
-template <int D>
-__global__ void __launch_bounds__(kSelThreads) bd_block_select_kernel(const SelectArgs a) {
-  constexpr int LPB = D / 16, GPW = 32 / LPB;  // lanes of a block; blocks of a warp at a time, times U
-  constexpr int U = 4;
-  static_assert(LPB >= U, "four sums meet in four lanes at least");
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The digit of a threshold from counts of 256 digits (bins past those in use are zero): the highest
+// with `want` keys in it and above. A warp, 8 digits a lane. Takes the keys above off want; `exact`: the
+// digit's own keys are just as many as are wanted.
+__device__ __forceinline__ uint32_t find_digit(const uint32_t* hist, int lane, int* want, bool* exact) {
+  const uint4 lo = reinterpret_cast<const uint4*>(hist)[2 * lane], hi = reinterpret_cast<const uint4*>(hist)[2 * lane + 1];
+  const uint32_t c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += c[i];
+  uint32_t above = sum;  // of this lane and those behind it
+#pragma unroll
+  for (int y = 1; y < 32; y <<= 1) {
+    const uint32_t v = __shfl_down_sync(kFull, above, y);
+    if (lane + y < 32) above += v;
+  }
+  above -= sum;
+  const bool mine = int(above) < *want && int(above + sum) >= *want;
+  uint32_t digit = 0, over = above, own = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    if (own == 0 && int(over + c[i]) >= *want) { digit = 8 * lane + i; own = c[i]; }
+    if (own == 0) over += c[i];
+  }
+  const int from = __ffs(__ballot_sync(kFull, mine)) - 1;
+  *want -= int(__shfl_sync(kFull, over, from));
+  *exact = int(__shfl_sync(kFull, own, from)) == *want;
+  return __shfl_sync(kFull, digit, from);
+}
+
+template <int D, int THREADS>
+__global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_block_select_kernel(const SelectArgs a) {
+  constexpr int NW = THREADS / 32;
+  constexpr int S = D / 32;                // contraction steps; a lane has D / 4 neighbouring codes of a block
+  constexpr int QP = select_pitch(D);
   extern __shared__ uint4 sel_smem[];
-  uint8_t* s_q = reinterpret_cast<uint8_t*>(sel_smem);
-  int* s_eq = reinterpret_cast<int*>(s_q + a.G * 2 * D);
-  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_eq + a.G);
-  __shared__ uint32_t s_red[kSelWarps][4];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int cols = a.rows * a.G, colt = (cols + 7) / 8;
+  uint8_t* s_q = reinterpret_cast<uint8_t*>(sel_smem);          // [8 colt]: positive, then negative codes
+  int* s_eq = reinterpret_cast<int*>(s_q + colt * 8 * QP);      // [8 colt]
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_eq + colt * 8);  // [rows][cap]
+  __shared__ uint32_t s_red[NW][2];
+  __shared__ __align__(16) uint32_t s_hist[8][256];  // a row by the CTA: one for each pass, rows by warps: for each warp
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = lane & 3, rw = lane >> 2;
   const int32_t* plan = a.plan;
   grid_wait();
-  const int T = plan[PH_T];
-  const int32_t *where = plan + plan[PH_OFF_POS], *rowpg = plan + plan[PH_OFF_ROWPG];
-  for (int64_t x = blockIdx.x; x < int64_t(T) * a.Hkv; x += gridDim.x) {
-    const int t = int(x / a.Hkv), g = int(x % a.Hkv);
-    const int pos = where[t], nblk = pos < 0 ? 0 : (pos >> a.page_shift) + 1;
-    int32_t* out = a.out + int64_t(t) * a.o_sr + int64_t(g) * a.o_sh;
-    if (nblk <= a.blocks) {  // all there are
-      for (int i = tid; i < a.blocks; i += kSelThreads) out[i] = i < nblk ? i : -1;
+  const int groups = plan[PH_NSELG];
+  const int32_t *where = plan + plan[PH_OFF_POS], *rowpg = plan + plan[PH_OFF_ROWPG], *list = plan + plan[PH_OFF_SELG];
+  const uint32_t units = uint32_t(groups) * uint32_t(a.Hkv);  // (no more than new rows times heads)
+  for (uint32_t x = blockIdx.x; x < units; x += gridDim.x) {
+    const int gi = int(x / uint32_t(a.Hkv)), g = int(x) - gi * a.Hkv;
+    const int t0 = a.rows == 1 ? gi : list[2 * gi], n = a.rows == 1 ? 1 : list[2 * gi + 1];
+    auto blocks_of = [&](int r) { const int pos = where[t0 + r]; return pos < 0 ? 0 : (pos >> a.page_shift) + 1; };
+    auto out_of = [&](int r) { return a.out + int64_t(t0 + r) * a.o_sr + int64_t(g) * a.o_sh; };
+    const int most = blocks_of(n - 1);
+    if (most <= a.blocks) {  // all there are, for every row
+      for (int r = 0; r < n; ++r) {
+        const int nblk = blocks_of(r);
+        for (int i = tid; i < a.blocks; i += THREADS) out_of(r)[i] = i < nblk ? i : -1;
+      }
       continue;
     }
-    const int32_t* pages = plan + rowpg[t];
-    // ---- q's codes: a warp for each head
-    for (int h = warp; h < a.G; h += kSelWarps) {
-      const uint8_t* p = a.q + int64_t(t) * a.q_sr + int64_t(g * a.G + h) * a.q_sh;
-      const bool in = lane < D / 8;
-      const uint4 v = in ? *(reinterpret_cast<const uint4*>(p) + lane) : make_uint4(0, 0, 0, 0);
-      uint32_t mx = absmax8(v);
-      mx = __reduce_max_sync(kFull, mx);
+    const int32_t* pages = plan + rowpg[t0];
+    // the first tile's blocks are looked up while q is turned into codes
+    int pg[2];
+    auto look_up = [&](int tile) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) pg[h] = pages[min(tile * 16 + rw + 8 * h, most - 1)];
+    };
+    look_up(warp);
+    // ---- q's codes: a warp for each (row, head)
+    for (int c = warp; c < colt * 8; c += NW) {
+      const bool there = c < n * a.G, in = lane < D / 8;
+      const uint8_t* p = a.q + int64_t(t0 + c / a.G) * a.q_sr + int64_t(g * a.G + c % a.G) * a.q_sh;
+      const uint4 v = in && there ? *(reinterpret_cast<const uint4*>(p) + lane) : make_uint4(0, 0, 0, 0);
+      const uint32_t mx = __reduce_max_sync(kFull, absmax8(v));
       const bool bad = mx >= 0x7f80u;
       const int e = bad ? 0 : pow8(__uint_as_float(mx << 16));
       const float f = bad ? 0.f : pow2f(-e);
@@ -208,128 +255,181 @@ __global__ void __launch_bounds__(kSelThreads) bd_block_select_kernel(const Sele
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float y = i & 1 ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-        const int c = bad ? 0 : int(fminf(fmaxf(rintf(y * f), -127.f), 127.f));
-        up[i >> 2] |= uint32_t(max(c, 0) & 255) << (8 * (i & 3));
-        down[i >> 2] |= uint32_t(min(c, 0) & 255) << (8 * (i & 3));
+        const int z = bad ? 0 : int(fminf(fmaxf(rintf(y * f), -127.f), 127.f));
+        up[i >> 2] |= uint32_t(max(z, 0) & 255) << (8 * (i & 3));
+        down[i >> 2] |= uint32_t(min(z, 0) & 255) << (8 * (i & 3));
       }
       if (in) {
-        *reinterpret_cast<uint2*>(s_q + (h * 2) * D + lane * 8) = make_uint2(up[0], up[1]);
-        *reinterpret_cast<uint2*>(s_q + (h * 2 + 1) * D + lane * 8) = make_uint2(down[0], down[1]);
+        *reinterpret_cast<uint2*>(s_q + c * QP + lane * 8) = make_uint2(up[0], up[1]);
+        *reinterpret_cast<uint2*>(s_q + c * QP + D + lane * 8) = make_uint2(down[0], down[1]);
       }
-      if (lane == 0) s_eq[h] = e;
+      if (lane == 0) s_eq[c] = e;
     }
+    for (int r = 0; r < n; ++r)
+      for (int i = tid; i < most; i += THREADS) s_key[r * a.cap + i] = 0u;
+    if (a.rows == 1)
+      for (int i = tid; i < 1024; i += THREADS) s_hist[0][i] = 0u;
     __syncthreads();
-    // ---- scores
-    const int sub = lane % LPB;
-    for (int b0 = (warp * GPW + lane / LPB) * U; b0 - (lane / LPB) * U < nblk; b0 += kSelWarps * GPW * U) {
-      uint4 lo[U], hi[U];
-      int page[U];
+    // ---- scores: 16 blocks of a warp at a time against 8 (row, head) columns
+    for (int tile = warp; tile * 16 < most; tile += NW) {
+      uint32_t hi[2][2 * S], lo[2][2 * S], eb[2];
 #pragma unroll
-      for (int u = 0; u < U; ++u) page[u] = pages[min(b0 + u, nblk - 1)];
+      for (int h = 0; h < 2; ++h) {
+        const int8_t* p = a.code + int64_t(pg[h]) * a.c_sp + int64_t(g) * a.c_sh + j * (D / 4);
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int8_t* p = a.code + int64_t(page[u]) * a.c_sp + int64_t(g) * a.c_sh + sub * 16;
-        lo[u] = *reinterpret_cast<const uint4*>(p);
-        hi[u] = *reinterpret_cast<const uint4*>(p + a.c_sb);
-      }
-      // after the sums have met a lane has block b0 + mine
-      const int mine = (sub & 1) * 2 + ((sub >> 1) & 1);
-      int mypage = page[0];
-#pragma unroll
-      for (int u = 1; u < U; ++u) mypage = mine == u ? page[u] : mypage;
-      const uint32_t eb = a.exp[int64_t(mypage) * a.x_sp + int64_t(g) * a.x_sh];
-      float best = -CUDART_INF_F;
-      for (int h = 0; h < a.G; ++h) {
-        const uint4 p = *reinterpret_cast<const uint4*>(s_q + (h * 2) * D + sub * 16);
-        const uint4 m = *reinterpret_cast<const uint4*>(s_q + (h * 2 + 1) * D + sub * 16);
-        int s[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          int v = __dp4a(int(p.x), int(hi[u].x), 0);
-          v = __dp4a(int(p.y), int(hi[u].y), v);
-          v = __dp4a(int(p.z), int(hi[u].z), v);
-          v = __dp4a(int(p.w), int(hi[u].w), v);
-          v = __dp4a(int(m.x), int(lo[u].x), v);
-          v = __dp4a(int(m.y), int(lo[u].y), v);
-          v = __dp4a(int(m.z), int(lo[u].z), v);
-          s[u] = __dp4a(int(m.w), int(lo[u].w), v);
+        for (int i = 0; i < D / 64; ++i) {
+          const uint4 u = *(reinterpret_cast<const uint4*>(p + a.c_sb) + i), v = *(reinterpret_cast<const uint4*>(p) + i);
+          hi[h][4 * i] = u.x; hi[h][4 * i + 1] = u.y; hi[h][4 * i + 2] = u.z; hi[h][4 * i + 3] = u.w;
+          lo[h][4 * i] = v.x; lo[h][4 * i + 1] = v.y; lo[h][4 * i + 2] = v.z; lo[h][4 * i + 3] = v.w;
         }
-        // lanes of odd number go on with blocks 2 and 3, then those with bit 1 set with 1 and 3
-        const int t0 = __shfl_xor_sync(kFull, sub & 1 ? s[0] : s[2], 1), t1 = __shfl_xor_sync(kFull, sub & 1 ? s[1] : s[3], 1);
-        const int r0 = (sub & 1 ? s[2] : s[0]) + t0, r1 = (sub & 1 ? s[3] : s[1]) + t1;
-        int v = (sub & 2 ? r1 : r0) + __shfl_xor_sync(kFull, sub & 2 ? r0 : r1, 2);
-#pragma unroll
-        for (int y = 4; y < LPB; y <<= 1) v += __shfl_xor_sync(kFull, v, y);
-        best = fmaxf(best, float(v) * pow2f(s_eq[h] + int(eb) - 127));
+        eb[h] = a.exp[int64_t(pg[h]) * a.x_sp + int64_t(g) * a.x_sh];
       }
-      const int b = b0 + mine;
-      if (sub < U && b < nblk)
-        s_key[b] = b < a.first || b >= nblk - a.recent ? kAlways : eb == 255u ? kOddBlock : order_of(best);
+      if ((tile + NW) * 16 < most) look_up(tile + NW);
+      for (int ct = 0; ct < colt; ++ct) {
+        int c[4] = {0, 0, 0, 0};
+        const uint8_t* q = s_q + (ct * 8 + rw) * QP + j * (D / 4);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const uint4 u = *(reinterpret_cast<const uint4*>(q) + i), v = *(reinterpret_cast<const uint4*>(q + D) + i);
+          mma_s8(c, hi[0][4 * i], hi[1][4 * i], hi[0][4 * i + 1], hi[1][4 * i + 1], u.x, u.y);
+          mma_s8(c, hi[0][4 * i + 2], hi[1][4 * i + 2], hi[0][4 * i + 3], hi[1][4 * i + 3], u.z, u.w);
+          mma_s8(c, lo[0][4 * i], lo[1][4 * i], lo[0][4 * i + 1], lo[1][4 * i + 1], v.x, v.y);
+          mma_s8(c, lo[0][4 * i + 2], lo[1][4 * i + 2], lo[0][4 * i + 3], lo[1][4 * i + 3], v.z, v.w);
+        }
+        // this lane's columns 2 j, 2 j + 1 of blocks rw, rw + 8: the largest of a row's heads
+        const int c0 = ct * 8 + 2 * j, r0 = c0 / a.G, r1 = (c0 + 1) / a.G;
+        const bool in0 = r0 < n, in1 = r1 < n;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int b = tile * 16 + rw + 8 * h;
+          if (b >= most) continue;
+          const uint32_t k0 = eb[h] == 255u ? kOddBlock : order_of(float(c[2 * h]) * pow2f(s_eq[c0] + int(eb[h]) - 127));
+          const uint32_t k1 = eb[h] == 255u ? kOddBlock : order_of(float(c[2 * h + 1]) * pow2f(s_eq[c0 + 1] + int(eb[h]) - 127));
+          if (r0 == r1) {
+            if (in0) atomicMax(&s_key[r0 * a.cap + b], max(k0, k1));
+          } else {
+            if (in0) atomicMax(&s_key[r0 * a.cap + b], k0);
+            if (in1) atomicMax(&s_key[r1 * a.cap + b], k1);
+          }
+        }
+      }
     }
     __syncthreads();
-    // ---- the blocks-th largest key. Keys from tid * per on are this thread's.
-    const int per = (nblk + kSelThreads - 1) / kSelThreads;
-    const int i0 = min(tid * per, nblk), i1 = min(i0 + per, nblk);
-    uint32_t all1 = ~0u, any1 = 0;
-    for (int i = i0; i < i1; ++i) { all1 &= s_key[i]; any1 |= s_key[i]; }
-    all1 = __reduce_and_sync(kFull, all1);
-    any1 = __reduce_or_sync(kFull, any1);
-    if (lane == 0) { s_red[warp][0] = all1; s_red[warp][1] = any1; }
-    __syncthreads();
+    // ---- the choice, of the blocks that are not listed always: K of [first, most - recent)
+    const int K = a.blocks - a.first - a.recent;
+    if (a.rows == 1) {
+      // one row by the whole CTA. Keys from tid * per on are this thread's.
+      int32_t* out = out_of(0);
+      const int per = (most + THREADS - 1) / THREADS, i0 = min(tid * per, most), i1 = min(i0 + per, most);
+      const int b0 = max(i0, a.first), b1 = min(i1, most - a.recent);
+      uint32_t all1 = ~0u, any1 = 0;
+      for (int i = b0; i < b1; ++i) { all1 &= s_key[i]; any1 |= s_key[i]; }
+      all1 = __reduce_and_sync(kFull, all1);
+      any1 = __reduce_or_sync(kFull, any1);
+      if (lane == 0) { s_red[warp][0] = all1; s_red[warp][1] = any1; }
+      __syncthreads();
+      all1 = __reduce_and_sync(kFull, lane < NW ? s_red[lane][0] : ~0u);
+      any1 = __reduce_or_sync(kFull, lane < NW ? s_red[lane][1] : 0u);
+      // thr: the K-th largest key, 8 bits a pass from the first that differs; or, when all keys from
+      // thr on are wanted, the number before it
+      const uint32_t differ = all1 ^ any1;
+      int bit = differ ? 32 - __clz(differ) : 0, want = K;
+      uint32_t thr = K == 0 ? ~0u : bit == 0 ? all1 : bit == 32 ? 0u : all1 & ~((1u << bit) - 1u);
+      for (int pass = 0; K > 0 && bit > 0; ++pass) {
+        const int lo = max(bit - 8, 0);
+        const uint32_t mask = (1u << (bit - lo)) - 1u;
+        for (int i = b0; i < b1; ++i) {
+          const uint32_t k = s_key[i];
+          if (bit == 32 || ((k ^ thr) >> bit) == 0) atomicAdd(&s_hist[pass][(k >> lo) & mask], 1u);
+        }
+        __syncthreads();
+        bool exact;
+        thr |= find_digit(s_hist[pass], lane, &want, &exact) << lo;
+        bit = lo;
+        if (exact && thr > 0) {
+          --thr;
+          break;
+        }
+      }
+      // those above thr, and of those equal to it the first ones, in order
+      uint32_t cnt = 0;  // above in the lower 16 bits, equal in the upper ones
+      auto always = [&](int i) { return i < a.first || i >= most - a.recent; };
+      for (int i = i0; i < i1; ++i) cnt += always(i) || s_key[i] > thr ? 1u : s_key[i] == thr ? 0x10000u : 0u;
+      uint32_t sum = cnt;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) { all1 &= s_red[w][0]; any1 |= s_red[w][1]; }
-    const uint32_t differ = all1 ^ any1;
-    // thr: the largest number that `blocks` keys are not below, bit by bit from the first that differs
-    int bit = differ ? 31 - __clz(differ) : -1;
-    uint32_t thr = bit < 0 ? all1 : bit == 31 ? 0u : all1 & ~((2u << bit) - 1u);
-    while (bit >= 0) {
-      const int sh = max(bit - 1, 0), steps = bit > 0 ? 3 : 1;
-      const uint32_t c1 = thr + (1u << sh), c2 = steps == 3 ? thr + (2u << sh) : ~0u, c3 = steps == 3 ? thr + (3u << sh) : ~0u;
-      uint32_t n1 = 0, n23 = 0;  // two counts of 16 bits
+      for (int y = 1; y < 32; y <<= 1) {
+        const uint32_t v = __shfl_up_sync(kFull, sum, y);
+        if (lane >= y) sum += v;
+      }
+      __syncthreads();
+      if (lane == 31) s_red[warp][0] = sum;
+      __syncthreads();
+      const uint32_t others = lane < NW ? s_red[lane][0] : 0u;
+      const uint32_t before = sum - cnt + __reduce_add_sync(kFull, lane < warp ? others : 0u);
+      const int room = a.blocks - int(__reduce_add_sync(kFull, others) & 0xffffu);  // for keys equal to thr
+      int above = int(before & 0xffffu), equal = int(before >> 16);
       for (int i = i0; i < i1; ++i) {
         const uint32_t k = s_key[i];
-        n1 += k >= c1 ? 1u : 0u;
-        n23 += (k >= c2 ? 1u : 0u) + (k >= c3 ? 0x10000u : 0u);
+        if (always(i) || k > thr) out[above++ + min(equal, room)] = i;
+        else if (k == thr) {
+          if (equal < room) out[above + equal] = i;
+          ++equal;
+        }
       }
-      n1 = __reduce_add_sync(kFull, n1);
-      n23 = __reduce_add_sync(kFull, n23);
-      __syncthreads();
-      if (lane == 0) { s_red[warp][0] = n1; s_red[warp][1] = n23; }
-      __syncthreads();
-      n1 = n23 = 0;
+    } else {
+      // a row by a warp; a lane has keys lane, lane + 32, ...
+      for (int r = warp; r < n; r += NW) {
+        int32_t* out = out_of(r);
+        const uint32_t* key = s_key + r * a.cap;
+        const int nblk = blocks_of(r);
+        if (nblk <= a.blocks) {
+          for (int i = lane; i < a.blocks; i += 32) out[i] = i < nblk ? i : -1;
+          continue;
+        }
+        const int b0 = a.first + lane, b1 = nblk - a.recent;
+        uint32_t all1 = ~0u, any1 = 0;
+        for (int i = b0; i < b1; i += 32) { all1 &= key[i]; any1 |= key[i]; }
+        const uint32_t differ = __reduce_and_sync(kFull, all1) ^ __reduce_or_sync(kFull, any1);
+        all1 = __reduce_and_sync(kFull, all1);
+        int bit = differ ? 32 - __clz(differ) : 0, want = K;
+        uint32_t thr = K == 0 ? ~0u : bit == 0 ? all1 : bit == 32 ? 0u : all1 & ~((1u << bit) - 1u);
+        uint32_t* hist = s_hist[warp & 7];  // (8 warps where rows are theirs)
+        while (K > 0 && bit > 0) {
+          const int lo = max(bit - 8, 0);
+          const uint32_t mask = (1u << (bit - lo)) - 1u;
+          __syncwarp();
 #pragma unroll
-      for (int w = 0; w < kSelWarps; ++w) { n1 += s_red[w][0]; n23 += s_red[w][1]; }
-      const int K = a.blocks;
-      if (steps == 1) thr = int(n1) >= K ? c1 : thr;
-      else thr = int(n23 >> 16) >= K ? c3 : int(n23 & 0xffffu) >= K ? c2 : int(n1) >= K ? c1 : thr;
-      bit -= 2;
-    }
-    // ---- those above thr, and of those equal to it the first ones, in order
-    uint32_t cnt = 0;  // above in the lower 16 bits, equal in the upper ones
-    for (int i = i0; i < i1; ++i) cnt += s_key[i] > thr ? 1u : s_key[i] == thr ? 0x10000u : 0u;
-    uint32_t sum = cnt;
-#pragma unroll
-    for (int y = 1; y < 32; y <<= 1) {
-      const uint32_t v = __shfl_up_sync(kFull, sum, y);
-      if (lane >= y) sum += v;
-    }
-    __syncthreads();
-    if (lane == 31) s_red[warp][0] = sum;
-    __syncthreads();
-    uint32_t before = sum - cnt, total = 0;
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-      before += w < warp ? s_red[w][0] : 0u;
-      total += s_red[w][0];
-    }
-    const int room = a.blocks - int(total & 0xffffu);  // for keys equal to thr
-    int above = int(before & 0xffffu), equal = int(before >> 16);
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = s_key[i];
-      if (k > thr) out[above++ + min(equal, room)] = i;
-      else if (k == thr) {
-        if (equal < room) out[above + equal] = i;
-        ++equal;
+          for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(hist)[lane + 32 * i] = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+          for (int i = b0; i < b1; i += 32) {
+            const uint32_t k = key[i];
+            if (bit == 32 || ((k ^ thr) >> bit) == 0) atomicAdd(&hist[(k >> lo) & mask], 1u);
+          }
+          __syncwarp();
+          bool exact;
+          thr |= find_digit(hist, lane, &want, &exact) << lo;
+          bit = lo;
+          if (exact && thr > 0) {
+            --thr;
+            break;
+          }
+        }
+        auto always = [&](int i) { return i < a.first || i >= b1; };
+        uint32_t over = 0;
+        for (int i = lane; i < nblk; i += 32) over += always(i) || key[i] > thr ? 1u : 0u;
+        const int room = a.blocks - int(__reduce_add_sync(kFull, over));
+        int at = 0, equal = 0;
+        for (int base = 0; base < nblk; base += 32) {
+          const int i = base + lane;
+          const uint32_t k = i < nblk ? key[i] : 0u;
+          const bool sure = i < nblk && (always(i) || k > thr), same = i < nblk && !sure && k == thr;
+          const uint32_t e = __ballot_sync(kFull, same), before = (1u << lane) - 1u;
+          const bool take = sure || (same && equal + __popc(e & before) < room);
+          const uint32_t m = __ballot_sync(kFull, take);
+          if (take) out[at + __popc(m & before)] = i;
+          at += __popc(m);
+          equal += __popc(e);
+        }
       }
     }
     __syncthreads();
@@ -357,19 +457,25 @@ cudaError_t launch_bounds(int d, int grid, cudaStream_t s, const BoundsArgs& a) 
                     : launch_kernel(bd_block_bounds_kernel<256, FMT>, grid, kBoundThreads, 0, s, a);
 }
 
-template <int D>
-int32_t launch_select(int grid, size_t smem, cudaStream_t s, const SelectArgs& a) {
+template <int D, int THREADS>
+int32_t launch_select_t(int grid, size_t smem, cudaStream_t s, const SelectArgs& a) {
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(bd_block_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(select_smem(128, D, kMostBlocks)));
+    const cudaError_t e = cudaFuncSetAttribute(bd_block_select_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               int(kSelMostSmem));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(block select)");
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
-  const cudaError_t e = launch_kernel(bd_block_select_kernel<D>, grid, kSelThreads, smem, s, a);
+  const cudaError_t e = launch_kernel(bd_block_select_kernel<D, THREADS>, grid, THREADS, smem, s, a);
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_block_select_kernel launch");
+}
+
+// One row by 16 warps, several by 8.
+template <int D>
+int32_t launch_select(int grid, size_t smem, cudaStream_t s, const SelectArgs& a) {
+  return a.rows == 1 ? launch_select_t<D, 512>(grid, smem, s, a) : launch_select_t<D, 256>(grid, smem, s, a);
 }
 
 }  // namespace
@@ -441,10 +547,10 @@ extern "C" int32_t bd_block_select(const void* plan_host, const void* plan_dev, 
   a.o_sr = blocks->stride_row; a.o_sh = blocks->stride_head;
   a.G = w[PH_G]; a.Hkv = w[PH_HKV];
   a.blocks = w[PH_BLOCKS]; a.first = w[PH_FIRST]; a.recent = w[PH_RECENT];
-  a.page_shift = w[PH_PAGE_SHIFT]; a.cap = w[PH_SEL_CAP];
-  const int64_t ctas = int64_t(w[PH_T]) * w[PH_HKV];
+  a.page_shift = w[PH_PAGE_SHIFT]; a.cap = w[PH_SEL_CAP]; a.rows = w[PH_SEL_ROWS];
+  const int64_t ctas = int64_t(w[PH_NSELG]) * w[PH_HKV];
   const int grid = int(ctas < kPagedSms * 8 ? ctas : kPagedSms * 8);
-  const size_t smem = select_smem(a.G, w[PH_D], a.cap);
+  const size_t smem = select_smem(a.rows, a.G, w[PH_D], a.cap);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   st = w[PH_D] == 64 ? launch_select<64>(grid, smem, s, a) : w[PH_D] == 128 ? launch_select<128>(grid, smem, s, a)
                                                                             : launch_select<256>(grid, smem, s, a);

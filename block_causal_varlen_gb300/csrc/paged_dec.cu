@@ -75,7 +75,7 @@ struct DecCfg {
   static constexpr int kChunk = kRowBytes <= 128 && NB <= 2 ? 32 : 16;
   static constexpr int kMatBytes = kChunk * kRowBytes;        // K (or V) of a chunk
   static constexpr int kStageBytes = 2 * kMatBytes;
-  static constexpr int kWarps = 4, kLanes = kWarps / kSplit;  // kLanes: chunks in work at a time
+  static constexpr int kWarps = kF4 && NB == 1 ? 8 : 4, kLanes = kWarps / kSplit;  // kLanes: chunks in work at a time
   static constexpr int kThreads = 32 * kWarps;
   // a warp's share of a block is added up 8 rows x kCols columns at a time; head dim 256's
   // scores pass through the same place, two chunks in turn
@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   constexpr int DW = Cfg::kDim, PW = Cfg::kSplit, NL = Cfg::kLanes;
   constexpr int KT = kChunk / 16;            // 16-key tiles of a chunk
   constexpr int KS = DW / 16, MT = DW / 16;  // contraction steps of q . k, 16-column tiles of O
-  constexpr float kPShift = 7.f;             // F16: P is held times 2^7
+  constexpr float kPShift = 7.f;             // fp16: P is held times 2^7
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
   int cp = p0 - 1, ck = 0, ck1 = 0, chkv = 0, cpages = 0, cpage = 0;  // cpage: of key ck + lane (mod kChunk)
   const int32_t* list = nullptr;  // BLOCKS: the row's list, its entry for the chunk after next, its blocks' number
   int entry = 0, nblk = 0;
+  int ceo = 0;  // e2m1: offset of the head's scales
   auto next_chunk = [&]() {
     ck += kChunk * NL;
     bool other = false;  // another piece
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         nblk = W[PC_NBLK];
         other = true;
       }
+      if constexpr (F4) ceo = chkv * int(a.e_sh) + half * Cfg::kScale;
     }
     const int k = min(ck + lane % kChunk, ck1 - 1);
     if constexpr (BLOCKS) {
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     const int keys = ck1 - ck, row = min(ck + lane % kChunk, ck1 - 1) & ((1 << pshift) - 1);
     const bool two = kChunk == 32 && brows == 16 && keys > 16;  // copies of K and of V: one, or two
     if constexpr (F4) {
-      const int64_t o = int64_t(cpage) * a.e_sp + row * int(a.e_sr) + chkv * int(a.e_sh) + half * Cfg::kScale;
+      const int64_t o = int64_t(cpage) * a.e_sp + (row * int(a.e_sr) + ceo);
       static_assert(!F4 || kChunk == 32, "a lane for each key");
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -564,10 +566,16 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float mx = -CUDART_INF_F;
+          if constexpr (F4) {  // (the factor is positive)
 #pragma unroll
-          for (int y = 0; y < 2 * KT; ++y) {
-            const float v = s[y >> 1][b][2 * (y & 1) + e];
-            mx = fmaxf(mx, F8 ? fmaf(v, factor(b, e), ve[y]) : v * factor(b, e));
+            for (int y = 0; y < KT; ++y) mx = max3f(mx, s[y][b][e], s[y][b][2 + e]);
+            mx *= factor(b, e);
+          } else {
+#pragma unroll
+            for (int y = 0; y < 2 * KT; ++y) {
+              const float v = s[y >> 1][b][2 * (y & 1) + e];
+              mx = fmaxf(mx, F8 ? fmaf(v, factor(b, e), ve[y]) : v * factor(b, e));
+            }
           }
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
@@ -601,7 +609,22 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
       for (int b = 0; b < NB; ++b) {
         float me[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) me[e] = m[b][e] == -CUDART_INF_F ? 0.f : m[b][e];
+        for (int e = 0; e < 2; ++e) me[e] = (m[b][e] == -CUDART_INF_F ? 0.f : m[b][e]) - (F4 ? kPShift : 0.f);
+        if constexpr (F4) {  // l is held times 2^kPShift, too
+          const float2 f2 = make_float2(factor(b, 0), factor(b, 1)), r2 = make_float2(-me[0], -me[1]);
+          float2 sum = make_float2(l[b][0], l[b][1]);
+#pragma unroll
+          for (int y = 0; y < 2 * KT; ++y) {
+            float2 v = ffma2(make_float2(s[y >> 1][b][2 * (y & 1)], s[y >> 1][b][2 * (y & 1) + 1]), f2, r2);
+            v.x = ex2(v.x);
+            v.y = ex2(v.y);
+            sum = fadd2(sum, v);
+            pb[y >> 1][b][y & 1] = transpose8(pack_f16(v.x, v.y));
+          }
+          l[b][0] = sum.x;
+          l[b][1] = sum.y;
+          continue;
+        }
 #pragma unroll
         for (int y = 0; y < 2 * KT; ++y) {
           const float x0 = fmaf(s[y >> 1][b][2 * (y & 1)], factor(b, 0), -me[0]);
@@ -617,8 +640,6 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
               if (__shfl_sync(0xffffffffu, vb, key) == 255u)
                 w |= (k + key < lim[b][0] ? 0x7e00u : 0u) | (k + key < lim[b][1] ? 0x7e000000u : 0u);
             }
-          } else if constexpr (F4) {
-            w = pack_f16(p0f * 128.f, p1f * 128.f);  // 2^kPShift
           } else {
             w = pack_bf16(p0f, p1f);
           }
@@ -793,6 +814,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         for (int x = 4; x < 32; x <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], x);
         // NaN scores leave the maximum alone: what they gave was taken relative to 0
         if (m[b][e] == -CUDART_INF_F && l[b][e] != 0.f) m[b][e] = 0.f;
+        if constexpr (F4) m[b][e] -= kPShift;  // l and O are relative to this
         if (rw == 0)
           *reinterpret_cast<float2*>(&ml[(warp * 8 * NB + 8 * b + 2 * j + e) * 2]) = make_float2(m[b][e], l[b][e]);
       }
@@ -826,7 +848,7 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
         float M = -CUDART_INF_F;
 #pragma unroll
         for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[(w * 8 * NB + 8 * b + 2 * j + e) * 2]);
-        fac[e] = (m[b][e] == -CUDART_INF_F ? 0.f : ex2(m[b][e] - M)) * (F16 ? 0.0078125f : 1.f);  // 2^-kPShift
+        fac[e] = (m[b][e] == -CUDART_INF_F ? 0.f : ex2(m[b][e] - M)) * (F8 ? 0.0078125f : 1.f);  // 2^-kPShift
       }
 #pragma unroll
       for (int rd = 0; rd < DW / Cfg::kCols; ++rd) {

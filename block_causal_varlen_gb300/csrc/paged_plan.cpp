@@ -32,7 +32,8 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
   if (!in(w[PH_OFF_TOK], w[PH_T], 1) || !in(w[PH_OFF_PAGES], w[PH_NPAGES], 1) || !in(w[PH_OFF_PGROW], w[PH_NPAGES], 1) ||
       !in(w[PH_OFF_PGCNT], w[PH_NPAGES], 1) || !in(w[PH_OFF_DEC], w[PH_NDEC], kPieceWords) ||
       !in(w[PH_OFF_POS], w[PH_T], 1) || !in(w[PH_OFF_TOUCH], w[PH_NTOUCH], 1) ||
-      (w[PH_BLOCKS] && !in(w[PH_OFF_ROWPG], w[PH_T], 1)) ||
+      (w[PH_BLOCKS] && (!in(w[PH_OFF_ROWPG], w[PH_T], 1) || w[PH_SEL_ROWS] < 1 || w[PH_SEL_ROWS] > kSelRows ||
+                        (w[PH_SEL_ROWS] > 1 && !in(w[PH_OFF_SELG], w[PH_NSELG], 2)))) ||
       !in(w[PH_OFF_TILE], w[PH_NTILE], kPieceWords) || w[PH_NDECM] < 0 || w[PH_NDECM] > kDecSlots / 2 ||
       w[PH_NTILEM] < 0 || w[PH_NTILEM] > kTilePartSlots / 2)
     return fail(BD_ERR_PLAN, "paged plan blob offsets are inconsistent");
@@ -371,7 +372,8 @@ struct Built {
   std::vector<Item> dec_items, tile_items;
   Seqs S;                          // of the items
   std::vector<int32_t> page_off;   // of the sequences
-  int32_t dec_rows, dec_live = 0, sel_cap = 0;
+  int32_t dec_rows, dec_live = 0, sel_cap = 0, sel_rows = 1;
+  int64_t sel_groups = 0;
 };
 
 int32_t check_sparse(const bd_paged_desc* D, const bd_sparse_desc* X) {
@@ -447,6 +449,15 @@ int32_t prepare(const bd_paged_desc* D, const bd_sparse_desc* X, Built* B) {
       }
     B->sel_cap = 512;
     while (B->sel_cap < widest_row) B->sel_cap *= 2;
+    auto groups = [&](int rows) {
+      int64_t n = 0;
+      for (int32_t b = 0; b < D->B; ++b) n += (int64_t(D->q_len[b]) + rows - 1) / rows;
+      return n;
+    };
+    B->sel_rows = kSelRows;
+    while (B->sel_rows > 1 && (groups(B->sel_rows) * D->Hkv < kSelCtas || select_smem(B->sel_rows, G, D->d, B->sel_cap) > kSelSmem))
+      B->sel_rows /= 2;
+    B->sel_groups = groups(B->sel_rows);
     return BD_OK;
   }
   for (int32_t b = 0; b < D->B; ++b) {
@@ -474,7 +485,7 @@ int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 
 // Words of the header, the fixed places and the lists of rows and pages.
 int64_t list_words(const Built& X, bool sparse) {
-  return up4(kOffLists + (sparse ? 3 : 2) * X.T + 3 * X.npages + X.ntouch);
+  return up4(kOffLists + (sparse ? 3 : 2) * X.T + 3 * X.npages + X.ntouch + (X.sel_rows > 1 ? 2 * X.sel_groups : 0));
 }
 
 // Words that hold the plan however its blocks are cut: a cut block's parts but one come
@@ -551,7 +562,15 @@ static int32_t plan_build(const bd_paged_desc* desc, const bd_sparse_desc* spars
   if (sparse) {
     w[PH_BLOCKS] = sparse->blocks; w[PH_FIRST] = sparse->first; w[PH_RECENT] = sparse->recent;
     w[PH_OFF_ROWPG] = int32_t(w[PH_OFF_TOUCH] + X.ntouch);
-    w[PH_SEL_CAP] = X.sel_cap;
+    w[PH_SEL_CAP] = X.sel_cap; w[PH_SEL_ROWS] = X.sel_rows;
+    w[PH_OFF_SELG] = int32_t(w[PH_OFF_ROWPG] + X.T);
+    w[PH_NSELG] = int32_t(X.sel_groups);
+    int32_t* group = w + w[PH_OFF_SELG];
+    for (int32_t b = 0, t = 0; X.sel_rows > 1 && b < D.B; t += D.q_len[b++])
+      for (int32_t i = 0; i < D.q_len[b]; i += X.sel_rows) {
+        *group++ = t + i;
+        *group++ = std::min(X.sel_rows, D.q_len[b] - i);
+      }
     std::copy(X.S.page_off.begin(), X.S.page_off.end(), w + w[PH_OFF_ROWPG]);
   }
   int64_t tok = 0, pg = 0, kv = 0, touch = 0;
@@ -636,7 +655,8 @@ extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
   const int32_t fields[] = {w[PH_H], w[PH_HKV], w[PH_D], w[PH_PAGE], w[PH_NUM_PAGES], w[PH_FMT], w[PH_CAUSAL],
                             w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0,
                             w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0, w[PH_NTILE] > 0, w[PH_NTILEM] > 0,
-                            w[PH_NTOUCH] > 0, w[PH_BOUNDS_OK], w[PH_BLOCKS], w[PH_FIRST], w[PH_RECENT], w[PH_SEL_CAP]};
+                            w[PH_NTOUCH] > 0, w[PH_BOUNDS_OK], w[PH_BLOCKS], w[PH_FIRST], w[PH_RECENT], w[PH_SEL_CAP],
+                            w[PH_SEL_ROWS]};
   uint64_t h = 1469598103934665603ull;
   for (int32_t f : fields)
     for (int i = 0; i < 4; ++i) h = (h ^ ((uint32_t(f) >> (8 * i)) & 255u)) * 1099511628211ull;

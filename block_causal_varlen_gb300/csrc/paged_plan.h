@@ -68,6 +68,9 @@ enum : int {
   PH_RECENT,
   PH_OFF_ROWPG,    // int32 [T]: word offset of the pages of every new row's sequence
   PH_SEL_CAP,      // a power of two that no new row has more blocks than
+  PH_SEL_ROWS,     // rows of a group whose blocks are selected together (1: every row is one)
+  PH_OFF_SELG,     // int32 [NSELG][2]: first row and number of rows of every group, none where rows are groups
+  PH_NSELG,
   PH_STATUS = H_STATUS, PH_STATUS_DETAIL = H_STATUS_DETAIL, // 5 few-rows attention, 6 tile attention
   kPagedHdrWords = kHdrWords
 };
@@ -95,6 +98,8 @@ enum : int { RC_P0 = 0, RC_P1, RC_RESERVED0, RC_RESERVED1, RC_PIECE, kRecordWord
 // A join of the n partial results in slots slot0, slot0 + 1, ... of one block.
 enum : int { MG_SLOT0 = 0, MG_N, MG_Q0, MG_HKV, MG_ROW0, MG_NROWS, MG_RESERVED0, MG_RESERVED1, kMergeWords = 8 };
 
+static_assert(PH_NSELG < PH_STATUS, "header words");
+
 // Records and joins have fixed places and room for the most there can be (a join has
 // two slots at least).
 constexpr int kOffDecRec = kPagedHdrWords;
@@ -104,8 +109,20 @@ constexpr int kOffTileMerge = kOffTileRec + kTileCtas * kRecordWords;
 constexpr int kOffLists = kOffTileMerge + kTilePartSlots / 2 * kMergeWords;
 
 // Sparse plans: the most blocks of a list, and of a sequence (its scores stay in one CTA's
-// shared memory, 4 bytes each).
+// shared memory).
 constexpr int kMostListed = 4096, kMostBlocks = 16384;
+// Groups of up to kSelRows rows of a sequence select their blocks together, where that leaves
+// enough CTAs and their scores and codes take no more than kSelSmem bytes.
+constexpr int kSelRows = 8, kSelCtas = 2 * kPagedSms;
+constexpr int64_t kSelSmem = 48 << 10;
+// Shared memory of the selection: codes of q (bytes of a (row, head): two lots of d, and what
+// sets eight of them apart in the banks), a power of two each, a score for each block and row.
+constexpr int select_pitch(int d) { return 2 * d + (d == 64 ? 64 : 16); }
+constexpr int64_t select_smem(int rows, int G, int d, int cap) {
+  return (int64_t(rows) * G + 7) / 8 * 8 * (select_pitch(d) + 4) + int64_t(rows) * cap * 4;
+}
+constexpr int64_t kSelMostSmem = select_smem(1, 128, 256, kMostBlocks);
+static_assert(kSelMostSmem <= 232448 - 1024, "selection over the per-CTA limit of shared memory");
 
 // Bytes of one head's K (or V) of a cached row, and of its scales' alignment (e2m1).
 constexpr int row_bytes(int fmt, int d) { return fmt == BD_CACHE_BF16 ? 2 * d : fmt == BD_CACHE_E4M3 ? d : d / 2; }
