@@ -42,7 +42,7 @@ struct AppendArgs {
 };
 
 template <int D, int FMT, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) bd_cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) bd_cache_append_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8, RPB = kThreads / LPR;
   constexpr int NF = PAIRS ? 4 : 8;  // frequencies of a lane
   const int sub = threadIdx.x % LPR;
@@ -59,9 +59,7 @@ __global__ void __launch_bounds__(kThreads) bd_cache_append_kernel(const AppendA
   const bool upper = !PAIRS && sub >= half;       // the second elements of their pairs
   const int other = PAIRS ? 0 : upper ? sub - half : sub + half;
   const int partner = int(threadIdx.x & 31u) - sub + (turns ? other : sub);
-  uint64_t f[NF];
-#pragma unroll
-  for (int i = 0; i < NF; ++i) f[i] = turns ? a.phase[PAIRS ? sub * 4 + i : (upper ? sub - half : sub) * 8 + i] : 0ull;
+  const uint64_t* phase = a.phase + (!turns ? 0 : PAIRS ? sub * 4 : (upper ? sub - half : sub) * 8);
 
   // (whole warps stay together for the shuffles: groups past the last repeat the last)
   for (uint32_t g0 = blockIdx.x * uint32_t(RPB); g0 < n; g0 += gridDim.x * uint32_t(RPB)) {
@@ -86,7 +84,7 @@ __global__ void __launch_bounds__(kThreads) bd_cache_append_kernel(const AppendA
     float c[NF], s[NF];
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
-      const int32_t turn = int32_t(uint32_t((f[i] * uint64_t(uint32_t(max(pos, 0)))) >> 32));
+      const int32_t turn = int32_t(uint32_t((__ldg(phase + i) * uint64_t(uint32_t(max(pos, 0)))) >> 32));
       sincospif(float(turn) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
       c[i] *= a.scale;
       s[i] *= a.scale;

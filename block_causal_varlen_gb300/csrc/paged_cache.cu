@@ -30,9 +30,12 @@ struct CacheArgs {
   int64_t kx_sr, kx_sh, vx_sr, vx_sh;          // in bytes
 };
 
+// Values of a row that a lane takes: of an e2m1 cache the 16 that share a scale.
+constexpr int write_values(int fmt) { return fmt == BD_CACHE_E2M1 ? 16 : 8; }
+
 template <int D, int FMT>
 __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArgs a) {
-  constexpr int LPR = D / 8, RPB = kThreads / LPR;  // lanes of a head's row, such rows of a block
+  constexpr int NV = write_values(FMT) / 8, LPR = D / (8 * NV), RPB = kThreads / LPR;  // lanes of a head's row, such rows of a block
   const int32_t* plan = a.plan;
   grid_wait();
   const uint32_t Hkv = uint32_t(plan[PH_HKV]), n = uint32_t(plan[PH_T]) * Hkv;
@@ -42,8 +45,11 @@ __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArg
   // (the whole warp takes part in the shuffles: rows past the last repeat the last)
   for (uint32_t r0 = blockIdx.x * uint32_t(RPB); r0 < n; r0 += gridDim.x * uint32_t(RPB)) {
     const uint32_t r = min(r0 + threadIdx.x / LPR, n - 1), t = r / Hkv, h = r - t * Hkv;
-    const uint4 kx = __ldcs(reinterpret_cast<const uint4*>(a.kx + int64_t(t) * a.kx_sr + int64_t(h) * a.kx_sh) + sub);
-    const uint4 vx = __ldcs(reinterpret_cast<const uint4*>(a.vx + int64_t(t) * a.vx_sr + int64_t(h) * a.vx_sh) + sub);
+    const uint4* kp = reinterpret_cast<const uint4*>(a.kx + int64_t(t) * a.kx_sr + int64_t(h) * a.kx_sh) + sub * NV;
+    const uint4* vp = reinterpret_cast<const uint4*>(a.vx + int64_t(t) * a.vx_sr + int64_t(h) * a.vx_sh) + sub * NV;
+    uint4 kx[NV], vx[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) { kx[i] = __ldcs(kp + i); vx[i] = __ldcs(vp + i); }
     const int32_t row = tok[t];
     const int64_t pg = row >> shift, ro = row & ((1 << shift) - 1);
     const bool store = row >= 0 && r0 + threadIdx.x / LPR < n;
@@ -51,13 +57,18 @@ __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArg
     uint8_t* vd = a.v + pg * a.v_sp + ro * a.v_sr + int64_t(h) * a.v_sh;
     if constexpr (FMT == BD_CACHE_BF16) {
       if (store) {
-        reinterpret_cast<uint4*>(kd)[sub] = kx;
-        reinterpret_cast<uint4*>(vd)[sub] = vx;
+        reinterpret_cast<uint4*>(kd)[sub] = kx[0];
+        reinterpret_cast<uint4*>(vd)[sub] = vx[0];
       }
     } else {
       const int64_t eo = pg * a.e_sp + ro * a.e_sr + int64_t(h) * a.e_sh;
-      store_quantised<LPR, FMT>(kx, sub, store, kd, a.k_exp + eo);
-      store_quantised<LPR, FMT>(vx, sub, store, vd, a.v_exp + eo);
+      if constexpr (FMT == BD_CACHE_E4M3) {
+        store_quantised<LPR, FMT>(kx[0], sub, store, kd, a.k_exp + eo);
+        store_quantised<LPR, FMT>(vx[0], sub, store, vd, a.v_exp + eo);
+      } else if (store) {
+        store_group_e2m1(kx[0], kx[NV - 1], sub, kd, a.k_exp + eo);
+        store_group_e2m1(vx[0], vx[NV - 1], sub, vd, a.v_exp + eo);
+      }
     }
   }
 }
@@ -229,7 +240,7 @@ extern "C" int32_t bd_cache_write(const void* plan_host, const void* plan_dev, c
   if (st) return st;
   if (w[PH_T] == 0) return ok();
   const CacheArgs a = cache_args(plan_dev, cache, k, v);
-  const int64_t blocks = (int64_t(w[PH_T]) * w[PH_HKV] * (w[PH_D] / 8) + kThreads - 1) / kThreads;
+  const int64_t blocks = (int64_t(w[PH_T]) * w[PH_HKV] * (w[PH_D] / write_values(cache->fmt)) + kThreads - 1) / kThreads;
   // three rounds of 8 CTAs an SM: 30000 / 100000 e4m3 rows of 8 heads 33.4 / 93-95 us, with
   // one round 35.5 / 97-99, with two 33.4 / 97
   const int grid = int(blocks < kPagedSms * 24 ? blocks : kPagedSms * 24);

@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include "../../include/bd_paged.h"
+#include "ptx.cuh"
 
 namespace bd {
 
@@ -129,22 +130,32 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t mx) {
   return uint32_t(min(b + (6.f * s < t ? 1 : 0), int(kMostScale)));
 }
 
-// 8 values as codes of scale byte b (255: zeros). x / s is taken as x times fp32's 1 / s, off by
-// less than 2^-22, and rounded to 12 bits: a quotient midway between two codes (three
-// significant bits) comes out exact, and others are 2^-8 away from there at least (8
-// significant bits of x against 7 of the code's midpoint times s).
+// 8 values as codes of scale byte b (255: zeros). x / s is taken as x times an approximate 1 / s, off
+// by less than 2^-22, and rounded to a multiple of 2^-10 (by adding and taking off 1.5 * 2^13; what
+// saturates anyway may come out anyhow above 6): a quotient midway between two codes, a multiple of 1/4,
+// comes out exact, and others are 2^-8 of it away from there at least (8 significant bits of x against 7 of
+// the code's midpoint times s). The sign is x's, of zeros too.
 __device__ __forceinline__ uint32_t quantise8_e2m1(const uint4& x, uint32_t b) {
   if (b == 255u) return 0u;
-  const float r = __frcp_rn(__uint_as_float((b << 20) + (112u << 23)));
-  auto y = [&](float v) { return __uint_as_float((__float_as_uint(v * r) + 0x800u) & 0xfffff000u); };
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float((b << 20) + (112u << 23))));
+  float y[8];
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = bf16_lo(w[i]), hi = bf16_hi(w[i]);
+    float2 v = dev::ffma2(make_float2(lo, hi), make_float2(r, r), make_float2(12288.f, 12288.f));
+    v = dev::fadd2(v, make_float2(-12288.f, -12288.f));
+    y[2 * i] = copysignf(v.x, lo);
+    y[2 * i + 1] = copysignf(v.y, hi);
+  }
   uint32_t c;
   asm("{\n\t.reg .b8 p, q, r, s;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 p, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %4, %3;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 r, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 s, %8, %7;\n\t"
       "mov.b32 %0, {p, q, r, s};\n\t}"
       : "=r"(c)
-      : "f"(y(bf16_lo(x.x))), "f"(y(bf16_hi(x.x))), "f"(y(bf16_lo(x.y))), "f"(y(bf16_hi(x.y))), "f"(y(bf16_lo(x.z))),
-        "f"(y(bf16_hi(x.z))), "f"(y(bf16_lo(x.w))), "f"(y(bf16_hi(x.w))));
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
   return c;
 }
 
@@ -160,6 +171,13 @@ __device__ __forceinline__ uint4 dequantise8_e2m1(uint32_t c, uint32_t b) {
     h[i] = bf16_pair(v.x, v.y);
   }
   return make_uint4(h[0], h[1], h[2], h[3]);
+}
+
+// The 16 values of scale number i of a row: codes at d, the scale's byte at e.
+__device__ __forceinline__ void store_group_e2m1(const uint4& x, const uint4& y, uint32_t i, uint8_t* d, uint8_t* e) {
+  const uint32_t mx = max(absmax8(x), absmax8(y)), byte = mx >= 0x7f80u ? 255u : scale_byte(mx);
+  reinterpret_cast<uint2*>(d)[i] = make_uint2(quantise8_e2m1(x, byte), quantise8_e2m1(y, byte));
+  e[i] = uint8_t(byte);
 }
 
 // Quantises a row spread over LPR lanes (8 values each; the whole warp takes part) and stores

@@ -74,8 +74,8 @@ struct TileCfg {
   // out. 4096 rows over 16384 (10 ragged sequences for e4m3) in registers and through
   // shared memory: bf16 d 64 624 and 590 us, d 128 650 and 672, d 256 1856 and 1872; e4m3
   // d 128 274 and 272.
-  static constexpr bool kTurnInRegs = !kConv && D >= 128;
-  static constexpr bool kStageInQ = kConv && D >= 128;
+  static constexpr bool kTurnInRegs = !kF8 && D >= 128;
+  static constexpr bool kStageInQ = kConv && D >= 128 && !kTurnInRegs;
   static constexpr int kOffStage = kOffRaw + kRawStages * kRawBytes;
   static constexpr int kOffBar = kOffStage + (kStageInQ || kTurnInRegs ? 0 : kSlots * 16384);
   static constexpr int kOffPieces = kOffBar + 512;
@@ -89,10 +89,13 @@ struct TileCfg {
   // gets in their way (d 128: 668 -> 724).
   static constexpr bool kPHalves = kSlots == 1;
   static constexpr int kThreads = kConv ? 512 : 384;
+  // warps from here on convert: with one slot four softmax warps more (e2m1, whose rows go in halves then)
+  static constexpr int kConvWarp = kF4 && kSlots == 1 ? 8 : 12;
+  static constexpr int kConvThreads = 32 * (16 - kConvWarp);
   // registers after setmaxnreg: warps 0-3, the softmax warps, the converting warps
-  static constexpr int kRegsCtl = kConv ? 40 : 72, kRegsSoftmax = kConv ? 200 : 216, kRegsConv = 72;
+  static constexpr int kRegsCtl = kConv ? 40 : 72, kRegsSoftmax = kConvWarp == 8 ? 240 : kConv ? 200 : 216, kRegsConv = kConvWarp == 8 ? 112 : 72;
   static constexpr int kRegsLaunch = kConv ? 128 : 168;
-  static_assert(128 * kRegsCtl + 256 * kRegsSoftmax + (kConv ? 128 * kRegsConv : 0) <= kRegsLaunch * kThreads,
+  static_assert(128 * kRegsCtl + 32 * (kConvWarp - 4) * kRegsSoftmax + (kConv ? kConvThreads * kRegsConv : 0) <= kRegsLaunch * kThreads,
                 "register split exceeds the launch's registers");
   static_assert(kSmem <= 232448, "shared memory over the per-CTA limit");
   static_assert(kOCol + kSlots * D <= 512, "O accumulators exceed TMEM");
@@ -179,18 +182,18 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     mbar_init(bar(T_QFULL), 1);
-    mbar_init(bar(T_QCONV), 128);
+    mbar_init(bar(T_QCONV), Cfg::kConvThreads);
     mbar_init(bar(T_QEMPTY), Cfg::kStageInQ ? 4 * NS : NS);  // softmax warps, or MMA threads
     for (int s = 0; s < NST; ++s) {
-      mbar_init(bar(T_KFULL + s), CONV ? 128 : 1);
+      mbar_init(bar(T_KFULL + s), CONV ? Cfg::kConvThreads : 1);
       mbar_init(bar(T_KEMPTY + s), NS);
-      mbar_init(bar(T_VFULL + s), CONV ? 128 : 1);
+      mbar_init(bar(T_VFULL + s), CONV ? Cfg::kConvThreads : 1);
       mbar_init(bar(T_VEMPTY + s), NS);
       mbar_init(bar(T_VTAIL + s), 1);
     }
     for (int s = 0; s < NR; ++s) {
       mbar_init(bar(T_RFULL + s), 1);
-      mbar_init(bar(T_REMPTY + s), 128);
+      mbar_init(bar(T_REMPTY + s), Cfg::kConvThreads);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(bar(T_SFULL + s), 1);
@@ -337,6 +340,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             mma_ss_lo(d_s, qa + off, kb + off, idS, kk > 0);
           }
         };
+        // V's tile is free when P V is done, not when the next S is: with one slot and one stage the next
+        // tile of V waits for that (10 ragged sequences at d 256: bf16 226 -> 193 us); with two slots it
+        // only costs a commit
+        constexpr bool kEarlyV = NS == 1;
         constexpr int kHalf = Cfg::kPHalves ? 4 : 0;  // steps of P V that start after the first half of P
         auto issue_pv = [&](auto from, auto to, int st, bool acc) {
           const uint32_t vb = sdesc_lo(sV + st * Cfg::kTileBytes, 16384);
@@ -396,9 +403,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             if (act) {
               tc_fence_after();
               issue_pv(StepsH{}, Steps8{}, svp, j > 1);
+              if (kEarlyV) tc_commit(bar(T_VEMPTY + svp));
               if (j < P.nt) issue_s(skn);
               pass_turn();
-              tc_commit(bar(T_VEMPTY + svp));
+              if (!kEarlyV) tc_commit(bar(T_VEMPTY + svp));
               if (j < P.nt) {
                 tc_commit(bar(T_SFULL + s));
                 tc_commit(bar(T_KEMPTY + skn));
@@ -464,7 +472,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         it += P.nt;
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < Cfg::kConvWarp) {
     regs_set<Cfg::kRegsSoftmax, Cfg::kRegsLaunch>();
     // ---------------------------------------------------------- softmax
     const int s = (warp - 4) >> 2, quarter = warp & 3;
@@ -716,27 +724,38 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
   } else {
     if constexpr (F4) {
       regs_set<Cfg::kRegsConv, Cfg::kRegsLaunch>();
-      // -------------------------------------------------------- raw tiles to fp16, thread = key
-      const int r = threadIdx.x - 384;
-      constexpr int RB = Cfg::kRowBytes, NW = D / 64;  // words of a row's scales
-      struct Scales { uint32_t k[NW], v[NW]; };
+      // -------------------------------------------------------- raw tiles to fp16, thread = key (or half of one)
+      const int x = threadIdx.x - 32 * Cfg::kConvWarp, r = x & 127, part = x >> 7;
+      constexpr int PARTS = Cfg::kConvThreads / 128;
+      constexpr int RB = Cfg::kRowBytes, CH = D / 32 / PARTS;  // 16-byte pieces of a raw row in a part
+      static_assert(CH <= 4, "a part's scales are eight bytes at most");
+      struct Scales { uint64_t k, v; };
       uint32_t it = 0, rit = 0, n = 0;
       bool ok = true;
-      auto convert = [&](uint32_t src, uint32_t dst, const uint32_t (&sc)[NW]) {
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {  // 16 bytes: 32 codes, two scales
-          const int x = RB == 32 ? c ^ ((r >> 2) & 1) : RB == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7);
-          const uint4 u = ld_shared_u4(src + r * RB + (x << 4));
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w}, two = sc[c >> 1] >> (16 * (c & 1));
+      // One piece (32 codes, two scales) after another, the next one's load in flight: unrolled, the loop
+      // takes more registers than these warps have.
+      auto convert = [&](uint32_t src, uint32_t dst, uint64_t sc) {
+        auto load = [&](int ci) {
+          const int c = part * CH + ci, x = RB == 32 ? c ^ ((r >> 2) & 1) : RB == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7);
+          return ld_shared_u4(src + r * RB + (x << 4));
+        };
+        uint4 u = load(0);
+#pragma unroll(PARTS > 1 ? 4 : 2)
+        for (int ci = 0; ci < CH; ++ci, sc >>= 16) {
+          const int c = part * CH + ci;
+          const uint4 next = load(min(ci + 1, CH - 1));
+          const uint32_t f0 = scale_twice(uint32_t(sc) & 255u), f1 = scale_twice(uint32_t(sc >> 8) & 255u);
+          const uint32_t d = dst + (c >> 1) * 16384 + r * 128;
+          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t h[4];
             e2m1x8_to_f16(w[i], h);
-            const uint32_t f = scale_twice(i < 2 ? two & 255u : (two >> 8) & 255u);
-            const int oc = (c & 1) * 4 + i;
-            st_shared_v4(dst + (c >> 1) * 16384 + r * 128 + ((oc ^ (r & 7)) << 4), mul_f16x2(h[0], f), mul_f16x2(h[1], f),
-                         mul_f16x2(h[2], f), mul_f16x2(h[3], f));
+            const uint32_t f = i < 2 ? f0 : f1;
+            st_shared_v4(d + ((((c & 1) * 4 + i) ^ (r & 7)) << 4), mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f),
+                         mul_f16x2(h[3], f));
           }
+          u = next;
         }
         fence_proxy_async_smem();
       };
@@ -747,19 +766,27 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           const uint32_t q = sQ + s * Cfg::kTileBytes + r * 128;
           auto at = [&](int c) { return q + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4); };
           uint32_t mx = 0;
-#pragma unroll 8
+#pragma unroll 4
           for (int c = 0; c < D / 8; ++c) mx = max(mx, absmax8(ld_shared_u4(at(c))));
           float inv;
           const float2 up = q_factors(mx, &inv);
-          qs[((n - 1) & 1) * 128 * NS + s * 128 + r] = a.scale_log2 * inv;
-#pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
+          if (part == 0) qs[((n - 1) & 1) * 128 * NS + s * 128 + r] = a.scale_log2 * inv;
+          if (PARTS > 1) named_bar_sync(1, Cfg::kConvThreads);  // every part has seen the whole row
+#pragma unroll 2
+          for (int ci = 0; ci < D / 8 / PARTS; ++ci) {
+            const int c = part * (D / 8 / PARTS) + ci;
             const uint4 u = ld_shared_u4(at(c));
             auto f16 = [&](uint32_t x) { return pack_f16(bf16_lo(x) * up.x * up.y, bf16_hi(x) * up.x * up.y); };
             st_shared_v4(at(c), f16(u.x), f16(u.y), f16(u.z), f16(u.w));
           }
         }
         fence_proxy_async_smem();
+      };
+      auto turn_q = [&](int ns) -> bool {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(T_QFULL), (n - 1) & 1, abort_flag))) return false;
+        convert_q(ns);
+        mbar_arrive(bar(T_QCONV));
+        return true;
       };
       for (int p = p0; p < p1 && ok; ++p) {
         const Piece P = piece(p);
@@ -769,19 +796,15 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           return j < P.nt && pos < P.k1 ? plan[P.pages + (pos >> pshift)] : -1;
         };
         auto scales_of = [&](int j, int page) {
-          Scales x = {};
+          Scales x = {0, 0};
           if (page < 0) return x;
-          const int64_t o = int64_t(page) * a.e_sp + int64_t((P.k0 + 128 * j + r) & ((1 << pshift) - 1)) * a.e_sr + int64_t(P.hkv) * a.e_sh;
+          const int64_t o = int64_t(page) * a.e_sp + int64_t((P.k0 + 128 * j + r) & ((1 << pshift) - 1)) * a.e_sr + int64_t(P.hkv) * a.e_sh + part * 2 * CH;
           if constexpr (D == 64) {
-            x.k[0] = *reinterpret_cast<const uint32_t*>(a.k_exp + o);
-            x.v[0] = *reinterpret_cast<const uint32_t*>(a.v_exp + o);
+            x.k = *reinterpret_cast<const uint32_t*>(a.k_exp + o);
+            x.v = *reinterpret_cast<const uint32_t*>(a.v_exp + o);
           } else {
-#pragma unroll
-            for (int i = 0; i < NW; i += 2) {
-              const uint2 k = *reinterpret_cast<const uint2*>(a.k_exp + o + 4 * i), v = *reinterpret_cast<const uint2*>(a.v_exp + o + 4 * i);
-              x.k[i] = k.x; x.k[i + 1] = k.y;
-              x.v[i] = v.x; x.v[i + 1] = v.y;
-            }
+            x.k = *reinterpret_cast<const uint64_t*>(a.k_exp + o);
+            x.v = *reinterpret_cast<const uint64_t*>(a.v_exp + o);
           }
           return x;
         };
@@ -796,14 +819,16 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           pg = page_of(j + 2);
           const int s = it % NST;
           // V's scales of NaN stay out of the products where some row does not see the key
-          if (P.k0 + 128 * j + r >= P.clear)
-#pragma unroll
-            for (int i = 0; i < NW; ++i) {
-              const uint32_t gone = __vcmpgtu4(now.v[i], kMostScale * 0x01010101u);
-              now.v[i] &= ~gone;
-              if (gone) odd[(n - 1) % kOddMarks] = n;
-            }
+          if (P.k0 + 128 * j + r >= P.clear) {
+            const uint32_t lo = __vcmpgtu4(uint32_t(now.v), kMostScale * 0x01010101u);
+            const uint32_t hi = __vcmpgtu4(uint32_t(now.v >> 32), kMostScale * 0x01010101u);
+            now.v &= ~(uint64_t(hi) << 32 | lo);
+            if (lo | hi) odd[(n - 1) % kOddMarks] = n;
+          }
           for (int h = 0; h < 2; ++h, ++rit) {
+            // Q where its tile is free before the last block's results are out between its K and V, else
+            // behind them
+            if (j == 0 && h == 1 && !Cfg::kStageInQ && !(ok = turn_q(P.ns))) break;
             const int rs = rit % NR;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_RFULL + rs), (rit / NR) & 1, abort_flag)))) break;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar((h ? T_VEMPTY : T_KEMPTY) + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
@@ -812,11 +837,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             mbar_arrive(bar((h ? T_VFULL : T_KFULL) + s));
           }
           if (!ok) break;
-          if (j == 0) {
-            if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_QFULL), (n - 1) & 1, abort_flag)))) break;
-            convert_q(P.ns);
-            mbar_arrive(bar(T_QCONV));
-          }
+          if (j == 0 && Cfg::kStageInQ && !(ok = turn_q(P.ns))) break;
         }
       }
     } else if constexpr (F8) {
