@@ -31,7 +31,8 @@ struct AppendArgs {
   float scale;
   int32_t rot;                               // turned elements of a head
   int32_t H, Hkv;                            // H = 0: no q
-  int32_t per, chunks;                       // heads of a group, groups of a row
+  int32_t per;                               // heads of a group, all of q, of K or of V
+  int32_t nq, nkv, chunks;                   // groups of a row: nq of q, nkv of K, nkv of V
   const uint8_t *q, *k, *v;                  // packed bf16 rows, strides in bytes
   uint8_t* qo;
   int64_t q_sr, q_sh, k_sr, k_sh, v_sr, v_sh, o_sr, o_sh;
@@ -42,9 +43,8 @@ struct AppendArgs {
 };
 
 template <int D, int FMT, bool PAIRS>
-__global__ void __launch_bounds__(kThreads, 3) bd_cache_append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) bd_cache_append_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8, RPB = kThreads / LPR;
-  constexpr int NF = PAIRS ? 4 : 8;  // frequencies of a lane
   const int sub = threadIdx.x % LPR;
   const int32_t* plan = a.plan;
   // (the phases are weights, and not written by the kernels in front of this one, but by whom is
@@ -57,79 +57,82 @@ __global__ void __launch_bounds__(kThreads, 3) bd_cache_append_kernel(const Appe
   const int half = a.rot / 16;                    // lanes of half of the turned elements
   const bool turns = sub < 2 * half;
   const bool upper = !PAIRS && sub >= half;       // the second elements of their pairs
-  const int other = PAIRS ? 0 : upper ? sub - half : sub + half;
-  const int partner = int(threadIdx.x & 31u) - sub + (turns ? other : sub);
+  const int partner = int(threadIdx.x & 31u) - sub + (!turns || PAIRS ? sub : upper ? sub - half : sub + half);
   const uint64_t* phase = a.phase + (!turns ? 0 : PAIRS ? sub * 4 : (upper ? sub - half : sub) * 8);
 
   // (whole warps stay together for the shuffles: groups past the last repeat the last)
   for (uint32_t g0 = blockIdx.x * uint32_t(RPB); g0 < n; g0 += gridDim.x * uint32_t(RPB)) {
     const bool there = g0 + threadIdx.x / LPR < n;
     const uint32_t g = min(g0 + threadIdx.x / LPR, n - 1), t = g / uint32_t(a.chunks);
-    const int h0 = int(g - t * uint32_t(a.chunks)) * a.per, h1 = min(h0 + a.per, a.H + 2 * a.Hkv);
+    const int c = int(g - t * uint32_t(a.chunks));
+    const bool is_q = c < a.nq, is_k = !is_q && c < a.nq + a.nkv;
+    const int h0 = (is_q ? c : is_k ? c - a.nq : c - a.nq - a.nkv) * a.per, cnt = min(a.per, (is_q ? a.H : a.Hkv) - h0);
     const int32_t row = tok[t], pos = where[t];
     const int64_t pg = row >> shift, ro = row & ((1 << shift) - 1);
-    const bool place = there && row >= 0;
-    auto from = [&](int h) {
-      return h < a.H           ? a.q + int64_t(t) * a.q_sr + int64_t(h) * a.q_sh
-             : h < a.H + a.Hkv ? a.k + int64_t(t) * a.k_sr + int64_t(h - a.H) * a.k_sh
-                               : a.v + int64_t(t) * a.v_sr + int64_t(h - a.H - a.Hkv) * a.v_sh;
-    };
+    const bool store = there && (is_q || row >= 0), turn = turns && (is_q || is_k) && pos >= 0;
+    // where the group's heads are read and go to, and its exponents or scales
+    const int64_t ss = is_q ? a.q_sh : is_k ? a.k_sh : a.v_sh, ds = is_q ? a.o_sh : is_k ? a.k_ch : a.v_ch;
+    const uint8_t* src = (is_q ? a.q + int64_t(t) * a.q_sr : is_k ? a.k + int64_t(t) * a.k_sr : a.v + int64_t(t) * a.v_sr) + h0 * ss + sub * 16;
+    uint8_t* dst = (is_q ? a.qo + int64_t(t) * a.o_sr
+                    : is_k ? a.kc + pg * a.k_cp + ro * a.k_cr : a.vc + pg * a.v_cp + ro * a.v_cr) + h0 * ds;
+    uint8_t* exps = FMT == BD_CACHE_BF16 || is_q ? nullptr : (is_k ? a.k_exp : a.v_exp) + pg * a.e_sp + ro * a.e_sr + h0 * a.e_sh;
     constexpr int U = 4;  // heads in flight
     uint4 x[U];
     auto load = [&](int h) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = __ldcs(reinterpret_cast<const uint4*>(from(min(h + u, h1 - 1))) + sub);
+      for (int u = 0; u < U; ++u, src += ss)
+        if (h + u < cnt) x[u] = __ldcs(reinterpret_cast<const uint4*>(src));
     };
-    load(h0);
-    float c[NF], s[NF];
 #pragma unroll
-    for (int i = 0; i < NF; ++i) {
-      const int32_t turn = int32_t(uint32_t((__ldg(phase + i) * uint64_t(uint32_t(max(pos, 0)))) >> 32));
-      sincospif(float(turn) * 4.656612873077393e-10f, &s[i], &c[i]);  // 2^-31: half turns
-      c[i] *= a.scale;
-      s[i] *= a.scale;
+    for (int u = 0; u < U; ++u) x[u] = make_uint4(0, 0, 0, 0);
+    load(0);
+    // cosines and sines of this lane's four words of a head (pairs: of one pair each); the sign of a word's
+    // own sine goes with its element's place in the pair
+    float2 cs[4], sn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float cc[2], sv[2];
+#pragma unroll
+      for (int e = 0; e < (PAIRS ? 1 : 2); ++e) {
+        const uint64_t f = __ldg(phase + (PAIRS ? i : 2 * i + e));
+        const int32_t part = int32_t(uint32_t((f * uint64_t(uint32_t(max(pos, 0)))) >> 32));
+        sincospif(float(part) * 4.656612873077393e-10f, &sv[e], &cc[e]);  // 2^-31: half turns
+        cc[e] *= a.scale;
+        sv[e] *= a.scale;
+      }
+      cs[i] = PAIRS ? make_float2(cc[0], cc[0]) : make_float2(cc[0], cc[PAIRS ? 0 : 1]);
+      sn[i] = PAIRS ? make_float2(-sv[0], sv[0])
+              : upper ? make_float2(sv[0], sv[PAIRS ? 0 : 1]) : make_float2(-sv[0], -sv[PAIRS ? 0 : 1]);
     }
     for (int hb = 0; hb < a.per; hb += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (hb + u >= a.per) break;
-        const int h = h0 + hb + u;                 // past h1 the last head comes again, and is not stored
-        uint4 y = x[u];
-        uint32_t z[4] = {y.x, y.y, y.z, y.w};
-        if constexpr (!PAIRS) {
-          z[0] = __shfl_sync(kFull, y.x, partner); z[1] = __shfl_sync(kFull, y.y, partner);
-          z[2] = __shfl_sync(kFull, y.z, partner); z[3] = __shfl_sync(kFull, y.w, partner);
-        }
-        if (turns && h < a.H + a.Hkv && pos >= 0) {
-          const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-          uint32_t r[4];
+        uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = PAIRS ? w[i] : __shfl_sync(kFull, w[i], partner);
+        if (turn) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float lo = bf16_lo(w[i]), hi = bf16_hi(w[i]);
-            if constexpr (PAIRS) {
-              r[i] = bf16_pair(lo * c[i] - hi * s[i], hi * c[i] + lo * s[i]);
-            } else {
-              const float pl = bf16_lo(z[i]), ph = bf16_hi(z[i]);
-              const float sl = upper ? s[2 * i] : -s[2 * i], sh = upper ? s[2 * i + 1] : -s[2 * i + 1];
-              r[i] = bf16_pair(lo * c[2 * i] + pl * sl, hi * c[2 * i + 1] + ph * sh);
-            }
+            const float2 v = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
+            const float2 o = PAIRS ? make_float2(v.y, v.x) : make_float2(bf16_lo(z[i]), bf16_hi(z[i]));
+            const float2 r = dev::ffma2(v, cs[i], dev::fmul2(o, sn[i]));
+            w[i] = bf16_pair(r.x, r.y);
           }
-          y = make_uint4(r[0], r[1], r[2], r[3]);
         }
-        const bool mine = h < h1, is_q = h < a.H, is_k = h < a.H + a.Hkv;
-        if (mine && is_q && there) __stcs(reinterpret_cast<uint4*>(a.qo + int64_t(t) * a.o_sr + int64_t(h) * a.o_sh) + sub, y);
-        const bool store = place && mine && !is_q;
-        if (!__any_sync(kFull, store)) continue;
-        const int64_t hk = is_q ? 0 : is_k ? h - a.H : h - a.H - a.Hkv;
-        uint8_t* d = is_k ? a.kc + pg * a.k_cp + ro * a.k_cr + hk * a.k_ch : a.vc + pg * a.v_cp + ro * a.v_cr + hk * a.v_ch;
+        const uint4 y = make_uint4(w[0], w[1], w[2], w[3]);
+        const bool mine = store && hb + u < cnt;
         if constexpr (FMT == BD_CACHE_BF16) {
-          if (store) reinterpret_cast<uint4*>(d)[sub] = y;
+          if (mine) __stcs(reinterpret_cast<uint4*>(dst) + sub, y);
         } else {
-          uint8_t* e = (is_k ? a.k_exp : a.v_exp) + pg * a.e_sp + ro * a.e_sr + hk * a.e_sh;
-          store_quantised<LPR, FMT>(y, sub, store, d, e);
+          if (mine && is_q) __stcs(reinterpret_cast<uint4*>(dst) + sub, y);
+          if (__any_sync(kFull, mine && !is_q)) store_quantised<LPR, FMT>(y, sub, mine && !is_q, dst, exps);
+          exps += a.e_sh;
         }
+        dst += ds;
       }
-      if (hb + U < a.per) load(h0 + hb + U);
+      if (hb + U < a.per) load(hb + U);
     }
   }
 }
@@ -211,12 +214,13 @@ extern "C" int32_t bd_cache_append(const void* plan_host, const void* plan_dev, 
   a.v_cp = cache->v.stride_b * es; a.v_cr = cache->v.stride_row * es; a.v_ch = cache->v.stride_head * es;
   a.k_exp = cache->k_exp; a.v_exp = cache->v_exp;
   a.e_sp = cache->exp_stride_page; a.e_sr = cache->exp_stride_row; a.e_sh = cache->exp_stride_head;
-  // heads of a group: as many as leave every SM 2048 lanes
-  const int heads = a.H + 2 * a.Hkv;
-  const int64_t lanes = int64_t(w[PH_T]) * heads * (w[PH_D] / 8);
+  // heads of a group: as many as leave every SM 2048 lanes, up to 16
+  const int64_t lanes = int64_t(w[PH_T]) * (a.H + 2 * a.Hkv) * (w[PH_D] / 8);
   a.per = int(lanes / (int64_t(kPagedSms) * 2048));
   a.per = a.per < 1 ? 1 : a.per > 16 ? 16 : a.per;
-  a.chunks = (heads + a.per - 1) / a.per;
+  a.nq = (a.H + a.per - 1) / a.per;
+  a.nkv = (a.Hkv + a.per - 1) / a.per;
+  a.chunks = a.nq + 2 * a.nkv;
   if (int64_t(w[PH_T]) * a.chunks > INT32_MAX) return fail(BD_ERR_CAPACITY, "new rows times heads past 2^31 - 1");
   const int64_t blocks = (int64_t(w[PH_T]) * a.chunks * (w[PH_D] / 8) + kThreads - 1) / kThreads;
   const int grid = int(blocks < kPagedSms * 8 ? blocks : kPagedSms * 8);
