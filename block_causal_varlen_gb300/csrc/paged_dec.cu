@@ -75,7 +75,9 @@ struct DecCfg {
   static constexpr int kChunk = kRowBytes <= 128 && NB <= 2 ? 32 : 16;
   static constexpr int kMatBytes = kChunk * kRowBytes;        // K (or V) of a chunk
   static constexpr int kStageBytes = 2 * kMatBytes;
-  static constexpr int kWarps = kF4 && NB == 1 ? 8 : 4, kLanes = kWarps / kSplit;  // kLanes: chunks in work at a time
+  // (e2m1 turns codes into operands all the time: with 4, 6 and 8 warps 64 ragged sequences took 81.6, 73.0
+  // and 73.5 us, one of 4096 rows 7.6, 7.8 and 8.1. More warps cost more at a block's end)
+  static constexpr int kWarps = kF4 && NB == 1 ? 6 : 4, kLanes = kWarps / kSplit;  // kLanes: chunks in work at a time
   static constexpr int kThreads = 32 * kWarps;
   // a warp's share of a block is added up 8 rows x kCols columns at a time; head dim 256's
   // scores pass through the same place, two chunks in turn

@@ -377,3 +377,20 @@ def test_captured_steps_replay(fmt):
         torch.cuda.synchronize()
         bd.bd_check_status(nxt)
         assert all(torch.equal(a, b) for a, b in zip((q, out, lse, lists, bounds.code, bounds.exp), want[i])), i
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 300])
+def test_scores_of_the_largest_codes_are_exact(new, d):
+    """Codes of +-127 throughout but for single ones: sums that differ by one, the largest there are."""
+    s = Sparse([new], [700], 4, 1, d, 5, 0, 1, junk=0.0)
+    s.c.q[:] = 127.0
+    s.c.q[:, 1:] = -127.0
+    g = torch.Generator().manual_seed(0)
+    code = torch.full((s.c.num_pages, 1, 2, d), 127, dtype=torch.int8)
+    code[:, :, 0] = -127
+    for p in range(s.c.num_pages):
+        code[p, 0, :, int(torch.randint(0, d, (1,), generator=g))] -= torch.tensor([-(p % 3), p % 5], dtype=torch.int8)
+    s.bounds.code.copy_(code)
+    s.bounds.exp[:] = 127
+    assert torch.equal(s.lists().cpu(), s.want_lists())
