@@ -303,8 +303,10 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
         for (int h = 0; h < 2; ++h) {
           const int b = tile * 16 + rw + 8 * h;
           if (b >= most) continue;
-          const uint32_t k0 = eb[h] == 255u ? kOddBlock : order_of(float(c[2 * h]) * pow2f(s_eq[c0] + int(eb[h]) - 127));
-          const uint32_t k1 = eb[h] == 255u ? kOddBlock : order_of(float(c[2 * h + 1]) * pow2f(s_eq[c0 + 1] + int(eb[h]) - 127));
+          // (bounds that were never set may hold any byte)
+          auto key = [&](int v, int e) { return order_of(float(v) * pow2f(min(max(e + int(eb[h]) - 127, -126), 126))); };
+          const uint32_t k0 = eb[h] == 255u ? kOddBlock : key(c[2 * h], s_eq[c0]);
+          const uint32_t k1 = eb[h] == 255u ? kOddBlock : key(c[2 * h + 1], s_eq[c0 + 1]);
           if (r0 == r1) {
             if (in0) atomicMax(&s_key[r0 * a.cap + b], max(k0, k1));
           } else {
