@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
   extern __shared__ uint4 sel_smem[];
   const int cols = a.rows * a.G, colt = (cols + 7) / 8;
   uint8_t* s_q = reinterpret_cast<uint8_t*>(sel_smem);          // [8 colt]: positive, then negative codes
-  int* s_eq = reinterpret_cast<int*>(s_q + colt * 8 * QP);      // [8 colt]
-  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_eq + colt * 8);  // [rows][cap]
+  float2* s_col = reinterpret_cast<float2*>(s_q + colt * 8 * QP);    // [8 colt]: q's power of two, the row's keys (-1: no row)
+  uint32_t* s_key = reinterpret_cast<uint32_t*>(s_col + colt * 8);   // [rows][cap]
   __shared__ uint32_t s_red[NW][2];
   __shared__ __align__(16) uint32_t s_hist[8][256];  // a row by the CTA: one for each pass, rows by warps: for each warp
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = lane & 3, rw = lane >> 2;
@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
         *reinterpret_cast<uint2*>(s_q + c * QP + lane * 8) = make_uint2(up[0], up[1]);
         *reinterpret_cast<uint2*>(s_q + c * QP + D + lane * 8) = make_uint2(down[0], down[1]);
       }
-      if (lane == 0) s_eq[c] = e;
+      if (lane == 0) s_col[c] = make_float2(pow2f(e), __int_as_float(there ? c / a.G * a.cap : -1));
     }
     for (int r = 0; r < n; ++r)
       for (int i = tid; i < most; i += THREADS) s_key[r * a.cap + i] = 0u;
@@ -285,6 +285,8 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
         eb[h] = a.exp[int64_t(pg[h]) * a.x_sp + int64_t(g) * a.x_sh];
       }
       if ((tile + NW) * 16 < most) look_up(tile + NW);
+      // (bounds that were never set may hold any byte)
+      const float ebf[2] = {pow2f(min(max(int(eb[0]) - 127, -126), 126)), pow2f(min(max(int(eb[1]) - 127, -126), 126))};
       for (int ct = 0; ct < colt; ++ct) {
         int c[4] = {0, 0, 0, 0};
         const uint8_t* q = s_q + (ct * 8 + rw) * QP + j * (D / 4);
@@ -297,21 +299,19 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
           mma_s8(c, lo[0][4 * i + 2], lo[1][4 * i + 2], lo[0][4 * i + 3], lo[1][4 * i + 3], v.z, v.w);
         }
         // this lane's columns 2 j, 2 j + 1 of blocks rw, rw + 8: the largest of a row's heads
-        const int c0 = ct * 8 + 2 * j, r0 = c0 / a.G, r1 = (c0 + 1) / a.G;
-        const bool in0 = r0 < n, in1 = r1 < n;
+        const float4 col = *reinterpret_cast<const float4*>(s_col + ct * 8 + 2 * j);
+        const int at0 = __float_as_int(col.y), at1 = __float_as_int(col.w);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int b = tile * 16 + rw + 8 * h;
           if (b >= most) continue;
-          // (bounds that were never set may hold any byte)
-          auto key = [&](int v, int e) { return order_of(float(v) * pow2f(min(max(e + int(eb[h]) - 127, -126), 126))); };
-          const uint32_t k0 = eb[h] == 255u ? kOddBlock : key(c[2 * h], s_eq[c0]);
-          const uint32_t k1 = eb[h] == 255u ? kOddBlock : key(c[2 * h + 1], s_eq[c0 + 1]);
-          if (r0 == r1) {
-            if (in0) atomicMax(&s_key[r0 * a.cap + b], max(k0, k1));
+          const uint32_t k0 = eb[h] == 255u ? kOddBlock : order_of(float(c[2 * h]) * (col.x * ebf[h]));
+          const uint32_t k1 = eb[h] == 255u ? kOddBlock : order_of(float(c[2 * h + 1]) * (col.z * ebf[h]));
+          if (at0 == at1) {
+            if (at0 >= 0) atomicMax(&s_key[at0 + b], max(k0, k1));
           } else {
-            if (in0) atomicMax(&s_key[r0 * a.cap + b], k0);
-            if (in1) atomicMax(&s_key[r1 * a.cap + b], k1);
+            if (at0 >= 0) atomicMax(&s_key[at0 + b], k0);
+            if (at1 >= 0) atomicMax(&s_key[at1 + b], k1);
           }
         }
       }

@@ -61,11 +61,20 @@ __global__ void __launch_bounds__(kThreads) bd_cache_write_kernel(const CacheArg
         reinterpret_cast<uint4*>(vd)[sub] = vx[0];
       }
     } else {
-      const int64_t eo = pg * a.e_sp + ro * a.e_sr + int64_t(h) * a.e_sh;
       if constexpr (FMT == BD_CACHE_E4M3) {
-        store_quantised<LPR, FMT>(kx[0], sub, store, kd, a.k_exp + eo);
-        store_quantised<LPR, FMT>(vx[0], sub, store, vd, a.v_exp + eo);
+        uint32_t kb, vb;
+        const uint2 kc = quantise8<LPR>(kx[0], &kb), vc = quantise8<LPR>(vx[0], &vb);
+        if (store) {
+          reinterpret_cast<uint2*>(kd)[sub] = kc;
+          reinterpret_cast<uint2*>(vd)[sub] = vc;
+          if (sub == 0) {
+            const int64_t eo = pg * a.e_sp + ro * a.e_sr + int64_t(h) * a.e_sh;
+            a.k_exp[eo] = uint8_t(kb);
+            a.v_exp[eo] = uint8_t(vb);
+          }
+        }
       } else if (store) {
+        const int64_t eo = pg * a.e_sp + ro * a.e_sr + int64_t(h) * a.e_sh;
         store_group_e2m1(kx[0], kx[NV - 1], sub, kd, a.k_exp + eo);
         store_group_e2m1(vx[0], vx[NV - 1], sub, vd, a.v_exp + eo);
       }

@@ -116,10 +116,10 @@ constexpr int kMostListed = 4096, kMostBlocks = 16384;
 constexpr int kSelRows = 8, kSelCtas = 2 * kPagedSms;
 constexpr int64_t kSelSmem = 48 << 10;
 // Shared memory of the selection: codes of q (bytes of a (row, head): two lots of d, and what
-// sets eight of them apart in the banks), a power of two each, a score for each block and row.
+// sets eight of them apart in the banks), a power of two and a place each, a score for each block and row.
 constexpr int select_pitch(int d) { return 2 * d + (d == 64 ? 64 : 16); }
 constexpr int64_t select_smem(int rows, int G, int d, int cap) {
-  return (int64_t(rows) * G + 7) / 8 * 8 * (select_pitch(d) + 4) + int64_t(rows) * cap * 4;
+  return (int64_t(rows) * G + 7) / 8 * 8 * (select_pitch(d) + 8) + int64_t(rows) * cap * 4;
 }
 constexpr int64_t kSelMostSmem = select_smem(1, 128, 256, kMostBlocks);
 static_assert(kSelMostSmem <= 232448 - 1024, "selection over the per-CTA limit of shared memory");

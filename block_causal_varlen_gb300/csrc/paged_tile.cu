@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     mbar_init(bar(T_QFULL), 1);
-    mbar_init(bar(T_QCONV), Cfg::kConvThreads);
+    if (F4) mbar_init(bar(T_QCONV), Cfg::kConvThreads);
     mbar_init(bar(T_QEMPTY), Cfg::kStageInQ ? 4 * NS : NS);  // softmax warps, or MMA threads
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(T_KFULL + s), CONV ? Cfg::kConvThreads : 1);
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_base + s * 128, tO = tmem + lane_base + Cfg::kOCol + s * D;
     const int tl = r / G, hg = r - tl * G;
-    constexpr float kPShift = F4 ? 7.f : 0.f;  // P, and with it l and O, are held times 2^this
+    constexpr float kPShift = 7.f;  // e2m1: P, and with it l and O, are held times 2^this
     uint32_t tc = 0, ai = 0, n = 0;
     bool ok = s < NS;
     for (int p = p0; p < p1 && ok; ++p) {
@@ -500,12 +500,12 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         }
         continue;
       }
-      float m_run = -CUDART_INF_F, l_run = 0.f, scale = a.scale_log2;
+      float m_run = -CUDART_INF_F, l_run = 0.f, row_scale = 0.f;
       for (int j = 0; j < P.nt; ++j, ++tc) {
         // (warps leave together: what follows is warp-wide)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_SFULL + s), tc & 1, abort_flag)))) break;
         tc_fence_after();
-        if (F4 && j == 0) scale = qs[((n - 1) & 1) * 128 * NS + s * 128 + r];
+        if (F4 && j == 0) row_scale = qs[((n - 1) & 1) * 128 * NS + s * 128 + r];
         uint32_t u[4][32];
 #pragma unroll
         for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, u[q]);
@@ -517,6 +517,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 32; ++e) x[q * 32 + e] = __uint_as_float(u[q][e]);
+        const float scale = F4 ? row_scale : a.scale_log2;
         // the row sees the tile's columns below `see`; per group of 32 columns the warp
         // skips what no row sees and leaves alone what every row sees
         const int see = lim - (P.k0 + 128 * j);
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             tmem_st32(tO + q * 32, ov);
           }
         }
-        const float m_eff = ((m_run == -CUDART_INF_F) ? 0.f : m_run) - kPShift;
+        const float m_ref = (m_run == -CUDART_INF_F) ? 0.f : m_run, m_eff = F4 ? m_ref - kPShift : m_ref;
         const float2 cs = make_float2(scale, scale), cm = make_float2(-m_eff, -m_eff);
         float2 s4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[2][32];
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         }
       };
       // NaN scores leave the maximum alone: what they gave was taken relative to 0
-      const float m_fin = (m_run == -CUDART_INF_F && l_run != 0.f ? 0.f : m_run) - kPShift;
+      const float m_end = m_run == -CUDART_INF_F && l_run != 0.f ? 0.f : m_run, m_fin = F4 ? m_end - kPShift : m_end;
       const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
       if (part) {
         if (live) {

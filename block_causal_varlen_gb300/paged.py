@@ -246,6 +246,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i:
 _tensor = struct.Struct("PqqqqiI").pack        # bd_tensor
 _rowstat = struct.Struct("Pqqq").pack          # bd_rowstat
 _entries = {}
+_BF16 = torch.bfloat16
 
 
 def _entry(name):
@@ -271,15 +272,15 @@ def _refuse(t, name, dtype, idx):
 def _rows3(t, name, heads, d, rows, idx):
     """A packed [rows, heads, d] bf16 tensor as the ABI's strided tensor (its bytes). The C ABI
     carries neither dtypes nor head counts, so they are checked here."""
-    if t.dtype is not torch.bfloat16 or t.get_device() != idx or idx < 0:
-        _refuse(t, name, torch.bfloat16, idx)
-    s = t.shape
-    if len(s) != 3 or s[1] != heads or s[2] != d or s[0] < rows:
-        raise ValueError(f"{name}: shape {tuple(s)}, expected [{rows} or more, {heads}, {d}]")
-    st = t.stride()
-    if st[2] != 1:
+    if t.dtype is not _BF16 or t.get_device() != idx or idx < 0:
+        _refuse(t, name, _BF16, idx)
+    n, h, c = t.shape if t.dim() == 3 else (-1, 0, 0)
+    if h != heads or c != d or n < rows:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{rows} or more, {heads}, {d}]")
+    row, head, one = t.stride()
+    if one != 1:
         raise ValueError(f"{name}: head dim must be contiguous")
-    return _tensor(t.data_ptr(), 0, 0, st[0], st[1], s[0], 0)
+    return _tensor(t.data_ptr(), 0, 0, row, head, n, 0)
 
 
 def _device(plan, cache):
