@@ -284,12 +284,12 @@ __global__ void __launch_bounds__(DecCfg<D, FMT, NB>::kThreads, 2)
     const bool two = kChunk == 32 && brows == 16 && keys > 16;  // copies of K and of V: one, or two
     if constexpr (F4) {
       const int64_t o = int64_t(cpage) * a.e_sp + (row * int(a.e_sr) + ceo);
-      static_assert(!F4 || kChunk == 32, "a lane for each key");
 #pragma unroll
       for (int m = 0; m < 2; ++m)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(exps + ((is * 2 + m) * kChunk + lane) * Cfg::kScale),
-                     "l"((m ? a.v_exp : a.k_exp) + o), "n"(F4 ? Cfg::kScale : 4)
-                     : "memory");
+        if (kChunk == 32 || (lane >> 4) == m)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(exps + ((is * 2 + m) * kChunk + lane % kChunk) * Cfg::kScale),
+                       "l"((m ? a.v_exp : a.k_exp) + o), "n"(F4 ? Cfg::kScale : 4)
+                       : "memory");
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full) : "memory");
     }
     if constexpr (F8) {
@@ -943,10 +943,10 @@ int32_t launch_dec_rows(const int32_t* w, const bd_paged_cache* c, const AttnArg
   const int rows = w[PH_DEC_ROWS];
   if (rows == 8) return launch_dec_t<D, FMT, 1, BLOCKS>(w, c, a, s);
   if (rows == 16) return launch_dec_t<D, FMT, 2, BLOCKS>(w, c, a, s);
-  if constexpr (dec_block_rows(FMT) == 32) {
+  if constexpr (dec_block_rows(FMT) >= 24)
     if (rows == 24) return launch_dec_t<D, FMT, 3, BLOCKS>(w, c, a, s);
+  if constexpr (dec_block_rows(FMT) >= 32)
     if (rows == 32) return launch_dec_t<D, FMT, 4, BLOCKS>(w, c, a, s);
-  }
   return fail(BD_ERR_PLAN, "few-rows blocks of %d rows at head dim %d", rows, D);
 }
 

@@ -411,14 +411,15 @@ int32_t prepare(const bd_paged_desc* D, const bd_sparse_desc* X, Built* B) {
   // few-rows kernel, in blocks of one size (a tile of 32 rows in use costs what one of 128
   // does). 16 sequences of 8000 rows, bf16 d 256, 32 pairs: 220 us, as tiles 253; d 128, 48
   // pairs: 195 and 138; e4m3 d 128, 48 pairs in three blocks: 144, as tiles 167; 64 pairs of
-  // 300-8000 rows: 66 and 63. Rows with blocks of their own go there one by one.
-  const int most = dec_most_rows(D->fmt), block = dec_block_rows(D->fmt);
+  // 300-8000 rows: 66 and 63; e2m1 d 128, 48 pairs: 127, as tiles 153 (d 256: 138 and 115, of 4 sequences of
+  // 3000 rows 23 and 26). Rows with blocks of their own go there one by one.
+  const int most = dec_most_rows(D->fmt);
   int32_t widest = 1;
-  if (X) widest = std::min(G, block);
+  if (X) widest = G;
   else
     for (int32_t b = 0; b < D->B; ++b)
       if (int64_t(D->q_len[b]) * G <= most) widest = std::max(widest, D->q_len[b] * G);
-  B->dec_rows = std::min((widest + 7) / 8 * 8, block);
+  B->dec_rows = dec_rows_for(D->fmt, widest);
   // every row block of a (sequence, K/V head): keys up to what its last row sees
   std::vector<Item>&dec = B->dec_items, &tile = B->tile_items;
   int64_t nitems = 0;

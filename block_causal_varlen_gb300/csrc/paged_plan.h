@@ -15,10 +15,16 @@ constexpr int32_t kPagedVersion = 2;
 // (tiles) or two (few rows: one adds up a block while the other's loads go on) on each.
 constexpr int kPagedSms = 152;
 constexpr int kDecCtas = 2 * kPagedSms, kTileCtas = kPagedSms;
-// A few-rows block has 8, 16 or (bf16: e4m3 lacks the registers) 24 or 32 (new row, query head)
-// pairs of one K/V head: the least that holds every sequence of the plan that goes there.
+// A few-rows block has 8, 16, 24 (bf16, e2m1) or 32 (bf16: the others lack the registers) (new row,
+// query head) pairs of one K/V head: the least that holds every sequence of the plan that goes there. e2m1
+// sequences of more than 24 go in blocks of 16 (16 of 8000 rows, 20 / 32 / 48 pairs: 76 us in blocks of
+// 24, 88 and 127 of 16; 32 pairs in a block of 32, whose sums spill: 127).
 constexpr int dec_most_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 48; }  // of a sequence that goes there
-constexpr int dec_block_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : 16; }
+constexpr int dec_block_rows(int fmt) { return fmt == BD_CACHE_BF16 ? 32 : fmt == BD_CACHE_E2M1 ? 24 : 16; }
+constexpr int dec_rows_for(int fmt, int widest) {
+  const int r = (widest + 7) / 8 * 8;
+  return r <= dec_block_rows(fmt) ? r : fmt == BD_CACHE_BF16 ? 32 : 16;
+}
 constexpr int kDecSlotRows = 32;
 // Rows of the joins get a CTA each, not a warp, if a block has more parts than kWideJoin, or
 // more than kWideJoinFew and every row finds a CTA at once (one sequence of 512 keys: 8.7 us by
