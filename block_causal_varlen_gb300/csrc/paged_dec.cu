@@ -6,7 +6,7 @@
 // keys [k0, k1) computes, per row, m = max_j s_j, l = sum_j 2^(s_j - m) and
 // O = sum_j 2^(s_j - m) v_j with s_j = log2(e) q . k_j / sqrt(d), in one pass.
 //
-// What bounds it is reading K and V once: a few rows use 2 x 2 x rows x d operations
+// What bounds it is reading K and V once (e2m1: turning them into operands): a few rows use 2 x 2 x rows x d operations
 // per key and 4 d bytes, far below the tensor rate, so the products use the
 // register-operand matrix instructions (m16n8k16), which want no TMEM and no 128-row
 // tiles, and everything is laid out to keep HBM busy:
@@ -35,7 +35,9 @@
 // 2^-21 of the row's largest, to 2^-32 of that), scaled by 2^7 for their sake.
 //
 // 64 ragged sequences of 500-16000 rows, 8 K/V heads of 128: bf16 (4 pairs a head) 164 us,
-// 6.8 TB/s; e4m3 (2 pairs) 92 us, 6.1 TB/s. One sequence of 4096 rows 7.7 us in a graph.
+// 6.8 TB/s; e4m3 (2 pairs) 92 us, 6.1 TB/s; e2m1 (4 pairs) 73 us, 4.3 TB/s, no longer HBM's: 700
+// instructions a chunk of 32 keys, 256 of them the conversions and the scales' products, the ALU (which
+// converts at half rate) 52% busy. One sequence of 4096 rows 7.5-7.8 us in a graph.
 // (Blocks of 32 bf16 rows at d 128 and 256 spill some 30 registers, 132 bytes.)
 //
 // A row takes nothing from a key it does not see, whatever is there: V's infinities

@@ -34,9 +34,9 @@
 //
 // What bounds it is the chain softmax -> P V -> next S of a slot: a tile pair takes 3250
 // cycles for 2048 of products (4000 with the conversion beside it), a block some 4500
-// more. 4096 rows over 16384 keys, 32 / 8 heads of 128: bf16 653 us (1473 TFLOP/s), e4m3 792, with
-// pauses between calls; bf16 681-696 in a row, under the power cap. (The e4m3 kernels spill some 10
-// registers, 36-44 bytes.)
+// more. 4096 rows over 16384 keys, 32 / 8 heads of 128: bf16 653 us (1473 TFLOP/s), e4m3 792, e2m1 743
+// (1295), with pauses between calls; bf16 681-696 in a row, under the power cap; at d 256 bf16 1493, e4m3
+// 2703, e2m1 2020. (The converting kernels spill 10 to 17 registers, 36-68 bytes.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -341,9 +341,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           }
         };
         // V's tile is free when P V is done, not when the next S is: with one slot and one stage the next
-        // tile of V waits for that (10 ragged sequences at d 256: bf16 226 -> 193 us); with two slots it
-        // only costs a commit
-        constexpr bool kEarlyV = NS == 1;
+        // tile of V waits for that (4096 rows over 16384 at d 256, bf16: 1854 -> 1493 us). Where tiles are
+        // converted, V's then gets in the way of K's (e4m3 2703 -> 2840, e2m1 2020 -> 2038); with two slots
+        // it only costs a commit.
+        constexpr bool kEarlyV = NS == 1 && !CONV;
         constexpr int kHalf = Cfg::kPHalves ? 4 : 0;  // steps of P V that start after the first half of P
         auto issue_pv = [&](auto from, auto to, int st, bool acc) {
           const uint32_t vb = sdesc_lo(sV + st * Cfg::kTileBytes, 16384);
