@@ -221,7 +221,7 @@ def test_most_blocks():
 # ------------------------------------------------------------------ attention
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("H,Hkv,d", HEADS + [(10, 2, 128), (40, 1, 128)])
+@pytest.mark.parametrize("H,Hkv,d", HEADS + [(10, 2, 128), (40, 1, 128), (24, 1, 128)])
 @pytest.mark.parametrize("page,blocks", [(16, 5), (64, 3)])
 def test_attention(page, blocks, H, Hkv, d, fmt):
     s = Sparse([1, 3, 0, 20, 2], [300, 33, 40, 530, 1], H, Hkv, d, blocks, seed=d, page=page, fmt=fmt, heads_first=page == 64)

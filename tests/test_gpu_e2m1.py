@@ -148,7 +148,8 @@ def test_few_rows(new, kv, H, Hkv, d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-@pytest.mark.parametrize("new,kv", [([8, 9], [300, 1000]), ([12, 5, 13], [700, 33, 2000]), ([12], [9001])])
+@pytest.mark.parametrize("new,kv", [([8, 9], [300, 1000]), ([12, 5, 13], [700, 33, 2000]), ([12], [9001]), ([5, 6, 2], [700, 50, 3000]),
+                                    ([6, 90], [5000, 300])])
 def test_around_the_few_rows_limit(new, kv, d):
     c = Case(new, kv, 8, 2, d, page=32, seed=d + len(new))
     pm.check_attention(c, *pu.run_attention(c))
