@@ -15,7 +15,8 @@
 // against hi, negative against lo; they stay in shared memory as whole numbers of the same order.
 // Choice: the threshold eight bits a pass from the highest bit in which scores differ, by counts
 // of the digits, then the blocks above it and the first ones equal to it, in order. Few rows have a
-// CTA of 16 warps each, bound by a chain of lookups (16 rows, 8 heads: 47 blocks 6.4 us, 938 blocks 12); many
+// CTA of 16 warps each, bound by a chain of lookups and what one SM takes in (16 rows, 8 heads: 47 blocks 6.4 us,
+// 938 blocks 12), or a cluster of them where there are SMs left (1 row: 12 -> 8.6); many
 // go by eight, a warp for each one's choice, which read their bounds once (600 rows, 255 blocks: 31 us). Scores as
 // fp16 products, or bounds fetched a tile ahead, were no faster (13.3 and 12.3 us for the 938 blocks).
 #include <cuda_bf16.h>
@@ -158,7 +159,7 @@ struct SelectArgs {
   int64_t x_sp, x_sh;
   int32_t* out;
   int64_t o_sr, o_sh;
-  int32_t G, Hkv, blocks, first, recent, page_shift, cap, rows;
+  int32_t G, Hkv, blocks, first, recent, page_shift, cap, rows, split;
 };
 
 // A score as a whole number of the same order (0: below all of them), an infinity of a block with
@@ -173,6 +174,22 @@ __device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, ui
   asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The word of another CTA of the cluster that lies where p does here.
+__device__ __forceinline__ uint32_t load_cluster(const uint32_t* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(uint32_t(__cvta_generic_to_shared(p))), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
 }
 
 // The digit of a threshold from counts of 256 digits (bins past those in use are zero): the highest
@@ -204,8 +221,9 @@ __device__ __forceinline__ uint32_t find_digit(const uint32_t* hist, int lane, i
   return __shfl_sync(kFull, digit, from);
 }
 
-template <int D, int THREADS>
-__global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_block_select_kernel(const SelectArgs a) {
+// SPLIT: a row's scores are shared out to the `split` CTAs of a cluster, the first of which chooses.
+template <int D, int THREADS, bool SPLIT>
+__global__ void __launch_bounds__(THREADS, D == 256 || SPLIT ? 1 : 1024 / THREADS) bd_block_select_kernel(const SelectArgs a) {
   constexpr int NW = THREADS / 32;
   constexpr int S = D / 32;                // contraction steps; a lane has D / 4 neighbouring codes of a block
   constexpr int QP = select_pitch(D);
@@ -222,14 +240,15 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
   const int groups = plan[PH_NSELG];
   const int32_t *where = plan + plan[PH_OFF_POS], *rowpg = plan + plan[PH_OFF_ROWPG], *list = plan + plan[PH_OFF_SELG];
   const uint32_t units = uint32_t(groups) * uint32_t(a.Hkv);  // (no more than new rows times heads)
-  for (uint32_t x = blockIdx.x; x < units; x += gridDim.x) {
+  const uint32_t parts = SPLIT ? a.split : 1, part = SPLIT ? cluster_rank() : 0;
+  for (uint32_t x = blockIdx.x / parts; x < units; x += gridDim.x / parts) {
     const int gi = int(x / uint32_t(a.Hkv)), g = int(x) - gi * a.Hkv;
     const int t0 = a.rows == 1 ? gi : list[2 * gi], n = a.rows == 1 ? 1 : list[2 * gi + 1];
     auto blocks_of = [&](int r) { const int pos = where[t0 + r]; return pos < 0 ? 0 : (pos >> a.page_shift) + 1; };
     auto out_of = [&](int r) { return a.out + int64_t(t0 + r) * a.o_sr + int64_t(g) * a.o_sh; };
     const int most = blocks_of(n - 1);
     if (most <= a.blocks) {  // all there are, for every row
-      for (int r = 0; r < n; ++r) {
+      for (int r = 0; r < n && part == 0; ++r) {
         const int nblk = blocks_of(r);
         for (int i = tid; i < a.blocks; i += THREADS) out_of(r)[i] = i < nblk ? i : -1;
       }
@@ -242,7 +261,8 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
 #pragma unroll
       for (int h = 0; h < 2; ++h) pg[h] = pages[min(tile * 16 + rw + 8 * h, most - 1)];
     };
-    look_up(warp);
+    const int step = NW * int(parts), tile0 = warp + NW * int(part);
+    look_up(tile0);
     // ---- q's codes: a warp for each (row, head)
     for (int c = warp; c < colt * 8; c += NW) {
       const bool there = c < n * a.G, in = lane < D / 8;
@@ -273,7 +293,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
       for (int i = tid; i < 1024; i += THREADS) s_hist[0][i] = 0u;
     __syncthreads();
     // ---- scores: 16 blocks of a warp at a time against 8 (row, head) columns
-    for (int tile = warp; tile * 16 < most; tile += NW) {
+    for (int tile = tile0; tile * 16 < most; tile += step) {
       uint32_t hi[2][2 * S], lo[2][2 * S], eb[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -286,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
         }
         eb[h] = a.exp[int64_t(pg[h]) * a.x_sp + int64_t(g) * a.x_sh];
       }
-      if ((tile + NW) * 16 < most) look_up(tile + NW);
+      if ((tile + step) * 16 < most) look_up(tile + step);
       // (bounds that were never set may hold any byte)
       const float ebf[2] = {pow2f(min(max(int(eb[0]) - 127, -126), 126)), pow2f(min(max(int(eb[1]) - 127, -126), 126))};
       for (int ct = 0; ct < colt; ++ct) {
@@ -318,7 +338,18 @@ __global__ void __launch_bounds__(THREADS, D == 256 ? 1 : 1024 / THREADS) bd_blo
         }
       }
     }
-    __syncthreads();
+    if constexpr (SPLIT) {
+      cluster_sync();
+      if (part == 0)
+        for (int i = tid; i < most; i += THREADS) {
+          const uint32_t from = uint32_t(i >> 4) / NW % parts;
+          if (from != 0) s_key[i] = load_cluster(&s_key[i], from);
+        }
+      cluster_sync();  // (the others' keys are theirs again)
+      if (part != 0) continue;
+    } else {
+      __syncthreads();
+    }
     // ---- the choice, of the blocks that are not listed always: K of [first, most - recent)
     const int K = a.blocks - a.first - a.recent;
     if (a.rows == 1) {
@@ -461,25 +492,45 @@ cudaError_t launch_bounds(int d, int grid, cudaStream_t s, const BoundsArgs& a) 
                     : launch_kernel(bd_block_bounds_kernel<256, FMT>, grid, kBoundThreads, 0, s, a);
 }
 
-template <int D, int THREADS>
+template <int D, int THREADS, bool SPLIT>
 int32_t launch_select_t(int grid, size_t smem, cudaStream_t s, const SelectArgs& a) {
+  auto kernel = bd_block_select_kernel<D, THREADS, SPLIT>;
   static std::atomic<bool> done[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 64 || !done[dev].load(std::memory_order_acquire)) {
-    const cudaError_t e = cudaFuncSetAttribute(bd_block_select_kernel<D, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               int(kSelMostSmem));
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSelMostSmem));
     if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(block select)");
     if (dev < 64) done[dev].store(true, std::memory_order_release);
   }
-  const cudaError_t e = launch_kernel(bd_block_select_kernel<D, THREADS>, grid, THREADS, smem, s, a);
+  cudaError_t e;
+  if constexpr (SPLIT) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(grid * a.split);
+    c.blockDim = dim3(THREADS);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = a.split;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = 2;
+    e = cudaLaunchKernelEx(&c, kernel, a);
+  } else {
+    e = launch_kernel(kernel, grid, THREADS, smem, s, a);
+  }
   return e == cudaSuccess ? BD_OK : cuda_fail(e, "bd_block_select_kernel launch");
 }
 
-// One row by 16 warps, several by 8.
+// One row by 16 warps, or by those of a few CTAs; several rows by 8.
 template <int D>
 int32_t launch_select(int grid, size_t smem, cudaStream_t s, const SelectArgs& a) {
-  return a.rows == 1 ? launch_select_t<D, 512>(grid, smem, s, a) : launch_select_t<D, 256>(grid, smem, s, a);
+  return a.rows > 1    ? launch_select_t<D, 256, false>(grid, smem, s, a)
+         : a.split > 1 ? launch_select_t<D, 512, true>(grid, smem, s, a)
+                       : launch_select_t<D, 512, false>(grid, smem, s, a);
 }
 
 }  // namespace
@@ -551,7 +602,7 @@ extern "C" int32_t bd_block_select(const void* plan_host, const void* plan_dev, 
   a.o_sr = blocks->stride_row; a.o_sh = blocks->stride_head;
   a.G = w[PH_G]; a.Hkv = w[PH_HKV];
   a.blocks = w[PH_BLOCKS]; a.first = w[PH_FIRST]; a.recent = w[PH_RECENT];
-  a.page_shift = w[PH_PAGE_SHIFT]; a.cap = w[PH_SEL_CAP]; a.rows = w[PH_SEL_ROWS];
+  a.page_shift = w[PH_PAGE_SHIFT]; a.cap = w[PH_SEL_CAP]; a.rows = w[PH_SEL_ROWS]; a.split = w[PH_SEL_SPLIT];
   const int64_t ctas = int64_t(w[PH_NSELG]) * w[PH_HKV];
   const int grid = int(ctas < kPagedSms * 8 ? ctas : kPagedSms * 8);
   const size_t smem = select_smem(a.rows, a.G, w[PH_D], a.cap);

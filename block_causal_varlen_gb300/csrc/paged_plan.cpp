@@ -33,6 +33,7 @@ int32_t view_paged_plan(const void* plan_host, const int32_t** out) {
       !in(w[PH_OFF_PGCNT], w[PH_NPAGES], 1) || !in(w[PH_OFF_DEC], w[PH_NDEC], kPieceWords) ||
       !in(w[PH_OFF_POS], w[PH_T], 1) || !in(w[PH_OFF_TOUCH], w[PH_NTOUCH], 1) ||
       (w[PH_BLOCKS] && (!in(w[PH_OFF_ROWPG], w[PH_T], 1) || w[PH_SEL_ROWS] < 1 || w[PH_SEL_ROWS] > kSelRows ||
+                        w[PH_SEL_SPLIT] < 1 || w[PH_SEL_SPLIT] > kSelMostSplit ||
                         (w[PH_SEL_ROWS] > 1 && !in(w[PH_OFF_SELG], w[PH_NSELG], 2)))) ||
       !in(w[PH_OFF_TILE], w[PH_NTILE], kPieceWords) || w[PH_NDECM] < 0 || w[PH_NDECM] > kDecSlots / 2 ||
       w[PH_NTILEM] < 0 || w[PH_NTILEM] > kTilePartSlots / 2)
@@ -372,7 +373,7 @@ struct Built {
   std::vector<Item> dec_items, tile_items;
   Seqs S;                          // of the items
   std::vector<int32_t> page_off;   // of the sequences
-  int32_t dec_rows, dec_live = 0, sel_cap = 0, sel_rows = 1;
+  int32_t dec_rows, dec_live = 0, sel_cap = 0, sel_rows = 1, sel_split = 1;
   int64_t sel_groups = 0;
 };
 
@@ -459,6 +460,8 @@ int32_t prepare(const bd_paged_desc* D, const bd_sparse_desc* X, Built* B) {
     while (B->sel_rows > 1 && (groups(B->sel_rows) * D->Hkv < kSelCtas || select_smem(B->sel_rows, G, D->d, B->sel_cap) > kSelSmem))
       B->sel_rows /= 2;
     B->sel_groups = groups(B->sel_rows);
+    if (B->sel_rows == 1 && B->sel_cap > kSelSplitCap)
+      while (B->sel_split < kSelMostSplit && 2 * B->sel_split * B->sel_groups * D->Hkv <= kPagedSms) B->sel_split *= 2;
     return BD_OK;
   }
   for (int32_t b = 0; b < D->B; ++b) {
@@ -563,7 +566,7 @@ static int32_t plan_build(const bd_paged_desc* desc, const bd_sparse_desc* spars
   if (sparse) {
     w[PH_BLOCKS] = sparse->blocks; w[PH_FIRST] = sparse->first; w[PH_RECENT] = sparse->recent;
     w[PH_OFF_ROWPG] = int32_t(w[PH_OFF_TOUCH] + X.ntouch);
-    w[PH_SEL_CAP] = X.sel_cap; w[PH_SEL_ROWS] = X.sel_rows;
+    w[PH_SEL_CAP] = X.sel_cap; w[PH_SEL_ROWS] = X.sel_rows; w[PH_SEL_SPLIT] = X.sel_split;
     w[PH_OFF_SELG] = int32_t(w[PH_OFF_ROWPG] + X.T);
     w[PH_NSELG] = int32_t(X.sel_groups);
     int32_t* group = w + w[PH_OFF_SELG];
@@ -657,7 +660,7 @@ extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
                             w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0,
                             w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0, w[PH_NTILE] > 0, w[PH_NTILEM] > 0,
                             w[PH_NTOUCH] > 0, w[PH_BOUNDS_OK], w[PH_BLOCKS], w[PH_FIRST], w[PH_RECENT], w[PH_SEL_CAP],
-                            w[PH_SEL_ROWS]};
+                            w[PH_SEL_ROWS], w[PH_SEL_SPLIT]};
   uint64_t h = 1469598103934665603ull;
   for (int32_t f : fields)
     for (int i = 0; i < 4; ++i) h = (h ^ ((uint32_t(f) >> (8 * i)) & 255u)) * 1099511628211ull;

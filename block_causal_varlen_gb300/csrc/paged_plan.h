@@ -77,6 +77,7 @@ enum : int {
   PH_SEL_ROWS,     // rows of a group whose blocks are selected together (1: every row is one)
   PH_OFF_SELG,     // int32 [NSELG][2]: first row and number of rows of every group, none where rows are groups
   PH_NSELG,
+  PH_SEL_SPLIT,    // CTAs that share out a row's scores (a cluster; 1 where rows go together)
   PH_STATUS = H_STATUS, PH_STATUS_DETAIL = H_STATUS_DETAIL, // 5 few-rows attention, 6 tile attention
   kPagedHdrWords = kHdrWords
 };
@@ -104,7 +105,7 @@ enum : int { RC_P0 = 0, RC_P1, RC_RESERVED0, RC_RESERVED1, RC_PIECE, kRecordWord
 // A join of the n partial results in slots slot0, slot0 + 1, ... of one block.
 enum : int { MG_SLOT0 = 0, MG_N, MG_Q0, MG_HKV, MG_ROW0, MG_NROWS, MG_RESERVED0, MG_RESERVED1, kMergeWords = 8 };
 
-static_assert(PH_NSELG < PH_STATUS, "header words");
+static_assert(PH_SEL_SPLIT < PH_STATUS, "header words");
 
 // Records and joins have fixed places and room for the most there can be (a join has
 // two slots at least).
@@ -121,6 +122,10 @@ constexpr int kMostListed = 4096, kMostBlocks = 16384;
 // enough CTAs and their scores and codes take no more than kSelSmem bytes.
 constexpr int kSelRows = 8, kSelCtas = 2 * kPagedSms;
 constexpr int64_t kSelSmem = 48 << 10;
+// Where PH_SEL_CAP is past kSelSplitCap, rows get a cluster of 2 or 4 CTAs each if every one of them has an
+// SM to itself (4 sequences of 938 blocks, 8 heads: 12 us by a CTA a row and head, 8.8 by four; 16 of them by two,
+// two on an SM: 12 and 14.6; 2 of them by eight, which find no room side by side: 12.3).
+constexpr int kSelSplitCap = 512, kSelMostSplit = 4;
 // Shared memory of the selection: codes of q (bytes of a (row, head): two lots of d, and what
 // sets eight of them apart in the banks), a power of two and a place each, a score for each block and row.
 constexpr int select_pitch(int d) { return 2 * d + (d == 64 ? 64 : 16); }

@@ -14,7 +14,10 @@
  *   - new rows of all sequences are packed back to back, sequence by sequence;
  *   - bd_cache_write stores new K/V rows, bd_cache_read gets a batch's cached
  *     rows back as packed bf16 rows (the K/V bd_attn_fwd takes, sequences as
- *     documents), bd_paged_attn computes O and LSE of the new rows over the cache.
+ *     documents), bd_paged_attn computes O and LSE of the new rows over the cache;
+ *   - bd_cache_append writes new rows turned by their positions;
+ *   - bd_block_bounds, bd_block_select and bd_sparse_attn let each new row attend the blocks
+ *     (pages) of its sequence that a cheap score picks.
  *
  * Conventions are those of bd_attn.h (status returns, caller-owned buffers,
  * stream ordering, scale 1/sqrt(d), natural-log LSE, GQA head mapping). In
@@ -178,7 +181,8 @@ BD_API int32_t bd_paged_attn_workspace(const void* plan_host, size_t* bytes);
  * a new row does not see: an infinity or a NaN there reaches the rows that see it only.
  * O's error is that of probabilities rounded to bf16 (2^-8 of each) and of its own rounding; few
  * rows over a BD_CACHE_E4M3 cache (up to 48 (new row, query head) pairs of a K/V head) have
- * weights p * 2^e in fp16 instead: 2^-11 of each, and 2^-32 of the row's largest where that is more.
+ * weights p * 2^e in fp16 instead: 2^-11 of each, and 2^-32 of the row's largest where that is more. So do
+ * rows over a BD_CACHE_E2M1 cache, few or many, with weights p.
  * out must not alias q or the cache. workspace: bd_paged_attn_workspace bytes, 256-byte aligned;
  * it needs no clearing and holds nothing between calls. */
 BD_API int32_t bd_paged_attn(const void* plan_host, const void* plan_dev, const bd_tensor* q,

@@ -19,7 +19,7 @@ from oracle import rope as orope  # noqa: E402
 by = ctypes.byref
 DEV = ctypes.c_void_p(4096)     # never read: every refusal below comes before a launch
 # header words behind those of test_paged_plan (csrc/paged_plan.h)
-POS, TOUCH, NTOUCH, BOUNDS_OK, BLOCKS, FIRST, RECENT, ROWPG, SEL_CAP, SEL_ROWS, SELG, NSELG = range(31, 43)
+POS, TOUCH, NTOUCH, BOUNDS_OK, BLOCKS, FIRST, RECENT, ROWPG, SEL_CAP, SEL_ROWS, SELG, NSELG, SEL_SPLIT = range(31, 44)
 OFF_PAGES, DEC, NDEC = 18, 22, 23
 
 
@@ -292,6 +292,10 @@ def test_groups_of_rows_are_of_one_sequence_and_cover_all():
         rows += range(t, t + n)
     assert rows == list(range(338))
     assert make([1] * 4, [900] * 4, blocks=9).host[SEL_ROWS] == 1
+    # one row of more than 512 blocks is shared out to a cluster where it finds SMs
+    for B, kv, want in ((1, 8000, 1), (1, 9000, 4), (19, 9000, 4), (20, 9000, 2), (38, 9000, 2), (39, 9000, 1)):
+        plan = make([1] * B, [kv] * B, blocks=9)
+        assert plan.host[SEL_ROWS] == 1 and plan.host[SEL_SPLIT] == want, (B, kv)
 
 
 def test_key_covers_the_lists():
