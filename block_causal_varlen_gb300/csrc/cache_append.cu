@@ -3,7 +3,7 @@
 // Pair i of a head's turned elements, at position p: (x, y) -> scale (x cos a - y sin a,
 // y cos a + x sin a), a = p f_i. The angle is kept as turns: the host gives f_i / 2 pi modulo 1
 // in units of 2^-64 (bd_rope_phases), so p times it modulo 2^64 is the angle's fraction of a
-// turn, whatever p, and its upper 32 bits lose 2^-33 of a turn. No table of angles is read.
+// turn, whatever p, and its upper 32 bits lose less than 2^-32 of a turn. No table of angles is read.
 //
 // A group of d / 8 lanes takes some heads of a row, 8 elements a lane: cosines and sines are made
 // once and used for all of them. Pairs d / 2 apart meet by a shuffle. K goes on as
@@ -160,19 +160,20 @@ using namespace bd;
 
 extern "C" int32_t bd_rope_phases(const double* inv_freq, int32_t n, uint64_t* out) {
   if (n < 0 || (n > 0 && (!inv_freq || !out))) return fail(BD_ERR_ARG, "inv_freq or out is NULL, or n negative");
-  // 1 / 2 pi in two parts; the products are exact to some 100 bits
+  // 1 / 2 pi in two parts, off by less than 2^-109; the product and what it lost, off by less than |f| 2^-107
   constexpr double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
   for (int32_t i = 0; i < n; ++i) {
     const double f = inv_freq[i];
     if (!std::isfinite(f)) return fail(BD_ERR_ARG, "inv_freq[%d] is not finite", i);
     const double a = f * hi, b = std::fma(f, hi, -a) + f * lo;
-    // a and b modulo 1, in [0, 1), as 64-bit fractions
+    // modulo 1 as 64-bit fractions, of the magnitude (1 - |x| would lose what lies below 2^-53): the
+    // parts below 1 are exact, cut at 2^-64
     auto turns = [](double x) {
-      x -= std::floor(x);
-      const double u = std::ldexp(x, 32), w = std::floor(u);  // x < 1, or 1 by rounding: both parts wrap
-      return (uint64_t(w) << 32) + uint64_t(std::ldexp(u - w, 32));
+      const double y = std::fabs(x), u = std::ldexp(y - std::floor(y), 32), w = std::floor(u);
+      const uint64_t t = (uint64_t(w) << 32) + uint64_t(std::ldexp(u - w, 32));
+      return x < 0 ? 0 - t : t;
     };
-    out[i] = std::isfinite(a) ? turns(a) + turns(b) : 0;
+    out[i] = turns(a) + turns(b);
   }
   return ok();
 }

@@ -138,8 +138,9 @@ BD_API int32_t bd_cache_write(const void* plan_host, const void* plan_dev, const
 
 /* Frequencies of a position rotation as the kernels take them: out[i] = turns a position
  * advances pair i by, modulo 1, in units of 2^-64 (host, n values; inv_freq in radians a
- * position, any finite number). Angles of far positions lose nothing: a position's is its product
- * with out[i], modulo 2^64. BD_ERR_ARG for an infinity or a NaN. Pure host function. */
+ * position, any finite number), off by at most 2^-63 + |inv_freq[i]| 2^-106 of a turn. A position's angle
+ * is its product with out[i], modulo 2^64: exact, so positions up to 2^31 are off by no more than 2^-31 of
+ * a turn (|inv_freq| up to 2^42). BD_ERR_ARG for an infinity or a NaN. Pure host function. */
 BD_API int32_t bd_rope_phases(const double* inv_freq, int32_t n, uint64_t* out);
 
 /* A rotation of pairs of elements of a head by angles p * inv_freq[i] at position p. */

@@ -116,6 +116,19 @@ def test_phases_are_turns_to_64_bits():
     assert len(bd.bd_rope_phases([])) == 0
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+def test_phases_of_either_sign_are_off_by_units(sign):
+    """Two terms cut at 2^-64, and 2^-106 of the frequency: 1 / 2 pi is held to 2^-109, and the product's
+    second part, below |f| 2^-55, is rounded twice to 53 bits. No more for negative frequencies, or where
+    that second part is negative."""
+    g = np.random.default_rng(0)
+    f = sign * np.concatenate([np.exp(g.uniform(-25, 25, 600)), 500000.0 ** -(np.arange(64) / 64), 2.0 ** np.arange(-60, 60, 3.0)])
+    for x, p in zip(f, bd.bd_rope_phases(f)):
+        turns = Fraction(float(x)) / (2 * orope._PI)
+        off = (int(p) - (turns - turns.__floor__()) * 2 ** 64) % 2 ** 64
+        assert min(off, 2 ** 64 - off) <= 2 + abs(x) * 2.0 ** -42, (x, float(off))
+
+
 def test_append_refusals():
     lib = bd.load()
     plan = make([3], [40])
