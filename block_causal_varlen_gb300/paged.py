@@ -328,7 +328,9 @@ class Rope:
     """A position rotation of the first 2 * len(inv_freq) elements of a head: pair i turns by
     inv_freq[i] radians a position. ``interleaved``: pairs (2 i, 2 i + 1) instead of
     (i, i + len(inv_freq)); ``scale``: a factor of the turned elements. Made once (the
-    frequencies go through host memory), for the device of ``inv_freq`` or ``device``."""
+    frequencies go through host memory), for the device of ``inv_freq`` or ``device``. Its
+    memory stays its own until the calls made with it have run, on whichever streams; what a
+    captured graph uses is the caller's to keep."""
 
     def __init__(self, inv_freq, interleaved=False, scale=1.0, device=None):
         if isinstance(inv_freq, torch.Tensor):
@@ -342,6 +344,13 @@ class Rope:
         self._c = bd_rope(self.phase.data_ptr(), self.dim, int(self.interleaved), self.scale, 0)
         self._addr = C.addressof(self._c)
         self._index = self.phase.get_device()
+        self._streams = {_raw_stream(self._index)} if self.phase.is_cuda else set()   # that the allocator knows
+
+    def _used_on(self, raw, stream):
+        """As PagedPlan._used_on."""
+        if raw not in self._streams:
+            self.phase.record_stream(torch.cuda.current_stream(self._index) if stream is None else stream)
+            self._streams.add(raw)
 
 
 def bd_cache_append(plan: PagedPlan, q, k, v, rope: Rope, cache: PagedCache, q_out=None, stream=None):
@@ -356,6 +365,7 @@ def bd_cache_append(plan: PagedPlan, q, k, v, rope: Rope, cache: PagedCache, q_o
     to = _rows3(q_out, "q_out", plan.H, plan.d, plan.T, idx) if q is not None else None
     tk = _rows3(k, "k", plan.Hkv, plan.d, plan.T, idx)
     tv = _rows3(v, "v", plan.Hkv, plan.d, plan.T, idx)
+    rope._used_on(_raw_stream(idx) if stream is None else stream.cuda_stream, stream)
     _call(_entry("bd_cache_append"), plan, idx, stream, plan._host_ptr, plan._dev_ptr, tq, tk, tv, rope._addr, cache._addr, to)
 
 
