@@ -105,7 +105,7 @@ struct TileCfg {
 enum : int {
   T_QFULL = 0, T_QEMPTY, T_KFULL = 4, T_KEMPTY = 8, T_VFULL = 12, T_VEMPTY = 16, T_RFULL = 20, T_REMPTY = 24,
   T_SFULL = 28, T_PFULL = 30, T_OFINAL = 32, T_OEMPTY = 34, T_TURN = 36, T_DRAIN = 38, T_VTAIL = 40, T_PHALF = 44,
-  T_QCONV = 46, T_COUNT = 47
+  T_QCONV = 46, T_QSEEN = 47, T_COUNT = 48
 };
 constexpr int kOddMarks = 8;  // at most 4 key tiles, so 4 blocks, are under way at a time
 static_assert(8 * T_COUNT + 16 + 4 * kOddMarks <= 512, "barriers, TMEM slot, abort flag and marks overflow their region");
@@ -182,7 +182,10 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
     mbar_init(bar(T_QFULL), 1);
-    if (F4) mbar_init(bar(T_QCONV), Cfg::kConvThreads);
+    if (F4) {
+      mbar_init(bar(T_QCONV), Cfg::kConvThreads);
+      mbar_init(bar(T_QSEEN), Cfg::kConvThreads / 32);
+    }
     mbar_init(bar(T_QEMPTY), Cfg::kStageInQ ? 4 * NS : NS);  // softmax warps, or MMA threads
     for (int s = 0; s < NST; ++s) {
       mbar_init(bar(T_KFULL + s), CONV ? Cfg::kConvThreads : 1);
@@ -762,8 +765,9 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
         fence_proxy_async_smem();
       };
       // Q's rows of a block: bf16 to fp16, times a power of two each (its inverse goes to the
-      // row's score factor)
-      auto convert_q = [&](int ns) {
+      // row's score factor). False if a wait gave up.
+      auto convert_q = [&](int ns) -> bool {
+        static_assert(PARTS == 1 || NS == 1, "T_QSEEN completes once a block");
         for (int s = 0; s < ns; ++s) {
           const uint32_t q = sQ + s * Cfg::kTileBytes + r * 128;
           auto at = [&](int c) { return q + (c >> 3) * 16384 + (((c & 7) ^ (r & 7)) << 4); };
@@ -773,7 +777,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           float inv;
           const float2 up = q_factors(mx, &inv);
           if (part == 0) qs[((n - 1) & 1) * 128 * NS + s * 128 + r] = a.scale_log2 * inv;
-          if (PARTS > 1) named_bar_sync(1, Cfg::kConvThreads);  // every part has seen the whole row
+          if (PARTS > 1) {  // every part has seen the whole row (a wait with a limit: the others may have given up)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(T_QSEEN));
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(T_QSEEN), (n - 1) & 1, abort_flag))) return false;
+          }
 #pragma unroll 2
           for (int ci = 0; ci < D / 8 / PARTS; ++ci) {
             const int c = part * (D / 8 / PARTS) + ci;
@@ -783,10 +791,11 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
           }
         }
         fence_proxy_async_smem();
+        return true;
       };
       auto turn_q = [&](int ns) -> bool {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(T_QFULL), (n - 1) & 1, abort_flag))) return false;
-        convert_q(ns);
+        if (!convert_q(ns)) return false;
         mbar_arrive(bar(T_QCONV));
         return true;
       };

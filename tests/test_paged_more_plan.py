@@ -344,3 +344,14 @@ def test_the_new_kernels_wait_before_their_first_read():
             assert not re.search(r"\bplan\[|\bphase\[|->|__ld[cg]\w*\(|\bcp\.async", early), m.group(1)
             assert early[early.rfind("\n"):].strip() == ""
     assert set(names) == {"bd_cache_append_kernel", "bd_block_bounds_kernel", "bd_block_select_kernel"}
+
+
+def test_tile_warps_meet_where_waits_have_a_limit():
+    """A warp whose wait ran out leaves its loop: no other may wait for it without a limit. The tile
+    kernel's threads meet in barriers before its warps take their roles, and when all have ended."""
+    s = open(os.path.join(os.path.dirname(bd.__file__), "csrc", "paged_tile.cu")).read()
+    s = re.sub(r"//[^\n]*", "", s)
+    roles = s[s.index("if (warp == 0)", s.index("bd_paged_tile_kernel(")):s.index("launch_tile_t(")]
+    last = roles.rindex("__syncthreads()")
+    assert not re.search(r"named_bar_sync|__syncthreads|bar\.sync", roles[:last])
+    assert not re.search(r"\bfor \(|mbar_wait\(", roles[last:])
