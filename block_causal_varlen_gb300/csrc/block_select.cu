@@ -141,8 +141,10 @@ __global__ void __launch_bounds__(kBoundThreads) bd_block_bounds_kernel(const Bo
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int col = threadIdx.x + c * kBoundThreads;
-        out[col] = bad ? int8_t(0) : int8_t(fminf(fmaxf(floorf(lo[c] * f), -127.f), 127.f));
-        out[a.c_sb + col] = bad ? int8_t(0) : int8_t(fminf(fmaxf(ceilf(hi[c] * f), -127.f), 127.f));
+        // (a product below the least float is zero, its floor or ceil is not)
+        const float down = fminf(floorf(lo[c] * f), lo[c] < 0.f ? -1.f : 127.f), up = fmaxf(ceilf(hi[c] * f), hi[c] > 0.f ? 1.f : -127.f);
+        out[col] = bad ? int8_t(0) : int8_t(fmaxf(down, -127.f));
+        out[a.c_sb + col] = bad ? int8_t(0) : int8_t(fminf(up, 127.f));
       }
     if (threadIdx.x == 0) a.exp[page * a.x_sp + int64_t(h) * a.x_sh] = bad ? uint8_t(255) : uint8_t(e + 127);
     __syncthreads();

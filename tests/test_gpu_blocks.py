@@ -394,3 +394,20 @@ def test_scores_of_the_largest_codes_are_exact(new, d):
     s.bounds.code.copy_(code)
     s.bounds.exp[:] = 127
     assert torch.equal(s.lists().cpu(), s.want_lists())
+
+
+def test_bounds_of_values_far_below_the_largest():
+    """floor and ceil of what 2^-e takes below the least float: -1 and 1, not 0."""
+    c = pm.Case([32], [32], 4, 1, 64, page=16, junk=0.0)
+    k = c.k_new.clone()
+    k[:, 0, 0] = 2.0 ** 60
+    k[:16, 0, 1], k[:16, 0, 2], k[:16, 0, 3] = -2.0 ** -120, 2.0 ** -120, 2.0 ** -133
+    k[16:, 0, 1], k[16:, 0, 2], k[16:, 0, 3] = -2.0 ** -133, -0.0, 0.0
+    bd.bd_cache_write(c.plan, k.cuda(), k.cuda(), c.cache)
+    b = bd.BlockBounds.empty(c.cache)
+    bd.bd_block_bounds(c.plan, c.cache, b)
+    torch.cuda.synchronize()
+    for j in range(2):
+        p = c.pages[0][j]
+        lo, hi, e = ob.bounds(k[16 * j:16 * j + 16, 0])
+        assert b.exp[p, 0].item() == e and torch.equal(b.code[p, 0].cpu(), torch.stack([lo, hi])), j
