@@ -557,7 +557,7 @@ extern "C" int32_t bd_block_bounds(const void* plan_host, const void* plan_dev, 
   if (!w[PH_CAUSAL]) return fail(BD_ERR_PLAN, "new rows of a plan that is not causal have no cache positions");
   if (!w[PH_BOUNDS_OK]) return fail(BD_ERR_PLAN, "two sequences of the batch have new rows in the same page");
   if ((st = check_bounds(bounds, w))) return st;
-  if (w[PH_NTOUCH] == 0) return ok();
+  if (w[PH_T] == 0) return ok();
   const int64_t es = elem_bytes(cache->fmt);
   BoundsArgs a;
   a.plan = static_cast<const int32_t*>(plan_dev);
@@ -569,7 +569,8 @@ extern "C" int32_t bd_block_bounds(const void* plan_host, const void* plan_dev, 
   a.c_sp = bounds->stride_page; a.c_sh = bounds->stride_head; a.c_sb = bounds->stride_bound;
   a.exp = bounds->exp;
   a.x_sp = bounds->exp_stride_page; a.x_sh = bounds->exp_stride_head;
-  const int64_t ctas = int64_t(w[PH_NTOUCH]) * w[PH_HKV];
+  // (new rows of which none has a position enter no block, but those of a plan replayed here may)
+  const int64_t ctas = int64_t(w[PH_NTOUCH] > 0 ? w[PH_NTOUCH] : 1) * w[PH_HKV];
   const int grid = int(ctas < kPagedSms * 16 ? ctas : kPagedSms * 16);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = cache->fmt == BD_CACHE_BF16   ? launch_bounds<BD_CACHE_BF16>(w[PH_D], grid, s, a)

@@ -14,6 +14,7 @@
 #include <new>
 #include <queue>
 #include <stdexcept>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -578,7 +579,8 @@ static int32_t plan_build(const bd_paged_desc* desc, const bd_sparse_desc* spars
     std::copy(X.S.page_off.begin(), X.S.page_off.end(), w + w[PH_OFF_ROWPG]);
   }
   int64_t tok = 0, pg = 0, kv = 0, touch = 0;
-  std::vector<int32_t> entered;  // pages that new rows enter
+  struct Entered { int32_t page, rows, entry; };
+  std::vector<Entered> entered;  // pages that new rows enter, once a sequence
   struct Range { int32_t lo, hi; };
   std::vector<Range> written;  // cache rows the new rows take, one range per page touched
   for (int32_t b = 0; b < D.B; ++b) {
@@ -590,7 +592,7 @@ static int32_t plan_build(const bd_paged_desc* desc, const bd_sparse_desc* spars
       w[w[PH_OFF_PGCNT] + pg] = std::min(P, n - j);
       if (D.causal && j + P > n - q && q > 0) {
         w[w[PH_OFF_TOUCH] + touch++] = int32_t(pg);
-        entered.push_back(pages[j / P]);
+        entered.push_back({pages[j / P], std::min(P, n - j), int32_t(pg)});
       }
       ++pg;
     }
@@ -609,8 +611,18 @@ static int32_t plan_build(const bd_paged_desc* desc, const bd_sparse_desc* spars
   w[PH_WRITE_OK] = D.causal;
   for (size_t i = 1; i < written.size(); ++i)
     if (written[i].lo < written[i - 1].hi) w[PH_WRITE_OK] = 0;
-  std::sort(entered.begin(), entered.end());
-  w[PH_BOUNDS_OK] = D.causal && std::adjacent_find(entered.begin(), entered.end()) == entered.end();
+  std::sort(entered.begin(), entered.end(), [](const Entered& a, const Entered& b) {
+    return std::tie(a.page, b.rows, a.entry) < std::tie(b.page, a.rows, b.entry);
+  });
+  auto same = [](const Entered& a, const Entered& b) { return a.page == b.page; };
+  w[PH_BOUNDS_OK] = D.causal && std::adjacent_find(entered.begin(), entered.end(), same) == entered.end();
+  if (!w[PH_BOUNDS_OK]) {
+    // bd_block_bounds refuses such a plan, but it may be replayed under a call captured with another:
+    // each page once, with the most rows of it that are used, so that no two CTAs write the same bounds
+    entered.erase(std::unique(entered.begin(), entered.end(), same), entered.end());
+    w[PH_NTOUCH] = int32_t(entered.size());
+    for (size_t i = 0; i < entered.size(); ++i) w[w[PH_OFF_TOUCH] + i] = entered[i].entry;
+  }
   int64_t at = list_words(X, sparse);
   auto put = [&](const Lists& L, int off, int n, int nm, int rec, int mrg) {
     w[off] = int32_t(at);
@@ -659,8 +671,7 @@ extern "C" int32_t bd_paged_plan_key(const void* plan_host, uint64_t* key) {
   const int32_t fields[] = {w[PH_H], w[PH_HKV], w[PH_D], w[PH_PAGE], w[PH_NUM_PAGES], w[PH_FMT], w[PH_CAUSAL],
                             w[PH_WRITE_OK], w[PH_T] > 0, w[PH_NPAGES] > 0, w[PH_NDEC] > 0 ? w[PH_DEC_ROWS] : 0,
                             w[PH_NDECM] > 0 ? 1 + w[PH_DECM_WIDE] : 0, w[PH_NTILE] > 0, w[PH_NTILEM] > 0,
-                            w[PH_NTOUCH] > 0, w[PH_BOUNDS_OK], w[PH_BLOCKS], w[PH_FIRST], w[PH_RECENT], w[PH_SEL_CAP],
-                            w[PH_SEL_ROWS], w[PH_SEL_SPLIT]};
+                            w[PH_BLOCKS], w[PH_FIRST], w[PH_RECENT], w[PH_SEL_CAP], w[PH_SEL_ROWS], w[PH_SEL_SPLIT]};
   uint64_t h = 1469598103934665603ull;
   for (int32_t f : fields)
     for (int i = 0; i < 4; ++i) h = (h ^ ((uint32_t(f) >> (8 * i)) & 255u)) * 1099511628211ull;

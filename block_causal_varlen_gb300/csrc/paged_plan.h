@@ -66,9 +66,9 @@ enum : int {
   PH_NTILE,
   PH_NTILEM,
   PH_OFF_POS,      // int32 [T]: position of every new row, negative for none
-  PH_OFF_TOUCH,    // int32 [NTOUCH]: entries of the page list that hold new rows
+  PH_OFF_TOUCH,    // int32 [NTOUCH]: entries of the page list that hold new rows, every page once
   PH_NTOUCH,
-  PH_BOUNDS_OK,    // whether their pages are all different (causal plans)
+  PH_BOUNDS_OK,    // whether no two sequences have new rows in a page (causal plans)
   PH_BLOCKS,       // sparse plans: blocks of a list (0: not sparse), first and recent ones
   PH_FIRST,
   PH_RECENT,

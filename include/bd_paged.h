@@ -229,7 +229,8 @@ typedef struct {
 
 /* bd_block_bounds -- bounds of the blocks that hold new rows, from their cached rows below kv_len
  * (all blocks of a sequence whose rows are all new). BD_ERR_PLAN if two sequences have new rows
- * in the same page, or the plan is not causal. */
+ * in the same page, or the plan is not causal. (bd_paged_plan_key does not tell such a page: under a
+ * captured call it gets the bounds of the most rows that a sequence with new rows in it uses.) */
 BD_API int32_t bd_block_bounds(const void* plan_host, const void* plan_dev, const bd_paged_cache* cache,
                                const bd_bounds* bounds, void* stream);
 

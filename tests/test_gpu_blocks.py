@@ -411,3 +411,36 @@ def test_bounds_of_values_far_below_the_largest():
         p = c.pages[0][j]
         lo, hi, e = ob.bounds(k[16 * j:16 * j + 16, 0])
         assert b.exp[p, 0].item() == e and torch.equal(b.code[p, 0].cpu(), torch.stack([lo, hi])), j
+
+
+def test_captured_bounds_replay_over_pages_of_two_sequences():
+    """A step whose two sequences enter one page, under a graph captured with one whose do not: the
+    page's bounds are of the most rows of it that are used."""
+    c = pm.Case([64], [64], 4, 2, 64, page=16, junk=0.0)
+    p = c.pages[0]
+
+    def step(kv, pages):
+        return bd.PagedPlan([1, 1], kv, pages, 4, 2, 64, page_size=16, num_pages=c.num_pages)
+
+    b = bd.BlockBounds.empty(c.cache)
+    plan = step([20, 24], [[p[0], p[1]], [p[2], p[3]]])
+    buf = torch.zeros(plan.nbytes // 4, dtype=torch.int32, device="cuda")
+    plan.upload(buffer=buf)
+    bd.bd_block_bounds(plan, c.cache, b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        bd.bd_block_bounds(plan, c.cache, b)
+    K = c.rows(0)[0]
+    for kv in ([20, 24], [24, 20], [31, 32]):
+        nxt = step(kv, [[p[0], p[1]], [p[2], p[1]]])
+        assert nxt.key() == plan.key()
+        nxt.upload(buffer=buf)
+        b.code.fill_(99)
+        b.exp.fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        for g in range(2):
+            lo, hi, e = ob.bounds(K[16:max(kv), g])
+            assert b.exp[p[1], g] == e and torch.equal(b.code[p[1], g].cpu(), torch.stack([lo, hi])), (kv, g)
+        assert all((b.code[x] == 99).all() and (b.exp[x] == 9).all() for x in (p[0], p[2], p[3]))

@@ -319,6 +319,25 @@ def test_key_covers_the_lists():
     assert make([1, 1], [5008, 334], blocks=4).key() == plans[1].key()
 
 
+def test_key_leaves_out_which_pages_new_rows_enter():
+    """Steps that differ in it replay under one graph: sequences with new rows in a page of both, new
+    rows without a position. A page that two sequences enter is listed once, with the most rows."""
+    def step(new, kv, pages, **kw):
+        return bd.PagedPlan(new, kv, pages, 8, 2, 128, page_size=16, num_pages=4, **kw)
+
+    for kw in ({}, dict(blocks=4)):
+        apart = step([1, 1], [20, 24], [[0, 1], [2, 3]], **kw)
+        for kv in ([20, 24], [24, 20]):
+            both = step([1, 1], kv, [[0, 1], [2, 1]], **kw)
+            w = both.host
+            assert w[BOUNDS_OK] == 0 and apart.host[BOUNDS_OK] == 1 and both.key() == apart.key()
+            assert w[w[TOUCH]:w[TOUCH] + w[NTOUCH]].tolist() == [1 if kv[0] > kv[1] else 3]
+    none, some = (step([3], [n], [[0]]) for n in (0, 3))
+    assert none.host[NTOUCH] == 0 and some.host[NTOUCH] == 1
+    some, more = step([3], [2], [[0]]), step([3], [16], [[0]])
+    assert some.key() == more.key()
+
+
 def test_oracle_scores_bound_the_products():
     """A block's score is at least q . k of every key, up to q's rounding: a sanity check of the
     definition."""
