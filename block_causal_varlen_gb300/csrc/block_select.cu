@@ -309,8 +309,9 @@ __global__ void __launch_bounds__(THREADS, D == 256 || SPLIT ? 1 : 1024 / THREAD
         eb[h] = a.exp[int64_t(pg[h]) * a.x_sp + int64_t(g) * a.x_sh];
       }
       if ((tile + step) * 16 < most) look_up(tile + step);
-      // (bounds that were never set may hold any byte)
-      const float ebf[2] = {pow2f(min(max(int(eb[0]) - 127, -126), 126)), pow2f(min(max(int(eb[1]) - 127, -126), 126))};
+      // (memory that never was bounds may hold any byte: with q's 2^-50..2^50 and sums below 2^23 every
+      // score is a finite number)
+      const float ebf[2] = {pow2f(min(max(int(eb[0]) - 127, -50), 50)), pow2f(min(max(int(eb[1]) - 127, -50), 50))};
       for (int ct = 0; ct < colt; ++ct) {
         int c[4] = {0, 0, 0, 0};
         const uint8_t* q = s_q + (ct * 8 + rw) * QP + j * (D / 4);

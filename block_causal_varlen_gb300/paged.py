@@ -447,9 +447,10 @@ class BlockBounds:
 
     @classmethod
     def empty(cls, cache: PagedCache):
-        """Bounds for a cache's pool; a block's are there once bd_block_bounds has seen its rows."""
+        """Bounds for a cache's pool; a block's are there once bd_block_bounds has seen its rows. Until
+        then its byte is 255: a block of which nothing is known outscores the others."""
         return cls(torch.zeros(cache.num_pages, cache.Hkv, 2, cache.d, dtype=torch.int8, device=cache.device),
-                   torch.zeros(cache.num_pages, cache.Hkv, dtype=torch.uint8, device=cache.device))
+                   torch.full((cache.num_pages, cache.Hkv), 255, dtype=torch.uint8, device=cache.device))
 
 
 def _check_bounds(plan, bounds, idx):

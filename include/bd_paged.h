@@ -217,7 +217,8 @@ BD_API int32_t bd_sparse_plan_build(const bd_paged_desc* desc, const bd_sparse_d
  * element c, value = code * 2^(exp[page][head] - 127). bd_block_bounds takes the smallest e in
  * [-50, 50] with max|k| <= 127 * 2^e (50 if there is none) and stores floor(min k * 2^-e) and
  * ceil(max k * 2^-e), saturating at +-127, and byte e + 127; a block with an infinity or a NaN among
- * its keys gets byte 255, which outscores every other. Base pointers and strides of code are
+ * its keys gets byte 255, which outscores every other (and is what a block's byte is to be set to before its
+ * bounds are made; other bytes count as the nearest of 77..177). Base pointers and strides of code are
  * multiples of 16 bytes; strides of exp positive. */
 typedef struct {
   int8_t* code;

@@ -444,3 +444,28 @@ def test_captured_bounds_replay_over_pages_of_two_sequences():
             lo, hi, e = ob.bounds(K[16:max(kv), g])
             assert b.exp[p[1], g] == e and torch.equal(b.code[p[1], g].cpu(), torch.stack([lo, hi])), (kv, g)
         assert all((b.code[x] == 99).all() and (b.exp[x] == 9).all() for x in (p[0], p[2], p[3]))
+
+
+def test_blocks_without_bounds_are_listed():
+    """Bounds that nobody made: such a block is listed before all whose bounds are known."""
+    s = Sparse([2], [640], 4, 2, 64, 6, 1, 2, junk=0.0)
+    fresh = bd.BlockBounds.empty(s.c.cache)
+    known = [p for j, p in enumerate(s.c.pages[0]) if j not in (7, 31)]
+    fresh.code[known], fresh.exp[known] = s.bounds.code[known], s.bounds.exp[known]
+    s.bounds = fresh
+    got = s.lists().cpu()
+    assert torch.equal(got, s.want_lists()) and all({0, 7, 31, 38, 39} <= set(r.tolist()) for r in got.flatten(0, 1))
+
+
+@pytest.mark.parametrize("size", [-80, 0, 80])
+def test_any_byte_is_a_number(size):
+    """Bytes that bd_block_bounds does not write count as the nearest that it does, whatever q."""
+    s = Sparse([3], [1200], 4, 2, 64, 9, 0, 1, junk=0.0)
+    s.c.q *= 2.0 ** size
+    g = torch.Generator().manual_seed(1)
+    exp = torch.randint(0, 255, s.bounds.exp.shape, generator=g).to(torch.uint8)
+    s.bounds.exp.copy_(exp)
+    s.bounds.code[::3] = 0
+    got = s.lists().cpu()
+    s.bounds.exp.copy_(exp.clamp(77, 177))
+    assert torch.equal(got, s.want_lists())

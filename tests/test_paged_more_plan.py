@@ -261,6 +261,11 @@ def test_binding_refuses_other_lists_and_bounds():
         bd.sparse_attn(dense, q, cache, b)
 
 
+def test_bounds_start_as_those_of_unknown_blocks():
+    z = torch.zeros(25, 16, 2, 128, dtype=torch.bfloat16)
+    assert (bd.BlockBounds.empty(bd.PagedCache(z, z)).exp == 255).all()
+
+
 LAYOUTS = [([1], [1]), ([1], [5000]), ([3], [2]), ([5, 0, 1], [0, 7, 90]), ([1, 17, 0, 200, 1], [5000, 17, 40, 333, 16])]
 
 
