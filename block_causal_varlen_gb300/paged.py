@@ -163,7 +163,10 @@ class PagedPlan:
         desc = bd_paged_desc(self.B, H, Hkv, d, page_size, num_pages, fmt, int(self.causal), q.ctypes.data_as(_P32),
                              kv.ctypes.data_as(_P32), flat.ctypes.data_as(_P32), offs.ctypes.data_as(_P32))
         self.blocks = _int(blocks, "blocks")
-        sparse = bd_sparse_desc(self.blocks, _int(first, "first"), _int(recent, "recent"), 0) if self.blocks else None
+        first, recent = _int(first, "first"), _int(recent, "recent")
+        if not self.blocks and (first, recent) != (0, 1):
+            raise ValueError("first and recent are of a sparse plan: build it with blocks=...")
+        sparse = bd_sparse_desc(self.blocks, first, recent, 0) if self.blocks else None
         self.nbytes = bd_sparse_plan_bytes(desc, sparse) if sparse else bd_paged_plan_bytes(desc)
         self._raw = np.empty(self.nbytes // 4 + 16, dtype=np.int32)
         off = (-self._raw.ctypes.data % 64) // 4

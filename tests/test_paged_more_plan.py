@@ -193,6 +193,13 @@ def test_sparse_refusals():
     assert lib.bd_sparse_plan_bytes(by(_abi.bd_paged_desc()), None, by(n)) == A
 
 
+def test_a_plan_without_lists_has_no_first_or_recent_blocks():
+    for kw in (dict(first=1), dict(recent=2), dict(recent=0)):
+        with pytest.raises(ValueError, match="blocks="):
+            make([1], [100], **kw)
+    make([1], [100], first=0, recent=1)
+
+
 def test_sparse_calls_refuse_other_plans_bounds_and_lists():
     lib = bd.load()
     dense, plan = make([3], [400]), make([3], [400], blocks=4)
