@@ -21,8 +21,8 @@
 //                anything, and 0 x NaN is NaN), and infinities and NaN out of V rows that
 //                not every row sees; those who see them get them at the block's end, read
 //                from the cache (a rare and slow path)
-//   warps 4-11   softmax, thread = row; they also store the results
-//   warps 12-15  e4m3: turn raw tiles into bf16 ones. A code's bits, shifted into
+//   warps 4-11   softmax, thread = row; they also store the results (e2m1 at head dim 256: 4-7)
+//   warps 12-15  (e2m1 at head dim 256: 8-15) e4m3: turn raw tiles into bf16 ones. A code's bits, shifted into
 //                a bf16, are its value times 2^-120; one packed multiplication by
 //                2^(120 + e) gives the exact value (e: the row's exponent). e2m1: turn raw
 //                tiles, and Q's, into fp16 ones, where a conversion and a multiplication
@@ -36,7 +36,7 @@
 // cycles for 2048 of products (4000 with the conversion beside it), a block some 4500
 // more. 4096 rows over 16384 keys, 32 / 8 heads of 128: bf16 653 us (1473 TFLOP/s), e4m3 792, e2m1 743
 // (1295), with pauses between calls; bf16 681-696 in a row, under the power cap; at d 256 bf16 1493, e4m3
-// 2703, e2m1 2020. (The converting kernels spill 10 to 17 registers, 36-68 bytes.)
+// 2703, e2m1 2020. (The converting kernels spill 9 to 17 registers, 36-68 bytes, the bf16 one at d 256 two.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -75,7 +75,7 @@ struct TileCfg {
   // shared memory: bf16 d 64 624 and 590 us, d 128 650 and 672, d 256 1856 and 1872; e4m3
   // d 128 274 and 272.
   static constexpr bool kTurnInRegs = !kF8 && D >= 128;
-  static constexpr bool kStageInQ = kConv && D >= 128 && !kTurnInRegs;
+  static constexpr bool kStageInQ = kF8 && D >= 128;
   static constexpr int kOffStage = kOffRaw + kRawStages * kRawBytes;
   static constexpr int kOffBar = kOffStage + (kStageInQ || kTurnInRegs ? 0 : kSlots * 16384);
   static constexpr int kOffPieces = kOffBar + 512;
@@ -837,9 +837,9 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             if (lo | hi) odd[(n - 1) % kOddMarks] = n;
           }
           for (int h = 0; h < 2; ++h, ++rit) {
-            // Q where its tile is free before the last block's results are out between its K and V, else
-            // behind them
-            if (j == 0 && h == 1 && !Cfg::kStageInQ && !(ok = turn_q(P.ns))) break;
+            // Q between its first K and V (its tile is free when the last block's products are done)
+            static_assert(!Cfg::kStageInQ, "Q would be waited for before the last block's results are out");
+            if (j == 0 && h == 1 && !(ok = turn_q(P.ns))) break;
             const int rs = rit % NR;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar(T_RFULL + rs), (rit / NR) & 1, abort_flag)))) break;
             if (!(ok = __all_sync(0xffffffffu, mbar_wait(bar((h ? T_VEMPTY : T_KEMPTY) + s), ((it / NST) & 1) ^ 1, abort_flag)))) break;
@@ -848,7 +848,6 @@ __global__ void __launch_bounds__(TileCfg<D, FMT>::kThreads, 1)
             mbar_arrive(bar((h ? T_VFULL : T_KFULL) + s));
           }
           if (!ok) break;
-          if (j == 0 && Cfg::kStageInQ && !(ok = turn_q(P.ns))) break;
         }
       }
     } else if constexpr (F8) {
