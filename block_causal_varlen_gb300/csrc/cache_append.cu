@@ -12,7 +12,8 @@
 // What bounds it is HBM, or for a few rows the launch and the chain plan - rows - stores; few
 // rows are cut into many groups of few heads each. 19074 rows of 32 + 8 + 8 heads of 128 into bf16 75 us (6.25
 // TB/s, 92% of a copy's rate; 114 with heads of q, K and V in one group, whose places were
-// looked up head by head), 30273 into e4m3 124 (5.5 TB/s), into e2m1 127 (5.1); 8 rows 2.3 us in a graph.
+// looked up head by head), 30273 into e4m3 124 (5.5 TB/s), into e2m1 127 (5.1; pairs d / 2 apart
+// spill three registers, 12 bytes); 8 rows 2.3 us in a graph.
 #include <cuda_runtime.h>
 
 #include <cmath>

@@ -413,8 +413,10 @@ int32_t prepare(const bd_paged_desc* D, const bd_sparse_desc* X, Built* B) {
   // few-rows kernel, in blocks of one size (a tile of 32 rows in use costs what one of 128
   // does). 16 sequences of 8000 rows, bf16 d 256, 32 pairs: 220 us, as tiles 253; d 128, 48
   // pairs: 195 and 138; e4m3 d 128, 48 pairs in three blocks: 144, as tiles 167; 64 pairs of
-  // 300-8000 rows: 66 and 63; e2m1 d 128, 48 pairs: 127, as tiles 153 (d 256: 138 and 115, of 4 sequences of
-  // 3000 rows 23 and 26). Rows with blocks of their own go there one by one.
+  // 300-8000 rows: 66 and 63; e2m1, 48 pairs of 8 K/V heads: d 64 91, as tiles 136, d 128 127 and 153, d 256 276 and
+  // 329 (64 of 300-8000 rows 355 and 343; of 2 heads 72 and 68, 4 of 3000 rows 15 and 22: past 32 pairs of
+  // long sequences tiles gain some 5% there, and take 1.4 to 2.4 times as long for short ones). Rows with blocks of
+  // their own go there one by one.
   const int most = dec_most_rows(D->fmt);
   int32_t widest = 1;
   if (X) widest = G;
