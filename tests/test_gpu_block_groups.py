@@ -58,12 +58,14 @@ class Lists:
         out = torch.full((self.q.shape[0], Hkv, self.blocks), -7, dtype=torch.int32)
         q = self.q.cuda().double()
         ok = torch.isfinite(q).all(-1)
+        # (powers on the device are off by a rounding, which a tie does not forgive)
+        two = torch.tensor([2.0 ** i for i in range(-300, 301)], dtype=torch.float64, device="cuda")
         q = torch.where(ok[..., None], q, torch.zeros_like(q))
         top = q.abs().amax(-1)
         e = torch.full_like(top, -50)
         for i in range(-50, 50):
             e = torch.where(top > 127 * 2.0 ** i, i + 1, e)
-        c = torch.round(q * 2.0 ** -e[..., None]).clamp(-127, 127).unflatten(1, (Hkv, G))
+        c = torch.round(q * two[(300 - e).long()][..., None]).clamp(-127, 127).unflatten(1, (Hkv, G))
         e = e.unflatten(1, (Hkv, G))
         end = 0
         for n, kv, pages in zip(self.new, self.kv, self.pages):
@@ -78,7 +80,7 @@ class Lists:
                     continue
                 x = c[t][:, :, None]                                                              # [Hkv, G, 1, d]
                 s = torch.maximum(x * lo[:, None, :nblk], x * hi[:, None, :nblk]).sum(-1)
-                s = (s * 2.0 ** (e[t][..., None] + eb[:, None, :nblk] - 127)).amax(1)
+                s = (s * two[(e[t][..., None] + eb[:, None, :nblk] + 173).long()]).amax(1)
                 s[eb[:, :nblk] == 255] = 1e300
                 s[:, :self.first] = s[:, nblk - self.recent:] = float("inf")
                 best = torch.sort(s, dim=1, descending=True, stable=True)[1][:, :self.blocks]
