@@ -36,9 +36,10 @@
 //
 // 64 ragged sequences of 500-16000 rows, 8 K/V heads of 128: bf16 (4 pairs a head) 164 us,
 // 6.8 TB/s; e4m3 (2 pairs) 92 us, 6.1 TB/s; e2m1 (4 pairs) 73 us, 4.3 TB/s, no longer HBM's: 700
-// instructions a chunk of 32 keys, 256 of them the conversions and the scales' products, one behind the other in
-// 12 warps an SM, which leave the ALU (it converts at half rate) 52% and the issue slots 53% busy. One sequence of 4096 rows 7.5-7.8 us in a graph.
-// (Blocks of 32 bf16 rows at d 128 and 256 spill some 30 registers, 132 bytes, over lists of blocks 45, 180.)
+// instructions a chunk of 32 keys, 256 of them the conversions and the scales' products, one
+// behind the other in 12 warps an SM, which leave the ALU (it converts at half rate) 52% and the issue
+// slots 53% busy. One sequence of 4096 rows 7.5-7.8 us in a graph. (Blocks of 32 bf16 rows at d 128
+// and 256 spill some 30 registers, 132 bytes, over lists of blocks 45, 180.)
 //
 // A row takes nothing from a key it does not see, whatever is there: V's infinities
 // and NaN, which a probability of zero would turn to NaN, stay out of the products of

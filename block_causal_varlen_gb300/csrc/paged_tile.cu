@@ -22,11 +22,11 @@
 //                not every row sees; those who see them get them at the block's end, read
 //                from the cache (a rare and slow path)
 //   warps 4-11   softmax, thread = row; they also store the results (e2m1 at head dim 256: 4-7)
-//   warps 12-15  (e2m1 at head dim 256: 8-15) e4m3: turn raw tiles into bf16 ones. A code's bits, shifted into
+//   warps 12-15  e4m3: turn raw tiles into bf16 ones. A code's bits, shifted into
 //                a bf16, are its value times 2^-120; one packed multiplication by
-//                2^(120 + e) gives the exact value (e: the row's exponent). e2m1: turn raw
-//                tiles, and Q's, into fp16 ones, where a conversion and a multiplication
-//                give two exact values; Q's rows are scaled by a power of two to a maximum
+//                2^(120 + e) gives the exact value (e: the row's exponent). e2m1 (at head
+//                dim 256 warps 8-15): turn raw tiles, and Q's, into fp16 ones, where a conversion
+//                and a multiplication give two exact values; Q's rows are scaled by a power of two to a maximum
 //                of 2^14 first (exact but for what is below 2^-31 of the row's largest), and
 //                P is fp16 as well
 // Work comes from the plan: every CTA walks its own list of pieces (block, key range).
